@@ -79,6 +79,12 @@ typedef enum { SC_F32 = 0, SC_F16 = 1, SC_BF16 = 2 } sc_dtype;
 #define SC_KMAP_SPLIT 0x8000u   /* sc_kmap_build, K^ndim <= 32: row orders for column splitting (see below) */
 #define SC_KMAP_TILE_TABLE 0x10000u /* K^ndim <= 128: also the fused layer's tile-transposed index table (see below) */
 
+/* flags for sc_qk_norm_rope_fwd / sc_qk_norm_rope_bwd */
+#define SC_ROPE_INTERLEAVED 0x1u /* pairs (2i, 2i+1); default: (i, i + rot_dim/2) */
+
+/* flags for sc_attn_fwd / sc_attn_bwd */
+#define SC_ATTN_CAUSAL 0x1u /* query i of a sequence sees its keys 0 .. i + (keys - queries) */
+
 typedef struct sc_hash_s* sc_hash;
 typedef struct sc_kmap_s* sc_kmap;
 
@@ -441,6 +447,138 @@ sc_status sc_subm_conv_bwd_weight(sc_kmap m, const void* d_feats, const void* d_
  */
 sc_status sc_subm_conv_fwd_noalloc(sc_kmap m, const void* d_feats, const void* d_W, void* d_out, int c_in,
                                    int c_out, sc_dtype dtype, unsigned flags, sc_stream stream);
+
+/* ------------------------------------------------------------- tokens -- */
+
+/*
+ * Operators on token rows [tokens, heads, head_dim]: voxels packed scene after
+ * scene (or window after window), or text tokens.  The source pages have no
+ * counterpart; these are the layers that networks put beside the convolutions
+ * to mix voxels at a distance.
+ *
+ * A strided view of such rows: element (t, h, i) lies at data + t *
+ * token_stride + h * head_stride + i (strides in elements), so q, k and v may
+ * be parts of one projection's output.  data is device memory, 16-byte
+ * aligned, and both strides are multiples of 16 bytes.
+ */
+typedef struct {
+  const void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} sc_heads;
+/* The same for rows that a call writes.  Rows must not share memory: every
+ * token's heads lie apart. */
+typedef struct {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} sc_heads_out;
+
+/*
+ * Norm of each head of queries and keys, and the rotation by position, in one
+ * pass.  For each row x (head_dim values) of q and of k:
+ *   z = w * x / sqrt(mean(x^2) + eps), or z = x when both weights are NULL;
+ *   pair i of the first rot_dim values turns by phi = pos[t, axis(i)] * freq[i],
+ *   y_a = amp (z_a cos phi - z_b sin phi), y_b = amp (z_b cos phi + z_a sin phi);
+ *   the values from rot_dim on are z.
+ *
+ * q, k        rows of heads_q and heads_k heads; either count may be 0 (its
+ *             struct is then not read and may be NULL).
+ * d_w_q, d_w_k  fp32 [head_dim], or both NULL (no norm).  A side without
+ *             heads may pass NULL.
+ * d_pos       int32: token t's position on axis a is d_pos[t * pos_stride + a]
+ *             (any int32 value).  With axes = 3 and pos_stride = 4,
+ *             d_pos = d_coords + 1 rotates by a voxel's x, y and z.
+ * axes        in [1, 4]; rot_dim / 2 is a multiple of it, and pair i belongs to
+ *             axis i / (rot_dim / 2 / axes).
+ * d_freq      fp32 [rot_dim / 2], radians a position; scaled contexts scale
+ *             these (and amp).  The angle keeps its fraction of a turn at any
+ *             position.
+ * rot_dim     even, in [0, head_dim]; 0: no rotation (d_pos, d_freq may be NULL).
+ * head_dim    a multiple of 8 in [16, 256].
+ * dtype       of q, k and the outputs: SC_F32, SC_F16 or SC_BF16.  The norm and
+ *             the rotation run in fp32 and round once.
+ * out_q, out_k  may be q and k themselves (the same pointer and strides); any
+ *             other overlap is refused.
+ * flags       0 or SC_ROPE_INTERLEAVED.
+ */
+sc_status sc_qk_norm_rope_fwd(const sc_heads* q, const sc_heads* k, const sc_heads_out* out_q,
+                              const sc_heads_out* out_k, const float* d_w_q, const float* d_w_k,
+                              const int32_t* d_pos, int64_t pos_stride, int axes, const float* d_freq,
+                              int64_t tokens, int heads_q, int heads_k, int head_dim, int rot_dim, float eps,
+                              float amp, sc_dtype dtype, unsigned flags, sc_stream stream);
+
+/*
+ * Its gradients: gin_q, gin_k from the outputs' gradients gout_q, gout_k and
+ * the forward's inputs q, k (read only with a norm; else they may be NULL),
+ * and with a norm d_gw_q, d_gw_k fp32 [head_dim] (either may be NULL), summed
+ * over tokens and heads in an order that depends on the sizes alone, so that
+ * the same inputs give the same bits.  gin may be gout itself.  The other
+ * arguments as for the forward.
+ */
+sc_status sc_qk_norm_rope_bwd(const sc_heads* gout_q, const sc_heads* gout_k, const sc_heads* q, const sc_heads* k,
+                              const sc_heads_out* gin_q, const sc_heads_out* gin_k, float* d_gw_q, float* d_gw_k,
+                              const float* d_w_q, const float* d_w_k, const int32_t* d_pos, int64_t pos_stride,
+                              int axes, const float* d_freq, int64_t tokens, int heads_q, int heads_k, int head_dim,
+                              int rot_dim, float eps, float amp, sc_dtype dtype, unsigned flags, sc_stream stream);
+
+/*
+ * Attention over packed sequences.  Sequence s has the query rows
+ * [d_q_off[s], d_q_off[s+1]) and the key and value rows [d_k_off[s],
+ * d_k_off[s+1]), or [d_k_off[s], d_k_off[s] + d_k_len[s]) when d_k_len is not
+ * NULL (key lists that grow in place, with room between them).  Query head h
+ * reads key head h / (heads_q / heads_kv).  For each query row
+ *   S_j = scale * q . k_j,  lse = log sum_j exp(S_j),
+ *   out = sum_j exp(S_j - lse) v_j
+ * over the keys it sees: all of its sequence, or with SC_ATTN_CAUSAL keys
+ * j <= i + (keys - queries) for query i (the last query sees all).  A row that
+ * sees no key gets out = 0 and lse = -inf.  Sums and statistics are fp32;
+ * exp(S - max) is rounded to dtype for the second product, and out once.
+ *
+ * d_q_off, d_k_off  int32 [n_seq + 1], device memory, not decreasing;
+ *             d_q_off[0] = 0 and d_q_off[n_seq] = t_q (every query row
+ *             belongs to a sequence); keys within [0, t_k).  The arrays are
+ *             read and checked on the device: a violation writes no output and
+ *             is latched for sc_attn_check.  n_seq is below 2^20.
+ * d_k_len     int32 [n_seq] or NULL.
+ * heads_q     a multiple of heads_kv, at most 128 times it.
+ * head_dim    a multiple of 8 in [16, 128].
+ * d_lse       fp32 [t_q, heads_q], or NULL.
+ * scale       positive and finite.
+ * dtype       SC_F16 or SC_BF16.
+ * out         must not overlap q, k or v.
+ *
+ * Values of other sequences never reach a row, whatever they are (NaN
+ * included).  Inside a sequence a masked value takes part with weight 0, so a
+ * row is finite only if the keys and values after it in its 128-key block are.
+ * Temporary device memory is allocated and freed stream-ordered on `stream`.
+ */
+sc_status sc_attn_fwd(const sc_heads* q, const sc_heads* k, const sc_heads* v, const sc_heads_out* out,
+                      float* d_lse, const int32_t* d_q_off, const int32_t* d_k_off, const int32_t* d_k_len,
+                      int64_t n_seq, int64_t t_q, int64_t t_k, int heads_q, int heads_kv, int head_dim, float scale,
+                      sc_dtype dtype, unsigned flags, sc_stream stream);
+
+/*
+ * Its gradients, from the forward's inputs, out and d_lse and the gradient
+ * gout of out:
+ *   P = exp(S - lse), delta = gout . out, dS = P * (gout . v - delta),
+ *   gq_i = scale sum_j dS_ij k_j, gk_j = scale sum_i dS_ij q_i, gv_j = sum_i P_ij gout_i,
+ * gk and gv also summed over the query heads that share the key head.  P and
+ * dS are rounded to dtype for the products, sums are fp32, and each gradient
+ * is rounded once.  No atomics: the same inputs give the same bits.  Here the
+ * key lists are packed too: d_k_off[0] = 0 and d_k_off[n_seq] = t_k, so that
+ * every row of gk and gv is written.  The outputs must not overlap the inputs.
+ */
+sc_status sc_attn_bwd(const sc_heads* gout, const sc_heads* q, const sc_heads* k, const sc_heads* v,
+                      const sc_heads* out, const float* d_lse, const sc_heads_out* gq, const sc_heads_out* gk,
+                      const sc_heads_out* gv, const int32_t* d_q_off, const int32_t* d_k_off, int64_t n_seq,
+                      int64_t t_q, int64_t t_k, int heads_q, int heads_kv, int head_dim, float scale,
+                      sc_dtype dtype, unsigned flags, sc_stream stream);
+
+/* Synchronises the stream, returns the status latched by the attention calls
+ * on the current device since the last check (SC_ERR_OUT_OF_RANGE: offsets
+ * that break the rules above; SC_ERR_TIMEOUT) and clears it. */
+sc_status sc_attn_check(sc_stream stream);
 
 /* ------------------------------------------------------- device memory -- */
 

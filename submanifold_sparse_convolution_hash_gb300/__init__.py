@@ -13,10 +13,16 @@ from .binding import (  # noqa: F401
     profile_enable,
     profile_only,
     profile_reset,
+    rope_frequencies,
+    sc_attn_bwd,
+    sc_attn_check,
+    sc_attn_fwd,
     sc_hash_build,
     sc_hash_build_conv_out,
     sc_kmap_build,
     sc_kmap_build_conv,
+    sc_qk_norm_rope_bwd,
+    sc_qk_norm_rope_fwd,
     sc_subm_conv_bwd_data,
     sc_subm_conv_bwd_weight,
     sc_subm_conv_fwd,

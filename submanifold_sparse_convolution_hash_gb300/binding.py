@@ -8,6 +8,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -29,6 +30,8 @@ SC_KMAP_TRANSPOSE = 0x2000
 SC_KMAP_HALF = 0x4000
 SC_KMAP_SPLIT = 0x8000
 SC_KMAP_TILE_TABLE = 0x10000
+SC_ROPE_INTERLEAVED = 0x1
+SC_ATTN_CAUSAL = 0x1
 VARIANTS = {"fused": SC_VARIANT_FUSED, "ws": SC_VARIANT_WS, "simt": SC_VARIANT_SIMT, "split": SC_VARIANT_SPLIT}
 VARIANT_NAMES = {v: k for k, v in VARIANTS.items()}
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
@@ -56,6 +59,7 @@ def lib():
                                " or __graft_entry__.build()")
         L = ctypes.CDLL(_LIB_PATH)
         P, I64, I32, U = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint
+        F = ctypes.c_float
         sig = {
             "sc_hash_build": ([P, I64, P, P, P], I32),
             "sc_hash_query": ([P, P, I64, P, P], I32),
@@ -76,6 +80,11 @@ def lib():
             "sc_subm_conv_bwd_weight": ([P, P, P, P, I32, I32, I32, U, P], I32),
             "sc_subm_conv_tune": ([P, P, P, P, I32, I32, I32, U, I32, P, P], I32),
             "sc_subm_conv_fwd_noalloc": ([P, P, P, P, I32, I32, I32, U, P], I32),
+            "sc_qk_norm_rope_fwd": ([P] * 7 + [I64, I32, P, I64, I32, I32, I32, I32, F, F, I32, U, P], I32),
+            "sc_qk_norm_rope_bwd": ([P] * 11 + [I64, I32, P, I64, I32, I32, I32, I32, F, F, I32, U, P], I32),
+            "sc_attn_fwd": ([P] * 8 + [I64, I64, I64, I32, I32, I32, F, I32, U, P], I32),
+            "sc_attn_bwd": ([P] * 11 + [I64, I64, I64, I32, I32, I32, F, I32, U, P], I32),
+            "sc_attn_check": ([P], I32),
             "sc_set_allocator": ([P, P, P], I32),
             "sc_status_str": ([I32], ctypes.c_char_p),
             "sc_last_error": ([], ctypes.c_char_p),
@@ -100,7 +109,8 @@ def exported_symbols() -> list:
                         "sc_kmap_build", "sc_kmap_info", "sc_kmap_check", "sc_kmap_export", "sc_kmap_view",
                         "sc_kmap_destroy",
                         "sc_subm_conv_fwd", "sc_subm_conv_tune", "sc_subm_conv_fwd_noalloc",
-                        "sc_subm_conv_bwd_data", "sc_subm_conv_bwd_weight", "sc_set_allocator",
+                        "sc_subm_conv_bwd_data", "sc_subm_conv_bwd_weight", "sc_qk_norm_rope_fwd",
+                        "sc_qk_norm_rope_bwd", "sc_attn_fwd", "sc_attn_bwd", "sc_attn_check", "sc_set_allocator",
                         "sc_status_str", "sc_last_error",
                         "sc_launch_count", "sc_profile_enable", "sc_profile_only", "sc_profile_collect",
                         "sc_profile_reset",
@@ -127,6 +137,10 @@ def _dev(t: torch.Tensor, name: str) -> torch.Tensor:
 
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+
+
+def _ref(s):
+    return ctypes.byref(s) if s is not None else None
 
 
 class Hash:
@@ -433,6 +447,228 @@ def sc_subm_conv_tune(kmap: KernelMap, feats: torch.Tensor, W: torch.Tensor, out
                                    SC_RELU if relu else 0, reps, _stream(stream), ctypes.byref(chosen)),
            "sc_subm_conv_tune")
     return VARIANT_NAMES[chosen.value]
+
+
+class _Heads(ctypes.Structure):
+    """sc_heads / sc_heads_out: a strided view of rows [tokens, heads, head_dim]."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+def _heads(t, name: str, like=None, shape=None):
+    """The view struct of a CUDA tensor [tokens, heads, head_dim] whose last
+    dimension is contiguous (the other strides are free)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have the dtype and device of the other rows")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    ts, hs, ds = t.stride()
+    if ds != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return _Heads(t.data_ptr(), ts, hs)
+
+
+def _f32(t, name: str, n: int, device):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.float32 or t.shape != (n,):
+        raise ValueError(f"{name} must be a float32 [{n}] tensor on {device}")
+    return _dev(t, name)
+
+
+def _rope_args(first, pos, freq, wq, wk, heads_q, heads_k):
+    tokens, _, d = first.shape
+    if first.dtype not in _DTYPES:
+        raise ValueError("rows must be float32, float16 or bfloat16")
+    rot, axes, stride = 0, 1, 0
+    if freq is not None:
+        rot = 2 * freq.shape[0]
+        _f32(freq, "freq", rot // 2, first.device)
+        if (not isinstance(pos, torch.Tensor) or pos.device != first.device or pos.dtype != torch.int32
+                or pos.dim() not in (1, 2) or pos.shape[0] != tokens):
+            raise ValueError("pos must be int32 [tokens] or [tokens, axes] on the rows' device")
+        stride = pos.stride(0)
+        if pos.dim() == 2:
+            axes = pos.shape[1]
+            if axes > 1 and pos.stride(1) != 1:
+                raise ValueError("pos: the axes must be contiguous")
+    _f32(wq, "wq", d, first.device)
+    _f32(wk, "wk", d, first.device)
+    if (wq is None) != (wk is None) and heads_q and heads_k:
+        raise ValueError("pass both norm weights, or neither")
+    return tokens, d, rot, axes, stride
+
+
+def sc_qk_norm_rope_fwd(q, k, pos=None, freq=None, wq=None, wk=None, eps: float = 1e-6, interleaved: bool = False,
+                        amp: float = 1.0, out_q=None, out_k=None, stream=None):
+    """(q', k'): rows q [tokens, heads_q, head_dim] and k [tokens, heads_k,
+    head_dim] (one of them may be None) normed per head by wq, wk (float32
+    [head_dim], or None) and rotated by pos (int32 [tokens] or [tokens, axes])
+    times freq (float32 [rot_dim / 2]; rope_frequencies makes them).  out_q,
+    out_k: where to write (q and k themselves are allowed)."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("pass q, k or both")
+    hq, hk = (_heads(x, n, like=first) if x is not None else None for x, n in ((q, "q"), (k, "k")))
+    nq, nk = (x.shape[1] if x is not None else 0 for x in (q, k))
+    tokens, d, rot, axes, stride = _rope_args(first, pos, freq, wq, wk, nq, nk)
+    if q is not None and k is not None and (k.shape[0] != tokens or k.shape[2] != d):
+        raise ValueError("q and k must have the same tokens and head_dim")
+    if q is not None and out_q is None:
+        out_q = torch.empty((tokens, nq, d), dtype=first.dtype, device=first.device)
+    if k is not None and out_k is None:
+        out_k = torch.empty((tokens, nk, d), dtype=first.dtype, device=first.device)
+    oq = _heads(out_q, "out_q", first, q.shape) if q is not None else None
+    ok = _heads(out_k, "out_k", first, k.shape) if k is not None else None
+    _check(lib().sc_qk_norm_rope_fwd(_ref(hq), _ref(hk), _ref(oq), _ref(ok), _ptr(wq), _ptr(wk),
+                                     _ptr(pos) if rot else None, stride, axes, _ptr(freq), tokens, nq, nk, d, rot,
+                                     eps, amp, _DTYPES[first.dtype], SC_ROPE_INTERLEAVED if interleaved else 0,
+                                     _stream(stream)), "sc_qk_norm_rope_fwd")
+    return out_q, out_k
+
+
+def sc_qk_norm_rope_bwd(gout_q, gout_k, q=None, k=None, pos=None, freq=None, wq=None, wk=None, eps: float = 1e-6,
+                        interleaved: bool = False, amp: float = 1.0, gin_q=None, gin_k=None, stream=None):
+    """(gq, gk, gwq, gwk): the gradients of sc_qk_norm_rope_fwd's inputs and
+    weights from those of its outputs.  q, k: the forward's inputs (read only
+    with a norm); gwq, gwk are float32, None without a norm."""
+    first = gout_q if gout_q is not None else gout_k
+    if first is None:
+        raise ValueError("pass gout_q, gout_k or both")
+    gq, gk = (_heads(x, n, like=first) if x is not None else None
+              for x, n in ((gout_q, "gout_q"), (gout_k, "gout_k")))
+    nq, nk = (x.shape[1] if x is not None else 0 for x in (gout_q, gout_k))
+    tokens, d, rot, axes, stride = _rope_args(first, pos, freq, wq, wk, nq, nk)
+    if gout_q is not None and gout_k is not None and (gout_k.shape[0] != tokens or gout_k.shape[2] != d):
+        raise ValueError("gout_q and gout_k must have the same tokens and head_dim")
+    norm = wq is not None or wk is not None
+    hq = _heads(q, "q", first, gout_q.shape) if norm and gout_q is not None else None
+    hk = _heads(k, "k", first, gout_k.shape) if norm and gout_k is not None else None
+    if gout_q is not None and gin_q is None:
+        gin_q = torch.empty((tokens, nq, d), dtype=first.dtype, device=first.device)
+    if gout_k is not None and gin_k is None:
+        gin_k = torch.empty((tokens, nk, d), dtype=first.dtype, device=first.device)
+    iq = _heads(gin_q, "gin_q", first, gout_q.shape) if gout_q is not None else None
+    ik = _heads(gin_k, "gin_k", first, gout_k.shape) if gout_k is not None else None
+    gwq = torch.empty(d, dtype=torch.float32, device=first.device) if norm and nq else None
+    gwk = torch.empty(d, dtype=torch.float32, device=first.device) if norm and nk else None
+    _check(lib().sc_qk_norm_rope_bwd(_ref(gq), _ref(gk), _ref(hq), _ref(hk), _ref(iq), _ref(ik), _ptr(gwq),
+                                     _ptr(gwk), _ptr(wq), _ptr(wk), _ptr(pos) if rot else None, stride, axes,
+                                     _ptr(freq), tokens, nq, nk, d, rot, eps, amp, _DTYPES[first.dtype],
+                                     SC_ROPE_INTERLEAVED if interleaved else 0, _stream(stream)),
+           "sc_qk_norm_rope_bwd")
+    return gin_q, gin_k, gwq, gwk
+
+
+def rope_frequencies(rot_dim: int, axes: int = 1, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original: int = 8192, slow: float = 1.0, fast: float = 32.0, device=None):
+    """(freq, amp) for sc_qk_norm_rope_*: float32 [rot_dim / 2] radians a
+    position, pair i of an axis's n pairs turning by base^(-i/n), and the factor
+    of the rotated values.
+
+    scaling, for contexts `factor` times the `original` length:
+      "none"    as they are
+      "linear"  every frequency divided by factor
+      "base"    the base raised so that the slowest pair slows by factor
+      "parts"   pairs that make under `slow` turns over the original length are
+                divided by factor, those over `fast` kept, a ramp between, and
+                amp = 1 + 0.1 ln(factor)"""
+    if axes < 1 or rot_dim < 2 or rot_dim % (2 * axes):
+        raise ValueError("rot_dim must be a positive multiple of 2 * axes")
+    if not factor >= 1.0 or not base > 1.0:
+        raise ValueError("factor must be at least 1 and base above 1")
+    n = rot_dim // 2 // axes
+    i = torch.arange(n, dtype=torch.float64)
+    amp = 1.0
+    if scaling == "base" and n > 1:
+        base = base * factor ** (n / (n - 1))
+    freq = base ** (-i / n)
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "parts":
+        if not fast > slow:
+            raise ValueError("fast must be above slow")
+        turns = original * freq / (2 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0, 1)
+        freq = freq * (keep + (1 - keep) / factor)
+        amp = 1.0 + 0.1 * math.log(factor)
+    elif scaling not in ("none", "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return freq.float().repeat(axes).to(device), amp
+
+
+def _offsets(off, name: str, device):
+    if (not isinstance(off, torch.Tensor) or off.device != device or off.dtype != torch.int32 or off.dim() != 1
+            or off.shape[0] < 1):
+        raise ValueError(f"{name} must be an int32 vector on the rows' device")
+    return _dev(off, name)
+
+
+def _attn_common(q, k, v, q_off, k_off, scale):
+    hq = _heads(q, "q")
+    hk = _heads(k, "k", q)
+    hv = _heads(v, "v", q, k.shape)
+    if k.shape[2] != q.shape[2]:
+        raise ValueError("q, k and v must have one head_dim")
+    _offsets(q_off, "q_off", q.device)
+    if k_off is None:
+        k_off = q_off
+    elif _offsets(k_off, "k_off", q.device).shape != q_off.shape:
+        raise ValueError("k_off must have q_off's length")
+    if q.dtype not in _DTYPES:
+        raise ValueError("rows must be float16 or bfloat16")
+    return hq, hk, hv, k_off, q.shape[2] ** -0.5 if scale is None else scale
+
+
+def sc_attn_fwd(q, k, v, q_off, k_off=None, k_len=None, causal: bool = False, scale: float | None = None,
+                return_lse: bool = False, out=None, stream=None):
+    """out [t_q, heads_q, head_dim] = softmax(scale q k^T) v over packed
+    sequences: q [t_q, heads_q, head_dim], k and v [t_k, heads_kv, head_dim]
+    (any token and head strides), sequence s holding query rows q_off[s] ..
+    q_off[s+1] and key rows k_off[s] .. k_off[s+1] (default: q_off), or k_len[s]
+    rows from k_off[s] on.  causal: query i sees keys 0 .. i + keys - queries.
+    scale: default head_dim^-0.5.  return_lse: (out, lse float32 [t_q, heads_q])."""
+    hq, hk, hv, k_off, scale = _attn_common(q, k, v, q_off, k_off, scale)
+    n = q_off.shape[0] - 1
+    if k_len is not None and _offsets(k_len, "k_len", q.device).shape[0] != n:
+        raise ValueError("k_len must hold one length a sequence")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    ho = _heads(out, "out", q, q.shape)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
+    _check(lib().sc_attn_fwd(_ref(hq), _ref(hk), _ref(hv), _ref(ho), _ptr(lse), _ptr(q_off), _ptr(k_off),
+                             _ptr(k_len), n, q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2], scale,
+                             _DTYPES[q.dtype], SC_ATTN_CAUSAL if causal else 0, _stream(stream)), "sc_attn_fwd")
+    return (out, lse) if return_lse else out
+
+
+def sc_attn_bwd(gout, q, k, v, out, lse, q_off, k_off=None, causal: bool = False, scale: float | None = None,
+                gq=None, gk=None, gv=None, stream=None):
+    """(gq, gk, gv): gradients of sc_attn_fwd's inputs from gout, that of its
+    output, with the forward's out and lse.  gq, gk, gv: where to write."""
+    hq, hk, hv, k_off, scale = _attn_common(q, k, v, q_off, k_off, scale)
+    hg, ho = _heads(gout, "gout", q, q.shape), _heads(out, "out", q, q.shape)
+    if (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.device != q.device
+            or lse.shape != q.shape[:2]):
+        raise ValueError("lse must be the forward's float32 [t_q, heads_q]")
+    _dev(lse, "lse")
+    gq, gk, gv = (torch.empty(x.shape, dtype=q.dtype, device=q.device) if g is None else g
+                  for g, x in ((gq, q), (gk, k), (gv, v)))
+    oq, ok, ov = (_heads(g, n, q, x.shape) for g, n, x in ((gq, "gq", q), (gk, "gk", k), (gv, "gv", v)))
+    _check(lib().sc_attn_bwd(_ref(hg), _ref(hq), _ref(hk), _ref(hv), _ref(ho), _ptr(lse), _ref(oq), _ref(ok),
+                             _ref(ov), _ptr(q_off), _ptr(k_off), q_off.shape[0] - 1, q.shape[0], k.shape[0],
+                             q.shape[1], k.shape[1], q.shape[2], scale, _DTYPES[q.dtype],
+                             SC_ATTN_CAUSAL if causal else 0, _stream(stream)), "sc_attn_bwd")
+    return gq, gk, gv
+
+
+def sc_attn_check(stream=None):
+    """Synchronises and raises what the attention calls on the current device
+    latched since the last check (offsets that leave the rows)."""
+    _check(lib().sc_attn_check(_stream(stream)), "sc_attn_check")
 
 
 _ALLOC_FN = ctypes.CFUNCTYPE(ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p)

@@ -276,14 +276,12 @@ void dev_free(void* p, cudaStream_t s) {
   else cudaFreeAsync(p, s);
 }
 
-namespace {
-
 // A device (or managed) pointer with the given alignment; host memory is
 // refused: the library has no host path.
 sc_status check_dev_ptr(const void* p, size_t align, const char* what) {
   if (!p) return set_error(SC_ERR_INVALID_ARG, (std::string(what) + " is NULL").c_str());
   if (reinterpret_cast<uintptr_t>(p) % align)
-    return set_error(SC_ERR_INVALID_ARG, (std::string(what) + " is not 16-byte aligned").c_str());
+    return set_error(SC_ERR_INVALID_ARG, (std::string(what) + " is not " + std::to_string(align) + "-byte aligned").c_str());
   cudaPointerAttributes at;
   cudaError_t e = cudaPointerGetAttributes(&at, p);
   if (e != cudaSuccess) {
@@ -302,6 +300,8 @@ sc_status status_from_bits(int bits) {
   if (bits & kDevErrTimeout) return set_error(SC_ERR_TIMEOUT, "device-side wait timed out");
   return SC_OK;
 }
+
+namespace {
 
 // Reads the map's status words, segment offsets and weight-stationary tile
 // prefix into host mirrors; synchronises the stream.

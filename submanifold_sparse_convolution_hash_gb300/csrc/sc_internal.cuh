@@ -197,6 +197,52 @@ sc_status kmap_unpermute_nbr(const KernelMap* m, int* dst, cudaStream_t s);
 bool fused_supported(const ConvArgs& a);
 sc_status conv_fused_noalloc(const ConvArgs& a);
 
+// kernels: token rows (rope.cu, attn*.cu); side 0 is the queries', 1 the keys'
+struct RopeArgs {
+  sc_heads x[2];
+  sc_heads gy[2];   // backward: the outputs' gradients (data null: forward)
+  sc_heads_out y[2];
+  const float* w[2];
+  float* gw[2];
+  const int32_t* pos;
+  int64_t pos_stride;
+  int axes;
+  const float* freq;
+  int64_t tokens;
+  int heads_q, heads_k, head_dim, rot_dim;
+  float eps, amp;
+  sc_dtype dtype;
+  bool interleaved;
+  bool backward;
+  cudaStream_t stream;
+};
+sc_status rope_run(const RopeArgs& a);
+
+struct AttnArgs {
+  sc_heads q, k, v;
+  sc_heads out_in, gout;  // backward
+  sc_heads_out out;       // forward
+  sc_heads_out gq, gk, gv;
+  float* lse;             // read by the backward
+  const int32_t* q_off;
+  const int32_t* k_off;
+  const int32_t* k_len;
+  int64_t n_seq, t_q, t_k;
+  int heads_q, heads_kv, head_dim;
+  float scale;
+  sc_dtype dtype;
+  bool causal;
+  cudaStream_t stream;
+};
+sc_status attn_fwd(const AttnArgs& a);
+sc_status attn_bwd(const AttnArgs& a);
+// Reads and clears the status bits the attention kernels latched; synchronises.
+sc_status attn_take_status(cudaStream_t s, int* bits);
+
+// A device (or managed) pointer with the given alignment.
+sc_status check_dev_ptr(const void* p, size_t align, const char* what);
+sc_status status_from_bits(int bits);
+
 // stream-ordered allocation helpers: `with` (if not null) is the caller's
 // allocator of a build call, else the process-wide setting is used; a buffer
 // goes back to whichever allocator made it
