@@ -1,255 +1,248 @@
-// Attention over packed sequences: the plain forms of its kernels, one warp a
-// row, fp32 throughout.
-//   S = scale q k^T, lse = log sum exp S, out = softmax(S) v, and the gradients.
-#include "sc_internal.cuh"
+// Attention over packed sequences: the work list of its kernels, made on the
+// device from the sequence offsets, and the latched status.
+#include "attn_internal.cuh"
 
 namespace sc {
 namespace {
 
-__device__ int g_status;
+__device__ int g_attn_status;
 
-struct View {
-  const uint8_t* p;
-  int64_t ts, hs;
-};
-struct SimpleParams {
-  View q, k, v, out, gout, gq, gk, gv;
-  float* lse;
-  float* delta;
-  const int *q_off, *k_off, *k_len;
-  int n_seq;
-  int64_t t_q, t_k;
-  int hq, hk, g, d;
-  float scale;
-  int causal;
-  int* bad;
-};
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 256;
 
-template <typename T>
-__device__ __forceinline__ void load_row(const View& v, int64_t t, int h, int d, float (&x)[4]) {
-  const T* p = reinterpret_cast<const T*>(v.p) + t * v.ts + h * v.hs;
-  const int lane = threadIdx.x & 31;
+// Exclusive prefix sum over the block's threads; returns this thread's and
+// sets *total.
+__device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int x = v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = lane + 32 * i < d ? static_cast<float>(p[lane + 32 * i]) : 0.f;
-}
-template <typename T>
-__device__ __forceinline__ void store_row(const View& v, int64_t t, int h, int d, const float (&x)[4]) {
-  T* p = reinterpret_cast<T*>(const_cast<uint8_t*>(v.p)) + t * v.ts + h * v.hs;
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < d) p[lane + 32 * i] = T(x[i]);
-}
-__device__ __forceinline__ float dot(const float (&a)[4], const float (&b)[4]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) s = fmaf(a[i], b[i], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-// the sequence s with off[s] <= t < off[s + 1]
-__device__ __forceinline__ int find(const int* off, int n, int t) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (__ldg(off + m) <= t) lo = m;
-    else hi = m - 1;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  return lo;
-}
-struct Range {
-  int64_t q0, q1, k0, k1;
-};
-__device__ __forceinline__ Range range_of(const SimpleParams& p, int s) {
-  Range r;
-  r.q0 = p.q_off[s];
-  r.q1 = p.q_off[s + 1];
-  r.k0 = p.k_off[s];
-  r.k1 = p.k_len ? r.k0 + p.k_len[s] : p.k_off[s + 1];
-  return r;
-}
-
-// Checks the offsets; *bad stays 0 when every rule holds.
-__global__ void k_check(const SimpleParams p, int packed_keys) {
-  for (int s = threadIdx.x; s < p.n_seq; s += blockDim.x) {
-    const Range r = range_of(p, s);
-    bool bad = r.q0 < 0 || r.q1 > p.t_q || r.k0 < 0 || r.k1 > p.t_k || r.q1 < r.q0 || r.k1 < r.k0;
-    bad = bad || (s == 0 && r.q0 != 0) || (s == p.n_seq - 1 && r.q1 != p.t_q);
-    if (packed_keys) bad = bad || (s == 0 && r.k0 != 0) || (s == p.n_seq - 1 && r.k1 != p.t_k);
-    if (bad) {
-      *p.bad = 1;
-      atomicOr(&g_status, kDevErrRange);
+  if (lane == 31) s_warp[w] = x;
+  __syncthreads();
+  if (w == 0) {
+    int y = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
     }
+    s_warp[lane] = y;
   }
+  __syncthreads();
+  const int base = w ? s_warp[w - 1] : 0;
+  *total = s_warp[kPlanThreads / 32 - 1];
+  __syncthreads();
+  return base + x - v;
 }
 
-template <typename T>
-__global__ void k_simple_fwd(const SimpleParams p) {
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (w >= p.t_q * p.hq || *p.bad) return;
-  const int64_t t = w / p.hq;
-  const int h = static_cast<int>(w % p.hq);
-  const Range r = range_of(p, find(p.q_off, p.n_seq, static_cast<int>(t)));
-  const int64_t end = p.causal ? min(r.k1, r.k1 - (r.q1 - t) + 1) : r.k1;
-  float q[4], k[4], v[4], o[4] = {}, m = -INFINITY, l = 0.f;
-  load_row<T>(p.q, t, h, p.d, q);
-  for (int64_t j = r.k0; j < end; ++j) {
-    load_row<T>(p.k, j, h / p.g, p.d, k);
-    load_row<T>(p.v, j, h / p.g, p.d, v);
-    const float s = dot(q, k) * p.scale;
-    const float mn = fmaxf(m, s), c = m == mn ? 1.f : expf(m - mn), e = expf(s - mn);
-    l = l * c + e;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * c + e * v[i];
-    m = mn;
+// One block lists the work, dearest first: a unit's cost is its number of
+// 128-key (or 128-row) steps, and the kernels take units in the list's order
+// as they get free, so the cheap ones fill the end.  Three passes over the
+// units (their largest cost, a histogram of costs, their places), each over
+// runs of 1024 sequences whose offsets lie in shared memory.  Offsets are
+// checked first; a list that breaks a rule gives no work and latches the error.
+__global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs p) {
+  __shared__ int s_q[kPlanThreads + 1], s_k0[kPlanThreads], s_k1[kPlanThreads], s_pre[kPlanThreads + 1];
+  __shared__ int s_hist[kBuckets], s_warp[32];
+  __shared__ int s_bad, s_max, s_slots, s_groups;
+  __shared__ unsigned long long s_steps;
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    s_bad = 0;
+    s_max = 1;
+    s_slots = 0;
+    s_groups = 0;
+    s_steps = 0;
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = end > r.k0 ? o[i] / l : 0.f;
-  store_row<T>(p.out, t, h, p.d, o);
-  if (p.lse && (threadIdx.x & 31) == 0) p.lse[t * p.hq + h] = end > r.k0 ? m + logf(l) : -INFINITY;
-}
-
-template <typename T>
-__global__ void k_simple_gq(const SimpleParams p) {
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (w >= p.t_q * p.hq || *p.bad) return;
-  const int64_t t = w / p.hq;
-  const int h = static_cast<int>(w % p.hq);
-  const Range r = range_of(p, find(p.q_off, p.n_seq, static_cast<int>(t)));
-  const int64_t end = p.causal ? min(r.k1, r.k1 - (r.q1 - t) + 1) : r.k1;
-  float q[4], k[4], v[4], g[4], o[4], acc[4] = {};
-  load_row<T>(p.q, t, h, p.d, q);
-  load_row<T>(p.gout, t, h, p.d, g);
-  load_row<T>(p.out, t, h, p.d, o);
-  const float delta = dot(g, o), lse = p.lse[t * p.hq + h];
-  if ((threadIdx.x & 31) == 0) p.delta[t * p.hq + h] = delta;
-  for (int64_t j = r.k0; j < end; ++j) {
-    load_row<T>(p.k, j, h / p.g, p.d, k);
-    load_row<T>(p.v, j, h / p.g, p.d, v);
-    const float ds = expf(dot(q, k) * p.scale - lse) * (dot(g, v) - delta) * p.scale;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(ds, k[i], acc[i]);
-  }
-  store_row<T>(p.gq, t, h, p.d, acc);
-}
-
-template <typename T>
-__global__ void k_simple_gkv(const SimpleParams p) {
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (w >= p.t_k * p.hk || *p.bad) return;
-  const int64_t t = w / p.hk;
-  const int h = static_cast<int>(w % p.hk);
-  const Range r = range_of(p, find(p.k_off, p.n_seq, static_cast<int>(t)));
-  float q[4], k[4], v[4], g[4], ak[4] = {}, av[4] = {};
-  load_row<T>(p.k, t, h, p.d, k);
-  load_row<T>(p.v, t, h, p.d, v);
-  int64_t first = r.q0;
-  if (p.causal) first = max(first, r.q1 - (r.k1 - t));
-  for (int64_t i = first; i < r.q1; ++i)
-    for (int gh = h * p.g; gh < (h + 1) * p.g; ++gh) {
-      load_row<T>(p.q, i, gh, p.d, q);
-      load_row<T>(p.gout, i, gh, p.d, g);
-      const float pr = expf(dot(q, k) * p.scale - p.lse[i * p.hq + gh]);
-      const float ds = pr * (dot(g, v) - p.delta[i * p.hq + gh]) * p.scale;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        ak[c] = fmaf(ds, q[c], ak[c]);
-        av[c] = fmaf(pr, g[c], av[c]);
+  if (tid < kBuckets) s_hist[tid] = 0;
+  __syncthreads();
+  int chunk = 0;  // key tiles of a part, 0: whole
+  int my_max = 1;
+  unsigned long long my_steps = 0;
+  for (int pass = 0; pass < 3; ++pass) {
+    for (int c0 = 0; c0 < p.n_seq; c0 += kPlanThreads) {
+      const int cnt = min(kPlanThreads, p.n_seq - c0);
+      __syncthreads();
+      int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+      if (tid < cnt) {
+        const int s = c0 + tid;
+        q0 = __ldg(p.q_off + s);
+        q1 = __ldg(p.q_off + s + 1);
+        k0 = __ldg(p.k_off + s);
+        k1 = p.k_len ? k0 : __ldg(p.k_off + s + 1);
+        bool bad = false;
+        if (p.k_len) {
+          const int len = __ldg(p.k_len + s);
+          bad = len < 0 || k0 < 0 || k0 + static_cast<int64_t>(len) > p.t_k;
+          if (!bad) k1 = k0 + len;
+        }
+        bad = bad || q0 < 0 || q1 < q0 || q1 > p.t_q || k0 < 0 || k1 < k0 || k1 > p.t_k;
+        bad = bad || (s == 0 && q0 != 0) || (s == p.n_seq - 1 && q1 != p.t_q);
+        if (p.packed_keys) bad = bad || (s == 0 && k0 != 0) || (s == p.n_seq - 1 && k1 != p.t_k);
+        if (bad) s_bad = 1;
+        s_q[tid] = q0;
+        s_k0[tid] = k0;
+        s_k1[tid] = k1;
+        if (tid == cnt - 1) s_q[cnt] = q1;
       }
+      __syncthreads();
+      if (s_bad) break;
+      int tiles = 0;
+      if (tid < cnt)
+        tiles = p.mode == kPlanRows ? (q1 - q0 + p.pos_per_item - 1) / p.pos_per_item
+                                    : (k1 - k0 + kKeyTile - 1) / kKeyTile;
+      int total;
+      s_pre[tid] = block_scan(tiles, s_warp, &total);
+      if (tid == 0) s_pre[cnt] = total;  // cnt == kPlanThreads: its own place
+      __syncthreads();
+      for (int u = tid; u < total; u += kPlanThreads) {
+        int lo = 0, hi = cnt - 1;  // the sequence with s_pre[lo] <= u < s_pre[lo + 1]
+        while (lo < hi) {
+          const int m = (lo + hi + 1) >> 1;
+          if (s_pre[m] <= u) lo = m;
+          else hi = m - 1;
+        }
+        const int t = u - s_pre[lo];
+        const int lq = s_q[lo + 1] - s_q[lo], lk = s_k1[lo] - s_k0[lo];
+        AttnItem it;
+        int cost;
+        if (p.mode == kPlanRows) {
+          const int i0 = t * p.pos_per_item;
+          it.q_row = s_q[lo] + i0;
+          it.n_pos = min(p.pos_per_item, lq - i0);
+          it.lim0 = i0 + lk - lq;
+          const int seen = p.causal ? max(0, min(lk, it.lim0 + it.n_pos)) : lk;
+          it.kt0 = 0;
+          it.kt1 = (seen + kKeyTile - 1) / kKeyTile;
+          cost = it.kt1;
+        } else {
+          it.q_row = s_q[lo];
+          it.n_pos = lq;
+          it.lim0 = lk - lq;
+          it.kt0 = t;
+          it.kt1 = t + 1;
+          const int first = p.causal ? max(0, t * kKeyTile - it.lim0) : 0;  // first query that sees the tile
+          cost = (max(0, lq - first) + p.pos_per_item - 1) / p.pos_per_item;
+        }
+        it.k_row = s_k0[lo];
+        it.lk = lk;
+        it.pad = 0;
+        const int ns = chunk && cost > chunk ? (cost + chunk - 1) / chunk : 1;
+        const int part = (cost + ns - 1) / ns;
+        if (pass == 0) {
+          my_max = max(my_max, cost);
+          my_steps += static_cast<unsigned long long>(cost);
+        } else if (pass == 1) {
+          const int b = static_cast<int>(static_cast<int64_t>(kBuckets - 1) * part / s_max);
+          atomicAdd(&s_hist[kBuckets - 1 - b], ns);
+        } else {
+          const int b = static_cast<int>(static_cast<int64_t>(kBuckets - 1) * part / s_max);
+          int at = atomicAdd(&s_hist[kBuckets - 1 - b], ns);
+          it.nsplit = ns;
+          it.slot = -1;
+          it.group = 0;
+          if (ns > 1) {
+            it.slot = atomicAdd(&s_slots, ns);
+            it.group = atomicAdd(&s_groups, 1);
+          }
+          const int end = it.kt1;
+          for (int i = 0; i < ns; ++i, ++at) {
+            it.split = i;
+            if (ns > 1) {
+              it.kt0 = min(end, i * part);
+              it.kt1 = min(end, it.kt0 + part);
+            }
+            if (at < p.cap) p.items[at] = it;
+          }
+        }
+      }
+      __syncthreads();
     }
-  store_row<T>(p.gk, t, h, p.d, ak);
-  store_row<T>(p.gv, t, h, p.d, av);
+    if (s_bad) break;
+    if (pass == 0) {
+      my_max = __reduce_max_sync(0xffffffffu, my_max);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) my_steps += __shfl_xor_sync(0xffffffffu, my_steps, o);
+      if ((tid & 31) == 0) {
+        atomicMax(&s_max, my_max);
+        atomicAdd(&s_steps, my_steps);
+      }
+      __syncthreads();
+    }
+    if (pass == 0 && p.split_units > 0) {
+      const unsigned long long steps = s_steps * p.heads_kv;
+      const unsigned long long c = (steps + p.split_units - 1) / p.split_units;
+      chunk = static_cast<int>(c < static_cast<unsigned long long>(p.min_tiles) ? p.min_tiles : c);
+      __syncthreads();
+      if (tid == 0) s_max = min(s_max, chunk);
+      __syncthreads();
+    }
+    if (pass == 1) {
+      __syncthreads();
+      int total;
+      const int v = tid < kBuckets ? s_hist[tid] : 0;
+      const int e = block_scan(v, s_warp, &total);
+      if (tid < kBuckets) s_hist[tid] = e;
+      if (tid == 0) p.header[0] = min(total, p.cap);
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    if (s_bad || p.n_seq == 0) p.header[0] = 0;
+    if (s_bad) atomicOr(p.status, kDevErrRange);
+    p.header[1] = 0;
+    p.header[2] = s_slots;
+    p.header[3] = s_groups;
+  }
+  const int n_done = min(p.done_cap, s_groups * p.heads_kv * 8);
+  for (int i = tid; i < n_done; i += kPlanThreads) p.done[i] = 0;
 }
-
-View view(const sc_heads& v) { return {static_cast<const uint8_t*>(v.data), v.token_stride, v.head_stride}; }
-View view(const sc_heads_out& v) { return {static_cast<const uint8_t*>(v.data), v.token_stride, v.head_stride}; }
-
-SimpleParams params(const AttnArgs& a) {
-  SimpleParams p{};
-  p.q = view(a.q);
-  p.k = view(a.k);
-  p.v = view(a.v);
-  p.lse = a.lse;
-  p.q_off = a.q_off;
-  p.k_off = a.k_off;
-  p.k_len = a.k_len;
-  p.n_seq = static_cast<int>(a.n_seq);
-  p.t_q = a.t_q;
-  p.t_k = a.t_k;
-  p.hq = a.heads_q;
-  p.hk = a.heads_kv;
-  p.g = a.heads_q / a.heads_kv;
-  p.d = a.head_dim;
-  p.scale = a.scale;
-  p.causal = a.causal;
-  return p;
-}
-sc_status check_offsets(SimpleParams& p, const AttnArgs& a, bool packed_keys) {
-  void* bad = nullptr;
-  const sc_status st = dev_alloc(&bad, sizeof(int), a.stream);
-  if (st) return st;
-  p.bad = static_cast<int*>(bad);
-  cudaMemsetAsync(bad, 0, sizeof(int), a.stream);
-  SC_LAUNCH("attn_check", a.stream, (k_check<<<1, 256, 0, a.stream>>>(p, packed_keys)));
-  return SC_OK;
-}
-unsigned blocks(int64_t warps) { return static_cast<unsigned>((warps + 7) / 8); }
 
 }  // namespace
 
-sc_status attn_fwd(const AttnArgs& a) {
-  SimpleParams p = params(a);
-  p.out = view(a.out);
-  const sc_status st = check_offsets(p, a, false);
-  if (st) return st;
-  const unsigned n = blocks(a.t_q * a.heads_q);
-  SC_LAUNCH("attn_fwd", a.stream,
-            (a.dtype == SC_F16 ? k_simple_fwd<__half><<<n, 256, 0, a.stream>>>(p)
-                               : k_simple_fwd<__nv_bfloat16><<<n, 256, 0, a.stream>>>(p)));
-  const cudaError_t e = cudaGetLastError();
-  dev_free(p.bad, a.stream);
-  return e == cudaSuccess ? SC_OK : set_cuda_error(e, "attn_fwd");
+int* attn_status_word() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_attn_status) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
-sc_status attn_bwd(const AttnArgs& a) {
-  SimpleParams p = params(a);
-  p.out = view(a.out_in);
-  p.gout = view(a.gout);
-  p.gq = view(a.gq);
-  p.gk = view(a.gk);
-  p.gv = view(a.gv);
-  void* delta = nullptr;
-  sc_status st = dev_alloc(&delta, sizeof(float) * a.t_q * a.heads_q, a.stream);
-  if (st) return st;
-  p.delta = static_cast<float*>(delta);
-  if ((st = check_offsets(p, a, true))) {
-    dev_free(delta, a.stream);
-    return st;
-  }
-  if (a.t_q > 0) {
-    const unsigned n = blocks(a.t_q * a.heads_q);
-    SC_LAUNCH("attn_bwd_q", a.stream,
-              (a.dtype == SC_F16 ? k_simple_gq<__half><<<n, 256, 0, a.stream>>>(p)
-                                 : k_simple_gq<__nv_bfloat16><<<n, 256, 0, a.stream>>>(p)));
-  }
-  if (a.t_k > 0) {
-    const unsigned n = blocks(a.t_k * a.heads_kv);
-    SC_LAUNCH("attn_bwd_kv", a.stream,
-              (a.dtype == SC_F16 ? k_simple_gkv<__half><<<n, 256, 0, a.stream>>>(p)
-                                 : k_simple_gkv<__nv_bfloat16><<<n, 256, 0, a.stream>>>(p)));
-  }
-  dev_free(delta, a.stream);
-  dev_free(p.bad, a.stream);
+sc_status attn_plan(const PlanArgs& a, cudaStream_t s) {
+  SC_LAUNCH("attn_plan", s, (k_attn_plan<<<1, kPlanThreads, 0, s>>>(a)));
   const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? SC_OK : set_cuda_error(e, "attn_bwd");
+  return e == cudaSuccess ? SC_OK : set_cuda_error(e, "attn_plan");
+}
+
+// The map of rows [tokens, heads, d] for boxes of 64 values x box_heads x
+// box_tokens, rows of 128 bytes in shared memory with their 16-byte pieces
+// swizzled as the matrix descriptors expect; past the ends it reads zeros.
+sc_status attn_map(CUtensorMap* m, const void* data, sc_dtype dt, int d, int heads, int64_t tokens, int64_t ts,
+                   int64_t hs, int box_heads, int box_tokens) {
+  const EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return set_error(SC_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  // a dimension of one row needs a legal stride all the same
+  const int64_t row = (static_cast<int64_t>(d) * 2 + 15) / 16 * 16;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? hs * 2 : row),
+                                 static_cast<cuuint64_t>(tokens > 1 ? ts * 2 : row)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(m, dt == SC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                         const_cast<void*>(data), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(SC_ERR_UNSUPPORTED, "these strides make no tensor map");
+  return SC_OK;
 }
 
 sc_status attn_take_status(cudaStream_t s, int* bits) {
   const int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_attn_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_attn_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   return e == cudaSuccess ? SC_OK : set_cuda_error(e, "attention status");
 }

@@ -1,0 +1,632 @@
+// Attention forward over packed sequences.
+//
+// A block takes one item (up to 2 P queries of a sequence, a key head, a run of
+// 128-key tiles) at a time.  Its queries are two tiles of 128 packed rows.  Per
+// key tile and row tile
+//   S = Q K^T                        tensor cores, 128 x 128 in TMEM
+//   m' = max(m, max S), P = exp2((S - m') scale log2 e), l = l 2^(..) + sum P
+//   O = O 2^((m - m') ..) + P V      P back in TMEM as the first operand
+// so the scores never leave the SM.  One warp loads by TMA, one issues the
+// products, and each row tile has four warps of its own for the exponentials,
+// a row a thread; while one tile's exponentials run, the other tile's products
+// do.  O is corrected only when a row's maximum grew by more than 2^8: until
+// then P is up to 256 instead of 1, which costs no bits in floating point.
+#include "attn_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace sc {
+namespace {
+
+constexpr int kFwdThreads = 384;
+constexpr int kFwdMaxStages = 10;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct FwdParams {
+  uint8_t* out;
+  int64_t out_t, out_h;  // bytes
+  float* lse;            // [t_q, heads_q] or null
+  const int* header;
+  int* counter;          // next unit
+  const AttnItem* items;
+  int* done;
+  float* part;           // partial results [slot][head][2 * 128 rows][d + 2]
+  int heads_q, heads_kv, g, pos;  // pos: queries of a row tile
+  int d;
+  float scale_log2, scale;
+  int causal;
+  int stages;
+  int* status;
+};
+
+struct FwdSmem {
+  uint64_t full[kFwdMaxStages], empty[kFwdMaxStages];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_ready[2], o_full[2];
+  uint64_t fix_v, v_fixed;
+  uint64_t it_full[2], it_empty[2];
+  uint64_t drained;
+  uint32_t tmem;
+  int abort;
+  int fix_at, fix_rows;  // ring stage of a V tile that ends inside, and its keys
+  AttnItem item[2];
+  int head[2];  // -1: no more work
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Key tiles that row tile s of the item has to see: [kt0, end).
+__device__ __forceinline__ int tile_end(const FwdParams& p, const AttnItem& it, int s) {
+  const int n = min(it.n_pos - s * p.pos, p.pos);  // queries of the tile
+  if (n <= 0) return it.kt0;
+  const int seen = p.causal ? min(it.lk, it.lim0 + s * p.pos + n) : it.lk;
+  const int end = (max(seen, 0) + kKeyTile - 1) / kKeyTile;
+  return max(it.kt0, min(end, it.kt1));
+}
+
+// Receives the next item; false: no more.  Every waiting thread passes its own
+// phase counter.
+struct ItemRing {
+  uint32_t n = 0;
+  __device__ __forceinline__ bool next(FwdSmem* sm, AttnItem* it, int* head, bool one_per_warp) {
+    const int slot = n & 1;
+    bool ok = mbar_wait_inl(smem_u32(&sm->it_full[slot]), (n >> 1) & 1, &sm->abort);
+    if (one_per_warp) ok = __all_sync(0xffffffffu, ok);
+    if (!ok) {
+      sm->abort = 1;
+      return false;
+    }
+    *it = sm->item[slot];
+    *head = sm->head[slot];
+    if (one_per_warp) {
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm->it_empty[slot]));
+    } else {
+      mbar_arrive(smem_u32(&sm->it_empty[slot]));
+    }
+    ++n;
+    return *head >= 0;
+  }
+};
+
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    k_attn_fwd(const FwdParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+               const __grid_constant__ CUtensorMap vmap) {
+  constexpr int PANELS = DP / 64;
+  constexpr uint32_t PANEL = 128 * 128;          // bytes of 128 rows x 64 values
+  constexpr uint32_t TILE = PANELS * PANEL;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sq = smem_u32(smem);            // two Q tiles
+  const uint32_t skv = sq + 2 * TILE;            // ring of K and V tiles
+  const int S = p.stages;
+  FwdSmem* sm = reinterpret_cast<FwdSmem*>(smem + (2 + S) * TILE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sm->abort;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&sm->full[s]), 1);
+      mbar_init(smem_u32(&sm->empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sm->q_full), 1);
+    mbar_init(smem_u32(&sm->q_empty), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sm->s_full[s]), 1);
+      mbar_init(smem_u32(&sm->p_ready[s]), 4);
+      mbar_init(smem_u32(&sm->o_full[s]), 1);
+      mbar_init(smem_u32(&sm->it_full[s]), 1);
+      mbar_init(smem_u32(&sm->it_empty[s]), 11);  // 8 softmax warps, TMA, MMA, tail
+    }
+    mbar_init(smem_u32(&sm->fix_v), 1);
+    mbar_init(smem_u32(&sm->v_fixed), 1);
+    mbar_init(smem_u32(&sm->drained), 1);
+    sm->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&sm->tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem;
+  const uint32_t t_s[2] = {tmem, tmem + 128}, t_o[2] = {tmem + 256, tmem + 384};
+  const int n_items = p.header[0];
+  const int units = n_items * p.heads_kv;
+
+  if (warp == 8) {
+    // =========================================================== loads
+    if (lane == 0) {
+      ItemRing ring;
+      AttnItem it;
+      int head;
+      uint32_t k = 0, nq = 0;
+      const uint32_t q_bytes = static_cast<uint32_t>(p.pos * p.g) * 128;
+      while (ring.next(sm, &it, &head, false)) {
+        const int e0 = tile_end(p, it, 0), e1 = tile_end(p, it, 1);
+        const int end = max(e0, e1);
+        if (end <= it.kt0) continue;
+        if (!mbar_wait_inl(smem_u32(&sm->q_empty), (nq & 1) ^ 1, abort_flag)) {
+          sm->abort = 1;
+          break;
+        }
+        ++nq;
+        const int tiles = (e0 > it.kt0 ? 1 : 0) + (e1 > it.kt0 ? 1 : 0);
+        mbar_arrive_expect_tx(smem_u32(&sm->q_full), tiles * PANELS * q_bytes);
+        for (int s = 0; s < 2; ++s) {
+          if ((s ? e1 : e0) <= it.kt0) continue;
+          for (int c = 0; c < PANELS; ++c)
+            tma_load_3d(sq + s * TILE + c * PANEL, &qmap, c * 64, head * p.g, it.q_row + s * p.pos,
+                        smem_u32(&sm->q_full));
+        }
+        bool ok = true;
+        for (int j = it.kt0; j < end && ok; ++j)
+          for (int kv = 0; kv < 2; ++kv, ++k) {
+            const int st = static_cast<int>(k % S);
+            if (!mbar_wait_inl(smem_u32(&sm->empty[st]), ((k / S) & 1) ^ 1, abort_flag)) {
+              sm->abort = 1;
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(smem_u32(&sm->full[st]), TILE);
+            for (int c = 0; c < PANELS; ++c)
+              tma_load_3d(skv + st * TILE + c * PANEL, kv ? &vmap : &kmap, c * 64, head, it.k_row + j * kKeyTile,
+                          smem_u32(&sm->full[st]));
+          }
+        if (!ok) break;
+      }
+      // every copy has landed before the block may end
+      if (nq > 0 && !mbar_drain_inl(smem_u32(&sm->q_full), (nq - 1) & 1)) sm->abort = 1;
+      const uint32_t first = k > static_cast<uint32_t>(S) ? k - S : 0;
+      for (uint32_t i = first; i < k; ++i)
+        if (!mbar_drain_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ======================================================== products
+    if (lane == 0) {
+      const uint32_t id_s = make_idesc(BF16, 128, 128);
+      const int dn = (p.d + 15) & ~15;
+      const uint32_t id_o = make_idesc(BF16, 128, dn) | (1u << 16);  // V: consecutive values of one key
+      const int ksteps = dn / 16;
+      const uint64_t dq[2] = {smem_desc(sq, 1024, 2), smem_desc(sq + TILE, 1024, 2)};
+      const uint64_t dk = smem_desc(skv, 1024, 2);
+      const uint64_t dv = smem_desc_mn(skv, PANEL, 1024, 2);
+      ItemRing ring;
+      AttnItem it;
+      int head;
+      uint32_t k = 0, nq = 0, nfix = 0;
+      uint32_t np[2] = {0, 0};
+      auto scores = [&](int s, uint32_t stage) {
+        for (int i = 0; i < ksteps; ++i) {
+          const uint32_t off = ((i >> 2) * PANEL + (i & 3) * 32) >> 4;
+          tc_mma(t_s[s], dq[s] + off, dk + ((stage * TILE) >> 4) + off, id_s, i > 0);
+        }
+        tc_commit(smem_u32(&sm->s_full[s]));
+      };
+      while (ring.next(sm, &it, &head, false)) {
+        const int end[2] = {tile_end(p, it, 0), tile_end(p, it, 1)};
+        const int last = max(end[0], end[1]);
+        if (last <= it.kt0) continue;
+        bool ok = mbar_wait_inl(smem_u32(&sm->q_full), nq & 1, abort_flag);
+        ++nq;
+        ok = ok && mbar_wait_inl(smem_u32(&sm->full[k % S]), (k / S) & 1, abort_flag);
+        if (!ok) {
+          sm->abort = 1;
+          break;
+        }
+        tc_fence_after();
+        for (int s = 0; s < 2; ++s)
+          if (end[s] > it.kt0) scores(s, k % S);
+        tc_commit(smem_u32(&sm->empty[k % S]));
+        if (last == it.kt0 + 1) tc_commit(smem_u32(&sm->q_empty));
+        ++k;
+        for (int j = it.kt0; j < last; ++j) {
+          const uint32_t kv = k++;  // V of tile j
+          ok = mbar_wait_inl(smem_u32(&sm->full[kv % S]), (kv / S) & 1, abort_flag);
+          const bool tail = it.lk - j * kKeyTile < kKeyTile;
+          if (ok && tail) {  // warp 11 zeroes the rows past the keys meanwhile
+            sm->fix_at = static_cast<int>(kv % S);
+            sm->fix_rows = it.lk - j * kKeyTile;
+            mbar_arrive(smem_u32(&sm->fix_v));
+          }
+          const bool more = j + 1 < last;
+          if (ok && more) ok = mbar_wait_inl(smem_u32(&sm->full[k % S]), (k / S) & 1, abort_flag);
+          bool fixed = false;
+          for (int s = 0; s < 2 && ok; ++s) {
+            if (j >= end[s]) continue;
+            ok = mbar_wait_inl(smem_u32(&sm->p_ready[s]), np[s]++ & 1, abort_flag);
+            if (ok && tail && !fixed) ok = fixed = mbar_wait_inl(smem_u32(&sm->v_fixed), nfix++ & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t bv = dv + (((kv % S) * TILE) >> 4);
+            for (int i = 0; i < kKeyTile / 16; ++i)
+              tc_mma_ts(t_o[s], t_s[s] + i * 8, bv + ((i * 2048) >> 4), id_o, (j > it.kt0 || i > 0) ? 1u : 0u);
+            if (j + 1 == end[s]) tc_commit(smem_u32(&sm->o_full[s]));
+            if (j + 1 < end[s]) scores(s, k % S);
+          }
+          if (!ok) break;
+          tc_commit(smem_u32(&sm->empty[kv % S]));
+          if (more) {
+            tc_commit(smem_u32(&sm->empty[k % S]));
+            if (j + 2 == last) tc_commit(smem_u32(&sm->q_empty));
+            ++k;
+          }
+        }
+        if (!ok) {
+          sm->abort = 1;
+          break;
+        }
+      }
+      tc_commit(smem_u32(&sm->drained));  // every product is done before TMEM is freed
+      if (!mbar_drain_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ====================================================== work units
+    if (lane == 0) {
+      for (uint32_t n = 0;; ++n) {
+        const int slot = n & 1;
+        const int u = atomicAdd(p.counter, 1);
+        if (!mbar_wait_inl(smem_u32(&sm->it_empty[slot]), ((n >> 1) & 1) ^ 1, abort_flag)) {
+          sm->abort = 1;
+          break;
+        }
+        if (u < units) {
+          const uint4* src = reinterpret_cast<const uint4*>(p.items + u / p.heads_kv);
+          uint4* dst = reinterpret_cast<uint4*>(&sm->item[slot]);
+          dst[0] = src[0];
+          dst[1] = src[1];
+          dst[2] = src[2];
+        }
+        sm->head[slot] = u < units ? u % p.heads_kv : -1;
+        mbar_arrive(smem_u32(&sm->it_full[slot]));
+        if (u >= units) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    // ==================================================== tail of V
+    // Rows of a V tile past the sequence's keys belong to someone else (or to
+    // nobody).  Their weights are zero, but zero times a NaN or an infinity is
+    // not, so they are zeroed before the product.
+    ItemRing ring;
+    AttnItem it;
+    int head;
+    uint32_t n = 0;
+    while (ring.next(sm, &it, &head, true)) {
+      const int end = max(tile_end(p, it, 0), tile_end(p, it, 1));
+      if (end <= it.kt0 || it.lk - (end - 1) * kKeyTile >= kKeyTile) continue;
+      // the issuing warp asks once the tile has landed
+      if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->fix_v), n & 1, abort_flag))) {
+        sm->abort = 1;
+        break;
+      }
+      ++n;
+      const int rows = sm->fix_rows;
+      uint8_t* v = smem + (2 + sm->fix_at) * TILE;
+      for (int c = 0; c < PANELS; ++c)
+        for (int i = rows * 8 + lane; i < kKeyTile * 8; i += 32)
+          *reinterpret_cast<uint4*>(v + c * PANEL + i * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm->v_fixed));
+    }
+    __syncwarp();
+  } else {
+    // ======================================================== softmax
+    const int s = warp >> 2;                      // row tile
+    const int row = threadIdx.x & 127;
+    const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;
+    const uint32_t ts = t_s[s] + lane_off, to = t_o[s] + lane_off;
+    const int pos = row / p.g, gh = row - pos * p.g;
+    const float sl = p.scale_log2;
+    const float grow = 8.f / sl;                  // growth of the maximum that is let stand
+    ItemRing ring;
+    AttnItem it;
+    int head;
+    uint32_t ns = 0, no = 0;
+    while (ring.next(sm, &it, &head, true)) {
+      const int end = tile_end(p, it, s);
+      const int i = s * p.pos + pos;              // this row's query in the item
+      const bool live = pos < p.pos && i < it.n_pos;
+      const int vis = p.causal ? min(it.lk, it.lim0 + i + 1) : it.lk;  // keys it sees
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = it.kt0; j < end; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->s_full[s]), ns & 1, abort_flag));
+        ++ns;
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[128];
+        tmem_ld128_raw(ts, x);
+        const int seen = vis - j * kKeyTile;
+        if (__any_sync(0xffffffffu, seen < kKeyTile)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= seen) x[c] = 0xff800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 128; c += 4)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(x[c + u]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool raise = mt > m + grow || (m == -INFINITY && mt > m);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float mn = raise ? mt : m;
+          const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sl);  // 1 for rows that stay
+          m = mn;
+          l *= f;
+          if (j > it.kt0) {
+            for (int c = 0; c < p.d; c += 16) {
+              uint32_t o[16];
+              tmem_ld16_raw(to + c, o);
+#pragma unroll
+              for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+              tmem_st16(to + c, o);
+            }
+          }
+        }
+        // (S - m) first, then the scale: the product m * scale alone would be off
+        // by its own rounding, which a large score turns into whole powers of two
+        const float mm = m == -INFINITY ? 0.f : -m;
+        const uint64_t nm = pair2(mm, mm), sl2 = pair2(sl, sl);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 128; c += 2) {
+          const uint64_t y = mul2(add2(pair2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), nm), sl2);
+          float e0, e1;
+          unpair2(y, e0, e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair2(e0, e1));
+          x[c / 2] = pack_pair<BF16>(e0, e1);
+        }
+        float s0, s1;
+        unpair2(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+        tmem_st32(ts, x);
+        tmem_st32(ts + 32, x + 32);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm->p_ready[s]));
+      }
+      if (!ok) {
+        sm->abort = 1;
+        break;
+      }
+      const bool have = end > it.kt0;
+      if (have) {
+        if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->o_full[s]), no & 1, abort_flag))) {
+          sm->abort = 1;
+          break;
+        }
+        ++no;
+        tc_fence_after();
+      }
+      const int64_t tok = static_cast<int64_t>(it.q_row) + i;
+      const int h = head * p.g + gh;
+      if (it.slot < 0) {
+        const float inv = vis > 0 ? 1.f / l : 0.f;  // a row that sees no key: 0
+        uint8_t* dst = p.out + tok * p.out_t + h * p.out_h;
+        for (int c = 0; c < p.d; c += 16) {
+          uint32_t o[16];
+          if (have) {
+            tmem_ld16_raw(to + c, o);
+          }
+          uint32_t w[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            w[u] = have && vis > 0 ? pack_pair<BF16>(__uint_as_float(o[2 * u]) * inv, __uint_as_float(o[2 * u + 1]) * inv)
+                                   : 0u;
+          if (live) {
+            *reinterpret_cast<uint4*>(dst + c * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (c + 8 < p.d) *reinterpret_cast<uint4*>(dst + c * 2 + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+        if (p.lse && live) p.lse[tok * p.heads_q + h] = vis > 0 ? m * p.scale + logf(l) : -INFINITY;
+      } else {
+        // a part of the keys: O, m and l in fp32
+        const int64_t pr = (static_cast<int64_t>(it.slot + it.split) * p.heads_kv + head) * 256 + threadIdx.x;
+        float* dst = p.part + pr * (p.d + 8);
+        if (live) {
+          dst[p.d] = have ? m : -INFINITY;
+          dst[p.d + 1] = l;
+        }
+        for (int c = 0; c < p.d && have; c += 8) {
+          uint32_t o[16];
+          tmem_ld16_raw(to + (c & ~15), o);
+          if (live) {
+            const int b = c & 8;
+            *reinterpret_cast<uint4*>(dst + c) = b ? make_uint4(o[8], o[9], o[10], o[11]) : make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + c + 4) = b ? make_uint4(o[12], o[13], o[14], o[15]) : make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+        // A warp's rows are joined by the warp that finishes their last part:
+        // no wait on anybody, and in the parts' order whoever comes last.
+        __threadfence();
+        __syncwarp();
+        int was = 0;
+        if (lane == 0) was = atomicAdd(p.done + (it.group * p.heads_kv + head) * 8 + warp, 1);
+        was = __shfl_sync(0xffffffffu, was, 0);
+        if (was == it.nsplit - 1 && live) {
+          __threadfence();
+          const int64_t step = static_cast<int64_t>(p.heads_kv) * 256 * (p.d + 8);
+          const float* src = p.part + ((static_cast<int64_t>(it.slot) * p.heads_kv + head) * 256 + threadIdx.x) * (p.d + 8);
+          float mm = -INFINITY, ll = 0.f;
+          for (int q = 0; q < it.nsplit; ++q) mm = fmaxf(mm, __ldcg(src + q * step + p.d));
+          const float base = mm == -INFINITY ? 0.f : mm;
+          for (int q = 0; q < it.nsplit; ++q)
+            ll += __ldcg(src + q * step + p.d + 1) * ex2((__ldcg(src + q * step + p.d) - base) * sl);
+          const float inv = vis > 0 ? 1.f / ll : 0.f;
+          uint8_t* out = p.out + tok * p.out_t + h * p.out_h;
+          for (int c = 0; c < p.d; c += 8) {
+            float a[8] = {};
+            for (int q = 0; q < it.nsplit; ++q) {
+              const float mq = __ldcg(src + q * step + p.d);
+              if (mq == -INFINITY) continue;  // nothing seen in this part: no O was written
+              const float f = ex2((mq - base) * sl) * inv;
+              const float4 u = __ldcg(reinterpret_cast<const float4*>(src + q * step + c));
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(src + q * step + c + 4));
+              a[0] = fmaf(u.x, f, a[0]);
+              a[1] = fmaf(u.y, f, a[1]);
+              a[2] = fmaf(u.z, f, a[2]);
+              a[3] = fmaf(u.w, f, a[3]);
+              a[4] = fmaf(v.x, f, a[4]);
+              a[5] = fmaf(v.y, f, a[5]);
+              a[6] = fmaf(v.z, f, a[6]);
+              a[7] = fmaf(v.w, f, a[7]);
+            }
+            *reinterpret_cast<uint4*>(out + c * 2) =
+                make_uint4(pack_pair<BF16>(a[0], a[1]), pack_pair<BF16>(a[2], a[3]), pack_pair<BF16>(a[4], a[5]),
+                           pack_pair<BF16>(a[6], a[7]));
+          }
+          if (p.lse) p.lse[tok * p.heads_q + h] = vis > 0 ? mm * p.scale + logf(ll) : -INFINITY;
+        }
+      }
+      tc_fence_before();  // O has been read before the next item's products
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, kDevErrTimeout);
+}
+
+template <bool BF16>
+const void* fwd_kernel(int dp) {
+  return dp == 64 ? reinterpret_cast<const void*>(k_attn_fwd<BF16, 64>)
+                  : reinterpret_cast<const void*>(k_attn_fwd<BF16, 128>);
+}
+
+}  // namespace
+
+sc_status attn_fwd(const AttnArgs& a) {
+  const int g = a.heads_q / a.heads_kv, pos = 128 / g;
+  const int sms = device_sm_count();
+  const int64_t items_ub = a.t_q / (2 * pos) + a.n_seq;
+  if (items_ub * a.heads_kv > 0x3fffffff) return set_error(SC_ERR_UNSUPPORTED, "too many query tiles");
+  // Few units for the card: the keys are cut, so that there are about four units an SM.
+  const bool split = items_ub * a.heads_kv <= 8ll * sms;
+  const int split_units = 4 * sms;
+  const int64_t slots = split ? split_units / a.heads_kv + 1 + items_ub : 0;
+  const int64_t cap = items_ub + slots;
+  Arena ar;
+  const size_t o_head = ar.take(kPlanHeader * sizeof(int));
+  const size_t o_items = ar.take(static_cast<size_t>(cap) * sizeof(AttnItem));
+  const size_t o_done = ar.take(split ? static_cast<size_t>(items_ub * a.heads_kv) * 8 * sizeof(int) : 0);
+  const size_t o_part = ar.take(static_cast<size_t>(slots) * a.heads_kv * 256 * (a.head_dim + 8) * sizeof(float));
+  int* status = attn_status_word();
+  if (!status) return set_error(SC_ERR_CUDA, "the attention status word is not available");
+  const int dp = a.head_dim <= 64 ? 64 : 128;
+  const size_t tile = static_cast<size_t>(dp) / 64 * 16384;
+  FwdParams p{};
+  p.stages = dp == 64 ? 10 : 5;
+  const size_t smem = (2 + p.stages) * tile + sizeof(FwdSmem) + 1024;
+  const void* kern = a.dtype == SC_BF16 ? fwd_kernel<true>(dp) : fwd_kernel<false>(dp);
+  sc_status st = kernel_setup(kern, smem, nullptr);
+  if (st) return st;
+  CUtensorMap qm, km, vm;
+  const void* any = a.q.data;  // no key rows: maps of legal sizes that nothing reads
+  const bool keys = a.t_k > 0;
+  if ((st = attn_map(&qm, a.q.data, a.dtype, a.head_dim, a.heads_q, a.t_q, a.q.token_stride, a.q.head_stride, g, pos)))
+    return st;
+  if ((st = attn_map(&km, keys ? a.k.data : any, a.dtype, a.head_dim, keys ? a.heads_kv : 1, keys ? a.t_k : 1,
+                     a.k.token_stride, a.k.head_stride, 1, kKeyTile)))
+    return st;
+  if ((st = attn_map(&vm, keys ? a.v.data : any, a.dtype, a.head_dim, keys ? a.heads_kv : 1, keys ? a.t_k : 1,
+                     a.v.token_stride, a.v.head_stride, 1, kKeyTile)))
+    return st;
+  void* ws = nullptr;
+  if ((st = dev_alloc(&ws, ar.bytes, a.stream))) return st;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  PlanArgs pl{};
+  pl.q_off = a.q_off;
+  pl.k_off = a.k_off;
+  pl.k_len = a.k_len;
+  pl.n_seq = static_cast<int>(a.n_seq);
+  pl.t_q = a.t_q;
+  pl.t_k = a.t_k;
+  pl.pos_per_item = 2 * pos;
+  pl.causal = a.causal;
+  pl.heads_kv = a.heads_kv;
+  pl.mode = kPlanRows;
+  pl.split_units = split ? split_units : 0;
+  pl.min_tiles = 2;
+  pl.cap = static_cast<int>(cap);
+  pl.header = reinterpret_cast<int*>(base + o_head);
+  pl.items = reinterpret_cast<AttnItem*>(base + o_items);
+  pl.done = reinterpret_cast<int*>(base + o_done);
+  pl.done_cap = split ? static_cast<int>(items_ub * a.heads_kv) * 8 : 0;
+  pl.status = status;
+  st = attn_plan(pl, a.stream);
+  if (!st) {
+    p.out = static_cast<uint8_t*>(a.out.data);
+    p.out_t = a.out.token_stride * 2;
+    p.out_h = a.out.head_stride * 2;
+    p.lse = a.lse;
+    p.header = pl.header;
+    p.counter = pl.header + 1;
+    p.items = pl.items;
+    p.done = pl.done;
+    p.part = reinterpret_cast<float*>(base + o_part);
+    p.heads_q = a.heads_q;
+    p.heads_kv = a.heads_kv;
+    p.g = g;
+    p.pos = pos;
+    p.d = a.head_dim;
+    p.scale_log2 = a.scale * kLog2e;
+    p.scale = a.scale;
+    p.causal = a.causal;
+    p.status = status;
+    const int64_t most = cap * a.heads_kv;
+    const int grid = static_cast<int>(most < sms ? most : sms);
+    void* args[] = {&p, &qm, &km, &vm};
+    cudaError_t e;
+    SC_LAUNCH("attn_fwd", a.stream,
+              (e = cudaLaunchKernel(kern, dim3(grid), dim3(kFwdThreads), args, smem, a.stream)));
+    if (e != cudaSuccess) st = set_cuda_error(e, "attn_fwd");
+  }
+  dev_free(ws, a.stream);
+  return st;
+}
+
+}  // namespace sc

@@ -60,10 +60,10 @@
 
 #include <cstdio>
 #include <cstdlib>
-#include <mutex>
 
 #include "sc_internal.cuh"
 #include "tc_ptx.cuh"
+#include "tma_map.cuh"
 
 // Packed-weight buffer of sc_subm_conv_fwd_noalloc: a fixed, file-scope
 // device array, so that entry point needs no allocation.  Every GPU that
@@ -944,25 +944,6 @@ TcParams base_params(const ConvArgs& a, const Plan& pl, const uint8_t* img) {
 
 bool fused_ok(const ConvArgs& a, Plan* pl) {
   return a.dtype != SC_F32 && a.m->V <= 128 && make_plan(a.c_in, a.c_out, true, pl);
-}
-
-// cuTensorMapEncodeTiled, resolved once through the runtime's driver entry
-// point (the library does not link the driver library).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn tensor_map_encoder() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
 }
 
 CUtensorMapSwizzle swizzle_for(int row_bytes) {
