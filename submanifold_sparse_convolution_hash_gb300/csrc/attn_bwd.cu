@@ -1,209 +1,944 @@
-// Attention's gradients: the plain forms of their kernels, one warp a row, fp32
-// throughout.
-//   S = scale q k^T, lse = log sum exp S, out = softmax(S) v, and the gradients.
-#include "attn_internal.cuh"
+// Attention's gradients over packed sequences.
+//
+// With P = exp(scale Q K^T - lse), delta = gout . out per row,
+//   dS = P * (gout V^T - delta),  gq = scale dS K,  gk = scale dS^T Q,  gv = P^T gout.
+// Two kernels, each of whose blocks owns what it writes, so nothing is added by
+// atomics and the same inputs give the same bits:
+//   gk, gv  a block owns 128 keys and walks the rows (all queries and heads of
+//           the group): four products a step, S^T = K Q^T, dP^T = V gout^T,
+//           gv += P^T gout, gk += dS^T Q
+//   gq      a block owns 128 rows and walks the keys: three products a step,
+//           S = Q K^T, dP = gout V^T, gq += dS K
+// That is seven products where one pass with atomic adds to gq needs five; the
+// two passes need no fp32 copy of gq and no order of arrival.
+// P and dS go back to TMEM, rounded to 16 bits, as the first operand of the
+// second products; sums stay in TMEM in fp32.  f16 has few bits below 2^-14 and
+// a weight of a list of thousands lies there, so P is held times 2^8 (at most
+// 256); dS, whose size the caller's loss scale sets, as it is.
+#include "attn_device.cuh"
 
 namespace sc {
 namespace {
 
+constexpr int kBwdThreads = 384;
+constexpr int kBwdMaxStages = 12;
 
-struct View {
-  const uint8_t* p;
-  int64_t ts, hs;
-};
-struct SimpleParams {
-  View q, k, v, out, gout, gq, gk, gv;
-  float* lse;
-  float* delta;
-  const int *q_off, *k_off, *k_len;
-  int n_seq;
-  int64_t t_q, t_k;
-  int hq, hk, g, d;
-  float scale;
+// P is held times 2^kPShift.
+template <bool BF16>
+constexpr float kPShift = BF16 ? 0.f : 8.f;
+template <bool BF16>
+constexpr float kPDown = BF16 ? 1.f : 1.f / 256.f;
+
+struct BwdParams {
+  // [t_q, heads_q]: lse log2 e - kPShift (+inf: no key seen), delta 2^-kPShift
+  const float2* stat;
+  const int* header;
+  int* counter;
+  const AttnItem* items;
+  uint8_t *o0, *o1;      // gq, or gk and gv
+  int64_t o0_t, o0_h, o1_t, o1_h;  // bytes
+  int heads_q, heads_kv, g, pos, d;
+  float scale, scale_log2;
   int causal;
-  int* bad;
+  int stages;            // ring tiles
   int* status;
 };
 
-template <typename T>
-__device__ __forceinline__ void load_row(const View& v, int64_t t, int h, int d, float (&x)[4]) {
-  const T* p = reinterpret_cast<const T*>(v.p) + t * v.ts + h * v.hs;
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = lane + 32 * i < d ? static_cast<float>(p[lane + 32 * i]) : 0.f;
+// 8 values of a 16-bit row, times `f`.
+template <bool BF16>
+__device__ __forceinline__ void store8(uint8_t* dst, const uint32_t* v, float f) {
+  *reinterpret_cast<uint4*>(dst) =
+      make_uint4(pack_pair<BF16>(__uint_as_float(v[0]) * f, __uint_as_float(v[1]) * f),
+                 pack_pair<BF16>(__uint_as_float(v[2]) * f, __uint_as_float(v[3]) * f),
+                 pack_pair<BF16>(__uint_as_float(v[4]) * f, __uint_as_float(v[5]) * f),
+                 pack_pair<BF16>(__uint_as_float(v[6]) * f, __uint_as_float(v[7]) * f));
 }
-template <typename T>
-__device__ __forceinline__ void store_row(const View& v, int64_t t, int h, int d, const float (&x)[4]) {
-  T* p = reinterpret_cast<T*>(const_cast<uint8_t*>(v.p)) + t * v.ts + h * v.hs;
-  const int lane = threadIdx.x & 31;
+
+// A TMEM accumulator row of d values to global memory (`have` false: zeros).
+template <bool BF16>
+__device__ __forceinline__ void store_acc(uint32_t t, uint8_t* dst, int d, float f, bool have, bool live) {
+  for (int c = 0; c < d; c += 16) {
+    uint32_t o[16];
+    if (have) {
+      tmem_ld16_raw(t + c, o);
+    } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < d) p[lane + 32 * i] = T(x[i]);
-}
-__device__ __forceinline__ float dot(const float (&a)[4], const float (&b)[4]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) s = fmaf(a[i], b[i], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-// the sequence s with off[s] <= t < off[s + 1]
-__device__ __forceinline__ int find(const int* off, int n, int t) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (__ldg(off + m) <= t) lo = m;
-    else hi = m - 1;
+      for (int u = 0; u < 16; ++u) o[u] = 0u;
+    }
+    if (live) {
+      store8<BF16>(dst + c * 2, o, f);
+      if (c + 8 < d) store8<BF16>(dst + c * 2 + 16, o + 8, f);
+    }
   }
-  return lo;
 }
-struct Range {
-  int64_t q0, q1, k0, k1;
+
+// ------------------------------------------------------------ statistics --
+struct StatParams {
+  const uint8_t *gout, *out;
+  int64_t gt, gh, ot, oh;  // bytes
+  const float* lse;
+  float2* stat;
+  int64_t rows;  // t_q * heads_q
+  int heads_q, d;
 };
-__device__ __forceinline__ Range range_of(const SimpleParams& p, int s) {
-  Range r;
-  r.q0 = p.q_off[s];
-  r.q1 = p.q_off[s + 1];
-  r.k0 = p.k_off[s];
-  r.k1 = p.k_len ? r.k0 + p.k_len[s] : p.k_off[s + 1];
-  return r;
+
+template <bool BF16>
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b) {
+  float2 x, y;
+  if constexpr (BF16) {
+    x = make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+    y = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
+  } else {
+    x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  }
+  return fmaf(x.x, y.x, x.y * y.y);
 }
 
-// Checks the offsets; *bad stays 0 when every rule holds.
-__global__ void k_check(const SimpleParams p, int packed_keys) {
-  for (int s = threadIdx.x; s < p.n_seq; s += blockDim.x) {
-    const Range r = range_of(p, s);
-    bool bad = r.q0 < 0 || r.q1 > p.t_q || r.k0 < 0 || r.k1 > p.t_k || r.q1 < r.q0 || r.k1 < r.k0;
-    bad = bad || (s == 0 && r.q0 != 0) || (s == p.n_seq - 1 && r.q1 != p.t_q);
-    if (packed_keys) bad = bad || (s == 0 && r.k0 != 0) || (s == p.n_seq - 1 && r.k1 != p.t_k);
-    if (bad) {
-      *p.bad = 1;
-      atomicOr(p.status, kDevErrRange);
+// delta = gout . out and lse in powers of two, LPR lanes a row.
+template <bool BF16, int LPR>
+__global__ void __launch_bounds__(256) k_attn_stat(const StatParams p) {
+  const int64_t r = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / LPR;
+  const int gl = threadIdx.x % LPR;
+  float s = 0.f;
+  if (r < p.rows && gl * 8 < p.d) {
+    const int64_t t = r / p.heads_q;
+    const int h = static_cast<int>(r - t * p.heads_q);
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.gout + t * p.gt + h * p.gh) + gl);
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.out + t * p.ot + h * p.oh) + gl);
+    s = (dot2<BF16>(a.x, b.x) + dot2<BF16>(a.y, b.y)) + (dot2<BF16>(a.z, b.z) + dot2<BF16>(a.w, b.w));
+  }
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (gl == 0 && r < p.rows) {
+    const float l = __ldg(p.lse + r);
+    p.stat[r] = make_float2(l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -kPShift<BF16>), s * kPDown<BF16>);
+  }
+}
+
+// --------------------------------------------------------------- gk, gv --
+struct KvSmem {
+  uint64_t full[kBwdMaxStages], empty[kBwdMaxStages];
+  uint64_t kv_full[2], kv_empty[2];
+  uint64_t rows_ok[2], rows_free[2];  // row statistics (and the rows of a tile that ends inside)
+  uint64_t s_full, p_ready, dp_full, ds_ready, acc_full;
+  uint64_t drained;
+  uint32_t tmem;
+  int abort;
+  ItemSlots slots;
+  __align__(16) float lse2[2][128];
+  __align__(16) float delta[2][128];
+  __align__(16) int lim[2][128];  // causal: the last key that the row sees
+};
+
+// First row tile (of p.pos queries) that sees key tile kt, and their number.
+__device__ __forceinline__ int row_tiles(const BwdParams& p, const AttnItem& it, int* first) {
+  int i0 = 0;
+  if (p.causal) i0 = max(0, it.kt0 * kKeyTile - it.lim0);
+  *first = i0 / p.pos;
+  if (i0 >= it.n_pos) return 0;
+  return (it.n_pos + p.pos - 1) / p.pos - *first;
+}
+
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    k_attn_bwd_kv(const BwdParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap gmap,
+                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  constexpr int PANELS = DP / 64, KVB = DP == 64 ? 2 : 1;
+  constexpr uint32_t PANEL = 128 * 128, TILE = PANELS * PANEL;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t skv = smem_u32(smem);                 // KVB pairs of K and V
+  const uint32_t srow = skv + 2 * KVB * TILE;          // ring: Q, gout, Q, gout, ...
+  const int S = p.stages;
+  KvSmem* sm = reinterpret_cast<KvSmem*>(smem + (2 * KVB + S) * TILE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sm->abort;
+  const int used = p.pos * p.g;  // rows of a tile; the rest stays zero
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&sm->full[s]), 1);
+      mbar_init(smem_u32(&sm->empty[s]), 1);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sm->kv_full[s]), 1);
+      mbar_init(smem_u32(&sm->kv_empty[s]), 1);
+      mbar_init(smem_u32(&sm->rows_ok[s]), 1);
+      mbar_init(smem_u32(&sm->rows_free[s]), 8);
+    }
+    mbar_init(smem_u32(&sm->s_full), 1);
+    mbar_init(smem_u32(&sm->p_ready), 8);
+    mbar_init(smem_u32(&sm->dp_full), 1);
+    mbar_init(smem_u32(&sm->ds_ready), 8);
+    mbar_init(smem_u32(&sm->acc_full), 1);
+    mbar_init(smem_u32(&sm->drained), 1);
+    sm->slots.init(11);
+    sm->abort = 0;
+    fence_mbar_init();
   }
-}
-
-template <typename T>
-__global__ void k_simple_gq(const SimpleParams p) {
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (w >= p.t_q * p.hq || *p.bad) return;
-  const int64_t t = w / p.hq;
-  const int h = static_cast<int>(w % p.hq);
-  const Range r = range_of(p, find(p.q_off, p.n_seq, static_cast<int>(t)));
-  const int64_t end = p.causal ? min(r.k1, r.k1 - (r.q1 - t) + 1) : r.k1;
-  float q[4], k[4], v[4], g[4], o[4], acc[4] = {};
-  load_row<T>(p.q, t, h, p.d, q);
-  load_row<T>(p.gout, t, h, p.d, g);
-  load_row<T>(p.out, t, h, p.d, o);
-  const float delta = dot(g, o), lse = p.lse[t * p.hq + h];
-  if ((threadIdx.x & 31) == 0) p.delta[t * p.hq + h] = delta;
-  for (int64_t j = r.k0; j < end; ++j) {
-    load_row<T>(p.k, j, h / p.g, p.d, k);
-    load_row<T>(p.v, j, h / p.g, p.d, v);
-    const float ds = expf(dot(q, k) * p.scale - lse) * (dot(g, v) - delta) * p.scale;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(ds, k[i], acc[i]);
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&sm->tmem), 512);
+    tmem_relinquish();
   }
-  store_row<T>(p.gq, t, h, p.d, acc);
-}
+  // rows of the ring that no copy writes
+  for (int s = 0; s < S * PANELS; ++s)
+    for (int i = used * 8 + static_cast<int>(threadIdx.x); i < 128 * 8; i += kBwdThreads)
+      *reinterpret_cast<uint4*>(smem + 2 * KVB * TILE + s * PANEL + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem;
+  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+  const int units = p.header[0] * p.heads_kv;
 
-template <typename T>
-__global__ void k_simple_gkv(const SimpleParams p) {
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (w >= p.t_k * p.hk || *p.bad) return;
-  const int64_t t = w / p.hk;
-  const int h = static_cast<int>(w % p.hk);
-  const Range r = range_of(p, find(p.k_off, p.n_seq, static_cast<int>(t)));
-  float q[4], k[4], v[4], g[4], ak[4] = {}, av[4] = {};
-  load_row<T>(p.k, t, h, p.d, k);
-  load_row<T>(p.v, t, h, p.d, v);
-  int64_t first = r.q0;
-  if (p.causal) first = max(first, r.q1 - (r.k1 - t));
-  for (int64_t i = first; i < r.q1; ++i)
-    for (int gh = h * p.g; gh < (h + 1) * p.g; ++gh) {
-      load_row<T>(p.q, i, gh, p.d, q);
-      load_row<T>(p.gout, i, gh, p.d, g);
-      const float pr = expf(dot(q, k) * p.scale - p.lse[i * p.hq + gh]);
-      const float ds = pr * (dot(g, v) - p.delta[i * p.hq + gh]) * p.scale;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        ak[c] = fmaf(ds, q[c], ak[c]);
-        av[c] = fmaf(pr, g[c], av[c]);
+  if (warp == 8) {
+    // =========================================================== loads
+    if (lane == 0) {
+      ItemRing ring(&sm->slots);
+      AttnItem it;
+      int head;
+      uint32_t k = 0, nkv = 0;
+      while (ring.next(&it, &head, abort_flag, false)) {
+        int first;
+        const int n = row_tiles(p, it, &first);
+        if (n == 0) continue;
+        const uint32_t b = nkv % KVB;
+        if (!mbar_wait_inl(smem_u32(&sm->kv_empty[b]), ((nkv / KVB) & 1) ^ 1, abort_flag)) {
+          sm->abort = 1;
+          break;
+        }
+        ++nkv;
+        mbar_arrive_expect_tx(smem_u32(&sm->kv_full[b]), 2 * TILE);
+        for (int c = 0; c < PANELS; ++c) {
+          tma_load_3d(skv + 2 * b * TILE + c * PANEL, &kmap, c * 64, head, it.k_row + it.kt0 * kKeyTile,
+                      smem_u32(&sm->kv_full[b]));
+          tma_load_3d(skv + (2 * b + 1) * TILE + c * PANEL, &vmap, c * 64, head, it.k_row + it.kt0 * kKeyTile,
+                      smem_u32(&sm->kv_full[b]));
+        }
+        bool ok = true;
+        for (int i = first; i < first + n && ok; ++i)
+          for (int which = 0; which < 2; ++which, ++k) {
+            const uint32_t st = k % S;
+            if (!mbar_wait_inl(smem_u32(&sm->empty[st]), ((k / S) & 1) ^ 1, abort_flag)) {
+              sm->abort = 1;
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(smem_u32(&sm->full[st]), PANELS * used * 128);
+            for (int c = 0; c < PANELS; ++c)
+              tma_load_3d(srow + st * TILE + c * PANEL, which ? &gmap : &qmap, c * 64, head * p.g,
+                          it.q_row + i * p.pos, smem_u32(&sm->full[st]));
+          }
+        if (!ok) break;
       }
+      const uint32_t f0 = nkv > KVB ? nkv - KVB : 0;
+      for (uint32_t i = f0; i < nkv; ++i)
+        if (!mbar_drain_inl(smem_u32(&sm->kv_full[i % KVB]), (i / KVB) & 1)) sm->abort = 1;
+      const uint32_t f1 = k > static_cast<uint32_t>(S) ? k - S : 0;
+      for (uint32_t i = f1; i < k; ++i)
+        if (!mbar_drain_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
     }
-  store_row<T>(p.gk, t, h, p.d, ak);
-  store_row<T>(p.gv, t, h, p.d, av);
+    __syncwarp();
+  } else if (warp == 9) {
+    // ======================================================== products
+    if (lane == 0) {
+      const int dn = (p.d + 15) & ~15;
+      const int ksteps = dn / 16;
+      const uint32_t id_s = make_idesc(BF16, 128, 128);
+      const uint32_t id_a = make_idesc(BF16, 128, dn) | (1u << 16);
+      const uint64_t d_kv = smem_desc(skv, 1024, 2);
+      const uint64_t d_row = smem_desc(srow, 1024, 2);
+      const uint64_t d_rowt = smem_desc_mn(srow, PANEL, 1024, 2);
+      ItemRing ring(&sm->slots);
+      AttnItem it;
+      int head;
+      uint32_t k = 0, nkv = 0, nr = 0, np = 0, nd = 0;
+      // D = A B^T over d, A a K or V tile, B a ring tile
+      auto first_product = [&](uint32_t t, uint32_t a_tile, uint32_t stage, uint64_t bar) {
+        for (int i = 0; i < ksteps; ++i) {
+          const uint32_t off = ((i >> 2) * PANEL + (i & 3) * 32) >> 4;
+          tc_mma(t, d_kv + ((a_tile * TILE) >> 4) + off, d_row + ((stage * TILE) >> 4) + off, id_s, i > 0);
+        }
+        tc_commit(static_cast<uint32_t>(bar));
+      };
+      // acc += A B over the rows, A in TMEM (the two halves of the rows apart), B a ring tile
+      auto second_product = [&](uint32_t acc, uint32_t a, uint32_t stage, bool add) {
+        for (int i = 0; i < 8; ++i)
+          tc_mma_ts(acc, a + (i >> 2) * 64 + (i & 3) * 8, d_rowt + ((stage * TILE + i * 2048) >> 4), id_a,
+                    add || i > 0);
+      };
+      while (ring.next(&it, &head, abort_flag, false)) {
+        int first;
+        const int n = row_tiles(p, it, &first);
+        if (n == 0) continue;
+        const uint32_t b = nkv % KVB;
+        bool ok = mbar_wait_inl(smem_u32(&sm->kv_full[b]), (nkv / KVB) & 1, abort_flag);
+        ++nkv;
+        // a row tile's copies have landed and its rows are in order
+        auto rows = [&](uint32_t kk) {
+          ok = ok && mbar_wait_inl(smem_u32(&sm->full[kk % S]), (kk / S) & 1, abort_flag) &&
+               mbar_wait_inl(smem_u32(&sm->full[(kk + 1) % S]), ((kk + 1) / S) & 1, abort_flag) &&
+               mbar_wait_inl(smem_u32(&sm->rows_ok[nr & 1]), (nr >> 1) & 1, abort_flag);
+          ++nr;
+          tc_fence_after();
+        };
+        rows(k);
+        if (ok) {
+          first_product(t_s, 2 * b, k % S, smem_u32(&sm->s_full));
+          first_product(t_dp, 2 * b + 1, (k + 1) % S, smem_u32(&sm->dp_full));
+        }
+        for (int i = 0; i < n && ok; ++i, k += 2) {
+          const bool more = i + 1 < n;
+          ok = mbar_wait_inl(smem_u32(&sm->p_ready), np++ & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          second_product(t_dv, t_s, (k + 1) % S, i > 0);
+          if (more) {
+            rows(k + 2);
+            if (!ok) break;
+            first_product(t_s, 2 * b, (k + 2) % S, smem_u32(&sm->s_full));
+          }
+          ok = mbar_wait_inl(smem_u32(&sm->ds_ready), nd++ & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          second_product(t_dk, t_dp, k % S, i > 0);
+          tc_commit(smem_u32(&sm->empty[k % S]));
+          tc_commit(smem_u32(&sm->empty[(k + 1) % S]));
+          if (more) first_product(t_dp, 2 * b + 1, (k + 3) % S, smem_u32(&sm->dp_full));
+        }
+        if (!ok) {
+          sm->abort = 1;
+          break;
+        }
+        tc_commit(smem_u32(&sm->kv_empty[b]));
+        tc_commit(smem_u32(&sm->acc_full));
+      }
+      tc_commit(smem_u32(&sm->drained));
+      if (!mbar_drain_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    if (lane == 0) hand_out(&sm->slots, p.counter, p.items, units, p.heads_kv, abort_flag);
+    __syncwarp();
+  } else if (warp == 11) {
+    // ============================================== row statistics, ends
+    // lse, delta and the causal limit of a tile's rows.  Rows past the
+    // sequence's last query belong to someone else: their weight is 0 (lse =
+    // +inf) and, the rows being summed over, so must be what they hold.
+    ItemRing ring(&sm->slots);
+    AttnItem it;
+    int head;
+    uint32_t k = 0, nr = 0;
+    while (ring.next(&it, &head, abort_flag, true)) {
+      int first;
+      const int n = row_tiles(p, it, &first);
+      bool ok = true;
+      for (int i = first; i < first + n && ok; ++i, k += 2, ++nr) {
+        const uint32_t sl = nr & 1;
+        const int live = min(p.pos, it.n_pos - i * p.pos) * p.g;
+        float2 st[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = lane + 32 * u;
+          st[u] = make_float2(INFINITY, 0.f);
+          if (r < live) {
+            const int64_t t = static_cast<int64_t>(it.q_row) + i * p.pos + r / p.g;
+            st[u] = __ldg(p.stat + t * p.heads_q + head * p.g + r % p.g);
+          }
+        }
+        ok = mbar_wait_inl(smem_u32(&sm->rows_free[sl]), ((nr >> 1) & 1) ^ 1, abort_flag);
+        ok = ok && mbar_wait_inl(smem_u32(&sm->full[k % S]), (k / S) & 1, abort_flag) &&
+             mbar_wait_inl(smem_u32(&sm->full[(k + 1) % S]), ((k + 1) / S) & 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          sm->abort = 1;
+          break;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = lane + 32 * u;
+          sm->lse2[sl][r] = st[u].x;
+          sm->delta[sl][r] = st[u].y;
+          sm->lim[sl][r] = it.lim0 + i * p.pos + r / p.g;
+        }
+        if (live < used) {
+          for (int w = 0; w < 2; ++w)
+            for (int c = 0; c < PANELS; ++c) {
+              uint8_t* tile = smem + (2 * KVB + (k + w) % S) * TILE + c * PANEL;
+              for (int j = live * 8 + lane; j < used * 8; j += 32)
+                *reinterpret_cast<uint4*>(tile + j * 16) = make_uint4(0, 0, 0, 0);
+            }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm->rows_ok[sl]));
+      }
+      if (!ok) break;
+    }
+    __syncwarp();
+  } else {
+    // ================================================ weights and dS
+    // A key a lane; warps 0-3 take the rows (columns) 0-63, warps 4-7 the rest.
+    const int half = warp >> 2;
+    const int key_lane = threadIdx.x & 127;
+    const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;
+    const uint32_t ts = t_s + lane_off + half * 64, tdp = t_dp + lane_off + half * 64;
+    const uint64_t sl2 = pair2(p.scale_log2, p.scale_log2), down = pair2(kPDown<BF16>, kPDown<BF16>);
+    ItemRing ring(&sm->slots);
+    AttnItem it;
+    int head;
+    uint32_t np = 0, nr = 0, na = 0;
+    while (ring.next(&it, &head, abort_flag, true)) {
+      int first;
+      const int n = row_tiles(p, it, &first);
+      const int key = it.kt0 * kKeyTile + key_lane;
+      bool ok = true;
+      for (int i = first; i < first + n; ++i, ++np, ++nr) {
+        const uint32_t sl = nr & 1;
+        ok = mbar_wait_inl(smem_u32(&sm->rows_ok[sl]), (nr >> 1) & 1, abort_flag) &&
+             mbar_wait_inl(smem_u32(&sm->s_full), np & 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[64], y[64];
+        tmem_ld64_raw(ts, x);
+        const float4* l4 = reinterpret_cast<const float4*>(sm->lse2[sl] + half * 64);
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 l = l4[c / 4];
+          float e[4];
+          unpair2(fma2(pair2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, pair2(-l.x, -l.y)), e[0], e[1]);
+          unpair2(fma2(pair2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sl2, pair2(-l.z, -l.w)), e[2], e[3]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x[c + u] = __float_as_uint(ex2(e[u]));
+        }
+        if (p.causal && it.kt0 * kKeyTile + kKeyTile - 1 > it.lim0 + i * p.pos) {
+          const int4* m4 = reinterpret_cast<const int4*>(sm->lim[sl] + half * 64);
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const int4 m = m4[c / 4];
+            if (key > m.x) x[c] = 0u;
+            if (key > m.y) x[c + 1] = 0u;
+            if (key > m.z) x[c + 2] = 0u;
+            if (key > m.w) x[c + 3] = 0u;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          y[c] = pack_pair<BF16>(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+        tmem_st32(ts, y);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm->p_ready));
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->dp_full), np & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld64_raw(tdp, y);
+        const float4* d4 = reinterpret_cast<const float4*>(sm->delta[sl] + half * 64);
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 dl = d4[c / 4];
+          float e[4];
+          unpair2(mul2(pair2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
+                       fma2(pair2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), down, pair2(-dl.x, -dl.y))),
+                  e[0], e[1]);
+          unpair2(mul2(pair2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])),
+                       fma2(pair2(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), down, pair2(-dl.z, -dl.w))),
+                  e[2], e[3]);
+          y[c / 2] = pack_pair<BF16>(e[0], e[1]);
+          y[c / 2 + 1] = pack_pair<BF16>(e[2], e[3]);
+        }
+        tmem_st32(tdp, y);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sm->ds_ready));
+          mbar_arrive(smem_u32(&sm->rows_free[sl]));
+        }
+      }
+      if (!ok) {
+        sm->abort = 1;
+        break;
+      }
+      if (n > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->acc_full), na & 1, abort_flag))) {
+          sm->abort = 1;
+          break;
+        }
+        ++na;
+        tc_fence_after();
+      }
+      // warps 0-3 write gv, warps 4-7 gk
+      const bool live = key < it.lk;
+      const int64_t row = static_cast<int64_t>(it.k_row) + key;
+      if (half == 0)
+        store_acc<BF16>(t_dv + lane_off, p.o1 + row * p.o1_t + head * p.o1_h, p.d, kPDown<BF16>, n > 0, live);
+      else
+        store_acc<BF16>(t_dk + lane_off, p.o0 + row * p.o0_t + head * p.o0_h, p.d, p.scale, n > 0, live);
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, kDevErrTimeout);
 }
 
-View view(const sc_heads& v) { return {static_cast<const uint8_t*>(v.data), v.token_stride, v.head_stride}; }
-View view(const sc_heads_out& v) { return {static_cast<const uint8_t*>(v.data), v.token_stride, v.head_stride}; }
+// ------------------------------------------------------------------- gq --
+struct QSmem {
+  uint64_t full[kBwdMaxStages], empty[kBwdMaxStages];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], dp_full, ds_ready, acc_full;
+  uint64_t fix_k, k_fixed;
+  uint64_t drained;
+  uint32_t tmem;
+  int abort;
+  int fix_at, fix_rows;  // ring stage of a K tile that ends inside, and its keys
+  ItemSlots slots;
+};
 
-SimpleParams params(const AttnArgs& a) {
-  SimpleParams p{};
-  p.q = view(a.q);
-  p.k = view(a.k);
-  p.v = view(a.v);
-  p.lse = a.lse;
-  p.q_off = a.q_off;
-  p.k_off = a.k_off;
-  p.k_len = a.k_len;
-  p.n_seq = static_cast<int>(a.n_seq);
-  p.t_q = a.t_q;
-  p.t_k = a.t_k;
-  p.hq = a.heads_q;
-  p.hk = a.heads_kv;
-  p.g = a.heads_q / a.heads_kv;
-  p.d = a.head_dim;
-  p.scale = a.scale;
-  p.causal = a.causal;
-  return p;
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    k_attn_bwd_q(const BwdParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap gmap,
+                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  constexpr int PANELS = DP / 64;
+  constexpr uint32_t PANEL = 128 * 128, TILE = PANELS * PANEL;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sq = smem_u32(smem);        // Q and gout
+  const uint32_t skv = sq + 2 * TILE;        // ring: K, V, K, V, ...
+  const int S = p.stages;
+  QSmem* sm = reinterpret_cast<QSmem*>(smem + (2 + S) * TILE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sm->abort;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&sm->full[s]), 1);
+      mbar_init(smem_u32(&sm->empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sm->q_full), 1);
+    mbar_init(smem_u32(&sm->q_empty), 1);
+    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&sm->s_full[s]), 1);
+    mbar_init(smem_u32(&sm->dp_full), 1);
+    mbar_init(smem_u32(&sm->ds_ready), 8);
+    mbar_init(smem_u32(&sm->acc_full), 1);
+    mbar_init(smem_u32(&sm->fix_k), 1);
+    mbar_init(smem_u32(&sm->k_fixed), 1);
+    mbar_init(smem_u32(&sm->drained), 1);
+    sm->slots.init(11);
+    sm->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&sm->tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem;
+  const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;
+  const int units = p.header[0] * p.heads_kv;
+
+  if (warp == 8) {
+    // =========================================================== loads
+    if (lane == 0) {
+      ItemRing ring(&sm->slots);
+      AttnItem it;
+      int head;
+      uint32_t k = 0, nq = 0;
+      while (ring.next(&it, &head, abort_flag, false)) {
+        if (it.kt1 == 0) continue;
+        if (!mbar_wait_inl(smem_u32(&sm->q_empty), (nq & 1) ^ 1, abort_flag)) {
+          sm->abort = 1;
+          break;
+        }
+        ++nq;
+        mbar_arrive_expect_tx(smem_u32(&sm->q_full), 2 * PANELS * p.pos * p.g * 128);
+        for (int c = 0; c < PANELS; ++c) {
+          tma_load_3d(sq + c * PANEL, &qmap, c * 64, head * p.g, it.q_row, smem_u32(&sm->q_full));
+          tma_load_3d(sq + TILE + c * PANEL, &gmap, c * 64, head * p.g, it.q_row, smem_u32(&sm->q_full));
+        }
+        bool ok = true;
+        for (int j = 0; j < it.kt1 && ok; ++j)
+          for (int kv = 0; kv < 2; ++kv, ++k) {
+            const uint32_t st = k % S;
+            if (!mbar_wait_inl(smem_u32(&sm->empty[st]), ((k / S) & 1) ^ 1, abort_flag)) {
+              sm->abort = 1;
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(smem_u32(&sm->full[st]), TILE);
+            for (int c = 0; c < PANELS; ++c)
+              tma_load_3d(skv + st * TILE + c * PANEL, kv ? &vmap : &kmap, c * 64, head, it.k_row + j * kKeyTile,
+                          smem_u32(&sm->full[st]));
+          }
+        if (!ok) break;
+      }
+      if (nq > 0 && !mbar_drain_inl(smem_u32(&sm->q_full), (nq - 1) & 1)) sm->abort = 1;
+      const uint32_t f1 = k > static_cast<uint32_t>(S) ? k - S : 0;
+      for (uint32_t i = f1; i < k; ++i)
+        if (!mbar_drain_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ======================================================== products
+    if (lane == 0) {
+      const int dn = (p.d + 15) & ~15;
+      const int ksteps = dn / 16;
+      const uint32_t id_s = make_idesc(BF16, 128, 128);
+      const uint32_t id_a = make_idesc(BF16, 128, dn) | (1u << 16);
+      const uint64_t d_q = smem_desc(sq, 1024, 2);
+      const uint64_t d_kv = smem_desc(skv, 1024, 2);
+      const uint64_t d_kvt = smem_desc_mn(skv, PANEL, 1024, 2);
+      ItemRing ring(&sm->slots);
+      AttnItem it;
+      int head;
+      uint32_t k0 = 0, nq = 0, nd = 0, nfix = 0, nbuf = 0;
+      auto first_product = [&](uint32_t t, uint32_t a_tile, uint32_t stage, uint32_t bar) {
+        for (int i = 0; i < ksteps; ++i) {
+          const uint32_t off = ((i >> 2) * PANEL + (i & 3) * 32) >> 4;
+          tc_mma(t, d_q + ((a_tile * TILE) >> 4) + off, d_kv + ((stage * TILE) >> 4) + off, id_s, i > 0);
+        }
+        tc_commit(bar);
+      };
+      while (ring.next(&it, &head, abort_flag, false)) {
+        const int n = it.kt1;
+        if (n == 0) continue;
+        bool ok = mbar_wait_inl(smem_u32(&sm->q_full), nq & 1, abort_flag);
+        ++nq;
+        // S of key tile j into its buffer; the tile's rows past the keys are zeroed first
+        auto scores = [&](int j) {
+          const uint32_t kk = k0 + 2 * j;
+          ok = ok && mbar_wait_inl(smem_u32(&sm->full[kk % S]), (kk / S) & 1, abort_flag);
+          if (ok && it.lk - j * kKeyTile < kKeyTile) {
+            sm->fix_at = static_cast<int>(kk % S);
+            sm->fix_rows = it.lk - j * kKeyTile;
+            mbar_arrive(smem_u32(&sm->fix_k));
+            ok = mbar_wait_inl(smem_u32(&sm->k_fixed), nfix++ & 1, abort_flag);
+          }
+          if (!ok) return;
+          tc_fence_after();
+          first_product(t_s + ((nbuf + j) & 1) * 128, 0, kk % S, smem_u32(&sm->s_full[(nbuf + j) & 1]));
+        };
+        // dP of key tile j; V is done with
+        auto dp = [&](int j) {
+          const uint32_t kk = k0 + 2 * j + 1;
+          ok = ok && mbar_wait_inl(smem_u32(&sm->full[kk % S]), (kk / S) & 1, abort_flag);
+          if (!ok) return;
+          tc_fence_after();
+          first_product(t_dp, 1, kk % S, smem_u32(&sm->dp_full));
+          tc_commit(smem_u32(&sm->empty[kk % S]));
+        };
+        scores(0);
+        dp(0);
+        if (n > 1) scores(1);
+        for (int j = 0; j < n && ok; ++j) {
+          ok = mbar_wait_inl(smem_u32(&sm->ds_ready), nd++ & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t kk = k0 + 2 * j;
+          for (int i = 0; i < 8; ++i)
+            tc_mma_ts(t_dq, t_dp + (i >> 2) * 64 + (i & 3) * 8, d_kvt + (((kk % S) * TILE + i * 2048) >> 4), id_a,
+                      j > 0 || i > 0);
+          tc_commit(smem_u32(&sm->empty[kk % S]));
+          if (j + 1 < n) dp(j + 1);
+          if (j + 2 < n) scores(j + 2);
+        }
+        if (!ok) {
+          sm->abort = 1;
+          break;
+        }
+        tc_commit(smem_u32(&sm->q_empty));
+        tc_commit(smem_u32(&sm->acc_full));
+        k0 += 2 * n;
+        nbuf += n;
+      }
+      tc_commit(smem_u32(&sm->drained));
+      if (!mbar_drain_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    if (lane == 0) hand_out(&sm->slots, p.counter, p.items, units, p.heads_kv, abort_flag);
+    __syncwarp();
+  } else if (warp == 11) {
+    // ==================================================== tail of K
+    ItemRing ring(&sm->slots);
+    AttnItem it;
+    int head;
+    uint32_t n = 0;
+    while (ring.next(&it, &head, abort_flag, true)) {
+      if (it.kt1 == 0 || it.lk - (it.kt1 - 1) * kKeyTile >= kKeyTile) continue;
+      if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->fix_k), n & 1, abort_flag))) {
+        sm->abort = 1;
+        break;
+      }
+      ++n;
+      const int rows = sm->fix_rows;
+      uint8_t* tile = smem + (2 + sm->fix_at) * TILE;
+      for (int c = 0; c < PANELS; ++c)
+        for (int i = rows * 8 + lane; i < kKeyTile * 8; i += 32)
+          *reinterpret_cast<uint4*>(tile + c * PANEL + i * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm->k_fixed));
+    }
+    __syncwarp();
+  } else {
+    // ========================================================= dS
+    // A row a lane; warps 0-3 take the keys (columns) 0-63 of a tile, 4-7 the rest.
+    const int half = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;
+    const uint32_t tdp = t_dp + lane_off + half * 64;
+    const int pos = row / p.g, gh = row - pos * p.g;
+    const uint64_t sl2 = pair2(p.scale_log2, p.scale_log2), down = pair2(kPDown<BF16>, kPDown<BF16>);
+    ItemRing ring(&sm->slots);
+    AttnItem it;
+    int head;
+    uint32_t nd = 0, na = 0;
+    while (ring.next(&it, &head, abort_flag, true)) {
+      const int n = it.kt1;
+      const bool live = pos < p.pos && pos < it.n_pos;
+      const int64_t tok = static_cast<int64_t>(it.q_row) + pos;
+      const int h = head * p.g + gh;
+      const int vis = p.causal ? min(it.lk, it.lim0 + pos + 1) : it.lk;
+      float2 st = make_float2(INFINITY, 0.f);
+      if (live) st = __ldg(p.stat + tok * p.heads_q + h);
+      const uint64_t nl = pair2(-st.x, -st.x), ndl = pair2(-st.y, -st.y);
+      bool ok = true;
+      for (int j = 0; j < n; ++j, ++nd) {
+        const uint32_t b = nd & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->s_full[b]), (nd >> 1) & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[64], y[64];
+        tmem_ld64_raw(t_s + b * 128 + lane_off + half * 64, x);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float e0, e1;
+          unpair2(fma2(pair2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, nl), e0, e1);
+          x[c] = __float_as_uint(ex2(e0));
+          x[c + 1] = __float_as_uint(ex2(e1));
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->dp_full), nd & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld64_raw(tdp, y);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float e0, e1;
+          unpair2(mul2(pair2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
+                       fma2(pair2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), down, ndl)),
+                  e0, e1);
+          x[c] = __float_as_uint(e0);
+          x[c + 1] = __float_as_uint(e1);
+        }
+        const int seen = vis - j * kKeyTile - half * 64;
+        if (__any_sync(0xffffffffu, seen < 64)) {  // selected, not multiplied: V may hold anything there
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c >= seen) x[c] = 0u;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          y[c] = pack_pair<BF16>(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+        tmem_st32(tdp, y);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm->ds_ready));
+      }
+      if (!ok) {
+        sm->abort = 1;
+        break;
+      }
+      if (n > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->acc_full), na & 1, abort_flag))) {
+          sm->abort = 1;
+          break;
+        }
+        ++na;
+        tc_fence_after();
+      }
+      // each half writes the columns of its half
+      const int c0 = half ? (p.d / 2 + 15) / 16 * 16 : 0;
+      const int c1 = half ? p.d : min(p.d, (p.d / 2 + 15) / 16 * 16);
+      if (c1 > c0)
+        store_acc<BF16>(t_dq + lane_off + c0, p.o0 + tok * p.o0_t + h * p.o0_h + c0 * 2, c1 - c0, p.scale, n > 0, live);
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, kDevErrTimeout);
 }
-sc_status check_offsets(SimpleParams& p, const AttnArgs& a, bool packed_keys) {
-  void* bad = nullptr;
-  const sc_status st = dev_alloc(&bad, sizeof(int), a.stream);
-  if (st) return st;
-  p.bad = static_cast<int*>(bad);
-  p.status = attn_status_word();
-  cudaMemsetAsync(bad, 0, sizeof(int), a.stream);
-  SC_LAUNCH("attn_check", a.stream, (k_check<<<1, 256, 0, a.stream>>>(p, packed_keys)));
-  return SC_OK;
+
+template <bool BF16>
+const void* kv_kernel(int dp) {
+  return dp == 64 ? reinterpret_cast<const void*>(k_attn_bwd_kv<BF16, 64>)
+                  : reinterpret_cast<const void*>(k_attn_bwd_kv<BF16, 128>);
 }
-unsigned blocks(int64_t warps) { return static_cast<unsigned>((warps + 7) / 8); }
+template <bool BF16>
+const void* q_kernel(int dp) {
+  return dp == 64 ? reinterpret_cast<const void*>(k_attn_bwd_q<BF16, 64>)
+                  : reinterpret_cast<const void*>(k_attn_bwd_q<BF16, 128>);
+}
+
+template <bool BF16>
+void run_stat(const StatParams& p, cudaStream_t s) {
+  const int lpr = p.d <= 16 ? 2 : p.d <= 32 ? 4 : p.d <= 64 ? 8 : 16;
+  const unsigned n = static_cast<unsigned>((p.rows * lpr + 255) / 256);
+  switch (lpr) {
+    case 2: k_attn_stat<BF16, 2><<<n, 256, 0, s>>>(p); break;
+    case 4: k_attn_stat<BF16, 4><<<n, 256, 0, s>>>(p); break;
+    case 8: k_attn_stat<BF16, 8><<<n, 256, 0, s>>>(p); break;
+    default: k_attn_stat<BF16, 16><<<n, 256, 0, s>>>(p); break;
+  }
+}
 
 }  // namespace
 
 sc_status attn_bwd(const AttnArgs& a) {
-  SimpleParams p = params(a);
-  p.out = view(a.out_in);
-  p.gout = view(a.gout);
-  p.gq = view(a.gq);
-  p.gk = view(a.gk);
-  p.gv = view(a.gv);
-  void* delta = nullptr;
-  sc_status st = dev_alloc(&delta, sizeof(float) * a.t_q * a.heads_q, a.stream);
+  const int g = a.heads_q / a.heads_kv, pos = 128 / g;
+  const int sms = device_sm_count();
+  const bool bf = a.dtype == SC_BF16;
+  const int64_t q_items = a.t_q / pos + a.n_seq, k_items = a.t_k / kKeyTile + a.n_seq;
+  if (q_items * a.heads_kv > 0x3fffffff || k_items * a.heads_kv > 0x3fffffff ||
+      a.t_q * a.heads_q > (int64_t(1) << 34))
+    return set_error(SC_ERR_UNSUPPORTED, "too many tiles");
+  Arena ar;
+  const size_t o_hq = ar.take(kPlanHeader * sizeof(int)), o_hk = ar.take(kPlanHeader * sizeof(int));
+  const size_t o_iq = ar.take(static_cast<size_t>(q_items) * sizeof(AttnItem));
+  const size_t o_ik = ar.take(static_cast<size_t>(k_items) * sizeof(AttnItem));
+  const size_t o_st = ar.take(static_cast<size_t>(a.t_q) * a.heads_q * sizeof(float2));
+  int* status = attn_status_word();
+  if (!status) return set_error(SC_ERR_CUDA, "the attention status word is not available");
+  const int dp = a.head_dim <= 64 ? 64 : 128;
+  const size_t tile = static_cast<size_t>(dp) / 64 * 16384;
+  const void* kk = bf ? kv_kernel<true>(dp) : kv_kernel<false>(dp);
+  const void* kq = bf ? q_kernel<true>(dp) : q_kernel<false>(dp);
+  const int kv_stages = dp == 64 ? 8 : 4, kv_res = dp == 64 ? 4 : 2, q_stages = dp == 64 ? 10 : 5;
+  const size_t kv_smem = (kv_res + kv_stages) * tile + sizeof(KvSmem) + 1024;
+  const size_t q_smem = (2 + q_stages) * tile + sizeof(QSmem) + 1024;
+  sc_status st = kernel_setup(kk, kv_smem, nullptr);
+  if (!st) st = kernel_setup(kq, q_smem, nullptr);
   if (st) return st;
-  p.delta = static_cast<float*>(delta);
-  if ((st = check_offsets(p, a, true))) {
-    dev_free(delta, a.stream);
+  const bool have_q = a.t_q > 0, have_k = a.t_k > 0;
+  const void* any = have_q ? a.q.data : a.k.data;  // a side without rows: maps of legal sizes that nothing reads
+  CUtensorMap qm, gm, km, vm;
+  const int hq = have_q ? a.heads_q : 1, hk = have_k ? a.heads_kv : 1;
+  const int64_t tq = have_q ? a.t_q : 1, tk = have_k ? a.t_k : 1;
+  if ((st = attn_map(&qm, have_q ? a.q.data : any, a.dtype, a.head_dim, hq, tq, a.q.token_stride, a.q.head_stride, g, pos)) ||
+      (st = attn_map(&gm, have_q ? a.gout.data : any, a.dtype, a.head_dim, hq, tq, a.gout.token_stride, a.gout.head_stride, g, pos)) ||
+      (st = attn_map(&km, have_k ? a.k.data : any, a.dtype, a.head_dim, hk, tk, a.k.token_stride, a.k.head_stride, 1, kKeyTile)) ||
+      (st = attn_map(&vm, have_k ? a.v.data : any, a.dtype, a.head_dim, hk, tk, a.v.token_stride, a.v.head_stride, 1, kKeyTile)))
     return st;
+  void* ws = nullptr;
+  if ((st = dev_alloc(&ws, ar.bytes, a.stream))) return st;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  PlanArgs pl{};
+  pl.q_off = a.q_off;
+  pl.k_off = a.k_off;
+  pl.n_seq = static_cast<int>(a.n_seq);
+  pl.t_q = a.t_q;
+  pl.t_k = a.t_k;
+  pl.pos_per_item = pos;
+  pl.causal = a.causal;
+  pl.packed_keys = 1;
+  pl.heads_kv = a.heads_kv;
+  pl.status = status;
+  PlanArgs plq = pl, plk = pl;
+  plq.mode = kPlanRows;
+  plq.cap = static_cast<int>(q_items);
+  plq.header = reinterpret_cast<int*>(base + o_hq);
+  plq.items = reinterpret_cast<AttnItem*>(base + o_iq);
+  plk.mode = kPlanKeys;
+  plk.cap = static_cast<int>(k_items);
+  plk.header = reinterpret_cast<int*>(base + o_hk);
+  plk.items = reinterpret_cast<AttnItem*>(base + o_ik);
+  st = attn_plan(plk, a.stream);
+  if (!st) st = attn_plan(plq, a.stream);
+  cudaError_t e = cudaSuccess;
+  BwdParams p{};
+  p.stat = reinterpret_cast<const float2*>(base + o_st);
+  p.heads_q = a.heads_q;
+  p.heads_kv = a.heads_kv;
+  p.g = g;
+  p.pos = pos;
+  p.d = a.head_dim;
+  p.scale = a.scale;
+  p.scale_log2 = a.scale * kLog2e;
+  p.causal = a.causal;
+  p.status = status;
+  if (!st && have_q) {
+    StatParams sp{};
+    sp.gout = static_cast<const uint8_t*>(a.gout.data);
+    sp.out = static_cast<const uint8_t*>(a.out_in.data);
+    sp.gt = a.gout.token_stride * 2;
+    sp.gh = a.gout.head_stride * 2;
+    sp.ot = a.out_in.token_stride * 2;
+    sp.oh = a.out_in.head_stride * 2;
+    sp.lse = a.lse;
+    sp.stat = reinterpret_cast<float2*>(base + o_st);
+    sp.rows = a.t_q * a.heads_q;
+    sp.heads_q = a.heads_q;
+    sp.d = a.head_dim;
+    SC_LAUNCH("attn_stat", a.stream, (bf ? run_stat<true>(sp, a.stream) : run_stat<false>(sp, a.stream)));
+    e = cudaGetLastError();
+    if (e != cudaSuccess) st = set_cuda_error(e, "attn_stat");
   }
-  if (a.t_q > 0) {
-    const unsigned n = blocks(a.t_q * a.heads_q);
-    SC_LAUNCH("attn_bwd_q", a.stream,
-              (a.dtype == SC_F16 ? k_simple_gq<__half><<<n, 256, 0, a.stream>>>(p)
-                                 : k_simple_gq<__nv_bfloat16><<<n, 256, 0, a.stream>>>(p)));
-  }
-  if (a.t_k > 0) {
-    const unsigned n = blocks(a.t_k * a.heads_kv);
+  if (!st && have_k) {
+    BwdParams pk = p;
+    pk.header = plk.header;
+    pk.counter = plk.header + 1;
+    pk.items = plk.items;
+    pk.o0 = static_cast<uint8_t*>(a.gk.data);
+    pk.o0_t = a.gk.token_stride * 2;
+    pk.o0_h = a.gk.head_stride * 2;
+    pk.o1 = static_cast<uint8_t*>(a.gv.data);
+    pk.o1_t = a.gv.token_stride * 2;
+    pk.o1_h = a.gv.head_stride * 2;
+    pk.stages = kv_stages;
+    const int64_t most = k_items * a.heads_kv;
+    void* args[] = {&pk, &qm, &gm, &km, &vm};
     SC_LAUNCH("attn_bwd_kv", a.stream,
-              (a.dtype == SC_F16 ? k_simple_gkv<__half><<<n, 256, 0, a.stream>>>(p)
-                                 : k_simple_gkv<__nv_bfloat16><<<n, 256, 0, a.stream>>>(p)));
+              (e = cudaLaunchKernel(kk, dim3(static_cast<unsigned>(most < sms ? most : sms)), dim3(kBwdThreads), args,
+                                    kv_smem, a.stream)));
+    if (e != cudaSuccess) st = set_cuda_error(e, "attn_bwd_kv");
   }
-  dev_free(delta, a.stream);
-  dev_free(p.bad, a.stream);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? SC_OK : set_cuda_error(e, "attn_bwd");
+  if (!st && have_q) {
+    BwdParams pq = p;
+    pq.header = plq.header;
+    pq.counter = plq.header + 1;
+    pq.items = plq.items;
+    pq.o0 = static_cast<uint8_t*>(a.gq.data);
+    pq.o0_t = a.gq.token_stride * 2;
+    pq.o0_h = a.gq.head_stride * 2;
+    pq.stages = q_stages;
+    const int64_t most = q_items * a.heads_kv;
+    void* args[] = {&pq, &qm, &gm, &km, &vm};
+    SC_LAUNCH("attn_bwd_q", a.stream,
+              (e = cudaLaunchKernel(kq, dim3(static_cast<unsigned>(most < sms ? most : sms)), dim3(kBwdThreads), args,
+                                    q_smem, a.stream)));
+    if (e != cudaSuccess) st = set_cuda_error(e, "attn_bwd_q");
+  }
+  dev_free(ws, a.stream);
+  return st;
 }
 
 }  // namespace sc

@@ -11,15 +11,13 @@
 // a row a thread; while one tile's exponentials run, the other tile's products
 // do.  O is corrected only when a row's maximum grew by more than 2^8: until
 // then P is up to 256 instead of 1, which costs no bits in floating point.
-#include "attn_internal.cuh"
-#include "tc_ptx.cuh"
+#include "attn_device.cuh"
 
 namespace sc {
 namespace {
 
 constexpr int kFwdThreads = 384;
 constexpr int kFwdMaxStages = 10;
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct FwdParams {
   uint8_t* out;
@@ -43,46 +41,12 @@ struct FwdSmem {
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_ready[2], o_full[2];
   uint64_t fix_v, v_fixed;
-  uint64_t it_full[2], it_empty[2];
+  ItemSlots slots;
   uint64_t drained;
   uint32_t tmem;
   int abort;
   int fix_at, fix_rows;  // ring stage of a V tile that ends inside, and its keys
-  AttnItem item[2];
-  int head[2];  // -1: no more work
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
-  uint32_t r;
-  if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // Key tiles that row tile s of the item has to see: [kt0, end).
 __device__ __forceinline__ int tile_end(const FwdParams& p, const AttnItem& it, int s) {
@@ -92,31 +56,6 @@ __device__ __forceinline__ int tile_end(const FwdParams& p, const AttnItem& it, 
   const int end = (max(seen, 0) + kKeyTile - 1) / kKeyTile;
   return max(it.kt0, min(end, it.kt1));
 }
-
-// Receives the next item; false: no more.  Every waiting thread passes its own
-// phase counter.
-struct ItemRing {
-  uint32_t n = 0;
-  __device__ __forceinline__ bool next(FwdSmem* sm, AttnItem* it, int* head, bool one_per_warp) {
-    const int slot = n & 1;
-    bool ok = mbar_wait_inl(smem_u32(&sm->it_full[slot]), (n >> 1) & 1, &sm->abort);
-    if (one_per_warp) ok = __all_sync(0xffffffffu, ok);
-    if (!ok) {
-      sm->abort = 1;
-      return false;
-    }
-    *it = sm->item[slot];
-    *head = sm->head[slot];
-    if (one_per_warp) {
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm->it_empty[slot]));
-    } else {
-      mbar_arrive(smem_u32(&sm->it_empty[slot]));
-    }
-    ++n;
-    return *head >= 0;
-  }
-};
 
 template <bool BF16, int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -145,12 +84,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(smem_u32(&sm->s_full[s]), 1);
       mbar_init(smem_u32(&sm->p_ready[s]), 4);
       mbar_init(smem_u32(&sm->o_full[s]), 1);
-      mbar_init(smem_u32(&sm->it_full[s]), 1);
-      mbar_init(smem_u32(&sm->it_empty[s]), 11);  // 8 softmax warps, TMA, MMA, tail
     }
     mbar_init(smem_u32(&sm->fix_v), 1);
     mbar_init(smem_u32(&sm->v_fixed), 1);
     mbar_init(smem_u32(&sm->drained), 1);
+    sm->slots.init(11);  // 8 softmax warps, loads, products, tail
     sm->abort = 0;
     fence_mbar_init();
   }
@@ -169,12 +107,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (warp == 8) {
     // =========================================================== loads
     if (lane == 0) {
-      ItemRing ring;
+      ItemRing ring(&sm->slots);
       AttnItem it;
       int head;
       uint32_t k = 0, nq = 0;
       const uint32_t q_bytes = static_cast<uint32_t>(p.pos * p.g) * 128;
-      while (ring.next(sm, &it, &head, false)) {
+      while (ring.next(&it, &head, abort_flag, false)) {
         const int e0 = tile_end(p, it, 0), e1 = tile_end(p, it, 1);
         const int end = max(e0, e1);
         if (end <= it.kt0) continue;
@@ -224,7 +162,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const uint64_t dq[2] = {smem_desc(sq, 1024, 2), smem_desc(sq + TILE, 1024, 2)};
       const uint64_t dk = smem_desc(skv, 1024, 2);
       const uint64_t dv = smem_desc_mn(skv, PANEL, 1024, 2);
-      ItemRing ring;
+      ItemRing ring(&sm->slots);
       AttnItem it;
       int head;
       uint32_t k = 0, nq = 0, nfix = 0;
@@ -236,7 +174,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         tc_commit(smem_u32(&sm->s_full[s]));
       };
-      while (ring.next(sm, &it, &head, false)) {
+      while (ring.next(&it, &head, abort_flag, false)) {
         const int end[2] = {tile_end(p, it, 0), tile_end(p, it, 1)};
         const int last = max(end[0], end[1]);
         if (last <= it.kt0) continue;
@@ -296,37 +234,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     __syncwarp();
   } else if (warp == 10) {
     // ====================================================== work units
-    if (lane == 0) {
-      for (uint32_t n = 0;; ++n) {
-        const int slot = n & 1;
-        const int u = atomicAdd(p.counter, 1);
-        if (!mbar_wait_inl(smem_u32(&sm->it_empty[slot]), ((n >> 1) & 1) ^ 1, abort_flag)) {
-          sm->abort = 1;
-          break;
-        }
-        if (u < units) {
-          const uint4* src = reinterpret_cast<const uint4*>(p.items + u / p.heads_kv);
-          uint4* dst = reinterpret_cast<uint4*>(&sm->item[slot]);
-          dst[0] = src[0];
-          dst[1] = src[1];
-          dst[2] = src[2];
-        }
-        sm->head[slot] = u < units ? u % p.heads_kv : -1;
-        mbar_arrive(smem_u32(&sm->it_full[slot]));
-        if (u >= units) break;
-      }
-    }
+    if (lane == 0) hand_out(&sm->slots, p.counter, p.items, units, p.heads_kv, abort_flag);
     __syncwarp();
   } else if (warp == 11) {
     // ==================================================== tail of V
     // Rows of a V tile past the sequence's keys belong to someone else (or to
     // nobody).  Their weights are zero, but zero times a NaN or an infinity is
     // not, so they are zeroed before the product.
-    ItemRing ring;
+    ItemRing ring(&sm->slots);
     AttnItem it;
     int head;
     uint32_t n = 0;
-    while (ring.next(sm, &it, &head, true)) {
+    while (ring.next(&it, &head, abort_flag, true)) {
       const int end = max(tile_end(p, it, 0), tile_end(p, it, 1));
       if (end <= it.kt0 || it.lk - (end - 1) * kKeyTile >= kKeyTile) continue;
       // the issuing warp asks once the tile has landed
@@ -354,11 +273,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int pos = row / p.g, gh = row - pos * p.g;
     const float sl = p.scale_log2;
     const float grow = 8.f / sl;                  // growth of the maximum that is let stand
-    ItemRing ring;
+    ItemRing ring(&sm->slots);
     AttnItem it;
     int head;
     uint32_t ns = 0, no = 0;
-    while (ring.next(sm, &it, &head, true)) {
+    while (ring.next(&it, &head, abort_flag, true)) {
       const int end = tile_end(p, it, s);
       const int i = s * p.pos + pos;              // this row's query in the item
       const bool live = pos < p.pos && i < it.n_pos;
