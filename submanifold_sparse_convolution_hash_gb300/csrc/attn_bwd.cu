@@ -22,6 +22,11 @@ namespace {
 
 constexpr int kBwdThreads = 384;
 constexpr int kBwdMaxStages = 12;
+// Ring tiles beside what stays: two pairs of K and V (one at 128 values) and
+// pairs of Q and gout; or Q, gout and single K and V tiles.
+constexpr int kv_pairs(int dp) { return dp == 64 ? 2 : 1; }
+constexpr int kv_stages(int dp) { return dp == 64 ? 8 : 4; }
+constexpr int q_stages(int dp) { return dp == 64 ? 10 : 5; }
 
 // P is held times 2^kPShift.
 template <bool BF16>
@@ -40,7 +45,6 @@ struct BwdParams {
   int heads_q, heads_kv, g, pos, d;
   float scale, scale_log2;
   int causal;
-  int stages;            // ring tiles
   int* status;
 };
 
@@ -144,20 +148,20 @@ template <bool BF16, int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     k_attn_bwd_kv(const BwdParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap gmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  constexpr int PANELS = DP / 64, KVB = DP == 64 ? 2 : 1;
+  constexpr int PANELS = DP / 64, KVB = kv_pairs(DP);
   constexpr uint32_t PANEL = 128 * 128, TILE = PANELS * PANEL;
+  constexpr uint32_t S = kv_stages(DP);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t skv = smem_u32(smem);                 // KVB pairs of K and V
   const uint32_t srow = skv + 2 * KVB * TILE;          // ring: Q, gout, Q, gout, ...
-  const int S = p.stages;
   KvSmem* sm = reinterpret_cast<KvSmem*>(smem + (2 * KVB + S) * TILE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm->abort;
   const int used = p.pos * p.g;  // rows of a tile; the rest stays zero
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
+    for (uint32_t s = 0; s < S; ++s) {
       mbar_init(smem_u32(&sm->full[s]), 1);
       mbar_init(smem_u32(&sm->empty[s]), 1);
     }
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_relinquish();
   }
   // rows of the ring that no copy writes
-  for (int s = 0; s < S * PANELS; ++s)
+  for (uint32_t s = 0; s < S * PANELS; ++s)
     for (int i = used * 8 + static_cast<int>(threadIdx.x); i < 128 * 8; i += kBwdThreads)
       *reinterpret_cast<uint4*>(smem + 2 * KVB * TILE + s * PANEL + i * 16) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
@@ -200,6 +204,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       AttnItem it;
       int head;
       uint32_t k = 0, nkv = 0;
+      RingPos<S> r;
       while (ring.next(&it, &head, abort_flag, false)) {
         int first;
         const int n = row_tiles(p, it, &first);
@@ -219,9 +224,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         bool ok = true;
         for (int i = first; i < first + n && ok; ++i)
-          for (int which = 0; which < 2; ++which, ++k) {
-            const uint32_t st = k % S;
-            if (!mbar_wait_inl(smem_u32(&sm->empty[st]), ((k / S) & 1) ^ 1, abort_flag)) {
+          for (int which = 0; which < 2; ++which, ++k, r.step()) {
+            const uint32_t st = r.st;
+            if (!mbar_wait_inl(smem_u32(&sm->empty[st]), r.ph ^ 1, abort_flag)) {
               sm->abort = 1;
               ok = false;
               break;
@@ -236,88 +241,96 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const uint32_t f0 = nkv > KVB ? nkv - KVB : 0;
       for (uint32_t i = f0; i < nkv; ++i)
         if (!mbar_drain_inl(smem_u32(&sm->kv_full[i % KVB]), (i / KVB) & 1)) sm->abort = 1;
-      const uint32_t f1 = k > static_cast<uint32_t>(S) ? k - S : 0;
+      const uint32_t f1 = k > S ? k - S : 0;
       for (uint32_t i = f1; i < k; ++i)
         if (!mbar_drain_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
     }
     __syncwarp();
   } else if (warp == 9) {
     // ======================================================== products
-    if (lane == 0) {
-      const int dn = (p.d + 15) & ~15;
-      const int ksteps = dn / 16;
-      const uint32_t id_s = make_idesc(BF16, 128, 128);
-      const uint32_t id_a = make_idesc(BF16, 128, dn) | (1u << 16);
-      const uint64_t d_kv = smem_desc(skv, 1024, 2);
-      const uint64_t d_row = smem_desc(srow, 1024, 2);
-      const uint64_t d_rowt = smem_desc_mn(srow, PANEL, 1024, 2);
-      ItemRing ring(&sm->slots);
-      AttnItem it;
-      int head;
-      uint32_t k = 0, nkv = 0, nr = 0, np = 0, nd = 0;
-      // D = A B^T over d, A a K or V tile, B a ring tile
-      auto first_product = [&](uint32_t t, uint32_t a_tile, uint32_t stage, uint64_t bar) {
-        for (int i = 0; i < ksteps; ++i) {
-          const uint32_t off = ((i >> 2) * PANEL + (i & 3) * 32) >> 4;
-          tc_mma(t, d_kv + ((a_tile * TILE) >> 4) + off, d_row + ((stage * TILE) >> 4) + off, id_s, i > 0);
-        }
-        tc_commit(static_cast<uint32_t>(bar));
+    const int dn = (p.d + 15) & ~15;
+    const int ksteps = dn / 16;
+    const uint32_t id_s = make_idesc(BF16, 128, 128);
+    const uint32_t id_a = make_idesc(BF16, 128, dn) | (1u << 16);
+    const uint64_t dk = smem_desc(skv, 1024, 2), dt = smem_desc_mn(srow, PANEL, 1024, 2);
+    const uint32_t kv_lo = static_cast<uint32_t>(dk), hi = static_cast<uint32_t>(dk >> 32);
+    const uint32_t row_lo = static_cast<uint32_t>(smem_desc(srow, 1024, 2));
+    const uint32_t rowt_lo = static_cast<uint32_t>(dt), rowt_hi = static_cast<uint32_t>(dt >> 32);
+    constexpr uint32_t T16 = TILE >> 4;
+    ItemRing ring(&sm->slots);
+    AttnItem it;
+    int head;
+    uint32_t nkv = 0, nr = 0, np = 0;
+    RingPos<S> cur;  // the row tile's Q; its gout is the next stage
+    while (ring.next(&it, &head, abort_flag, true)) {
+      int first;
+      const int n = row_tiles(p, it, &first);
+      if (n == 0) continue;
+      const uint32_t b = nkv % KVB;
+      bool ok = mbar_wait_inl(smem_u32(&sm->kv_full[b]), (nkv / KVB) & 1, abort_flag);
+      ++nkv;
+      // a row tile's copies have landed and its rows are in order
+      auto rows = [&](const RingPos<S>& at) {
+        ok = ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph, abort_flag) &&
+             mbar_wait_inl(smem_u32(&sm->full[at.st + 1]), at.ph, abort_flag) &&
+             mbar_wait_inl(smem_u32(&sm->rows_ok[nr & 1]), (nr >> 1) & 1, abort_flag);
+        ++nr;
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
       };
-      // acc += A B over the rows, A in TMEM (the two halves of the rows apart), B a ring tile
-      auto second_product = [&](uint32_t acc, uint32_t a, uint32_t stage, bool add) {
-        for (int i = 0; i < 8; ++i)
-          tc_mma_ts(acc, a + (i >> 2) * 64 + (i & 3) * 8, d_rowt + ((stage * TILE + i * 2048) >> 4), id_a,
-                    add || i > 0);
-      };
-      while (ring.next(&it, &head, abort_flag, false)) {
-        int first;
-        const int n = row_tiles(p, it, &first);
-        if (n == 0) continue;
-        const uint32_t b = nkv % KVB;
-        bool ok = mbar_wait_inl(smem_u32(&sm->kv_full[b]), (nkv / KVB) & 1, abort_flag);
-        ++nkv;
-        // a row tile's copies have landed and its rows are in order
-        auto rows = [&](uint32_t kk) {
-          ok = ok && mbar_wait_inl(smem_u32(&sm->full[kk % S]), (kk / S) & 1, abort_flag) &&
-               mbar_wait_inl(smem_u32(&sm->full[(kk + 1) % S]), ((kk + 1) / S) & 1, abort_flag) &&
-               mbar_wait_inl(smem_u32(&sm->rows_ok[nr & 1]), (nr >> 1) & 1, abort_flag);
-          ++nr;
-          tc_fence_after();
-        };
-        rows(k);
-        if (ok) {
-          first_product(t_s, 2 * b, k % S, smem_u32(&sm->s_full));
-          first_product(t_dp, 2 * b + 1, (k + 1) % S, smem_u32(&sm->dp_full));
-        }
-        for (int i = 0; i < n && ok; ++i, k += 2) {
-          const bool more = i + 1 < n;
-          ok = mbar_wait_inl(smem_u32(&sm->p_ready), np++ & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          second_product(t_dv, t_s, (k + 1) % S, i > 0);
-          if (more) {
-            rows(k + 2);
-            if (!ok) break;
-            first_product(t_s, 2 * b, (k + 2) % S, smem_u32(&sm->s_full));
-          }
-          ok = mbar_wait_inl(smem_u32(&sm->ds_ready), nd++ & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          second_product(t_dk, t_dp, k % S, i > 0);
-          tc_commit(smem_u32(&sm->empty[k % S]));
-          tc_commit(smem_u32(&sm->empty[(k + 1) % S]));
-          if (more) first_product(t_dp, 2 * b + 1, (k + 3) % S, smem_u32(&sm->dp_full));
-        }
-        if (!ok) {
-          sm->abort = 1;
-          break;
-        }
-        tc_commit(smem_u32(&sm->kv_empty[b]));
-        tc_commit(smem_u32(&sm->acc_full));
+      rows(cur);
+      if (ok && elect_lane()) {
+        product_rows<DP>(t_s, kv_lo + 2 * b * T16, row_lo + cur.st * T16, hi, id_s, ksteps);
+        tc_commit(smem_u32(&sm->s_full));
+        product_rows<DP>(t_dp, kv_lo + (2 * b + 1) * T16, row_lo + (cur.st + 1) * T16, hi, id_s, ksteps);
+        tc_commit(smem_u32(&sm->dp_full));
       }
-      tc_commit(smem_u32(&sm->drained));
-      if (!mbar_drain_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
+      __syncwarp();
+      for (int i = 0; i < n && ok; ++i, ++np) {
+        const bool more = i + 1 < n;
+        RingPos<S> nxt = cur;
+        nxt.step();
+        nxt.step();
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->p_ready), np & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_lane()) product_cols<0, 8>(t_dv, t_s, 32, rowt_lo + (cur.st + 1) * T16, rowt_hi, id_a, i > 0);
+        __syncwarp();
+        if (more) {
+          rows(nxt);
+          if (!ok) break;
+          if (elect_lane()) {
+            product_rows<DP>(t_s, kv_lo + 2 * b * T16, row_lo + nxt.st * T16, hi, id_s, ksteps);
+            tc_commit(smem_u32(&sm->s_full));
+          }
+          __syncwarp();
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->ds_ready), np & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_lane()) {
+          product_cols<0, 8>(t_dk, t_dp, 32, rowt_lo + cur.st * T16, rowt_hi, id_a, i > 0);
+          tc_commit(smem_u32(&sm->empty[cur.st]));
+          tc_commit(smem_u32(&sm->empty[cur.st + 1]));
+          if (more) {
+            product_rows<DP>(t_dp, kv_lo + (2 * b + 1) * T16, row_lo + (nxt.st + 1) * T16, hi, id_s, ksteps);
+            tc_commit(smem_u32(&sm->dp_full));
+          } else {
+            tc_commit(smem_u32(&sm->kv_empty[b]));
+            tc_commit(smem_u32(&sm->acc_full));
+          }
+        }
+        __syncwarp();
+        cur = nxt;
+      }
+      if (!ok) {
+        sm->abort = 1;
+        break;
+      }
     }
+    if (elect_lane()) tc_commit(smem_u32(&sm->drained));
+    __syncwarp();
+    if (!mbar_drain_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
     __syncwarp();
   } else if (warp == 10) {
     if (lane == 0) hand_out(&sm->slots, p.counter, p.items, units, p.heads_kv, abort_flag);
@@ -330,12 +343,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     ItemRing ring(&sm->slots);
     AttnItem it;
     int head;
-    uint32_t k = 0, nr = 0;
+    uint32_t nr = 0;
+    RingPos<S> cur;
     while (ring.next(&it, &head, abort_flag, true)) {
       int first;
       const int n = row_tiles(p, it, &first);
       bool ok = true;
-      for (int i = first; i < first + n && ok; ++i, k += 2, ++nr) {
+      for (int i = first; i < first + n && ok; ++i, ++nr, cur.step(), cur.step()) {
         const uint32_t sl = nr & 1;
         const int live = min(p.pos, it.n_pos - i * p.pos) * p.g;
         float2 st[4];
@@ -349,8 +363,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         }
         ok = mbar_wait_inl(smem_u32(&sm->rows_free[sl]), ((nr >> 1) & 1) ^ 1, abort_flag);
-        ok = ok && mbar_wait_inl(smem_u32(&sm->full[k % S]), (k / S) & 1, abort_flag) &&
-             mbar_wait_inl(smem_u32(&sm->full[(k + 1) % S]), ((k + 1) / S) & 1, abort_flag);
+        ok = ok && mbar_wait_inl(smem_u32(&sm->full[cur.st]), cur.ph, abort_flag) &&
+             mbar_wait_inl(smem_u32(&sm->full[cur.st + 1]), cur.ph, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           sm->abort = 1;
@@ -366,7 +380,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (live < used) {
           for (int w = 0; w < 2; ++w)
             for (int c = 0; c < PANELS; ++c) {
-              uint8_t* tile = smem + (2 * KVB + (k + w) % S) * TILE + c * PANEL;
+              uint8_t* tile = smem + (2 * KVB + cur.st + w) * TILE + c * PANEL;
               for (int j = live * 8 + lane; j < used * 8; j += 32)
                 *reinterpret_cast<uint4*>(tile + j * 16) = make_uint4(0, 0, 0, 0);
             }
@@ -511,17 +525,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   constexpr int PANELS = DP / 64;
   constexpr uint32_t PANEL = 128 * 128, TILE = PANELS * PANEL;
+  constexpr uint32_t S = q_stages(DP);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sq = smem_u32(smem);        // Q and gout
   const uint32_t skv = sq + 2 * TILE;        // ring: K, V, K, V, ...
-  const int S = p.stages;
   QSmem* sm = reinterpret_cast<QSmem*>(smem + (2 + S) * TILE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm->abort;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
+    for (uint32_t s = 0; s < S; ++s) {
       mbar_init(smem_u32(&sm->full[s]), 1);
       mbar_init(smem_u32(&sm->empty[s]), 1);
     }
@@ -556,6 +570,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       AttnItem it;
       int head;
       uint32_t k = 0, nq = 0;
+      RingPos<S> r;
       while (ring.next(&it, &head, abort_flag, false)) {
         if (it.kt1 == 0) continue;
         if (!mbar_wait_inl(smem_u32(&sm->q_empty), (nq & 1) ^ 1, abort_flag)) {
@@ -570,9 +585,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         bool ok = true;
         for (int j = 0; j < it.kt1 && ok; ++j)
-          for (int kv = 0; kv < 2; ++kv, ++k) {
-            const uint32_t st = k % S;
-            if (!mbar_wait_inl(smem_u32(&sm->empty[st]), ((k / S) & 1) ^ 1, abort_flag)) {
+          for (int kv = 0; kv < 2; ++kv, ++k, r.step()) {
+            const uint32_t st = r.st;
+            if (!mbar_wait_inl(smem_u32(&sm->empty[st]), r.ph ^ 1, abort_flag)) {
               sm->abort = 1;
               ok = false;
               break;
@@ -585,87 +600,103 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!ok) break;
       }
       if (nq > 0 && !mbar_drain_inl(smem_u32(&sm->q_full), (nq - 1) & 1)) sm->abort = 1;
-      const uint32_t f1 = k > static_cast<uint32_t>(S) ? k - S : 0;
+      const uint32_t f1 = k > S ? k - S : 0;
       for (uint32_t i = f1; i < k; ++i)
         if (!mbar_drain_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
     }
     __syncwarp();
   } else if (warp == 9) {
     // ======================================================== products
-    if (lane == 0) {
-      const int dn = (p.d + 15) & ~15;
-      const int ksteps = dn / 16;
-      const uint32_t id_s = make_idesc(BF16, 128, 128);
-      const uint32_t id_a = make_idesc(BF16, 128, dn) | (1u << 16);
-      const uint64_t d_q = smem_desc(sq, 1024, 2);
-      const uint64_t d_kv = smem_desc(skv, 1024, 2);
-      const uint64_t d_kvt = smem_desc_mn(skv, PANEL, 1024, 2);
-      ItemRing ring(&sm->slots);
-      AttnItem it;
-      int head;
-      uint32_t k0 = 0, nq = 0, nd = 0, nfix = 0, nbuf = 0;
-      auto first_product = [&](uint32_t t, uint32_t a_tile, uint32_t stage, uint32_t bar) {
-        for (int i = 0; i < ksteps; ++i) {
-          const uint32_t off = ((i >> 2) * PANEL + (i & 3) * 32) >> 4;
-          tc_mma(t, d_q + ((a_tile * TILE) >> 4) + off, d_kv + ((stage * TILE) >> 4) + off, id_s, i > 0);
-        }
-        tc_commit(bar);
-      };
-      while (ring.next(&it, &head, abort_flag, false)) {
-        const int n = it.kt1;
-        if (n == 0) continue;
-        bool ok = mbar_wait_inl(smem_u32(&sm->q_full), nq & 1, abort_flag);
-        ++nq;
-        // S of key tile j into its buffer; the tile's rows past the keys are zeroed first
-        auto scores = [&](int j) {
-          const uint32_t kk = k0 + 2 * j;
-          ok = ok && mbar_wait_inl(smem_u32(&sm->full[kk % S]), (kk / S) & 1, abort_flag);
-          if (ok && it.lk - j * kKeyTile < kKeyTile) {
-            sm->fix_at = static_cast<int>(kk % S);
+    const int dn = (p.d + 15) & ~15;
+    const int ksteps = dn / 16;
+    const uint32_t id_s = make_idesc(BF16, 128, 128);
+    const uint32_t id_a = make_idesc(BF16, 128, dn) | (1u << 16);
+    const uint64_t dk = smem_desc(skv, 1024, 2), dt = smem_desc_mn(skv, PANEL, 1024, 2);
+    const uint32_t kv_lo = static_cast<uint32_t>(dk), hi = static_cast<uint32_t>(dk >> 32);
+    const uint32_t q_lo = static_cast<uint32_t>(smem_desc(sq, 1024, 2));
+    const uint32_t kt_lo = static_cast<uint32_t>(dt), kt_hi = static_cast<uint32_t>(dt >> 32);
+    constexpr uint32_t T16 = TILE >> 4;
+    ItemRing ring(&sm->slots);
+    AttnItem it;
+    int head;
+    uint32_t nq = 0, nd = 0, nfix = 0, nbuf = 0;
+    RingPos<S> rs, rd;  // next tile's K for S (its V one stage on); tile in hand
+    while (ring.next(&it, &head, abort_flag, true)) {
+      const int n = it.kt1;
+      if (n == 0) continue;
+      bool ok = mbar_wait_inl(smem_u32(&sm->q_full), nq & 1, abort_flag);
+      ++nq;
+      // S of key tile j into its buffer; the tile's rows past the keys are zeroed first
+      auto scores = [&](int j) {
+        ok = ok && mbar_wait_inl(smem_u32(&sm->full[rs.st]), rs.ph, abort_flag);
+        if (it.lk - j * kKeyTile < kKeyTile) {
+          if (lane == 0 && ok) {
+            sm->fix_at = static_cast<int>(rs.st);
             sm->fix_rows = it.lk - j * kKeyTile;
             mbar_arrive(smem_u32(&sm->fix_k));
-            ok = mbar_wait_inl(smem_u32(&sm->k_fixed), nfix++ & 1, abort_flag);
           }
-          if (!ok) return;
-          tc_fence_after();
-          first_product(t_s + ((nbuf + j) & 1) * 128, 0, kk % S, smem_u32(&sm->s_full[(nbuf + j) & 1]));
-        };
-        // dP of key tile j; V is done with
-        auto dp = [&](int j) {
-          const uint32_t kk = k0 + 2 * j + 1;
-          ok = ok && mbar_wait_inl(smem_u32(&sm->full[kk % S]), (kk / S) & 1, abort_flag);
-          if (!ok) return;
-          tc_fence_after();
-          first_product(t_dp, 1, kk % S, smem_u32(&sm->dp_full));
-          tc_commit(smem_u32(&sm->empty[kk % S]));
-        };
-        scores(0);
-        dp(0);
-        if (n > 1) scores(1);
-        for (int j = 0; j < n && ok; ++j) {
-          ok = mbar_wait_inl(smem_u32(&sm->ds_ready), nd++ & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t kk = k0 + 2 * j;
-          for (int i = 0; i < 8; ++i)
-            tc_mma_ts(t_dq, t_dp + (i >> 2) * 64 + (i & 3) * 8, d_kvt + (((kk % S) * TILE + i * 2048) >> 4), id_a,
-                      j > 0 || i > 0);
-          tc_commit(smem_u32(&sm->empty[kk % S]));
-          if (j + 1 < n) dp(j + 1);
-          if (j + 2 < n) scores(j + 2);
+          ok = ok && mbar_wait_inl(smem_u32(&sm->k_fixed), nfix & 1, abort_flag);
+          ++nfix;
         }
-        if (!ok) {
-          sm->abort = 1;
-          break;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_lane()) {
+          product_rows<DP>(t_s + (nbuf & 1) * 128, q_lo, kv_lo + rs.st * T16, hi, id_s, ksteps);
+          tc_commit(smem_u32(&sm->s_full[nbuf & 1]));
         }
-        tc_commit(smem_u32(&sm->q_empty));
-        tc_commit(smem_u32(&sm->acc_full));
-        k0 += 2 * n;
-        nbuf += n;
+        __syncwarp();
+        ++nbuf;
+        rs.step();
+        rs.step();
+      };
+      // dP of the tile whose V lies at `at`, which is then done with
+      auto dp = [&](const RingPos<S>& at) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph, abort_flag));
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_lane()) {
+          product_rows<DP>(t_dp, q_lo + T16, kv_lo + at.st * T16, hi, id_s, ksteps);
+          tc_commit(smem_u32(&sm->dp_full));
+          tc_commit(smem_u32(&sm->empty[at.st]));
+        }
+        __syncwarp();
+      };
+      scores(0);
+      RingPos<S> v = rd;
+      v.step();
+      dp(v);
+      if (n > 1) scores(1);
+      for (int j = 0; j < n && ok; ++j, ++nd) {
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->ds_ready), nd & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_lane()) {
+          product_cols<0, 8>(t_dq, t_dp, 32, kt_lo + rd.st * T16, kt_hi, id_a, j > 0);
+          tc_commit(smem_u32(&sm->empty[rd.st]));
+          if (j + 1 == n) {
+            tc_commit(smem_u32(&sm->q_empty));
+            tc_commit(smem_u32(&sm->acc_full));
+          }
+        }
+        __syncwarp();
+        rd.step();
+        rd.step();
+        if (j + 1 < n) {
+          v = rd;
+          v.step();
+          dp(v);
+        }
+        if (j + 2 < n) scores(j + 2);
       }
-      tc_commit(smem_u32(&sm->drained));
-      if (!mbar_drain_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
+      if (!ok) {
+        sm->abort = 1;
+        break;
+      }
     }
+    if (elect_lane()) tc_commit(smem_u32(&sm->drained));
+    __syncwarp();
+    if (!mbar_drain_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
     __syncwarp();
   } else if (warp == 10) {
     if (lane == 0) hand_out(&sm->slots, p.counter, p.items, units, p.heads_kv, abort_flag);
@@ -832,9 +863,8 @@ sc_status attn_bwd(const AttnArgs& a) {
   const size_t tile = static_cast<size_t>(dp) / 64 * 16384;
   const void* kk = bf ? kv_kernel<true>(dp) : kv_kernel<false>(dp);
   const void* kq = bf ? q_kernel<true>(dp) : q_kernel<false>(dp);
-  const int kv_stages = dp == 64 ? 8 : 4, kv_res = dp == 64 ? 4 : 2, q_stages = dp == 64 ? 10 : 5;
-  const size_t kv_smem = (kv_res + kv_stages) * tile + sizeof(KvSmem) + 1024;
-  const size_t q_smem = (2 + q_stages) * tile + sizeof(QSmem) + 1024;
+  const size_t kv_smem = (2 * kv_pairs(dp) + kv_stages(dp)) * tile + sizeof(KvSmem) + 1024;
+  const size_t q_smem = (2 + q_stages(dp)) * tile + sizeof(QSmem) + 1024;
   sc_status st = kernel_setup(kk, kv_smem, nullptr);
   if (!st) st = kernel_setup(kq, q_smem, nullptr);
   if (st) return st;
@@ -913,7 +943,6 @@ sc_status attn_bwd(const AttnArgs& a) {
     pk.o1 = static_cast<uint8_t*>(a.gv.data);
     pk.o1_t = a.gv.token_stride * 2;
     pk.o1_h = a.gv.head_stride * 2;
-    pk.stages = kv_stages;
     const int64_t most = k_items * a.heads_kv;
     void* args[] = {&pk, &qm, &gm, &km, &vm};
     SC_LAUNCH("attn_bwd_kv", a.stream,
@@ -929,7 +958,6 @@ sc_status attn_bwd(const AttnArgs& a) {
     pq.o0 = static_cast<uint8_t*>(a.gq.data);
     pq.o0_t = a.gq.token_stride * 2;
     pq.o0_h = a.gq.head_stride * 2;
-    pq.stages = q_stages;
     const int64_t most = q_items * a.heads_kv;
     void* args[] = {&pq, &qm, &gm, &km, &vm};
     SC_LAUNCH("attn_bwd_q", a.stream,

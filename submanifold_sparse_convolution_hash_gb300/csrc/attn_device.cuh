@@ -14,6 +14,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pair2(float lo, float hi) {
   uint64_t r;
@@ -47,6 +52,56 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+
+// One lane of the warp, the same one every time.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Products of 128-row tiles.  The issuing warp runs as one and its elected lane
+// issues: every operand is the warp's, and the steps are unrolled with constant
+// offsets, because a lane that works out a descriptor a step is slower than the
+// tensor core (176 cycles a 128 x 128 x 16 step against 64).
+//
+// D = A B^T over the head's values: tiles of `ksteps` (at most DP / 16) steps
+// of 16 values, 64-value panels of 16 KB.
+template <int DP>
+__device__ __forceinline__ void product_rows(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                             int ksteps) {
+#pragma unroll
+  for (int i = 0; i < DP / 16; ++i) {
+    constexpr uint32_t kPanel = 16384 >> 4;
+    const uint32_t off = (i >> 2) * kPanel + (i & 3) * 2;
+    if (i < ksteps) tc_mma_lohi(d, a_lo + off, b_lo + off, hi, idesc, i > 0);
+  }
+}
+// D (+)= A B over N steps of 16 rows of a tile from step I0 on; A lies in TMEM,
+// `gap` extra columns apart from step 4 on.
+template <int I0, int N>
+__device__ __forceinline__ void product_cols(uint32_t d, uint32_t a, int gap, uint32_t b_lo, uint32_t b_hi,
+                                             uint32_t idesc, bool add) {
+#pragma unroll
+  for (int i = I0; i < I0 + N; ++i)
+    tc_mma_ts_lohi(d, a + i * 8 + (i >= 4 ? gap : 0), b_lo + i * (2048 >> 4), b_hi, idesc, add || i > 0);
+}
+
+// A ring's place: stage and how often it came round.
+template <int S>
+struct RingPos {
+  uint32_t st = 0, ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++st == S) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
 
 // Work units reach a block's warps through two slots: one warp takes the next
 // unit from the list's counter, the others read it in turn.  Which block takes
@@ -105,6 +160,22 @@ struct ItemRing {
     if (!warp || (threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sl->empty[slot]));
     ++n;
     return *head >= 0;
+  }
+  // A warp's next item in place, for warps short of registers: null when there
+  // is no more; it stays until release().
+  __device__ __forceinline__ const AttnItem* peek(volatile int* abort_flag) {
+    const int slot = n & 1;
+    if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sl->full[slot]), (n >> 1) & 1, abort_flag))) {
+      *abort_flag = 1;
+      return nullptr;
+    }
+    return sl->head[slot] >= 0 ? &sl->item[slot] : nullptr;
+  }
+  __device__ __forceinline__ int head() const { return sl->head[n & 1]; }
+  __device__ __forceinline__ void release() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sl->empty[n & 1]));
+    ++n;
   }
 };
 

@@ -18,6 +18,12 @@ namespace {
 
 constexpr int kFwdThreads = 384;
 constexpr int kFwdMaxStages = 10;
+// K and V tiles in flight: 160 KB of them beside the two Q tiles.
+constexpr int fwd_stages(int dp) { return dp == 64 ? 10 : 5; }
+// Registers a thread: the block is launched with kFwdRegs for all, four warps
+// drop to the lesser share and eight raise to the greater.
+constexpr int kFwdRegs = 168, kFwdSideRegs = 72, kFwdMainRegs = 216;
+static_assert(128 * kFwdSideRegs + 256 * kFwdMainRegs <= kFwdThreads * kFwdRegs, "no more than the block has");
 
 struct FwdParams {
   uint8_t* out;
@@ -32,14 +38,13 @@ struct FwdParams {
   int d;
   float scale_log2, scale;
   int causal;
-  int stages;
   int* status;
 };
 
 struct FwdSmem {
   uint64_t full[kFwdMaxStages], empty[kFwdMaxStages];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_ready[2], o_full[2];
+  uint64_t s_full[2], p_ready[2][2], o_full[2];
   uint64_t fix_v, v_fixed;
   ItemSlots slots;
   uint64_t drained;
@@ -64,17 +69,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   constexpr int PANELS = DP / 64;
   constexpr uint32_t PANEL = 128 * 128;          // bytes of 128 rows x 64 values
   constexpr uint32_t TILE = PANELS * PANEL;
+  constexpr uint32_t S = fwd_stages(DP);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sq = smem_u32(smem);            // two Q tiles
   const uint32_t skv = sq + 2 * TILE;            // ring of K and V tiles
-  const int S = p.stages;
   FwdSmem* sm = reinterpret_cast<FwdSmem*>(smem + (2 + S) * TILE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm->abort;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
+    for (uint32_t s = 0; s < S; ++s) {
       mbar_init(smem_u32(&sm->full[s]), 1);
       mbar_init(smem_u32(&sm->empty[s]), 1);
     }
@@ -82,7 +87,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     mbar_init(smem_u32(&sm->q_empty), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&sm->s_full[s]), 1);
-      mbar_init(smem_u32(&sm->p_ready[s]), 4);
+      for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&sm->p_ready[s][h]), 4);
       mbar_init(smem_u32(&sm->o_full[s]), 1);
     }
     mbar_init(smem_u32(&sm->fix_v), 1);
@@ -100,17 +105,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm->tmem;
-  const uint32_t t_s[2] = {tmem, tmem + 128}, t_o[2] = {tmem + 256, tmem + 384};
+  // TMEM: S (and P over it) of the two row tiles, then their O, 128 columns each
   const int n_items = p.header[0];
   const int units = n_items * p.heads_kv;
 
   if (warp == 8) {
     // =========================================================== loads
+    regs_drop<kFwdSideRegs>();
     if (lane == 0) {
       ItemRing ring(&sm->slots);
       AttnItem it;
       int head;
-      uint32_t k = 0, nq = 0;
+      uint32_t nq = 0, loads = 0;
+      RingPos<S> r;
       const uint32_t q_bytes = static_cast<uint32_t>(p.pos * p.g) * 128;
       while (ring.next(&it, &head, abort_flag, false)) {
         const int e0 = tile_end(p, it, 0), e1 = tile_end(p, it, 1);
@@ -131,113 +138,141 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         bool ok = true;
         for (int j = it.kt0; j < end && ok; ++j)
-          for (int kv = 0; kv < 2; ++kv, ++k) {
-            const int st = static_cast<int>(k % S);
-            if (!mbar_wait_inl(smem_u32(&sm->empty[st]), ((k / S) & 1) ^ 1, abort_flag)) {
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!mbar_wait_inl(smem_u32(&sm->empty[r.st]), r.ph ^ 1, abort_flag)) {
               sm->abort = 1;
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(smem_u32(&sm->full[st]), TILE);
+            mbar_arrive_expect_tx(smem_u32(&sm->full[r.st]), TILE);
             for (int c = 0; c < PANELS; ++c)
-              tma_load_3d(skv + st * TILE + c * PANEL, kv ? &vmap : &kmap, c * 64, head, it.k_row + j * kKeyTile,
-                          smem_u32(&sm->full[st]));
+              tma_load_3d(skv + r.st * TILE + c * PANEL, kv ? &vmap : &kmap, c * 64, head, it.k_row + j * kKeyTile,
+                          smem_u32(&sm->full[r.st]));
+            r.step();
+            ++loads;
           }
         if (!ok) break;
       }
       // every copy has landed before the block may end
       if (nq > 0 && !mbar_drain_inl(smem_u32(&sm->q_full), (nq - 1) & 1)) sm->abort = 1;
-      const uint32_t first = k > static_cast<uint32_t>(S) ? k - S : 0;
-      for (uint32_t i = first; i < k; ++i)
+      const uint32_t first = loads > S ? loads - S : 0;
+      for (uint32_t i = first; i < loads; ++i)
         if (!mbar_drain_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
     }
     __syncwarp();
   } else if (warp == 9) {
     // ======================================================== products
-    if (lane == 0) {
-      const uint32_t id_s = make_idesc(BF16, 128, 128);
-      const int dn = (p.d + 15) & ~15;
-      const uint32_t id_o = make_idesc(BF16, 128, dn) | (1u << 16);  // V: consecutive values of one key
-      const int ksteps = dn / 16;
-      const uint64_t dq[2] = {smem_desc(sq, 1024, 2), smem_desc(sq + TILE, 1024, 2)};
-      const uint64_t dk = smem_desc(skv, 1024, 2);
-      const uint64_t dv = smem_desc_mn(skv, PANEL, 1024, 2);
-      ItemRing ring(&sm->slots);
-      AttnItem it;
-      int head;
-      uint32_t k = 0, nq = 0, nfix = 0;
-      uint32_t np[2] = {0, 0};
-      auto scores = [&](int s, uint32_t stage) {
-        for (int i = 0; i < ksteps; ++i) {
-          const uint32_t off = ((i >> 2) * PANEL + (i & 3) * 32) >> 4;
-          tc_mma(t_s[s], dq[s] + off, dk + ((stage * TILE) >> 4) + off, id_s, i > 0);
-        }
-        tc_commit(smem_u32(&sm->s_full[s]));
-      };
-      while (ring.next(&it, &head, abort_flag, false)) {
-        const int end[2] = {tile_end(p, it, 0), tile_end(p, it, 1)};
-        const int last = max(end[0], end[1]);
-        if (last <= it.kt0) continue;
-        bool ok = mbar_wait_inl(smem_u32(&sm->q_full), nq & 1, abort_flag);
-        ++nq;
-        ok = ok && mbar_wait_inl(smem_u32(&sm->full[k % S]), (k / S) & 1, abort_flag);
-        if (!ok) {
-          sm->abort = 1;
-          break;
-        }
-        tc_fence_after();
-        for (int s = 0; s < 2; ++s)
-          if (end[s] > it.kt0) scores(s, k % S);
-        tc_commit(smem_u32(&sm->empty[k % S]));
-        if (last == it.kt0 + 1) tc_commit(smem_u32(&sm->q_empty));
-        ++k;
-        for (int j = it.kt0; j < last; ++j) {
-          const uint32_t kv = k++;  // V of tile j
-          ok = mbar_wait_inl(smem_u32(&sm->full[kv % S]), (kv / S) & 1, abort_flag);
-          const bool tail = it.lk - j * kKeyTile < kKeyTile;
-          if (ok && tail) {  // warp 11 zeroes the rows past the keys meanwhile
-            sm->fix_at = static_cast<int>(kv % S);
-            sm->fix_rows = it.lk - j * kKeyTile;
-            mbar_arrive(smem_u32(&sm->fix_v));
-          }
-          const bool more = j + 1 < last;
-          if (ok && more) ok = mbar_wait_inl(smem_u32(&sm->full[k % S]), (k / S) & 1, abort_flag);
-          bool fixed = false;
-          for (int s = 0; s < 2 && ok; ++s) {
-            if (j >= end[s]) continue;
-            ok = mbar_wait_inl(smem_u32(&sm->p_ready[s]), np[s]++ & 1, abort_flag);
-            if (ok && tail && !fixed) ok = fixed = mbar_wait_inl(smem_u32(&sm->v_fixed), nfix++ & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t bv = dv + (((kv % S) * TILE) >> 4);
-            for (int i = 0; i < kKeyTile / 16; ++i)
-              tc_mma_ts(t_o[s], t_s[s] + i * 8, bv + ((i * 2048) >> 4), id_o, (j > it.kt0 || i > 0) ? 1u : 0u);
-            if (j + 1 == end[s]) tc_commit(smem_u32(&sm->o_full[s]));
-            if (j + 1 < end[s]) scores(s, k % S);
-          }
-          if (!ok) break;
-          tc_commit(smem_u32(&sm->empty[kv % S]));
-          if (more) {
-            tc_commit(smem_u32(&sm->empty[k % S]));
-            if (j + 2 == last) tc_commit(smem_u32(&sm->q_empty));
-            ++k;
-          }
-        }
-        if (!ok) {
-          sm->abort = 1;
-          break;
-        }
+    regs_drop<kFwdSideRegs>();
+    const int dn = (p.d + 15) & ~15;
+    const int ksteps = dn / 16;
+    const uint32_t id_s = make_idesc(BF16, 128, 128);
+    const uint32_t id_o = make_idesc(BF16, 128, dn) | (1u << 16);  // V: consecutive values of one key
+    const uint64_t dk = smem_desc(skv, 1024, 2), dv = smem_desc_mn(skv, PANEL, 1024, 2);
+    const uint32_t q_lo = static_cast<uint32_t>(smem_desc(sq, 1024, 2)), k_lo = static_cast<uint32_t>(dk),
+                   v_lo = static_cast<uint32_t>(dv);
+    const uint32_t k_hi = static_cast<uint32_t>(dk >> 32), v_hi = static_cast<uint32_t>(dv >> 32);
+    ItemRing ring(&sm->slots);
+    AttnItem it;
+    int head;
+    uint32_t nq = 0, nfix = 0;
+    RingPos<S> r;
+    uint32_t np = 0;  // bit s: phase of p_ready[s]
+    while (ring.next(&it, &head, abort_flag, true)) {
+      const int e0 = tile_end(p, it, 0), e1 = tile_end(p, it, 1);
+      const int last = max(e0, e1);
+      if (last <= it.kt0) continue;
+      bool ok = mbar_wait_inl(smem_u32(&sm->q_full), nq & 1, abort_flag);
+      ++nq;
+      ok = ok && mbar_wait_inl(smem_u32(&sm->full[r.st]), r.ph, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        sm->abort = 1;
+        break;
       }
-      tc_commit(smem_u32(&sm->drained));  // every product is done before TMEM is freed
-      if (!mbar_drain_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
+      tc_fence_after();
+      if (elect_lane()) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if ((s ? e1 : e0) <= it.kt0) continue;
+          product_rows<DP>(tmem + s * 128, q_lo + s * (TILE >> 4), k_lo + r.st * (TILE >> 4), k_hi, id_s, ksteps);
+          tc_commit(smem_u32(&sm->s_full[s]));
+        }
+        tc_commit(smem_u32(&sm->empty[r.st]));
+        if (last == it.kt0 + 1) tc_commit(smem_u32(&sm->q_empty));
+      }
+      __syncwarp();
+      r.step();
+      for (int j = it.kt0; j < last; ++j) {
+        const RingPos<S> v = r;  // V of tile j
+        r.step();
+        ok = mbar_wait_inl(smem_u32(&sm->full[v.st]), v.ph, abort_flag);
+        const bool tail = it.lk - j * kKeyTile < kKeyTile;
+        if (tail && lane == 0) {  // warp 11 zeroes the rows past the keys meanwhile
+          sm->fix_at = static_cast<int>(v.st);
+          sm->fix_rows = it.lk - j * kKeyTile;
+          if (ok) mbar_arrive(smem_u32(&sm->fix_v));
+        }
+        const bool more = j + 1 < last;
+        if (more) ok = ok && mbar_wait_inl(smem_u32(&sm->full[r.st]), r.ph, abort_flag);
+        bool fixed = false;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int end = s ? e1 : e0;
+          if (j >= end) continue;
+          ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][0]), (np >> s) & 1, abort_flag);
+          if (tail && !fixed) {
+            ok = ok && mbar_wait_inl(smem_u32(&sm->v_fixed), nfix & 1, abort_flag);
+            ++nfix;
+            fixed = true;
+          }
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+          const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128, b = v_lo + v.st * (TILE >> 4);
+          if (elect_lane()) product_cols<0, 4>(t_o, t_s, 0, b, v_hi, id_o, j > it.kt0);
+          __syncwarp();
+          ok = mbar_wait_inl(smem_u32(&sm->p_ready[s][1]), (np >> s) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          np ^= 1u << s;
+          tc_fence_after();
+          if (elect_lane()) {
+            product_cols<4, 4>(t_o, t_s, 0, b, v_hi, id_o, true);
+            if (j + 1 == end) {
+              tc_commit(smem_u32(&sm->o_full[s]));
+            } else {
+              product_rows<DP>(t_s, q_lo + s * (TILE >> 4), k_lo + r.st * (TILE >> 4), k_hi, id_s, ksteps);
+              tc_commit(smem_u32(&sm->s_full[s]));
+            }
+          }
+          __syncwarp();
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (elect_lane()) {
+          tc_commit(smem_u32(&sm->empty[v.st]));
+          if (more) {
+            tc_commit(smem_u32(&sm->empty[r.st]));
+            if (j + 2 == last) tc_commit(smem_u32(&sm->q_empty));
+          }
+        }
+        __syncwarp();
+        if (more) r.step();
+      }
+      if (!ok) {
+        sm->abort = 1;
+        break;
+      }
     }
+    if (elect_lane()) tc_commit(smem_u32(&sm->drained));  // every product is done before TMEM is freed
+    __syncwarp();
+    if (!mbar_drain_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
     __syncwarp();
   } else if (warp == 10) {
     // ====================================================== work units
+    regs_drop<kFwdSideRegs>();
     if (lane == 0) hand_out(&sm->slots, p.counter, p.items, units, p.heads_kv, abort_flag);
     __syncwarp();
   } else if (warp == 11) {
     // ==================================================== tail of V
+    regs_drop<kFwdSideRegs>();
     // Rows of a V tile past the sequence's keys belong to someone else (or to
     // nobody).  Their weights are zero, but zero times a NaN or an infinity is
     // not, so they are zeroed before the product.
@@ -266,25 +301,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     __syncwarp();
   } else {
     // ======================================================== softmax
+    regs_raise<kFwdMainRegs>();
     const int s = warp >> 2;                      // row tile
     const int row = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t ts = t_s[s] + lane_off, to = t_o[s] + lane_off;
+    const uint32_t ts = tmem + s * 128 + lane_off, to = ts + 256;
     const int pos = row / p.g, gh = row - pos * p.g;
     const float sl = p.scale_log2;
     const float grow = 8.f / sl;                  // growth of the maximum that is let stand
     ItemRing ring(&sm->slots);
-    AttnItem it;
-    int head;
     uint32_t ns = 0, no = 0;
-    while (ring.next(&it, &head, abort_flag, true)) {
-      const int end = tile_end(p, it, s);
+    while (const AttnItem* itp = ring.peek(abort_flag)) {
+      const int kt0 = itp->kt0, end = tile_end(p, *itp, s);
       const int i = s * p.pos + pos;              // this row's query in the item
-      const bool live = pos < p.pos && i < it.n_pos;
-      const int vis = p.causal ? min(it.lk, it.lim0 + i + 1) : it.lk;  // keys it sees
+      const int vis = p.causal ? min(itp->lk, itp->lim0 + i + 1) : itp->lk;  // keys it sees
       float m = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int j = it.kt0; j < end; ++j) {
+      for (int j = kt0; j < end; ++j) {
         ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->s_full[s]), ns & 1, abort_flag));
         ++ns;
         if (!ok) break;
@@ -299,9 +332,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 128; c += 4)
+        for (int c = 0; c < 128; c += 8)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __uint_as_float(x[c + u]));
+          for (int u = 0; u < 4; ++u)
+            mx[u] = max3(mx[u], __uint_as_float(x[c + 2 * u]), __uint_as_float(x[c + 2 * u + 1]));
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const bool raise = mt > m + grow || (m == -INFINITY && mt > m);
         if (__any_sync(0xffffffffu, raise)) {
@@ -309,7 +343,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sl);  // 1 for rows that stay
           m = mn;
           l *= f;
-          if (j > it.kt0) {
+          if (j > kt0) {
             for (int c = 0; c < p.d; c += 16) {
               uint32_t o[16];
               tmem_ld16_raw(to + c, o);
@@ -325,30 +359,36 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint64_t nm = pair2(mm, mm), sl2 = pair2(sl, sl);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < 128; c += 2) {
-          const uint64_t y = mul2(add2(pair2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), nm), sl2);
-          float e0, e1;
-          unpair2(y, e0, e1);
-          e0 = ex2(e0);
-          e1 = ex2(e1);
-          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair2(e0, e1));
-          x[c / 2] = pack_pair<BF16>(e0, e1);
+        for (int q = 0; q < 4; ++q) {  // 32 keys at a time, stored as they are done
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const uint64_t y = mul2(
+                add2(pair2(__uint_as_float(x[q * 32 + 2 * c]), __uint_as_float(x[q * 32 + 2 * c + 1])), nm), sl2);
+            float e0, e1;
+            unpair2(y, e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            sum[c & 1] = add2(sum[c & 1], pair2(e0, e1));
+            w[c] = pack_pair<BF16>(e0, e1);
+          }
+          tmem_st16(ts + q * 16, w);
+          if (q & 1) {  // half of the keys: their product can begin
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm->p_ready[s][q >> 1]));
+          }
         }
         float s0, s1;
         unpair2(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
-        tmem_st32(ts, x);
-        tmem_st32(ts + 32, x + 32);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm->p_ready[s]));
       }
       if (!ok) {
         sm->abort = 1;
         break;
       }
-      const bool have = end > it.kt0;
+      const bool have = end > kt0;
       if (have) {
         if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->o_full[s]), no & 1, abort_flag))) {
           sm->abort = 1;
@@ -357,6 +397,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ++no;
         tc_fence_after();
       }
+      const AttnItem it = *itp;
+      const int head = ring.head();
+      const bool live = pos < p.pos && i < it.n_pos;
       const int64_t tok = static_cast<int64_t>(it.q_row) + i;
       const int h = head * p.g + gh;
       if (it.slot < 0) {
@@ -437,6 +480,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (p.lse) p.lse[tok * p.heads_q + h] = vis > 0 ? mm * p.scale + logf(ll) : -INFINITY;
         }
       }
+      ring.release();
       tc_fence_before();  // O has been read before the next item's products
     }
   }
@@ -478,11 +522,12 @@ sc_status attn_fwd(const AttnArgs& a) {
   const int dp = a.head_dim <= 64 ? 64 : 128;
   const size_t tile = static_cast<size_t>(dp) / 64 * 16384;
   FwdParams p{};
-  p.stages = dp == 64 ? 10 : 5;
-  const size_t smem = (2 + p.stages) * tile + sizeof(FwdSmem) + 1024;
+  const size_t smem = (2 + fwd_stages(dp)) * tile + sizeof(FwdSmem) + 1024;
   const void* kern = a.dtype == SC_BF16 ? fwd_kernel<true>(dp) : fwd_kernel<false>(dp);
-  sc_status st = kernel_setup(kern, smem, nullptr);
+  int regs = 0;
+  sc_status st = kernel_setup(kern, smem, &regs);
   if (st) return st;
+  if (regs != kFwdRegs) return set_error(SC_ERR_CUDA, "attention kernel: not the registers it was written for");
   CUtensorMap qm, km, vm;
   const void* any = a.q.data;  // no key rows: maps of legal sizes that nothing reads
   const bool keys = a.t_k > 0;

@@ -60,16 +60,18 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity, abort_flag);
 }
 // The same wait with its loop inline, for kernels that share out registers
-// between warps (a call would tie all of them to one frame).
+// between warps (a call would tie all of them to one frame), bounded by the
+// SM's cycle counter (about the same two seconds; cheaper to read).
+constexpr long long kWaitCycles = 4000000000ll;
 __device__ __forceinline__ bool mbar_wait_inl(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer();
+  const long long t0 = clock64();
 #pragma unroll 1
   for (uint32_t it = 1; it < (1u << 30); ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63) == 0) {
       if (*abort_flag) return false;
-      if (globaltimer() - t0 > kWaitNs) return false;
+      if (clock64() - t0 > kWaitCycles) return false;
     }
   }
   return false;
@@ -84,11 +86,11 @@ __device__ __noinline__ bool mbar_drain(uint32_t bar, uint32_t parity) {
   return false;
 }
 __device__ __forceinline__ bool mbar_drain_inl(uint32_t bar, uint32_t parity) {
-  const unsigned long long t0 = globaltimer();
+  const long long t0 = clock64();
 #pragma unroll 1
   for (uint32_t it = 0; it < (1u << 30); ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63) == 63 && globaltimer() - t0 > kWaitNs) return false;
+    if ((it & 63) == 63 && clock64() - t0 > kWaitCycles) return false;
   }
   return false;
 }
@@ -122,6 +124,16 @@ __device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar) {
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// A warpgroup's registers a thread, down or up from what the block was launched
+// with (all four warps execute it; raises wait for what others dropped).
+template <int N>
+__device__ __forceinline__ void regs_drop() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_raise() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
@@ -235,14 +247,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 // D[tmem] (+)= A[tmem] * B for one K = 16 step: A's 16-bit values lie two to a
-// column in 8 columns of its rows' lanes.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// column in 8 columns of its rows' lanes; B's descriptor as its two halves.
+__device__ __forceinline__ void tc_mma_ts_lohi(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
+                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // 3D tile of a tensor map at element coordinates (x innermost, y, z).
