@@ -40,27 +40,34 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
 
 // One block lists the work, dearest first: a unit's cost is its number of
 // 128-key (or 128-row) steps, and the kernels take units in the list's order
-// as they get free, so the cheap ones fill the end.  Three passes over the
-// units (their largest cost, a histogram of costs, their places), each over
-// runs of 1024 sequences whose offsets lie in shared memory.  Offsets are
-// checked first; a list that breaks a rule gives no work and latches the error.
+// as they get free, so the cheap ones fill the end.  Passes over the units
+// (their largest cost, a histogram of costs, their places), each over runs of
+// 1024 sequences whose offsets lie in shared memory.  Offsets are checked
+// first; a list that breaks a rule gives no work and latches the error.
+//
+// The keys of a unit are cut where the card would otherwise wait for it: with
+// fewer than two units an SM into about four parts an SM, else only units dearer
+// than an SM's share.  A part costs its fp32 rows written and read once more.
 __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs p) {
   __shared__ int s_q[kPlanThreads + 1], s_k0[kPlanThreads], s_k1[kPlanThreads], s_pre[kPlanThreads + 1];
   __shared__ int s_hist[kBuckets], s_warp[32];
-  __shared__ int s_bad, s_max, s_slots, s_groups;
+  __shared__ int s_bad, s_max, s_items, s_joins, s_parts, s_rows;
   __shared__ unsigned long long s_steps;
   const int tid = threadIdx.x;
   if (tid == 0) {
     s_bad = 0;
     s_max = 1;
-    s_slots = 0;
-    s_groups = 0;
+    s_items = 0;
+    s_joins = 0;
+    s_parts = 0;
+    s_rows = 0;
     s_steps = 0;
   }
   if (tid < kBuckets) s_hist[tid] = 0;
   __syncthreads();
-  int chunk = 0;  // key tiles of a part, 0: whole
-  int my_max = 1;
+  int chunk = 0;     // key tiles of a part, 0: whole
+  bool dual = false;  // single row tiles are worked on by both halves
+  int my_max = 1, my_rows = 0;
   unsigned long long my_steps = 0;
   for (int pass = 0; pass < 3; ++pass) {
     for (int c0 = 0; c0 < p.n_seq; c0 += kPlanThreads) {
@@ -96,7 +103,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs p) {
                                     : (k1 - k0 + kKeyTile - 1) / kKeyTile;
       int total;
       s_pre[tid] = block_scan(tiles, s_warp, &total);
-      if (tid == 0) s_pre[cnt] = total;  // cnt == kPlanThreads: its own place
+      if (tid == 0) {
+        s_pre[cnt] = total;  // cnt == kPlanThreads: its own place
+        if (pass == 0) s_items += total;
+      }
       __syncthreads();
       for (int u = tid; u < total; u += kPlanThreads) {
         int lo = 0, hi = cnt - 1;  // the sequence with s_pre[lo] <= u < s_pre[lo + 1]
@@ -130,23 +140,28 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs p) {
         it.k_row = s_k0[lo];
         it.lk = lk;
         it.pad = 0;
+        it.dual = dual && 2 * it.n_pos <= p.pos_per_item && cost > 1;
         const int ns = chunk && cost > chunk ? (cost + chunk - 1) / chunk : 1;
         const int part = (cost + ns - 1) / ns;
+        const int parts = ns * (it.dual ? 2 : 1);
         if (pass == 0) {
           my_max = max(my_max, cost);
+          my_rows = max(my_rows, it.n_pos * p.g);
           my_steps += static_cast<unsigned long long>(cost);
         } else if (pass == 1) {
           const int b = static_cast<int>(static_cast<int64_t>(kBuckets - 1) * part / s_max);
           atomicAdd(&s_hist[kBuckets - 1 - b], ns);
+          if (parts > 1) atomicAdd(&s_parts, parts);
         } else {
           const int b = static_cast<int>(static_cast<int64_t>(kBuckets - 1) * part / s_max);
           int at = atomicAdd(&s_hist[kBuckets - 1 - b], ns);
           it.nsplit = ns;
+          it.split = 0;
           it.slot = -1;
-          it.group = 0;
-          if (ns > 1) {
-            it.slot = atomicAdd(&s_slots, ns);
-            it.group = atomicAdd(&s_groups, 1);
+          if (parts > 1) {
+            it.slot = atomicAdd(&s_parts, parts);
+            const int j = atomicAdd(&s_joins, 1);
+            if (j < p.join_cap) p.joins[j] = it;
           }
           const int end = it.kt1;
           for (int i = 0; i < ns; ++i, ++at) {
@@ -164,29 +179,44 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs p) {
     if (s_bad) break;
     if (pass == 0) {
       my_max = __reduce_max_sync(0xffffffffu, my_max);
+      my_rows = __reduce_max_sync(0xffffffffu, my_rows);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) my_steps += __shfl_xor_sync(0xffffffffu, my_steps, o);
       if ((tid & 31) == 0) {
         atomicMax(&s_max, my_max);
+        atomicMax(&s_rows, my_rows);
         atomicAdd(&s_steps, my_steps);
       }
       __syncthreads();
-    }
-    if (pass == 0 && p.split_units > 0) {
-      const unsigned long long steps = s_steps * p.heads_kv;
-      const unsigned long long c = (steps + p.split_units - 1) / p.split_units;
-      chunk = static_cast<int>(c < static_cast<unsigned long long>(p.min_tiles) ? p.min_tiles : c);
-      __syncthreads();
-      if (tid == 0) s_max = min(s_max, chunk);
-      __syncthreads();
+      if (p.part_rows > 0) {
+        const unsigned long long steps = s_steps * p.heads_kv;
+        const bool few = static_cast<int64_t>(s_items) * p.heads_kv < 2 * p.sms;
+        const unsigned long long over = static_cast<unsigned long long>(p.sms) * (few ? 4 : 1);
+        const unsigned long long c = (steps + over - 1) / over;
+        chunk = static_cast<int>(c < static_cast<unsigned long long>(p.min_tiles) ? p.min_tiles : c);
+        dual = true;
+      }
     }
     if (pass == 1) {
-      __syncthreads();
+      // partial results that do not fit: whole units after all
+      if (s_parts * static_cast<int64_t>(p.heads_kv) * s_rows > p.part_rows) {
+        __syncthreads();
+        chunk = 0;
+        dual = false;
+        if (tid < kBuckets) s_hist[tid] = 0;
+        if (tid == 0) s_parts = 0;
+        pass = 0;  // the histogram again
+        __syncthreads();
+        continue;
+      }
       int total;
       const int v = tid < kBuckets ? s_hist[tid] : 0;
       const int e = block_scan(v, s_warp, &total);
       if (tid < kBuckets) s_hist[tid] = e;
-      if (tid == 0) p.header[0] = min(total, p.cap);
+      if (tid == 0) {
+        s_parts = 0;
+        p.header[0] = min(total, p.cap);
+      }
       __syncthreads();
     }
   }
@@ -195,11 +225,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs p) {
     if (s_bad || p.n_seq == 0) p.header[0] = 0;
     if (s_bad) atomicOr(p.status, kDevErrRange);
     p.header[1] = 0;
-    p.header[2] = s_slots;
-    p.header[3] = s_groups;
+    p.header[2] = s_bad ? 0 : min(s_joins, p.join_cap);
+    p.header[3] = s_rows;
   }
-  const int n_done = min(p.done_cap, s_groups * p.heads_kv * 8);
-  for (int i = tid; i < n_done; i += kPlanThreads) p.done[i] = 0;
 }
 
 }  // namespace

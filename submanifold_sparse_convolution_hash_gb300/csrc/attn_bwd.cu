@@ -888,6 +888,8 @@ sc_status attn_bwd(const AttnArgs& a) {
   pl.t_q = a.t_q;
   pl.t_k = a.t_k;
   pl.pos_per_item = pos;
+  pl.g = g;
+  pl.sms = sms;
   pl.causal = a.causal;
   pl.packed_keys = 1;
   pl.heads_kv = a.heads_kv;

@@ -32,8 +32,7 @@ struct FwdParams {
   const int* header;
   int* counter;          // next unit
   const AttnItem* items;
-  int* done;
-  float* part;           // partial results [slot][head][2 * 128 rows][d + 2]
+  float* part;           // partial results [slot][head][header[3] rows][d + 8]: O, m, l
   int heads_q, heads_kv, g, pos;  // pos: queries of a row tile
   int d;
   float scale_log2, scale;
@@ -53,8 +52,10 @@ struct FwdSmem {
   int fix_at, fix_rows;  // ring stage of a V tile that ends inside, and its keys
 };
 
-// Key tiles that row tile s of the item has to see: [kt0, end).
+// Key tiles that row tile s of the item has to see: [kt0, end).  In a dual item
+// both halves have the one row tile, half s every other key tile from kt0 + s.
 __device__ __forceinline__ int tile_end(const FwdParams& p, const AttnItem& it, int s) {
+  if (it.dual) s = 0;
   const int n = min(it.n_pos - s * p.pos, p.pos);  // queries of the tile
   if (n <= 0) return it.kt0;
   const int seen = p.causal ? min(it.lk, it.lim0 + s * p.pos + n) : it.lk;
@@ -128,17 +129,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           break;
         }
         ++nq;
-        const int tiles = (e0 > it.kt0 ? 1 : 0) + (e1 > it.kt0 ? 1 : 0);
-        mbar_arrive_expect_tx(smem_u32(&sm->q_full), tiles * PANELS * q_bytes);
+        const bool second = e1 > it.kt0 && !it.dual;
+        mbar_arrive_expect_tx(smem_u32(&sm->q_full), ((e0 > it.kt0 ? 1 : 0) + (second ? 1 : 0)) * PANELS * q_bytes);
         for (int s = 0; s < 2; ++s) {
-          if ((s ? e1 : e0) <= it.kt0) continue;
+          if (s ? !second : e0 <= it.kt0) continue;
           for (int c = 0; c < PANELS; ++c)
             tma_load_3d(sq + s * TILE + c * PANEL, &qmap, c * 64, head * p.g, it.q_row + s * p.pos,
                         smem_u32(&sm->q_full));
         }
         bool ok = true;
-        for (int j = it.kt0; j < end && ok; ++j)
-          for (int kv = 0; kv < 2; ++kv) {
+        // K and V by turns; a dual item's in pairs: K K V V
+        const int step = it.dual ? 2 : 1;
+        for (int j = it.kt0; j < end && ok; j += step)
+          for (int u = 0; u < 2 * step; ++u) {
+            const int kv = u >= step, tile = j + u % step;
+            if (tile >= end) continue;
             if (!mbar_wait_inl(smem_u32(&sm->empty[r.st]), r.ph ^ 1, abort_flag)) {
               sm->abort = 1;
               ok = false;
@@ -146,7 +151,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
             mbar_arrive_expect_tx(smem_u32(&sm->full[r.st]), TILE);
             for (int c = 0; c < PANELS; ++c)
-              tma_load_3d(skv + r.st * TILE + c * PANEL, kv ? &vmap : &kmap, c * 64, head, it.k_row + j * kKeyTile,
+              tma_load_3d(skv + r.st * TILE + c * PANEL, kv ? &vmap : &kmap, c * 64, head, it.k_row + tile * kKeyTile,
                           smem_u32(&sm->full[r.st]));
             r.step();
             ++loads;
@@ -183,6 +188,79 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (last <= it.kt0) continue;
       bool ok = mbar_wait_inl(smem_u32(&sm->q_full), nq & 1, abort_flag);
       ++nq;
+      if (it.dual) {
+        const int n = last - it.kt0;  // half t & 1 takes tile t
+        auto scores = [&](int t, const RingPos<S>& at) {
+          ok = __all_sync(0xffffffffu, ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph, abort_flag));
+          if (!ok) return;
+          tc_fence_after();
+          if (elect_lane()) {
+            product_rows<DP>(tmem + (t & 1) * 128, q_lo, k_lo + at.st * (TILE >> 4), k_hi, id_s, ksteps);
+            tc_commit(smem_u32(&sm->s_full[t & 1]));
+            tc_commit(smem_u32(&sm->empty[at.st]));
+            if (t + 1 == n) tc_commit(smem_u32(&sm->q_empty));
+          }
+          __syncwarp();
+        };
+        scores(0, r);
+        r.step();
+        if (n > 1) {
+          scores(1, r);
+          r.step();
+        }
+        for (int t0 = 0; t0 < n && ok; t0 += 2) {
+          RingPos<S> v = r;  // V of t0 (and t0 + 1), then K of t0 + 2 (and t0 + 3)
+          RingPos<S> k = r;
+          k.step();
+          if (t0 + 1 < n) k.step();
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int t = t0 + s;
+            if (t >= n) continue;
+            ok = ok && mbar_wait_inl(smem_u32(&sm->full[v.st]), v.ph, abort_flag);
+            const int left = it.lk - (it.kt0 + t) * kKeyTile;
+            if (left < kKeyTile) {
+              if (lane == 0 && ok) {
+                sm->fix_at = static_cast<int>(v.st);
+                sm->fix_rows = left;
+                mbar_arrive(smem_u32(&sm->fix_v));
+              }
+              ok = ok && mbar_wait_inl(smem_u32(&sm->v_fixed), nfix & 1, abort_flag);
+              ++nfix;
+            }
+            for (int h = 0; h < 2; ++h) {
+              ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][h]), (np >> s) & 1, abort_flag);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_lane()) {
+                const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128, b = v_lo + v.st * (TILE >> 4);
+                if (h == 0) {
+                  product_cols<0, 4>(t_o, t_s, 0, b, v_hi, id_o, t > 1);
+                } else {
+                  product_cols<4, 4>(t_o, t_s, 0, b, v_hi, id_o, true);
+                  tc_commit(smem_u32(&sm->empty[v.st]));
+                  if (t + 2 >= n) tc_commit(smem_u32(&sm->o_full[s]));
+                }
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+            np ^= 1u << s;
+            if (t + 2 < n) {
+              scores(t + 2, k);
+              k.step();
+            }
+            v.step();
+          }
+          r = k;
+        }
+        if (!ok) {
+          sm->abort = 1;
+          break;
+        }
+        continue;
+      }
       ok = ok && mbar_wait_inl(smem_u32(&sm->full[r.st]), r.ph, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) {
         sm->abort = 1;
@@ -312,12 +390,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     ItemRing ring(&sm->slots);
     uint32_t ns = 0, no = 0;
     while (const AttnItem* itp = ring.peek(abort_flag)) {
-      const int kt0 = itp->kt0, end = tile_end(p, *itp, s);
-      const int i = s * p.pos + pos;              // this row's query in the item
+      const int dual = itp->dual;
+      const int j0 = itp->kt0 + (dual ? s : 0), end = tile_end(p, *itp, s);
+      const int i = (dual ? 0 : s * p.pos) + pos;  // this row's query in the item
       const int vis = p.causal ? min(itp->lk, itp->lim0 + i + 1) : itp->lk;  // keys it sees
       float m = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int j = kt0; j < end; ++j) {
+      for (int j = j0; j < end; j += 1 + dual) {
         ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->s_full[s]), ns & 1, abort_flag));
         ++ns;
         if (!ok) break;
@@ -343,7 +422,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sl);  // 1 for rows that stay
           m = mn;
           l *= f;
-          if (j > kt0) {
+          if (j > j0) {
             for (int c = 0; c < p.d; c += 16) {
               uint32_t o[16];
               tmem_ld16_raw(to + c, o);
@@ -388,7 +467,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         sm->abort = 1;
         break;
       }
-      const bool have = end > kt0;
+      const bool have = end > j0;
       if (have) {
         if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->o_full[s]), no & 1, abort_flag))) {
           sm->abort = 1;
@@ -422,62 +501,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         if (p.lse && live) p.lse[tok * p.heads_q + h] = vis > 0 ? m * p.scale + logf(l) : -INFINITY;
       } else {
-        // a part of the keys: O, m and l in fp32
-        const int64_t pr = (static_cast<int64_t>(it.slot + it.split) * p.heads_kv + head) * 256 + threadIdx.x;
-        float* dst = p.part + pr * (p.d + 8);
+        // a part of the keys: O, m and l in fp32 for k_attn_join
+        const int part = it.slot + (dual ? 2 * it.split + s : it.split);
+        float* dst = p.part + ((static_cast<int64_t>(part) * p.heads_kv + head) * p.header[3] + i * p.g + gh) * (p.d + 8);
         if (live) {
           dst[p.d] = have ? m : -INFINITY;
           dst[p.d + 1] = l;
         }
-        for (int c = 0; c < p.d && have; c += 8) {
+        for (int c = 0; c < p.d && have; c += 16) {
           uint32_t o[16];
-          tmem_ld16_raw(to + (c & ~15), o);
+          tmem_ld16_raw(to + c, o);
           if (live) {
-            const int b = c & 8;
-            *reinterpret_cast<uint4*>(dst + c) = b ? make_uint4(o[8], o[9], o[10], o[11]) : make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + c + 4) = b ? make_uint4(o[12], o[13], o[14], o[15]) : make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+            for (int u = 0; u < 16; u += 4)
+              if (c + u < p.d) *reinterpret_cast<uint4*>(dst + c + u) = make_uint4(o[u], o[u + 1], o[u + 2], o[u + 3]);
           }
-        }
-        // A warp's rows are joined by the warp that finishes their last part:
-        // no wait on anybody, and in the parts' order whoever comes last.
-        __threadfence();
-        __syncwarp();
-        int was = 0;
-        if (lane == 0) was = atomicAdd(p.done + (it.group * p.heads_kv + head) * 8 + warp, 1);
-        was = __shfl_sync(0xffffffffu, was, 0);
-        if (was == it.nsplit - 1 && live) {
-          __threadfence();
-          const int64_t step = static_cast<int64_t>(p.heads_kv) * 256 * (p.d + 8);
-          const float* src = p.part + ((static_cast<int64_t>(it.slot) * p.heads_kv + head) * 256 + threadIdx.x) * (p.d + 8);
-          float mm = -INFINITY, ll = 0.f;
-          for (int q = 0; q < it.nsplit; ++q) mm = fmaxf(mm, __ldcg(src + q * step + p.d));
-          const float base = mm == -INFINITY ? 0.f : mm;
-          for (int q = 0; q < it.nsplit; ++q)
-            ll += __ldcg(src + q * step + p.d + 1) * ex2((__ldcg(src + q * step + p.d) - base) * sl);
-          const float inv = vis > 0 ? 1.f / ll : 0.f;
-          uint8_t* out = p.out + tok * p.out_t + h * p.out_h;
-          for (int c = 0; c < p.d; c += 8) {
-            float a[8] = {};
-            for (int q = 0; q < it.nsplit; ++q) {
-              const float mq = __ldcg(src + q * step + p.d);
-              if (mq == -INFINITY) continue;  // nothing seen in this part: no O was written
-              const float f = ex2((mq - base) * sl) * inv;
-              const float4 u = __ldcg(reinterpret_cast<const float4*>(src + q * step + c));
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(src + q * step + c + 4));
-              a[0] = fmaf(u.x, f, a[0]);
-              a[1] = fmaf(u.y, f, a[1]);
-              a[2] = fmaf(u.z, f, a[2]);
-              a[3] = fmaf(u.w, f, a[3]);
-              a[4] = fmaf(v.x, f, a[4]);
-              a[5] = fmaf(v.y, f, a[5]);
-              a[6] = fmaf(v.z, f, a[6]);
-              a[7] = fmaf(v.w, f, a[7]);
-            }
-            *reinterpret_cast<uint4*>(out + c * 2) =
-                make_uint4(pack_pair<BF16>(a[0], a[1]), pack_pair<BF16>(a[2], a[3]), pack_pair<BF16>(a[4], a[5]),
-                           pack_pair<BF16>(a[6], a[7]));
-          }
-          if (p.lse) p.lse[tok * p.heads_q + h] = vis > 0 ? mm * p.scale + logf(ll) : -INFINITY;
         }
       }
       ring.release();
@@ -494,6 +532,57 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, kDevErrTimeout);
 }
 
+// Joins the parts of the rows whose keys were cut, a warp a row, four values a
+// lane: with m the largest of the parts' maxima, out = sum O_q f_q / sum l_q f_q,
+// f_q = exp(scale (m_q - m)).  The parts are taken in order, whoever made them.
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const AttnItem* joins) {
+  const int n = p.header[2], stride = p.header[3];
+  const int lane = threadIdx.x & 31;
+  const int64_t step = static_cast<int64_t>(p.heads_kv) * stride * (p.d + 8);  // one part to the next
+  const int64_t total = static_cast<int64_t>(n) * p.heads_kv * stride;
+  for (int64_t u = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5; u < total;
+       u += static_cast<int64_t>(gridDim.x) * 8) {
+    const int r = static_cast<int>(u % stride);
+    const int64_t jh = u / stride;
+    const int head = static_cast<int>(jh % p.heads_kv);
+    const AttnItem* it = joins + jh / p.heads_kv;
+    if (r >= it->n_pos * p.g) continue;
+    const int i = r / p.g, h = head * p.g + r - i * p.g;
+    const int parts = it->nsplit * (it->dual ? 2 : 1);
+    const float* src = p.part + ((static_cast<int64_t>(it->slot) * p.heads_kv + head) * stride + r) * (p.d + 8);
+    float m = -INFINITY;
+    for (int q = lane; q < parts; q += 32) m = fmaxf(m, __ldg(src + q * step + p.d));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool on = lane * 4 < p.d;
+#pragma unroll 4
+    for (int q = 0; q < parts; ++q) {
+      const float mq = __ldg(src + q * step + p.d);
+      const float f = ex2((mq - base) * p.scale_log2);
+      l += __ldg(src + q * step + p.d + 1) * f;
+      // nothing seen in this part: no O was written
+      const float4 o = on && mq != -INFINITY ? __ldg(reinterpret_cast<const float4*>(src + q * step) + lane)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+      a.x = fmaf(o.x, f, a.x);
+      a.y = fmaf(o.y, f, a.y);
+      a.z = fmaf(o.z, f, a.z);
+      a.w = fmaf(o.w, f, a.w);
+    }
+    const int vis = p.causal ? min(it->lk, it->lim0 + i + 1) : it->lk;
+    const float inv = vis > 0 ? 1.f / l : 0.f;
+    const int64_t tok = static_cast<int64_t>(it->q_row) + i;
+    if (on)
+      *reinterpret_cast<uint2*>(p.out + tok * p.out_t + h * p.out_h + lane * 8) =
+          vis > 0 ? make_uint2(pack_pair<BF16>(a.x * inv, a.y * inv), pack_pair<BF16>(a.z * inv, a.w * inv))
+                  : make_uint2(0u, 0u);
+    if (p.lse && lane == 0) p.lse[tok * p.heads_q + h] = vis > 0 ? m * p.scale + logf(l) : -INFINITY;
+  }
+}
+
 template <bool BF16>
 const void* fwd_kernel(int dp) {
   return dp == 64 ? reinterpret_cast<const void*>(k_attn_fwd<BF16, 64>)
@@ -507,16 +596,22 @@ sc_status attn_fwd(const AttnArgs& a) {
   const int sms = device_sm_count();
   const int64_t items_ub = a.t_q / (2 * pos) + a.n_seq;
   if (items_ub * a.heads_kv > 0x3fffffff) return set_error(SC_ERR_UNSUPPORTED, "too many query tiles");
-  // Few units for the card: the keys are cut, so that there are about four units an SM.
-  const bool split = items_ub * a.heads_kv <= 8ll * sms;
-  const int split_units = 4 * sms;
-  const int64_t slots = split ? split_units / a.heads_kv + 1 + items_ub : 0;
-  const int64_t cap = items_ub + slots;
+  // Partial results: room for about four parts an SM and two an item, where an
+  // item has few rows (a guess from the average; the plan sees whether they
+  // fit) or the items are few.
+  const int64_t avg = a.n_seq ? (a.t_q * g + a.n_seq - 1) / a.n_seq : 0;
+  const bool few = items_ub * a.heads_kv <= 8ll * sms;
+  const int64_t rows_guess = few ? 2 * pos * g : 2 * avg;
+  const int64_t slots = 8ll * sms / a.heads_kv + 2 + 2 * items_ub;
+  int64_t part_rows = few || avg <= 32 ? slots * a.heads_kv * (rows_guess < 2 * pos * g ? rows_guess : 2 * pos * g) : 0;
+  const int64_t row_bytes = (a.head_dim + 8) * 4ll;
+  if (part_rows * row_bytes > (int64_t(1) << 28)) part_rows = (int64_t(1) << 28) / row_bytes;
+  const int64_t cap = items_ub + (part_rows ? slots : 0);
   Arena ar;
   const size_t o_head = ar.take(kPlanHeader * sizeof(int));
   const size_t o_items = ar.take(static_cast<size_t>(cap) * sizeof(AttnItem));
-  const size_t o_done = ar.take(split ? static_cast<size_t>(items_ub * a.heads_kv) * 8 * sizeof(int) : 0);
-  const size_t o_part = ar.take(static_cast<size_t>(slots) * a.heads_kv * 256 * (a.head_dim + 8) * sizeof(float));
+  const size_t o_joins = ar.take(part_rows ? static_cast<size_t>(items_ub) * sizeof(AttnItem) : 0);
+  const size_t o_part = ar.take(static_cast<size_t>(part_rows * row_bytes));
   int* status = attn_status_word();
   if (!status) return set_error(SC_ERR_CUDA, "the attention status word is not available");
   const int dp = a.head_dim <= 64 ? 64 : 128;
@@ -553,13 +648,15 @@ sc_status attn_fwd(const AttnArgs& a) {
   pl.causal = a.causal;
   pl.heads_kv = a.heads_kv;
   pl.mode = kPlanRows;
-  pl.split_units = split ? split_units : 0;
-  pl.min_tiles = 2;
+  pl.g = g;
+  pl.sms = sms;
+  pl.part_rows = part_rows;
+  pl.min_tiles = 4;
   pl.cap = static_cast<int>(cap);
+  pl.join_cap = part_rows ? static_cast<int>(items_ub) : 0;
   pl.header = reinterpret_cast<int*>(base + o_head);
   pl.items = reinterpret_cast<AttnItem*>(base + o_items);
-  pl.done = reinterpret_cast<int*>(base + o_done);
-  pl.done_cap = split ? static_cast<int>(items_ub * a.heads_kv) * 8 : 0;
+  pl.joins = reinterpret_cast<AttnItem*>(base + o_joins);
   pl.status = status;
   st = attn_plan(pl, a.stream);
   if (!st) {
@@ -570,7 +667,6 @@ sc_status attn_fwd(const AttnArgs& a) {
     p.header = pl.header;
     p.counter = pl.header + 1;
     p.items = pl.items;
-    p.done = pl.done;
     p.part = reinterpret_cast<float*>(base + o_part);
     p.heads_q = a.heads_q;
     p.heads_kv = a.heads_kv;
@@ -588,6 +684,15 @@ sc_status attn_fwd(const AttnArgs& a) {
     SC_LAUNCH("attn_fwd", a.stream,
               (e = cudaLaunchKernel(kern, dim3(grid), dim3(kFwdThreads), args, smem, a.stream)));
     if (e != cudaSuccess) st = set_cuda_error(e, "attn_fwd");
+    if (!st && part_rows) {
+      const int64_t warps = a.t_q * a.heads_q;
+      const unsigned nb = static_cast<unsigned>(warps < 32ll * sms ? (warps + 7) / 8 : 4 * sms);
+      SC_LAUNCH("attn_join", a.stream,
+                (a.dtype == SC_BF16 ? k_attn_join<true><<<nb, 256, 0, a.stream>>>(p, pl.joins)
+                                    : k_attn_join<false><<<nb, 256, 0, a.stream>>>(p, pl.joins)));
+      e = cudaGetLastError();
+      if (e != cudaSuccess) st = set_cuda_error(e, "attn_join");
+    }
   }
   dev_free(ws, a.stream);
   return st;

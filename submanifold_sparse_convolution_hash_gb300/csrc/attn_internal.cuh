@@ -25,12 +25,13 @@ struct __align__(16) AttnItem {
   int kt0, kt1;  // key tiles [kt0, kt1); gk, gv: kt0 is the item's key tile
   int slot;    // first of its partial results, or -1: it writes the result itself
   int split, nsplit;  // which of how many parts of the keys
-  int group;   // counter of the parts that are done
+  int dual;    // one row tile: both halves of the block work on it, on every other key tile
   int pad;
 };
 static_assert(sizeof(AttnItem) == 48, "read as three 16-byte words");
 
-// Written by k_attn_plan: [0] items, [1] next work unit, [2] slots, [3] groups.
+// Written by k_attn_plan: [0] items, [1] next work unit, [2] joins, [3] rows of
+// a partial result.
 constexpr int kPlanHeader = 16;  // ints
 
 enum PlanMode { kPlanRows = 0, kPlanKeys = 1 };
@@ -39,18 +40,19 @@ struct PlanArgs {
   const int *q_off, *k_off, *k_len;
   int n_seq;
   int64_t t_q, t_k;
-  int pos_per_item;  // queries of an item (kPlanRows)
+  int pos_per_item;  // queries of an item (kPlanRows), of a row tile (kPlanKeys)
+  int g;
   int causal;
   int packed_keys;   // the key lists have to cover every key row
   int heads_kv;
   int mode;
-  int split_units;   // kPlanRows: cut the keys so that there are about so many units; 0: never
-  int min_tiles;     // least key tiles of a part
-  int cap;           // items that fit
+  int sms;
+  int64_t part_rows;  // rows of partial results that fit; 0: the keys are never cut
+  int min_tiles;      // least key tiles of a part
+  int cap, join_cap;  // items and joins that fit
   int* header;
   AttnItem* items;
-  int* done;         // per group, key head and warp of rows: parts that are done (zeroed here)
-  int done_cap;
+  AttnItem* joins;    // per item that has parts: where its rows and parts are
   int* status;
 };
 sc_status attn_plan(const PlanArgs& a, cudaStream_t s);
