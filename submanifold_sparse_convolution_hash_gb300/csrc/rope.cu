@@ -12,8 +12,11 @@
 // memory bounds it.  A row lies in a group of LPR lanes, eight consecutive
 // values (one 16-byte load of 16-bit types) a lane, so the norm is a sum over
 // the group by shuffles; the partner of a pair comes from the lane that holds
-// it.  The angles of a token serve all its heads: a block computes them once
-// for its tokens and keeps them in shared memory.
+// it.  A group takes one token's heads, or some of them, one after the other,
+// four rows' loads in flight: a lane's angles are the same for all heads of a
+// token, so it works them out once and keeps them, with the weights folded in,
+// in registers (a table in shared memory, read for every row, made the kernel
+// three times slower).
 #include "sc_internal.cuh"
 
 namespace sc {
@@ -78,7 +81,7 @@ template <int NW>
 __device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[NW]) {
 #pragma unroll
   for (int i = 0; i < NW / 4; ++i) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
     w[4 * i] = v.x;
     w[4 * i + 1] = v.y;
     w[4 * i + 2] = v.z;
@@ -89,7 +92,7 @@ template <int NW>
 __device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[NW]) {
 #pragma unroll
   for (int i = 0; i < NW / 4; ++i)
-    reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    __stcs(reinterpret_cast<uint4*>(p) + i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
 }
 
 template <int LPR>
@@ -101,23 +104,33 @@ __device__ __forceinline__ float group_sum(float v) {
 
 // cos and sin of pos * f, times amp.  The product can be thousands of turns,
 // and 32 bits of it would leave few for the fraction (1e-3 radians at position
-// 32768, f = 1).  So it is formed in turns and in parts whose whole turns drop
-// out exactly: c = f / 2 pi as a sum of two floats, the position as a multiple
-// of 4096 and a rest, and the rounding error of each product by fma.
+// 32768, f = 1).  So it is formed in turns, c = f / 2 pi as a sum of two floats,
+// and the product's rounding error is taken along by fma; a position that a
+// float does not hold goes in two parts, a multiple of 4096 and a rest.  The
+// rows are then f32 (EXACT: a few units in the last place) or 16-bit, for which
+// the fast sine's 2^-20 is far below the output's rounding.
+template <bool EXACT>
 __device__ __forceinline__ float2 angle(int pos, float f, float amp) {
   const float kInv2PiHi = 0x1.45f306p-3f;   // 1 / 2 pi to 24 bits
   const float kInv2PiLo = 0x1.b9391p-28f;   // the rest of it
   const float c = f * kInv2PiHi;
   const float ce = fmaf(f, kInv2PiHi, -c) + f * kInv2PiLo;
   const int lo = pos & 4095;
-  const float xh = static_cast<float>(pos - lo), xl = static_cast<float>(lo);
-  const float th = xh * c, tl = xl * c;
-  const float eh = fmaf(xh, c, -th) + xh * ce, el = fmaf(xl, c, -tl) + xl * ce;
-  float t = (th - rintf(th)) + (tl - rintf(tl));
-  t += eh + el;
+  const bool small = pos > -(1 << 24) && pos < (1 << 24);
+  const float xh = static_cast<float>(small ? pos : pos - lo);
+  float t = xh * c;
+  float e = fmaf(xh, c, -t) + xh * ce;
+  t -= rintf(t);
+  if (!small) {
+    const float xl = static_cast<float>(lo), tl = xl * c;
+    e += fmaf(xl, c, -tl) + xl * ce;
+    t += tl - rintf(tl);
+  }
+  t += e;
   t -= rintf(t);
   float s, co;
-  sincospif(2.f * t, &s, &co);
+  if constexpr (EXACT) sincospif(2.f * t, &s, &co);
+  else __sincosf(6.283185307179586f * t, &s, &co);
   return make_float2(co * amp, s * amp);
 }
 
@@ -130,24 +143,36 @@ struct RopeParams {
   int64_t yt[2], yh[2];
   int heads[2];
   const float* w[2];
-  float* gw_part;            // backward with a norm: [blocks][2][D]
+  float* gw_part;            // backward with a norm: [blocks][D]
   const int* pos;
   int64_t pos_stride;        // elements between tokens
   const float* freq;
   int64_t tokens;
   int d, half, per;          // half = R / 2 pairs, per = pairs of one axis
-  int nt;                    // tokens of a block's step
+  int chunks;                // groups that share a token's heads
+  int per_chunk[2];          // heads of each
+  int blocks_q;              // backward: blocks that take q, the others take k
   float eps, amp;
 };
 
-// Partner values (the other member of the pair) of this lane's eight, pairs
-// (i, i + half): by shuffles where half is a multiple of 8 (a whole lane's
-// values move), else through `stage`, the warp's rows in shared memory.
-template <typename T, int LPR, bool ALIGNED>
-__device__ __forceinline__ void partner_half(const uint32_t (&w)[Vec8<T>::kWords], float (&p)[8], int gl, int half,
-                                             T* stage) {
+// How the partners of a lane's eight values, pairs (i, i + half), are fetched.
+enum Pairing {
+  kInterleaved,  // pairs (2i, 2i + 1): in the lane itself
+  kHalf8,        // half a multiple of 8: a whole lane's values, by shuffles
+  kHalf2,        // even: two values at a time from the warp's rows in shared memory
+  kHalf1,        // odd: one at a time
+};
+
+template <typename T, int LPR, int PAIRING>
+__device__ __forceinline__ void partners(const uint32_t (&w)[Vec8<T>::kWords], float (&p)[8], int gl, int half,
+                                         T* stage) {
   constexpr int NW = Vec8<T>::kWords;
-  if constexpr (ALIGNED) {
+  if constexpr (PAIRING == kInterleaved) {
+    float x[8];
+    Vec8<T>::unpack(w, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = x[j ^ 1];
+  } else if constexpr (PAIRING == kHalf8) {
     const int step = half >> 3;
     const int from = gl < step ? gl + step : (gl < 2 * step ? gl - step : gl);
     uint32_t o[NW];
@@ -155,240 +180,297 @@ __device__ __forceinline__ void partner_half(const uint32_t (&w)[Vec8<T>::kWords
     for (int i = 0; i < NW; ++i) o[i] = __shfl_sync(0xffffffffu, w[i], from, LPR);
     Vec8<T>::unpack(o, p);
   } else {
-    const int lane = threadIdx.x & 31;
-    T* row = stage + (lane / LPR) * (LPR * 8);
-    __syncwarp();
-    store_words<NW>(row + gl * 8, w);
+    T* row = stage + ((threadIdx.x & 31) / LPR) * (LPR * 8);
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = gl * 8 + j;
-      const int o = e < half ? e + half : (e < 2 * half ? e - half : e);
-      p[j] = static_cast<float>(row[o]);
-    }
-  }
-}
-
-// The angles of a step's tokens into shared memory: [nt][half].
-__device__ __forceinline__ void fill_angles(const RopeParams& p, int64_t t0, float2* s_cs) {
-  const int n = static_cast<int>(min(static_cast<int64_t>(p.nt), p.tokens - t0)) * p.half;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int t = i / p.half, pair = i - t * p.half;
-    const int pos = __ldg(p.pos + (t0 + t) * p.pos_stride + pair / p.per);
-    s_cs[i] = angle(pos, __ldg(p.freq + pair), p.amp);
-  }
-}
-
-// Turns z (this lane's values e0 .. e0 + 7) by its angles, `sign` -1 for the
-// transpose.  zp: the partners of z.
-template <bool ILV>
-__device__ __forceinline__ void turn(float (&y)[8], const float (&z)[8], const float (&zp)[8], const float2* cs,
-                                     int e0, int half, float sign) {
-  if constexpr (ILV) {
+    for (int i = 0; i < NW / 4; ++i)
+      reinterpret_cast<uint4*>(row + gl * 8)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    __syncwarp();
+    if constexpr (PAIRING == kHalf2 && sizeof(T) == 2) {
+      uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const int pair = (e0 + j) >> 1;
-      const float2 c = pair < half ? cs[pair] : make_float2(1.f, 0.f);
-      y[j] = z[j] * c.x - sign * z[j + 1] * c.y;
-      y[j + 1] = z[j + 1] * c.x + sign * z[j] * c.y;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = e0 + j;
-      const bool first = e < half;
-      const int pair = first ? e : e - half;
-      const float2 c = pair < half ? cs[pair] : make_float2(1.f, 0.f);
-      y[j] = z[j] * c.x + (first ? -sign : sign) * zp[j] * c.y;
-    }
-  }
-}
-
-// One block's step covers nt tokens: rows of q, then rows of k.
-template <typename T, int LPR, bool ILV, bool ALIGNED, bool NORM>
-__global__ void __launch_bounds__(kThreads) k_rope_fwd(const RopeParams p) {
-  constexpr int NW = Vec8<T>::kWords, GROUPS = kThreads / LPR;
-  extern __shared__ float2 s_cs[];
-  T* stage = reinterpret_cast<T*>(s_cs + ((p.nt * p.half + 1) & ~1)) + (threadIdx.x >> 5) * 256;
-  const int gl = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-  const int e0 = gl * 8;
-  const bool act = e0 < p.d;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.nt;
-  const int nt = static_cast<int>(min(static_cast<int64_t>(p.nt), p.tokens - t0));
-  fill_angles(p, t0, s_cs);
-  __syncthreads();
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const int heads = p.heads[side];
-    if (heads == 0) continue;
-    const int rows = nt * heads;
-    float w[8], wp[8];
-    if constexpr (NORM) {
+      for (int j = 0; j < 4; ++j) {
+        const int e = gl * 8 + 2 * j;
+        o[j] = *reinterpret_cast<const uint32_t*>(row + (e < half ? e + half : (e < 2 * half ? e - half : e)));
+      }
+      Vec8<T>::unpack(o, p);
+    } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int e = e0 + j;
-        const int o = e < p.half ? e + p.half : (e < 2 * p.half ? e - p.half : e);
-        w[j] = e < p.d ? __ldg(p.w[side] + e) : 0.f;
-        wp[j] = o < p.d ? __ldg(p.w[side] + o) : 0.f;
-      }
-    }
-    // whole warps stay in the loop: the shuffles below are warp-wide
-    for (int r0 = 0; r0 < rows; r0 += GROUPS) {
-      const int r = r0 + grp;
-      const bool on = r < rows && act;
-      const int t = on ? r / heads : 0, h = on ? r - t * heads : 0;
-      uint32_t a[NW] = {};
-      if (on) load_words<NW>(p.x[side] + (t0 + t) * p.xt[side] + h * p.xh[side] + e0 * sizeof(T), a);
-      float x[8], xp[8] = {}, y[8];
-      Vec8<T>::unpack(a, x);
-      if constexpr (!ILV) partner_half<T, LPR, ALIGNED>(a, xp, gl, p.half, stage);
-      if constexpr (NORM) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-        const float rn = 1.f / sqrtf(group_sum<LPR>(ss) / static_cast<float>(p.d) + p.eps);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[j] *= rn * w[j];
-          if constexpr (!ILV) xp[j] *= rn * wp[j];
-        }
-      }
-      turn<ILV>(y, x, xp, s_cs + t * p.half, e0, p.half, 1.f);
-      if (on) {
-        Vec8<T>::pack(y, a);
-        store_words<NW>(p.y[side] + (t0 + t) * p.yt[side] + h * p.yh[side] + e0 * sizeof(T), a);
+        const int e = gl * 8 + j;
+        p[j] = static_cast<float>(row[e < half ? e + half : (e < 2 * half ? e - half : e)]);
       }
     }
   }
 }
 
-// The gradient.  Blocks walk the steps grid-wide, so that each keeps its sum of
-// the weights' gradient in registers and writes it once: [block][2][D] in
-// gw_part, summed in order by k_rope_gw (the same result every time).
-template <typename T, int LPR, bool ILV, bool ALIGNED, bool NORM>
-__global__ void __launch_bounds__(kThreads) k_rope_bwd(const RopeParams p) {
-  constexpr int NW = Vec8<T>::kWords, GROUPS = kThreads / LPR;
-  extern __shared__ float2 s_cs[];
-  T* stage = reinterpret_cast<T*>(s_cs + ((p.nt * p.half + 1) & ~1)) + (threadIdx.x >> 5) * 256;
+// Value e's pair (-1: past the rotated ones) and its partner.
+template <int PAIRING>
+__device__ __forceinline__ int pair_of(int e, int half) {
+  if (e >= 2 * half) return -1;
+  if constexpr (PAIRING == kInterleaved) return e >> 1;
+  return e < half ? e : e - half;
+}
+template <int PAIRING>
+__device__ __forceinline__ int partner_of(int e, int half) {
+  if (e >= 2 * half) return e;
+  if constexpr (PAIRING == kInterleaved) return e ^ 1;
+  return e < half ? e + half : e - half;
+}
+
+// y_e = z_e ca_e + z_partner(e) sb_e turns by a token's angles: the partner's
+// sine has the sign of the second member's formula, and `back` turns back.  The
+// group's lanes work out the token's pairs between them, and each picks its own
+// from `table`, the warp's 128 pairs in shared memory.
+template <typename T, int LPR, int PAIRING>
+__device__ __forceinline__ void token_angles(const RopeParams& p, int64_t t, int gl, bool back, float2* table,
+                                             float (&ca)[8], float (&sb)[8]) {
+  float2* mine = table + (threadIdx.x & 31) / LPR * (LPR * 4);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int pair = gl + i * LPR;
+    if (pair < p.half) {
+      const int axis = (pair >= p.per) + (pair >= 2 * p.per) + (pair >= 3 * p.per);
+      mine[pair] = angle<sizeof(T) == 4>(__ldg(p.pos + t * p.pos_stride + axis), __ldg(p.freq + pair), p.amp);
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int e = gl * 8 + j, pair = pair_of<PAIRING>(e, p.half);
+    const float2 cs = pair >= 0 ? mine[pair] : make_float2(1.f, 0.f);
+    const bool first = PAIRING == kInterleaved ? (j & 1) == 0 : e < p.half;
+    ca[j] = cs.x;
+    sb[j] = first != back ? -cs.y : cs.y;
+  }
+}
+
+// A group's token and part of its heads; whole warps run the loops, for the
+// shuffles, and groups without a token do nothing in them.
+struct Unit {
+  int64_t token;
+  int chunk;
+  bool on;
+};
+template <int LPR>
+__device__ __forceinline__ Unit unit_of(const RopeParams& p, int64_t block) {
+  const int64_t u = block * (kThreads / LPR) + threadIdx.x / LPR;
+  Unit r;
+  r.token = u;
+  r.chunk = 0;
+  if (p.chunks > 1) {  // few tokens: the units fit 32 bits
+    r.token = static_cast<uint32_t>(u) / static_cast<uint32_t>(p.chunks);
+    r.chunk = static_cast<int>(static_cast<uint32_t>(u) % static_cast<uint32_t>(p.chunks));
+  }
+  r.on = r.token < p.tokens;
+  if (!r.on) r.token = 0;
+  return r;
+}
+
+constexpr int kRows = 4;  // rows in flight
+
+template <typename T, int LPR, int PAIRING, bool NORM>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_rope_fwd(const RopeParams p) {
+  constexpr int NW = Vec8<T>::kWords, U = sizeof(T) == 4 ? kRows / 2 : kRows;
+  __shared__ __align__(16) T s_stage[PAIRING >= kHalf2 ? kThreads * 8 : 8];
+  __shared__ float2 s_table[kThreads * 4];
+  T* stage = s_stage + (PAIRING >= kHalf2 ? (threadIdx.x >> 5) * 256 : 0);
+  const int gl = threadIdx.x % LPR;
+  const int e0 = gl * 8;
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  const Unit u = unit_of<LPR>(p, blockIdx.x);
+  const bool act = u.on && e0 < p.d;
+  float c[8], s[8];
+  token_angles<T, LPR, PAIRING>(p, u.token, gl, false, s_table + (threadIdx.x >> 5) * 128, c, s);
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const int n = p.per_chunk[side];
+    float a[8], b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      a[j] = c[j];
+      b[j] = s[j];
+      if constexpr (NORM) {
+        const int o = partner_of<PAIRING>(e0 + j, p.half);
+        a[j] *= n && e0 + j < p.d ? __ldg(p.w[side] + e0 + j) : 0.f;
+        b[j] *= n && o < p.d ? __ldg(p.w[side] + o) : 0.f;
+      }
+    }
+    const int h0 = u.chunk * n;
+    const int left = act ? min(n, p.heads[side] - h0) : 0;
+    const int64_t xh = p.xh[side], yh = p.yh[side];
+    const uint8_t* x = p.x[side] + u.token * p.xt[side] + e0 * sizeof(T) + h0 * xh;
+    uint8_t* y = p.y[side] + u.token * p.yt[side] + e0 * sizeof(T) + h0 * yh;
+    for (int i = 0; i < n; i += U, x += U * xh, y += U * yh) {
+      uint32_t w[U][NW];
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+#pragma unroll
+        for (int k = 0; k < NW; ++k) w[q][k] = 0u;
+        if (i + q < left) load_words<NW>(x + q * xh, w[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        float v[8], vp[8];
+        Vec8<T>::unpack(w[q], v);
+        partners<T, LPR, PAIRING>(w[q], vp, gl, p.half, stage);
+        float rn = 1.f;
+        if constexpr (NORM) {
+          float ss = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+          rn = rsqrtf(group_sum<LPR>(ss) * inv_d + p.eps);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[j] = fmaf(v[j], a[j], vp[j] * b[j]);
+          if constexpr (NORM) v[j] *= rn;
+        }
+        if (i + q < left) {
+          Vec8<T>::pack(v, w[q]);
+          store_words<NW>(y + q * yh, w[q]);
+        }
+      }
+    }
+  }
+}
+
+// The gradient.  The first blocks_q blocks walk q's units, the others k's, so
+// that each keeps its sum of one weight's gradient in registers and writes it
+// once: [block][D] in gw_part, summed in order by k_rope_gw (the same result
+// every time).
+template <typename T, int LPR, int PAIRING, bool NORM>
+__global__ void __launch_bounds__(kThreads, 3) k_rope_bwd(const RopeParams p) {
+  constexpr int NW = Vec8<T>::kWords, GROUPS = kThreads / LPR, U = sizeof(T) == 4 || NORM ? kRows / 2 : kRows;
+  __shared__ __align__(16) T s_stage[PAIRING >= kHalf2 ? kThreads * 8 : 8];
+  __shared__ float2 s_table[kThreads * 4];
+  T* stage = s_stage + (PAIRING >= kHalf2 ? (threadIdx.x >> 5) * 256 : 0);
   const int gl = threadIdx.x % LPR, grp = threadIdx.x / LPR;
   const int e0 = gl * 8;
-  const bool act = e0 < p.d;
-  float gw[2][8] = {};
-  float w[2][8];
+  const int side = static_cast<int>(blockIdx.x) >= p.blocks_q;
+  const int first = side ? p.blocks_q : 0, count = side ? gridDim.x - p.blocks_q : p.blocks_q;
+  const int n = side ? p.per_chunk[1] : p.per_chunk[0], heads = side ? p.heads[1] : p.heads[0];
+  const int64_t gh = side ? p.gh[1] : p.gh[0], xh = side ? p.xh[1] : p.xh[0], yh = side ? p.yh[1] : p.yh[0];
+  float gw[8] = {}, wt[8] = {};
   if constexpr (NORM) {
 #pragma unroll
-    for (int side = 0; side < 2; ++side)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[side][j] = p.heads[side] && e0 + j < p.d ? __ldg(p.w[side] + e0 + j) : 0.f;
+    for (int j = 0; j < 8; ++j) wt[j] = e0 + j < p.d ? __ldg((side ? p.w[1] : p.w[0]) + e0 + j) : 0.f;
   }
-  const int64_t steps = (p.tokens + p.nt - 1) / p.nt;
-  for (int64_t s = blockIdx.x; s < steps; s += gridDim.x) {
-    const int64_t t0 = s * p.nt;
-    const int nt = static_cast<int>(min(static_cast<int64_t>(p.nt), p.tokens - t0));
-    __syncthreads();  // the previous step's angles have been read
-    fill_angles(p, t0, s_cs);
-    __syncthreads();
+  const float inv_d = 1.f / static_cast<float>(p.d);
+  const int64_t blocks = (p.tokens * p.chunks + GROUPS - 1) / GROUPS;
+  for (int64_t blk = static_cast<int64_t>(blockIdx.x) - first; blk < blocks; blk += count) {
+    const Unit u = unit_of<LPR>(p, blk);
+    const bool act = u.on && e0 < p.d;
+    float c[8], s[8];
+    token_angles<T, LPR, PAIRING>(p, u.token, gl, true, s_table + (threadIdx.x >> 5) * 128, c, s);
+    const int h0 = u.chunk * n, left = act ? min(n, heads - h0) : 0;
+    const uint8_t* gy = (side ? p.gy[1] : p.gy[0]) + u.token * (side ? p.gt[1] : p.gt[0]) + e0 * sizeof(T) + h0 * gh;
+    const uint8_t* x = (side ? p.x[1] : p.x[0]) + u.token * (side ? p.xt[1] : p.xt[0]) + e0 * sizeof(T) + h0 * xh;
+    uint8_t* y = (side ? p.y[1] : p.y[0]) + u.token * (side ? p.yt[1] : p.yt[0]) + e0 * sizeof(T) + h0 * yh;
+    for (int i = 0; i < n; i += U, gy += U * gh, x += U * xh, y += U * yh) {
+      uint32_t wg[U][NW], wx[U][NW];
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const int heads = p.heads[side];
-      if (heads == 0) continue;
-      const int rows = nt * heads;
-      for (int r0 = 0; r0 < rows; r0 += GROUPS) {
-        const int r = r0 + grp;
-        const bool on = r < rows && act;
-        const int t = on ? r / heads : 0, h = on ? r - t * heads : 0;
-        uint32_t a[NW] = {}, b[NW] = {};
-        if (on) {
-          load_words<NW>(p.gy[side] + (t0 + t) * p.gt[side] + h * p.gh[side] + e0 * sizeof(T), a);
-          if constexpr (NORM) load_words<NW>(p.x[side] + (t0 + t) * p.xt[side] + h * p.xh[side] + e0 * sizeof(T), b);
+      for (int q = 0; q < U; ++q) {
+#pragma unroll
+        for (int k = 0; k < NW; ++k) wg[q][k] = wx[q][k] = 0u;
+        if (i + q < left) {
+          load_words<NW>(gy + q * gh, wg[q]);
+          if constexpr (NORM) load_words<NW>(x + q * xh, wx[q]);
         }
-        float gy[8], gp[8] = {}, g[8];
-        Vec8<T>::unpack(a, gy);
-        if constexpr (!ILV) partner_half<T, LPR, ALIGNED>(a, gp, gl, p.half, stage);
-        turn<ILV>(g, gy, gp, s_cs + t * p.half, e0, p.half, -1.f);
+      }
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const bool on = i + q < left;
+        float g[8], gp[8];
+        Vec8<T>::unpack(wg[q], g);
+        partners<T, LPR, PAIRING>(wg[q], gp, gl, p.half, stage);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = fmaf(g[j], c[j], gp[j] * s[j]);
         if constexpr (NORM) {
-          float x[8];
-          Vec8<T>::unpack(b, x);
-          float ss = 0.f, hx = 0.f;
+          float v[8], ss = 0.f, hx = 0.f;
+          Vec8<T>::unpack(wx[q], v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            ss = fmaf(x[j], x[j], ss);
-            hx = fmaf(g[j] * w[side][j], x[j], hx);
+            ss = fmaf(v[j], v[j], ss);
+            hx = fmaf(g[j] * wt[j], v[j], hx);
           }
-          const float inv_d = 1.f / static_cast<float>(p.d);
-          const float rn = 1.f / sqrtf(group_sum<LPR>(ss) * inv_d + p.eps);
+          const float rn = rsqrtf(group_sum<LPR>(ss) * inv_d + p.eps);
           const float m = group_sum<LPR>(hx) * rn * inv_d;  // mean(h x r)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float xn = x[j] * rn;
-            // rows past the end hold zeros, and the masked add keeps NaN weights of idle lanes out
-            if (on) gw[side][j] = fmaf(g[j], xn, gw[side][j]);
-            g[j] = rn * (g[j] * w[side][j] - xn * m);
+            const float xn = v[j] * rn;
+            if (on) gw[j] = fmaf(g[j], xn, gw[j]);
+            g[j] = rn * (g[j] * wt[j] - xn * m);
           }
         }
         if (on) {
-          Vec8<T>::pack(g, a);
-          store_words<NW>(p.y[side] + (t0 + t) * p.yt[side] + h * p.yh[side] + e0 * sizeof(T), a);
+          Vec8<T>::pack(g, wg[q]);
+          store_words<NW>(y + q * yh, wg[q]);
         }
       }
     }
   }
   if constexpr (NORM) {
-    // groups' sums in order, one side at a time
-    float* s_gw = reinterpret_cast<float*>(s_cs);  // [GROUPS][LPR * 8], sized by the launch
+    // the groups' sums in order, in the table's place
+    float* s_gw = reinterpret_cast<float*>(s_table);  // [GROUPS][LPR * 8]
+    __syncthreads();
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s_gw[grp * (LPR * 8) + e0 + j] = gw[side][j];
-      __syncthreads();
-      for (int c = threadIdx.x; c < p.d; c += kThreads) {
-        float v = 0.f;
-        for (int g = 0; g < GROUPS; ++g) v += s_gw[g * (LPR * 8) + c];
-        p.gw_part[(static_cast<int64_t>(blockIdx.x) * 2 + side) * p.d + c] = v;
-      }
+    for (int j = 0; j < 8; ++j) s_gw[grp * (LPR * 8) + e0 + j] = gw[j];
+    __syncthreads();
+    for (int col = threadIdx.x; col < p.d; col += kThreads) {
+      float v = 0.f;
+      for (int g = 0; g < GROUPS; ++g) v += s_gw[g * (LPR * 8) + col];
+      p.gw_part[static_cast<int64_t>(blockIdx.x) * p.d + col] = v;
     }
   }
 }
 
-// gw[side][c] = sum over blocks of part[block][side][c], each column by one
-// warp: lanes take blocks in strides, then a fixed tree.
-__global__ void __launch_bounds__(kThreads) k_rope_gw(const float* __restrict__ part, int blocks, int d, float* gwq,
-                                                      float* gwk) {
+// gw[c] = sum over its side's blocks of part[block][c], each column by one warp:
+// lanes take blocks in strides, then a fixed tree.
+__global__ void __launch_bounds__(kThreads) k_rope_gw(const float* __restrict__ part, int blocks_q, int blocks, int d,
+                                                      float* gwq, float* gwk) {
   const int col = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (col >= 2 * d) return;
+  const bool k = col >= d;
+  const int c = k ? col - d : col;
   float v = 0.f;
-  for (int b = lane; b < blocks; b += 32) v += __ldg(part + static_cast<int64_t>(b) * 2 * d + col);
+  for (int b = (k ? blocks_q : 0) + lane; b < (k ? blocks : blocks_q); b += 32)
+    v += __ldg(part + static_cast<int64_t>(b) * d + c);
   v = group_sum<32>(v);
-  float* dst = col < d ? gwq : gwk;
-  if (lane == 0 && dst) dst[col < d ? col : col - d] = v;
+  float* dst = k ? gwk : gwq;
+  if (lane == 0 && dst) dst[c] = v;
 }
 
 using Kern = void (*)(RopeParams);
 
-template <typename T, int LPR, bool ILV, bool ALIGNED>
+template <typename T, int LPR, int PAIRING>
 Kern pick_norm(bool bwd, bool norm) {
-  if (bwd) return norm ? k_rope_bwd<T, LPR, ILV, ALIGNED, true> : k_rope_bwd<T, LPR, ILV, ALIGNED, false>;
-  return norm ? k_rope_fwd<T, LPR, ILV, ALIGNED, true> : k_rope_fwd<T, LPR, ILV, ALIGNED, false>;
+  if (bwd) return norm ? k_rope_bwd<T, LPR, PAIRING, true> : k_rope_bwd<T, LPR, PAIRING, false>;
+  return norm ? k_rope_fwd<T, LPR, PAIRING, true> : k_rope_fwd<T, LPR, PAIRING, false>;
 }
 template <typename T, int LPR>
-Kern pick_layout(bool bwd, bool norm, bool ilv, bool aligned) {
-  if (ilv) return pick_norm<T, LPR, true, true>(bwd, norm);
-  return aligned ? pick_norm<T, LPR, false, true>(bwd, norm) : pick_norm<T, LPR, false, false>(bwd, norm);
+Kern pick_pairing(bool bwd, bool norm, int pairing) {
+  switch (pairing) {
+    case kInterleaved: return pick_norm<T, LPR, kInterleaved>(bwd, norm);
+    case kHalf8: return pick_norm<T, LPR, kHalf8>(bwd, norm);
+    case kHalf2:
+      if constexpr (sizeof(T) == 2) return pick_norm<T, LPR, kHalf2>(bwd, norm);  // f32: one at a time
+    default: return pick_norm<T, LPR, kHalf1>(bwd, norm);
+  }
 }
 template <typename T>
-Kern pick(int lpr, bool bwd, bool norm, bool ilv, bool aligned) {
+Kern pick(int lpr, bool bwd, bool norm, int pairing) {
   switch (lpr) {
-    case 2: return pick_layout<T, 2>(bwd, norm, ilv, aligned);
-    case 4: return pick_layout<T, 4>(bwd, norm, ilv, aligned);
-    case 8: return pick_layout<T, 8>(bwd, norm, ilv, aligned);
-    case 16: return pick_layout<T, 16>(bwd, norm, ilv, aligned);
-    default: return pick_layout<T, 32>(bwd, norm, ilv, aligned);
+    case 4: return pick_pairing<T, 4>(bwd, norm, pairing);
+    case 8: return pick_pairing<T, 8>(bwd, norm, pairing);
+    case 16: return pick_pairing<T, 16>(bwd, norm, pairing);
+    default: return pick_pairing<T, 32>(bwd, norm, pairing);
   }
 }
 
 int lanes_per_row(int d) {
-  int l = 2;
+  int l = 4;
   while (l * 8 < d) l *= 2;
   return l;
 }
@@ -437,43 +519,45 @@ sc_status rope_run(const RopeArgs& a) {
   p.amp = a.amp;
   const int lpr = lanes_per_row(p.d), groups = kThreads / lpr;
   const int sms = device_sm_count();
-  // tokens of a step: enough rows for four passes of the block's groups, but
-  // first enough blocks for the card (a few tokens: one block each)
-  int64_t nt = (4 * groups + heads - 1) / heads;
-  const int64_t most = a.tokens / (4 * sms);
-  if (nt > most) nt = most;
-  if (nt < 1) nt = 1;
-  while (nt > 1 && nt * p.half * 8 > 16384) --nt;
-  p.nt = static_cast<int>(nt);
-  const bool aligned = p.half % 8 == 0;
-  size_t smem = static_cast<size_t>(p.nt) * p.half * sizeof(float2);
-  smem = (smem + 15) & ~size_t(15);
-  if (!a.interleaved && !aligned) smem += kThreads / 32 * 256 * static_cast<size_t>(eb);
-  if (bwd && norm && smem < static_cast<size_t>(groups) * lpr * 8 * 4) smem = static_cast<size_t>(groups) * lpr * 8 * 4;
-  const int64_t steps = (a.tokens + nt - 1) / nt;
-  Kern k = a.dtype == SC_F32   ? pick<float>(lpr, bwd, norm, a.interleaved, aligned)
-           : a.dtype == SC_F16 ? pick<__half>(lpr, bwd, norm, a.interleaved, aligned)
-                               : pick<__nv_bfloat16>(lpr, bwd, norm, a.interleaved, aligned);
+  // A token's heads go to as many groups as fill the card (2048 threads an SM).
+  const int most = a.heads_q > a.heads_k ? a.heads_q : a.heads_k;
+  int64_t chunks = 2048ll * sms / (a.tokens * lpr);
+  p.chunks = static_cast<int>(chunks < 1 ? 1 : chunks > most ? most : chunks);
+  p.per_chunk[0] = (a.heads_q + p.chunks - 1) / p.chunks;
+  p.per_chunk[1] = (a.heads_k + p.chunks - 1) / p.chunks;
+  const int64_t steps = (a.tokens * p.chunks + groups - 1) / groups;
+  const int pairing = a.interleaved ? kInterleaved : p.half % 8 == 0 ? kHalf8 : p.half % 2 == 0 ? kHalf2 : kHalf1;
+  Kern k = a.dtype == SC_F32   ? pick<float>(lpr, bwd, norm, pairing)
+           : a.dtype == SC_F16 ? pick<__half>(lpr, bwd, norm, pairing)
+                               : pick<__nv_bfloat16>(lpr, bwd, norm, pairing);
   if (steps > 0x7fffffff) return set_error(SC_ERR_UNSUPPORTED, "too many tokens");
   if (!bwd) {
-    SC_LAUNCH("qk_norm_rope_fwd", a.stream, (k<<<static_cast<unsigned>(steps), kThreads, smem, a.stream>>>(p)));
+    SC_LAUNCH("qk_norm_rope_fwd", a.stream, (k<<<static_cast<unsigned>(steps), kThreads, 0, a.stream>>>(p)));
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SC_OK : set_cuda_error(e, "qk_norm_rope_fwd");
   }
-  const int64_t cap = 6ll * sms;
-  const int blocks = static_cast<int>(steps < cap ? steps : cap);
+  // blocks by the sides' heads, one at least for each that has some
+  const int64_t cap = 3ll * sms;
+  int64_t nb[2] = {0, 0};
+  for (int s = 0; s < 2; ++s)
+    if (p.heads[s]) {
+      nb[s] = (cap * p.heads[s] + heads / 2) / heads;
+      nb[s] = nb[s] < 1 ? 1 : nb[s] > steps ? steps : nb[s];
+    }
+  p.blocks_q = static_cast<int>(nb[0]);
+  const int blocks = static_cast<int>(nb[0] + nb[1]);
   void* part = nullptr;
   if (norm) {
-    const sc_status st = dev_alloc(&part, sizeof(float) * 2 * p.d * static_cast<size_t>(blocks), a.stream);
+    const sc_status st = dev_alloc(&part, sizeof(float) * p.d * static_cast<size_t>(blocks), a.stream);
     if (st) return st;
     p.gw_part = static_cast<float*>(part);
   }
-  SC_LAUNCH("qk_norm_rope_bwd", a.stream, (k<<<blocks, kThreads, smem, a.stream>>>(p)));
+  SC_LAUNCH("qk_norm_rope_bwd", a.stream, (k<<<blocks, kThreads, 0, a.stream>>>(p)));
   cudaError_t e = cudaGetLastError();
   if (norm && e == cudaSuccess) {
     const int grid = (2 * p.d * 32 + kThreads - 1) / kThreads;
     SC_LAUNCH("qk_norm_rope_gw", a.stream,
-              (k_rope_gw<<<grid, kThreads, 0, a.stream>>>(p.gw_part, blocks, p.d, a.gw[0], a.gw[1])));
+              (k_rope_gw<<<grid, kThreads, 0, a.stream>>>(p.gw_part, p.blocks_q, blocks, p.d, a.gw[0], a.gw[1])));
     e = cudaGetLastError();
   }
   dev_free(part, a.stream);
