@@ -123,8 +123,10 @@ def _check(st: int, what: str):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # the current stream's handle, without a Stream object around it
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _dev(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -459,44 +461,48 @@ def _heads(t, name: str, like=None, shape=None):
     dimension is contiguous (the other strides are free)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3:
+    stride = t.stride()
+    if len(stride) != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must have the dtype and device of the other rows")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    ts, hs, ds = t.stride()
-    if ds != 1 and t.shape[2] > 1:
+    if stride[2] != 1 and t.shape[2] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return _Heads(t.data_ptr(), ts, hs)
+    return _Heads(t.data_ptr(), stride[0], stride[1])
 
 
-def _f32(t, name: str, n: int, device):
+def _f32(t, name: str, n: int, device: int):
     if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.float32 or t.shape != (n,):
-        raise ValueError(f"{name} must be a float32 [{n}] tensor on {device}")
-    return _dev(t, name)
+        return
+    if (not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not torch.float32
+            or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 [{n}] tensor on the rows' device")
 
 
 def _rope_args(first, pos, freq, wq, wk, heads_q, heads_k):
     tokens, _, d = first.shape
     if first.dtype not in _DTYPES:
         raise ValueError("rows must be float32, float16 or bfloat16")
+    device = first.get_device()
     rot, axes, stride = 0, 1, 0
     if freq is not None:
-        rot = 2 * freq.shape[0]
-        _f32(freq, "freq", rot // 2, first.device)
-        if (not isinstance(pos, torch.Tensor) or pos.device != first.device or pos.dtype != torch.int32
-                or pos.dim() not in (1, 2) or pos.shape[0] != tokens):
-            raise ValueError("pos must be int32 [tokens] or [tokens, axes] on the rows' device")
-        stride = pos.stride(0)
-        if pos.dim() == 2:
+        half = freq.shape[0]
+        rot = 2 * half
+        _f32(freq, "freq", half, device)
+        if not isinstance(pos, torch.Tensor) or pos.get_device() != device or pos.dtype is not torch.int32:
+            raise ValueError("pos must be int32 on the rows' device")
+        st = pos.stride()
+        if len(st) not in (1, 2) or pos.shape[0] != tokens:
+            raise ValueError("pos must be [tokens] or [tokens, axes]")
+        stride = st[0]
+        if len(st) == 2:
             axes = pos.shape[1]
-            if axes > 1 and pos.stride(1) != 1:
+            if axes > 1 and st[1] != 1:
                 raise ValueError("pos: the axes must be contiguous")
-    _f32(wq, "wq", d, first.device)
-    _f32(wk, "wk", d, first.device)
+    _f32(wq, "wq", d, device)
+    _f32(wk, "wk", d, device)
     if (wq is None) != (wk is None) and heads_q and heads_k:
         raise ValueError("pass both norm weights, or neither")
     return tokens, d, rot, axes, stride
@@ -600,11 +606,11 @@ def rope_frequencies(rot_dim: int, axes: int = 1, base: float = 10000.0, scaling
     return freq.float().repeat(axes).to(device), amp
 
 
-def _offsets(off, name: str, device):
-    if (not isinstance(off, torch.Tensor) or off.device != device or off.dtype != torch.int32 or off.dim() != 1
-            or off.shape[0] < 1):
-        raise ValueError(f"{name} must be an int32 vector on the rows' device")
-    return _dev(off, name)
+def _offsets(off, name: str, device: int) -> int:
+    if (not isinstance(off, torch.Tensor) or off.get_device() != device or off.dtype is not torch.int32
+            or off.dim() != 1 or not off.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 vector on the rows' device")
+    return off.shape[0]
 
 
 def _attn_common(q, k, v, q_off, k_off, scale):
@@ -613,10 +619,13 @@ def _attn_common(q, k, v, q_off, k_off, scale):
     hv = _heads(v, "v", q, k.shape)
     if k.shape[2] != q.shape[2]:
         raise ValueError("q, k and v must have one head_dim")
-    _offsets(q_off, "q_off", q.device)
+    device = q.get_device()
+    n = _offsets(q_off, "q_off", device) - 1
+    if n < 0:
+        raise ValueError("q_off must hold one more offset than there are sequences")
     if k_off is None:
         k_off = q_off
-    elif _offsets(k_off, "k_off", q.device).shape != q_off.shape:
+    elif _offsets(k_off, "k_off", device) != n + 1:
         raise ValueError("k_off must have q_off's length")
     if q.dtype not in _DTYPES:
         raise ValueError("rows must be float16 or bfloat16")
@@ -633,7 +642,7 @@ def sc_attn_fwd(q, k, v, q_off, k_off=None, k_len=None, causal: bool = False, sc
     scale: default head_dim^-0.5.  return_lse: (out, lse float32 [t_q, heads_q])."""
     hq, hk, hv, k_off, scale = _attn_common(q, k, v, q_off, k_off, scale)
     n = q_off.shape[0] - 1
-    if k_len is not None and _offsets(k_len, "k_len", q.device).shape[0] != n:
+    if k_len is not None and _offsets(k_len, "k_len", q.get_device()) != n:
         raise ValueError("k_len must hold one length a sequence")
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)

@@ -196,6 +196,20 @@ sc_status kernel_carveout(const void* kern, int ctas_per_sm, size_t smem) {
   return SC_OK;
 }
 
+cudaError_t launch_after(const void* kern, unsigned grid, unsigned block, size_t smem, cudaStream_t s, void** args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
 // The device's default stream-ordered pool keeps freed blocks for reuse
 // (release threshold = unlimited) instead of trimming them at every
 // synchronisation; set once per device on first use.

@@ -48,12 +48,14 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
 // The keys of a unit are cut where the card would otherwise wait for it: with
 // fewer than two units an SM into about four parts an SM, else only units dearer
 // than an SM's share.  A part costs its fp32 rows written and read once more.
-__global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs p) {
+__global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs pa, const PlanArgs pb) {
+  const PlanArgs& p = blockIdx.x ? pb : pa;
   __shared__ int s_q[kPlanThreads + 1], s_k0[kPlanThreads], s_k1[kPlanThreads], s_pre[kPlanThreads + 1];
   __shared__ int s_hist[kBuckets], s_warp[32];
   __shared__ int s_bad, s_max, s_items, s_joins, s_parts, s_rows;
   __shared__ unsigned long long s_steps;
   const int tid = threadIdx.x;
+  grid_release();
   if (tid == 0) {
     s_bad = 0;
     s_max = 1;
@@ -72,6 +74,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs p) {
   for (int pass = 0; pass < 3; ++pass) {
     for (int c0 = 0; c0 < p.n_seq; c0 += kPlanThreads) {
       const int cnt = min(kPlanThreads, p.n_seq - c0);
+      int total = s_pre[cnt];  // one run: it stays from the first pass
+      if (pass == 0 || p.n_seq > kPlanThreads) {
       __syncthreads();
       int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
       if (tid < cnt) {
@@ -101,13 +105,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs p) {
       if (tid < cnt)
         tiles = p.mode == kPlanRows ? (q1 - q0 + p.pos_per_item - 1) / p.pos_per_item
                                     : (k1 - k0 + kKeyTile - 1) / kKeyTile;
-      int total;
       s_pre[tid] = block_scan(tiles, s_warp, &total);
       if (tid == 0) {
         s_pre[cnt] = total;  // cnt == kPlanThreads: its own place
         if (pass == 0) s_items += total;
       }
       __syncthreads();
+      }
       for (int u = tid; u < total; u += kPlanThreads) {
         int lo = 0, hi = cnt - 1;  // the sequence with s_pre[lo] <= u < s_pre[lo + 1]
         while (lo < hi) {
@@ -228,6 +232,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs p) {
     p.header[2] = s_bad ? 0 : min(s_joins, p.join_cap);
     p.header[3] = s_rows;
   }
+  grid_wait();  // the kernel before this one is done when this one is
 }
 
 }  // namespace
@@ -237,9 +242,15 @@ int* attn_status_word() {
   return cudaGetSymbolAddress(&p, g_attn_status) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
-sc_status attn_plan(const PlanArgs& a, cudaStream_t s) {
-  SC_LAUNCH("attn_plan", s, (k_attn_plan<<<1, kPlanThreads, 0, s>>>(a)));
-  const cudaError_t e = cudaGetLastError();
+sc_status attn_plan(const PlanArgs& a, const PlanArgs* b, bool after, cudaStream_t s) {
+  PlanArgs x = a, y = b ? *b : a;
+  void* args[] = {&x, &y};
+  const void* kern = reinterpret_cast<const void*>(k_attn_plan);
+  const unsigned grid = b ? 2 : 1;
+  cudaError_t e;
+  SC_LAUNCH("attn_plan", s,
+            (e = after ? launch_after(kern, grid, kPlanThreads, 0, s, args)
+                       : cudaLaunchKernel(kern, dim3(grid), dim3(kPlanThreads), args, 0, s)));
   return e == cudaSuccess ? SC_OK : set_cuda_error(e, "attn_plan");
 }
 

@@ -45,6 +45,7 @@ struct BwdParams {
   int heads_q, heads_kv, g, pos, d;
   float scale, scale_log2;
   int causal;
+  int first;             // gq: no gk, gv kernel ran before it
   int* status;
 };
 
@@ -102,6 +103,7 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b) {
 // delta = gout . out and lse in powers of two, LPR lanes a row.
 template <bool BF16, int LPR>
 __global__ void __launch_bounds__(256) k_attn_stat(const StatParams p) {
+  grid_release();
   const int64_t r = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / LPR;
   const int gl = threadIdx.x % LPR;
   float s = 0.f;
@@ -193,9 +195,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_wait();     // the plan and the statistics
+  grid_release();  // gq's kernel needs no more than these either
   const uint32_t tmem = sm->tmem;
   const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
-  const int units = p.header[0] * p.heads_kv;
+  const int units = __ldcg(p.header) * p.heads_kv;
 
   if (warp == 8) {
     // =========================================================== loads
@@ -359,7 +363,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           st[u] = make_float2(INFINITY, 0.f);
           if (r < live) {
             const int64_t t = static_cast<int64_t>(it.q_row) + i * p.pos + r / p.g;
-            st[u] = __ldg(p.stat + t * p.heads_q + head * p.g + r % p.g);
+            st[u] = __ldcg(p.stat + t * p.heads_q + head * p.g + r % p.g);
           }
         }
         ok = mbar_wait_inl(smem_u32(&sm->rows_free[sl]), ((nr >> 1) & 1) ^ 1, abort_flag);
@@ -559,9 +563,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.first) grid_wait();  // the plan and the statistics; else gk's kernel has waited for them
   const uint32_t tmem = sm->tmem;
   const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;
-  const int units = p.header[0] * p.heads_kv;
+  const int units = __ldcg(p.header) * p.heads_kv;
 
   if (warp == 8) {
     // =========================================================== loads
@@ -744,7 +749,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int h = head * p.g + gh;
       const int vis = p.causal ? min(it.lk, it.lim0 + pos + 1) : it.lk;
       float2 st = make_float2(INFINITY, 0.f);
-      if (live) st = __ldg(p.stat + tok * p.heads_q + h);
+      if (live) st = __ldcg(p.stat + tok * p.heads_q + h);
       const uint64_t nl = pair2(-st.x, -st.x), ndl = pair2(-st.y, -st.y);
       bool ok = true;
       for (int j = 0; j < n; ++j, ++nd) {
@@ -816,6 +821,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  grid_wait();  // done only when gk's kernel is
   if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, kDevErrTimeout);
 }
 
@@ -903,8 +909,6 @@ sc_status attn_bwd(const AttnArgs& a) {
   plk.cap = static_cast<int>(k_items);
   plk.header = reinterpret_cast<int*>(base + o_hk);
   plk.items = reinterpret_cast<AttnItem*>(base + o_ik);
-  st = attn_plan(plk, a.stream);
-  if (!st) st = attn_plan(plq, a.stream);
   cudaError_t e = cudaSuccess;
   BwdParams p{};
   p.stat = reinterpret_cast<const float2*>(base + o_st);
@@ -934,6 +938,7 @@ sc_status attn_bwd(const AttnArgs& a) {
     e = cudaGetLastError();
     if (e != cudaSuccess) st = set_cuda_error(e, "attn_stat");
   }
+  if (!st) st = attn_plan(plk, &plq, have_q, a.stream);
   if (!st && have_k) {
     BwdParams pk = p;
     pk.header = plk.header;
@@ -948,8 +953,8 @@ sc_status attn_bwd(const AttnArgs& a) {
     const int64_t most = k_items * a.heads_kv;
     void* args[] = {&pk, &qm, &gm, &km, &vm};
     SC_LAUNCH("attn_bwd_kv", a.stream,
-              (e = cudaLaunchKernel(kk, dim3(static_cast<unsigned>(most < sms ? most : sms)), dim3(kBwdThreads), args,
-                                    kv_smem, a.stream)));
+              (e = launch_after(kk, static_cast<unsigned>(most < sms ? most : sms), kBwdThreads, kv_smem, a.stream,
+                                args)));
     if (e != cudaSuccess) st = set_cuda_error(e, "attn_bwd_kv");
   }
   if (!st && have_q) {
@@ -960,11 +965,12 @@ sc_status attn_bwd(const AttnArgs& a) {
     pq.o0 = static_cast<uint8_t*>(a.gq.data);
     pq.o0_t = a.gq.token_stride * 2;
     pq.o0_h = a.gq.head_stride * 2;
+    pq.first = !have_k;
     const int64_t most = q_items * a.heads_kv;
     void* args[] = {&pq, &qm, &gm, &km, &vm};
     SC_LAUNCH("attn_bwd_q", a.stream,
-              (e = cudaLaunchKernel(kq, dim3(static_cast<unsigned>(most < sms ? most : sms)), dim3(kBwdThreads), args,
-                                    q_smem, a.stream)));
+              (e = launch_after(kq, static_cast<unsigned>(most < sms ? most : sms), kBwdThreads, q_smem, a.stream,
+                                args)));
     if (e != cudaSuccess) st = set_cuda_error(e, "attn_bwd_q");
   }
   dev_free(ws, a.stream);

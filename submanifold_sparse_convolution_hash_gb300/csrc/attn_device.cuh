@@ -130,9 +130,9 @@ __device__ __forceinline__ void hand_out(ItemSlots* sl, int* counter, const Attn
     if (u < units) {
       const uint4* src = reinterpret_cast<const uint4*>(items + u / heads);
       uint4* dst = reinterpret_cast<uint4*>(&sl->item[slot]);
-      dst[0] = src[0];
-      dst[1] = src[1];
-      dst[2] = src[2];
+      dst[0] = __ldcg(src);
+      dst[1] = __ldcg(src + 1);
+      dst[2] = __ldcg(src + 2);
     }
     sl->head[slot] = u < units ? u % heads : -1;
     mbar_arrive(smem_u32(&sl->full[slot]));

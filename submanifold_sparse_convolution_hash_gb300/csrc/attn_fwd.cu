@@ -105,9 +105,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_wait();  // the plan
+  grid_release();
   const uint32_t tmem = sm->tmem;
   // TMEM: S (and P over it) of the two row tiles, then their O, 128 columns each
-  const int n_items = p.header[0];
+  const int n_items = __ldcg(p.header);
   const int units = n_items * p.heads_kv;
 
   if (warp == 8) {
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       } else {
         // a part of the keys: O, m and l in fp32 for k_attn_join
         const int part = it.slot + (dual ? 2 * it.split + s : it.split);
-        float* dst = p.part + ((static_cast<int64_t>(part) * p.heads_kv + head) * p.header[3] + i * p.g + gh) * (p.d + 8);
+        float* dst = p.part + ((static_cast<int64_t>(part) * p.heads_kv + head) * __ldcg(p.header + 3) + i * p.g + gh) * (p.d + 8);
         if (live) {
           dst[p.d] = have ? m : -INFINITY;
           dst[p.d + 1] = l;
@@ -537,7 +539,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // f_q = exp(scale (m_q - m)).  The parts are taken in order, whoever made them.
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const AttnItem* joins) {
-  const int n = p.header[2], stride = p.header[3];
+  grid_wait();
+  const int n = __ldcg(p.header + 2), stride = __ldcg(p.header + 3);
   const int lane = threadIdx.x & 31;
   const int64_t step = static_cast<int64_t>(p.heads_kv) * stride * (p.d + 8);  // one part to the next
   const int64_t total = static_cast<int64_t>(n) * p.heads_kv * stride;
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Attn
     const int parts = it->nsplit * (it->dual ? 2 : 1);
     const float* src = p.part + ((static_cast<int64_t>(it->slot) * p.heads_kv + head) * stride + r) * (p.d + 8);
     float m = -INFINITY;
-    for (int q = lane; q < parts; q += 32) m = fmaxf(m, __ldg(src + q * step + p.d));
+    for (int q = lane; q < parts; q += 32) m = fmaxf(m, __ldcg(src + q * step + p.d));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float base = m == -INFINITY ? 0.f : m;
@@ -561,11 +564,11 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Attn
     const bool on = lane * 4 < p.d;
 #pragma unroll 4
     for (int q = 0; q < parts; ++q) {
-      const float mq = __ldg(src + q * step + p.d);
+      const float mq = __ldcg(src + q * step + p.d);
       const float f = ex2((mq - base) * p.scale_log2);
-      l += __ldg(src + q * step + p.d + 1) * f;
+      l += __ldcg(src + q * step + p.d + 1) * f;
       // nothing seen in this part: no O was written
-      const float4 o = on && mq != -INFINITY ? __ldg(reinterpret_cast<const float4*>(src + q * step) + lane)
+      const float4 o = on && mq != -INFINITY ? __ldcg(reinterpret_cast<const float4*>(src + q * step) + lane)
                                              : make_float4(0.f, 0.f, 0.f, 0.f);
       a.x = fmaf(o.x, f, a.x);
       a.y = fmaf(o.y, f, a.y);
@@ -599,11 +602,12 @@ sc_status attn_fwd(const AttnArgs& a) {
   // Partial results: room for about four parts an SM and two an item, where an
   // item has few rows (a guess from the average; the plan sees whether they
   // fit) or the items are few.
+  // no list over 128 keys: nothing to cut, and the join is not launched
   const int64_t avg = a.n_seq ? (a.t_q * g + a.n_seq - 1) / a.n_seq : 0;
   const bool few = items_ub * a.heads_kv <= 8ll * sms;
   const int64_t rows_guess = few ? 2 * pos * g : 2 * avg;
   const int64_t slots = 8ll * sms / a.heads_kv + 2 + 2 * items_ub;
-  int64_t part_rows = few || avg <= 32 ? slots * a.heads_kv * (rows_guess < 2 * pos * g ? rows_guess : 2 * pos * g) : 0;
+  int64_t part_rows = a.t_k > kKeyTile && (few || avg <= 32) ? slots * a.heads_kv * (rows_guess < 2 * pos * g ? rows_guess : 2 * pos * g) : 0;
   const int64_t row_bytes = (a.head_dim + 8) * 4ll;
   if (part_rows * row_bytes > (int64_t(1) << 28)) part_rows = (int64_t(1) << 28) / row_bytes;
   const int64_t cap = items_ub + (part_rows ? slots : 0);
@@ -658,7 +662,7 @@ sc_status attn_fwd(const AttnArgs& a) {
   pl.items = reinterpret_cast<AttnItem*>(base + o_items);
   pl.joins = reinterpret_cast<AttnItem*>(base + o_joins);
   pl.status = status;
-  st = attn_plan(pl, a.stream);
+  st = attn_plan(pl, nullptr, false, a.stream);
   if (!st) {
     p.out = static_cast<uint8_t*>(a.out.data);
     p.out_t = a.out.token_stride * 2;
@@ -682,15 +686,16 @@ sc_status attn_fwd(const AttnArgs& a) {
     void* args[] = {&p, &qm, &km, &vm};
     cudaError_t e;
     SC_LAUNCH("attn_fwd", a.stream,
-              (e = cudaLaunchKernel(kern, dim3(grid), dim3(kFwdThreads), args, smem, a.stream)));
+              (e = launch_after(kern, grid, kFwdThreads, smem, a.stream, args)));
     if (e != cudaSuccess) st = set_cuda_error(e, "attn_fwd");
     if (!st && part_rows) {
       const int64_t warps = a.t_q * a.heads_q;
       const unsigned nb = static_cast<unsigned>(warps < 32ll * sms ? (warps + 7) / 8 : 4 * sms);
-      SC_LAUNCH("attn_join", a.stream,
-                (a.dtype == SC_BF16 ? k_attn_join<true><<<nb, 256, 0, a.stream>>>(p, pl.joins)
-                                    : k_attn_join<false><<<nb, 256, 0, a.stream>>>(p, pl.joins)));
-      e = cudaGetLastError();
+      const AttnItem* joins = pl.joins;
+      void* jargs[] = {&p, &joins};
+      const void* jk = a.dtype == SC_BF16 ? reinterpret_cast<const void*>(k_attn_join<true>)
+                                          : reinterpret_cast<const void*>(k_attn_join<false>);
+      SC_LAUNCH("attn_join", a.stream, (e = launch_after(jk, nb, 256, 0, a.stream, jargs)));
       if (e != cudaSuccess) st = set_cuda_error(e, "attn_join");
     }
   }

@@ -55,7 +55,9 @@ struct PlanArgs {
   AttnItem* joins;    // per item that has parts: where its rows and parts are
   int* status;
 };
-sc_status attn_plan(const PlanArgs& a, cudaStream_t s);
+// Two plans in one launch where b is given; `after`: it may overlap the kernel
+// before it, which it then outlasts.
+sc_status attn_plan(const PlanArgs& a, const PlanArgs* b, bool after, cudaStream_t s);
 int* attn_status_word();
 
 // Workspace pieces, 256-byte aligned.

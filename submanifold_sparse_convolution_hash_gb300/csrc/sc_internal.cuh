@@ -155,6 +155,18 @@ sc_status kernel_setup(const void* kern, size_t smem, int* num_regs);
 // holds the neighbour-index loads); cached, so set only when it changes.
 sc_status kernel_carveout(const void* kern, int ctas_per_sm, size_t smem);
 
+// Launches a kernel that may begin while the one before it on the stream still
+// runs (programmatic dependent launch): it calls grid_wait() before it touches
+// what that one writes, and again grid_wait() before it ends if it did not.
+cudaError_t launch_after(const void* kern, unsigned grid, unsigned block, size_t smem, cudaStream_t s, void** args);
+
+#ifdef __CUDACC__
+// Waits until the kernels before this one on the stream are done and their
+// writes visible; lets the next one begin.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
+
 // kernels: hash + map (hash_kmap.cu)
 sc_status launch_hash_insert(const int32_t* coords, int64_t n, HashTable* h, cudaStream_t s);
 sc_status launch_hash_query(const HashTable* h, const int32_t* q, int64_t m, int32_t* rows,
