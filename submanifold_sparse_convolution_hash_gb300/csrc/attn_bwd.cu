@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int n = row_tiles(p, it, &first);
         if (n == 0) continue;
         const uint32_t b = nkv % KVB;
-        if (!mbar_wait_inl(smem_u32(&sm->kv_empty[b]), ((nkv / KVB) & 1) ^ 1, abort_flag)) {
+        if (!mbar_wait_inl(smem_u32(&sm->kv_empty[b]), ((nkv / KVB) & 1) ^ 1)) {
           sm->abort = 1;
           break;
         }
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int i = first; i < first + n && ok; ++i)
           for (int which = 0; which < 2; ++which, ++k, r.step()) {
             const uint32_t st = r.st;
-            if (!mbar_wait_inl(smem_u32(&sm->empty[st]), r.ph ^ 1, abort_flag)) {
+            if (!mbar_wait_inl(smem_u32(&sm->empty[st]), r.ph ^ 1)) {
               sm->abort = 1;
               ok = false;
               break;
@@ -244,10 +244,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       const uint32_t f0 = nkv > KVB ? nkv - KVB : 0;
       for (uint32_t i = f0; i < nkv; ++i)
-        if (!mbar_drain_inl(smem_u32(&sm->kv_full[i % KVB]), (i / KVB) & 1)) sm->abort = 1;
+        if (!mbar_wait_inl(smem_u32(&sm->kv_full[i % KVB]), (i / KVB) & 1)) sm->abort = 1;
       const uint32_t f1 = k > S ? k - S : 0;
       for (uint32_t i = f1; i < k; ++i)
-        if (!mbar_drain_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
+        if (!mbar_wait_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -271,13 +271,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int n = row_tiles(p, it, &first);
       if (n == 0) continue;
       const uint32_t b = nkv % KVB;
-      bool ok = mbar_wait_inl(smem_u32(&sm->kv_full[b]), (nkv / KVB) & 1, abort_flag);
+      bool ok = mbar_wait_inl(smem_u32(&sm->kv_full[b]), (nkv / KVB) & 1);
       ++nkv;
       // a row tile's copies have landed and its rows are in order
       auto rows = [&](const RingPos<S>& at) {
-        ok = ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph, abort_flag) &&
-             mbar_wait_inl(smem_u32(&sm->full[at.st + 1]), at.ph, abort_flag) &&
-             mbar_wait_inl(smem_u32(&sm->rows_ok[nr & 1]), (nr >> 1) & 1, abort_flag);
+        ok = ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph) &&
+             mbar_wait_inl(smem_u32(&sm->full[at.st + 1]), at.ph) &&
+             mbar_wait_inl(smem_u32(&sm->rows_ok[nr & 1]), (nr >> 1) & 1);
         ++nr;
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         RingPos<S> nxt = cur;
         nxt.step();
         nxt.step();
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->p_ready), np & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->p_ready), np & 1));
         if (!ok) break;
         tc_fence_after();
         if (elect_lane()) product_cols<0, 8>(t_dv, t_s, 32, rowt_lo + (cur.st + 1) * T16, rowt_hi, id_a, i > 0);
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
           __syncwarp();
         }
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->ds_ready), np & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->ds_ready), np & 1));
         if (!ok) break;
         tc_fence_after();
         if (elect_lane()) {
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     if (elect_lane()) tc_commit(smem_u32(&sm->drained));
     __syncwarp();
-    if (!mbar_drain_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
+    if (!mbar_wait_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
     __syncwarp();
   } else if (warp == 10) {
     if (lane == 0) hand_out(&sm->slots, p.counter, p.items, units, p.heads_kv, abort_flag);
@@ -366,9 +366,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             st[u] = __ldcg(p.stat + t * p.heads_q + head * p.g + r % p.g);
           }
         }
-        ok = mbar_wait_inl(smem_u32(&sm->rows_free[sl]), ((nr >> 1) & 1) ^ 1, abort_flag);
-        ok = ok && mbar_wait_inl(smem_u32(&sm->full[cur.st]), cur.ph, abort_flag) &&
-             mbar_wait_inl(smem_u32(&sm->full[cur.st + 1]), cur.ph, abort_flag);
+        ok = mbar_wait_inl(smem_u32(&sm->rows_free[sl]), ((nr >> 1) & 1) ^ 1);
+        ok = ok && mbar_wait_inl(smem_u32(&sm->full[cur.st]), cur.ph) &&
+             mbar_wait_inl(smem_u32(&sm->full[cur.st + 1]), cur.ph);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           sm->abort = 1;
@@ -415,8 +415,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       bool ok = true;
       for (int i = first; i < first + n; ++i, ++np, ++nr) {
         const uint32_t sl = nr & 1;
-        ok = mbar_wait_inl(smem_u32(&sm->rows_ok[sl]), (nr >> 1) & 1, abort_flag) &&
-             mbar_wait_inl(smem_u32(&sm->s_full), np & 1, abort_flag);
+        ok = mbar_wait_inl(smem_u32(&sm->rows_ok[sl]), (nr >> 1) & 1) &&
+             mbar_wait_inl(smem_u32(&sm->s_full), np & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm->p_ready));
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->dp_full), np & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->dp_full), np & 1));
         if (!ok) break;
         tc_fence_after();
         tmem_ld64_raw(tdp, y);
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         break;
       }
       if (n > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->acc_full), na & 1, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->acc_full), na & 1))) {
           sm->abort = 1;
           break;
         }
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       RingPos<S> r;
       while (ring.next(&it, &head, abort_flag, false)) {
         if (it.kt1 == 0) continue;
-        if (!mbar_wait_inl(smem_u32(&sm->q_empty), (nq & 1) ^ 1, abort_flag)) {
+        if (!mbar_wait_inl(smem_u32(&sm->q_empty), (nq & 1) ^ 1)) {
           sm->abort = 1;
           break;
         }
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int j = 0; j < it.kt1 && ok; ++j)
           for (int kv = 0; kv < 2; ++kv, ++k, r.step()) {
             const uint32_t st = r.st;
-            if (!mbar_wait_inl(smem_u32(&sm->empty[st]), r.ph ^ 1, abort_flag)) {
+            if (!mbar_wait_inl(smem_u32(&sm->empty[st]), r.ph ^ 1)) {
               sm->abort = 1;
               ok = false;
               break;
@@ -604,10 +604,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         if (!ok) break;
       }
-      if (nq > 0 && !mbar_drain_inl(smem_u32(&sm->q_full), (nq - 1) & 1)) sm->abort = 1;
+      if (nq > 0 && !mbar_wait_inl(smem_u32(&sm->q_full), (nq - 1) & 1)) sm->abort = 1;
       const uint32_t f1 = k > S ? k - S : 0;
       for (uint32_t i = f1; i < k; ++i)
-        if (!mbar_drain_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
+        if (!mbar_wait_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -629,18 +629,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     while (ring.next(&it, &head, abort_flag, true)) {
       const int n = it.kt1;
       if (n == 0) continue;
-      bool ok = mbar_wait_inl(smem_u32(&sm->q_full), nq & 1, abort_flag);
+      bool ok = mbar_wait_inl(smem_u32(&sm->q_full), nq & 1);
       ++nq;
       // S of key tile j into its buffer; the tile's rows past the keys are zeroed first
       auto scores = [&](int j) {
-        ok = ok && mbar_wait_inl(smem_u32(&sm->full[rs.st]), rs.ph, abort_flag);
+        ok = ok && mbar_wait_inl(smem_u32(&sm->full[rs.st]), rs.ph);
         if (it.lk - j * kKeyTile < kKeyTile) {
           if (lane == 0 && ok) {
             sm->fix_at = static_cast<int>(rs.st);
             sm->fix_rows = it.lk - j * kKeyTile;
             mbar_arrive(smem_u32(&sm->fix_k));
           }
-          ok = ok && mbar_wait_inl(smem_u32(&sm->k_fixed), nfix & 1, abort_flag);
+          ok = ok && mbar_wait_inl(smem_u32(&sm->k_fixed), nfix & 1);
           ++nfix;
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       };
       // dP of the tile whose V lies at `at`, which is then done with
       auto dp = [&](const RingPos<S>& at) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph, abort_flag));
+        ok = __all_sync(0xffffffffu, ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph));
         if (!ok) return;
         tc_fence_after();
         if (elect_lane()) {
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       dp(v);
       if (n > 1) scores(1);
       for (int j = 0; j < n && ok; ++j, ++nd) {
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->ds_ready), nd & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->ds_ready), nd & 1));
         if (!ok) break;
         tc_fence_after();
         if (elect_lane()) {
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     if (elect_lane()) tc_commit(smem_u32(&sm->drained));
     __syncwarp();
-    if (!mbar_drain_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
+    if (!mbar_wait_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
     __syncwarp();
   } else if (warp == 10) {
     if (lane == 0) hand_out(&sm->slots, p.counter, p.items, units, p.heads_kv, abort_flag);
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t n = 0;
     while (ring.next(&it, &head, abort_flag, true)) {
       if (it.kt1 == 0 || it.lk - (it.kt1 - 1) * kKeyTile >= kKeyTile) continue;
-      if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->fix_k), n & 1, abort_flag))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->fix_k), n & 1))) {
         sm->abort = 1;
         break;
       }
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       bool ok = true;
       for (int j = 0; j < n; ++j, ++nd) {
         const uint32_t b = nd & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->s_full[b]), (nd >> 1) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->s_full[b]), (nd >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
         uint32_t x[64], y[64];
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           x[c] = __float_as_uint(ex2(e0));
           x[c + 1] = __float_as_uint(ex2(e1));
         }
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->dp_full), nd & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->dp_full), nd & 1));
         if (!ok) break;
         tc_fence_after();
         tmem_ld64_raw(tdp, y);
@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         break;
       }
       if (n > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->acc_full), na & 1, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->acc_full), na & 1))) {
           sm->abort = 1;
           break;
         }

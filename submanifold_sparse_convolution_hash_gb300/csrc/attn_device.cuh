@@ -64,10 +64,16 @@ __device__ __forceinline__ bool elect_lane() {
   return p != 0;
 }
 
+// A value that all lanes hold, as one of the warp: what is worked out from such
+// values alone stays in the warp's own registers, which is where a product's
+// operands are read from.
+__device__ __forceinline__ uint32_t of_warp(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
+__device__ __forceinline__ int of_warp(int v) { return static_cast<int>(of_warp(static_cast<uint32_t>(v))); }
+
 // Products of 128-row tiles.  The issuing warp runs as one and its elected lane
-// issues: every operand is the warp's, and the steps are unrolled with constant
-// offsets, because a lane that works out a descriptor a step is slower than the
-// tensor core (176 cycles a 128 x 128 x 16 step against 64).
+// issues: every operand is the warp's (of_warp), and the steps are unrolled with
+// constant offsets, because a lane that works out a descriptor a step is slower
+// than the tensor core (176 cycles a 128 x 128 x 16 step against 64).
 //
 // D = A B^T over the head's values: tiles of `ksteps` (at most DP / 16) steps
 // of 16 values, 64-value panels of 16 KB.
@@ -101,6 +107,18 @@ struct RingPos {
       ph ^= 1;
     }
   }
+  // `off` places on, off at most 2 S
+  __device__ __forceinline__ RingPos at(uint32_t off) const {
+    RingPos r = *this;
+    r.st += off;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (r.st >= S) {
+        r.st -= S;
+        r.ph ^= 1;
+      }
+    return r;
+  }
 };
 
 // Work units reach a block's warps through two slots: one warp takes the next
@@ -123,7 +141,7 @@ __device__ __forceinline__ void hand_out(ItemSlots* sl, int* counter, const Attn
   for (uint32_t n = 0;; ++n) {
     const int slot = n & 1;
     const int u = atomicAdd(counter, 1);
-    if (!mbar_wait_inl(smem_u32(&sl->empty[slot]), ((n >> 1) & 1) ^ 1, abort_flag)) {
+    if (!mbar_wait_inl(smem_u32(&sl->empty[slot]), ((n >> 1) & 1) ^ 1)) {
       *abort_flag = 1;
       break;
     }
@@ -148,7 +166,7 @@ struct ItemRing {
   // The next item; false: no more (or the block gives up).
   __device__ __forceinline__ bool next(AttnItem* it, int* head, volatile int* abort_flag, bool warp) {
     const int slot = n & 1;
-    bool ok = mbar_wait_inl(smem_u32(&sl->full[slot]), (n >> 1) & 1, abort_flag);
+    bool ok = mbar_wait_inl(smem_u32(&sl->full[slot]), (n >> 1) & 1);
     if (warp) ok = __all_sync(0xffffffffu, ok);
     if (!ok) {
       *abort_flag = 1;
@@ -165,7 +183,7 @@ struct ItemRing {
   // is no more; it stays until release().
   __device__ __forceinline__ const AttnItem* peek(volatile int* abort_flag) {
     const int slot = n & 1;
-    if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sl->full[slot]), (n >> 1) & 1, abort_flag))) {
+    if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sl->full[slot]), (n >> 1) & 1))) {
       *abort_flag = 1;
       return nullptr;
     }

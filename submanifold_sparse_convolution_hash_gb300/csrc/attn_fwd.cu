@@ -6,10 +6,9 @@
 //   S = Q K^T                        tensor cores, 128 x 128 in TMEM
 //   m' = max(m, max S), P = exp2((S - m') scale log2 e), l = l 2^(..) + sum P
 //   O = O 2^((m - m') ..) + P V      P back in TMEM as the first operand
-// so the scores never leave the SM.  One warp loads by TMA, one issues the
-// products, and each row tile has four warps of its own for the exponentials,
-// a row a thread; while one tile's exponentials run, the other tile's products
-// do.  O is corrected only when a row's maximum grew by more than 2^8: until
+// so the scores never leave the SM.  One warp loads by TMA; each row tile has a
+// warp that issues its products and four for the exponentials, a row a thread;
+// while one tile's exponentials run, the other tile's products do.  O is corrected only when a row's maximum grew by more than 2^8: until
 // then P is up to 256 instead of 1, which costs no bits in floating point.
 #include "attn_device.cuh"
 
@@ -18,6 +17,7 @@ namespace {
 
 constexpr int kFwdThreads = 384;
 constexpr int kFwdMaxStages = 10;
+constexpr float kLn2 = 0.6931471805599453f;
 // K and V tiles in flight: 160 KB of them beside the two Q tiles.
 constexpr int fwd_stages(int dp) { return dp == 64 ? 10 : 5; }
 // Registers a thread: the block is launched with kFwdRegs for all, four warps
@@ -43,14 +43,23 @@ struct FwdParams {
 struct FwdSmem {
   uint64_t full[kFwdMaxStages], empty[kFwdMaxStages];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_ready[2][2], o_full[2];
-  uint64_t fix_v, v_fixed;
+  uint64_t s_full[2], s_free[2], p_ready[2][2], o_full[2];
+  uint64_t v_fixed;
   ItemSlots slots;
   uint64_t drained;
   uint32_t tmem;
   int abort;
-  int fix_at, fix_rows;  // ring stage of a V tile that ends inside, and its keys
 };
+
+// What a row's exponents are taken from, m scale as it rounds (0 before any
+// key), and the factor from one such base to the next.
+constexpr float kFar = 16777216.f;
+__device__ __forceinline__ float base_of(float m, float scale_log2) {
+  return m == -INFINITY ? 0.f : __fmul_rn(m, scale_log2);
+}
+__device__ __forceinline__ float step_down(float m, float mn, float base, float nb, float scale_log2) {
+  return fabsf(nb) > kFar ? ex2((m - mn) * scale_log2) : ex2(base - nb);
+}
 
 // Key tiles that row tile s of the item has to see: [kt0, end).  In a dual item
 // both halves have the one row tile, half s every other key tile from kt0 + s.
@@ -82,19 +91,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < S; ++s) {
       mbar_init(smem_u32(&sm->full[s]), 1);
-      mbar_init(smem_u32(&sm->empty[s]), 1);
+      mbar_init(smem_u32(&sm->empty[s]), 2);
     }
     mbar_init(smem_u32(&sm->q_full), 1);
-    mbar_init(smem_u32(&sm->q_empty), 1);
+    mbar_init(smem_u32(&sm->q_empty), 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&sm->s_full[s]), 1);
+      mbar_init(smem_u32(&sm->s_free[s]), 4);
       for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&sm->p_ready[s][h]), 4);
       mbar_init(smem_u32(&sm->o_full[s]), 1);
     }
-    mbar_init(smem_u32(&sm->fix_v), 1);
     mbar_init(smem_u32(&sm->v_fixed), 1);
-    mbar_init(smem_u32(&sm->drained), 1);
-    sm->slots.init(11);  // 8 softmax warps, loads, products, tail
+    mbar_init(smem_u32(&sm->drained), 2);
+    sm->slots.init(11);  // 8 softmax warps, loads, two for products
     sm->abort = 0;
     fence_mbar_init();
   }
@@ -108,7 +117,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   grid_wait();  // the plan
   grid_release();
   const uint32_t tmem = sm->tmem;
-  // TMEM: S (and P over it) of the two row tiles, then their O, 128 columns each
+  // TMEM: S of the two row tiles, 128 columns each; to 64 values P (64 columns
+  // each) and O behind them, else P over S and O of 128 columns.
+  constexpr bool EARLY = DP == 64;
+  const uint32_t t_p = EARLY ? tmem + 256 : tmem, t_o = EARLY ? tmem + 384 : tmem + 256;
+  constexpr uint32_t P_COLS = EARLY ? 64 : 128, O_COLS = EARLY ? 64 : 128;
   const int n_items = __ldcg(p.header);
   const int units = n_items * p.heads_kv;
 
@@ -126,7 +139,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int e0 = tile_end(p, it, 0), e1 = tile_end(p, it, 1);
         const int end = max(e0, e1);
         if (end <= it.kt0) continue;
-        if (!mbar_wait_inl(smem_u32(&sm->q_empty), (nq & 1) ^ 1, abort_flag)) {
+        if (!mbar_wait_inl(smem_u32(&sm->q_empty), (nq & 1) ^ 1)) {
           sm->abort = 1;
           break;
         }
@@ -146,7 +159,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           for (int u = 0; u < 2 * step; ++u) {
             const int kv = u >= step, tile = j + u % step;
             if (tile >= end) continue;
-            if (!mbar_wait_inl(smem_u32(&sm->empty[r.st]), r.ph ^ 1, abort_flag)) {
+            if (!mbar_wait_inl(smem_u32(&sm->empty[r.st]), r.ph ^ 1)) {
               sm->abort = 1;
               ok = false;
               break;
@@ -161,15 +174,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (!ok) break;
       }
       // every copy has landed before the block may end
-      if (nq > 0 && !mbar_drain_inl(smem_u32(&sm->q_full), (nq - 1) & 1)) sm->abort = 1;
+      if (nq > 0 && !mbar_wait_inl(smem_u32(&sm->q_full), (nq - 1) & 1)) sm->abort = 1;
       const uint32_t first = loads > S ? loads - S : 0;
       for (uint32_t i = first; i < loads; ++i)
-        if (!mbar_drain_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
+        if (!mbar_wait_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 9 || warp == 11) {
     // ======================================================== products
+    // A warp for each half: its products wait for its softmax alone, and the two
+    // keep the tensor cores busy by turns.  Every K and V tile is given back by
+    // both, by a half that has no use for it as soon as it is there.
     regs_drop<kFwdSideRegs>();
+    const int s = warp == 11;
     const int dn = (p.d + 15) & ~15;
     const int ksteps = dn / 16;
     const uint32_t id_s = make_idesc(BF16, 128, 128);
@@ -178,206 +195,139 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t q_lo = static_cast<uint32_t>(smem_desc(sq, 1024, 2)), k_lo = static_cast<uint32_t>(dk),
                    v_lo = static_cast<uint32_t>(dv);
     const uint32_t k_hi = static_cast<uint32_t>(dk >> 32), v_hi = static_cast<uint32_t>(dv >> 32);
+    const uint32_t tbase = of_warp(tmem);
+    const uint32_t ts = tbase + s * 128, tp = tbase + (EARLY ? 256 : 0) + s * P_COLS,
+                   to = tbase + (EARLY ? 384 : 256) + s * O_COLS;
     ItemRing ring(&sm->slots);
     AttnItem it;
     int head;
-    uint32_t nq = 0, nfix = 0;
-    RingPos<S> r;
-    uint32_t np = 0;  // bit s: phase of p_ready[s]
+    uint32_t nq = 0, nfix = 0, np = 0, nf = 0;
+    RingPos<S> kv;  // ring place of the tile's (a dual item's pair's) first K
     while (ring.next(&it, &head, abort_flag, true)) {
-      const int e0 = tile_end(p, it, 0), e1 = tile_end(p, it, 1);
-      const int last = max(e0, e1);
-      if (last <= it.kt0) continue;
-      bool ok = mbar_wait_inl(smem_u32(&sm->q_full), nq & 1, abort_flag);
+      const int kt0 = of_warp(it.kt0), dual = of_warp(it.dual), lk = of_warp(it.lk);
+      const int e0 = of_warp(tile_end(p, it, 0)) - kt0, e1 = of_warp(tile_end(p, it, 1)) - kt0;
+      const int n = max(e0, e1);
+      if (n <= 0) continue;
+      // this half's tiles: t0, t0 + step, ... below `end`
+      const int step = 1 + dual, t0 = dual ? s : 0, end = dual ? n : s ? e1 : e0;
+      const uint32_t q_at = q_lo + (dual ? 0 : s * (TILE >> 4));
+      bool ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->q_full), nq & 1));
       ++nq;
-      if (it.dual) {
-        const int n = last - it.kt0;  // half t & 1 takes tile t
-        auto scores = [&](int t, const RingPos<S>& at) {
-          ok = __all_sync(0xffffffffu, ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph, abort_flag));
-          if (!ok) return;
+      auto full = [&](const RingPos<S>& at) { ok = ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph); };
+      // Tiles that only the other half uses, up to tile `to`: given back as soon as they are there.
+      int seen = 0;
+      auto pass_to = [&](int to) {
+#pragma unroll 1
+        for (; seen < to; ++seen) {
+          const uint32_t odd = dual ? seen & 1 : 0;
+#pragma unroll 1
+          for (int u = 0; u < 2; ++u) {
+            const RingPos<S> at = kv.at(odd + (u == 0 ? 0 : dual && (seen | 1) < n ? 2 : 1));
+            full(at);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm->empty[at.st]));
+          }
+          if (!dual || odd || seen + 1 == n) kv = kv.at(odd ? 4 : 2);
+        }
+      };
+      const bool tail = lk < (kt0 + n) * kKeyTile;  // the last tile ends inside
+      const bool fixer = dual ? ((n - 1) & 1) == s : (e0 == n) == (s == 0);
+      bool fixed = false;
+      if (t0 >= end && lane == 0) mbar_arrive(smem_u32(&sm->q_empty));
+      // Step t makes S of the next tile and P V of this one; the first makes S
+      // alone.  With P in columns of its own S comes first, as soon as the softmax
+      // has this tile's in registers; else P lies over S, and S comes second.
+#pragma unroll 1
+      for (int t = t0 - step; t < end && ok; t += step) {
+        if (t > 0 && seen < t) pass_to(t);
+        const uint32_t odd = dual ? t & 1 : 0;
+        const bool cur = t >= t0, more = t + step < end;
+        const RingPos<S> k = cur ? kv.at(dual ? 4 + odd : 2) : kv.at(t0), v = kv.at(odd + (dual && (t | 1) < n ? 2 : 1));
+        const uint32_t kk = k_lo + k.st * (TILE >> 4), vv = v_lo + v.st * (TILE >> 4);
+        if (more) {
+          if (EARLY && cur) ok = mbar_wait_inl(smem_u32(&sm->s_free[s]), nf++ & 1);
+          full(k);
+        }
+        if (EARLY && more) {
           tc_fence_after();
           if (elect_lane()) {
-            product_rows<DP>(tmem + (t & 1) * 128, q_lo, k_lo + at.st * (TILE >> 4), k_hi, id_s, ksteps);
-            tc_commit(smem_u32(&sm->s_full[t & 1]));
-            tc_commit(smem_u32(&sm->empty[at.st]));
-            if (t + 1 == n) tc_commit(smem_u32(&sm->q_empty));
+            product_rows<DP>(ts, q_at, kk, k_hi, id_s, ksteps);
+            tc_commit(smem_u32(&sm->s_full[s]));
+            tc_commit(smem_u32(&sm->empty[k.st]));
           }
           __syncwarp();
-        };
-        scores(0, r);
-        r.step();
-        if (n > 1) {
-          scores(1, r);
-          r.step();
         }
-        for (int t0 = 0; t0 < n && ok; t0 += 2) {
-          RingPos<S> v = r;  // V of t0 (and t0 + 1), then K of t0 + 2 (and t0 + 3)
-          RingPos<S> k = r;
-          k.step();
-          if (t0 + 1 < n) k.step();
+        if (cur) {
+          full(v);
+          if (tail && t + 1 == n) {
+            // Rows of the last V tile past the sequence's keys belong to someone
+            // else (or to nobody).  Their weights are zero, but zero times a NaN or
+            // an infinity is not, so they are zeroed before the product.
+            if (fixer) {
+              const int rows = lk - (kt0 + t) * kKeyTile;
+              uint8_t* tile = smem + (2 + v.st) * TILE;
+#pragma unroll 1
+              for (int i = rows * 8 + lane; i < kKeyTile * 8; i += 32)
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const int t = t0 + s;
-            if (t >= n) continue;
-            ok = ok && mbar_wait_inl(smem_u32(&sm->full[v.st]), v.ph, abort_flag);
-            const int left = it.lk - (it.kt0 + t) * kKeyTile;
-            if (left < kKeyTile) {
-              if (lane == 0 && ok) {
-                sm->fix_at = static_cast<int>(v.st);
-                sm->fix_rows = left;
-                mbar_arrive(smem_u32(&sm->fix_v));
-              }
-              ok = ok && mbar_wait_inl(smem_u32(&sm->v_fixed), nfix & 1, abort_flag);
-              ++nfix;
-            }
-            for (int h = 0; h < 2; ++h) {
-              ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][h]), (np >> s) & 1, abort_flag);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-              tc_fence_after();
-              if (elect_lane()) {
-                const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128, b = v_lo + v.st * (TILE >> 4);
-                if (h == 0) {
-                  product_cols<0, 4>(t_o, t_s, 0, b, v_hi, id_o, t > 1);
-                } else {
-                  product_cols<4, 4>(t_o, t_s, 0, b, v_hi, id_o, true);
-                  tc_commit(smem_u32(&sm->empty[v.st]));
-                  if (t + 2 >= n) tc_commit(smem_u32(&sm->o_full[s]));
-                }
-              }
+                for (int c = 0; c < PANELS; ++c)
+                  *reinterpret_cast<uint4*>(tile + c * PANEL + i * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
               __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&sm->v_fixed));
+            } else {
+              ok = ok && mbar_wait_inl(smem_u32(&sm->v_fixed), nfix & 1);
             }
-            if (!ok) break;
-            np ^= 1u << s;
-            if (t + 2 < n) {
-              scores(t + 2, k);
-              k.step();
-            }
-            v.step();
-          }
-          r = k;
-        }
-        if (!ok) {
-          sm->abort = 1;
-          break;
-        }
-        continue;
-      }
-      ok = ok && mbar_wait_inl(smem_u32(&sm->full[r.st]), r.ph, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) {
-        sm->abort = 1;
-        break;
-      }
-      tc_fence_after();
-      if (elect_lane()) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if ((s ? e1 : e0) <= it.kt0) continue;
-          product_rows<DP>(tmem + s * 128, q_lo + s * (TILE >> 4), k_lo + r.st * (TILE >> 4), k_hi, id_s, ksteps);
-          tc_commit(smem_u32(&sm->s_full[s]));
-        }
-        tc_commit(smem_u32(&sm->empty[r.st]));
-        if (last == it.kt0 + 1) tc_commit(smem_u32(&sm->q_empty));
-      }
-      __syncwarp();
-      r.step();
-      for (int j = it.kt0; j < last; ++j) {
-        const RingPos<S> v = r;  // V of tile j
-        r.step();
-        ok = mbar_wait_inl(smem_u32(&sm->full[v.st]), v.ph, abort_flag);
-        const bool tail = it.lk - j * kKeyTile < kKeyTile;
-        if (tail && lane == 0) {  // warp 11 zeroes the rows past the keys meanwhile
-          sm->fix_at = static_cast<int>(v.st);
-          sm->fix_rows = it.lk - j * kKeyTile;
-          if (ok) mbar_arrive(smem_u32(&sm->fix_v));
-        }
-        const bool more = j + 1 < last;
-        if (more) ok = ok && mbar_wait_inl(smem_u32(&sm->full[r.st]), r.ph, abort_flag);
-        bool fixed = false;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int end = s ? e1 : e0;
-          if (j >= end) continue;
-          ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][0]), (np >> s) & 1, abort_flag);
-          if (tail && !fixed) {
-            ok = ok && mbar_wait_inl(smem_u32(&sm->v_fixed), nfix & 1, abort_flag);
-            ++nfix;
             fixed = true;
           }
-          if (!__all_sync(0xffffffffu, ok)) break;
-          tc_fence_after();
-          const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128, b = v_lo + v.st * (TILE >> 4);
-          if (elect_lane()) product_cols<0, 4>(t_o, t_s, 0, b, v_hi, id_o, j > it.kt0);
-          __syncwarp();
-          ok = mbar_wait_inl(smem_u32(&sm->p_ready[s][1]), (np >> s) & 1, abort_flag);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          np ^= 1u << s;
-          tc_fence_after();
-          if (elect_lane()) {
-            product_cols<4, 4>(t_o, t_s, 0, b, v_hi, id_o, true);
-            if (j + 1 == end) {
-              tc_commit(smem_u32(&sm->o_full[s]));
-            } else {
-              product_rows<DP>(t_s, q_lo + s * (TILE >> 4), k_lo + r.st * (TILE >> 4), k_hi, id_s, ksteps);
-              tc_commit(smem_u32(&sm->s_full[s]));
-            }
+          ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][0]), np & 1);
+          if constexpr (!EARLY) {  // the product begins with half of the keys
+            tc_fence_after();
+            if (elect_lane()) product_cols<0, 4>(to, tp, 0, vv, v_hi, id_o, t > t0);
+            __syncwarp();
+            ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][1]), np & 1);
           }
-          __syncwarp();
+          ++np;
         }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        tc_fence_after();
         if (elect_lane()) {
-          tc_commit(smem_u32(&sm->empty[v.st]));
-          if (more) {
-            tc_commit(smem_u32(&sm->empty[r.st]));
-            if (j + 2 == last) tc_commit(smem_u32(&sm->q_empty));
+          if (cur) {
+            if constexpr (EARLY) product_cols<0, 8>(to, tp, 0, vv, v_hi, id_o, t > t0);
+            else product_cols<4, 4>(to, tp, 0, vv, v_hi, id_o, true);
+            if (EARLY || !more) tc_commit(smem_u32(&sm->o_full[s]));
+            tc_commit(smem_u32(&sm->empty[v.st]));
           }
+          if (!EARLY && more) {
+            product_rows<DP>(ts, q_at, kk, k_hi, id_s, ksteps);
+            tc_commit(smem_u32(&sm->s_full[s]));
+            tc_commit(smem_u32(&sm->empty[k.st]));
+          }
+          if (t + 2 * step >= end && more) tc_commit(smem_u32(&sm->q_empty));  // the last S
         }
         __syncwarp();
-        if (more) r.step();
+        ok = __all_sync(0xffffffffu, ok);
+        if (cur) {
+          if (!dual || odd || t + 1 == n) kv = kv.at(odd ? 4 : 2);
+          seen = t + 1;
+        }
       }
-      if (!ok) {
+      if (seen < n) pass_to(n);
+      if (tail) {  // both keep the barrier's phase
+        if (ok && !fixed) ok = mbar_wait_inl(smem_u32(&sm->v_fixed), nfix & 1);
+        ++nfix;
+      }
+      if (!__all_sync(0xffffffffu, ok)) {
         sm->abort = 1;
         break;
       }
     }
     if (elect_lane()) tc_commit(smem_u32(&sm->drained));  // every product is done before TMEM is freed
     __syncwarp();
-    if (!mbar_drain_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
+    if (!mbar_wait_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
     __syncwarp();
   } else if (warp == 10) {
     // ====================================================== work units
     regs_drop<kFwdSideRegs>();
     if (lane == 0) hand_out(&sm->slots, p.counter, p.items, units, p.heads_kv, abort_flag);
-    __syncwarp();
-  } else if (warp == 11) {
-    // ==================================================== tail of V
-    regs_drop<kFwdSideRegs>();
-    // Rows of a V tile past the sequence's keys belong to someone else (or to
-    // nobody).  Their weights are zero, but zero times a NaN or an infinity is
-    // not, so they are zeroed before the product.
-    ItemRing ring(&sm->slots);
-    AttnItem it;
-    int head;
-    uint32_t n = 0;
-    while (ring.next(&it, &head, abort_flag, true)) {
-      const int end = max(tile_end(p, it, 0), tile_end(p, it, 1));
-      if (end <= it.kt0 || it.lk - (end - 1) * kKeyTile >= kKeyTile) continue;
-      // the issuing warp asks once the tile has landed
-      if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->fix_v), n & 1, abort_flag))) {
-        sm->abort = 1;
-        break;
-      }
-      ++n;
-      const int rows = sm->fix_rows;
-      uint8_t* v = smem + (2 + sm->fix_at) * TILE;
-      for (int c = 0; c < PANELS; ++c)
-        for (int i = rows * 8 + lane; i < kKeyTile * 8; i += 32)
-          *reinterpret_cast<uint4*>(v + c * PANEL + i * 16) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm->v_fixed));
-    }
     __syncwarp();
   } else {
     // ======================================================== softmax
@@ -385,7 +335,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int s = warp >> 2;                      // row tile
     const int row = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t ts = tmem + s * 128 + lane_off, to = ts + 256;
+    const uint32_t ts = tmem + s * 128 + lane_off;
+    const uint32_t tp = t_p + s * P_COLS + lane_off, to = t_o + s * O_COLS + lane_off;
     const int pos = row / p.g, gh = row - pos * p.g;
     const float sl = p.scale_log2;
     const float grow = 8.f / sl;                  // growth of the maximum that is let stand
@@ -397,19 +348,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const int i = (dual ? 0 : s * p.pos) + pos;  // this row's query in the item
       const int vis = p.causal ? min(itp->lk, itp->lim0 + i + 1) : itp->lk;  // keys it sees
       float m = -INFINITY, l = 0.f;
+      float base = 0.f;  // P = exp2(S scale - base)
       bool ok = true;
       for (int j = j0; j < end; j += 1 + dual) {
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->s_full[s]), ns & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->s_full[s]), ns & 1));
         ++ns;
         if (!ok) break;
         tc_fence_after();
         uint32_t x[128];
         tmem_ld128_raw(ts, x);
+        if constexpr (EARLY) {
+          if (j + 1 + dual < end) {  // another S of this half is wanted
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm->s_free[s]));
+          }
+        }
         const int seen = vis - j * kKeyTile;
-        if (__any_sync(0xffffffffu, seen < kKeyTile)) {
+        if (__any_sync(0xffffffffu, seen < kKeyTile)) [[unlikely]] {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= seen) x[c] = 0xff800000u;
+          for (int q = 0; q < 4; ++q) {
+            if (!__any_sync(0xffffffffu, seen < 32 * q + 32)) continue;
+#pragma unroll
+            for (int c = 32 * q; c < 32 * q + 32; ++c)
+              if (c >= seen) x[c] = 0xff800000u;
+          }
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -418,13 +381,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           for (int u = 0; u < 4; ++u)
             mx[u] = max3(mx[u], __uint_as_float(x[c + 2 * u]), __uint_as_float(x[c + 2 * u + 1]));
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if constexpr (EARLY) {  // the tile before: O is settled, P's columns are free
+          if (j > j0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->o_full[s]), no & 1));
+            ++no;
+            if (!ok) break;
+            tc_fence_after();
+          }
+        }
         const bool raise = mt > m + grow || (m == -INFINITY && mt > m);
-        if (__any_sync(0xffffffffu, raise)) {
+        if (__any_sync(0xffffffffu, raise)) [[unlikely]] {
           const float mn = raise ? mt : m;
-          const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sl);  // 1 for rows that stay
+          const float nb = base_of(mn, sl);
+          const float f = m == -INFINITY ? 0.f : step_down(m, mn, base, nb, sl);  // 1 for rows that stay
           m = mn;
+          base = nb;
           l *= f;
           if (j > j0) {
+#pragma unroll 1
             for (int c = 0; c < p.d; c += 16) {
               uint32_t o[16];
               tmem_ld16_raw(to + c, o);
@@ -434,31 +408,36 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
           }
         }
-        // (S - m) first, then the scale: the product m * scale alone would be off
-        // by its own rounding, which a large score turns into whole powers of two
-        const float mm = m == -INFINITY ? 0.f : -m;
-        const uint64_t nm = pair2(mm, mm), sl2 = pair2(sl, sl);
+        // P = exp2(S scale - base); base is m scale with its rounding, the same for
+        // the whole row, which O, the sum and lse have too.  Past 2^24 it is off by
+        // whole powers of two, so there the difference comes first.
+        const bool far = __any_sync(0xffffffffu, fabsf(base) > kFar);
+        if (far) [[unlikely]] {
+          const float mm = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+          for (int c = 0; c < 128; ++c) x[c] = __float_as_uint((__uint_as_float(x[c]) + mm) * sl);
+        }
+        const uint64_t nm = far ? 0 : pair2(-base, -base), sl2 = far ? pair2(1.f, 1.f) : pair2(sl, sl);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {  // 32 keys at a time, stored as they are done
           uint32_t w[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const uint64_t y = mul2(
-                add2(pair2(__uint_as_float(x[q * 32 + 2 * c]), __uint_as_float(x[q * 32 + 2 * c + 1])), nm), sl2);
             float e0, e1;
-            unpair2(y, e0, e1);
+            unpair2(fma2(pair2(__uint_as_float(x[q * 32 + 2 * c]), __uint_as_float(x[q * 32 + 2 * c + 1])), sl2, nm), e0,
+                    e1);
             e0 = ex2(e0);
             e1 = ex2(e1);
             sum[c & 1] = add2(sum[c & 1], pair2(e0, e1));
             w[c] = pack_pair<BF16>(e0, e1);
           }
-          tmem_st16(ts + q * 16, w);
-          if (q & 1) {  // half of the keys: their product can begin
+          tmem_st16(tp + q * 16, w);
+          if (q == 3 || (q == 1 && !EARLY)) {  // half of the keys: their product can begin
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm->p_ready[s][q >> 1]));
+            if (lane == 0) mbar_arrive(smem_u32(&sm->p_ready[s][EARLY ? 0 : q >> 1]));
           }
         }
         float s0, s1;
@@ -471,7 +450,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       const bool have = end > j0;
       if (have) {
-        if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->o_full[s]), no & 1, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->o_full[s]), no & 1))) {
           sm->abort = 1;
           break;
         }
@@ -501,7 +480,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (c + 8 < p.d) *reinterpret_cast<uint4*>(dst + c * 2 + 16) = make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
-        if (p.lse && live) p.lse[tok * p.heads_q + h] = vis > 0 ? m * p.scale + logf(l) : -INFINITY;
+        if (p.lse && live) p.lse[tok * p.heads_q + h] = vis > 0 ? base * kLn2 + logf(l) : -INFINITY;
       } else {
         // a part of the keys: O, m and l in fp32 for k_attn_join
         const int part = it.slot + (dual ? 2 * it.split + s : it.split);
@@ -558,14 +537,14 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Attn
     for (int q = lane; q < parts; q += 32) m = fmaxf(m, __ldcg(src + q * step + p.d));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float base = m == -INFINITY ? 0.f : m;
+    const float base = base_of(m, p.scale_log2);
     float l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     const bool on = lane * 4 < p.d;
 #pragma unroll 4
     for (int q = 0; q < parts; ++q) {
       const float mq = __ldcg(src + q * step + p.d);
-      const float f = ex2((mq - base) * p.scale_log2);
+      const float f = mq == -INFINITY ? 0.f : step_down(mq, m, base_of(mq, p.scale_log2), base, p.scale_log2);
       l += __ldcg(src + q * step + p.d + 1) * f;
       // nothing seen in this part: no O was written
       const float4 o = on && mq != -INFINITY ? __ldcg(reinterpret_cast<const float4*>(src + q * step) + lane)
@@ -582,7 +561,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Attn
       *reinterpret_cast<uint2*>(p.out + tok * p.out_t + h * p.out_h + lane * 8) =
           vis > 0 ? make_uint2(pack_pair<BF16>(a.x * inv, a.y * inv), pack_pair<BF16>(a.z * inv, a.w * inv))
                   : make_uint2(0u, 0u);
-    if (p.lse && lane == 0) p.lse[tok * p.heads_q + h] = vis > 0 ? m * p.scale + logf(l) : -INFINITY;
+    if (p.lse && lane == 0) p.lse[tok * p.heads_q + h] = vis > 0 ? base * kLn2 + logf(l) : -INFINITY;
   }
 }
 

@@ -59,22 +59,26 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volat
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity, abort_flag);
 }
-// The same wait with its loop inline, for kernels that share out registers
-// between warps (a call would tie all of them to one frame), bounded by the
-// SM's cycle counter (about the same two seconds; cheaper to read).
-constexpr long long kWaitCycles = 4000000000ll;
-__device__ __forceinline__ bool mbar_wait_inl(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-#pragma unroll 1
-  for (uint32_t it = 1; it < (1u << 30); ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63) == 0) {
-      if (*abort_flag) return false;
-      if (clock64() - t0 > kWaitCycles) return false;
-    }
-  }
-  return false;
+// A wait in few instructions, for kernels whose warps run different code: the
+// instruction caches are what such code fights over.  The hardware suspends the
+// thread for up to a millisecond a try; about two seconds in all.
+__device__ __forceinline__ bool mbar_wait_inl(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n\t"
+      "WAIT_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 q, n, 2000;\n\t"
+      "@q bra WAIT_%=;\n\t"
+      "DONE_%=:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 // Same bound, ignoring the abort flag: used to drain work already issued.
 __device__ __noinline__ bool mbar_drain(uint32_t bar, uint32_t parity) {
@@ -82,15 +86,6 @@ __device__ __noinline__ bool mbar_drain(uint32_t bar, uint32_t parity) {
   for (uint32_t it = 0; it < (1u << 30); ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63) == 63 && globaltimer() - t0 > kWaitNs) return false;
-  }
-  return false;
-}
-__device__ __forceinline__ bool mbar_drain_inl(uint32_t bar, uint32_t parity) {
-  const long long t0 = clock64();
-#pragma unroll 1
-  for (uint32_t it = 0; it < (1u << 30); ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63) == 63 && clock64() - t0 > kWaitCycles) return false;
   }
   return false;
 }
