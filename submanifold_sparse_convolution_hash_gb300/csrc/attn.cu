@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs pa, c
         const unsigned long long over = static_cast<unsigned long long>(p.sms) * (few ? 4 : 1);
         const unsigned long long c = (steps + over - 1) / over;
         chunk = static_cast<int>(c < static_cast<unsigned long long>(p.min_tiles) ? p.min_tiles : c);
-        dual = true;
+        dual = p.dual;
       }
     }
     if (pass == 1) {

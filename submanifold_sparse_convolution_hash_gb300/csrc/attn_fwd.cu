@@ -43,7 +43,7 @@ struct FwdParams {
 struct FwdSmem {
   uint64_t full[kFwdMaxStages], empty[kFwdMaxStages];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], s_free[2], p_ready[2][2], o_full[2];
+  uint64_t s_full[2], p_ready[2][2], o_full[2];
   uint64_t v_fixed;
   ItemSlots slots;
   uint64_t drained;
@@ -72,7 +72,18 @@ __device__ __forceinline__ int tile_end(const FwdParams& p, const AttnItem& it, 
   return max(it.kt0, min(end, it.kt1));
 }
 
-template <bool BF16, int DP>
+// Zeroes the rows of a tile from `rows` on, by a warp, for the products to come.
+template <int PANELS>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int rows) {
+#pragma unroll 1
+  for (int i = rows * 8 + static_cast<int>(threadIdx.x & 31); i < kKeyTile * 8; i += 32)
+#pragma unroll
+    for (int c = 0; c < PANELS; ++c) *reinterpret_cast<uint4*>(tile + c * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+template <bool BF16, int DP, bool ONE>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     k_attn_fwd(const FwdParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                const __grid_constant__ CUtensorMap vmap) {
@@ -91,19 +102,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < S; ++s) {
       mbar_init(smem_u32(&sm->full[s]), 1);
-      mbar_init(smem_u32(&sm->empty[s]), 2);
+      mbar_init(smem_u32(&sm->empty[s]), ONE ? 1 : 2);
     }
     mbar_init(smem_u32(&sm->q_full), 1);
-    mbar_init(smem_u32(&sm->q_empty), 2);
+    mbar_init(smem_u32(&sm->q_empty), ONE ? 1 : 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&sm->s_full[s]), 1);
-      mbar_init(smem_u32(&sm->s_free[s]), 4);
       for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&sm->p_ready[s][h]), 4);
       mbar_init(smem_u32(&sm->o_full[s]), 1);
     }
     mbar_init(smem_u32(&sm->v_fixed), 1);
-    mbar_init(smem_u32(&sm->drained), 2);
-    sm->slots.init(11);  // 8 softmax warps, loads, two for products
+    mbar_init(smem_u32(&sm->drained), ONE ? 1 : 2);
+    sm->slots.init(ONE ? 10 : 11);  // 8 softmax warps, loads, those for products
     sm->abort = 0;
     fence_mbar_init();
   }
@@ -184,7 +194,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // ======================================================== products
     // A warp for each half: its products wait for its softmax alone, and the two
     // keep the tensor cores busy by turns.  Every K and V tile is given back by
-    // both, by a half that has no use for it as soon as it is there.
+    // both, by a half that has no use for it as soon as it is there.  Where a row
+    // tile is all an item has (ONE), one warp issues for both halves, which then
+    // work on every other key tile: a tile is given back by its one reader.
     regs_drop<kFwdSideRegs>();
     const int s = warp == 11;
     const int dn = (p.d + 15) & ~15;
@@ -198,131 +210,164 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t tbase = of_warp(tmem);
     const uint32_t ts = tbase + s * 128, tp = tbase + (EARLY ? 256 : 0) + s * P_COLS,
                    to = tbase + (EARLY ? 384 : 256) + s * O_COLS;
-    ItemRing ring(&sm->slots);
-    AttnItem it;
-    int head;
-    uint32_t nq = 0, nfix = 0, np = 0, nf = 0;
-    RingPos<S> kv;  // ring place of the tile's (a dual item's pair's) first K
-    while (ring.next(&it, &head, abort_flag, true)) {
-      const int kt0 = of_warp(it.kt0), dual = of_warp(it.dual), lk = of_warp(it.lk);
-      const int e0 = of_warp(tile_end(p, it, 0)) - kt0, e1 = of_warp(tile_end(p, it, 1)) - kt0;
-      const int n = max(e0, e1);
-      if (n <= 0) continue;
-      // this half's tiles: t0, t0 + step, ... below `end`
-      const int step = 1 + dual, t0 = dual ? s : 0, end = dual ? n : s ? e1 : e0;
-      const uint32_t q_at = q_lo + (dual ? 0 : s * (TILE >> 4));
-      bool ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->q_full), nq & 1));
-      ++nq;
-      auto full = [&](const RingPos<S>& at) { ok = ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph); };
-      // Tiles that only the other half uses, up to tile `to`: given back as soon as they are there.
-      int seen = 0;
-      auto pass_to = [&](int to) {
+    if constexpr (ONE) {
+      ItemRing ring(&sm->slots);
+      AttnItem it;
+      int head;
+      uint32_t nq = 0, np = 0;  // np: bit s, phase of p_ready[s]
+      RingPos<S> kv;            // ring place of the tile's (a dual item's pair's) first K
+      while (warp == 9 && ring.next(&it, &head, abort_flag, true)) {
+        const int kt0 = of_warp(it.kt0), dual = of_warp(it.dual), lk = of_warp(it.lk);
+        const int e0 = of_warp(tile_end(p, it, 0)) - kt0, e1 = of_warp(tile_end(p, it, 1)) - kt0;
+        const int n = max(e0, e1);
+        if (n <= 0) continue;
+        bool ok = mbar_wait_inl(smem_u32(&sm->q_full), nq & 1), fixed = false;
+        ++nq;
+        // Step q is half q & 1's: P V of its tile t and S of its next one.
+        const int steps = dual ? n + 2 : 2 * n + 2;
 #pragma unroll 1
-        for (; seen < to; ++seen) {
-          const uint32_t odd = dual ? seen & 1 : 0;
-#pragma unroll 1
-          for (int u = 0; u < 2; ++u) {
-            const RingPos<S> at = kv.at(odd + (u == 0 ? 0 : dual && (seen | 1) < n ? 2 : 1));
-            full(at);
+        for (int q = 0; q < steps && ok; ++q) {
+          const int h = q & 1, t = dual ? q - 2 : (q >> 1) - 1, nt = t + 1 + dual;
+          const int end = dual ? n : h ? e1 : e0;
+          const bool cur = t >= 0 && t < end, more = nt < end;
+          // ring places from the tile's first K: K V K V .., a dual item's pairs K K V V
+          const RingPos<S> k = kv.at(t < 0 ? (dual ? h : 0) : dual ? 4 + h : 2);
+          const RingPos<S> v = kv.at(dual ? h + ((t | 1) < n ? 2 : 1) : 1);
+          const uint32_t sc = tbase + h * 128, pc = tbase + (EARLY ? 256 : 0) + h * P_COLS,
+                         oc = tbase + (EARLY ? 384 : 256) + h * O_COLS;
+          const uint32_t kk = k_lo + k.st * (TILE >> 4), vv = v_lo + v.st * (TILE >> 4);
+          const uint32_t q_at = q_lo + (dual ? 0 : h * (TILE >> 4));
+          if (cur) {
+            ok = ok && mbar_wait_inl(smem_u32(&sm->full[v.st]), v.ph);
+            const int rows = lk - (kt0 + t) * kKeyTile;
+            if (rows < kKeyTile && !fixed) {  // the last tile ends inside, as below
+              zero_rows<PANELS>(smem + (2 + v.st) * TILE, rows);
+              fixed = true;
+            }
+            ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[h][0]), (np >> h) & 1);
+            if constexpr (!EARLY) ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[h][1]), (np >> h) & 1);
+            np ^= 1u << h;
+            tc_fence_after();
+            if (elect_lane()) {
+              product_cols<0, 8>(oc, pc, 0, vv, v_hi, id_o, t > (dual ? h : 0));
+              if (EARLY || !more) tc_commit(smem_u32(&sm->o_full[h]));
+              if (dual || h || t >= e1) tc_commit(smem_u32(&sm->empty[v.st]));  // its last reader
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm->empty[at.st]));
           }
-          if (!dual || odd || seen + 1 == n) kv = kv.at(odd ? 4 : 2);
-        }
-      };
-      const bool tail = lk < (kt0 + n) * kKeyTile;  // the last tile ends inside
-      const bool fixer = dual ? ((n - 1) & 1) == s : (e0 == n) == (s == 0);
-      bool fixed = false;
-      if (t0 >= end && lane == 0) mbar_arrive(smem_u32(&sm->q_empty));
-      // Step t makes S of the next tile and P V of this one; the first makes S
-      // alone.  With P in columns of its own S comes first, as soon as the softmax
-      // has this tile's in registers; else P lies over S, and S comes second.
-#pragma unroll 1
-      for (int t = t0 - step; t < end && ok; t += step) {
-        if (t > 0 && seen < t) pass_to(t);
-        const uint32_t odd = dual ? t & 1 : 0;
-        const bool cur = t >= t0, more = t + step < end;
-        const RingPos<S> k = cur ? kv.at(dual ? 4 + odd : 2) : kv.at(t0), v = kv.at(odd + (dual && (t | 1) < n ? 2 : 1));
-        const uint32_t kk = k_lo + k.st * (TILE >> 4), vv = v_lo + v.st * (TILE >> 4);
-        if (more) {
-          if (EARLY && cur) ok = mbar_wait_inl(smem_u32(&sm->s_free[s]), nf++ & 1);
-          full(k);
-        }
-        if (EARLY && more) {
-          tc_fence_after();
-          if (elect_lane()) {
-            product_rows<DP>(ts, q_at, kk, k_hi, id_s, ksteps);
-            tc_commit(smem_u32(&sm->s_full[s]));
-            tc_commit(smem_u32(&sm->empty[k.st]));
+          if (more) {  // waited for last: loads bound these calls, and V has been given back
+            ok = ok && mbar_wait_inl(smem_u32(&sm->full[k.st]), k.ph);
+            tc_fence_after();
+            if (elect_lane()) {
+              product_rows<DP>(sc, q_at, kk, k_hi, id_s, ksteps);
+              tc_commit(smem_u32(&sm->s_full[h]));
+              if (dual || h || nt >= e1) tc_commit(smem_u32(&sm->empty[k.st]));
+              if (dual ? nt + 1 == n : nt + 1 == n && (h == (e1 == n))) tc_commit(smem_u32(&sm->q_empty));
+            }
           }
           __syncwarp();
+          ok = __all_sync(0xffffffffu, ok);
+          if (t >= 0 && (dual ? h || t + 1 == n : h)) kv = kv.at(dual && h ? 4 : 2);
         }
-        if (cur) {
-          full(v);
-          if (tail && t + 1 == n) {
-            // Rows of the last V tile past the sequence's keys belong to someone
-            // else (or to nobody).  Their weights are zero, but zero times a NaN or
-            // an infinity is not, so they are zeroed before the product.
-            if (fixer) {
-              const int rows = lk - (kt0 + t) * kKeyTile;
-              uint8_t* tile = smem + (2 + v.st) * TILE;
+        if (!__all_sync(0xffffffffu, ok)) {
+          sm->abort = 1;
+          break;
+        }
+      }
+    } else {
+      ItemRing ring(&sm->slots);
+      AttnItem it;
+      int head;
+      uint32_t nq = 0, nfix = 0, np = 0;
+      RingPos<S> kv;  // ring place of the tile's K
+      while (ring.next(&it, &head, abort_flag, true)) {
+        const int kt0 = of_warp(it.kt0), lk = of_warp(it.lk);
+        const int e0 = of_warp(tile_end(p, it, 0)) - kt0, e1 = of_warp(tile_end(p, it, 1)) - kt0;
+        const int n = max(e0, e1);
+        if (n <= 0) continue;
+        const int end = s ? e1 : e0;  // this half's tiles
+        const uint32_t q_at = q_lo + s * (TILE >> 4);
+        bool ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->q_full), nq & 1));
+        ++nq;
+        auto full = [&](const RingPos<S>& at) { ok = ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph); };
+        const bool tail = lk < (kt0 + n) * kKeyTile;  // the last tile ends inside
+        const bool fixer = (e0 == n) == (s == 0);
+        bool fixed = false;
+        if (end <= 0 && lane == 0) mbar_arrive(smem_u32(&sm->q_empty));
+        // Step t makes S of the next tile and P V of this one; the first makes S
+        // alone.  S comes first where P has columns of its own: the softmax waits for
+        // nothing else.  Else P lies over S, and S comes second.
 #pragma unroll 1
-              for (int i = rows * 8 + lane; i < kKeyTile * 8; i += 32)
-#pragma unroll
-                for (int c = 0; c < PANELS; ++c)
-                  *reinterpret_cast<uint4*>(tile + c * PANEL + i * 16) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&sm->v_fixed));
-            } else {
-              ok = ok && mbar_wait_inl(smem_u32(&sm->v_fixed), nfix & 1);
-            }
-            fixed = true;
-          }
-          ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][0]), np & 1);
-          if constexpr (!EARLY) {  // the product begins with half of the keys
-            tc_fence_after();
-            if (elect_lane()) product_cols<0, 4>(to, tp, 0, vv, v_hi, id_o, t > t0);
-            __syncwarp();
-            ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][1]), np & 1);
-          }
-          ++np;
-        }
-        tc_fence_after();
-        if (elect_lane()) {
+        for (int t = -1; t < end && ok; ++t) {
+          const bool cur = t >= 0, more = t + 1 < end;
+          const RingPos<S> k = cur ? kv.at(2) : kv, v = kv.at(1);
+          const uint32_t kk = k_lo + k.st * (TILE >> 4), vv = v_lo + v.st * (TILE >> 4);
+          if (more) full(k);
           if (cur) {
-            if constexpr (EARLY) product_cols<0, 8>(to, tp, 0, vv, v_hi, id_o, t > t0);
-            else product_cols<4, 4>(to, tp, 0, vv, v_hi, id_o, true);
-            if (EARLY || !more) tc_commit(smem_u32(&sm->o_full[s]));
-            tc_commit(smem_u32(&sm->empty[v.st]));
+            full(v);
+            if (tail && t + 1 == n) {
+              // Rows of the last V tile past the sequence's keys belong to someone
+              // else (or to nobody).  Their weights are zero, but zero times a NaN or
+              // an infinity is not, so they are zeroed before the product.
+              if (fixer) {
+                zero_rows<PANELS>(smem + (2 + v.st) * TILE, lk - (kt0 + t) * kKeyTile);
+                if (lane == 0) mbar_arrive(smem_u32(&sm->v_fixed));
+              } else {
+                ok = ok && mbar_wait_inl(smem_u32(&sm->v_fixed), nfix & 1);
+              }
+              fixed = true;
+            }
+            ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][0]), np & 1);
+            if constexpr (!EARLY) {  // the product begins with half of the keys
+              tc_fence_after();
+              if (elect_lane()) product_cols<0, 4>(to, tp, 0, vv, v_hi, id_o, t > 0);
+              __syncwarp();
+              ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][1]), np & 1);
+            }
+            ++np;
           }
-          if (!EARLY && more) {
-            product_rows<DP>(ts, q_at, kk, k_hi, id_s, ksteps);
-            tc_commit(smem_u32(&sm->s_full[s]));
-            tc_commit(smem_u32(&sm->empty[k.st]));
+          tc_fence_after();
+          if (elect_lane()) {
+            auto scores = [&] {
+              product_rows<DP>(ts, q_at, kk, k_hi, id_s, ksteps);
+              tc_commit(smem_u32(&sm->s_full[s]));
+              tc_commit(smem_u32(&sm->empty[k.st]));
+              if (t + 2 >= end) tc_commit(smem_u32(&sm->q_empty));  // the last S
+            };
+            if (EARLY && more) scores();
+            if (cur) {
+              if constexpr (EARLY) product_cols<0, 8>(to, tp, 0, vv, v_hi, id_o, t > 0);
+              else product_cols<4, 4>(to, tp, 0, vv, v_hi, id_o, true);
+              if (EARLY || !more) tc_commit(smem_u32(&sm->o_full[s]));
+              tc_commit(smem_u32(&sm->empty[v.st]));
+            }
+            if (!EARLY && more) scores();
           }
-          if (t + 2 * step >= end && more) tc_commit(smem_u32(&sm->q_empty));  // the last S
+          __syncwarp();
+          ok = __all_sync(0xffffffffu, ok);
+          if (cur) kv = kv.at(2);
         }
-        __syncwarp();
-        ok = __all_sync(0xffffffffu, ok);
-        if (cur) {
-          if (!dual || odd || t + 1 == n) kv = kv.at(odd ? 4 : 2);
-          seen = t + 1;
+#pragma unroll 1
+        for (int u = 2 * max(end, 0); u < 2 * n; ++u, kv = kv.at(1)) {  // tiles that only the other half uses
+          full(kv);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm->empty[kv.st]));
         }
-      }
-      if (seen < n) pass_to(n);
-      if (tail) {  // both keep the barrier's phase
-        if (ok && !fixed) ok = mbar_wait_inl(smem_u32(&sm->v_fixed), nfix & 1);
-        ++nfix;
-      }
-      if (!__all_sync(0xffffffffu, ok)) {
-        sm->abort = 1;
-        break;
+        if (tail) {  // both keep the barrier's phase
+          if (ok && !fixed) ok = mbar_wait_inl(smem_u32(&sm->v_fixed), nfix & 1);
+          ++nfix;
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+          sm->abort = 1;
+          break;
+        }
       }
     }
-    if (elect_lane()) tc_commit(smem_u32(&sm->drained));  // every product is done before TMEM is freed
-    __syncwarp();
-    if (!mbar_wait_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
+    if (!ONE || warp == 9) {
+      if (elect_lane()) tc_commit(smem_u32(&sm->drained));  // every product is done before TMEM is freed
+      __syncwarp();
+      if (!mbar_wait_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
+    }
     __syncwarp();
   } else if (warp == 10) {
     // ====================================================== work units
@@ -357,13 +402,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tc_fence_after();
         uint32_t x[128];
         tmem_ld128_raw(ts, x);
-        if constexpr (EARLY) {
-          if (j + 1 + dual < end) {  // another S of this half is wanted
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm->s_free[s]));
-          }
-        }
         const int seen = vis - j * kKeyTile;
         if (__any_sync(0xffffffffu, seen < kKeyTile)) [[unlikely]] {
 #pragma unroll
@@ -565,10 +603,10 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Attn
   }
 }
 
-template <bool BF16>
+template <bool BF16, bool ONE>
 const void* fwd_kernel(int dp) {
-  return dp == 64 ? reinterpret_cast<const void*>(k_attn_fwd<BF16, 64>)
-                  : reinterpret_cast<const void*>(k_attn_fwd<BF16, 128>);
+  return dp == 64 ? reinterpret_cast<const void*>(k_attn_fwd<BF16, 64, ONE>)
+                  : reinterpret_cast<const void*>(k_attn_fwd<BF16, 128, ONE>);
 }
 
 }  // namespace
@@ -601,7 +639,10 @@ sc_status attn_fwd(const AttnArgs& a) {
   const size_t tile = static_cast<size_t>(dp) / 64 * 16384;
   FwdParams p{};
   const size_t smem = (2 + fwd_stages(dp)) * tile + sizeof(FwdSmem) + 1024;
-  const void* kern = a.dtype == SC_BF16 ? fwd_kernel<true>(dp) : fwd_kernel<false>(dp);
+  // On average at most one row tile a sequence: the form whose halves share one.
+  const bool one = avg <= 128;
+  const void* kern = a.dtype == SC_BF16 ? (one ? fwd_kernel<true, true>(dp) : fwd_kernel<true, false>(dp))
+                                        : (one ? fwd_kernel<false, true>(dp) : fwd_kernel<false, false>(dp));
   int regs = 0;
   sc_status st = kernel_setup(kern, smem, &regs);
   if (st) return st;
@@ -635,6 +676,7 @@ sc_status attn_fwd(const AttnArgs& a) {
   pl.sms = sms;
   pl.part_rows = part_rows;
   pl.min_tiles = 4;
+  pl.dual = one;
   pl.cap = static_cast<int>(cap);
   pl.join_cap = part_rows ? static_cast<int>(items_ub) : 0;
   pl.header = reinterpret_cast<int*>(base + o_head);

@@ -49,6 +49,7 @@ struct PlanArgs {
   int sms;
   int64_t part_rows;  // rows of partial results that fit; 0: the keys are never cut
   int min_tiles;      // least key tiles of a part
+  int dual;           // items of one row tile may be worked on by both halves
   int cap, join_cap;  // items and joins that fit
   int* header;
   AttnItem* items;
