@@ -46,7 +46,7 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
 // first; a list that breaks a rule gives no work and latches the error.
 //
 // The keys of a unit are cut where the card would otherwise wait for it: with
-// fewer than two units an SM into about four parts an SM, else only units dearer
+// fewer than two units an SM into about `over` parts an SM, else only units dearer
 // than an SM's share.  A part costs its fp32 rows written and read once more.
 __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs pa, const PlanArgs pb) {
   const PlanArgs& p = blockIdx.x ? pb : pa;
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs pa, c
         const int parts = ns * (it.dual ? 2 : 1);
         if (pass == 0) {
           my_max = max(my_max, cost);
-          my_rows = max(my_rows, it.n_pos * p.g);
+          my_rows = max(my_rows, p.mode == kPlanRows ? it.n_pos * p.g : kKeyTile);
           my_steps += static_cast<unsigned long long>(cost);
         } else if (pass == 1) {
           const int b = static_cast<int>(static_cast<int64_t>(kBuckets - 1) * part / s_max);
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs pa, c
           const int end = it.kt1;
           for (int i = 0; i < ns; ++i, ++at) {
             it.split = i;
-            if (ns > 1) {
+            if (ns > 1 && p.mode == kPlanRows) {
               it.kt0 = min(end, i * part);
               it.kt1 = min(end, it.kt0 + part);
             }
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs pa, c
       if (p.part_rows > 0) {
         const unsigned long long steps = s_steps * p.heads_kv;
         const bool few = static_cast<int64_t>(s_items) * p.heads_kv < 2 * p.sms;
-        const unsigned long long over = static_cast<unsigned long long>(p.sms) * (few ? 4 : 1);
+        const unsigned long long over = static_cast<unsigned long long>(p.sms) * (few ? p.over : 1);
         const unsigned long long c = (steps + over - 1) / over;
         chunk = static_cast<int>(c < static_cast<unsigned long long>(p.min_tiles) ? p.min_tiles : c);
         dual = p.dual;

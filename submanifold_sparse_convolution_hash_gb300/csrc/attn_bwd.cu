@@ -20,13 +20,17 @@
 namespace sc {
 namespace {
 
-constexpr int kBwdThreads = 384;
+constexpr int kBwdThreads = 640;
 constexpr int kBwdMaxStages = 12;
+// gk, gv: registers a thread as launched; four warps drop, sixteen raise.
+constexpr int kKvRegs = 96, kKvSideRegs = 64, kKvMainRegs = 104;
+static_assert(128 * kKvSideRegs + 512 * kKvMainRegs <= kBwdThreads * kKvRegs, "no more than the block has");
 // Ring tiles beside what stays: two pairs of K and V (one at 128 values) and
-// pairs of Q and gout; or Q, gout and single K and V tiles.
+// pairs of Q and gout; or such pairs of Q and gout, and single K and V tiles.
 constexpr int kv_pairs(int dp) { return dp == 64 ? 2 : 1; }
 constexpr int kv_stages(int dp) { return dp == 64 ? 8 : 4; }
-constexpr int q_stages(int dp) { return dp == 64 ? 10 : 5; }
+constexpr int q_pairs(int dp) { return dp == 64 ? 2 : 1; }
+constexpr int q_stages(int dp) { return dp == 64 ? 8 : 5; }
 
 // P is held times 2^kPShift.
 template <bool BF16>
@@ -46,6 +50,7 @@ struct BwdParams {
   float scale, scale_log2;
   int causal;
   int first;             // gq: no gk, gv kernel ran before it
+  float* part;           // gk, gv of cut key tiles: [slot][head][2][128][d]
   int* status;
 };
 
@@ -123,27 +128,35 @@ __global__ void __launch_bounds__(256) k_attn_stat(const StatParams p) {
 }
 
 // --------------------------------------------------------------- gk, gv --
+constexpr int kRowSlots = 4;
 struct KvSmem {
   uint64_t full[kBwdMaxStages], empty[kBwdMaxStages];
   uint64_t kv_full[2], kv_empty[2];
-  uint64_t rows_ok[2], rows_free[2];  // row statistics (and the rows of a tile that ends inside)
-  uint64_t s_full, p_ready, dp_full, ds_ready, acc_full;
+  uint64_t rows_ok[kRowSlots], rows_free[kRowSlots];  // row statistics (and the rows of a tile that ends inside)
+  uint64_t s_full[2], p_ready, dp_full, ds_ready, acc_full;
   uint64_t drained;
   uint32_t tmem;
   int abort;
   ItemSlots slots;
-  __align__(16) float lse2[2][128];
-  __align__(16) float delta[2][128];
-  __align__(16) int lim[2][128];  // causal: the last key that the row sees
+  __align__(16) float nlse2[kRowSlots][128];  // negated, as the products take them
+  __align__(16) float ndelta[kRowSlots][128];
+  __align__(16) int lim[kRowSlots][128];  // causal: the last key that the row sees
 };
 
-// First row tile (of p.pos queries) that sees key tile kt, and their number.
+// First row tile (of p.pos queries) of the item, of those that see its key tile,
+// and their number.
 __device__ __forceinline__ int row_tiles(const BwdParams& p, const AttnItem& it, int* first) {
   int i0 = 0;
   if (p.causal) i0 = max(0, it.kt0 * kKeyTile - it.lim0);
   *first = i0 / p.pos;
   if (i0 >= it.n_pos) return 0;
-  return (it.n_pos + p.pos - 1) / p.pos - *first;
+  int n = (it.n_pos + p.pos - 1) / p.pos - *first;
+  if (it.nsplit > 1) {
+    const int part = (n + it.nsplit - 1) / it.nsplit, skip = min(n, it.split * part);
+    *first += skip;
+    n = min(part, n - skip);
+  }
+  return n;
 }
 
 template <bool BF16, int DP>
@@ -170,20 +183,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&sm->kv_full[s]), 1);
       mbar_init(smem_u32(&sm->kv_empty[s]), 1);
-      mbar_init(smem_u32(&sm->rows_ok[s]), 1);
-      mbar_init(smem_u32(&sm->rows_free[s]), 8);
+      mbar_init(smem_u32(&sm->s_full[s]), 1);
     }
-    mbar_init(smem_u32(&sm->s_full), 1);
-    mbar_init(smem_u32(&sm->p_ready), 8);
+    for (int s = 0; s < kRowSlots; ++s) {
+      mbar_init(smem_u32(&sm->rows_ok[s]), 1);
+      mbar_init(smem_u32(&sm->rows_free[s]), 16);
+    }
+    mbar_init(smem_u32(&sm->p_ready), 16);
     mbar_init(smem_u32(&sm->dp_full), 1);
-    mbar_init(smem_u32(&sm->ds_ready), 8);
+    mbar_init(smem_u32(&sm->ds_ready), 16);
     mbar_init(smem_u32(&sm->acc_full), 1);
     mbar_init(smem_u32(&sm->drained), 1);
-    sm->slots.init(11);
+    sm->slots.init(19);  // 16 warps for the weights, loads, products, ends
     sm->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(smem_u32(&sm->tmem), 512);
     tmem_relinquish();
   }
@@ -198,11 +213,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   grid_wait();     // the plan and the statistics
   grid_release();  // gq's kernel needs no more than these either
   const uint32_t tmem = sm->tmem;
-  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+  // To 64 values there is room for a second S, so that the next tile's is made
+  // ahead; else S waits for the product that reads P over it.
+  constexpr int SB = DP == 64 ? 2 : 1;
+  const uint32_t t_s = tmem, t_dp = tmem + SB * 128, t_dv = t_dp + 128, t_dk = t_dv + DP;
   const int units = __ldcg(p.header) * p.heads_kv;
 
-  if (warp == 8) {
+  if (warp == 16) {
     // =========================================================== loads
+    regs_drop<kKvSideRegs>();
     if (lane == 0) {
       ItemRing ring(&sm->slots);
       AttnItem it;
@@ -250,8 +269,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!mbar_wait_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ======================================================== products
+    regs_drop<kKvSideRegs>();
     const int dn = (p.d + 15) & ~15;
     const int ksteps = dn / 16;
     const uint32_t id_s = make_idesc(BF16, 128, 128);
@@ -261,6 +281,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t row_lo = static_cast<uint32_t>(smem_desc(srow, 1024, 2));
     const uint32_t rowt_lo = static_cast<uint32_t>(dt), rowt_hi = static_cast<uint32_t>(dt >> 32);
     constexpr uint32_t T16 = TILE >> 4;
+    const uint32_t tb = of_warp(tmem);
+    const uint32_t u_s = tb, u_dp = tb + SB * 128, u_dv = u_dp + 128, u_dk = u_dv + DP;
     ItemRing ring(&sm->slots);
     AttnItem it;
     int head;
@@ -268,64 +290,63 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     RingPos<S> cur;  // the row tile's Q; its gout is the next stage
     while (ring.next(&it, &head, abort_flag, true)) {
       int first;
-      const int n = row_tiles(p, it, &first);
+      const int n = of_warp(row_tiles(p, it, &first));
       if (n == 0) continue;
       const uint32_t b = nkv % KVB;
       bool ok = mbar_wait_inl(smem_u32(&sm->kv_full[b]), (nkv / KVB) & 1);
       ++nkv;
-      // a row tile's copies have landed and its rows are in order
-      auto rows = [&](const RingPos<S>& at) {
-        ok = ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph) &&
-             mbar_wait_inl(smem_u32(&sm->full[at.st + 1]), at.ph) &&
-             mbar_wait_inl(smem_u32(&sm->rows_ok[nr & 1]), (nr >> 1) & 1);
-        ++nr;
-        ok = __all_sync(0xffffffffu, ok);
-        tc_fence_after();
-      };
-      rows(cur);
-      if (ok && elect_lane()) {
-        product_rows<DP>(t_s, kv_lo + 2 * b * T16, row_lo + cur.st * T16, hi, id_s, ksteps);
-        tc_commit(smem_u32(&sm->s_full));
-        product_rows<DP>(t_dp, kv_lo + (2 * b + 1) * T16, row_lo + (cur.st + 1) * T16, hi, id_s, ksteps);
-        tc_commit(smem_u32(&sm->dp_full));
-      }
-      __syncwarp();
-      for (int i = 0; i < n && ok; ++i, ++np) {
-        const bool more = i + 1 < n;
-        RingPos<S> nxt = cur;
-        nxt.step();
-        nxt.step();
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->p_ready), np & 1));
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_lane()) product_cols<0, 8>(t_dv, t_s, 32, rowt_lo + (cur.st + 1) * T16, rowt_hi, id_a, i > 0);
-        __syncwarp();
-        if (more) {
-          rows(nxt);
-          if (!ok) break;
-          if (elect_lane()) {
-            product_rows<DP>(t_s, kv_lo + 2 * b * T16, row_lo + nxt.st * T16, hi, id_s, ksteps);
-            tc_commit(smem_u32(&sm->s_full));
-          }
-          __syncwarp();
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->ds_ready), np & 1));
-        if (!ok) break;
+      const uint32_t k_at = kv_lo + 2 * b * T16, v_at = k_at + T16;
+      // S of row tile nr, once its copies have landed and its rows are in order
+      // (the statistics' warp has waited for the copies; they are looked at again,
+      // because the products read them by another path)
+      auto scores = [&](const RingPos<S>& at) {
+        ok = ok && mbar_wait2_inl(smem_u32(&sm->rows_ok[nr % kRowSlots]), (nr / kRowSlots) & 1,
+                                  smem_u32(&sm->full[at.st]), at.ph);
         tc_fence_after();
         if (elect_lane()) {
-          product_cols<0, 8>(t_dk, t_dp, 32, rowt_lo + cur.st * T16, rowt_hi, id_a, i > 0);
+          product_rows<DP>(u_s + (SB == 2 ? (nr & 1) * 128 : 0), k_at, row_lo + at.st * T16, hi, id_s, ksteps);
+          tc_commit(smem_u32(&sm->s_full[SB == 2 ? nr & 1 : 0]));
+        }
+        __syncwarp();
+        ++nr;
+      };
+      auto dp = [&](const RingPos<S>& at) {
+        ok = ok && mbar_wait_inl(smem_u32(&sm->full[at.st + 1]), at.ph);
+        tc_fence_after();
+        if (elect_lane()) {
+          product_rows<DP>(u_dp, v_at, row_lo + (at.st + 1) * T16, hi, id_s, ksteps);
+          tc_commit(smem_u32(&sm->dp_full));
+        }
+        __syncwarp();
+      };
+      scores(cur);
+      dp(cur);
+      if (SB == 2 && n > 1) scores(cur.at(2));
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i, ++np) {
+        ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready), np & 1);
+        tc_fence_after();
+        const uint32_t p_at = u_s + (SB == 2 ? (np & 1) * 128 : 0);
+        if (elect_lane()) product_cols<0, 8, true>(u_dv, p_at, rowt_lo + (cur.st + 1) * T16, rowt_hi, id_a, i > 0);
+        __syncwarp();
+        const RingPos<S> nxt = cur.at(2);
+        if (SB == 1 && i + 1 < n) scores(nxt);
+        ok = ok && mbar_wait_inl(smem_u32(&sm->ds_ready), np & 1);
+        tc_fence_after();
+        if (elect_lane()) {
+          product_cols<0, 8, true>(u_dk, u_dp, rowt_lo + cur.st * T16, rowt_hi, id_a, i > 0);
           tc_commit(smem_u32(&sm->empty[cur.st]));
           tc_commit(smem_u32(&sm->empty[cur.st + 1]));
-          if (more) {
-            product_rows<DP>(t_dp, kv_lo + (2 * b + 1) * T16, row_lo + (nxt.st + 1) * T16, hi, id_s, ksteps);
-            tc_commit(smem_u32(&sm->dp_full));
-          } else {
+          if (i + 1 == n) {
             tc_commit(smem_u32(&sm->kv_empty[b]));
             tc_commit(smem_u32(&sm->acc_full));
           }
         }
         __syncwarp();
+        if (i + 1 < n) dp(nxt);
+        if (SB == 2 && i + 2 < n) scores(cur.at(4));
         cur = nxt;
+        ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) {
         sm->abort = 1;
@@ -336,52 +357,59 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
     if (!mbar_wait_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == 18) {
+    regs_drop<kKvSideRegs>();
     if (lane == 0) hand_out(&sm->slots, p.counter, p.items, units, p.heads_kv, abort_flag);
     __syncwarp();
-  } else if (warp == 11) {
+  } else if (warp == 19) {
     // ============================================== row statistics, ends
+    regs_drop<kKvSideRegs>();
     // lse, delta and the causal limit of a tile's rows.  Rows past the
     // sequence's last query belong to someone else: their weight is 0 (lse =
     // +inf) and, the rows being summed over, so must be what they hold.
+    // A tile's values are loaded while the one before it is written.
     ItemRing ring(&sm->slots);
     AttnItem it;
     int head;
     uint32_t nr = 0;
     RingPos<S> cur;
+    int pos[4];       // this lane's rows lane + 32 u: query in the tile, place in stat
+    int64_t off[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = lane + 32 * u;
+      pos[u] = r / p.g;
+      off[u] = static_cast<int64_t>(pos[u]) * p.heads_q + r % p.g;
+    }
     while (ring.next(&it, &head, abort_flag, true)) {
       int first;
       const int n = row_tiles(p, it, &first);
       bool ok = true;
-      for (int i = first; i < first + n && ok; ++i, ++nr, cur.step(), cur.step()) {
-        const uint32_t sl = nr & 1;
-        const int live = min(p.pos, it.n_pos - i * p.pos) * p.g;
-        float2 st[4];
+      const float2* src = p.stat + (static_cast<int64_t>(it.q_row) + first * p.pos) * p.heads_q + head * p.g;
+      float2 st[4];
+      auto load = [&](int i) {  // tile i's rows that belong to the sequence
+        const int live = min(p.pos, it.n_pos - i * p.pos);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          st[u] = pos[u] < live ? __ldcg(src + off[u]) : make_float2(INFINITY, 0.f);
+        src += static_cast<int64_t>(p.pos) * p.heads_q;
+      };
+      if (n > 0) load(first);
+#pragma unroll 1
+      for (int i = first; i < first + n && ok; ++i, ++nr, cur = cur.at(2)) {
+        const uint32_t sl = nr % kRowSlots;
+        ok = mbar_wait_inl(smem_u32(&sm->rows_free[sl]), ((nr / kRowSlots) & 1) ^ 1);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int r = lane + 32 * u;
-          st[u] = make_float2(INFINITY, 0.f);
-          if (r < live) {
-            const int64_t t = static_cast<int64_t>(it.q_row) + i * p.pos + r / p.g;
-            st[u] = __ldcg(p.stat + t * p.heads_q + head * p.g + r % p.g);
-          }
+          sm->nlse2[sl][lane + 32 * u] = -st[u].x;
+          sm->ndelta[sl][lane + 32 * u] = -st[u].y;
+          sm->lim[sl][lane + 32 * u] = it.lim0 + i * p.pos + pos[u];
         }
-        ok = mbar_wait_inl(smem_u32(&sm->rows_free[sl]), ((nr >> 1) & 1) ^ 1);
-        ok = ok && mbar_wait_inl(smem_u32(&sm->full[cur.st]), cur.ph) &&
-             mbar_wait_inl(smem_u32(&sm->full[cur.st + 1]), cur.ph);
+        if (i + 1 < first + n) load(i + 1);
+        ok = ok && mbar_wait2_inl(smem_u32(&sm->full[cur.st]), cur.ph, smem_u32(&sm->full[cur.st + 1]), cur.ph);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          sm->abort = 1;
-          break;
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = lane + 32 * u;
-          sm->lse2[sl][r] = st[u].x;
-          sm->delta[sl][r] = st[u].y;
-          sm->lim[sl][r] = it.lim0 + i * p.pos + r / p.g;
-        }
-        if (live < used) {
+        const int live = min(p.pos, it.n_pos - i * p.pos) * p.g;
+        if (live < used) [[unlikely]] {
           for (int w = 0; w < 2; ++w)
             for (int c = 0; c < PANELS; ++c) {
               uint8_t* tile = smem + (2 * KVB + cur.st + w) * TILE + c * PANEL;
@@ -393,16 +421,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm->rows_ok[sl]));
       }
-      if (!ok) break;
+      if (!ok) {
+        sm->abort = 1;
+        break;
+      }
     }
     __syncwarp();
   } else {
     // ================================================ weights and dS
-    // A key a lane; warps 0-3 take the rows (columns) 0-63, warps 4-7 the rest.
-    const int half = warp >> 2;
+    regs_raise<kKvMainRegs>();
+    // A key a lane; four warps share 32 keys, 32 rows (columns) each.  Sixteen
+    // warps and not eight, because the steps (reads, exponentials, conversions,
+    // barriers) are chains of latencies.
+    const int quarter = warp >> 2;
     const int key_lane = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t ts = t_s + lane_off + half * 64, tdp = t_dp + lane_off + half * 64;
+    const uint32_t ts = t_s + lane_off + quarter * 32, tdp = t_dp + lane_off + quarter * 32;
     const uint64_t sl2 = pair2(p.scale_log2, p.scale_log2), down = pair2(kPDown<BF16>, kPDown<BF16>);
     ItemRing ring(&sm->slots);
     AttnItem it;
@@ -413,29 +447,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int n = row_tiles(p, it, &first);
       const int key = it.kt0 * kKeyTile + key_lane;
       bool ok = true;
-      for (int i = first; i < first + n; ++i, ++np, ++nr) {
-        const uint32_t sl = nr & 1;
-        ok = mbar_wait_inl(smem_u32(&sm->rows_ok[sl]), (nr >> 1) & 1) &&
-             mbar_wait_inl(smem_u32(&sm->s_full), np & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+#pragma unroll 1
+      for (int i = first; i < first + n && ok; ++i, ++np, ++nr) {
+        const uint32_t sl = nr % kRowSlots;
+        const uint32_t sb = SB == 2 ? np & 1 : 0;
+        ok = mbar_wait2_inl(smem_u32(&sm->rows_ok[sl]), (nr / kRowSlots) & 1, smem_u32(&sm->s_full[sb]),
+                            (SB == 2 ? np >> 1 : np) & 1);
         tc_fence_after();
-        uint32_t x[64], y[64];
-        tmem_ld64_raw(ts, x);
-        const float4* l4 = reinterpret_cast<const float4*>(sm->lse2[sl] + half * 64);
+        uint32_t x[32], y[32], w[16];
+        tmem_ld32_raw(ts + sb * 128, x);
+        const ulonglong2* l4 = reinterpret_cast<const ulonglong2*>(sm->nlse2[sl] + quarter * 32);
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 l = l4[c / 4];
+        for (int c = 0; c < 32; c += 4) {
+          const ulonglong2 l = l4[c / 4];
           float e[4];
-          unpair2(fma2(pair2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, pair2(-l.x, -l.y)), e[0], e[1]);
-          unpair2(fma2(pair2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sl2, pair2(-l.z, -l.w)), e[2], e[3]);
+          unpair2(fma2(pair2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, l.x), e[0], e[1]);
+          unpair2(fma2(pair2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sl2, l.y), e[2], e[3]);
 #pragma unroll
           for (int u = 0; u < 4; ++u) x[c + u] = __float_as_uint(ex2(e[u]));
         }
-        if (p.causal && it.kt0 * kKeyTile + kKeyTile - 1 > it.lim0 + i * p.pos) {
-          const int4* m4 = reinterpret_cast<const int4*>(sm->lim[sl] + half * 64);
+        if (p.causal && it.kt0 * kKeyTile + kKeyTile - 1 > it.lim0 + i * p.pos) [[unlikely]] {
+          const int4* m4 = reinterpret_cast<const int4*>(sm->lim[sl] + quarter * 32);
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
+          for (int c = 0; c < 32; c += 4) {
             const int4 m = m4[c / 4];
             if (key > m.x) x[c] = 0u;
             if (key > m.y) x[c + 1] = 0u;
@@ -444,66 +478,78 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         }
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          y[c] = pack_pair<BF16>(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
-        tmem_st32(ts, y);
+        for (int c = 0; c < 16; ++c)
+          w[c] = pack_pair<BF16>(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+        tmem_st16(ts + sb * 128, w);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm->p_ready));
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->dp_full), np & 1));
-        if (!ok) break;
+        ok = ok && mbar_wait_inl(smem_u32(&sm->dp_full), np & 1);
         tc_fence_after();
-        tmem_ld64_raw(tdp, y);
-        const float4* d4 = reinterpret_cast<const float4*>(sm->delta[sl] + half * 64);
+        tmem_ld32_raw(tdp, y);
+        const ulonglong2* d4 = reinterpret_cast<const ulonglong2*>(sm->ndelta[sl] + quarter * 32);
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 dl = d4[c / 4];
+        for (int c = 0; c < 32; c += 4) {
+          const ulonglong2 dl = d4[c / 4];
           float e[4];
           unpair2(mul2(pair2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
-                       fma2(pair2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), down, pair2(-dl.x, -dl.y))),
+                       fma2(pair2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), down, dl.x)),
                   e[0], e[1]);
           unpair2(mul2(pair2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])),
-                       fma2(pair2(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), down, pair2(-dl.z, -dl.w))),
+                       fma2(pair2(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), down, dl.y)),
                   e[2], e[3]);
-          y[c / 2] = pack_pair<BF16>(e[0], e[1]);
-          y[c / 2 + 1] = pack_pair<BF16>(e[2], e[3]);
+          w[c / 2] = pack_pair<BF16>(e[0], e[1]);
+          w[c / 2 + 1] = pack_pair<BF16>(e[2], e[3]);
         }
-        tmem_st32(tdp, y);
+        tmem_st16(tdp, w);
         tmem_wait_st();
         tc_fence_before();
-        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
         if (lane == 0) {
           mbar_arrive(smem_u32(&sm->ds_ready));
           mbar_arrive(smem_u32(&sm->rows_free[sl]));
         }
       }
+      if (n > 0 && ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->acc_full), na & 1));
+        ++na;
+        tc_fence_after();
+      }
       if (!ok) {
         sm->abort = 1;
         break;
       }
-      if (n > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->acc_full), na & 1))) {
-          sm->abort = 1;
-          break;
-        }
-        ++na;
-        tc_fence_after();
-      }
-      // warps 0-3 write gv, warps 4-7 gk
+      // quarters 0 and 1 write the halves of gv's columns, 2 and 3 gk's
       const bool live = key < it.lk;
-      const int64_t row = static_cast<int64_t>(it.k_row) + key;
-      if (half == 0)
-        store_acc<BF16>(t_dv + lane_off, p.o1 + row * p.o1_t + head * p.o1_h, p.d, kPDown<BF16>, n > 0, live);
-      else
-        store_acc<BF16>(t_dk + lane_off, p.o0 + row * p.o0_t + head * p.o0_h, p.d, p.scale, n > 0, live);
+      const bool is_k = quarter >= 2;
+      const uint32_t acc = (is_k ? t_dk : t_dv) + lane_off;
+      const int split = (p.d / 2 + 15) & ~15;
+      const int c0 = quarter & 1 ? split : 0, c1 = quarter & 1 ? p.d : min(split, p.d);
+      if (it.slot < 0) {
+        const int64_t row = static_cast<int64_t>(it.k_row) + key;
+        uint8_t* dst = is_k ? p.o0 + row * p.o0_t + head * p.o0_h : p.o1 + row * p.o1_t + head * p.o1_h;
+        if (c1 > c0)
+          store_acc<BF16>(acc + c0, dst + c0 * 2, c1 - c0, is_k ? p.scale : kPDown<BF16>, n > 0, live);
+      } else {
+        float* dst = p.part + (((static_cast<int64_t>(it.slot + it.split) * p.heads_kv + head) * 2 + is_k) * 128 +
+                               key_lane) * p.d;
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 16) {
+          uint32_t o[16] = {};
+          if (n > 0) tmem_ld16_raw(acc + c, o);
+#pragma unroll
+          for (int u = 0; u < 16; u += 4)
+            if (live && c + u < p.d) *reinterpret_cast<uint4*>(dst + c + u) = make_uint4(o[u], o[u + 1], o[u + 2], o[u + 3]);
+        }
+      }
       tc_fence_before();
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -513,7 +559,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ------------------------------------------------------------------- gq --
 struct QSmem {
   uint64_t full[kBwdMaxStages], empty[kBwdMaxStages];
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], dp_full, ds_ready, acc_full;
   uint64_t fix_k, k_fixed;
   uint64_t drained;
@@ -533,8 +579,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sq = smem_u32(smem);        // Q and gout
-  const uint32_t skv = sq + 2 * TILE;        // ring: K, V, K, V, ...
-  QSmem* sm = reinterpret_cast<QSmem*>(smem + (2 + S) * TILE);
+  constexpr int QB = q_pairs(DP);
+  const uint32_t skv = sq + 2 * QB * TILE;   // ring: K, V, K, V, ...
+  QSmem* sm = reinterpret_cast<QSmem*>(smem + (2 * QB + S) * TILE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm->abort;
 
@@ -543,20 +590,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(smem_u32(&sm->full[s]), 1);
       mbar_init(smem_u32(&sm->empty[s]), 1);
     }
-    mbar_init(smem_u32(&sm->q_full), 1);
-    mbar_init(smem_u32(&sm->q_empty), 1);
-    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&sm->s_full[s]), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sm->q_full[s]), 1);
+      mbar_init(smem_u32(&sm->q_empty[s]), 1);
+      mbar_init(smem_u32(&sm->s_full[s]), 1);
+    }
     mbar_init(smem_u32(&sm->dp_full), 1);
-    mbar_init(smem_u32(&sm->ds_ready), 8);
+    mbar_init(smem_u32(&sm->ds_ready), 16);
     mbar_init(smem_u32(&sm->acc_full), 1);
     mbar_init(smem_u32(&sm->fix_k), 1);
     mbar_init(smem_u32(&sm->k_fixed), 1);
     mbar_init(smem_u32(&sm->drained), 1);
-    sm->slots.init(11);
+    sm->slots.init(19);  // 16 warps for the weights, loads, products, ends
     sm->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(smem_u32(&sm->tmem), 512);
     tmem_relinquish();
   }
@@ -568,7 +617,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;
   const int units = __ldcg(p.header) * p.heads_kv;
 
-  if (warp == 8) {
+  if (warp == 16) {
     // =========================================================== loads
     if (lane == 0) {
       ItemRing ring(&sm->slots);
@@ -578,15 +627,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       RingPos<S> r;
       while (ring.next(&it, &head, abort_flag, false)) {
         if (it.kt1 == 0) continue;
-        if (!mbar_wait_inl(smem_u32(&sm->q_empty), (nq & 1) ^ 1)) {
+        const uint32_t b = nq % QB;
+        if (!mbar_wait_inl(smem_u32(&sm->q_empty[b]), ((nq / QB) & 1) ^ 1)) {
           sm->abort = 1;
           break;
         }
         ++nq;
-        mbar_arrive_expect_tx(smem_u32(&sm->q_full), 2 * PANELS * p.pos * p.g * 128);
+        mbar_arrive_expect_tx(smem_u32(&sm->q_full[b]), 2 * PANELS * p.pos * p.g * 128);
         for (int c = 0; c < PANELS; ++c) {
-          tma_load_3d(sq + c * PANEL, &qmap, c * 64, head * p.g, it.q_row, smem_u32(&sm->q_full));
-          tma_load_3d(sq + TILE + c * PANEL, &gmap, c * 64, head * p.g, it.q_row, smem_u32(&sm->q_full));
+          tma_load_3d(sq + 2 * b * TILE + c * PANEL, &qmap, c * 64, head * p.g, it.q_row, smem_u32(&sm->q_full[b]));
+          tma_load_3d(sq + (2 * b + 1) * TILE + c * PANEL, &gmap, c * 64, head * p.g, it.q_row,
+                      smem_u32(&sm->q_full[b]));
         }
         bool ok = true;
         for (int j = 0; j < it.kt1 && ok; ++j)
@@ -604,13 +655,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         if (!ok) break;
       }
-      if (nq > 0 && !mbar_wait_inl(smem_u32(&sm->q_full), (nq - 1) & 1)) sm->abort = 1;
+      const uint32_t f0 = nq > QB ? nq - QB : 0;
+      for (uint32_t i = f0; i < nq; ++i)
+        if (!mbar_wait_inl(smem_u32(&sm->q_full[i % QB]), (i / QB) & 1)) sm->abort = 1;
       const uint32_t f1 = k > S ? k - S : 0;
       for (uint32_t i = f1; i < k; ++i)
         if (!mbar_wait_inl(smem_u32(&sm->full[i % S]), (i / S) & 1)) sm->abort = 1;
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ======================================================== products
     const int dn = (p.d + 15) & ~15;
     const int ksteps = dn / 16;
@@ -621,78 +674,71 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t q_lo = static_cast<uint32_t>(smem_desc(sq, 1024, 2));
     const uint32_t kt_lo = static_cast<uint32_t>(dt), kt_hi = static_cast<uint32_t>(dt >> 32);
     constexpr uint32_t T16 = TILE >> 4;
+    const uint32_t tb = of_warp(tmem);
+    const uint32_t u_s = tb, u_dp = tb + 256, u_dq = tb + 384;
     ItemRing ring(&sm->slots);
     AttnItem it;
     int head;
     uint32_t nq = 0, nd = 0, nfix = 0, nbuf = 0;
-    RingPos<S> rs, rd;  // next tile's K for S (its V one stage on); tile in hand
+    RingPos<S> rd;  // K of the tile in hand; its V is the next stage
     while (ring.next(&it, &head, abort_flag, true)) {
-      const int n = it.kt1;
+      const int n = of_warp(it.kt1), lk = of_warp(it.lk);
       if (n == 0) continue;
-      bool ok = mbar_wait_inl(smem_u32(&sm->q_full), nq & 1);
+      const uint32_t qb = nq % QB, q_at = q_lo + 2 * qb * T16;
+      bool ok = mbar_wait_inl(smem_u32(&sm->q_full[qb]), (nq / QB) & 1);
       ++nq;
       // S of key tile j into its buffer; the tile's rows past the keys are zeroed first
-      auto scores = [&](int j) {
-        ok = ok && mbar_wait_inl(smem_u32(&sm->full[rs.st]), rs.ph);
-        if (it.lk - j * kKeyTile < kKeyTile) {
-          if (lane == 0 && ok) {
-            sm->fix_at = static_cast<int>(rs.st);
-            sm->fix_rows = it.lk - j * kKeyTile;
+      auto scores = [&](int j, const RingPos<S>& at) {
+        ok = ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph);
+        if (lk - j * kKeyTile < kKeyTile) {
+          if (lane == 0) {
+            sm->fix_at = static_cast<int>(at.st);
+            sm->fix_rows = lk - j * kKeyTile;
             mbar_arrive(smem_u32(&sm->fix_k));
           }
           ok = ok && mbar_wait_inl(smem_u32(&sm->k_fixed), nfix & 1);
           ++nfix;
         }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
         tc_fence_after();
         if (elect_lane()) {
-          product_rows<DP>(t_s + (nbuf & 1) * 128, q_lo, kv_lo + rs.st * T16, hi, id_s, ksteps);
+          product_rows<DP>(u_s + (nbuf & 1) * 128, q_at, kv_lo + at.st * T16, hi, id_s, ksteps);
           tc_commit(smem_u32(&sm->s_full[nbuf & 1]));
         }
         __syncwarp();
         ++nbuf;
-        rs.step();
-        rs.step();
       };
       // dP of the tile whose V lies at `at`, which is then done with
       auto dp = [&](const RingPos<S>& at) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph));
-        if (!ok) return;
+        ok = ok && mbar_wait_inl(smem_u32(&sm->full[at.st]), at.ph);
         tc_fence_after();
         if (elect_lane()) {
-          product_rows<DP>(t_dp, q_lo + T16, kv_lo + at.st * T16, hi, id_s, ksteps);
+          product_rows<DP>(u_dp, q_at + T16, kv_lo + at.st * T16, hi, id_s, ksteps);
           tc_commit(smem_u32(&sm->dp_full));
           tc_commit(smem_u32(&sm->empty[at.st]));
         }
         __syncwarp();
       };
-      scores(0);
-      RingPos<S> v = rd;
-      v.step();
-      dp(v);
-      if (n > 1) scores(1);
+      scores(0, rd);
+      dp(rd.at(1));
+      if (n > 1) scores(1, rd.at(2));
+#pragma unroll 1
       for (int j = 0; j < n && ok; ++j, ++nd) {
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->ds_ready), nd & 1));
-        if (!ok) break;
+        ok = ok && mbar_wait_inl(smem_u32(&sm->ds_ready), nd & 1);
+        // dS lies over its S, so dP of the next tile comes first: it is waited for
+        if (j + 1 < n) dp(rd.at(3));
         tc_fence_after();
         if (elect_lane()) {
-          product_cols<0, 8>(t_dq, t_dp, 32, kt_lo + rd.st * T16, kt_hi, id_a, j > 0);
+          product_cols<0, 8, true>(u_dq, u_s + (nd & 1) * 128, kt_lo + rd.st * T16, kt_hi, id_a, j > 0);
           tc_commit(smem_u32(&sm->empty[rd.st]));
           if (j + 1 == n) {
-            tc_commit(smem_u32(&sm->q_empty));
+            tc_commit(smem_u32(&sm->q_empty[qb]));
             tc_commit(smem_u32(&sm->acc_full));
           }
         }
         __syncwarp();
-        rd.step();
-        rd.step();
-        if (j + 1 < n) {
-          v = rd;
-          v.step();
-          dp(v);
-        }
-        if (j + 2 < n) scores(j + 2);
+        if (j + 2 < n) scores(j + 2, rd.at(4));
+        rd = rd.at(2);
+        ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) {
         sm->abort = 1;
@@ -703,10 +749,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
     if (!mbar_wait_inl(smem_u32(&sm->drained), 0)) sm->abort = 1;
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     if (lane == 0) hand_out(&sm->slots, p.counter, p.items, units, p.heads_kv, abort_flag);
     __syncwarp();
-  } else if (warp == 11) {
+  } else if (warp == 19) {
     // ==================================================== tail of K
     ItemRing ring(&sm->slots);
     AttnItem it;
@@ -720,7 +766,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       ++n;
       const int rows = sm->fix_rows;
-      uint8_t* tile = smem + (2 + sm->fix_at) * TILE;
+      uint8_t* tile = smem + (2 * QB + sm->fix_at) * TILE;
       for (int c = 0; c < PANELS; ++c)
         for (int i = rows * 8 + lane; i < kKeyTile * 8; i += 32)
           *reinterpret_cast<uint4*>(tile + c * PANEL + i * 16) = make_uint4(0, 0, 0, 0);
@@ -731,11 +777,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
   } else {
     // ========================================================= dS
-    // A row a lane; warps 0-3 take the keys (columns) 0-63 of a tile, 4-7 the rest.
-    const int half = warp >> 2;
+    // A row a lane; four warps share 32 rows, 32 keys (columns) of a tile each.
+    const int quarter = warp >> 2;
     const int row = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;
-    const uint32_t tdp = t_dp + lane_off + half * 64;
+    const uint32_t tdp = t_dp + lane_off + quarter * 32;
     const int pos = row / p.g, gh = row - pos * p.g;
     const uint64_t sl2 = pair2(p.scale_log2, p.scale_log2), down = pair2(kPDown<BF16>, kPDown<BF16>);
     ItemRing ring(&sm->slots);
@@ -752,77 +798,105 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (live) st = __ldcg(p.stat + tok * p.heads_q + h);
       const uint64_t nl = pair2(-st.x, -st.x), ndl = pair2(-st.y, -st.y);
       bool ok = true;
-      for (int j = 0; j < n; ++j, ++nd) {
+#pragma unroll 1
+      for (int j = 0; j < n && ok; ++j, ++nd) {
         const uint32_t b = nd & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->s_full[b]), (nd >> 1) & 1));
-        if (!ok) break;
+        ok = mbar_wait_inl(smem_u32(&sm->s_full[b]), (nd >> 1) & 1);
         tc_fence_after();
-        uint32_t x[64], y[64];
-        tmem_ld64_raw(t_s + b * 128 + lane_off + half * 64, x);
+        uint32_t x[32], y[32], w[16];
+        tmem_ld32_raw(t_s + b * 128 + lane_off + quarter * 32, x);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
+        for (int c = 0; c < 32; c += 2) {
           float e0, e1;
           unpair2(fma2(pair2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, nl), e0, e1);
           x[c] = __float_as_uint(ex2(e0));
           x[c + 1] = __float_as_uint(ex2(e1));
         }
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->dp_full), nd & 1));
-        if (!ok) break;
+        ok = ok && mbar_wait_inl(smem_u32(&sm->dp_full), nd & 1);
         tc_fence_after();
-        tmem_ld64_raw(tdp, y);
+        tmem_ld32_raw(tdp, y);
+        const int seen = vis - j * kKeyTile - quarter * 32;
+        if (__any_sync(0xffffffffu, seen < 32)) [[unlikely]] {  // both to zero: V may hold anything there
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
+          for (int c = 0; c < 32; ++c)
+            if (c >= seen) x[c] = y[c] = 0u;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
           float e0, e1;
           unpair2(mul2(pair2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
                        fma2(pair2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), down, ndl)),
                   e0, e1);
-          x[c] = __float_as_uint(e0);
-          x[c + 1] = __float_as_uint(e1);
+          w[c / 2] = pack_pair<BF16>(e0, e1);
         }
-        const int seen = vis - j * kKeyTile - half * 64;
-        if (__any_sync(0xffffffffu, seen < 64)) {  // selected, not multiplied: V may hold anything there
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c >= seen) x[c] = 0u;
-        }
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          y[c] = pack_pair<BF16>(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
-        tmem_st32(tdp, y);
+        tmem_st16(t_s + b * 128 + lane_off + quarter * 32, w);
         tmem_wait_st();
         tc_fence_before();
-        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
         if (lane == 0) mbar_arrive(smem_u32(&sm->ds_ready));
+      }
+      if (n > 0 && ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->acc_full), na & 1));
+        ++na;
+        tc_fence_after();
       }
       if (!ok) {
         sm->abort = 1;
         break;
       }
-      if (n > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->acc_full), na & 1))) {
-          sm->abort = 1;
-          break;
-        }
-        ++na;
-        tc_fence_after();
-      }
-      // each half writes the columns of its half
-      const int c0 = half ? (p.d / 2 + 15) / 16 * 16 : 0;
-      const int c1 = half ? p.d : min(p.d, (p.d / 2 + 15) / 16 * 16);
-      if (c1 > c0)
-        store_acc<BF16>(t_dq + lane_off + c0, p.o0 + tok * p.o0_t + h * p.o0_h + c0 * 2, c1 - c0, p.scale, n > 0, live);
+      // each quarter writes its columns, 16 at a time
+#pragma unroll 1
+      for (int c = quarter * 16; c < p.d; c += 64)
+        store_acc<BF16>(t_dq + lane_off + c, p.o0 + tok * p.o0_t + h * p.o0_h + c * 2, min(16, p.d - c), p.scale, n > 0,
+                        live);
       tc_fence_before();
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
   grid_wait();  // done only when gk's kernel is
   if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, kDevErrTimeout);
+}
+
+// gk and gv of the key tiles whose rows were cut: the parts' sums in order, four
+// values a lane.
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_attn_bwd_join(const BwdParams p, const AttnItem* joins) {
+  grid_wait();
+  const int n = __ldcg(p.header + 2);
+  const int lanes = p.d / 4;  // of a row
+  const int64_t step = static_cast<int64_t>(p.heads_kv) * 256 * p.d;
+  const int64_t total = static_cast<int64_t>(n) * p.heads_kv * 256 * lanes;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u < total;
+       u += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = u / lanes;
+    const int c = static_cast<int>(u - r * lanes) * 4, row = static_cast<int>(r & 127), is_k = (r >> 7) & 1;
+    const int64_t jh = r >> 8;
+    const int head = static_cast<int>(jh % p.heads_kv);
+    const AttnItem* it = joins + jh / p.heads_kv;
+    const int key = it->kt0 * kKeyTile + row;
+    if (key >= it->lk) continue;
+    const float* src = p.part + (((static_cast<int64_t>(it->slot) * p.heads_kv + head) * 2 + is_k) * 128 + row) * p.d + c;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int q = 0; q < it->nsplit; ++q) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src + q * step));
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+    const float f = is_k ? p.scale : kPDown<BF16>;
+    const int64_t t = static_cast<int64_t>(it->k_row) + key;
+    uint8_t* dst = is_k ? p.o0 + t * p.o0_t + head * p.o0_h : p.o1 + t * p.o1_t + head * p.o1_h;
+    *reinterpret_cast<uint2*>(dst + c * 2) =
+        make_uint2(pack_pair<BF16>(a.x * f, a.y * f), pack_pair<BF16>(a.z * f, a.w * f));
+  }
 }
 
 template <bool BF16>
@@ -861,8 +935,15 @@ sc_status attn_bwd(const AttnArgs& a) {
   Arena ar;
   const size_t o_hq = ar.take(kPlanHeader * sizeof(int)), o_hk = ar.take(kPlanHeader * sizeof(int));
   const size_t o_iq = ar.take(static_cast<size_t>(q_items) * sizeof(AttnItem));
-  const size_t o_ik = ar.take(static_cast<size_t>(k_items) * sizeof(AttnItem));
+  const int64_t k_cap = k_items + (k_items * a.heads_kv <= 8ll * sms ? 8ll * sms / a.heads_kv + 2 : 0);
+  const size_t o_ik = ar.take(static_cast<size_t>(k_cap) * sizeof(AttnItem));
   const size_t o_st = ar.take(static_cast<size_t>(a.t_q) * a.heads_q * sizeof(float2));
+  // Partial gk and gv: room for eight an SM where the key tiles are few (the plan
+  // makes about four).
+  const bool cut = k_items * a.heads_kv <= 8ll * sms;
+  const int64_t slots = cut ? 8ll * sms / a.heads_kv + 2 : 0;
+  const size_t o_joins = ar.take(cut ? static_cast<size_t>(k_items) * sizeof(AttnItem) : 0);
+  const size_t o_part = ar.take(static_cast<size_t>(slots) * a.heads_kv * 256 * a.head_dim * sizeof(float));
   int* status = attn_status_word();
   if (!status) return set_error(SC_ERR_CUDA, "the attention status word is not available");
   const int dp = a.head_dim <= 64 ? 64 : 128;
@@ -870,8 +951,10 @@ sc_status attn_bwd(const AttnArgs& a) {
   const void* kk = bf ? kv_kernel<true>(dp) : kv_kernel<false>(dp);
   const void* kq = bf ? q_kernel<true>(dp) : q_kernel<false>(dp);
   const size_t kv_smem = (2 * kv_pairs(dp) + kv_stages(dp)) * tile + sizeof(KvSmem) + 1024;
-  const size_t q_smem = (2 + q_stages(dp)) * tile + sizeof(QSmem) + 1024;
-  sc_status st = kernel_setup(kk, kv_smem, nullptr);
+  const size_t q_smem = (2 * q_pairs(dp) + q_stages(dp)) * tile + sizeof(QSmem) + 1024;
+  int regs = 0;
+  sc_status st = kernel_setup(kk, kv_smem, &regs);
+  if (!st && regs != kKvRegs) st = set_error(SC_ERR_CUDA, "attention kernel: not the registers it was written for");
   if (!st) st = kernel_setup(kq, q_smem, nullptr);
   if (st) return st;
   const bool have_q = a.t_q > 0, have_k = a.t_k > 0;
@@ -906,7 +989,12 @@ sc_status attn_bwd(const AttnArgs& a) {
   plq.header = reinterpret_cast<int*>(base + o_hq);
   plq.items = reinterpret_cast<AttnItem*>(base + o_iq);
   plk.mode = kPlanKeys;
-  plk.cap = static_cast<int>(k_items);
+  plk.cap = static_cast<int>(k_cap);
+  plk.part_rows = slots * a.heads_kv * kKeyTile;
+  plk.over = 4;
+  plk.min_tiles = 8;
+  plk.join_cap = cut ? static_cast<int>(k_items) : 0;
+  plk.joins = reinterpret_cast<AttnItem*>(base + o_joins);
   plk.header = reinterpret_cast<int*>(base + o_hk);
   plk.items = reinterpret_cast<AttnItem*>(base + o_ik);
   cudaError_t e = cudaSuccess;
@@ -939,6 +1027,7 @@ sc_status attn_bwd(const AttnArgs& a) {
     if (e != cudaSuccess) st = set_cuda_error(e, "attn_stat");
   }
   if (!st) st = attn_plan(plk, &plq, have_q, a.stream);
+  BwdParams joined = p;
   if (!st && have_k) {
     BwdParams pk = p;
     pk.header = plk.header;
@@ -950,12 +1039,14 @@ sc_status attn_bwd(const AttnArgs& a) {
     pk.o1 = static_cast<uint8_t*>(a.gv.data);
     pk.o1_t = a.gv.token_stride * 2;
     pk.o1_h = a.gv.head_stride * 2;
-    const int64_t most = k_items * a.heads_kv;
+    pk.part = reinterpret_cast<float*>(base + o_part);
+    const int64_t most = k_cap * a.heads_kv;
     void* args[] = {&pk, &qm, &gm, &km, &vm};
     SC_LAUNCH("attn_bwd_kv", a.stream,
               (e = launch_after(kk, static_cast<unsigned>(most < sms ? most : sms), kBwdThreads, kv_smem, a.stream,
                                 args)));
     if (e != cudaSuccess) st = set_cuda_error(e, "attn_bwd_kv");
+    joined = pk;
   }
   if (!st && have_q) {
     BwdParams pq = p;
@@ -972,6 +1063,14 @@ sc_status attn_bwd(const AttnArgs& a) {
               (e = launch_after(kq, static_cast<unsigned>(most < sms ? most : sms), kBwdThreads, q_smem, a.stream,
                                 args)));
     if (e != cudaSuccess) st = set_cuda_error(e, "attn_bwd_q");
+  }
+  if (!st && have_k && cut) {  // after gq's kernel, which outlasts gk's
+    const AttnItem* joins = plk.joins;
+    void* args[] = {&joined, &joins};
+    const void* kj = bf ? reinterpret_cast<const void*>(k_attn_bwd_join<true>)
+                        : reinterpret_cast<const void*>(k_attn_bwd_join<false>);
+    SC_LAUNCH("attn_bwd_join", a.stream, (e = launch_after(kj, 4 * sms, 256, 0, a.stream, args)));
+    if (e != cudaSuccess) st = set_cuda_error(e, "attn_bwd_join");
   }
   dev_free(ws, a.stream);
   return st;

@@ -87,14 +87,14 @@ __device__ __forceinline__ void product_rows(uint32_t d, uint32_t a_lo, uint32_t
     if (i < ksteps) tc_mma_lohi(d, a_lo + off, b_lo + off, hi, idesc, i > 0);
   }
 }
-// D (+)= A B over N steps of 16 rows of a tile from step I0 on; A lies in TMEM,
-// `gap` extra columns apart from step 4 on.
-template <int I0, int N>
-__device__ __forceinline__ void product_cols(uint32_t d, uint32_t a, int gap, uint32_t b_lo, uint32_t b_hi,
-                                             uint32_t idesc, bool add) {
+// D (+)= A B over N steps of 16 rows of a tile from step I0 on.  A lies in TMEM,
+// 8 columns a step; QUARTERS: two steps at the start of every 32 columns.
+template <int I0, int N, bool QUARTERS = false>
+__device__ __forceinline__ void product_cols(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                             bool add) {
 #pragma unroll
   for (int i = I0; i < I0 + N; ++i)
-    tc_mma_ts_lohi(d, a + i * 8 + (i >= 4 ? gap : 0), b_lo + i * (2048 >> 4), b_hi, idesc, add || i > 0);
+    tc_mma_ts_lohi(d, a + i * 8 + (QUARTERS ? (i >> 1) * 16 : 0), b_lo + i * (2048 >> 4), b_hi, idesc, add || i > 0);
 }
 
 // A ring's place: stage and how often it came round.

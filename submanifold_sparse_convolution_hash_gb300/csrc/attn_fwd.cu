@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             np ^= 1u << h;
             tc_fence_after();
             if (elect_lane()) {
-              product_cols<0, 8>(oc, pc, 0, vv, v_hi, id_o, t > (dual ? h : 0));
+              product_cols<0, 8>(oc, pc, vv, v_hi, id_o, t > (dual ? h : 0));
               if (EARLY || !more) tc_commit(smem_u32(&sm->o_full[h]));
               if (dual || h || t >= e1) tc_commit(smem_u32(&sm->empty[v.st]));  // its last reader
             }
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][0]), np & 1);
             if constexpr (!EARLY) {  // the product begins with half of the keys
               tc_fence_after();
-              if (elect_lane()) product_cols<0, 4>(to, tp, 0, vv, v_hi, id_o, t > 0);
+              if (elect_lane()) product_cols<0, 4>(to, tp, vv, v_hi, id_o, t > 0);
               __syncwarp();
               ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][1]), np & 1);
             }
@@ -336,8 +336,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             };
             if (EARLY && more) scores();
             if (cur) {
-              if constexpr (EARLY) product_cols<0, 8>(to, tp, 0, vv, v_hi, id_o, t > 0);
-              else product_cols<4, 4>(to, tp, 0, vv, v_hi, id_o, true);
+              if constexpr (EARLY) product_cols<0, 8>(to, tp, vv, v_hi, id_o, t > 0);
+              else product_cols<4, 4>(to, tp, vv, v_hi, id_o, true);
               if (EARLY || !more) tc_commit(smem_u32(&sm->o_full[s]));
               tc_commit(smem_u32(&sm->empty[v.st]));
             }
@@ -674,6 +674,7 @@ sc_status attn_fwd(const AttnArgs& a) {
   pl.mode = kPlanRows;
   pl.g = g;
   pl.sms = sms;
+  pl.over = 4;
   pl.part_rows = part_rows;
   pl.min_tiles = 4;
   pl.dual = one;

@@ -47,6 +47,7 @@ struct PlanArgs {
   int heads_kv;
   int mode;
   int sms;
+  int over;           // parts an SM that a short list is cut into
   int64_t part_rows;  // rows of partial results that fit; 0: the keys are never cut
   int min_tiles;      // least key tiles of a part
   int dual;           // items of one row tile may be worked on by both halves
