@@ -863,28 +863,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, kDevErrTimeout);
 }
 
-// gk and gv of the key tiles whose rows were cut: the parts' sums in order, four
-// values a lane.
+// gk and gv of the key tiles whose rows were cut: the parts' sums in order, a
+// row a warp, four values a lane.
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_attn_bwd_join(const BwdParams p, const AttnItem* joins) {
   grid_wait();
-  const int n = __ldcg(p.header + 2);
-  const int lanes = p.d / 4;  // of a row
+  const int n = __ldcg(p.header + 2) * p.heads_kv * 32;  // eight rows of one of the two a block
+  const int c = (threadIdx.x & 31) * 4;
   const int64_t step = static_cast<int64_t>(p.heads_kv) * 256 * p.d;
-  const int64_t total = static_cast<int64_t>(n) * p.heads_kv * 256 * lanes;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u < total;
-       u += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = u / lanes;
-    const int c = static_cast<int>(u - r * lanes) * 4, row = static_cast<int>(r & 127), is_k = (r >> 7) & 1;
-    const int64_t jh = r >> 8;
-    const int head = static_cast<int>(jh % p.heads_kv);
-    const AttnItem* it = joins + jh / p.heads_kv;
-    const int key = it->kt0 * kKeyTile + row;
-    if (key >= it->lk) continue;
+  for (int u = blockIdx.x; u < n; u += gridDim.x) {
+    const int jh = u >> 5, row = (u & 15) * 8 + (threadIdx.x >> 5), is_k = (u >> 4) & 1;
+    const int j = jh / p.heads_kv, head = jh - j * p.heads_kv;
+    const AttnItem* it = joins + j;
+    const int key = it->kt0 * kKeyTile + row, parts = it->nsplit;
+    if (key >= it->lk || c >= p.d) continue;
     const float* src = p.part + (((static_cast<int64_t>(it->slot) * p.heads_kv + head) * 2 + is_k) * 128 + row) * p.d + c;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int q = 0; q < it->nsplit; ++q) {
+    for (int q = 0; q < parts; ++q) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(src + q * step));
       a.x += v.x;
       a.y += v.y;
@@ -935,13 +931,13 @@ sc_status attn_bwd(const AttnArgs& a) {
   Arena ar;
   const size_t o_hq = ar.take(kPlanHeader * sizeof(int)), o_hk = ar.take(kPlanHeader * sizeof(int));
   const size_t o_iq = ar.take(static_cast<size_t>(q_items) * sizeof(AttnItem));
-  const int64_t k_cap = k_items + (k_items * a.heads_kv <= 8ll * sms ? 8ll * sms / a.heads_kv + 2 : 0);
+  const int64_t k_cap = k_items + (k_items * a.heads_kv <= 8ll * sms ? 2ll * sms / a.heads_kv + 2 : 0);
   const size_t o_ik = ar.take(static_cast<size_t>(k_cap) * sizeof(AttnItem));
   const size_t o_st = ar.take(static_cast<size_t>(a.t_q) * a.heads_q * sizeof(float2));
-  // Partial gk and gv: room for eight an SM where the key tiles are few (the plan
-  // makes about four).
+  // Partial gk and gv: room for two an SM where the key tiles are few (the plan
+  // cuts those that are dearer than an SM's share).
   const bool cut = k_items * a.heads_kv <= 8ll * sms;
-  const int64_t slots = cut ? 8ll * sms / a.heads_kv + 2 : 0;
+  const int64_t slots = cut ? 2ll * sms / a.heads_kv + 2 : 0;
   const size_t o_joins = ar.take(cut ? static_cast<size_t>(k_items) * sizeof(AttnItem) : 0);
   const size_t o_part = ar.take(static_cast<size_t>(slots) * a.heads_kv * 256 * a.head_dim * sizeof(float));
   int* status = attn_status_word();
@@ -991,7 +987,7 @@ sc_status attn_bwd(const AttnArgs& a) {
   plk.mode = kPlanKeys;
   plk.cap = static_cast<int>(k_cap);
   plk.part_rows = slots * a.heads_kv * kKeyTile;
-  plk.over = 4;
+  plk.over = 1;
   plk.min_tiles = 8;
   plk.join_cap = cut ? static_cast<int>(k_items) : 0;
   plk.joins = reinterpret_cast<AttnItem*>(base + o_joins);

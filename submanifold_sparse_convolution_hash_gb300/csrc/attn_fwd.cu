@@ -579,18 +579,32 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Attn
     float l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     const bool on = lane * 4 < p.d;
-#pragma unroll 4
-    for (int q = 0; q < parts; ++q) {
-      const float mq = __ldcg(src + q * step + p.d);
-      const float f = mq == -INFINITY ? 0.f : step_down(mq, m, base_of(mq, p.scale_log2), base, p.scale_log2);
-      l += __ldcg(src + q * step + p.d + 1) * f;
-      // nothing seen in this part: no O was written
-      const float4 o = on && mq != -INFINITY ? __ldcg(reinterpret_cast<const float4*>(src + q * step) + lane)
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
-      a.x = fmaf(o.x, f, a.x);
-      a.y = fmaf(o.y, f, a.y);
-      a.z = fmaf(o.z, f, a.z);
-      a.w = fmaf(o.w, f, a.w);
+    for (int q0 = 0; q0 < parts; q0 += 32) {
+      // a part's factor a lane; 0 where it saw nothing (no O was written then)
+      float f = 0.f, lq = 0.f;
+      bool seen = false;
+      if (q0 + lane < parts) {
+        const float mq = __ldcg(src + (q0 + lane) * step + p.d);
+        lq = __ldcg(src + (q0 + lane) * step + p.d + 1);
+        seen = mq != -INFINITY;
+        f = !seen ? 0.f : step_down(mq, m, base_of(mq, p.scale_log2), base, p.scale_log2);
+      }
+      const uint32_t have = __ballot_sync(0xffffffffu, seen);
+      lq *= f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) lq += __shfl_xor_sync(0xffffffffu, lq, o);
+      l += lq;
+      const int cnt = min(32, parts - q0);
+#pragma unroll 8
+      for (int q = 0; q < cnt; ++q) {
+        const float fq = __shfl_sync(0xffffffffu, f, q);
+        const float4 o = on && (have >> q & 1) ? __ldcg(reinterpret_cast<const float4*>(src + (q0 + q) * step) + lane)
+                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        a.x = fmaf(o.x, fq, a.x);
+        a.y = fmaf(o.y, fq, a.y);
+        a.z = fmaf(o.z, fq, a.z);
+        a.w = fmaf(o.w, fq, a.w);
+      }
     }
     const int vis = p.causal ? min(it->lk, it->lim0 + i + 1) : it->lk;
     const float inv = vis > 0 ? 1.f / l : 0.f;
