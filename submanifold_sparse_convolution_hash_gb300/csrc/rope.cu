@@ -275,12 +275,21 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_rope_fwd(c
   constexpr int NW = Vec8<T>::kWords, U = sizeof(T) == 4 ? kRows / 2 : kRows;
   __shared__ __align__(16) T s_stage[PAIRING >= kHalf2 ? kThreads * 8 : 8];
   __shared__ float2 s_table[kThreads * 4];
+  __shared__ __align__(16) float s_w[NORM ? 2 : 1][2][NORM ? LPR * 8 : 4];  // [side][a value's, its partner's][value]
   T* stage = s_stage + (PAIRING >= kHalf2 ? (threadIdx.x >> 5) * 256 : 0);
   const int gl = threadIdx.x % LPR;
   const int e0 = gl * 8;
   const float inv_d = 1.f / static_cast<float>(p.d);
   const Unit u = unit_of<LPR>(p, blockIdx.x);
   const bool act = u.on && e0 < p.d;
+  if constexpr (NORM) {
+    for (int i = threadIdx.x; i < 4 * LPR * 8; i += kThreads) {
+      const int side = i / (2 * LPR * 8), which = i / (LPR * 8) & 1, e = i % (LPR * 8);
+      const int o = which ? partner_of<PAIRING>(e, p.half) : e;
+      s_w[side][which][e] = p.heads[side] && o < p.d ? __ldg(p.w[side] + o) : 0.f;
+    }
+    __syncthreads();
+  }
   float c[8], s[8];
   token_angles<T, LPR, PAIRING>(p, u.token, gl, false, s_table + (threadIdx.x >> 5) * 128, c, s);
 #pragma unroll
@@ -292,9 +301,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_rope_fwd(c
       a[j] = c[j];
       b[j] = s[j];
       if constexpr (NORM) {
-        const int o = partner_of<PAIRING>(e0 + j, p.half);
-        a[j] *= n && e0 + j < p.d ? __ldg(p.w[side] + e0 + j) : 0.f;
-        b[j] *= n && o < p.d ? __ldg(p.w[side] + o) : 0.f;
+        a[j] *= s_w[side][0][e0 + j];
+        b[j] *= s_w[side][1][e0 + j];
       }
     }
     const int h0 = u.chunk * n;
