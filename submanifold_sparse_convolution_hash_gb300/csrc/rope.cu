@@ -109,21 +109,28 @@ __device__ __forceinline__ float group_sum(float v) {
 // float does not hold goes in two parts, a multiple of 4096 and a rest.  The
 // rows are then f32 (EXACT: a few units in the last place) or 16-bit, for which
 // the fast sine's 2^-20 is far below the output's rounding.
-template <bool EXACT>
-__device__ __forceinline__ float2 angle(int pos, float f, float amp) {
+struct Turn {
+  float c, ce;  // f / 2 pi, as a sum
+};
+__device__ __forceinline__ Turn turn_of(float f) {
   const float kInv2PiHi = 0x1.45f306p-3f;   // 1 / 2 pi to 24 bits
   const float kInv2PiLo = 0x1.b9391p-28f;   // the rest of it
-  const float c = f * kInv2PiHi;
-  const float ce = fmaf(f, kInv2PiHi, -c) + f * kInv2PiLo;
-  const int lo = pos & 4095;
+  Turn r;
+  r.c = f * kInv2PiHi;
+  r.ce = fmaf(f, kInv2PiHi, -r.c) + f * kInv2PiLo;
+  return r;
+}
+template <bool EXACT>
+__device__ __forceinline__ float2 angle(int pos, Turn f, float amp) {
   const bool small = pos > -(1 << 24) && pos < (1 << 24);
-  const float xh = static_cast<float>(small ? pos : pos - lo);
-  float t = xh * c;
-  float e = fmaf(xh, c, -t) + xh * ce;
+  const int lo = small ? 0 : pos & 4095;
+  const float xh = static_cast<float>(pos - lo);
+  float t = xh * f.c;
+  float e = fmaf(xh, f.c, -t) + xh * f.ce;
   t -= rintf(t);
-  if (!small) {
-    const float xl = static_cast<float>(lo), tl = xl * c;
-    e += fmaf(xl, c, -tl) + xl * ce;
+  if (!small) [[unlikely]] {
+    const float xl = static_cast<float>(lo), tl = xl * f.c;
+    e += fmaf(xl, f.c, -tl) + xl * f.ce;
     t += tl - rintf(tl);
   }
   t += e;
@@ -220,31 +227,42 @@ __device__ __forceinline__ int partner_of(int e, int half) {
 
 // y_e = z_e ca_e + z_partner(e) sb_e turns by a token's angles: the partner's
 // sine has the sign of the second member's formula, and `back` turns back.  The
-// group's lanes work out the token's pairs between them, and each picks its own
-// from `table`, the warp's 128 pairs in shared memory.
-template <typename T, int LPR, int PAIRING>
-__device__ __forceinline__ void token_angles(const RopeParams& p, int64_t t, int gl, bool back, float2* table,
-                                             float (&ca)[8], float (&sb)[8]) {
-  float2* mine = table + (threadIdx.x & 31) / LPR * (LPR * 4);
-  __syncwarp();
+// group's lanes work out the token's pairs between them, four each, and put each
+// under both its values in `table`, value e of the warp's group g at
+// [e % 8][g * LPR + e / 8]: a lane then reads its eight without conflicts.
+template <int LPR, int PAIRING>
+struct Angles {
+  Turn f[4];
+  int axis[4];
+  float2* mine;
+  __device__ __forceinline__ Angles(const RopeParams& p, int gl, float2* table) {
+    mine = table + ((threadIdx.x & 31) / LPR) * LPR;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int pair = gl + i * LPR;
-    if (pair < p.half) {
-      const int axis = (pair >= p.per) + (pair >= 2 * p.per) + (pair >= 3 * p.per);
-      mine[pair] = angle<sizeof(T) == 4>(__ldg(p.pos + t * p.pos_stride + axis), __ldg(p.freq + pair), p.amp);
+    for (int i = 0; i < 4; ++i) {
+      const int pair = gl + i * LPR;
+      f[i] = turn_of(pair < p.half ? __ldg(p.freq + pair) : 0.f);
+      axis[i] = (pair >= p.per) + (pair >= 2 * p.per) + (pair >= 3 * p.per);
     }
+    for (int j = 0; j < 8; ++j) mine[j * 32 + gl] = make_float2(1.f, 0.f);  // values that do not turn
+    __syncwarp();
   }
-  __syncwarp();
+  template <typename T>
+  __device__ __forceinline__ void fill(const RopeParams& p, int64_t t, int gl, bool back) {
+    __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int e = gl * 8 + j, pair = pair_of<PAIRING>(e, p.half);
-    const float2 cs = pair >= 0 ? mine[pair] : make_float2(1.f, 0.f);
-    const bool first = PAIRING == kInterleaved ? (j & 1) == 0 : e < p.half;
-    ca[j] = cs.x;
-    sb[j] = first != back ? -cs.y : cs.y;
+    for (int i = 0; i < 4; ++i) {
+      const int pair = gl + i * LPR;
+      if (pair < p.half) {
+        float2 cs = angle<sizeof(T) == 4>(__ldg(p.pos + t * p.pos_stride + axis[i]), f[i], p.amp);
+        if (back) cs.y = -cs.y;
+        const int e0 = PAIRING == kInterleaved ? 2 * pair : pair, e1 = PAIRING == kInterleaved ? e0 + 1 : pair + p.half;
+        mine[(e0 & 7) * 32 + (e0 >> 3)] = make_float2(cs.x, -cs.y);
+        mine[(e1 & 7) * 32 + (e1 >> 3)] = cs;
+      }
+    }
+    __syncwarp();
   }
-}
+};
 
 // A group's token and part of its heads; whole warps run the loops, for the
 // shuffles, and groups without a token do nothing in them.
@@ -272,16 +290,14 @@ constexpr int kRows = 4;  // rows in flight
 
 template <typename T, int LPR, int PAIRING, bool NORM>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_rope_fwd(const RopeParams p) {
-  constexpr int NW = Vec8<T>::kWords, U = sizeof(T) == 4 ? kRows / 2 : kRows;
+  constexpr int NW = Vec8<T>::kWords, GROUPS = kThreads / LPR, U = sizeof(T) == 4 ? kRows / 2 : kRows;
   __shared__ __align__(16) T s_stage[PAIRING >= kHalf2 ? kThreads * 8 : 8];
-  __shared__ float2 s_table[kThreads * 4];
+  __shared__ float2 s_table[kThreads * 8];
   __shared__ __align__(16) float s_w[NORM ? 2 : 1][2][NORM ? LPR * 8 : 4];  // [side][a value's, its partner's][value]
   T* stage = s_stage + (PAIRING >= kHalf2 ? (threadIdx.x >> 5) * 256 : 0);
   const int gl = threadIdx.x % LPR;
   const int e0 = gl * 8;
   const float inv_d = 1.f / static_cast<float>(p.d);
-  const Unit u = unit_of<LPR>(p, blockIdx.x);
-  const bool act = u.on && e0 < p.d;
   if constexpr (NORM) {
     for (int i = threadIdx.x; i < 4 * LPR * 8; i += kThreads) {
       const int side = i / (2 * LPR * 8), which = i / (LPR * 8) & 1, e = i % (LPR * 8);
@@ -290,54 +306,62 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_rope_fwd(c
     }
     __syncthreads();
   }
-  float c[8], s[8];
-  token_angles<T, LPR, PAIRING>(p, u.token, gl, false, s_table + (threadIdx.x >> 5) * 128, c, s);
+  Angles<LPR, PAIRING> angles(p, gl, s_table + (threadIdx.x >> 5) * 256);
+  const int64_t blocks = (p.tokens * p.chunks + GROUPS - 1) / GROUPS;
+#pragma unroll 1
+  for (int64_t blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
+    const Unit u = unit_of<LPR>(p, blk);
+    const bool act = u.on && e0 < p.d;
+    angles.template fill<T>(p, u.token, gl, false);
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const int n = p.per_chunk[side];
-    float a[8], b[8];
+    for (int side = 0; side < 2; ++side) {
+      const int n = p.per_chunk[side];
+      float a[8], b[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a[j] = c[j];
-      b[j] = s[j];
-      if constexpr (NORM) {
-        a[j] *= s_w[side][0][e0 + j];
-        b[j] *= s_w[side][1][e0 + j];
-      }
-    }
-    const int h0 = u.chunk * n;
-    const int left = act ? min(n, p.heads[side] - h0) : 0;
-    const int64_t xh = p.xh[side], yh = p.yh[side];
-    const uint8_t* x = p.x[side] + u.token * p.xt[side] + e0 * sizeof(T) + h0 * xh;
-    uint8_t* y = p.y[side] + u.token * p.yt[side] + e0 * sizeof(T) + h0 * yh;
-    for (int i = 0; i < n; i += U, x += U * xh, y += U * yh) {
-      uint32_t w[U][NW];
-#pragma unroll
-      for (int q = 0; q < U; ++q) {
-#pragma unroll
-        for (int k = 0; k < NW; ++k) w[q][k] = 0u;
-        if (i + q < left) load_words<NW>(x + q * xh, w[q]);
-      }
-#pragma unroll
-      for (int q = 0; q < U; ++q) {
-        float v[8], vp[8];
-        Vec8<T>::unpack(w[q], v);
-        partners<T, LPR, PAIRING>(w[q], vp, gl, p.half, stage);
-        float rn = 1.f;
+      for (int j = 0; j < 8; ++j) {
+        const float2 cs = angles.mine[j * 32 + gl];
+        a[j] = cs.x;
+        b[j] = cs.y;
         if constexpr (NORM) {
-          float ss = 0.f;
+          a[j] *= s_w[side][0][e0 + j];
+          b[j] *= s_w[side][1][e0 + j];
+        }
+      }
+      const int h0 = u.chunk * n;
+      const int left = act ? min(n, p.heads[side] - h0) : 0;
+      const int64_t xh = p.xh[side], yh = p.yh[side];
+      const uint8_t* x = p.x[side] + u.token * p.xt[side] + e0 * sizeof(T) + h0 * xh;
+      uint8_t* y = p.y[side] + u.token * p.yt[side] + e0 * sizeof(T) + h0 * yh;
+#pragma unroll 1
+      for (int i = 0; i < n; i += U, x += U * xh, y += U * yh) {
+        uint32_t w[U][NW];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-          rn = rsqrtf(group_sum<LPR>(ss) * inv_d + p.eps);
+        for (int q = 0; q < U; ++q) {
+#pragma unroll
+          for (int k = 0; k < NW; ++k) w[q][k] = 0u;
+          if (i + q < left) load_words<NW>(x + q * xh, w[q]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[j] = fmaf(v[j], a[j], vp[j] * b[j]);
-          if constexpr (NORM) v[j] *= rn;
-        }
-        if (i + q < left) {
-          Vec8<T>::pack(v, w[q]);
-          store_words<NW>(y + q * yh, w[q]);
+        for (int q = 0; q < U; ++q) {
+          float v[8], vp[8];
+          Vec8<T>::unpack(w[q], v);
+          partners<T, LPR, PAIRING>(w[q], vp, gl, p.half, stage);
+          float rn = 1.f;
+          if constexpr (NORM) {
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+            rn = rsqrtf(group_sum<LPR>(ss) * inv_d + p.eps);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            v[j] = fmaf(v[j], a[j], vp[j] * b[j]);
+            if constexpr (NORM) v[j] *= rn;
+          }
+          if (i + q < left) {
+            Vec8<T>::pack(v, w[q]);
+            store_words<NW>(y + q * yh, w[q]);
+          }
         }
       }
     }
@@ -352,7 +376,7 @@ template <typename T, int LPR, int PAIRING, bool NORM>
 __global__ void __launch_bounds__(kThreads, 3) k_rope_bwd(const RopeParams p) {
   constexpr int NW = Vec8<T>::kWords, GROUPS = kThreads / LPR, U = sizeof(T) == 4 || NORM ? kRows / 2 : kRows;
   __shared__ __align__(16) T s_stage[PAIRING >= kHalf2 ? kThreads * 8 : 8];
-  __shared__ float2 s_table[kThreads * 4];
+  __shared__ float2 s_table[kThreads * 8];
   T* stage = s_stage + (PAIRING >= kHalf2 ? (threadIdx.x >> 5) * 256 : 0);
   const int gl = threadIdx.x % LPR, grp = threadIdx.x / LPR;
   const int e0 = gl * 8;
@@ -366,12 +390,20 @@ __global__ void __launch_bounds__(kThreads, 3) k_rope_bwd(const RopeParams p) {
     for (int j = 0; j < 8; ++j) wt[j] = e0 + j < p.d ? __ldg((side ? p.w[1] : p.w[0]) + e0 + j) : 0.f;
   }
   const float inv_d = 1.f / static_cast<float>(p.d);
+  Angles<LPR, PAIRING> angles(p, gl, s_table + (threadIdx.x >> 5) * 256);
   const int64_t blocks = (p.tokens * p.chunks + GROUPS - 1) / GROUPS;
+#pragma unroll 1
   for (int64_t blk = static_cast<int64_t>(blockIdx.x) - first; blk < blocks; blk += count) {
     const Unit u = unit_of<LPR>(p, blk);
     const bool act = u.on && e0 < p.d;
+    angles.template fill<T>(p, u.token, gl, true);
     float c[8], s[8];
-    token_angles<T, LPR, PAIRING>(p, u.token, gl, true, s_table + (threadIdx.x >> 5) * 128, c, s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 cs = angles.mine[j * 32 + gl];
+      c[j] = cs.x;
+      s[j] = cs.y;
+    }
     const int h0 = u.chunk * n, left = act ? min(n, heads - h0) : 0;
     const uint8_t* gy = (side ? p.gy[1] : p.gy[0]) + u.token * (side ? p.gt[1] : p.gt[0]) + e0 * sizeof(T) + h0 * gh;
     const uint8_t* x = (side ? p.x[1] : p.x[0]) + u.token * (side ? p.xt[1] : p.xt[0]) + e0 * sizeof(T) + h0 * xh;
@@ -540,7 +572,8 @@ sc_status rope_run(const RopeArgs& a) {
                                : pick<__nv_bfloat16>(lpr, bwd, norm, pairing);
   if (steps > 0x7fffffff) return set_error(SC_ERR_UNSUPPORTED, "too many tokens");
   if (!bwd) {
-    SC_LAUNCH("qk_norm_rope_fwd", a.stream, (k<<<static_cast<unsigned>(steps), kThreads, 0, a.stream>>>(p)));
+    const int64_t most_blocks = 4ll * sms;  // as many as are resident
+    SC_LAUNCH("qk_norm_rope_fwd", a.stream, (k<<<static_cast<unsigned>(steps < most_blocks ? steps : most_blocks), kThreads, 0, a.stream>>>(p)));
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SC_OK : set_cuda_error(e, "qk_norm_rope_fwd");
   }
