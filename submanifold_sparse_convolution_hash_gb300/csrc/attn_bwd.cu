@@ -133,7 +133,10 @@ struct KvSmem {
   uint64_t full[kBwdMaxStages], empty[kBwdMaxStages];
   uint64_t kv_full[2], kv_empty[2];
   uint64_t rows_ok[kRowSlots], rows_free[kRowSlots];  // row statistics (and the rows of a tile that ends inside)
-  uint64_t s_full[2], p_ready, dp_full, ds_ready, acc_full;
+  // p_ready: one for each S.  S of the next tile is there already, so a quick warp
+  // may arrive for the next P before a slow one has for this; on one barrier the
+  // two would count as one tile's.
+  uint64_t s_full[2], p_ready[2], dp_full, ds_ready, acc_full;
   uint64_t drained;
   uint32_t tmem;
   int abort;
@@ -184,12 +187,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(smem_u32(&sm->kv_full[s]), 1);
       mbar_init(smem_u32(&sm->kv_empty[s]), 1);
       mbar_init(smem_u32(&sm->s_full[s]), 1);
+      mbar_init(smem_u32(&sm->p_ready[s]), 16);
     }
     for (int s = 0; s < kRowSlots; ++s) {
       mbar_init(smem_u32(&sm->rows_ok[s]), 1);
       mbar_init(smem_u32(&sm->rows_free[s]), 16);
     }
-    mbar_init(smem_u32(&sm->p_ready), 16);
     mbar_init(smem_u32(&sm->dp_full), 1);
     mbar_init(smem_u32(&sm->ds_ready), 16);
     mbar_init(smem_u32(&sm->acc_full), 1);
@@ -324,9 +327,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (SB == 2 && n > 1) scores(cur.at(2));
 #pragma unroll 1
       for (int i = 0; i < n && ok; ++i, ++np) {
-        ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready), np & 1);
+        const uint32_t sb = SB == 2 ? np & 1 : 0;
+        ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[sb]), (SB == 2 ? np >> 1 : np) & 1);
         tc_fence_after();
-        const uint32_t p_at = u_s + (SB == 2 ? (np & 1) * 128 : 0);
+        const uint32_t p_at = u_s + sb * 128;
         if (elect_lane()) product_cols<0, 8, true>(u_dv, p_at, rowt_lo + (cur.st + 1) * T16, rowt_hi, id_a, i > 0);
         __syncwarp();
         const RingPos<S> nxt = cur.at(2);
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm->p_ready));
+        if (lane == 0) mbar_arrive(smem_u32(&sm->p_ready[sb]));
         ok = ok && mbar_wait_inl(smem_u32(&sm->dp_full), np & 1);
         tc_fence_after();
         tmem_ld32_raw(tdp, y);

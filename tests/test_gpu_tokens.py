@@ -462,3 +462,98 @@ def test_refusals_that_need_a_device():
         sc.sc_qk_norm_rope_fwd(x, y, p[:, 0], f, out_q=y, out_k=x)
     with pytest.raises(ValueError, match="both norm weights"):
         sc.sc_qk_norm_rope_fwd(x, y, p[:, 0], f, wq=torch.ones(64, device="cuda"))
+
+
+@pytest.mark.parametrize("hk,d,dtype", [(8, 32, "f16"), (2, 64, "bf16"), (2, 128, "f16")])
+def test_attention_copies_of_a_sequence_have_the_same_bits(hk, d, dtype):
+    """Enough work for every block to run several tiles in a row, in which its warps drift apart:
+    what one copy's outputs and gradients are, all copies' are."""
+    n, copies = 400, 120
+    q, k, v, gout, qo, ko, lk, kvd = attn_inputs([n], None, 8, hk, d, dtype)
+    qd, kd, vd, gd = (x.cuda().repeat(copies, 1, 1) for x in (q, k, v, gout))
+    off = torch.arange(copies + 1, dtype=torch.int32).cuda() * n
+    scale = d ** -0.5
+    out, lse, mag, grads, gmag, smax = attn_ref(q.double(), k.double(), v.double(), [n], [n], [0, n], False, scale,
+                                                gout.double())
+    rel = 2.0 ** -22 * max(1.0, smax) + 2.0 ** -20
+    for _ in range(3):
+        o, l = sc.sc_attn_fwd(qd, kd, vd, off, return_lse=True)
+        got = (o,) + sc.sc_attn_bwd(gd, qd, kd, vd, o, l, off)
+        for x, want, m, f, name in zip(got, (out,) + tuple(grads), (mag,) + tuple(gmag), (1, 4, 4, 4),
+                                       ("out", "gq", "gk", "gv")):
+            c = x.view(copies, n, *x.shape[1:])
+            same = (c == c[:1]).flatten(1).all(1)
+            assert bool(same.all()), (name, (~same).nonzero().flatten().tolist())
+            close(c[0], want, m, U[dtype], f * rel, name)
+
+
+LONG = [
+    # keys cut where row tiles are few but whole (two parts of rows a block, several of keys)
+    ([300], [5000], 2, 1, 128, True, "bf16"),
+    ([300, 20], [2600, 4000], 4, 4, 64, False, "f16"),
+    # one row tile a sequence, keys cut in odd numbers of tiles
+    ([9, 1, 30], [1153, 6000, 385], 4, 2, 32, False, "bf16"),
+    ([2, 2], [129, 2500], 8, 1, 128, True, "f16"),
+    # few keys, many rows: the rows of a key tile cut in the gradients
+    ([3000], [130], 4, 2, 64, False, "f16"),
+    ([2500, 40], [1, 260], 6, 2, 128, False, "bf16"),
+]
+
+
+@pytest.mark.parametrize("lq,lk,hq,hk,d,causal,dtype", LONG)
+def test_attention_with_cut_keys_and_rows(lq, lk, hq, hk, d, causal, dtype):
+    test_attention_forward_and_gradients(lq, lk, hq, hk, d, causal, dtype)
+
+
+def test_attention_many_sequences():
+    """More sequences than the plan looks at in one run, most of them tiny or empty."""
+    g = torch.Generator().manual_seed(12)
+    lq = torch.randint(0, 4, (2300,), generator=g).tolist()
+    lq[5], lq[1500], lq[2299] = 140, 77, 0
+    test_attention_forward_and_gradients(lq, None, 2, 1, 16, True, "f16")
+
+
+def test_attention_in_a_graph():
+    """The calls can be captured and replayed on new inputs in the same buffers."""
+    lq = [200, 31]
+    q, k, v, gout, qo, ko, lk, kvd = attn_inputs(lq, None, 4, 2, 64, "bf16")
+    qd, kd, vd, gd, qo = q.cuda(), k.cuda(), v.cuda(), gout.cuda(), qo.cuda()
+    freq, _ = sc.rope_frequencies(64, device="cuda")
+    pos = torch.arange(231, dtype=torch.int32, device="cuda")
+
+    def step():
+        qr, kr = sc.sc_qk_norm_rope_fwd(qd, kd, pos, freq)
+        o, l = sc.sc_attn_fwd(qr, kr, vd, qo, causal=True, return_lse=True)
+        return (o,) + sc.sc_attn_bwd(gd, qr, kr, vd, o, l, qo, causal=True)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for scale in (1.0, 0.5):
+        qd.copy_((q * scale).cuda())
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+    sc.sc_attn_check()
+
+
+def test_fused_buffers_side_by_side():
+    """Inputs and gradients that lie side by side in the rows of one buffer."""
+    lq = [150, 9]
+    hq, hk, d = 4, 2, 32
+    q, k, v, gout, qo, ko, lk, kvd = attn_inputs(lq, None, hq, hk, d, "f16")
+    rows = torch.cat([q, k, v], 1).cuda()
+    qd, kd, vd = rows.split([hq, hk, hk], 1)
+    qo = qo.cuda()
+    o, l = sc.sc_attn_fwd(qd, kd, vd, qo, return_lse=True)
+    want = sc.sc_attn_bwd(gout.cuda(), qd, kd, vd, o, l, qo)
+    grads = torch.full_like(rows, math.nan)
+    gq, gk, gv = grads.split([hq, hk, hk], 1)
+    sc.sc_attn_bwd(gout.cuda(), qd, kd, vd, o, l, qo, gq=gq, gk=gk, gv=gv)
+    assert torch.equal(grads, torch.cat(want, 1))
+    # [heads, tokens, head_dim] storage
+    t = [x.contiguous().permute(1, 0, 2).contiguous().permute(1, 0, 2) for x in (qd, kd, vd)]
+    assert torch.equal(sc.sc_attn_fwd(*t, qo), o)
