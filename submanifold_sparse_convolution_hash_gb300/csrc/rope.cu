@@ -17,7 +17,9 @@
 // token, so it works them out once and keeps them, with the weights folded in,
 // in registers (a table in shared memory, read for every row, made the kernel
 // three times slower).
+#include "f32x2.cuh"
 #include "sc_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace sc {
 namespace {
@@ -25,23 +27,26 @@ namespace {
 constexpr int kThreads = 256;
 
 // ------------------------------------------------------------ 8 values --
+// As four pairs (v[2i], v[2i + 1]), which one instruction takes at once: the
+// kernels are bound by the instructions they issue before memory is.
 template <typename T>
 struct Vec8;
 template <>
 struct Vec8<__half> {
   static constexpr int kWords = 4;
-  static __device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&x)[8]) {
+  static __device__ __forceinline__ void unpack(const uint32_t (&w)[4], uint64_t (&x)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
+      x[i] = pair2(f.x, f.y);
     }
   }
-  static __device__ __forceinline__ void pack(const float (&x)[8], uint32_t (&w)[4]) {
+  static __device__ __forceinline__ void pack(const uint64_t (&x)[4], uint32_t (&w)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      float lo, hi;
+      unpair2(x[i], lo, hi);
+      const __half2 h = __floats2half2_rn(lo, hi);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
@@ -49,17 +54,16 @@ struct Vec8<__half> {
 template <>
 struct Vec8<__nv_bfloat16> {
   static constexpr int kWords = 4;
-  static __device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&x)[8]) {
+  static __device__ __forceinline__ void unpack(const uint32_t (&w)[4], uint64_t (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = pair2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ void pack(const float (&x)[8], uint32_t (&w)[4]) {
+  static __device__ __forceinline__ void pack(const uint64_t (&x)[4], uint32_t (&w)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      float lo, hi;
+      unpair2(x[i], lo, hi);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
@@ -67,13 +71,18 @@ struct Vec8<__nv_bfloat16> {
 template <>
 struct Vec8<float> {
   static constexpr int kWords = 8;
-  static __device__ __forceinline__ void unpack(const uint32_t (&w)[8], float (&x)[8]) {
+  static __device__ __forceinline__ void unpack(const uint32_t (&w)[8], uint64_t (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    for (int i = 0; i < 4; ++i) x[i] = pair2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
   }
-  static __device__ __forceinline__ void pack(const float (&x)[8], uint32_t (&w)[8]) {
+  static __device__ __forceinline__ void pack(const uint64_t (&x)[4], uint32_t (&w)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[i]);
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpair2(x[i], lo, hi);
+      w[2 * i] = __float_as_uint(lo);
+      w[2 * i + 1] = __float_as_uint(hi);
+    }
   }
 };
 
@@ -93,6 +102,13 @@ __device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[NW]) {
 #pragma unroll
   for (int i = 0; i < NW / 4; ++i)
     __stcs(reinterpret_cast<uint4*>(p) + i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+}
+
+// The sum of a lane's four pairs.
+__device__ __forceinline__ float sum8(const uint64_t (&v)[4]) {
+  float lo, hi;
+  unpair2(add2(add2(v[0], v[1]), add2(v[2], v[3])), lo, hi);
+  return lo + hi;
 }
 
 template <int LPR>
@@ -150,7 +166,7 @@ struct RopeParams {
   int64_t yt[2], yh[2];
   int heads[2];
   const float* w[2];
-  float* gw_part;            // backward with a norm: [blocks][D]
+  float* gw_part;            // backward with a norm: [blocks][side][D]
   const int* pos;
   int64_t pos_stride;        // elements between tokens
   const float* freq;
@@ -158,7 +174,6 @@ struct RopeParams {
   int d, half, per;          // half = R / 2 pairs, per = pairs of one axis
   int chunks;                // groups that share a token's heads
   int per_chunk[2];          // heads of each
-  int blocks_q;              // backward: blocks that take q, the others take k
   float eps, amp;
 };
 
@@ -171,14 +186,18 @@ enum Pairing {
 };
 
 template <typename T, int LPR, int PAIRING>
-__device__ __forceinline__ void partners(const uint32_t (&w)[Vec8<T>::kWords], float (&p)[8], int gl, int half,
+__device__ __forceinline__ void partners(const uint32_t (&w)[Vec8<T>::kWords], uint64_t (&p)[4], int gl, int half,
                                          T* stage) {
   constexpr int NW = Vec8<T>::kWords;
   if constexpr (PAIRING == kInterleaved) {
-    float x[8];
+    uint64_t x[4];
     Vec8<T>::unpack(w, x);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] = x[j ^ 1];
+    for (int j = 0; j < 4; ++j) {
+      float lo, hi;
+      unpair2(x[j], lo, hi);
+      p[j] = pair2(hi, lo);
+    }
   } else if constexpr (PAIRING == kHalf8) {
     const int step = half >> 3;
     const int from = gl < step ? gl + step : (gl < 2 * step ? gl - step : gl);
@@ -187,25 +206,34 @@ __device__ __forceinline__ void partners(const uint32_t (&w)[Vec8<T>::kWords], f
     for (int i = 0; i < NW; ++i) o[i] = __shfl_sync(0xffffffffu, w[i], from, LPR);
     Vec8<T>::unpack(o, p);
   } else {
-    T* row = stage + ((threadIdx.x & 31) / LPR) * (LPR * 8);
+    // word k of the warp's lane l at [k][l]: neither side has bank conflicts
+    uint32_t* words = reinterpret_cast<uint32_t*>(stage);
+    const int row = (threadIdx.x & 31) / LPR * LPR;
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < NW / 4; ++i)
-      reinterpret_cast<uint4*>(row + gl * 8)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    for (int i = 0; i < NW; ++i) words[i * 32 + row + gl] = w[i];
     __syncwarp();
     if constexpr (PAIRING == kHalf2 && sizeof(T) == 2) {
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int e = gl * 8 + 2 * j;
-        o[j] = *reinterpret_cast<const uint32_t*>(row + (e < half ? e + half : (e < 2 * half ? e - half : e)));
+        const int from = (e < half ? e + half : (e < 2 * half ? e - half : e)) >> 1;
+        o[j] = words[(from & 3) * 32 + row + (from >> 2)];
       }
       Vec8<T>::unpack(o, p);
     } else {
+      constexpr int PER = 8 / NW;  // values of a word
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = gl * 8 + j;
-        p[j] = static_cast<float>(row[e < half ? e + half : (e < 2 * half ? e - half : e)]);
+      for (int j = 0; j < 4; ++j) {
+        float v[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int e = gl * 8 + 2 * j + k;
+          const int from = e < half ? e + half : (e < 2 * half ? e - half : e);
+          v[k] = static_cast<float>(stage[((from / PER % NW) * 32 + row + (from >> 3)) * PER + from % PER]);
+        }
+        p[j] = pair2(v[0], v[1]);
       }
     }
   }
@@ -228,39 +256,64 @@ __device__ __forceinline__ int partner_of(int e, int half) {
 // y_e = z_e ca_e + z_partner(e) sb_e turns by a token's angles: the partner's
 // sine has the sign of the second member's formula, and `back` turns back.  The
 // group's lanes work out the token's pairs between them, four each, and put each
-// under both its values in `table`, value e of the warp's group g at
-// [e % 8][g * LPR + e / 8]: a lane then reads its eight without conflicts.
+// under both its values in `table`, value e of the warp's group g in row e % 8
+// at g * LPR + e / 8, each row turned by some places from the one before: then
+// neither the lanes that write consecutive pairs nor those that read their eight
+// values meet in a bank.
 template <int LPR, int PAIRING>
 struct Angles {
   Turn f[4];
-  int axis[4];
-  float2* mine;
-  __device__ __forceinline__ Angles(const RopeParams& p, int gl, float2* table) {
-    mine = table + ((threadIdx.x & 31) / LPR) * LPR;
+  int axis;         // of the lane's four pairs, a byte each
+  uint32_t to[4];   // a pair's two places in the table (bytes, 16 bits each)
+  float2* table;
+  static __device__ __forceinline__ int place(int col, int e) {  // value e of the group whose lane 0 is `col`
+    const int j = e & 7;
+    return j * 32 + ((col + (e >> 3) + j * (LPR >= 16 ? 2 : 1)) & 31);
+  }
+  __device__ __forceinline__ Angles(const RopeParams& p, int gl, float2* table_) : axis(0), table(table_) {
+    const int col = (threadIdx.x & 31) / LPR * LPR;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int pair = gl + i * LPR;
       f[i] = turn_of(pair < p.half ? __ldg(p.freq + pair) : 0.f);
-      axis[i] = (pair >= p.per) + (pair >= 2 * p.per) + (pair >= 3 * p.per);
+      axis |= ((pair >= p.per) + (pair >= 2 * p.per) + (pair >= 3 * p.per)) << (8 * i);
+      const int e0 = PAIRING == kInterleaved ? 2 * pair : pair, e1 = PAIRING == kInterleaved ? e0 + 1 : pair + p.half;
+      to[i] = static_cast<uint32_t>(place(col, e0)) * 8 | static_cast<uint32_t>(place(col, e1)) * 8 << 16;
     }
-    for (int j = 0; j < 8; ++j) mine[j * 32 + gl] = make_float2(1.f, 0.f);  // values that do not turn
+    for (int j = 0; j < 8; ++j) table[place(col, gl * 8 + j)] = make_float2(1.f, 0.f);  // values that do not turn
     __syncwarp();
   }
+  // Token t's positions, ahead of its angles.
+  __device__ __forceinline__ void positions(const RopeParams& p, int64_t t, int gl, int (&pos)[4]) const {
+    const int* at = p.pos + t * p.pos_stride;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (gl + i * LPR < p.half) pos[i] = __ldg(at + (axis >> (8 * i) & 255));
+  }
   template <typename T>
-  __device__ __forceinline__ void fill(const RopeParams& p, int64_t t, int gl, bool back) {
+  __device__ __forceinline__ void fill(const RopeParams& p, const int (&pos)[4], int gl, bool back) {
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int pair = gl + i * LPR;
-      if (pair < p.half) {
-        float2 cs = angle<sizeof(T) == 4>(__ldg(p.pos + t * p.pos_stride + axis[i]), f[i], p.amp);
+      if (gl + i * LPR < p.half) {
+        float2 cs = angle<sizeof(T) == 4>(pos[i], f[i], p.amp);
         if (back) cs.y = -cs.y;
-        const int e0 = PAIRING == kInterleaved ? 2 * pair : pair, e1 = PAIRING == kInterleaved ? e0 + 1 : pair + p.half;
-        mine[(e0 & 7) * 32 + (e0 >> 3)] = make_float2(cs.x, -cs.y);
-        mine[(e1 & 7) * 32 + (e1 >> 3)] = cs;
+        uint8_t* at = reinterpret_cast<uint8_t*>(table);
+        *reinterpret_cast<float2*>(at + (to[i] & 0xFFFF)) = make_float2(cs.x, -cs.y);
+        *reinterpret_cast<float2*>(at + (to[i] >> 16)) = cs;
       }
     }
     __syncwarp();
+  }
+  // The lane's eight values' factors.
+  __device__ __forceinline__ void read(int gl, uint64_t (&a)[4], uint64_t (&b)[4]) const {
+    const int col = (threadIdx.x & 31) / LPR * LPR;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 u = table[place(col, gl * 8 + 2 * j)], v = table[place(col, gl * 8 + 2 * j + 1)];
+      a[j] = pair2(u.x, v.x);
+      b[j] = pair2(u.y, v.y);
+    }
   }
 };
 
@@ -286,14 +339,102 @@ __device__ __forceinline__ Unit unit_of(const RopeParams& p, int64_t block) {
   return r;
 }
 
-constexpr int kRows = 4;  // rows in flight
+// Rows on their way: each lane copies its own 16 or 32 bytes of a row to its
+// own places in shared memory, ST steps of U rows ahead of the one it works on
+// (of the unit's next heads, its other side, or the next unit), so no barrier is
+// needed and the copies cost no registers.
+template <int N>
+__device__ __forceinline__ void copies_left() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <typename T, int LPR, int NSRC>
+struct Rows {
+  static constexpr int NW = Vec8<T>::kWords, Q = NW / 4, U = sizeof(T) == 4 ? 1 : 2, ST = 4;
+  static constexpr int kBytes = ST * U * NSRC * Q * 16 * kThreads;
+  uint32_t mine, put = 0, got = 0;  // stages
+  int64_t blk, blocks, count;
+  int side, last, i, n, left;       // side: the next rows'; last: of a unit
+  const uint8_t* src[NSRC];
+  __device__ __forceinline__ Rows(const RopeParams& p, void* smem, int64_t first, int64_t count_, int64_t blocks_,
+                                  int side0, int side1)
+      : mine(smem_u32(smem) + threadIdx.x * 16), blk(first), blocks(blocks_), count(count_), side(side0), last(side1) {
+    place(p);
+#pragma unroll
+    for (int k = 0; k < ST - 1; ++k) fetch(p, side0);
+  }
+  __device__ __forceinline__ const uint8_t* base(const RopeParams& p, int which) const {
+    return which == 0 ? p.gy[side] : p.x[side];
+  }
+  __device__ __forceinline__ int64_t head_stride(const RopeParams& p, int which) const {
+    return which == 0 ? p.gh[side] : p.xh[side];
+  }
+  __device__ __forceinline__ void place(const RopeParams& p) {
+    i = 0;
+    n = p.per_chunk[side];
+    left = 0;
+    if (blk >= blocks) return;
+    const Unit u = unit_of<LPR>(p, blk);
+    const int e0 = threadIdx.x % LPR * 8, h0 = u.chunk * n;
+    if (u.on && e0 < p.d) left = min(n, p.heads[side] - h0);
+#pragma unroll
+    for (int k = 0; k < NSRC; ++k)
+      src[k] = base(p, k) + u.token * (k == 0 ? p.gt[side] : p.xt[side]) + e0 * sizeof(T) +
+               h0 * head_stride(p, k);
+  }
+  __device__ __forceinline__ void fetch(const RopeParams& p, int side0) {
+    if (blk < blocks) {
+#pragma unroll
+      for (int q = 0; q < U; ++q)
+        if (i + q < left)
+#pragma unroll
+          for (int k = 0; k < NSRC; ++k)
+#pragma unroll
+            for (int h = 0; h < Q; ++h)
+              cp_async_16(mine + (((put * U + q) * NSRC + k) * Q + h) * (16 * kThreads),
+                          src[k] + q * head_stride(p, k) + h * 16, 16);
+      i += U;
+#pragma unroll
+      for (int k = 0; k < NSRC; ++k) src[k] += U * head_stride(p, k);
+      if (i >= n) {
+        if (side == last) {
+          side = side0;
+          blk += count;
+        } else {
+          side = last;
+        }
+        place(p);
+      }
+      put = put + 1 == ST ? 0 : put + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // The oldest step's rows have landed.
+  __device__ __forceinline__ void land() { copies_left<ST - 2>(); }
+  __device__ __forceinline__ void read(int q, int k, bool on, uint32_t (&w)[NW]) const {
+#pragma unroll
+    for (int h = 0; h < Q; ++h) {
+      uint32_t a = 0, b = 0, c = 0, d = 0;
+      if (on)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+                     : "r"(mine + (((got * U + q) * NSRC + k) * Q + h) * (16 * kThreads))
+                     : "memory");
+      w[4 * h] = a;
+      w[4 * h + 1] = b;
+      w[4 * h + 2] = c;
+      w[4 * h + 3] = d;
+    }
+  }
+  __device__ __forceinline__ void next() { got = got + 1 == ST ? 0 : got + 1; }
+};
 
 template <typename T, int LPR, int PAIRING, bool NORM>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_rope_fwd(const RopeParams p) {
-  constexpr int NW = Vec8<T>::kWords, GROUPS = kThreads / LPR, U = sizeof(T) == 4 ? kRows / 2 : kRows;
+  constexpr int NW = Vec8<T>::kWords, GROUPS = kThreads / LPR, U = sizeof(T) == 4 ? 2 : 4;
   __shared__ __align__(16) T s_stage[PAIRING >= kHalf2 ? kThreads * 8 : 8];
   __shared__ float2 s_table[kThreads * 8];
-  __shared__ __align__(16) float s_w[NORM ? 2 : 1][2][NORM ? LPR * 8 : 4];  // [side][a value's, its partner's][value]
+  // [side][a value's, its partner's][values 0-3, 4-7 of a lane][lane]
+  __shared__ float4 s_w[NORM ? 2 : 1][2][2][NORM ? LPR : 1];
   T* stage = s_stage + (PAIRING >= kHalf2 ? (threadIdx.x >> 5) * 256 : 0);
   const int gl = threadIdx.x % LPR;
   const int e0 = gl * 8;
@@ -302,29 +443,32 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_rope_fwd(c
     for (int i = threadIdx.x; i < 4 * LPR * 8; i += kThreads) {
       const int side = i / (2 * LPR * 8), which = i / (LPR * 8) & 1, e = i % (LPR * 8);
       const int o = which ? partner_of<PAIRING>(e, p.half) : e;
-      s_w[side][which][e] = p.heads[side] && o < p.d ? __ldg(p.w[side] + o) : 0.f;
+      reinterpret_cast<float*>(&s_w[side][which][e >> 2 & 1][e >> 3])[e & 3] =
+          p.heads[side] && o < p.d ? __ldg(p.w[side] + o) : 0.f;
     }
     __syncthreads();
   }
   Angles<LPR, PAIRING> angles(p, gl, s_table + (threadIdx.x >> 5) * 256);
   const int64_t blocks = (p.tokens * p.chunks + GROUPS - 1) / GROUPS;
+  int pos[4] = {};
+  if (blockIdx.x < blocks) angles.positions(p, unit_of<LPR>(p, blockIdx.x).token, gl, pos);
 #pragma unroll 1
   for (int64_t blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
     const Unit u = unit_of<LPR>(p, blk);
     const bool act = u.on && e0 < p.d;
-    angles.template fill<T>(p, u.token, gl, false);
+    angles.template fill<T>(p, pos, gl, false);
+    if (blk + gridDim.x < blocks) angles.positions(p, unit_of<LPR>(p, blk + gridDim.x).token, gl, pos);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const int n = p.per_chunk[side];
-      float a[8], b[8];
+      uint64_t a[4], b[4];
+      angles.read(gl, a, b);
+      if constexpr (NORM) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 cs = angles.mine[j * 32 + gl];
-        a[j] = cs.x;
-        b[j] = cs.y;
-        if constexpr (NORM) {
-          a[j] *= s_w[side][0][e0 + j];
-          b[j] *= s_w[side][1][e0 + j];
+        for (int h = 0; h < 2; ++h) {
+          const float4 wa = s_w[side][0][h][gl], wb = s_w[side][1][h][gl];
+          a[2 * h] = mul2(a[2 * h], pair2(wa.x, wa.y)), a[2 * h + 1] = mul2(a[2 * h + 1], pair2(wa.z, wa.w));
+          b[2 * h] = mul2(b[2 * h], pair2(wb.x, wb.y)), b[2 * h + 1] = mul2(b[2 * h + 1], pair2(wb.z, wb.w));
         }
       }
       const int h0 = u.chunk * n;
@@ -343,20 +487,21 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_rope_fwd(c
         }
 #pragma unroll
         for (int q = 0; q < U; ++q) {
-          float v[8], vp[8];
+          uint64_t v[4], vp[4];
           Vec8<T>::unpack(w[q], v);
           partners<T, LPR, PAIRING>(w[q], vp, gl, p.half, stage);
-          float rn = 1.f;
+          uint64_t rn = 0;
           if constexpr (NORM) {
-            float ss = 0.f;
+            uint64_t ss[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-            rn = rsqrtf(group_sum<LPR>(ss) * inv_d + p.eps);
+            for (int j = 0; j < 4; ++j) ss[j] = mul2(v[j], v[j]);
+            const float r = rsqrtf(group_sum<LPR>(sum8(ss)) * inv_d + p.eps);
+            rn = pair2(r, r);
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            v[j] = fmaf(v[j], a[j], vp[j] * b[j]);
-            if constexpr (NORM) v[j] *= rn;
+          for (int j = 0; j < 4; ++j) {
+            v[j] = fma2(v[j], a[j], mul2(vp[j], b[j]));
+            if constexpr (NORM) v[j] = mul2(v[j], rn);
           }
           if (i + q < left) {
             Vec8<T>::pack(v, w[q]);
@@ -368,121 +513,142 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) k_rope_fwd(c
   }
 }
 
-// The gradient.  The first blocks_q blocks walk q's units, the others k's, so
-// that each keeps its sum of one weight's gradient in registers and writes it
-// once: [block][D] in gw_part, summed in order by k_rope_gw (the same result
-// every time).
+// The gradient.  A block walks q's and k's heads of its tokens, keeps its sums of
+// both weights' gradients in registers and writes them once, [block][side][D] in
+// gw_part; k_rope_gw adds the blocks in order (the same result every time).
 template <typename T, int LPR, int PAIRING, bool NORM>
-__global__ void __launch_bounds__(kThreads, 3) k_rope_bwd(const RopeParams p) {
-  constexpr int NW = Vec8<T>::kWords, GROUPS = kThreads / LPR, U = sizeof(T) == 4 || NORM ? kRows / 2 : kRows;
+__global__ void __launch_bounds__(kThreads, NORM ? 2 : 3) k_rope_bwd(const RopeParams p) {
+  using R = Rows<T, LPR, NORM ? 2 : 1>;
+  constexpr int NW = R::NW, U = R::U, GROUPS = kThreads / LPR;
+  extern __shared__ __align__(16) uint8_t s_rows[];
   __shared__ __align__(16) T s_stage[PAIRING >= kHalf2 ? kThreads * 8 : 8];
   __shared__ float2 s_table[kThreads * 8];
+  __shared__ ulonglong2 s_w[NORM ? 2 : 1][2][NORM ? LPR : 1];  // [side][values 0-3, 4-7 of a lane][lane]
   T* stage = s_stage + (PAIRING >= kHalf2 ? (threadIdx.x >> 5) * 256 : 0);
   const int gl = threadIdx.x % LPR, grp = threadIdx.x / LPR;
   const int e0 = gl * 8;
-  const int side = static_cast<int>(blockIdx.x) >= p.blocks_q;
-  const int first = side ? p.blocks_q : 0, count = side ? gridDim.x - p.blocks_q : p.blocks_q;
-  const int n = side ? p.per_chunk[1] : p.per_chunk[0], heads = side ? p.heads[1] : p.heads[0];
-  const int64_t gh = side ? p.gh[1] : p.gh[0], xh = side ? p.xh[1] : p.xh[0], yh = side ? p.yh[1] : p.yh[0];
-  float gw[8] = {}, wt[8] = {};
-  if constexpr (NORM) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) wt[j] = e0 + j < p.d ? __ldg((side ? p.w[1] : p.w[0]) + e0 + j) : 0.f;
-  }
   const float inv_d = 1.f / static_cast<float>(p.d);
-  Angles<LPR, PAIRING> angles(p, gl, s_table + (threadIdx.x >> 5) * 256);
   const int64_t blocks = (p.tokens * p.chunks + GROUPS - 1) / GROUPS;
+  const int side0 = p.heads[0] ? 0 : 1, side1 = p.heads[1] ? 1 : 0;
+  R rows(p, s_rows, blockIdx.x, gridDim.x, blocks, side0, side1);
+  if constexpr (NORM) {
+    for (int i = threadIdx.x; i < 2 * LPR * 8; i += kThreads) {
+      const int side = i / (LPR * 8), e = i % (LPR * 8);
+      reinterpret_cast<float*>(&s_w[side][e >> 2 & 1][e >> 3])[e & 3] =
+          p.heads[side] && e < p.d ? __ldg(p.w[side] + e) : 0.f;
+    }
+    __syncthreads();
+  }
+  uint64_t gw[2][4] = {};
+  Angles<LPR, PAIRING> angles(p, gl, s_table + (threadIdx.x >> 5) * 256);
+  int pos[4] = {};
+  if (blockIdx.x < blocks) angles.positions(p, unit_of<LPR>(p, blockIdx.x).token, gl, pos);
 #pragma unroll 1
-  for (int64_t blk = static_cast<int64_t>(blockIdx.x) - first; blk < blocks; blk += count) {
+  for (int64_t blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
     const Unit u = unit_of<LPR>(p, blk);
     const bool act = u.on && e0 < p.d;
-    angles.template fill<T>(p, u.token, gl, true);
-    float c[8], s[8];
+    angles.template fill<T>(p, pos, gl, true);
+    if (blk + gridDim.x < blocks) angles.positions(p, unit_of<LPR>(p, blk + gridDim.x).token, gl, pos);
+    uint64_t c[4], s[4];
+    angles.read(gl, c, s);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 cs = angles.mine[j * 32 + gl];
-      c[j] = cs.x;
-      s[j] = cs.y;
-    }
-    const int h0 = u.chunk * n, left = act ? min(n, heads - h0) : 0;
-    const uint8_t* gy = (side ? p.gy[1] : p.gy[0]) + u.token * (side ? p.gt[1] : p.gt[0]) + e0 * sizeof(T) + h0 * gh;
-    const uint8_t* x = (side ? p.x[1] : p.x[0]) + u.token * (side ? p.xt[1] : p.xt[0]) + e0 * sizeof(T) + h0 * xh;
-    uint8_t* y = (side ? p.y[1] : p.y[0]) + u.token * (side ? p.yt[1] : p.yt[0]) + e0 * sizeof(T) + h0 * yh;
-    for (int i = 0; i < n; i += U, gy += U * gh, x += U * xh, y += U * yh) {
-      uint32_t wg[U][NW], wx[U][NW];
+    for (int side = 0; side < 2; ++side) {
+      const int n = p.per_chunk[side];
+      const int h0 = u.chunk * n, left = act ? min(n, p.heads[side] - h0) : 0;
+      const int64_t yh = p.yh[side];
+      uint8_t* y = p.y[side] + u.token * p.yt[side] + e0 * sizeof(T) + h0 * yh;
+      uint64_t wt[4] = {};
+      if constexpr (NORM) {
 #pragma unroll
-      for (int q = 0; q < U; ++q) {
-#pragma unroll
-        for (int k = 0; k < NW; ++k) wg[q][k] = wx[q][k] = 0u;
-        if (i + q < left) {
-          load_words<NW>(gy + q * gh, wg[q]);
-          if constexpr (NORM) load_words<NW>(x + q * xh, wx[q]);
+        for (int h = 0; h < 2; ++h) {
+          const ulonglong2 w2 = s_w[side][h][gl];
+          wt[2 * h] = w2.x, wt[2 * h + 1] = w2.y;
         }
       }
+#pragma unroll 1
+      for (int i = 0; i < n; i += U, y += U * yh) {
+        rows.land();
+        uint32_t wg[U][NW], wx[U][NW];
 #pragma unroll
-      for (int q = 0; q < U; ++q) {
-        const bool on = i + q < left;
-        float g[8], gp[8];
-        Vec8<T>::unpack(wg[q], g);
-        partners<T, LPR, PAIRING>(wg[q], gp, gl, p.half, stage);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = fmaf(g[j], c[j], gp[j] * s[j]);
-        if constexpr (NORM) {
-          float v[8], ss = 0.f, hx = 0.f;
-          Vec8<T>::unpack(wx[q], v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            ss = fmaf(v[j], v[j], ss);
-            hx = fmaf(g[j] * wt[j], v[j], hx);
-          }
-          const float rn = rsqrtf(group_sum<LPR>(ss) * inv_d + p.eps);
-          const float m = group_sum<LPR>(hx) * rn * inv_d;  // mean(h x r)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float xn = v[j] * rn;
-            if (on) gw[j] = fmaf(g[j], xn, gw[j]);
-            g[j] = rn * (g[j] * wt[j] - xn * m);
-          }
+        for (int q = 0; q < U; ++q) {
+          rows.read(q, 0, i + q < left, wg[q]);
+          if constexpr (NORM) rows.read(q, 1, i + q < left, wx[q]);
         }
-        if (on) {
-          Vec8<T>::pack(g, wg[q]);
-          store_words<NW>(y + q * yh, wg[q]);
+        rows.fetch(p, side0);
+        rows.next();
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          const bool on = i + q < left;
+          uint64_t g[4], gp[4];
+          Vec8<T>::unpack(wg[q], g);
+          partners<T, LPR, PAIRING>(wg[q], gp, gl, p.half, stage);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) g[j] = fma2(g[j], c[j], mul2(gp[j], s[j]));
+          if constexpr (NORM) {
+            uint64_t v[4], h[4], t[4];
+            Vec8<T>::unpack(wx[q], v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              t[j] = mul2(v[j], v[j]);
+              h[j] = mul2(g[j], wt[j]);
+            }
+            const float rs = rsqrtf(group_sum<LPR>(sum8(t)) * inv_d + p.eps), r = on ? rs : 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t[j] = mul2(h[j], v[j]);
+            const float m = -group_sum<LPR>(sum8(t)) * r * inv_d;  // -mean(h x r)
+            const uint64_t rn = pair2(r, r), mm = pair2(m, m);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[j] = mul2(v[j], rn);  // 0 in a row that is not there
+              gw[side][j] = fma2(g[j], v[j], gw[side][j]);
+              g[j] = mul2(rn, fma2(v[j], mm, h[j]));
+            }
+          }
+          if (on) {
+            Vec8<T>::pack(g, wg[q]);
+            store_words<NW>(y + q * yh, wg[q]);
+          }
         }
       }
     }
   }
   if constexpr (NORM) {
     // the groups' sums in order, in the table's place
-    float* s_gw = reinterpret_cast<float*>(s_table);  // [GROUPS][LPR * 8]
-    __syncthreads();
+    uint64_t* s_gw = reinterpret_cast<uint64_t*>(s_table);  // [GROUPS][LPR * 4] pairs
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s_gw[grp * (LPR * 8) + e0 + j] = gw[j];
-    __syncthreads();
-    for (int col = threadIdx.x; col < p.d; col += kThreads) {
-      float v = 0.f;
-      for (int g = 0; g < GROUPS; ++g) v += s_gw[g * (LPR * 8) + col];
-      p.gw_part[static_cast<int64_t>(blockIdx.x) * p.d + col] = v;
+    for (int side = 0; side < 2; ++side) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s_gw[grp * (LPR * 4) + gl * 4 + j] = gw[side][j];
+      __syncthreads();
+      for (int col = threadIdx.x; col < p.d; col += kThreads) {
+        float v = 0.f;
+        for (int g = 0; g < GROUPS; ++g) v += reinterpret_cast<const float*>(s_gw)[g * (LPR * 8) + col];
+        p.gw_part[(static_cast<int64_t>(blockIdx.x) * 2 + side) * p.d + col] = v;
+      }
     }
   }
 }
 
-// gw[c] = sum over its side's blocks of part[block][c], each column by one warp:
+// gw[c] = sum over the blocks of part[block][side][c], each column by one warp:
 // lanes take blocks in strides, then a fixed tree.
-__global__ void __launch_bounds__(kThreads) k_rope_gw(const float* __restrict__ part, int blocks_q, int blocks, int d,
-                                                      float* gwq, float* gwk) {
+__global__ void __launch_bounds__(kThreads) k_rope_gw(const float* __restrict__ part, int blocks, int d, float* gwq,
+                                                      float* gwk) {
   const int col = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (col >= 2 * d) return;
-  const bool k = col >= d;
-  const int c = k ? col - d : col;
   float v = 0.f;
-  for (int b = (k ? blocks_q : 0) + lane; b < (k ? blocks : blocks_q); b += 32)
-    v += __ldg(part + static_cast<int64_t>(b) * d + c);
+  for (int b = lane; b < blocks; b += 32) v += __ldcg(part + static_cast<int64_t>(b) * 2 * d + col);
   v = group_sum<32>(v);
-  float* dst = k ? gwk : gwq;
-  if (lane == 0 && dst) dst[c] = v;
+  float* dst = col >= d ? gwk : gwq;
+  if (lane == 0 && dst) dst[col >= d ? col - d : col] = v;
 }
 
 using Kern = void (*)(RopeParams);
+
+template <typename T>
+size_t ring_bytes(bool norm) {
+  return norm ? Rows<T, 8, 2>::kBytes : Rows<T, 8, 1>::kBytes;
+}
 
 template <typename T, int LPR, int PAIRING>
 Kern pick_norm(bool bwd, bool norm) {
@@ -577,28 +743,24 @@ sc_status rope_run(const RopeArgs& a) {
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SC_OK : set_cuda_error(e, "qk_norm_rope_fwd");
   }
-  // blocks by the sides' heads, one at least for each that has some
-  const int64_t cap = 3ll * sms;
-  int64_t nb[2] = {0, 0};
-  for (int s = 0; s < 2; ++s)
-    if (p.heads[s]) {
-      nb[s] = (cap * p.heads[s] + heads / 2) / heads;
-      nb[s] = nb[s] < 1 ? 1 : nb[s] > steps ? steps : nb[s];
-    }
-  p.blocks_q = static_cast<int>(nb[0]);
-  const int blocks = static_cast<int>(nb[0] + nb[1]);
+  const size_t ring = a.dtype == SC_F32 ? ring_bytes<float>(norm) : ring_bytes<__half>(norm);
+  // the ring lies beside up to 24 KB of static shared memory
+  const sc_status set = kernel_setup(reinterpret_cast<const void*>(k), 96 * 1024, nullptr);
+  if (set) return set;
+  const int64_t resident = (norm ? 2ll : 3ll) * sms;
+  const int blocks = static_cast<int>(steps < resident ? steps : resident);
   void* part = nullptr;
   if (norm) {
-    const sc_status st = dev_alloc(&part, sizeof(float) * p.d * static_cast<size_t>(blocks), a.stream);
+    const sc_status st = dev_alloc(&part, sizeof(float) * 2 * p.d * static_cast<size_t>(blocks), a.stream);
     if (st) return st;
     p.gw_part = static_cast<float*>(part);
   }
-  SC_LAUNCH("qk_norm_rope_bwd", a.stream, (k<<<blocks, kThreads, 0, a.stream>>>(p)));
+  SC_LAUNCH("qk_norm_rope_bwd", a.stream, (k<<<blocks, kThreads, ring, a.stream>>>(p)));
   cudaError_t e = cudaGetLastError();
   if (norm && e == cudaSuccess) {
     const int grid = (2 * p.d * 32 + kThreads - 1) / kThreads;
     SC_LAUNCH("qk_norm_rope_gw", a.stream,
-              (k_rope_gw<<<grid, kThreads, 0, a.stream>>>(p.gw_part, p.blocks_q, blocks, p.d, a.gw[0], a.gw[1])));
+              (k_rope_gw<<<grid, kThreads, 0, a.stream>>>(p.gw_part, blocks, p.d, a.gw[0], a.gw[1])));
     e = cudaGetLastError();
   }
   dev_free(part, a.stream);
