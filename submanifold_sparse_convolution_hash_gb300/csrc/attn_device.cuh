@@ -98,9 +98,13 @@ struct RingPos {
 
 // Work units reach a block's warps through two slots: one warp takes the next
 // unit from the list's counter, the others read it in turn.  Which block takes
-// which unit changes no result.
+// which unit changes no result.  A unit is taken when the loads ask for it, that
+// is when those of the unit before have been issued, and not as soon as a slot
+// is free: with two to four units a block, units taken two ahead are dealt out
+// before anyone knows who is done first (some SMs were busy half the time of
+// others, 29 % of a gradient's time over packed documents).
 struct ItemSlots {
-  uint64_t full[2], empty[2];
+  uint64_t full[2], empty[2], ask;
   AttnItem item[2];
   int head[2];  // -1: no more work
   __device__ __forceinline__ void init(int readers) {
@@ -108,6 +112,7 @@ struct ItemSlots {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), readers);
     }
+    mbar_init(smem_u32(&ask), 1);
   }
 };
 
@@ -115,8 +120,9 @@ __device__ __forceinline__ void hand_out(ItemSlots* sl, int* counter, const Attn
                                          volatile int* abort_flag) {
   for (uint32_t n = 0;; ++n) {
     const int slot = n & 1;
+    const bool asked = mbar_wait_inl(smem_u32(&sl->ask), n & 1);
     const int u = atomicAdd(counter, 1);
-    if (!mbar_wait_inl(smem_u32(&sl->empty[slot]), ((n >> 1) & 1) ^ 1)) {
+    if (!asked || !mbar_wait_inl(smem_u32(&sl->empty[slot]), ((n >> 1) & 1) ^ 1)) {
       *abort_flag = 1;
       break;
     }
@@ -133,7 +139,7 @@ __device__ __forceinline__ void hand_out(ItemSlots* sl, int* counter, const Attn
   }
 }
 
-// A reader's side: one thread, or a warp as one.
+// A reader's side: one thread (the loads), or a warp as one.
 struct ItemRing {
   ItemSlots* sl;
   uint32_t n = 0;
@@ -141,6 +147,7 @@ struct ItemRing {
   // The next item; false: no more (or the block gives up).
   __device__ __forceinline__ bool next(AttnItem* it, int* head, volatile int* abort_flag, bool warp) {
     const int slot = n & 1;
+    if (!warp) mbar_arrive(smem_u32(&sl->ask));
     bool ok = mbar_wait_inl(smem_u32(&sl->full[slot]), (n >> 1) & 1);
     if (warp) ok = __all_sync(0xffffffffu, ok);
     if (!ok) {
