@@ -127,9 +127,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   grid_wait();  // the plan
   grid_release();
   const uint32_t tmem = sm->tmem;
-  // TMEM: S of the two row tiles, 128 columns each; to 64 values P (64 columns
-  // each) and O behind them, else P over S and O of 128 columns.
-  constexpr bool EARLY = DP == 64;
+  // TMEM: S of the two row tiles, 128 columns each, P over S, O of 128 columns.
+  // One row tile of up to 64 values: P has 64 columns of its own behind S and O 64,
+  // so that S of the next tile need not wait for the product that reads P (four
+  // scenes' 100 queries of 8 heads of 64: 199 us, 209 with P over S; with two row
+  // tiles P over S is the faster form, 161 us for 164 on 160 voxel windows,
+  // because the product then begins with half of the keys).
+  constexpr bool EARLY = DP == 64 && ONE;
   const uint32_t t_p = EARLY ? tmem + 256 : tmem, t_o = EARLY ? tmem + 384 : tmem + 256;
   constexpr uint32_t P_COLS = EARLY ? 64 : 128, O_COLS = EARLY ? 64 : 128;
   const int n_items = __ldcg(p.header);
@@ -294,9 +298,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const bool fixer = (e0 == n) == (s == 0);
         bool fixed = false;
         if (end <= 0 && lane == 0) mbar_arrive(smem_u32(&sm->q_empty));
-        // Step t makes S of the next tile and P V of this one; the first makes S
-        // alone.  S comes first where P has columns of its own: the softmax waits for
-        // nothing else.  Else P lies over S, and S comes second.
+        // Step t makes P V of this tile and S of the next one; the first makes S alone.
 #pragma unroll 1
         for (int t = -1; t < end && ok; ++t) {
           const bool cur = t >= 0, more = t + 1 < end;
@@ -318,30 +320,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               fixed = true;
             }
             ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][0]), np & 1);
-            if constexpr (!EARLY) {  // the product begins with half of the keys
-              tc_fence_after();
-              if (elect_lane()) product_cols<0, 4>(to, tp, vv, v_hi, id_o, t > 0);
-              __syncwarp();
-              ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][1]), np & 1);
-            }
+            tc_fence_after();  // the product begins with half of the keys
+            if (elect_lane()) product_cols<0, 4>(to, tp, vv, v_hi, id_o, t > 0);
+            __syncwarp();
+            ok = ok && mbar_wait_inl(smem_u32(&sm->p_ready[s][1]), np & 1);
             ++np;
           }
           tc_fence_after();
           if (elect_lane()) {
-            auto scores = [&] {
+            if (cur) {
+              product_cols<4, 4>(to, tp, vv, v_hi, id_o, true);
+              if (!more) tc_commit(smem_u32(&sm->o_full[s]));
+              tc_commit(smem_u32(&sm->empty[v.st]));
+            }
+            if (more) {  // over this tile's P
               product_rows<DP>(ts, q_at, kk, k_hi, id_s, ksteps);
               tc_commit(smem_u32(&sm->s_full[s]));
               tc_commit(smem_u32(&sm->empty[k.st]));
               if (t + 2 >= end) tc_commit(smem_u32(&sm->q_empty));  // the last S
-            };
-            if (EARLY && more) scores();
-            if (cur) {
-              if constexpr (EARLY) product_cols<0, 8>(to, tp, vv, v_hi, id_o, t > 0);
-              else product_cols<4, 4>(to, tp, vv, v_hi, id_o, true);
-              if (EARLY || !more) tc_commit(smem_u32(&sm->o_full[s]));
-              tc_commit(smem_u32(&sm->empty[v.st]));
             }
-            if (!EARLY && more) scores();
           }
           __syncwarp();
           ok = __all_sync(0xffffffffu, ok);
@@ -552,7 +549,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 }
 
 // Joins the parts of the rows whose keys were cut, a warp a row, four values a
-// lane: with m the largest of the parts' maxima, out = sum O_q f_q / sum l_q f_q,
+// lane (to 64 values two parts at a time): with m the largest of the parts' maxima, out = sum O_q f_q / sum l_q f_q,
 // f_q = exp(scale (m_q - m)).  The parts are taken in order, whoever made them.
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const AttnItem* joins) {
@@ -578,7 +575,9 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Attn
     const float base = base_of(m, p.scale_log2);
     float l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool on = lane * 4 < p.d;
+    const int per = p.d <= 64 ? 16 : 32;  // lanes of a part
+    const int c = lane & (per - 1), first = lane / per, turn = 32 / per;
+    const bool on = c * 4 < p.d;
     for (int q0 = 0; q0 < parts; q0 += 32) {
       // a part's factor a lane; 0 where it saw nothing (no O was written then)
       float f = 0.f, lq = 0.f;
@@ -596,9 +595,10 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Attn
       l += lq;
       const int cnt = min(32, parts - q0);
 #pragma unroll 8
-      for (int q = 0; q < cnt; ++q) {
+      for (int u = 0; u < cnt; u += turn) {
+        const int q = u + first;  // past the last: its factor's lane holds 0
         const float fq = __shfl_sync(0xffffffffu, f, q);
-        const float4 o = on && (have >> q & 1) ? __ldcg(reinterpret_cast<const float4*>(src + (q0 + q) * step) + lane)
+        const float4 o = on && (have >> q & 1) ? __ldcg(reinterpret_cast<const float4*>(src + (q0 + q) * step) + c)
                                                : make_float4(0.f, 0.f, 0.f, 0.f);
         a.x = fmaf(o.x, fq, a.x);
         a.y = fmaf(o.y, fq, a.y);
@@ -606,11 +606,17 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Attn
         a.w = fmaf(o.w, fq, a.w);
       }
     }
+    if (turn == 2) {
+      a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
+      a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+      a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
+      a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
+    }
     const int vis = p.causal ? min(it->lk, it->lim0 + i + 1) : it->lk;
     const float inv = vis > 0 ? 1.f / l : 0.f;
     const int64_t tok = static_cast<int64_t>(it->q_row) + i;
-    if (on)
-      *reinterpret_cast<uint2*>(p.out + tok * p.out_t + h * p.out_h + lane * 8) =
+    if (on && first == 0)
+      *reinterpret_cast<uint2*>(p.out + tok * p.out_t + h * p.out_h + c * 8) =
           vis > 0 ? make_uint2(pack_pair<BF16>(a.x * inv, a.y * inv), pack_pair<BF16>(a.z * inv, a.w * inv))
                   : make_uint2(0u, 0u);
     if (p.lse && lane == 0) p.lse[tok * p.heads_q + h] = vis > 0 ? base * kLn2 + logf(l) : -INFINITY;
