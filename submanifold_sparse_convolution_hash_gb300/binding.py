@@ -141,10 +141,6 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
 
-def _ref(s):
-    return ctypes.byref(s) if s is not None else None
-
-
 class Hash:
     """Handle of a coordinate hash table built by sc_hash_build."""
 
@@ -456,56 +452,63 @@ class _Heads(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
-def _heads(t, name: str, like=None, shape=None):
+# A call on few rows is bound by the host, so these wrappers read a tensor's
+# properties once and pass plain integers (argtypes converts them).
+def _heads(t, name: str, dtype=None, device=None, shape=None):
     """The view struct of a CUDA tensor [tokens, heads, head_dim] whose last
-    dimension is contiguous (the other strides are free)."""
+    dimension is contiguous (the other strides are free), by reference."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     stride = t.stride()
     if len(stride) != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
+    if dtype is not None and (t.dtype is not dtype or t.get_device() != device):
         raise ValueError(f"{name} must have the dtype and device of the other rows")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if stride[2] != 1 and t.shape[2] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return _Heads(t.data_ptr(), stride[0], stride[1])
+    return ctypes.byref(_Heads(t.data_ptr(), stride[0], stride[1]))
+
+
+def _rows_out(t, name: str, like, shape, dtype, device):
+    """(t, its view): where to write rows of `shape`, made here if t is None."""
+    if t is not None:
+        return t, _heads(t, name, dtype, device, shape)
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    return t, ctypes.byref(_Heads(t.data_ptr(), shape[1] * shape[2], shape[2]))
+
+
+def _raw_stream(stream) -> int:
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _f32(t, name: str, n: int, device: int):
+    """The address of a float32 [n] vector, or None."""
     if t is None:
-        return
+        return None
     if (not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not torch.float32
             or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous float32 [{n}] tensor on the rows' device")
+    return t.data_ptr()
 
 
-def _rope_args(first, pos, freq, wq, wk, heads_q, heads_k):
-    tokens, _, d = first.shape
-    if first.dtype not in _DTYPES:
-        raise ValueError("rows must be float32, float16 or bfloat16")
-    device = first.get_device()
-    rot, axes, stride = 0, 1, 0
-    if freq is not None:
-        half = freq.shape[0]
-        rot = 2 * half
-        _f32(freq, "freq", half, device)
-        if not isinstance(pos, torch.Tensor) or pos.get_device() != device or pos.dtype is not torch.int32:
-            raise ValueError("pos must be int32 on the rows' device")
-        st = pos.stride()
-        if len(st) not in (1, 2) or pos.shape[0] != tokens:
-            raise ValueError("pos must be [tokens] or [tokens, axes]")
-        stride = st[0]
-        if len(st) == 2:
-            axes = pos.shape[1]
-            if axes > 1 and st[1] != 1:
-                raise ValueError("pos: the axes must be contiguous")
-    _f32(wq, "wq", d, device)
-    _f32(wk, "wk", d, device)
-    if (wq is None) != (wk is None) and heads_q and heads_k:
-        raise ValueError("pass both norm weights, or neither")
-    return tokens, d, rot, axes, stride
+def _positions(pos, freq, tokens, device):
+    """(address, token stride, axes, frequencies' address, rot_dim)."""
+    if freq is None:
+        return None, 0, 1, None, 0
+    half = freq.shape[0]
+    fp = _f32(freq, "freq", half, device)
+    if not isinstance(pos, torch.Tensor) or pos.get_device() != device or pos.dtype is not torch.int32:
+        raise ValueError("pos must be int32 on the rows' device")
+    st, axes = pos.stride(), 1
+    if len(st) not in (1, 2) or pos.shape[0] != tokens:
+        raise ValueError("pos must be [tokens] or [tokens, axes]")
+    if len(st) == 2:
+        axes = pos.shape[1]
+        if axes > 1 and st[1] != 1:
+            raise ValueError("pos: the axes must be contiguous")
+    return (pos.data_ptr() if half else None), st[0], axes, fp, 2 * half
 
 
 def sc_qk_norm_rope_fwd(q, k, pos=None, freq=None, wq=None, wk=None, eps: float = 1e-6, interleaved: bool = False,
@@ -518,21 +521,36 @@ def sc_qk_norm_rope_fwd(q, k, pos=None, freq=None, wq=None, wk=None, eps: float 
     first = q if q is not None else k
     if first is None:
         raise ValueError("pass q, k or both")
-    hq, hk = (_heads(x, n, like=first) if x is not None else None for x, n in ((q, "q"), (k, "k")))
-    nq, nk = (x.shape[1] if x is not None else 0 for x in (q, k))
-    tokens, d, rot, axes, stride = _rope_args(first, pos, freq, wq, wk, nq, nk)
-    if q is not None and k is not None and (k.shape[0] != tokens or k.shape[2] != d):
+    hq = hk = oq = ok = sq = sk = None
+    nq = nk = 0
+    if q is not None:
+        hq = _heads(q, "q")
+        sq = q.shape
+        nq = sq[1]
+    dtype, device = first.dtype, first.get_device()
+    if k is not None:
+        hk = _heads(k, "k", dtype, device)
+        sk = k.shape
+        nk = sk[1]
+    tokens, _, d = sq or sk
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("rows must be float32, float16 or bfloat16")
+    pp, stride, axes, fp, rot = _positions(pos, freq, tokens, device)
+    wqp, wkp = _f32(wq, "wq", d, device), _f32(wk, "wk", d, device)
+    if (wq is None) != (wk is None) and nq and nk:
+        raise ValueError("pass both norm weights, or neither")
+    if sq and sk and (sk[0] != tokens or sk[2] != d):
         raise ValueError("q and k must have the same tokens and head_dim")
-    if q is not None and out_q is None:
-        out_q = torch.empty((tokens, nq, d), dtype=first.dtype, device=first.device)
-    if k is not None and out_k is None:
-        out_k = torch.empty((tokens, nk, d), dtype=first.dtype, device=first.device)
-    oq = _heads(out_q, "out_q", first, q.shape) if q is not None else None
-    ok = _heads(out_k, "out_k", first, k.shape) if k is not None else None
-    _check(lib().sc_qk_norm_rope_fwd(_ref(hq), _ref(hk), _ref(oq), _ref(ok), _ptr(wq), _ptr(wk),
-                                     _ptr(pos) if rot else None, stride, axes, _ptr(freq), tokens, nq, nk, d, rot,
-                                     eps, amp, _DTYPES[first.dtype], SC_ROPE_INTERLEAVED if interleaved else 0,
-                                     _stream(stream)), "sc_qk_norm_rope_fwd")
+    if sq:
+        out_q, oq = _rows_out(out_q, "out_q", q, sq, dtype, device)
+    if sk:
+        out_k, ok = _rows_out(out_k, "out_k", k, sk, dtype, device)
+    st = (_lib or lib()).sc_qk_norm_rope_fwd(hq, hk, oq, ok, wqp, wkp, pp, stride, axes, fp, tokens, nq, nk, d, rot,
+                                             eps, amp, code, SC_ROPE_INTERLEAVED if interleaved else 0,
+                                             _raw_stream(stream))
+    if st:
+        _check(st, "sc_qk_norm_rope_fwd")
     return out_q, out_k
 
 
@@ -544,28 +562,46 @@ def sc_qk_norm_rope_bwd(gout_q, gout_k, q=None, k=None, pos=None, freq=None, wq=
     first = gout_q if gout_q is not None else gout_k
     if first is None:
         raise ValueError("pass gout_q, gout_k or both")
-    gq, gk = (_heads(x, n, like=first) if x is not None else None
-              for x, n in ((gout_q, "gout_q"), (gout_k, "gout_k")))
-    nq, nk = (x.shape[1] if x is not None else 0 for x in (gout_q, gout_k))
-    tokens, d, rot, axes, stride = _rope_args(first, pos, freq, wq, wk, nq, nk)
-    if gout_q is not None and gout_k is not None and (gout_k.shape[0] != tokens or gout_k.shape[2] != d):
+    gq = gk = hq = hk = iq = ik = sq = sk = gwq = gwk = None
+    nq = nk = 0
+    if gout_q is not None:
+        gq = _heads(gout_q, "gout_q")
+        sq = gout_q.shape
+        nq = sq[1]
+    dtype, device = first.dtype, first.get_device()
+    if gout_k is not None:
+        gk = _heads(gout_k, "gout_k", dtype, device)
+        sk = gout_k.shape
+        nk = sk[1]
+    tokens, _, d = sq or sk
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("rows must be float32, float16 or bfloat16")
+    pp, stride, axes, fp, rot = _positions(pos, freq, tokens, device)
+    wqp, wkp = _f32(wq, "wq", d, device), _f32(wk, "wk", d, device)
+    if (wq is None) != (wk is None) and nq and nk:
+        raise ValueError("pass both norm weights, or neither")
+    if sq and sk and (sk[0] != tokens or sk[2] != d):
         raise ValueError("gout_q and gout_k must have the same tokens and head_dim")
     norm = wq is not None or wk is not None
-    hq = _heads(q, "q", first, gout_q.shape) if norm and gout_q is not None else None
-    hk = _heads(k, "k", first, gout_k.shape) if norm and gout_k is not None else None
-    if gout_q is not None and gin_q is None:
-        gin_q = torch.empty((tokens, nq, d), dtype=first.dtype, device=first.device)
-    if gout_k is not None and gin_k is None:
-        gin_k = torch.empty((tokens, nk, d), dtype=first.dtype, device=first.device)
-    iq = _heads(gin_q, "gin_q", first, gout_q.shape) if gout_q is not None else None
-    ik = _heads(gin_k, "gin_k", first, gout_k.shape) if gout_k is not None else None
-    gwq = torch.empty(d, dtype=torch.float32, device=first.device) if norm and nq else None
-    gwk = torch.empty(d, dtype=torch.float32, device=first.device) if norm and nk else None
-    _check(lib().sc_qk_norm_rope_bwd(_ref(gq), _ref(gk), _ref(hq), _ref(hk), _ref(iq), _ref(ik), _ptr(gwq),
-                                     _ptr(gwk), _ptr(wq), _ptr(wk), _ptr(pos) if rot else None, stride, axes,
-                                     _ptr(freq), tokens, nq, nk, d, rot, eps, amp, _DTYPES[first.dtype],
-                                     SC_ROPE_INTERLEAVED if interleaved else 0, _stream(stream)),
-           "sc_qk_norm_rope_bwd")
+    if sq:
+        gin_q, iq = _rows_out(gin_q, "gin_q", gout_q, sq, dtype, device)
+        if norm:
+            hq = _heads(q, "q", dtype, device, sq)
+            if nq:
+                gwq = torch.empty_like(wq)
+    if sk:
+        gin_k, ik = _rows_out(gin_k, "gin_k", gout_k, sk, dtype, device)
+        if norm:
+            hk = _heads(k, "k", dtype, device, sk)
+            if nk:
+                gwk = torch.empty_like(wk)
+    st = (_lib or lib()).sc_qk_norm_rope_bwd(gq, gk, hq, hk, iq, ik, gwq.data_ptr() if gwq is not None else None,
+                                             gwk.data_ptr() if gwk is not None else None, wqp, wkp, pp, stride, axes,
+                                             fp, tokens, nq, nk, d, rot, eps, amp, code,
+                                             SC_ROPE_INTERLEAVED if interleaved else 0, _raw_stream(stream))
+    if st:
+        _check(st, "sc_qk_norm_rope_bwd")
     return gin_q, gin_k, gwq, gwk
 
 
@@ -606,30 +642,34 @@ def rope_frequencies(rot_dim: int, axes: int = 1, base: float = 10000.0, scaling
     return freq.float().repeat(axes).to(device), amp
 
 
-def _offsets(off, name: str, device: int) -> int:
+def _offsets(off, name: str, device: int, n: int | None = None):
+    """The address of an int32 vector (of n values)."""
     if (not isinstance(off, torch.Tensor) or off.get_device() != device or off.dtype is not torch.int32
             or off.dim() != 1 or not off.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous int32 vector on the rows' device")
-    return off.shape[0]
+    if n is not None and off.shape[0] != n:
+        raise ValueError(f"{name} must hold {n} values")
+    return off.data_ptr()
 
 
 def _attn_common(q, k, v, q_off, k_off, scale):
     hq = _heads(q, "q")
-    hk = _heads(k, "k", q)
-    hv = _heads(v, "v", q, k.shape)
-    if k.shape[2] != q.shape[2]:
+    dtype, device, sq = q.dtype, q.get_device(), q.shape
+    hk = _heads(k, "k", dtype, device)
+    sk = k.shape
+    hv = _heads(v, "v", dtype, device, sk)
+    if sk[2] != sq[2]:
         raise ValueError("q, k and v must have one head_dim")
-    device = q.get_device()
-    n = _offsets(q_off, "q_off", device) - 1
+    qp = kp = _offsets(q_off, "q_off", device)
+    n = q_off.shape[0] - 1
     if n < 0:
         raise ValueError("q_off must hold one more offset than there are sequences")
-    if k_off is None:
-        k_off = q_off
-    elif _offsets(k_off, "k_off", device) != n + 1:
-        raise ValueError("k_off must have q_off's length")
-    if q.dtype not in _DTYPES:
+    if k_off is not None:
+        kp = _offsets(k_off, "k_off", device, n + 1)
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise ValueError("rows must be float16 or bfloat16")
-    return hq, hk, hv, k_off, q.shape[2] ** -0.5 if scale is None else scale
+    return hq, hk, hv, dtype, device, sq, sk, qp, kp, n, code, sq[2] ** -0.5 if scale is None else scale
 
 
 def sc_attn_fwd(q, k, v, q_off, k_off=None, k_len=None, causal: bool = False, scale: float | None = None,
@@ -640,17 +680,15 @@ def sc_attn_fwd(q, k, v, q_off, k_off=None, k_len=None, causal: bool = False, sc
     q_off[s+1] and key rows k_off[s] .. k_off[s+1] (default: q_off), or k_len[s]
     rows from k_off[s] on.  causal: query i sees keys 0 .. i + keys - queries.
     scale: default head_dim^-0.5.  return_lse: (out, lse float32 [t_q, heads_q])."""
-    hq, hk, hv, k_off, scale = _attn_common(q, k, v, q_off, k_off, scale)
-    n = q_off.shape[0] - 1
-    if k_len is not None and _offsets(k_len, "k_len", q.get_device()) != n:
-        raise ValueError("k_len must hold one length a sequence")
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ho = _heads(out, "out", q, q.shape)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
-    _check(lib().sc_attn_fwd(_ref(hq), _ref(hk), _ref(hv), _ref(ho), _ptr(lse), _ptr(q_off), _ptr(k_off),
-                             _ptr(k_len), n, q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2], scale,
-                             _DTYPES[q.dtype], SC_ATTN_CAUSAL if causal else 0, _stream(stream)), "sc_attn_fwd")
+    hq, hk, hv, dtype, device, sq, sk, qp, kp, n, code, scale = _attn_common(q, k, v, q_off, k_off, scale)
+    lp = None if k_len is None else _offsets(k_len, "k_len", device, n)
+    out, ho = _rows_out(out, "out", q, sq, dtype, device)
+    lse = torch.empty(sq[:2], dtype=torch.float32, device=q.device) if return_lse else None
+    st = (_lib or lib()).sc_attn_fwd(hq, hk, hv, ho, lse.data_ptr() if return_lse else None, qp, kp, lp, n, sq[0],
+                                     sk[0], sq[1], sk[1], sq[2], scale, code, SC_ATTN_CAUSAL if causal else 0,
+                                     _raw_stream(stream))
+    if st:
+        _check(st, "sc_attn_fwd")
     return (out, lse) if return_lse else out
 
 
@@ -658,19 +696,18 @@ def sc_attn_bwd(gout, q, k, v, out, lse, q_off, k_off=None, causal: bool = False
                 gq=None, gk=None, gv=None, stream=None):
     """(gq, gk, gv): gradients of sc_attn_fwd's inputs from gout, that of its
     output, with the forward's out and lse.  gq, gk, gv: where to write."""
-    hq, hk, hv, k_off, scale = _attn_common(q, k, v, q_off, k_off, scale)
-    hg, ho = _heads(gout, "gout", q, q.shape), _heads(out, "out", q, q.shape)
-    if (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.device != q.device
-            or lse.shape != q.shape[:2]):
-        raise ValueError("lse must be the forward's float32 [t_q, heads_q]")
-    _dev(lse, "lse")
-    gq, gk, gv = (torch.empty(x.shape, dtype=q.dtype, device=q.device) if g is None else g
-                  for g, x in ((gq, q), (gk, k), (gv, v)))
-    oq, ok, ov = (_heads(g, n, q, x.shape) for g, n, x in ((gq, "gq", q), (gk, "gk", k), (gv, "gv", v)))
-    _check(lib().sc_attn_bwd(_ref(hg), _ref(hq), _ref(hk), _ref(hv), _ref(ho), _ptr(lse), _ref(oq), _ref(ok),
-                             _ref(ov), _ptr(q_off), _ptr(k_off), q_off.shape[0] - 1, q.shape[0], k.shape[0],
-                             q.shape[1], k.shape[1], q.shape[2], scale, _DTYPES[q.dtype],
-                             SC_ATTN_CAUSAL if causal else 0, _stream(stream)), "sc_attn_bwd")
+    hq, hk, hv, dtype, device, sq, sk, qp, kp, n, code, scale = _attn_common(q, k, v, q_off, k_off, scale)
+    hg, ho = _heads(gout, "gout", dtype, device, sq), _heads(out, "out", dtype, device, sq)
+    if (not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32 or lse.get_device() != device
+            or lse.shape != sq[:2] or not lse.is_contiguous()):
+        raise ValueError("lse must be the forward's contiguous float32 [t_q, heads_q]")
+    gq, oq = _rows_out(gq, "gq", q, sq, dtype, device)
+    gk, ok = _rows_out(gk, "gk", k, sk, dtype, device)
+    gv, ov = _rows_out(gv, "gv", v, sk, dtype, device)
+    st = (_lib or lib()).sc_attn_bwd(hg, hq, hk, hv, ho, lse.data_ptr(), oq, ok, ov, qp, kp, n, sq[0], sk[0], sq[1],
+                                     sk[1], sq[2], scale, code, SC_ATTN_CAUSAL if causal else 0, _raw_stream(stream))
+    if st:
+        _check(st, "sc_attn_bwd")
     return gq, gk, gv
 
 
