@@ -47,7 +47,11 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
 //
 // The keys of a unit are cut where the card would otherwise wait for it: with
 // fewer than two units an SM into about `over` parts an SM, else only units dearer
-// than an SM's share.  A part costs its fp32 rows written and read once more.
+// than an SM's share.  A part costs its fp32 rows written and read once more (four
+// scenes' 100 queries, 32 units, with a join slower than today's: four parts an SM
+// 228 us in all, three 227, two 244).  One block, because the list is short and a second
+// launch would cost more: 10 to 13 us between events around it, part of which the
+// next kernel's start overlaps.
 __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs pa, const PlanArgs pb) {
   const PlanArgs& p = blockIdx.x ? pb : pa;
   __shared__ int s_q[kPlanThreads + 1], s_k0[kPlanThreads], s_k1[kPlanThreads], s_pre[kPlanThreads + 1];

@@ -14,7 +14,19 @@
 // P and dS go back to TMEM, rounded to 16 bits, as the first operand of the
 // second products; sums stay in TMEM in fp32.  f16 has few bits below 2^-14 and
 // a weight of a list of thousands lies there, so P is held times 2^8 (at most
-// 256); dS, whose size the caller's loss scale sets, as it is.
+// 256); dS, whose size the caller's loss scale sets, as it is.  delta is taken
+// from `out` as the forward rounded it.  These two roundings are what gq and gk
+// are off by (1.6 to 1.9 times the error of an fp32 computation rounded once).
+//
+// What bounds them.  A step is a chain: S, P, dP, dS, product, each part waiting
+// for the one before; the tensor cores are busy 58 % (gk, gv) and 49 % (gq) of an
+// SM's time at 128 values and 22 % and 18 % at 32, where the exponentials, the
+// conversions and, for gk and gv, the row statistics read from shared memory by
+// every key's lane (47 % of that path) take as long as the products.  Kernel
+// times: five documents of 100 to 3500 tokens, causal, 16 query and 4 key heads of
+// 128, bf16: 126 us and 98 us; 96 windows of 300 to 1000 voxels, 8 heads of 32,
+// f16: 207 us and 191 us.  Measured and left out: tiles of 64 rows by two groups
+// of warps (287 and 224 us for the windows).
 #include "attn_device.cuh"
 
 namespace sc {
@@ -105,7 +117,8 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b) {
   return fmaf(x.x, y.x, x.y * y.y);
 }
 
-// delta = gout . out and lse in powers of two, LPR lanes a row.
+// delta = gout . out and lse in powers of two, LPR lanes a row.  Memory bounds it
+// (both are read once; 489000 rows of 32 values: 17 us).
 template <bool BF16, int LPR>
 __global__ void __launch_bounds__(256) k_attn_stat(const StatParams p) {
   grid_release();
@@ -868,7 +881,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 // gk and gv of the key tiles whose rows were cut: the parts' sums in order, a
-// row a warp, four values a lane.
+// row a warp, four values a lane.  Memory bounds it; 12 us for the five documents.
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_attn_bwd_join(const BwdParams p, const AttnItem* joins) {
   grid_wait();

@@ -9,14 +9,22 @@
 // norm: g = R^T gy, h = g w, gx = r (h - x r mean(h x r)), gw = sum g x r.
 //
 // Every value is read once and written once and takes about ten operations, so
-// memory bounds it.  A row lies in a group of LPR lanes, eight consecutive
-// values (one 16-byte load of 16-bit types) a lane, so the norm is a sum over
-// the group by shuffles; the partner of a pair comes from the lane that holds
-// it.  A group takes one token's heads, or some of them, one after the other,
-// four rows' loads in flight: a lane's angles are the same for all heads of a
-// token, so it works them out once and keeps them, with the weights folded in,
-// in registers (a table in shared memory, read for every row, made the kernel
-// three times slower).
+// memory should bound it; what comes near is the instructions a value takes.  A
+// row lies in a group of LPR lanes, eight consecutive values (one 16-byte load of
+// 16-bit types) a lane, so the norm is a sum over the group by shuffles; the
+// partner of a pair comes from the lane that holds it.  A group takes one token's
+// heads, or some of them, one after the other: a lane's angles are the same for
+// all heads of a token, so it works them out once and keeps them, with the weights
+// folded in, in registers (read from a table for every row they made the kernel
+// three times slower).  The forward has four rows' loads in flight and four blocks
+// an SM; the gradient, which needs twice the registers, has two blocks an SM and
+// its rows copied to shared memory two steps ahead (the forward was slower that
+// way: 241 us instead of 207 for the voxels below).
+//
+// Kernel times: 32768 tokens, 32 + 8 heads of 128, bf16: 126 us, 5.3 TB/s; 480000
+// tokens, 4 + 4 heads of 64 turned by three axes, f16: forward 198 us (5.0 TB/s; issue
+// slots 62 % busy, DRAM 54 %, no one unit), gradient 265 us (5.6 TB/s; 368 us with the
+// angles worked out for each side and one value an instruction, issue bound).
 #include "f32x2.cuh"
 #include "sc_internal.cuh"
 #include "tc_ptx.cuh"
