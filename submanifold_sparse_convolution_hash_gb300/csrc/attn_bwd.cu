@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kBwdThreads = 640;
 constexpr int kBwdMaxStages = 12;
+constexpr int kMinPartTiles = 8;  // least row tiles of a part
 // gk, gv: registers a thread as launched; four warps drop, sixteen raise.
 constexpr int kKvRegs = 96, kKvSideRegs = 64, kKvMainRegs = 104;
 static_assert(128 * kKvSideRegs + 512 * kKvMainRegs <= kBwdThreads * kKvRegs, "no more than the block has");
@@ -948,13 +949,14 @@ sc_status attn_bwd(const AttnArgs& a) {
   Arena ar;
   const size_t o_hq = ar.take(kPlanHeader * sizeof(int)), o_hk = ar.take(kPlanHeader * sizeof(int));
   const size_t o_iq = ar.take(static_cast<size_t>(q_items) * sizeof(AttnItem));
-  const int64_t k_cap = k_items + (k_items * a.heads_kv <= 8ll * sms ? 2ll * sms / a.heads_kv + 2 : 0);
+  // Partial gk and gv: room for two an SM where the key tiles are few (the plan
+  // cuts those that are dearer than an SM's share) and a sequence may have more
+  // rows than a part.
+  const bool cut = k_items * a.heads_kv <= 8ll * sms && a.t_q > static_cast<int64_t>(kMinPartTiles) * pos;
+  const int64_t slots = cut ? 2ll * sms / a.heads_kv + 2 : 0;
+  const int64_t k_cap = k_items + slots;
   const size_t o_ik = ar.take(static_cast<size_t>(k_cap) * sizeof(AttnItem));
   const size_t o_st = ar.take(static_cast<size_t>(a.t_q) * a.heads_q * sizeof(float2));
-  // Partial gk and gv: room for two an SM where the key tiles are few (the plan
-  // cuts those that are dearer than an SM's share).
-  const bool cut = k_items * a.heads_kv <= 8ll * sms;
-  const int64_t slots = cut ? 2ll * sms / a.heads_kv + 2 : 0;
   const size_t o_joins = ar.take(cut ? static_cast<size_t>(k_items) * sizeof(AttnItem) : 0);
   const size_t o_part = ar.take(static_cast<size_t>(slots) * a.heads_kv * 256 * a.head_dim * sizeof(float));
   int* status = attn_status_word();
@@ -1005,7 +1007,7 @@ sc_status attn_bwd(const AttnArgs& a) {
   plk.cap = static_cast<int>(k_cap);
   plk.part_rows = slots * a.heads_kv * kKeyTile;
   plk.over = 1;
-  plk.min_tiles = 8;
+  plk.min_tiles = kMinPartTiles;
   plk.join_cap = cut ? static_cast<int>(k_items) : 0;
   plk.joins = reinterpret_cast<AttnItem*>(base + o_joins);
   plk.header = reinterpret_cast<int*>(base + o_hk);

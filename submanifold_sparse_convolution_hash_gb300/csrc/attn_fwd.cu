@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kFwdThreads = 384;
 constexpr int kFwdMaxStages = 10;
+constexpr int kMinPartTiles = 4;  // least key tiles of a part
 constexpr float kLn2 = 0.6931471805599453f;
 // K and V tiles in flight: 160 KB of them beside the two Q tiles.
 constexpr int fwd_stages(int dp) { return dp == 64 ? 10 : 5; }
@@ -563,12 +564,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, kDevErrTimeout);
 }
 
-// Memory bounds it: every part's fp32 rows are read once (four scenes' 100
-// queries in 38 parts each, 35 MB: 19 us, 29 with one part at a time).
-//
 // Joins the parts of the rows whose keys were cut, a warp a row, four values a
-// lane (to 64 values two parts at a time): with m the largest of the parts' maxima, out = sum O_q f_q / sum l_q f_q,
-// f_q = exp(scale (m_q - m)).  The parts are taken in order, whoever made them.
+// lane (to 64 values two parts at a time): with m the largest of the parts'
+// maxima, out = sum O_q f_q / sum l_q f_q, f_q = exp(scale (m_q - m)).  The parts
+// are taken in order, whoever made them.  Memory bounds it: every part's fp32 rows
+// are read once (four scenes' 100 queries in 38 parts each, 35 MB: 19 us, 29 with
+// one part at a time).
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const AttnItem* joins) {
   grid_wait();
@@ -657,12 +658,15 @@ sc_status attn_fwd(const AttnArgs& a) {
   // Partial results: room for about four parts an SM and two an item, where an
   // item has few rows (a guess from the average; the plan sees whether they
   // fit) or the items are few.
-  // no list over 128 keys: nothing to cut, and the join is not launched
   const int64_t avg = a.n_seq ? (a.t_q * g + a.n_seq - 1) / a.n_seq : 0;
   const bool few = items_ub * a.heads_kv <= 8ll * sms;
   const int64_t rows_guess = few ? 2 * pos * g : 2 * avg;
   const int64_t slots = 8ll * sms / a.heads_kv + 2 + 2 * items_ub;
-  int64_t part_rows = a.t_k > kKeyTile && (few || avg <= 32) ? slots * a.heads_kv * (rows_guess < 2 * pos * g ? rows_guess : 2 * pos * g) : 0;
+  // On average at most one row tile a sequence: the form whose halves share one.
+  const bool one = avg <= 128;
+  // no list of more keys than a part (a half) has: nothing to cut, and the join is not launched
+  const bool cuts = a.t_k > (one ? 1 : kMinPartTiles) * kKeyTile && (few || avg <= 32);
+  int64_t part_rows = cuts ? slots * a.heads_kv * (rows_guess < 2 * pos * g ? rows_guess : 2 * pos * g) : 0;
   const int64_t row_bytes = (a.head_dim + 8) * 4ll;
   if (part_rows * row_bytes > (int64_t(1) << 28)) part_rows = (int64_t(1) << 28) / row_bytes;
   const int64_t cap = items_ub + (part_rows ? slots : 0);
@@ -677,8 +681,6 @@ sc_status attn_fwd(const AttnArgs& a) {
   const size_t tile = static_cast<size_t>(dp) / 64 * 16384;
   FwdParams p{};
   const size_t smem = (2 + fwd_stages(dp)) * tile + sizeof(FwdSmem) + 1024;
-  // On average at most one row tile a sequence: the form whose halves share one.
-  const bool one = avg <= 128;
   const void* kern = a.dtype == SC_BF16 ? (one ? fwd_kernel<true, true>(dp) : fwd_kernel<true, false>(dp))
                                         : (one ? fwd_kernel<false, true>(dp) : fwd_kernel<false, false>(dp));
   int regs = 0;
@@ -714,7 +716,7 @@ sc_status attn_fwd(const AttnArgs& a) {
   pl.sms = sms;
   pl.over = 4;
   pl.part_rows = part_rows;
-  pl.min_tiles = 4;
+  pl.min_tiles = kMinPartTiles;
   pl.dual = one;
   pl.cap = static_cast<int>(cap);
   pl.join_cap = part_rows ? static_cast<int>(items_ub) : 0;
