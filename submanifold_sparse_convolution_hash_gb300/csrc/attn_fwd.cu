@@ -516,20 +516,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (it.slot < 0) {
         const float inv = vis > 0 ? 1.f / l : 0.f;  // a row that sees no key: 0
         uint8_t* dst = p.out + tok * p.out_t + h * p.out_h;
-        for (int c = 0; c < p.d; c += 16) {
-          uint32_t o[16];
-          if (have) {
-            tmem_ld16_raw(to + c, o);
-          }
-          uint32_t w[8];
+#pragma unroll 1
+        for (int c = 0; c < p.d; c += 32) {  // O has whole 32s of columns
+          uint32_t o[32], w[16];
+          if (have) tmem_ld32_raw(to + c, o);
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
+          for (int u = 0; u < 16; ++u)
             w[u] = have && vis > 0 ? pack_pair<BF16>(__uint_as_float(o[2 * u]) * inv, __uint_as_float(o[2 * u + 1]) * inv)
                                    : 0u;
-          if (live) {
-            *reinterpret_cast<uint4*>(dst + c * 2) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (c + 8 < p.d) *reinterpret_cast<uint4*>(dst + c * 2 + 16) = make_uint4(w[4], w[5], w[6], w[7]);
-          }
+#pragma unroll
+          for (int u = 0; u < 16; u += 4)
+            if (live && c + 2 * u < p.d)
+              *reinterpret_cast<uint4*>(dst + c * 2 + u * 4) = make_uint4(w[u], w[u + 1], w[u + 2], w[u + 3]);
         }
         if (p.lse && live) p.lse[tok * p.heads_q + h] = vis > 0 ? base * kLn2 + logf(l) : -INFINITY;
       } else {
@@ -540,12 +538,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           dst[p.d] = have ? m : -INFINITY;
           dst[p.d + 1] = l;
         }
-        for (int c = 0; c < p.d && have; c += 16) {
-          uint32_t o[16];
-          tmem_ld16_raw(to + c, o);
+#pragma unroll 1
+        for (int c = 0; c < p.d && have; c += 32) {
+          uint32_t o[32];
+          tmem_ld32_raw(to + c, o);
           if (live) {
 #pragma unroll
-            for (int u = 0; u < 16; u += 4)
+            for (int u = 0; u < 32; u += 4)
               if (c + u < p.d) *reinterpret_cast<uint4*>(dst + c + u) = make_uint4(o[u], o[u + 1], o[u + 2], o[u + 3]);
           }
         }
