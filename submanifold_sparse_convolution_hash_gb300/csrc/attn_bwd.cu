@@ -16,7 +16,8 @@
 // a weight of a list of thousands lies there, so P is held times 2^8 (at most
 // 256); dS, whose size the caller's loss scale sets, as it is.  delta is taken
 // from `out` as the forward rounded it.  These two roundings are what gq and gk
-// are off by (1.6 to 1.9 times the error of an fp32 computation rounded once).
+// are off by (1.6 to 1.9 times the error of an fp32 computation rounded once, up to 2.5 where a
+// few keys take most of the weight and dP - delta cancels).
 //
 // What bounds them.  A step is a chain: S, P, dP, dS, product, each part waiting
 // for the one before; the tensor cores are busy 58 % (gk, gv) and 49 % (gq) of an

@@ -15,7 +15,7 @@
 //
 // What bounds it, with kernel times.  Long lists at 128 values: the tensor cores
 // and the chain S, maximum, exponentials, P, O of the two row tiles that share
-// them (16384 tokens, causal, 32 query and 8 key heads, bf16: 1325 us, 1.66
+// them (16384 tokens, causal, 32 query and 8 key heads, bf16: 1299 us, 1.69
 // PFLOP/s of the 1.97 that a library product reaches).  Heads of 32 or 64 values
 // have the same exponentials for a half or a quarter of the products, and that
 // chain bounds them (160 windows of 500 to 1000 voxels, 4 heads of 64, f16: 161
