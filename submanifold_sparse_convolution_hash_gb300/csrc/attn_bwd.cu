@@ -27,7 +27,8 @@
 // times: five documents of 100 to 3500 tokens, causal, 16 query and 4 key heads of
 // 128, bf16: 126 us and 98 us; 96 windows of 300 to 1000 voxels, 8 heads of 32,
 // f16: 207 us and 191 us.  Measured and left out: tiles of 64 rows by two groups
-// of warps (287 and 224 us for the windows).
+// of warps (287 and 224 us for the windows); the next dP made as soon as this one
+// has been read, with dS beside P (209 and 196 us).
 #include "attn_device.cuh"
 
 namespace sc {
