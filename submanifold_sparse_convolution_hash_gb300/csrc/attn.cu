@@ -80,41 +80,41 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs pa, c
       const int cnt = min(kPlanThreads, p.n_seq - c0);
       int total = s_pre[cnt];  // one run: it stays from the first pass
       if (pass == 0 || p.n_seq > kPlanThreads) {
-      __syncthreads();
-      int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-      if (tid < cnt) {
-        const int s = c0 + tid;
-        q0 = __ldg(p.q_off + s);
-        q1 = __ldg(p.q_off + s + 1);
-        k0 = __ldg(p.k_off + s);
-        k1 = p.k_len ? k0 : __ldg(p.k_off + s + 1);
-        bool bad = false;
-        if (p.k_len) {
-          const int len = __ldg(p.k_len + s);
-          bad = len < 0 || k0 < 0 || k0 + static_cast<int64_t>(len) > p.t_k;
-          if (!bad) k1 = k0 + len;
+        __syncthreads();
+        int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+        if (tid < cnt) {
+          const int s = c0 + tid;
+          q0 = __ldg(p.q_off + s);
+          q1 = __ldg(p.q_off + s + 1);
+          k0 = __ldg(p.k_off + s);
+          k1 = p.k_len ? k0 : __ldg(p.k_off + s + 1);
+          bool bad = false;
+          if (p.k_len) {
+            const int len = __ldg(p.k_len + s);
+            bad = len < 0 || k0 < 0 || k0 + static_cast<int64_t>(len) > p.t_k;
+            if (!bad) k1 = k0 + len;
+          }
+          bad = bad || q0 < 0 || q1 < q0 || q1 > p.t_q || k0 < 0 || k1 < k0 || k1 > p.t_k;
+          bad = bad || (s == 0 && q0 != 0) || (s == p.n_seq - 1 && q1 != p.t_q);
+          if (p.packed_keys) bad = bad || (s == 0 && k0 != 0) || (s == p.n_seq - 1 && k1 != p.t_k);
+          if (bad) s_bad = 1;
+          s_q[tid] = q0;
+          s_k0[tid] = k0;
+          s_k1[tid] = k1;
+          if (tid == cnt - 1) s_q[cnt] = q1;
         }
-        bad = bad || q0 < 0 || q1 < q0 || q1 > p.t_q || k0 < 0 || k1 < k0 || k1 > p.t_k;
-        bad = bad || (s == 0 && q0 != 0) || (s == p.n_seq - 1 && q1 != p.t_q);
-        if (p.packed_keys) bad = bad || (s == 0 && k0 != 0) || (s == p.n_seq - 1 && k1 != p.t_k);
-        if (bad) s_bad = 1;
-        s_q[tid] = q0;
-        s_k0[tid] = k0;
-        s_k1[tid] = k1;
-        if (tid == cnt - 1) s_q[cnt] = q1;
-      }
-      __syncthreads();
-      if (s_bad) break;
-      int tiles = 0;
-      if (tid < cnt)
-        tiles = p.mode == kPlanRows ? (q1 - q0 + p.pos_per_item - 1) / p.pos_per_item
-                                    : (k1 - k0 + kKeyTile - 1) / kKeyTile;
-      s_pre[tid] = block_scan(tiles, s_warp, &total);
-      if (tid == 0) {
-        s_pre[cnt] = total;  // cnt == kPlanThreads: its own place
-        if (pass == 0) s_items += total;
-      }
-      __syncthreads();
+        __syncthreads();
+        if (s_bad) break;
+        int tiles = 0;
+        if (tid < cnt)
+          tiles = p.mode == kPlanRows ? (q1 - q0 + p.pos_per_item - 1) / p.pos_per_item
+                                      : (k1 - k0 + kKeyTile - 1) / kKeyTile;
+        s_pre[tid] = block_scan(tiles, s_warp, &total);
+        if (tid == 0) {
+          s_pre[cnt] = total;  // cnt == kPlanThreads: its own place
+          if (pass == 0) s_items += total;
+        }
+        __syncthreads();
       }
       for (int u = tid; u < total; u += kPlanThreads) {
         int lo = 0, hi = cnt - 1;  // the sequence with s_pre[lo] <= u < s_pre[lo + 1]

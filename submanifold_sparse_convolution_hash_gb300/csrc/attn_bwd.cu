@@ -979,10 +979,11 @@ sc_status attn_bwd(const AttnArgs& a) {
   CUtensorMap qm, gm, km, vm;
   const int hq = have_q ? a.heads_q : 1, hk = have_k ? a.heads_kv : 1;
   const int64_t tq = have_q ? a.t_q : 1, tk = have_k ? a.t_k : 1;
-  if ((st = attn_map(&qm, have_q ? a.q.data : any, a.dtype, a.head_dim, hq, tq, a.q.token_stride, a.q.head_stride, g, pos)) ||
-      (st = attn_map(&gm, have_q ? a.gout.data : any, a.dtype, a.head_dim, hq, tq, a.gout.token_stride, a.gout.head_stride, g, pos)) ||
-      (st = attn_map(&km, have_k ? a.k.data : any, a.dtype, a.head_dim, hk, tk, a.k.token_stride, a.k.head_stride, 1, kKeyTile)) ||
-      (st = attn_map(&vm, have_k ? a.v.data : any, a.dtype, a.head_dim, hk, tk, a.v.token_stride, a.v.head_stride, 1, kKeyTile)))
+  const auto map_of = [&](CUtensorMap* m, const sc_heads& v, bool have, int heads, int64_t tokens, int bh, int bt) {
+    return attn_map(m, have ? v.data : any, a.dtype, a.head_dim, heads, tokens, v.token_stride, v.head_stride, bh, bt);
+  };
+  if ((st = map_of(&qm, a.q, have_q, hq, tq, g, pos)) || (st = map_of(&gm, a.gout, have_q, hq, tq, g, pos)) ||
+      (st = map_of(&km, a.k, have_k, hk, tk, 1, kKeyTile)) || (st = map_of(&vm, a.v, have_k, hk, tk, 1, kKeyTile)))
     return st;
   void* ws = nullptr;
   if ((st = dev_alloc(&ws, ar.bytes, a.stream))) return st;

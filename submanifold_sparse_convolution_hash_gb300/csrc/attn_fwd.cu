@@ -533,7 +533,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       } else {
         // a part of the keys: O, m and l in fp32 for k_attn_join
         const int part = it.slot + (dual ? 2 * it.split + s : it.split);
-        float* dst = p.part + ((static_cast<int64_t>(part) * p.heads_kv + head) * __ldcg(p.header + 3) + i * p.g + gh) * (p.d + 8);
+        const int64_t first = (static_cast<int64_t>(part) * p.heads_kv + head) * __ldcg(p.header + 3);
+        float* dst = p.part + (first + i * p.g + gh) * (p.d + 8);
         if (live) {
           dst[p.d] = have ? m : -INFINITY;
           dst[p.d + 1] = l;

@@ -358,7 +358,7 @@ __device__ __forceinline__ void copies_left() {
 template <typename T, int LPR, int NSRC>
 struct Rows {
   static constexpr int NW = Vec8<T>::kWords, Q = NW / 4, U = sizeof(T) == 4 ? 1 : 2, ST = 4;
-  static constexpr int kBytes = ST * U * NSRC * Q * 16 * kThreads;
+  static constexpr int bytes() { return ST * U * NSRC * Q * 16 * kThreads; }
   uint32_t mine, put = 0, got = 0;  // stages
   int64_t blk, blocks, count;
   int side, last, i, n, left;       // side: the next rows'; last: of a unit
@@ -655,7 +655,7 @@ using Kern = void (*)(RopeParams);
 
 template <typename T>
 size_t ring_bytes(bool norm) {
-  return norm ? Rows<T, 8, 2>::kBytes : Rows<T, 8, 1>::kBytes;
+  return norm ? Rows<T, 8, 2>::bytes() : Rows<T, 8, 1>::bytes();
 }
 
 template <typename T, int LPR, int PAIRING>
@@ -747,7 +747,8 @@ sc_status rope_run(const RopeArgs& a) {
   if (steps > 0x7fffffff) return set_error(SC_ERR_UNSUPPORTED, "too many tokens");
   if (!bwd) {
     const int64_t most_blocks = 4ll * sms;  // as many as are resident
-    SC_LAUNCH("qk_norm_rope_fwd", a.stream, (k<<<static_cast<unsigned>(steps < most_blocks ? steps : most_blocks), kThreads, 0, a.stream>>>(p)));
+    const unsigned grid = static_cast<unsigned>(steps < most_blocks ? steps : most_blocks);
+    SC_LAUNCH("qk_norm_rope_fwd", a.stream, (k<<<grid, kThreads, 0, a.stream>>>(p)));
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SC_OK : set_cuda_error(e, "qk_norm_rope_fwd");
   }
