@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t n = 0;
     while (ring.next(&it, &head, abort_flag, true)) {
       if (it.kt1 == 0 || it.lk - (it.kt1 - 1) * kKeyTile >= kKeyTile) continue;
-      if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sm->fix_k), n & 1))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_unit(smem_u32(&sm->fix_k), n & 1, abort_flag))) {
         sm->abort = 1;
         break;
       }

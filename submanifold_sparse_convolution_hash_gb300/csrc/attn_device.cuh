@@ -120,9 +120,9 @@ __device__ __forceinline__ void hand_out(ItemSlots* sl, int* counter, const Attn
                                          volatile int* abort_flag) {
   for (uint32_t n = 0;; ++n) {
     const int slot = n & 1;
-    const bool asked = mbar_wait_inl(smem_u32(&sl->ask), n & 1);
+    const bool asked = mbar_wait_unit(smem_u32(&sl->ask), n & 1, abort_flag);
     const int u = atomicAdd(counter, 1);
-    if (!asked || !mbar_wait_inl(smem_u32(&sl->empty[slot]), ((n >> 1) & 1) ^ 1)) {
+    if (!asked || !mbar_wait_unit(smem_u32(&sl->empty[slot]), ((n >> 1) & 1) ^ 1, abort_flag)) {
       *abort_flag = 1;
       break;
     }
@@ -148,7 +148,7 @@ struct ItemRing {
   __device__ __forceinline__ bool next(AttnItem* it, int* head, volatile int* abort_flag, bool warp) {
     const int slot = n & 1;
     if (!warp) mbar_arrive(smem_u32(&sl->ask));
-    bool ok = mbar_wait_inl(smem_u32(&sl->full[slot]), (n >> 1) & 1);
+    bool ok = mbar_wait_unit(smem_u32(&sl->full[slot]), (n >> 1) & 1, abort_flag);
     if (warp) ok = __all_sync(0xffffffffu, ok);
     if (!ok) {
       *abort_flag = 1;
@@ -165,7 +165,7 @@ struct ItemRing {
   // is no more; it stays until release().
   __device__ __forceinline__ const AttnItem* peek(volatile int* abort_flag) {
     const int slot = n & 1;
-    if (!__all_sync(0xffffffffu, mbar_wait_inl(smem_u32(&sl->full[slot]), (n >> 1) & 1))) {
+    if (!__all_sync(0xffffffffu, mbar_wait_unit(smem_u32(&sl->full[slot]), (n >> 1) & 1, abort_flag))) {
       *abort_flag = 1;
       return nullptr;
     }

@@ -60,18 +60,23 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity, abort_flag);
 }
 // A wait in few instructions, for kernels whose warps run different code: the
-// instruction caches are what such code fights over.  The hardware suspends the
-// thread for up to a millisecond a try; about two seconds in all.
+// instruction caches are what such code fights over.  A try that finds nothing
+// comes back after about four microseconds, whatever longer hint it is given, so
+// the bound is a time: two steps of the global timer's upper half, four to nine
+// seconds.
 __device__ __forceinline__ bool mbar_wait_inl(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 0;\n\t"
-      "WAIT_%=:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 t0, t;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "@p bra DONE_%=;\n\t"
-      "add.u32 n, n, 1;\n\t"
-      "setp.lt.u32 q, n, 2000;\n\t"
+      "mov.u32 t0, %%globaltimer_hi;\n\t"
+      "WAIT_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "mov.u32 t, %%globaltimer_hi;\n\t"
+      "sub.u32 t, t, t0;\n\t"
+      "setp.lt.u32 q, t, 2;\n\t"
       "@q bra WAIT_%=;\n\t"
       "DONE_%=:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
@@ -90,19 +95,24 @@ __device__ __noinline__ bool mbar_drain(uint32_t bar, uint32_t parity) {
   return false;
 }
 // Two waits at once: their tries are in flight together (one that finds its
-// phase complete still takes about ninety cycles).
+// phase complete still takes about ninety cycles).  The same bound.
 __device__ __forceinline__ bool mbar_wait2_inl(uint32_t bar_a, uint32_t par_a, uint32_t bar_b, uint32_t par_b) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 0;\n\t"
-      "WAIT_%=:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4, 1000000;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 t0, t;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
       "and.pred p, p, q;\n\t"
       "@p bra DONE_%=;\n\t"
-      "add.u32 n, n, 1;\n\t"
-      "setp.lt.u32 q, n, 1000;\n\t"
+      "mov.u32 t0, %%globaltimer_hi;\n\t"
+      "WAIT_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "mov.u32 t, %%globaltimer_hi;\n\t"
+      "sub.u32 t, t, t0;\n\t"
+      "setp.lt.u32 q, t, 2;\n\t"
       "@q bra WAIT_%=;\n\t"
       "DONE_%=:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
@@ -110,6 +120,20 @@ __device__ __forceinline__ bool mbar_wait2_inl(uint32_t bar_a, uint32_t par_a, u
       : "r"(bar_a), "r"(par_a), "r"(bar_b), "r"(par_b)
       : "memory");
   return ok != 0;
+}
+// A wait that lasts as long as a whole unit of work of other warps, which may be
+// seconds: it gives up when another wait of the block has (`abort_flag`), within
+// some milliseconds, and after four to five minutes by itself.
+__device__ __forceinline__ bool mbar_wait_unit(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  uint32_t t0, t;
+  asm volatile("mov.u32 %0, %%globaltimer_hi;" : "=r"(t0));
+  do {
+#pragma unroll 1
+    for (int i = 0; i < 1024; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    asm volatile("mov.u32 %0, %%globaltimer_hi;" : "=r"(t));
+  } while (!*abort_flag && t - t0 < 64);
+  return false;
 }
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),

@@ -1,0 +1,37 @@
+"""GPU tests of the token-row operators where values, sizes or layouts are at
+their limits.  Tolerances are fixed from the formats as in test_gpu_tokens.py;
+what differs is stated at each test."""
+import pytest
+import torch
+
+from submanifold_sparse_convolution_hash_gb300 import binding as sc
+from test_gpu_tokens import U
+
+pytestmark = pytest.mark.gpu
+
+
+def _grads64(q, k, v, gout, scale):
+    """Gradients of one sequence and one head in 64 bits, on the device."""
+    q, k, v, g = (x[:, 0].double() for x in (q, k, v, gout))
+    p = torch.softmax(q @ k.T * scale, 1)
+    gv = p.T @ g
+    ds = g @ v.T
+    ds -= (g * (p @ v)).sum(1, keepdim=True)
+    ds *= p
+    return ds @ k * scale, ds.T @ q * scale, gv
+
+
+def test_attention_gradient_of_a_list_that_one_block_walks():
+    """The keys of gq's rows are not cut: one query on a million keys is 7,813 steps of one block, far past
+    what any one wait may take if it covered them all."""
+    n, d = 1_000_000, 32
+    g = torch.Generator(device="cuda").manual_seed(9)
+    q, gout = (torch.randn((1, 1, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    k, v = (torch.randn((n, 1, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    off, koff = (torch.tensor([0, m], dtype=torch.int32).cuda() for m in (1, n))
+    o, l = sc.sc_attn_fwd(q, k, v, off, k_off=koff, return_lse=True)
+    gq, gk, gv = sc.sc_attn_bwd(gout, q, k, v, o, l, off, k_off=koff)
+    sc.sc_attn_check()
+    wq, wk, wv = _grads64(q, k, v, gout, d ** -0.5)
+    for got, want in ((gk, wk), (gv, wv), (gq, wq)):
+        assert float((got[:, 0].double() - want).norm() / want.norm()) <= 3 * U["bf16"]
