@@ -71,6 +71,12 @@ sc_status rope_call(const sc_heads* gout[2], const sc_heads* x[2], const sc_head
   if (!std::isfinite(amp) || !std::isfinite(eps) || eps < 0.f) return invalid("amp and eps must be finite, eps >= 0");
   const int heads[2] = {heads_q, heads_k};
   const bool norm = w[0] || w[1];
+  if (norm) {  // both are written, that of a side without rows with zeros
+    for (int s = 0; s < 2; ++s) {
+      const sc_status st = gw[s] ? check_dev_ptr(gw[s], 4, "weight gradients") : SC_OK;
+      if (st) return st;
+    }
+  }
   RopeArgs a{};
   if (tokens > 0 && heads_q + heads_k > 0) {
     sc_status st;
@@ -89,7 +95,6 @@ sc_status rope_call(const sc_heads* gout[2], const sc_heads* x[2], const sc_head
       if (!heads[s]) continue;
       if (norm && !w[s]) return invalid("norm weights: both sides that have heads need one, or neither");
       if (norm && (st = check_dev_ptr(w[s], 4, "norm weights"))) return st;
-      if (gw[s] && (st = check_dev_ptr(gw[s], 4, "weight gradients"))) return st;
       if (!y[s] || (bwd && !gout[s])) return invalid(std::string(names[s][2]) + " is NULL");
       if (!bwd || norm) {
         if (!x[s]) return invalid(std::string(names[s][0]) + " is NULL");

@@ -1,6 +1,8 @@
 """GPU tests of the token-row operators where values, sizes or layouts are at
 their limits.  Tolerances are fixed from the formats as in test_gpu_tokens.py;
 what differs is stated at each test."""
+import ctypes
+
 import pytest
 import torch
 
@@ -35,3 +37,24 @@ def test_attention_gradient_of_a_list_that_one_block_walks():
     wq, wk, wv = _grads64(q, k, v, gout, d ** -0.5)
     for got, want in ((gk, wk), (gv, wv), (gq, wq)):
         assert float((got[:, 0].double() - want).norm() / want.norm()) <= 3 * U["bf16"]
+
+
+# ---------------------------------------------------------------- refusals --
+def test_weight_gradients_of_a_side_without_heads_are_looked_at():
+    """They are written (with zeros), so a host address is refused although the side has no rows."""
+    x = torch.zeros((4, 2, 64), dtype=torch.float16, device="cuda")
+    y, w = torch.zeros_like(x), torch.ones(64, device="cuda")
+    gwk = torch.full((64,), 7.0, device="cuda")
+    view = [ctypes.byref(sc._Heads(t.data_ptr(), 128, 64)) for t in (x, y)]
+    host = (ctypes.c_float * 64)()
+
+    def call(gwq):
+        return sc.lib().sc_qk_norm_rope_bwd(None, view[0], None, view[0], None, view[1], gwq, gwk.data_ptr(),
+                                            w.data_ptr(), w.data_ptr(), None, 0, 1, None, 4, 0, 2, 64, 0, 1e-6, 1.0, 1,
+                                            0, torch.cuda.current_stream().cuda_stream)
+
+    assert call(ctypes.addressof(host)) == 1
+    assert b"weight gradients" in sc.lib().sc_last_error()
+    gwq = torch.full((64,), 7.0, device="cuda")
+    assert call(gwq.data_ptr()) == 0
+    assert not gwq.any() and not gwk.any()
