@@ -30,6 +30,9 @@ sc_status check_heads(const char* what, const void* data, int64_t ts, int64_t hs
   if (ts > (int64_t(1) << 36) || hs > (int64_t(1) << 36)) return invalid(std::string(what) + ": stride too large");
   if (tokens <= 1) ts = 0;
   if (heads <= 1) hs = 0;
+  // below 2^48 bytes, so that no offset passes 64 bits here or in the kernels
+  if ((static_cast<double>(tokens - 1) * ts + static_cast<double>(heads - 1) * hs) * eb > 0x1p48)
+    return invalid(std::string(what) + ": rows past the address space");
   if (apart) {
     const bool heads_ok = heads <= 1 || hs >= d;
     const bool tokens_inner = tokens > 1 && heads > 1 && hs >= (tokens - 1) * ts + d && ts >= d;

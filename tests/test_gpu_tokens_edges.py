@@ -58,3 +58,19 @@ def test_weight_gradients_of_a_side_without_heads_are_looked_at():
     gwq = torch.full((64,), 7.0, device="cuda")
     assert call(gwq.data_ptr()) == 0
     assert not gwq.any() and not gwk.any()
+
+
+def test_views_past_the_address_space_are_refused():
+    """Strides and counts that are legal each and together pass 64 bits: refused by the host, nothing runs."""
+    x = torch.zeros((4, 2, 64), dtype=torch.float16, device="cuda")
+    y = torch.zeros_like(x)
+    far = ctypes.byref(sc._Heads(x.data_ptr(), 1 << 36, 64))
+    out = ctypes.byref(sc._Heads(y.data_ptr(), 128, 64))
+    st = sc.lib().sc_qk_norm_rope_fwd(far, None, out, None, None, None, None, 0, 1, None, (1 << 31) - 1, 2, 0, 64, 0,
+                                      1e-6, 1.0, 1, 0, None)
+    assert st == 1 and b"address space" in sc.lib().sc_last_error()
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    near = ctypes.byref(sc._Heads(x.data_ptr(), 128, 64))
+    st = sc.lib().sc_attn_fwd(near, far, near, out, None, off.data_ptr(), off.data_ptr(), None, 1, 4, 1 << 30, 2, 2, 64,
+                              0.1, 1, 0, None)
+    assert st == 1 and b"address space" in sc.lib().sc_last_error()
