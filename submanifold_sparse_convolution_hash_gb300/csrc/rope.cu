@@ -198,8 +198,11 @@ __device__ __forceinline__ void partners(const uint32_t (&w)[Vec8<T>::kWords], u
                                          T* stage) {
   constexpr int NW = Vec8<T>::kWords;
   if constexpr (PAIRING == kInterleaved) {
+    uint32_t o[NW];  // the neighbours of values that do not turn are no partners
+#pragma unroll
+    for (int i = 0; i < NW; ++i) o[i] = i * (8 / NW) < 2 * half - gl * 8 ? w[i] : 0u;
     uint64_t x[4];
-    Vec8<T>::unpack(w, x);
+    Vec8<T>::unpack(o, x);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float lo, hi;
@@ -262,9 +265,12 @@ __device__ __forceinline__ int partner_of(int e, int half) {
 }
 
 // y_e = z_e ca_e + z_partner(e) sb_e turns by a token's angles: the partner's
-// sine has the sign of the second member's formula, and `back` turns back.  The
-// group's lanes work out the token's pairs between them, four each, and put each
-// under both its values in `table`, value e of the warp's group g in row e % 8
+// sine has the sign of the second member's formula, and `back` turns back.  A
+// value that does not turn is its own partner (with neighbours for pairs it has
+// none, a zero), with the factors 1 and 2^-60: the sum rounds to the value, an
+// infinity stays one (times 0 it would be NaN), and no other value has a part in it.
+// The group's lanes work out the token's pairs between them, four each, and put
+// each under both its values in `table`, value e of the warp's group g in row e % 8
 // at g * LPR + e / 8, each row turned by some places from the one before: then
 // neither the lanes that write consecutive pairs nor those that read their eight
 // values meet in a bank.
@@ -288,7 +294,7 @@ struct Angles {
       const int e0 = PAIRING == kInterleaved ? 2 * pair : pair, e1 = PAIRING == kInterleaved ? e0 + 1 : pair + p.half;
       to[i] = static_cast<uint32_t>(place(col, e0)) * 8 | static_cast<uint32_t>(place(col, e1)) * 8 << 16;
     }
-    for (int j = 0; j < 8; ++j) table[place(col, gl * 8 + j)] = make_float2(1.f, 0.f);  // values that do not turn
+    for (int j = 0; j < 8; ++j) table[place(col, gl * 8 + j)] = make_float2(1.f, 0x1p-60f);  // values that do not turn
     __syncwarp();
   }
   // Token t's positions, ahead of its angles.

@@ -2,12 +2,13 @@
 their limits.  Tolerances are fixed from the formats as in test_gpu_tokens.py;
 what differs is stated at each test."""
 import ctypes
+import math
 
 import pytest
 import torch
 
 from submanifold_sparse_convolution_hash_gb300 import binding as sc
-from test_gpu_tokens import U
+from test_gpu_tokens import DT, U
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,66 @@ def test_views_past_the_address_space_are_refused():
     st = sc.lib().sc_attn_fwd(near, far, near, out, None, off.data_ptr(), off.data_ptr(), None, 1, 4, 1 << 30, 2, 2, 64,
                               0.1, 1, 0, None)
     assert st == 1 and b"address space" in sc.lib().sc_last_error()
+
+
+def same(a, b):
+    """Equal bits, where NaN equals NaN."""
+    return torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(torch.nan_to_num(a.float(), nan=7.0),
+                                                                       torch.nan_to_num(b.float(), nan=7.0))
+
+
+# ---------------------------------------------------------------- rotation --
+# Pairings: (2i, 2i + 1); halves on the eight-value grid, of an even, of an odd number of pairs; no rotation.
+PARTS = [(64, 32, True), (96, 50, True), (64, 48, False), (64, 44, False), (64, 42, False), (64, 0, True),
+         (64, 0, False), (128, 64, False)]
+
+
+def _part(d, rot, dtype):
+    g = torch.Generator().manual_seed(d + rot)
+    clean = torch.randn((6, 2, d), generator=g).to(DT[dtype])
+    x = clean.clone()
+    x[1, 0, rot] = math.inf
+    x[2, 1, rot + 1] = math.nan
+    x[3, 0, d - 1] = -math.inf
+    x[4, 1, d - 2] = math.nan
+    kw = {}
+    if rot:
+        f, _ = sc.rope_frequencies(rot, device="cuda")
+        kw = dict(pos=torch.arange(6, dtype=torch.int32).cuda() * 1000 - 2500, freq=f, amp=1.25)
+    return clean.cuda(), x.cuda(), kw
+
+
+@pytest.mark.parametrize("d,rot,ilv", PARTS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_rope_values_that_do_not_turn_stay_themselves(d, rot, ilv, dtype):
+    """Without a norm they come out as they went in, whatever they and their neighbours are, and the
+    turned ones do not see them; the gradient, being a rotation back, likewise."""
+    clean, x, kw = _part(d, rot, dtype)
+    kw["interleaved"] = ilv
+    for call in (lambda a: sc.sc_qk_norm_rope_fwd(a, None, **kw)[0],
+                 lambda a: sc.sc_qk_norm_rope_bwd(a, None, **kw)[0]):
+        y, want = call(x), call(clean)
+        assert same(y[..., rot:], x[..., rot:])
+        assert same(y[..., :rot], want[..., :rot])
+
+
+@pytest.mark.parametrize("d,rot,ilv", PARTS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_rope_norm_beside_values_that_do_not_turn(d, rot, ilv, dtype):
+    """With the norm an infinite value makes its row's 1/sqrt(mean) 0: it becomes NaN and the others 0.  In the
+    gradient an infinite or NaN gout reaches its row, and the weight's gradient at its own place alone."""
+    clean, x, kw = _part(d, rot, dtype)
+    kw["interleaved"] = ilv
+    w = torch.linspace(0.5, 1.5, d).cuda()
+    y, _ = sc.sc_qk_norm_rope_fwd(x, None, wq=w, **kw)
+    want = torch.zeros((d,), dtype=torch.bool)
+    want[rot] = True
+    assert torch.equal(torch.isnan(y[1, 0]).cpu(), want) and not y[1, 0].cpu()[~want].any()
+    want = torch.zeros((d,), dtype=torch.bool)
+    want[d - 1] = True
+    assert torch.equal(torch.isnan(y[3, 0]).cpu(), want) and not y[3, 0].cpu()[~want].any()
+    assert torch.isnan(y[2, 1]).all() and torch.isnan(y[4, 1]).all()
+    _, _, gw, _ = sc.sc_qk_norm_rope_bwd(x, None, clean, None, wq=w, **kw)
+    want = torch.zeros((d,), dtype=torch.bool)
+    want[[rot, rot + 1, d - 1, d - 2]] = True
+    assert torch.equal(~torch.isfinite(gw).cpu(), want)
