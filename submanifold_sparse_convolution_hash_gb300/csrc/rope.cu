@@ -126,42 +126,43 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// cos and sin of pos * f, times amp.  The product can be thousands of turns,
-// and 32 bits of it would leave few for the fraction (1e-3 radians at position
-// 32768, f = 1).  So it is formed in turns, c = f / 2 pi as a sum of two floats,
-// and the product's rounding error is taken along by fma; a position that a
-// float does not hold goes in two parts, a multiple of 4096 and a rest.  The
-// rows are then f32 (EXACT: a few units in the last place) or 16-bit, for which
-// the fast sine's 2^-20 is far below the output's rounding.
-struct Turn {
-  float c, ce;  // f / 2 pi, as a sum
-};
-__device__ __forceinline__ Turn turn_of(float f) {
-  const float kInv2PiHi = 0x1.45f306p-3f;   // 1 / 2 pi to 24 bits
-  const float kInv2PiLo = 0x1.b9391p-28f;   // the rest of it
-  Turn r;
-  r.c = f * kInv2PiHi;
-  r.ce = fmaf(f, kInv2PiHi, -r.c) + f * kInv2PiLo;
-  return r;
+// cos and sin of pos * f, times amp.  The product can be thousands of turns, and
+// 32 bits of it would leave few for the fraction (1e-3 radians at position 32768,
+// f = 1).  Positions are whole numbers, so whole turns a position change nothing:
+// f / 2 pi is kept as a fixed-point fraction of a turn, c of 2^64, and pos * c
+// modulo 2^64 is the product's fraction, off by 2^-33 of a turn at any position.
+// The rows are f32 (EXACT: a few units in the last place) or 16-bit, for which its
+// upper half and the fast sine's 2^-20 are far below the output's rounding.
+typedef uint64_t Turn;
+// |f| = m 2^e times 1 / 2 pi, of which 128 bits after the point are enough for
+// e <= 40 (|f| < 2^64); `finite`: f is.
+__device__ __forceinline__ Turn turn_of(float f, bool* finite) {
+  constexpr uint64_t kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;  // 1 / 2 pi
+  const uint32_t bits = __float_as_uint(f);
+  const int ex = bits >> 23 & 255;
+  *finite = ex != 255;
+  const uint64_t m = ex ? (bits & 0x7fffff) | 0x800000 : bits & 0x7fffff;
+  const int shift = 64 - ((ex ? ex : 1) - 150);  // the product's places below 2^-64
+  const uint64_t w0 = m * kLo, w1 = m * kHi + __umul64hi(m, kLo);
+  const uint64_t w2 = __umul64hi(m, kHi) + (w1 < __umul64hi(m, kLo));
+  uint64_t c;
+  if (shift >= 128) c = shift < 192 ? w2 >> (shift - 128) : 0;
+  else if (shift >= 64) c = shift > 64 ? w1 >> (shift - 64) | w2 << (128 - shift) : w1;
+  else if (shift >= 0) c = shift > 0 ? w0 >> shift | w1 << (64 - shift) : w0;
+  else c = w0 << -shift;
+  return bits >> 31 ? 0 - c : c;
 }
 template <bool EXACT>
-__device__ __forceinline__ float2 angle(int pos, Turn f, float amp) {
-  const bool small = pos > -(1 << 24) && pos < (1 << 24);
-  const int lo = small ? 0 : pos & 4095;
-  const float xh = static_cast<float>(pos - lo);
-  float t = xh * f.c;
-  float e = fmaf(xh, f.c, -t) + xh * f.ce;
-  t -= rintf(t);
-  if (!small) [[unlikely]] {
-    const float xl = static_cast<float>(lo), tl = xl * f.c;
-    e += fmaf(xl, f.c, -tl) + xl * f.ce;
-    t += tl - rintf(tl);
-  }
-  t += e;
-  t -= rintf(t);
+__device__ __forceinline__ float2 angle(int pos, Turn c, float amp) {
   float s, co;
-  if constexpr (EXACT) sincospif(2.f * t, &s, &co);
-  else __sincosf(6.283185307179586f * t, &s, &co);
+  if constexpr (EXACT) {
+    const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(pos)) * c;
+    sincospif(__ll2float_rn(static_cast<int64_t>(t)) * 0x1p-63f, &s, &co);
+  } else {
+    const uint32_t lo = static_cast<uint32_t>(c), hi = static_cast<uint32_t>(c >> 32), x = static_cast<uint32_t>(pos);
+    const uint32_t t = x * hi + __umulhi(x, lo) - (pos < 0 ? lo : 0u);  // the product's upper half
+    __sincosf(static_cast<float>(static_cast<int>(t)) * (6.283185307179586f * 0x1p-32f), &s, &co);
+  }
   return make_float2(co * amp, s * amp);
 }
 
@@ -277,7 +278,7 @@ __device__ __forceinline__ int partner_of(int e, int half) {
 template <int LPR, int PAIRING>
 struct Angles {
   Turn f[4];
-  int axis;         // of the lane's four pairs, a byte each
+  int axis;         // of the lane's four pairs, a byte each; 128: the frequency is not finite
   uint32_t to[4];   // a pair's two places in the table (bytes, 16 bits each)
   float2* table;
   static __device__ __forceinline__ int place(int col, int e) {  // value e of the group whose lane 0 is `col`
@@ -289,8 +290,9 @@ struct Angles {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int pair = gl + i * LPR;
-      f[i] = turn_of(pair < p.half ? __ldg(p.freq + pair) : 0.f);
-      axis |= ((pair >= p.per) + (pair >= 2 * p.per) + (pair >= 3 * p.per)) << (8 * i);
+      bool finite;
+      f[i] = turn_of(pair < p.half ? __ldg(p.freq + pair) : 0.f, &finite);
+      axis |= ((pair >= p.per) + (pair >= 2 * p.per) + (pair >= 3 * p.per) + (finite ? 0 : 128)) << (8 * i);
       const int e0 = PAIRING == kInterleaved ? 2 * pair : pair, e1 = PAIRING == kInterleaved ? e0 + 1 : pair + p.half;
       to[i] = static_cast<uint32_t>(place(col, e0)) * 8 | static_cast<uint32_t>(place(col, e1)) * 8 << 16;
     }
@@ -302,7 +304,7 @@ struct Angles {
     const int* at = p.pos + t * p.pos_stride;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (gl + i * LPR < p.half) pos[i] = __ldg(at + (axis >> (8 * i) & 255));
+      if (gl + i * LPR < p.half) pos[i] = __ldg(at + (axis >> (8 * i) & 3));
   }
   template <typename T>
   __device__ __forceinline__ void fill(const RopeParams& p, const int (&pos)[4], int gl, bool back) {
@@ -316,6 +318,13 @@ struct Angles {
         *reinterpret_cast<float2*>(at + (to[i] & 0xFFFF)) = make_float2(cs.x, -cs.y);
         *reinterpret_cast<float2*>(at + (to[i] >> 16)) = cs;
       }
+    }
+    if (axis & 0x80808080) [[unlikely]] {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (axis >> (8 * i) & 128)
+          *reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(table) + (to[i] & 0xFFFF)) =
+              *reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(table) + (to[i] >> 16)) = make_float2(NAN, NAN);
     }
     __syncwarp();
   }

@@ -138,3 +138,42 @@ def test_rope_norm_beside_values_that_do_not_turn(d, rot, ilv, dtype):
     want = torch.zeros((d,), dtype=torch.bool)
     want[[rot, rot + 1, d - 1, d - 2]] = True
     assert torch.equal(~torch.isfinite(gw).cpu(), want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("ilv", [False, True])
+def test_rope_any_position(dtype, ilv):
+    """Positions to the ends of int32, frequencies above and below half a turn a position.  The reference's
+    angles: the position in two parts whose products with a frequency are exact in 64 bits, and the sum's
+    formula.  The bound is that of the rotation at small positions."""
+    pos = [0, 1, -1, 40000, 2 ** 24 - 1, 2 ** 24, 2 ** 24 + 1, -2 ** 24, -2 ** 24 - 1, 2 ** 31 - 1, -2 ** 31, 123456789,
+           -987654321, 2 ** 30 + 4095, -2 ** 30 - 1, 1999999999]
+    f = torch.cat([sc.rope_frequencies(48)[0], torch.tensor([3.0, -2.5, 7.0, 100.25, 6.2831855, 1e-9, 5000.0, 0.0])])
+    p = torch.tensor(pos, dtype=torch.int64)
+    hi = p // 65536 * 65536
+    a, b = hi.double()[:, None] * f.double(), (p - hi).double()[:, None] * f.double()
+    c = (a.cos() * b.cos() - a.sin() * b.sin())[:, None]
+    s = (a.sin() * b.cos() + a.cos() * b.sin())[:, None]
+    x = torch.randn((len(pos), 2, 64), generator=torch.Generator().manual_seed(1)).to(DT[dtype])
+    y, _ = sc.sc_qk_norm_rope_fwd(x.cuda(), None, p.int().cuda(), f.cuda(), interleaved=ilv)
+    z = x.double()
+    want = torch.empty_like(z)
+    ia, ib = (slice(0, 64, 2), slice(1, 64, 2)) if ilv else (slice(0, 32), slice(32, 64))
+    want[..., ia] = z[..., ia] * c - z[..., ib] * s
+    want[..., ib] = z[..., ib] * c + z[..., ia] * s
+    big = want.abs().amax(-1, keepdim=True)
+    err = (y.double().cpu() - want).abs()
+    bound = U[dtype] * want.abs() + 64 * 2.0 ** -24 * big + 2.0 ** -25 * (dtype == "f16")
+    assert bool((err <= bound).all()), float((err / bound).max())
+
+
+def test_rope_a_frequency_that_is_not_finite_spoils_its_own_pair():
+    f, _ = sc.rope_frequencies(64)
+    x = torch.randn((5, 2, 64), generator=torch.Generator().manual_seed(1)).half().cuda()
+    pos = torch.arange(5, dtype=torch.int32).cuda()
+    want, _ = sc.sc_qk_norm_rope_fwd(x, None, pos, f.cuda())
+    f[3], f[20] = math.nan, math.inf
+    y, _ = sc.sc_qk_norm_rope_fwd(x, None, pos, f.cuda())
+    bad = [3, 35, 20, 52]
+    keep = [i for i in range(64) if i not in bad]
+    assert torch.isnan(y[1:, :, bad]).all() and torch.equal(y[..., keep], want[..., keep])
