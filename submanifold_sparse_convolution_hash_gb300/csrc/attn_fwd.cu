@@ -67,14 +67,18 @@ struct FwdSmem {
   int abort;
 };
 
-// What a row's exponents are taken from, m scale as it rounds (0 before any
-// key), and the factor from one such base to the next.
+// What a row's exponents are taken from: m scale as it rounds (0 before any key),
+// and past 2^24, where rounding takes whole powers of two, what it left.  The factor
+// from one such base to the next.
 constexpr float kFar = 16777216.f;
 __device__ __forceinline__ float base_of(float m, float scale_log2) {
   return m == -INFINITY ? 0.f : __fmul_rn(m, scale_log2);
 }
+__device__ __forceinline__ float rest_of(float m, float base, float scale_log2) {
+  return fabsf(base) > kFar ? fmaf(m, scale_log2, -base) : 0.f;
+}
 __device__ __forceinline__ float step_down(float m, float mn, float base, float nb, float scale_log2) {
-  return fabsf(nb) > kFar ? ex2((m - mn) * scale_log2) : ex2(base - nb);
+  return ex2((base - nb) + (rest_of(m, base, scale_log2) - rest_of(mn, nb, scale_log2)));
 }
 
 // Key tiles that row tile s of the item has to see: [kt0, end).  In a dual item
@@ -460,13 +464,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           }
         }
         // P = exp2(S scale - base); base is m scale with its rounding, the same for
-        // the whole row, which O, the sum and lse have too.  Past 2^24 it is off by
-        // whole powers of two, so there the difference comes first.
-        const bool far = __any_sync(0xffffffffu, fabsf(base) > kFar);
+        // the whole row, which O, the sum and lse have too.  Where the rounding left
+        // more than a fraction it is taken off as well; the vote only spares the other
+        // warps that step, which changes no bit of a row whose rest is 0.
+        const float rest = rest_of(m, base, sl);
+        const bool far = __any_sync(0xffffffffu, rest != 0.f);
         if (far) [[unlikely]] {
-          const float mm = m == -INFINITY ? 0.f : -m;
 #pragma unroll
-          for (int c = 0; c < 128; ++c) x[c] = __float_as_uint((__uint_as_float(x[c]) + mm) * sl);
+          for (int c = 0; c < 128; ++c) x[c] = __float_as_uint(fmaf(__uint_as_float(x[c]), sl, -base) - rest);
         }
         const uint64_t nm = far ? 0 : pair2(-base, -base), sl2 = far ? pair2(1.f, 1.f) : pair2(sl, sl);
         uint64_t sum[2] = {0, 0};

@@ -4,11 +4,12 @@ what differs is stated at each test."""
 import ctypes
 import math
 
+import numpy as np
 import pytest
 import torch
 
 from submanifold_sparse_convolution_hash_gb300 import binding as sc
-from test_gpu_tokens import DT, U
+from test_gpu_tokens import DT, U, attn_inputs, attn_ref, close
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +178,68 @@ def test_rope_a_frequency_that_is_not_finite_spoils_its_own_pair():
     bad = [3, 35, 20, 52]
     keep = [i for i in range(64) if i not in bad]
     assert torch.isnan(y[1:, :, bad]).all() and torch.equal(y[..., keep], want[..., keep])
+
+
+# --------------------------------------------------------------- attention --
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lens", [[50, 130, 64], [1, 3, 40], [300, 200, 290]])
+def test_attention_huge_values_stay_in_their_sequence(lens, dtype):
+    """Finite values of the largest sizes in one sequence change no bit of the others."""
+    q, k, v, gout, qo, ko, lk, kvd = attn_inputs(lens, None, 4, 2, 64, dtype, sharp=0.05)
+    a, b = lens[0], lens[0] + lens[1]
+    qh, kvh, gh = q.clone(), kvd.clone(), gout.clone()
+    for x in (qh, kvh, gh):
+        x[a:b] = torch.sign(x[a:b].float()).to(x.dtype) * 60000.0
+    keep = torch.ones(sum(lens), dtype=torch.bool)
+    keep[a:b] = False
+    got = []
+    for qq, kv, gg in ((q, kvd, gout), (qh, kvh, gh)):
+        o, l = sc.sc_attn_fwd(qq.cuda(), kv[:, :2], kv[:, 2:4], qo.cuda(), scale=60.0, return_lse=True)
+        got.append((o, l) + sc.sc_attn_bwd(gg.cuda(), qq.cuda(), kv[:, :2], kv[:, 2:4], o, l, qo.cuda(), scale=60.0))
+    for x, y in zip(*got):
+        assert torch.equal(x.cpu()[keep], y.cpu()[keep])
+
+
+@pytest.mark.parametrize("g", [3, 7])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_bits_do_not_depend_on_what_ran_before(g, d):
+    """Three (seven) heads a key head leave rows of a tile that no copy writes; what an earlier call left
+    there changes no bit."""
+    lq = [200, 30]
+    q, k, v, gout, qo, ko, lk, kvd = attn_inputs(lq, None, 2 * g, 2, d, "f16", sharp=0.05)
+    qo = qo.cuda()
+    got = []
+    for fill in (0.0, 60000.0):
+        before = torch.full((4096, 4, d), fill, dtype=torch.float16, device="cuda")
+        small = torch.full_like(before, 1.0 if fill else 0.0)
+        off = torch.arange(33, dtype=torch.int32, device="cuda") * 128
+        sc.sc_attn_fwd(before, small, small, off, scale=60.0)
+        o, l = sc.sc_attn_fwd(q.cuda(), kvd[:, :2], kvd[:, 2:4], qo, scale=60.0, return_lse=True)
+        got.append((o, l) + sc.sc_attn_bwd(gout.cuda(), q.cuda(), kvd[:, :2], kvd[:, 2:4], o, l, qo, scale=60.0))
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("lq", [1, 200])
+@pytest.mark.parametrize("at", [1, 2])
+@pytest.mark.parametrize("first,then", [(1635, 1639), (1637, 1642), (-1639, -1635), (-1642, -1637)])
+def test_attention_scores_that_cross_2_to_the_24(lq, at, first, then):
+    """A row whose largest score (in powers of two) grows past 2^24, where fp32 holds no fraction, or comes up
+    from under -2^24: the weights of the 128 keys before and of the one after agree.  The scores, 4096 * 3276 + 2 e
+    or their negatives, are whole numbers that fp32 holds, and with 1.25 powers of two each the first base's fraction
+    is a half.  A weight is off by its exponent's own rounding and by that of scale log2 e over a difference of at
+    most 13 (together under 2^-19), and by its rounding to 16 bits."""
+    d, scale = 16, float(np.float32(1.25 * math.log(2.0)))
+    up = 1 if first > 0 else -1
+    q = torch.zeros((lq, 1, d), dtype=torch.float16)
+    q[:, 0, 0], q[:, 0, 1] = 4096.0 * up, 2.0
+    k = torch.zeros((384, 1, d), dtype=torch.float16)
+    k[:, 0, 0] = 3276.0
+    k[:128, 0, 1] = first
+    k[128:, 0, 1] = first - 400  # 1000 powers of two less
+    k[at * 128 + 17, 0, 1] = then
+    v = torch.randn((384, 1, d), generator=torch.Generator().manual_seed(2)).half()
+    out, _, mag, _, _, _ = attn_ref(q.double(), k.double(), v.double(), [lq], [384], [0, 384], False, scale)
+    off = [torch.tensor([0, n], dtype=torch.int32).cuda() for n in (lq, 384)]
+    o = sc.sc_attn_fwd(q.cuda(), k.cuda(), v.cuda(), off[0], k_off=off[1], scale=scale)
+    close(o, out, mag, U["f16"], 2.0 ** -19, "out")
