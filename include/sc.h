@@ -532,8 +532,10 @@ sc_status sc_qk_norm_rope_bwd(const sc_heads* gout_q, const sc_heads* gout_k, co
  *   out = sum_j exp(S_j - lse) v_j
  * over the keys it sees: all of its sequence, or with SC_ATTN_CAUSAL keys
  * j <= i + (keys - queries) for query i (the last query sees all).  A row that
- * sees no key gets out = 0 and lse = -inf.  Sums and statistics are fp32;
- * exp(S - max) is rounded to dtype for the second product, and out once.
+ * sees no key gets out = 0 and lse = -inf.  Sums and statistics are fp32 (the
+ * tensor cores cut a product off at 2^-25 of the sum that it is added to);
+ * exp(S - max) is rounded to dtype for the second product (f16: a weight below
+ * 2^-21 of the largest is off by up to 2^-32 of it), and out once.
  *
  * d_q_off, d_k_off  int32 [n_seq + 1], device memory, not decreasing;
  *             d_q_off[0] = 0 and d_q_off[n_seq] = t_q (every query row

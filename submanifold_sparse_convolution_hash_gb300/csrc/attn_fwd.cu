@@ -11,7 +11,10 @@
 // while one tile's exponentials run, the other tile's products do.  O is
 // corrected only when a row's maximum grew by more than 2^8: until then P is up
 // to 256 instead of 1, which costs no bits in floating point.  P is rounded to 16
-// bits as the operand of the second product; S, O, m and l are fp32.
+// bits as the operand of the second product; S, O, m and l are fp32.  f16 has few
+// bits below 2^-14 and none below 2^-24, where the weights of a long list under one
+// dominant key lie: there P is held times 2^7 (at most 2^15), so that a weight is
+// off by its rounding or by 2^-32 of the largest, whichever is more.
 //
 // What bounds it, with kernel times.  Long lists at 128 values: the tensor cores
 // and the chain S, maximum, exponentials, P, O of the two row tiles that share
@@ -67,18 +70,25 @@ struct FwdSmem {
   int abort;
 };
 
-// What a row's exponents are taken from: m scale as it rounds (0 before any key),
-// and past 2^24, where rounding takes whole powers of two, what it left.  The factor
-// from one such base to the next.
+// P is held times 2^kShift.
+template <bool BF16>
+constexpr float kShift = BF16 ? 0.f : 7.f;
+
+// What a row's exponents are taken from: m scale - kShift as it rounds (0 before
+// any key), and past 2^24, where rounding takes whole powers of two, what it left.
+// The factor from one such base to the next.
 constexpr float kFar = 16777216.f;
+template <bool BF16>
 __device__ __forceinline__ float base_of(float m, float scale_log2) {
-  return m == -INFINITY ? 0.f : __fmul_rn(m, scale_log2);
+  return m == -INFINITY ? 0.f : __fmaf_rn(m, scale_log2, -kShift<BF16>);
 }
+template <bool BF16>
 __device__ __forceinline__ float rest_of(float m, float base, float scale_log2) {
-  return fabsf(base) > kFar ? fmaf(m, scale_log2, -base) : 0.f;
+  return fabsf(base) > kFar ? fmaf(m, scale_log2, -base) - kShift<BF16> : 0.f;
 }
+template <bool BF16>
 __device__ __forceinline__ float step_down(float m, float mn, float base, float nb, float scale_log2) {
-  return ex2((base - nb) + (rest_of(m, base, scale_log2) - rest_of(mn, nb, scale_log2)));
+  return ex2((base - nb) + (rest_of<BF16>(m, base, scale_log2) - rest_of<BF16>(mn, nb, scale_log2)));
 }
 
 // Key tiles that row tile s of the item has to see: [kt0, end).  In a dual item
@@ -447,8 +457,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const bool raise = mt > m + grow || (m == -INFINITY && mt > m);
         if (__any_sync(0xffffffffu, raise)) [[unlikely]] {
           const float mn = raise ? mt : m;
-          const float nb = base_of(mn, sl);
-          const float f = m == -INFINITY ? 0.f : step_down(m, mn, base, nb, sl);  // 1 for rows that stay
+          const float nb = base_of<BF16>(mn, sl);
+          const float f = m == -INFINITY ? 0.f : step_down<BF16>(m, mn, base, nb, sl);  // 1 for rows that stay
           m = mn;
           base = nb;
           l *= f;
@@ -463,11 +473,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
           }
         }
-        // P = exp2(S scale - base); base is m scale with its rounding, the same for
+        // P = exp2(S scale - base); base is m scale - kShift with its rounding, the same for
         // the whole row, which O, the sum and lse have too.  Where the rounding left
         // more than a fraction it is taken off as well; the vote only spares the other
         // warps that step, which changes no bit of a row whose rest is 0.
-        const float rest = rest_of(m, base, sl);
+        const float rest = rest_of<BF16>(m, base, sl);
         const bool far = __any_sync(0xffffffffu, rest != 0.f);
         if (far) [[unlikely]] {
 #pragma unroll
@@ -596,7 +606,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Attn
     for (int q = lane; q < parts; q += 32) m = fmaxf(m, __ldcg(src + q * step + p.d));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float base = base_of(m, p.scale_log2);
+    const float base = base_of<BF16>(m, p.scale_log2);
     float l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     const int per = p.d <= 64 ? 16 : 32;  // lanes of a part
@@ -610,7 +620,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdParams p, const Attn
         const float mq = __ldcg(src + (q0 + lane) * step + p.d);
         lq = __ldcg(src + (q0 + lane) * step + p.d + 1);
         seen = mq != -INFINITY;
-        f = !seen ? 0.f : step_down(mq, m, base_of(mq, p.scale_log2), base, p.scale_log2);
+        f = !seen ? 0.f : step_down<BF16>(mq, m, base_of<BF16>(mq, p.scale_log2), base, p.scale_log2);
       }
       const uint32_t have = __ballot_sync(0xffffffffu, seen);
       lq *= f;

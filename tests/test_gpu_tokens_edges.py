@@ -243,3 +243,34 @@ def test_attention_scores_that_cross_2_to_the_24(lq, at, first, then):
     off = [torch.tensor([0, n], dtype=torch.int32).cuda() for n in (lq, 384)]
     o = sc.sc_attn_fwd(q.cuda(), k.cuda(), v.cuda(), off[0], k_off=off[1], scale=scale)
     close(o, out, mag, U["f16"], 2.0 ** -19, "out")
+
+
+@pytest.mark.parametrize("lq,hq,hk", [(1, 1, 1), (1, 8, 2), (130, 2, 2), (78000, 1, 1)])
+@pytest.mark.parametrize("below", [15.5, 17.0, 18.2])
+@pytest.mark.parametrize("value", [0.0, 0.25])
+def test_attention_one_key_and_a_long_tail(lq, hq, hk, below, value):
+    """f16: one key far above 120,000 nearly alike, whose own value is zero (all that comes out is the tail) or not.
+    Besides its relative rounding a weight is off by half the format's smallest step, which the kernel's power of
+    two brings to 2^-32 of the largest weight.  The last shape's lists are not cut, so one fp32 sum takes all
+    120,000 products; the tensor cores cut a product off at 2^-25 of the sum that it is added to."""
+    n, d = 120000, 64
+    g = torch.Generator().manual_seed(6)
+    q = torch.zeros((lq, hq, d))
+    q[..., 0], q[..., 1] = 8.0, 1.0
+    k = torch.zeros((n, hk, d))
+    k[..., 1] = torch.randn((n, hk), generator=g) * 0.1
+    k[77, :, 0] = below / 8.0
+    v = torch.ones((n, hk, d))
+    v[77] = value
+    q, k, v = q.half(), k.half(), v.half()
+    x = torch.einsum("hd,nhd->hn", q[0].double(), k.double().repeat_interleave(hq // hk, 1))
+    p = torch.softmax(x, 1)
+    want = ((1.0 - p[:, 77]) + value * p[:, 77])[:, None]
+    off = [torch.tensor([0, m], dtype=torch.int32).cuda() for m in (lq, n)]
+    o, l = sc.sc_attn_fwd(q.cuda(), k.cuda(), v.cuda(), off[0], k_off=off[1], scale=1.0, return_lse=True)
+    u, rel = U["f16"], 2.0 ** -22 * 19 + 2.0 ** -20
+    bound = 1.5 * ((2 * u + rel + 2.0 ** -25 * n) * want + 2.0 ** -32 * n) + 2.0 ** -24
+    err = (o.double().cpu() - want).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
+    # 938 tiles' sums are added one after the other in fp32, each to half a unit
+    assert bool(((l.double().cpu() - torch.logsumexp(x, 1)).abs() <= 938 * 2.0 ** -24 + rel).all())
