@@ -546,7 +546,7 @@ sc_status sc_qk_norm_rope_bwd(const sc_heads* gout_q, const sc_heads* gout_k, co
  * heads_q     a multiple of heads_kv, at most 128 times it.
  * head_dim    a multiple of 8 in [16, 128].
  * d_lse       fp32 [t_q, heads_q], or NULL.
- * scale       positive and finite.
+ * scale       positive, below 2^127.
  * dtype       SC_F16 or SC_BF16.
  * out         must not overlap q, k or v.
  *
@@ -567,9 +567,16 @@ sc_status sc_attn_fwd(const sc_heads* q, const sc_heads* k, const sc_heads* v, c
  *   gq_i = scale sum_j dS_ij k_j, gk_j = scale sum_i dS_ij q_i, gv_j = sum_i P_ij gout_i,
  * gk and gv also summed over the query heads that share the key head.  P and
  * dS are rounded to dtype for the products, sums are fp32, and each gradient
- * is rounded once.  No atomics: the same inputs give the same bits.  Here the
- * key lists are packed too: d_k_off[0] = 0 and d_k_off[n_seq] = t_k, so that
- * every row of gk and gv is written.  The outputs must not overlap the inputs.
+ * is rounded once.  P comes from the fp32 lse, so a weight is off by up to
+ * 2^-22 |lse| of itself: beyond the rounding to dtype from |lse| of 2^11 (f16)
+ * or 2^14 (bf16) on.  From 2^17 on it is taken low, so that none is above 1 and
+ * finite scores and products give finite gradients, if within dtype's range.
+ * As in the forward, a masked query or key inside a sequence takes part with
+ * weight 0, so a row of gk or gv is finite only if the queries of the 128-row
+ * tiles that it is seen from are.  No atomics: the same inputs give the same
+ * bits.  Here the key lists are packed too: d_k_off[0] = 0 and d_k_off[n_seq] =
+ * t_k, so that every row of gk and gv is written.  The outputs must not overlap
+ * the inputs.
  */
 sc_status sc_attn_bwd(const sc_heads* gout, const sc_heads* q, const sc_heads* k, const sc_heads* v,
                       const sc_heads* out, const float* d_lse, const sc_heads_out* gq, const sc_heads_out* gk,

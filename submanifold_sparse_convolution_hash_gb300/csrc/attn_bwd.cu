@@ -139,7 +139,12 @@ __global__ void __launch_bounds__(256) k_attn_stat(const StatParams p) {
   for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (gl == 0 && r < p.rows) {
     const float l = __ldg(p.lse + r);
-    p.stat[r] = make_float2(l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -kPShift<BF16>), s * kPDown<BF16>);
+    float l2 = l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -kPShift<BF16>);
+    // The fp32 lse holds a weight's exponent to 2^-22 of |lse|.  Where that is more
+    // than a fraction of a power of two a weight could come out as an infinity: there
+    // the exponents are taken lower by as much, so that none is above 1.
+    if (fabsf(l2) > 262144.f && l2 < INFINITY) l2 = fmaf(fabsf(l2), 0x1p-21f, l2);
+    p.stat[r] = make_float2(l2, s * kPDown<BF16>);
   }
 }
 

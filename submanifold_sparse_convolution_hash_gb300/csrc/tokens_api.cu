@@ -164,7 +164,8 @@ sc_status attn_sizes(const AttnArgs& a, unsigned flags) {
     return set_error(SC_ERR_UNSUPPORTED, "at most 128 query heads a key head, 65535 in all");
   if (a.head_dim < 16 || a.head_dim > 128 || a.head_dim % 8)
     return set_error(SC_ERR_UNSUPPORTED, "head_dim must be a multiple of 8 in [16, 128]");
-  if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return invalid("scale must be positive and finite");
+  if (!(a.scale > 0.f) || !std::isfinite(a.scale * 1.4426950408889634f))
+    return invalid("scale must be positive and, times log2 e, finite");
   if (a.n_seq == 0 && a.t_q > 0) return invalid("query rows, but no sequence");
   sc_status st = SC_OK;
   if (a.n_seq > 0) {

@@ -274,3 +274,42 @@ def test_attention_one_key_and_a_long_tail(lq, hq, hk, below, value):
     assert bool((err <= bound).all()), float((err / bound).max())
     # 938 tiles' sums are added one after the other in fp32, each to half a unit
     assert bool(((l.double().cpu() - torch.logsumexp(x, 1)).abs() <= 938 * 2.0 ** -24 + rel).all())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attention_extremes_gradients(dtype):
+    """Scores of the format's largest sizes: lse no longer holds a weight's exponent, but a weight is never
+    above 1, so the gradients are finite and gv is at most the sum of |gout|."""
+    d, n = 64, 17
+    q = torch.zeros((n, 1, d), dtype=DT[dtype])
+    k = torch.zeros((200, 1, d), dtype=DT[dtype])
+    q[:8, 0, 0], q[8:16, 0, 0] = torch.linspace(30000, 60000, 8), -torch.linspace(31000, 59000, 8)
+    k[:, 0, 0] = torch.linspace(-60000, 60000, 200)
+    g = torch.Generator().manual_seed(1)
+    v, gout = (torch.randn((m, 1, d), generator=g).to(DT[dtype]).cuda() for m in (200, n))
+    off, koff = (torch.tensor([0, m], dtype=torch.int32).cuda() for m in (n, 200))
+    kw = dict(k_off=koff, scale=1.0)
+    o, l = sc.sc_attn_fwd(q.cuda(), k.cuda(), v, off, return_lse=True, **kw)
+    gq, gk, gv = sc.sc_attn_bwd(gout, q.cuda(), k.cuda(), v, o, l, off, **kw)
+    assert all(bool(torch.isfinite(x).all()) for x in (gk, gv)), "gk, gv"
+    assert bool(torch.isfinite(gq).all()), "gq"
+    assert bool((gv.double().abs() <= gout.double().abs().sum(0) * (1 + 2 * U[dtype])).all())
+    # the last row's scores are equal and its lse is small: all that the keys in the middle get
+    want = gout[n - 1, 0].double() / 200
+    err = gv.double()[95:105, 0] - want
+    assert bool((err.abs() <= 1.5 * 2 * U[dtype] * want.abs() + 2.0 ** -24).all())
+
+
+def test_attention_scores_of_thousands():
+    """Gradients where |lse| is in the thousands: a weight taken from the fp32 lse is off by 2^-22 |lse|."""
+    q, k, v, gout, qo, ko, lk, kvd = attn_inputs([70, 200], None, 4, 2, 64, "bf16", sharp=64.0)
+    out, lse, mag, grads, gmag, smax = attn_ref(q.double(), k.double(), v.double(), [70, 200], lk, ko.tolist(), True, 1.0,
+                                                gout.double())
+    kw = dict(causal=True, scale=1.0)
+    args = (q.cuda(), kvd[:, :2], kvd[:, 2:4])
+    o, l = sc.sc_attn_fwd(*args, qo.cuda(), return_lse=True, **kw)
+    gs = sc.sc_attn_bwd(gout.cuda(), *args, o, l, qo.cuda(), **kw)
+    rel = 2.0 ** -22 * smax + 2.0 ** -20
+    close(o, out, mag, U["bf16"], rel, "out")
+    for got, want, m, name in zip(gs, grads, gmag, ("gq", "gk", "gv")):
+        close(got, want, m, U["bf16"], 4 * rel, name)
