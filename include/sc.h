@@ -566,8 +566,9 @@ sc_status sc_attn_fwd(const sc_heads* q, const sc_heads* k, const sc_heads* v, c
  *   P = exp(S - lse), delta = gout . out, dS = P * (gout . v - delta),
  *   gq_i = scale sum_j dS_ij k_j, gk_j = scale sum_i dS_ij q_i, gv_j = sum_i P_ij gout_i,
  * gk and gv also summed over the query heads that share the key head.  P and
- * dS are rounded to dtype for the products, sums are fp32, and each gradient
- * is rounded once.  P comes from the fp32 lse, so a weight is off by up to
+ * dS are rounded to dtype for the products (f16: held times powers of two, dS's
+ * from its sequence's largest values of gout and v, so that small weights and
+ * gradients keep their bits), sums are fp32, and each gradient is rounded once.  P comes from the fp32 lse, so a weight is off by up to
  * 2^-22 |lse| of itself: beyond the rounding to dtype from |lse| of 2^11 (f16)
  * or 2^14 (bf16) on.  From 2^17 on it is taken low, so that none is above 1 and
  * finite scores and products give finite gradients, if within dtype's range.

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const PlanArgs pa, c
         }
         it.k_row = s_k0[lo];
         it.lk = lk;
-        it.pad = 0;
+        it.seq = c0 + lo;
         it.dual = dual && 2 * it.n_pos <= p.pos_per_item && cost > 1;
         const int ns = chunk && cost > chunk ? (cost + chunk - 1) / chunk : 1;
         const int part = (cost + ns - 1) / ns;

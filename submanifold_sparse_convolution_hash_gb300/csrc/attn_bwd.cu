@@ -14,8 +14,9 @@
 // P and dS go back to TMEM, rounded to 16 bits, as the first operand of the
 // second products; sums stay in TMEM in fp32.  f16 has few bits below 2^-14 and
 // a weight of a list of thousands lies there, so P is held times 2^8 (at most
-// 256); dS, whose size the caller's loss scale sets, as it is.  delta is taken
-// from `out` as the forward rounded it.  These two roundings are what gq and gk
+// 256), and dS times a power of two of its sequence's own, from the largest |gout|
+// and |v| (undone in fp32 as the sums are written).  delta is taken from `out` as the
+// forward rounded it.  These two roundings are what gq and gk
 // are off by (1.6 to 1.9 times the error of an fp32 computation rounded once, up to 2.5 where a
 // few keys take most of the weight and dP - delta cancels).
 //
@@ -66,8 +67,23 @@ struct BwdParams {
   int causal;
   int first;             // gq: no gk, gv kernel ran before it
   float* part;           // gk, gv of cut key tiles: [slot][head][2][128][d]
+  const float* peak;     // f16: [sequence][largest value of |gout|, of |v|]; null: dS is held as it is
   int* status;
 };
+
+// f16 has few bits below 2^-14 and ends at 65504, and dS = P (dP - delta) may lie far
+// to either side.  |dP - delta| is at most 2 d times the sequence's largest values of
+// gout and of v, so dS is held times the power of two that takes this bound to between
+// 2^14 and 2^15.
+template <bool BF16>
+__device__ __forceinline__ float ds_up(const BwdParams& p, const AttnItem& it) {
+  if (BF16 || !p.peak) return 1.f;
+  const float2 m = __ldcg(reinterpret_cast<const float2*>(p.peak) + it.seq);
+  const float b = static_cast<float>(2 * p.d) * m.x * m.y;
+  return b > 0.f ? __uint_as_float((127u + 14 + 127 - (__float_as_uint(b) >> 23)) << 23) : 1.f;
+}
+// 1 / up
+__device__ __forceinline__ float ds_down(float up) { return __uint_as_float((254u << 23) - __float_as_uint(up)); }
 
 // 8 values of a 16-bit row, times `f`.
 template <bool BF16>
@@ -99,12 +115,17 @@ __device__ __forceinline__ void store_acc(uint32_t t, uint8_t* dst, int d, float
 
 // ------------------------------------------------------------ statistics --
 struct StatParams {
-  const uint8_t *gout, *out;
-  int64_t gt, gh, ot, oh;  // bytes
+  const uint8_t *gout, *out, *v;
+  int64_t gt, gh, ot, oh, vt, vh;  // bytes
   const float* lse;
   float2* stat;
-  int64_t rows;  // t_q * heads_q
-  int heads_q, d;
+  int64_t rows, v_rows;  // t_q * heads_q; f16: t_k * heads_kv
+  int heads_q, heads_kv, d;
+  int runs;              // of 32 / LPR rows a warp
+  unsigned blocks;       // of the rows; those of v come after them
+  const int *q_off, *k_off;
+  int n_seq;
+  float* peak;           // f16: as in BwdParams
 };
 
 template <bool BF16>
@@ -120,32 +141,150 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b) {
   return fmaf(x.x, y.x, x.y * y.y);
 }
 
-// delta = gout . out and lse in powers of two, LPR lanes a row.  Memory bounds it
-// (both are read once; 489000 rows of 32 values: 17 us).
+// The sequence that holds token t: the last one that begins at or before it.  A lane
+// by itself, or a warp as one, which takes two steps to 1024 sequences.
+__device__ __forceinline__ int seq_of(const int* off, int n_seq, int64_t t) {
+  int lo = 0, hi = n_seq - 1;
+  while (lo < hi) {
+    const int m = (lo + hi + 1) >> 1;
+    if (__ldg(off + m) <= t) lo = m;
+    else hi = m - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ int seq_of_warp(const int* off, int n_seq, int64_t t) {
+  int lo = 0, n = n_seq;  // among lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = (threadIdx.x & 31) * step;
+    const bool past = at >= n || __ldg(off + lo + at) > t;
+    const uint32_t b = __ballot_sync(0xffffffffu, past);
+    const int k = max((b ? __ffs(b) - 1 : 32) - 1, 0);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+// The largest magnitude among the f16 values that a warp meets in consecutive rows,
+// into their sequences' words.  The order of a maximum changes nothing; values that
+// are not finite spoil their own rows and do not count; offsets that break the rules
+// name some sequence or other.
+struct Peak {
+  float* peak;
+  const int* off;
+  int n_seq, heads, s;
+  int64_t begin = 0, end = 0;  // rows of sequence s
+  uint32_t m = 0;              // two f16 magnitudes
+  __device__ __forceinline__ Peak(float* peak_, const int* off_, int n_seq_, int heads_)
+      : peak(peak_), off(off_), n_seq(n_seq_), heads(heads_) {}
+  __device__ __forceinline__ void start(int64_t row) {
+    s = seq_of_warp(off, n_seq, row / heads);
+    begin = static_cast<int64_t>(__ldg(off + s)) * heads;
+    end = static_cast<int64_t>(__ldg(off + s + 1)) * heads;
+  }
+  static __device__ __forceinline__ uint32_t largest(uint32_t v) { return max(v & 0xFFFFu, v >> 16); }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  // f16 bits to a sequence's word, as fp32 bits (which order as the values do)
+  __device__ __forceinline__ void put(int seq, uint32_t v) const {
+    const float f = __half2float(__ushort_as_half(static_cast<unsigned short>(v)));
+    atomicMax(reinterpret_cast<uint32_t*>(peak + 2 * static_cast<int64_t>(seq)), __float_as_uint(f));
+  }
+  __device__ __forceinline__ void flush() {
+    const uint32_t v = __reduce_max_sync(0xffffffffu, largest(m));
+    if ((threadIdx.x & 31) == 0 && v) put(s, v);
+    m = 0;
+  }
+  // A lane's values of `row` (zeros past the end); `last`: the warp's last row.
+  __device__ __forceinline__ void take(uint4 a, int64_t row, int64_t last) {
+    constexpr uint32_t kAbs = 0x7FFF7FFFu, kInf = 0x7C00u;
+    uint32_t v = max2(max2(a.x & kAbs, a.y & kAbs), max2(a.z & kAbs, a.w & kAbs));
+    if (largest(v) >= kInf) [[unlikely]] {
+      const uint32_t w[4] = {a.x & kAbs, a.y & kAbs, a.z & kAbs, a.w & kAbs};
+      v = 0;
+      for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0xFFFFu) < kInf) v = max(v, w[i] & 0xFFFFu);
+        if (w[i] >> 16 < kInf) v = max(v, w[i] >> 16);
+      }
+    }
+    if (last < end) {
+      m = max2(m, v);
+      return;
+    }
+    // rows of this sequence, of the last row's, and of short ones between them
+    const bool of_s = row < end;
+    if (of_s) m = max2(m, v);
+    flush();
+    start(last);
+    if (of_s) return;
+    if (row >= begin) m = v;
+    else if (v) put(seq_of(off, n_seq, row / heads), largest(v));
+  }
+};
+
+// delta = gout . out and lse in powers of two, LPR lanes a row, a warp p.runs runs of
+// consecutive rows; for f16 also the largest values of gout and v of each sequence.
+// Memory bounds it (all are read once).
+constexpr int kStatBatch = 3, kStatBlocks = 4;  // runs at a time; blocks an SM
 template <bool BF16, int LPR>
-__global__ void __launch_bounds__(256) k_attn_stat(const StatParams p) {
+__global__ void __launch_bounds__(256, kStatBlocks) k_attn_stat(const StatParams p) {
+  constexpr int ROWS = 32 / LPR;
   grid_release();
-  const int64_t r = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / LPR;
-  const int gl = threadIdx.x % LPR;
-  float s = 0.f;
-  if (r < p.rows && gl * 8 < p.d) {
-    const int64_t t = r / p.heads_q;
-    const int h = static_cast<int>(r - t * p.heads_q);
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.gout + t * p.gt + h * p.gh) + gl);
-    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.out + t * p.ot + h * p.oh) + gl);
-    s = (dot2<BF16>(a.x, b.x) + dot2<BF16>(a.y, b.y)) + (dot2<BF16>(a.z, b.z) + dot2<BF16>(a.w, b.w));
-  }
+  const int gl = threadIdx.x % LPR, lane = threadIdx.x & 31;
+  const bool of_v = !BF16 && blockIdx.x >= p.blocks;
+  const int64_t rows = of_v ? p.v_rows : p.rows;
+  const int64_t block_first = (blockIdx.x - (of_v ? p.blocks : 0u)) * (8ll * ROWS * p.runs);
+  const int64_t first = block_first + (threadIdx.x >> 5) * (static_cast<int64_t>(ROWS) * p.runs);
+  const int heads = of_v ? p.heads_kv : p.heads_q;
+  if (first >= rows) return;
+  Peak peak(of_v ? p.peak + 1 : p.peak, of_v ? p.k_off : p.q_off, p.n_seq, heads);
+  const uint8_t* x = of_v ? p.v : p.gout;
+  const int64_t xt = of_v ? p.vt : p.gt, xh = of_v ? p.vh : p.gh;
+#pragma unroll 1
+  for (int i0 = 0; i0 < p.runs && first + i0 * ROWS < rows; i0 += kStatBatch) {
+    uint4 a[kStatBatch], b[kStatBatch];
+    float lse[kStatBatch];
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (gl == 0 && r < p.rows) {
-    const float l = __ldg(p.lse + r);
-    float l2 = l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -kPShift<BF16>);
-    // The fp32 lse holds a weight's exponent to 2^-22 of |lse|.  Where that is more
-    // than a fraction of a power of two a weight could come out as an infinity: there
-    // the exponents are taken lower by as much, so that none is above 1.
-    if (fabsf(l2) > 262144.f && l2 < INFINITY) l2 = fmaf(fabsf(l2), 0x1p-21f, l2);
-    p.stat[r] = make_float2(l2, s * kPDown<BF16>);
+    for (int i = 0; i < kStatBatch; ++i) {
+      const int64_t r = first + (i0 + i) * ROWS + lane / LPR;
+      a[i] = b[i] = make_uint4(0, 0, 0, 0);
+      lse[i] = 0.f;
+      if (i0 + i >= p.runs || r >= rows || gl * 8 >= p.d) continue;
+      int64_t t;
+      if (rows <= 0xffffffffll) t = static_cast<uint32_t>(r) / static_cast<uint32_t>(heads);
+      else t = r / heads;
+      const int h = static_cast<int>(r - t * heads);
+      a[i] = __ldg(reinterpret_cast<const uint4*>(x + t * xt + h * xh) + gl);
+      if (of_v) continue;
+      b[i] = __ldg(reinterpret_cast<const uint4*>(p.out + t * p.ot + h * p.oh) + gl);
+      if (gl == 0) lse[i] = __ldg(p.lse + r);
+    }
+    if (!BF16 && i0 == 0) peak.start(first);
+#pragma unroll
+    for (int i = 0; i < kStatBatch; ++i) {
+      const int64_t r0 = first + (i0 + i) * ROWS, r = r0 + lane / LPR;
+      if constexpr (!BF16) {
+        if (i0 + i < p.runs && r0 < rows) peak.take(a[i], r, min(r0 + ROWS, rows) - 1);
+        if (of_v) continue;
+      }
+      float s = (dot2<BF16>(a[i].x, b[i].x) + dot2<BF16>(a[i].y, b[i].y)) +
+                (dot2<BF16>(a[i].z, b[i].z) + dot2<BF16>(a[i].w, b[i].w));
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (gl == 0 && i0 + i < p.runs && r < rows) {
+        float l2 = lse[i] == -INFINITY ? INFINITY : fmaf(lse[i], kLog2e, -kPShift<BF16>);
+        // The fp32 lse holds a weight's exponent to 2^-22 of |lse|.  Where that is more
+        // than a fraction of a power of two a weight could come out as an infinity:
+        // there the exponents are taken lower by as much, so that none is above 1.
+        if (fabsf(l2) > 262144.f && l2 < INFINITY) l2 = fmaf(fabsf(l2), 0x1p-21f, l2);
+        p.stat[r] = make_float2(l2, s * kPDown<BF16>);
+      }
+    }
   }
+  if constexpr (!BF16) peak.flush();
 }
 
 // --------------------------------------------------------------- gk, gv --
@@ -410,6 +549,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       int first;
       const int n = row_tiles(p, it, &first);
       bool ok = true;
+      const float up = ds_up<BF16>(p, it);
       const float2* src = p.stat + (static_cast<int64_t>(it.q_row) + first * p.pos) * p.heads_q + head * p.g;
       float2 st[4];
       auto load = [&](int i) {  // tile i's rows that belong to the sequence
@@ -427,7 +567,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           sm->nlse2[sl][lane + 32 * u] = -st[u].x;
-          sm->ndelta[sl][lane + 32 * u] = -st[u].y;
+          sm->ndelta[sl][lane + 32 * u] = -st[u].y * up;
           sm->lim[sl][lane + 32 * u] = it.lim0 + i * p.pos + pos[u];
         }
         if (i + 1 < first + n) load(i + 1);
@@ -462,7 +602,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int key_lane = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t ts = t_s + lane_off + quarter * 32, tdp = t_dp + lane_off + quarter * 32;
-    const uint64_t sl2 = pair2(p.scale_log2, p.scale_log2), down = pair2(kPDown<BF16>, kPDown<BF16>);
+    const uint64_t sl2 = pair2(p.scale_log2, p.scale_log2);
     ItemRing ring(&sm->slots);
     AttnItem it;
     int head;
@@ -471,6 +611,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       int first;
       const int n = row_tiles(p, it, &first);
       const int key = it.kt0 * kKeyTile + key_lane;
+      const float up = ds_up<BF16>(p, it);
+      const uint64_t down = pair2(kPDown<BF16> * up, kPDown<BF16> * up);
       bool ok = true;
 #pragma unroll 1
       for (int i = first; i < first + n && ok; ++i, ++np, ++nr) {
@@ -555,7 +697,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int64_t row = static_cast<int64_t>(it.k_row) + key;
         uint8_t* dst = is_k ? p.o0 + row * p.o0_t + head * p.o0_h : p.o1 + row * p.o1_t + head * p.o1_h;
         if (c1 > c0)
-          store_acc<BF16>(acc + c0, dst + c0 * 2, c1 - c0, is_k ? p.scale : kPDown<BF16>, n > 0, live);
+          store_acc<BF16>(acc + c0, dst + c0 * 2, c1 - c0, is_k ? p.scale * ds_down(up) : kPDown<BF16>, n > 0, live);
       } else {
         float* dst = p.part + (((static_cast<int64_t>(it.slot + it.split) * p.heads_kv + head) * 2 + is_k) * 128 +
                                key_lane) * p.d;
@@ -563,6 +705,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int c = c0; c < c1; c += 16) {
           uint32_t o[16] = {};
           if (n > 0) tmem_ld16_raw(acc + c, o);
+          if (!BF16 && is_k)
+#pragma unroll
+            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * ds_down(up));
 #pragma unroll
           for (int u = 0; u < 16; u += 4)
             if (live && c + u < p.d) *reinterpret_cast<uint4*>(dst + c + u) = make_uint4(o[u], o[u + 1], o[u + 2], o[u + 3]);
@@ -808,7 +953,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t tdp = t_dp + lane_off + quarter * 32;
     const int pos = row / p.g, gh = row - pos * p.g;
-    const uint64_t sl2 = pair2(p.scale_log2, p.scale_log2), down = pair2(kPDown<BF16>, kPDown<BF16>);
+    const uint64_t sl2 = pair2(p.scale_log2, p.scale_log2);
     ItemRing ring(&sm->slots);
     AttnItem it;
     int head;
@@ -821,7 +966,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int vis = p.causal ? min(it.lk, it.lim0 + pos + 1) : it.lk;
       float2 st = make_float2(INFINITY, 0.f);
       if (live) st = __ldcg(p.stat + tok * p.heads_q + h);
-      const uint64_t nl = pair2(-st.x, -st.x), ndl = pair2(-st.y, -st.y);
+      const float up = ds_up<BF16>(p, it);
+      const uint64_t nl = pair2(-st.x, -st.x), ndl = pair2(-st.y * up, -st.y * up);
+      const uint64_t down = pair2(kPDown<BF16> * up, kPDown<BF16> * up);
       bool ok = true;
 #pragma unroll 1
       for (int j = 0; j < n && ok; ++j, ++nd) {
@@ -872,7 +1019,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // each quarter writes its columns, 16 at a time
 #pragma unroll 1
       for (int c = quarter * 16; c < p.d; c += 64)
-        store_acc<BF16>(t_dq + lane_off + c, p.o0 + tok * p.o0_t + h * p.o0_h + c * 2, min(16, p.d - c), p.scale, n > 0,
+        store_acc<BF16>(t_dq + lane_off + c, p.o0 + tok * p.o0_t + h * p.o0_h + c * 2, min(16, p.d - c), p.scale * ds_down(up), n > 0,
                         live);
       tc_fence_before();
     }
@@ -932,9 +1079,14 @@ const void* q_kernel(int dp) {
 }
 
 template <bool BF16>
-void run_stat(const StatParams& p, cudaStream_t s) {
+void run_stat(StatParams p, cudaStream_t s) {
   const int lpr = p.d <= 16 ? 2 : p.d <= 32 ? 4 : p.d <= 64 ? 8 : 16;
-  const unsigned n = static_cast<unsigned>((p.rows * lpr + 255) / 256);
+  const int64_t rows = p.rows + p.v_rows, per_run = 8 * 32 / lpr;  // a block's
+  const int64_t resident = static_cast<int64_t>(kStatBlocks) * device_sm_count();
+  p.runs = static_cast<int>((rows + per_run * resident - 1) / (per_run * resident));
+  const int64_t per_block = per_run * p.runs;
+  p.blocks = static_cast<unsigned>((p.rows + per_block - 1) / per_block);
+  const unsigned n = p.blocks + static_cast<unsigned>((p.v_rows + per_block - 1) / per_block);
   switch (lpr) {
     case 2: k_attn_stat<BF16, 2><<<n, 256, 0, s>>>(p); break;
     case 4: k_attn_stat<BF16, 4><<<n, 256, 0, s>>>(p); break;
@@ -964,6 +1116,7 @@ sc_status attn_bwd(const AttnArgs& a) {
   const int64_t k_cap = k_items + slots;
   const size_t o_ik = ar.take(static_cast<size_t>(k_cap) * sizeof(AttnItem));
   const size_t o_st = ar.take(static_cast<size_t>(a.t_q) * a.heads_q * sizeof(float2));
+  const size_t o_peak = ar.take(bf ? 0 : static_cast<size_t>(a.n_seq) * 2 * sizeof(float));
   const size_t o_joins = ar.take(cut ? static_cast<size_t>(k_items) * sizeof(AttnItem) : 0);
   const size_t o_part = ar.take(static_cast<size_t>(slots) * a.heads_kv * 256 * a.head_dim * sizeof(float));
   int* status = attn_status_word();
@@ -1044,8 +1197,22 @@ sc_status attn_bwd(const AttnArgs& a) {
     sp.stat = reinterpret_cast<float2*>(base + o_st);
     sp.rows = a.t_q * a.heads_q;
     sp.heads_q = a.heads_q;
+    sp.heads_kv = a.heads_kv;
     sp.d = a.head_dim;
-    SC_LAUNCH("attn_stat", a.stream, (bf ? run_stat<true>(sp, a.stream) : run_stat<false>(sp, a.stream)));
+    if (!bf) {
+      sp.v = static_cast<const uint8_t*>(a.v.data);
+      sp.vt = a.v.token_stride * 2;
+      sp.vh = a.v.head_stride * 2;
+      sp.v_rows = a.t_k * a.heads_kv;
+      sp.q_off = a.q_off;
+      sp.k_off = a.k_off;
+      sp.n_seq = static_cast<int>(a.n_seq);
+      sp.peak = reinterpret_cast<float*>(base + o_peak);
+      p.peak = sp.peak;
+      e = cudaMemsetAsync(sp.peak, 0, static_cast<size_t>(a.n_seq) * 2 * sizeof(float), a.stream);
+      if (e != cudaSuccess) st = set_cuda_error(e, "attention peaks");
+    }
+    if (!st) SC_LAUNCH("attn_stat", a.stream, (bf ? run_stat<true>(sp, a.stream) : run_stat<false>(sp, a.stream)));
     e = cudaGetLastError();
     if (e != cudaSuccess) st = set_cuda_error(e, "attn_stat");
   }

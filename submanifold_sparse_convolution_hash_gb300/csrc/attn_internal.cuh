@@ -26,7 +26,7 @@ struct __align__(16) AttnItem {
   int slot;    // first of its partial results, or -1: it writes the result itself
   int split, nsplit;  // which of how many parts of the keys
   int dual;    // one row tile: both halves of the block work on it, on every other key tile
-  int pad;
+  int seq;     // the item's sequence
 };
 static_assert(sizeof(AttnItem) == 48, "read as three 16-byte words");
 

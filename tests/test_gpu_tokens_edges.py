@@ -313,3 +313,73 @@ def test_attention_scores_of_thousands():
     close(o, out, mag, U["bf16"], rel, "out")
     for got, want, m, name in zip(gs, grads, gmag, ("gq", "gk", "gv")):
         close(got, want, m, U["bf16"], 4 * rel, name)
+
+
+@pytest.mark.parametrize("lq,lk,sq,sk,which", [(64, 16384, 2.0 ** -6, 16.0, 0), (4096, 16384, 16.0, 2.0 ** -6, 1)])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -8])
+def test_attention_small_gradients_over_long_lists(lq, lk, sq, sk, which, size):
+    """f16: dS of nearly even weights over 16384 keys lies below 2^-18.  gq (and gk) are sums of thousands of
+    terms of either sign, each off by the roundings of P and dS; with the result's own that is at most three
+    times u in the 2-norm."""
+    d, scale = 128, 128 ** -0.5
+    g = torch.Generator(device="cuda").manual_seed(8)
+
+    def rows(n, s):
+        return (torch.randn((n, 1, d), generator=g, device="cuda") * s).half()
+
+    q, k, v, gout = rows(lq, sq), rows(lk, sk), rows(lk, 1.0), rows(lq, size)
+    off = [torch.tensor([0, n], dtype=torch.int32).cuda() for n in (lq, lk)]
+    kw = dict(k_off=off[1], scale=scale)
+    o, l = sc.sc_attn_fwd(q, k, v, off[0], return_lse=True, **kw)
+    got = sc.sc_attn_bwd(gout, q, k, v, o, l, off[0], **kw)[which][:, 0].double()
+    want = _grads64(q, k, v, gout, scale)[which]
+    err = float((got - want).norm() / want.norm())
+    assert err <= 3 * U["f16"], err
+
+
+def test_attention_large_gradients_that_fit():
+    """f16: gout and v whose products pass 65504 while every gradient is below it."""
+    d, lq, lk = 128, [2, 3], [2, 5]
+    g = torch.Generator().manual_seed(11)
+
+    def rows(n, s):
+        return (torch.randn((n, 1, d), generator=g) * s).half()
+
+    q, k, v, gout = rows(5, 0.1), rows(7, 0.1), rows(7, 8.0), rows(5, 2048.0)
+    off = [torch.tensor(np.concatenate([[0], np.cumsum(x)]), dtype=torch.int32) for x in (lq, lk)]
+    ref = attn_ref(q.double(), k.double(), v.double(), lq, lk, off[1].tolist(), False, 0.1, gout.double())
+    out, lse, mag, grads, gmag, smax = ref
+    assert max(float(x.abs().max()) for x in grads) < 60000
+    args = [x.cuda() for x in (q, k, v)]
+    kw = dict(k_off=off[1].cuda(), scale=0.1)
+    o, l = sc.sc_attn_fwd(*args, off[0].cuda(), return_lse=True, **kw)
+    gs = sc.sc_attn_bwd(gout.cuda(), *args, o, l, off[0].cuda(), **kw)
+    rel = 2.0 ** -22 + 2.0 ** -20
+    for got, want, m, name in zip(gs, grads, gmag, ("gq", "gk", "gv")):
+        close(got, want, m, U["f16"], 4 * rel, name)
+
+
+def test_attention_sharp_scores_half_precision():
+    """f16 gradients at sharp scores, most of whose weights are far below the format's range.  Besides the
+    roundings a weight is off by 2^-25 2^-8 (P is held times 2^8) and a dS by 2^-25 where its bound, 2 head_dim
+    times the sequence's largest values of gout and v, is brought to between 2^14 and 2^15."""
+    lens = [70, 200]
+    q, k, v, gout, qo, ko, lk, kvd = attn_inputs(lens, None, 4, 2, 64, "f16", sharp=64.0)
+    out, lse, mag, grads, gmag, smax = attn_ref(q.double(), k.double(), v.double(), lens, lk, ko.tolist(), True, 1.0,
+                                                gout.double())
+    a = 0
+    for n in lens:
+        step = 2.0 ** -25 * 2.0 ** -14 * 2 * 64 * float(gout[a:a + n].abs().max()) * float(v[a:a + n].abs().max())
+        for h in range(4):
+            j = h // 2
+            gmag[0][a:a + n, h] += step / U["f16"] * k[a:a + n, j].double().abs().cumsum(0)
+            gmag[1][a:a + n, j] += step / U["f16"] * q[a:a + n, h].double().abs().flip(0).cumsum(0).flip(0)
+            gmag[2][a:a + n, j] += 2.0 ** -33 / U["f16"] * gout[a:a + n, h].double().abs().flip(0).cumsum(0).flip(0)
+        a += n
+    kw = dict(causal=True, scale=1.0)
+    args = (q.cuda(), kvd[:, :2], kvd[:, 2:4])
+    o, l = sc.sc_attn_fwd(*args, qo.cuda(), return_lse=True, **kw)
+    gs = sc.sc_attn_bwd(gout.cuda(), *args, o, l, qo.cuda(), **kw)
+    rel = 2.0 ** -22 * smax + 2.0 ** -20
+    for got, want, m, name in zip(gs, grads, gmag, ("gq", "gk", "gv")):
+        close(got, want, m, U["f16"], 4 * rel, name)
