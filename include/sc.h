@@ -568,16 +568,19 @@ sc_status sc_attn_fwd(const sc_heads* q, const sc_heads* k, const sc_heads* v, c
  * gk and gv also summed over the query heads that share the key head.  P and
  * dS are rounded to dtype for the products (f16: held times powers of two, dS's
  * from its sequence's largest values of gout and v, so that small weights and
- * gradients keep their bits), sums are fp32, and each gradient is rounded once.  P comes from the fp32 lse, so a weight is off by up to
- * 2^-22 |lse| of itself: beyond the rounding to dtype from |lse| of 2^11 (f16)
- * or 2^14 (bf16) on.  From 2^17 on it is taken low, so that none is above 1 and
- * finite scores and products give finite gradients, if within dtype's range.
- * As in the forward, a masked query or key inside a sequence takes part with
- * weight 0, so a row of gk or gv is finite only if the queries of the 128-row
- * tiles that it is seen from are.  No atomics: the same inputs give the same
- * bits.  Here the key lists are packed too: d_k_off[0] = 0 and d_k_off[n_seq] =
- * t_k, so that every row of gk and gv is written.  The outputs must not overlap
- * the inputs.
+ * gradients keep their bits), sums are fp32, and each gradient is rounded once.
+ * No sum depends on an order of arrival: the same inputs give the same bits.
+ *
+ * P comes from the fp32 lse, so a weight is off by up to 2^-22 |lse| of itself:
+ * beyond the rounding to dtype from |lse| of 2^11 (f16) or 2^14 (bf16) on.  From
+ * 2^17 on it is taken low, so that none is above 1 and finite scores and products
+ * give finite gradients, if within dtype's range.  As in the forward, a masked
+ * query or key inside a sequence takes part with weight 0, so a row of gk or gv
+ * is finite only if the queries of the 128-row tiles that it is seen from are.
+ *
+ * Here the key lists are packed too: d_k_off[0] = 0 and d_k_off[n_seq] = t_k, so
+ * that every row of gk and gv is written.  The outputs must not overlap the
+ * inputs.
  */
 sc_status sc_attn_bwd(const sc_heads* gout, const sc_heads* q, const sc_heads* k, const sc_heads* v,
                       const sc_heads* out, const float* d_lse, const sc_heads_out* gq, const sc_heads_out* gk,

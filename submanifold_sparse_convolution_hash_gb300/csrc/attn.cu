@@ -7,6 +7,10 @@ namespace {
 
 __device__ int g_attn_status;
 
+// Reads and clears the word in one step: what other streams latch meanwhile is either
+// in `taken` or stays for the next check.
+__global__ void k_attn_take_status(int* taken) { *taken = atomicExch(&g_attn_status, 0); }
+
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 256;
 
@@ -282,11 +286,14 @@ sc_status attn_map(CUtensorMap* m, const void* data, sc_dtype dt, int d, int hea
 }
 
 sc_status attn_take_status(cudaStream_t s, int* bits) {
-  const int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_attn_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  int* taken = nullptr;
+  sc_status st = dev_alloc(reinterpret_cast<void**>(&taken), sizeof(int), s);
+  if (st) return st;
+  SC_LAUNCH("attn_take_status", s, (k_attn_take_status<<<1, 1, 0, s>>>(taken)));
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyAsync(bits, taken, sizeof(int), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_attn_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  dev_free(taken, s);
   return e == cudaSuccess ? SC_OK : set_cuda_error(e, "attention status");
 }
 

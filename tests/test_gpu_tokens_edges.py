@@ -3,6 +3,7 @@ their limits.  Tolerances are fixed from the formats as in test_gpu_tokens.py;
 what differs is stated at each test."""
 import ctypes
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -383,3 +384,35 @@ def test_attention_sharp_scores_half_precision():
     rel = 2.0 ** -22 * smax + 2.0 ** -20
     for got, want, m, name in zip(gs, grads, gmag, ("gq", "gk", "gv")):
         close(got, want, m, U["f16"], 4 * rel, name)
+
+
+def test_attention_errors_reach_the_one_who_checks():
+    """A thread whose calls fail, one after another, and a thread that checks on a stream of its own: every
+    error is seen, those too that come while a check is under way."""
+    sc.sc_attn_check()
+    x, y, out = (torch.zeros((16, 2, 32), dtype=torch.float16, device="cuda") for _ in range(3))
+    off = torch.tensor([0, 40, 16], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    seen, stop, failed = threading.Semaphore(0), threading.Event(), []
+
+    def check():
+        s = torch.cuda.Stream()
+        while not stop.is_set():
+            try:
+                sc.sc_attn_check(stream=s)
+            except sc.ScError:
+                seen.release()
+
+    t = threading.Thread(target=check)
+    t.start()
+    try:
+        for i in range(200):
+            sc.sc_attn_fwd(x, y, y, off, out=out)
+            torch.cuda.current_stream().synchronize()
+            if not seen.acquire(timeout=5):
+                failed.append(i)
+                break
+    finally:
+        stop.set()
+        t.join()
+    assert not failed, failed
