@@ -11,11 +11,12 @@ namespace {
 
 sc_status invalid(const std::string& msg) { return set_error(SC_ERR_INVALID_ARG, msg.c_str()); }
 
-// The bytes that a view of rows spans: [lo, hi) from its first to past its
-// last value, `pitch` between tokens and `width` of one token's heads.
+// The bytes of a view of rows: [lo, hi) from its first to past its last value, and
+// how they repeat: `n[0]` pieces of `width` bytes `step[0]` apart, n[1] of those
+// step[1] apart, the larger step last.
 struct Span {
   uintptr_t lo = 0, hi = 0;
-  int64_t pitch = 0, width = 0;
+  int64_t width = 0, step[2] = {0, 0}, n[2] = {0, 0};
 };
 
 // A view of `tokens` rows of `heads` heads of `d` values of `eb` bytes.
@@ -39,23 +40,46 @@ sc_status check_heads(const char* what, const void* data, int64_t ts, int64_t hs
     const bool tokens_outer = tokens <= 1 || ts >= (heads - 1) * hs + d;
     if (!heads_ok || !(tokens_outer || tokens_inner)) return invalid(std::string(what) + ": rows overlap");
   }
+  const bool by_token = ts >= hs;  // heads within a token, or tokens within a head
+  span->width = static_cast<int64_t>(d) * eb;
+  span->step[0] = (by_token ? hs : ts) * eb;
+  span->step[1] = (by_token ? ts : hs) * eb;
+  span->n[0] = by_token ? heads : tokens;
+  span->n[1] = by_token ? tokens : heads;
   span->lo = reinterpret_cast<uintptr_t>(data);
-  span->width = ((heads - 1) * hs + d) * eb;
-  span->pitch = ts * eb;
-  span->hi = span->lo + static_cast<uintptr_t>((tokens - 1) * ts * eb + span->width);
+  span->hi = span->lo + static_cast<uintptr_t>((tokens - 1) * ts * eb + (heads - 1) * hs * eb + span->width);
   return SC_OK;
 }
 
-// Whether two views may share a byte.  Views that lie side by side in the rows
-// of one buffer (the same pitch, columns apart) do not.
+// Whether pieces of `wa` bytes at `at` mod `pitch` and of `wb` at 0 can meet.
+bool meet(int64_t at, int64_t wa, int64_t wb, int64_t pitch) {
+  at = (at % pitch + pitch) % pitch;
+  return at < wb || at + wa > pitch;
+}
+
+// Whether two views may share a byte.  Of views that repeat with the same outer step,
+// as parts of one buffer do, the places within a step are compared: as whole runs,
+// and where those meet (heads of one between heads of the other) piece by piece, up
+// to 4096 of them.
 bool overlap(const Span& a, const Span& b) {
   if (a.lo == a.hi || b.lo == b.hi || a.hi <= b.lo || b.hi <= a.lo) return false;
-  if (a.pitch == b.pitch && a.pitch > 0) {
-    const Span &f = a.lo <= b.lo ? a : b, &s = a.lo <= b.lo ? b : a;
-    const int64_t at = static_cast<int64_t>((s.lo - f.lo) % static_cast<uintptr_t>(a.pitch));
-    if (at >= f.width && at + s.width <= a.pitch) return false;
+  const int64_t pitch = a.step[1];
+  if (pitch == 0 || pitch != b.step[1]) return true;
+  const int64_t at = static_cast<int64_t>(a.lo - b.lo);
+  const int64_t ra = (a.n[0] - 1) * a.step[0] + a.width, rb = (b.n[0] - 1) * b.step[0] + b.width;
+  if (ra <= pitch && rb <= pitch && !meet(at, ra, rb, pitch)) return false;
+  if (a.step[0] == b.step[0]) {
+    // only the difference of two places counts
+    if (a.n[0] + b.n[0] > 4096) return true;
+    for (int64_t i = 1 - b.n[0]; i < a.n[0]; ++i)
+      if (meet(at + i * a.step[0], a.width, b.width, pitch)) return true;
+    return false;
   }
-  return true;
+  if (a.n[0] * b.n[0] > 4096) return true;
+  for (int64_t i = 0; i < a.n[0]; ++i)
+    for (int64_t j = 0; j < b.n[0]; ++j)
+      if (meet(at + i * a.step[0] - j * b.step[0], a.width, b.width, pitch)) return true;
+  return false;
 }
 
 sc_status check_ints(const void* p, const char* what) { return check_dev_ptr(p, 4, what); }

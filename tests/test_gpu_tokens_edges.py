@@ -416,3 +416,47 @@ def test_attention_errors_reach_the_one_who_checks():
         stop.set()
         t.join()
     assert not failed, failed
+
+
+# ------------------------------------------------------------------- views --
+def test_views_that_interleave_by_head():
+    """q, k and v of each head side by side ([tokens, heads, 3, head_dim] storage): rotated in place, and
+    gradients written into a buffer laid out alike."""
+    t, h, d = 70, 4, 32
+    g = torch.Generator().manual_seed(5)
+    rows = torch.randn((t, h, 3, d), generator=g).half().cuda()
+    q, k, v = rows.unbind(2)
+    f, _ = sc.rope_frequencies(d, device="cuda")
+    pos = torch.arange(t, dtype=torch.int32).cuda()
+    off = torch.tensor([0, 50, 70], dtype=torch.int32).cuda()
+    want = sc.sc_qk_norm_rope_fwd(q.contiguous(), k.contiguous(), pos, f)
+    keep = v.clone()
+    sc.sc_qk_norm_rope_fwd(q, k, pos, f, out_q=q, out_k=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, keep)
+    gout = torch.randn((t, h, d), generator=g).half().cuda()
+    o, l = sc.sc_attn_fwd(q, k, v, off, return_lse=True)
+    want = sc.sc_attn_bwd(gout, q, k, v, o, l, off)
+    grads = torch.full_like(rows, math.nan)
+    sc.sc_attn_bwd(gout, q, k, v, o, l, off, gq=grads[:, :, 0], gk=grads[:, :, 1], gv=grads[:, :, 2])
+    assert torch.equal(grads, torch.stack(want, 2))
+    # [heads, 2, tokens, head_dim] storage: heads lie farther apart than tokens
+    kv = torch.full((h, 2, t, d), math.nan, dtype=torch.float16, device="cuda")
+    gk, gv = kv[:, 0].transpose(0, 1), kv[:, 1].transpose(0, 1)
+    sc.sc_attn_bwd(gout, q, k, v, o, l, off, gk=gk, gv=gv)
+    assert torch.equal(gk, want[1]) and torch.equal(gv, want[2])
+
+
+def test_views_that_share_rows_are_refused():
+    """Interleaved views of which some rows do fall on one another."""
+    rows = torch.zeros((70, 9, 32), dtype=torch.float16, device="cuda")
+    off = torch.tensor([0, 70], dtype=torch.int32, device="cuda")
+    q, k, v = rows[:, 0:6:3], rows[:, 1:6:3], rows[:, 2:6:3]
+    o, l = sc.sc_attn_fwd(q, k, v, off, return_lse=True)
+    g = torch.zeros_like(rows)
+    for gk in (g[:, 3:9:3], g[:, 0:4:2], g[:, 2:4]):  # one head of gq's 0 and 3, of gv's 2 and 5
+        with pytest.raises(sc.ScError, match="overlap"):
+            sc.sc_attn_bwd(o, q, k, v, o.clone(), l, off, gq=g[:, 0:6:3], gk=gk, gv=g[:, 2:6:3])
+    with pytest.raises(sc.ScError, match="overlap"):
+        sc.sc_attn_fwd(q, k, v, off, out=rows[:, 3:9:3])
+    with pytest.raises(sc.ScError, match="overlap"):  # the same columns a row further on
+        sc.sc_attn_fwd(q[:-1], k[:-1], v[:-1], off - (off > 0).int(), out=rows[1:, 0:6:3])
