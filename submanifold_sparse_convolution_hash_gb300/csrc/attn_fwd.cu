@@ -54,7 +54,7 @@ struct FwdParams {
   float* part;           // partial results [slot][head][header[3] rows][d + 8]: O, m, l
   int heads_q, heads_kv, g, pos;  // pos: queries of a row tile
   int d;
-  float scale_log2, scale;
+  float scale_log2;
   int causal;
   int* status;
 };
@@ -755,7 +755,6 @@ sc_status attn_fwd(const AttnArgs& a) {
     p.pos = pos;
     p.d = a.head_dim;
     p.scale_log2 = a.scale * kLog2e;
-    p.scale = a.scale;
     p.causal = a.causal;
     p.status = status;
     const int64_t most = cap * a.heads_kv;
