@@ -460,3 +460,56 @@ def test_views_that_share_rows_are_refused():
         sc.sc_attn_fwd(q, k, v, off, out=rows[:, 3:9:3])
     with pytest.raises(sc.ScError, match="overlap"):  # the same columns a row further on
         sc.sc_attn_fwd(q[:-1], k[:-1], v[:-1], off - (off > 0).int(), out=rows[1:, 0:6:3])
+
+
+# ------------------------------------------------------- plans, long lists --
+def test_attention_parts_that_do_not_fit_are_whole_again():
+    """Many single queries, some on long key lists, and one long sequence of queries: by the average there is
+    room for parts of a few rows each, by the longest there is not, and no list is cut."""
+    g = torch.Generator().manual_seed(3)
+    lq = [1] * 1400
+    lq[700] = 300
+    lk = [1] * 1400
+    for i in range(0, 1400, 35):
+        lk[i] = 5000 + i
+    lk[700] = 400
+    test = attn_inputs(lq, lk, 1, 1, 32, "f16")
+    q, k, v, gout, qo, ko, lk, kvd = test
+    scale = 32 ** -0.5
+    out, lse, mag, grads, gmag, smax = attn_ref(q.double(), k.double(), v.double(), lq, lk, ko.tolist(), False, scale,
+                                                gout.double())
+    args = (q.cuda(), kvd[:, :1], kvd[:, 1:2])
+    kw = dict(k_off=ko.cuda(), scale=scale)
+    o, l = sc.sc_attn_fwd(*args, qo.cuda(), return_lse=True, **kw)
+    gs = sc.sc_attn_bwd(gout.cuda(), *args, o, l, qo.cuda(), **kw)
+    sc.sc_attn_check()
+    rel = 2.0 ** -22 * max(1.0, smax) + 2.0 ** -20
+    close(o, out, mag, U["f16"], rel, "out")
+    assert bool(((l.double().cpu() - lse).abs() <= rel + 2.0 ** -22 * lse.abs()).all())
+    for got, want, m, name in zip(gs, grads, gmag, ("gq", "gk", "gv")):
+        close(got, want, m, U["f16"], 4 * rel, name)
+
+
+def test_views_that_broadcast():
+    """Steps of zero: one key head's rows seen as four heads', one row of gout as every token's."""
+    lq, hq, d = [150, 9, 300], 4, 64
+    g = torch.Generator().manual_seed(5)
+    q = torch.randn((459, hq, d), generator=g).half().cuda()
+    k, v = (torch.randn((459, 1, d), generator=g).half().cuda().expand(459, hq, d) for _ in range(2))
+    gout = torch.randn((1, 1, d), generator=g).half().cuda().expand(459, hq, d)
+    row = torch.randn((1, hq, d), generator=g).half().cuda().expand(459, hq, d)
+    off = torch.tensor([0, 150, 159, 459], dtype=torch.int32).cuda()
+    for qq in (q, row):
+        o, l = sc.sc_attn_fwd(qq, k, v, off, causal=True, return_lse=True)
+        got = (o, l) + sc.sc_attn_bwd(gout, qq, k, v, o, l, off, causal=True)
+        c = [x.contiguous() for x in (gout, qq, k, v)]
+        o, l = sc.sc_attn_fwd(*c[1:], off, causal=True, return_lse=True)
+        want = (o, l) + sc.sc_attn_bwd(*c, o, l, off, causal=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    f, _ = sc.rope_frequencies(d, device="cuda")
+    pos = torch.arange(459, dtype=torch.int32).cuda()
+    w = torch.linspace(0.5, 1.5, d).cuda()
+    got = sc.sc_qk_norm_rope_fwd(row, k, pos, f, w, w) + sc.sc_qk_norm_rope_bwd(gout, gout, row, k, pos, f, w, w)
+    row, k, gout = (x.contiguous() for x in (row, k, gout))
+    want = sc.sc_qk_norm_rope_fwd(row, k, pos, f, w, w) + sc.sc_qk_norm_rope_bwd(gout, gout, row, k, pos, f, w, w)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
