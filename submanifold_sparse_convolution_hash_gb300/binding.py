@@ -497,6 +497,8 @@ def _positions(pos, freq, tokens, device):
     """(address, token stride, axes, frequencies' address, rot_dim)."""
     if freq is None:
         return None, 0, 1, None, 0
+    if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
+        raise ValueError("freq must be a float32 vector")
     half = freq.shape[0]
     fp = _f32(freq, "freq", half, device)
     if not isinstance(pos, torch.Tensor) or pos.get_device() != device or pos.dtype is not torch.int32:
@@ -669,7 +671,9 @@ def _attn_common(q, k, v, q_off, k_off, scale):
     code = _DTYPES.get(dtype)
     if code is None:
         raise ValueError("rows must be float16 or bfloat16")
-    return hq, hk, hv, dtype, device, sq, sk, qp, kp, n, code, sq[2] ** -0.5 if scale is None else scale
+    if scale is None:
+        scale = max(sq[2], 1) ** -0.5
+    return hq, hk, hv, dtype, device, sq, sk, qp, kp, n, code, scale
 
 
 def sc_attn_fwd(q, k, v, q_off, k_off=None, k_len=None, causal: bool = False, scale: float | None = None,

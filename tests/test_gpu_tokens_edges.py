@@ -513,3 +513,16 @@ def test_views_that_broadcast():
     row, k, gout = (x.contiguous() for x in (row, k, gout))
     want = sc.sc_qk_norm_rope_fwd(row, k, pos, f, w, w) + sc.sc_qk_norm_rope_bwd(gout, gout, row, k, pos, f, w, w)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_arguments_of_the_wrong_kind():
+    """Refused with the errors that the wrappers name, not with those of what they do inside."""
+    x = torch.zeros((4, 2, 64), dtype=torch.float16, device="cuda")
+    pos = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for freq in (1.0, [1.0] * 32, torch.tensor(1.0, device="cuda"), torch.ones((32, 1), device="cuda")):
+        with pytest.raises(ValueError, match="freq"):
+            sc.sc_qk_norm_rope_fwd(x, None, pos, freq)
+    z = torch.zeros((4, 2, 0), dtype=torch.float16, device="cuda")
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    with pytest.raises(sc.ScError, match="head_dim"):
+        sc.sc_attn_fwd(z, z, z, off)
