@@ -121,7 +121,7 @@ struct StatParams {
   float2* stat;
   int64_t rows, v_rows;  // t_q * heads_q; f16: t_k * heads_kv
   int heads_q, heads_kv, d;
-  int runs;              // of 32 / LPR rows a warp
+  int runs;              // of 32 / LPR rows a warp, a multiple of kStatBatch
   unsigned blocks;       // of the rows; those of v come after them
   const int *q_off, *k_off;
   int n_seq;
@@ -241,8 +241,15 @@ __global__ void __launch_bounds__(256, kStatBlocks) k_attn_stat(const StatParams
   const int heads = of_v ? p.heads_kv : p.heads_q;
   if (first >= rows) return;
   Peak peak(of_v ? p.peak + 1 : p.peak, of_v ? p.k_off : p.q_off, p.n_seq, heads);
-  const uint8_t* x = of_v ? p.v : p.gout;
   const int64_t xt = of_v ? p.vt : p.gt, xh = of_v ? p.vh : p.gh;
+  // this lane's row, and its place in x and in out, a run further each time
+  const int64_t t0 = (first + lane / LPR) / heads;
+  int h = static_cast<int>(first + lane / LPR - t0 * heads);
+  const int dt = ROWS / heads, dh = ROWS % heads;
+  const uint8_t* x = (of_v ? p.v : p.gout) + t0 * xt + h * xh + gl * 16;
+  const uint8_t* y = p.out + t0 * p.ot + h * p.oh + gl * 16;
+  const int64_t x_run = dt * xt + dh * xh, x_wrap = xt - heads * xh;
+  const int64_t y_run = dt * p.ot + dh * p.oh, y_wrap = p.ot - heads * p.oh;
 #pragma unroll 1
   for (int i0 = 0; i0 < p.runs && first + i0 * ROWS < rows; i0 += kStatBatch) {
     uint4 a[kStatBatch], b[kStatBatch];
@@ -252,29 +259,35 @@ __global__ void __launch_bounds__(256, kStatBlocks) k_attn_stat(const StatParams
       const int64_t r = first + (i0 + i) * ROWS + lane / LPR;
       a[i] = b[i] = make_uint4(0, 0, 0, 0);
       lse[i] = 0.f;
-      if (i0 + i >= p.runs || r >= rows || gl * 8 >= p.d) continue;
-      int64_t t;
-      if (rows <= 0xffffffffll) t = static_cast<uint32_t>(r) / static_cast<uint32_t>(heads);
-      else t = r / heads;
-      const int h = static_cast<int>(r - t * heads);
-      a[i] = __ldg(reinterpret_cast<const uint4*>(x + t * xt + h * xh) + gl);
-      if (of_v) continue;
-      b[i] = __ldg(reinterpret_cast<const uint4*>(p.out + t * p.ot + h * p.oh) + gl);
-      if (gl == 0) lse[i] = __ldg(p.lse + r);
+      if (r < rows && gl * 8 < p.d) {
+        a[i] = __ldg(reinterpret_cast<const uint4*>(x));
+        if (!of_v) {
+          b[i] = __ldg(reinterpret_cast<const uint4*>(y));
+          if (gl == 0) lse[i] = __ldg(p.lse + r);
+        }
+      }
+      x += x_run;
+      y += y_run;
+      h += dh;
+      if (h >= heads) {
+        h -= heads;
+        x += x_wrap;
+        y += y_wrap;
+      }
     }
     if (!BF16 && i0 == 0) peak.start(first);
 #pragma unroll
     for (int i = 0; i < kStatBatch; ++i) {
       const int64_t r0 = first + (i0 + i) * ROWS, r = r0 + lane / LPR;
       if constexpr (!BF16) {
-        if (i0 + i < p.runs && r0 < rows) peak.take(a[i], r, min(r0 + ROWS, rows) - 1);
+        if (r0 < rows) peak.take(a[i], r, min(r0 + ROWS, rows) - 1);
         if (of_v) continue;
       }
       float s = (dot2<BF16>(a[i].x, b[i].x) + dot2<BF16>(a[i].y, b[i].y)) +
                 (dot2<BF16>(a[i].z, b[i].z) + dot2<BF16>(a[i].w, b[i].w));
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (gl == 0 && i0 + i < p.runs && r < rows) {
+      if (gl == 0 && r < rows) {
         float l2 = lse[i] == -INFINITY ? INFINITY : fmaf(lse[i], kLog2e, -kPShift<BF16>);
         // The fp32 lse holds a weight's exponent to 2^-22 of |lse|.  Where that is more
         // than a fraction of a power of two a weight could come out as an infinity:
@@ -1084,6 +1097,7 @@ void run_stat(StatParams p, cudaStream_t s) {
   const int64_t rows = p.rows + p.v_rows, per_run = 8 * 32 / lpr;  // a block's
   const int64_t resident = static_cast<int64_t>(kStatBlocks) * device_sm_count();
   p.runs = static_cast<int>((rows + per_run * resident - 1) / (per_run * resident));
+  p.runs = (p.runs + kStatBatch - 1) / kStatBatch * kStatBatch;
   const int64_t per_block = per_run * p.runs;
   p.blocks = static_cast<unsigned>((p.rows + per_block - 1) / per_block);
   const unsigned n = p.blocks + static_cast<unsigned>((p.v_rows + per_block - 1) / per_block);
