@@ -553,7 +553,10 @@ sc_status sc_qk_norm_rope_bwd(const sc_heads* gout_q, const sc_heads* gout_k, co
  * Values of other sequences never reach a row, whatever they are (NaN
  * included).  Inside a sequence a masked value takes part with weight 0, so a
  * row is finite only if the keys and values after it in its 128-key block are.
- * Temporary device memory is allocated and freed stream-ordered on `stream`.
+ * Temporary device memory is allocated and freed stream-ordered on `stream`: lists of
+ * 48 bytes a query tile and, where queries are few and keys may be cut, fp32 partial
+ * results of up to 256 MB (a decoding step takes all of it: the size is set by the
+ * largest tile, whatever the sequences hold).
  */
 sc_status sc_attn_fwd(const sc_heads* q, const sc_heads* k, const sc_heads* v, const sc_heads_out* out,
                       float* d_lse, const int32_t* d_q_off, const int32_t* d_k_off, const int32_t* d_k_len,

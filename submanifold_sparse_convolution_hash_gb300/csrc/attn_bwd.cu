@@ -2,8 +2,8 @@
 //
 // With P = exp(scale Q K^T - lse), delta = gout . out per row,
 //   dS = P * (gout V^T - delta),  gq = scale dS K,  gk = scale dS^T Q,  gv = P^T gout.
-// Two kernels, each of whose blocks owns what it writes, so nothing is added by
-// atomics and the same inputs give the same bits:
+// Two kernels, each of whose blocks owns what it writes, so no sum depends on an order
+// of arrival and the same inputs give the same bits:
 //   gk, gv  a block owns 128 keys and walks the rows (all queries and heads of
 //           the group): four products a step, S^T = K Q^T, dP^T = V gout^T,
 //           gv += P^T gout, gk += dS^T Q
@@ -16,18 +16,18 @@
 // a weight of a list of thousands lies there, so P is held times 2^8 (at most
 // 256), and dS times a power of two of its sequence's own, from the largest |gout|
 // and |v| (undone in fp32 as the sums are written).  delta is taken from `out` as the
-// forward rounded it.  These two roundings are what gq and gk
-// are off by (1.6 to 1.9 times the error of an fp32 computation rounded once, up to 2.5 where a
-// few keys take most of the weight and dP - delta cancels).
+// forward rounded it.  The roundings of dS and of `out` are what gq and gk are off by (1.5
+// to 1.9 times the error of an fp32 computation rounded once, up to 2.5 where a few keys
+// take most of the weight and dP - delta cancels).
 //
 // What bounds them.  A step is a chain: S, P, dP, dS, product, each part waiting
-// for the one before; the tensor cores are busy 58 % (gk, gv) and 49 % (gq) of an
+// for the one before; the tensor cores are busy 60 % (gk, gv) and 50 % (gq) of an
 // SM's time at 128 values and 22 % and 18 % at 32, where the exponentials, the
 // conversions and, for gk and gv, the row statistics read from shared memory by
 // every key's lane (47 % of that path) take as long as the products.  Kernel
 // times: five documents of 100 to 3500 tokens, causal, 16 query and 4 key heads of
-// 128, bf16: 126 us and 98 us; 96 windows of 300 to 1000 voxels, 8 heads of 32,
-// f16: 207 us and 191 us.  Measured and left out: tiles of 64 rows by two groups
+// 128, bf16: 123 us and 97 us; 96 windows of 300 to 1000 voxels, 8 heads of 32,
+// f16: 205 us and 190 us, and 27 us for the row statistics.  Measured and left out: tiles of 64 rows by two groups
 // of warps (287 and 224 us for the windows); the next dP made as soon as this one
 // has been read, with dS beside P (209 and 196 us).
 #include "attn_device.cuh"
@@ -1032,8 +1032,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // each quarter writes its columns, 16 at a time
 #pragma unroll 1
       for (int c = quarter * 16; c < p.d; c += 64)
-        store_acc<BF16>(t_dq + lane_off + c, p.o0 + tok * p.o0_t + h * p.o0_h + c * 2, min(16, p.d - c), p.scale * ds_down(up), n > 0,
-                        live);
+        store_acc<BF16>(t_dq + lane_off + c, p.o0 + tok * p.o0_t + h * p.o0_h + c * 2, min(16, p.d - c),
+                        p.scale * ds_down(up), n > 0, live);
       tc_fence_before();
     }
   }

@@ -22,9 +22,12 @@
 // way: 241 us instead of 207 for the voxels below).
 //
 // Kernel times: 32768 tokens, 32 + 8 heads of 128, bf16: 126 us, 5.3 TB/s; 480000
-// tokens, 4 + 4 heads of 64 turned by three axes, f16: forward 198 us (5.0 TB/s; issue
-// slots 62 % busy, DRAM 54 %, no one unit), gradient 265 us (5.6 TB/s; 368 us with the
-// angles worked out for each side and one value an instruction, issue bound).
+// tokens, 4 + 4 heads of 64 turned by three axes, f16: forward 196 us (5.0 TB/s; issue
+// slots 60 % busy, DRAM 61 %, no one unit), gradient 269 us (5.5 TB/s, bound by the
+// instructions it issues: issue slots 70 % busy; 368 us with the angles worked out for
+// each side and one value an instruction); 240000 of them, f32: 205 us (4.8 TB/s) and
+// 364 us (4.1 TB/s).  Four blocks an SM leave the forward 64 registers: its 16-bit forms
+// spill 28 to 128 bytes.
 #include "f32x2.cuh"
 #include "sc_internal.cuh"
 #include "tc_ptx.cuh"
@@ -761,7 +764,7 @@ sc_status rope_run(const RopeArgs& a) {
                                : pick<__nv_bfloat16>(lpr, bwd, norm, pairing);
   if (steps > 0x7fffffff) return set_error(SC_ERR_UNSUPPORTED, "too many tokens");
   if (!bwd) {
-    const int64_t most_blocks = 4ll * sms;  // as many as are resident
+    const int64_t most_blocks = 4ll * sms;  // as many as are resident (f32 rows: three an SM)
     const unsigned grid = static_cast<unsigned>(steps < most_blocks ? steps : most_blocks);
     SC_LAUNCH("qk_norm_rope_fwd", a.stream, (k<<<grid, kThreads, 0, a.stream>>>(p)));
     const cudaError_t e = cudaGetLastError();

@@ -304,8 +304,8 @@ def test_attention_extremes_gradients(dtype):
 def test_attention_scores_of_thousands():
     """Gradients where |lse| is in the thousands: a weight taken from the fp32 lse is off by 2^-22 |lse|."""
     q, k, v, gout, qo, ko, lk, kvd = attn_inputs([70, 200], None, 4, 2, 64, "bf16", sharp=64.0)
-    out, lse, mag, grads, gmag, smax = attn_ref(q.double(), k.double(), v.double(), [70, 200], lk, ko.tolist(), True, 1.0,
-                                                gout.double())
+    out, lse, mag, grads, gmag, smax = attn_ref(q.double(), k.double(), v.double(), [70, 200], lk, ko.tolist(), True,
+                                                1.0, gout.double())
     kw = dict(causal=True, scale=1.0)
     args = (q.cuda(), kvd[:, :2], kvd[:, 2:4])
     o, l = sc.sc_attn_fwd(*args, qo.cuda(), return_lse=True, **kw)
