@@ -189,7 +189,7 @@ def prepare(case, seed):
             s["pre"] = normal(rows, c_out).to(dt)
     if case["fp8"]:  # as a quantising norm leaves the rows, and the weights laid out once
         s["x"], s["sx"] = _quantised(s["x"].float())
-        s["W"], s["sw"] = _quantised(s["W"].float().t())
+        s["W"], s["sw"] = _quantised(s["W"].float().t().contiguous())
         if room:  # the rows within wider ones
             buf = torch.zeros(rows, c_in + room, device=dev, dtype=torch.uint8).view(torch.float8_e4m3fn)
             buf.view(torch.uint8)[:, :c_in] = s["x"].view(torch.uint8)
