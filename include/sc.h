@@ -58,7 +58,8 @@ typedef enum {
   SC_ERR_TIMEOUT = 8          /* a bounded device-side wait gave up (kernel bug) */
 } sc_status;
 
-typedef enum { SC_F32 = 0, SC_F16 = 1, SC_BF16 = 2 } sc_dtype;
+/* SC_E4M3 (8 bits, largest value 448): only where an entry point names it */
+typedef enum { SC_F32 = 0, SC_F16 = 1, SC_BF16 = 2, SC_E4M3 = 3 } sc_dtype;
 
 /* flags for sc_subm_conv_fwd / sc_subm_conv_tune */
 #define SC_RELU 0x1u            /* max(out, 0) before the cast to the output dtype */
@@ -595,6 +596,154 @@ sc_status sc_attn_bwd(const sc_heads* gout, const sc_heads* q, const sc_heads* k
  * on the current device since the last check (SC_ERR_OUT_OF_RANGE: offsets
  * that break the rules above; SC_ERR_TIMEOUT) and clears it. */
 sc_status sc_attn_check(sc_stream stream);
+
+/* --------------------------------------------------------------- rows -- */
+
+/*
+ * Operators on rows [rows, channels]: the features of voxels or text tokens
+ * between the convolutions and the attention.  The source pages have no
+ * counterpart; with these a whole block of such a network, its training step
+ * and its inference in 8 bits run on the library.
+ *
+ * A strided view of rows: channel c of row r lies at data + r * stride + c
+ * (stride in elements), so rows may be parts of wider ones.  data is device
+ * memory, 16-byte aligned, and the stride a multiple of 16 bytes.
+ */
+typedef struct {
+  const void* data;
+  int64_t stride;
+} sc_rows;
+/* The same for rows that a call writes; they must not overlap one another. */
+typedef struct {
+  void* data;
+  int64_t stride;
+} sc_rows_out;
+
+/*
+ * The residual's addition and the norm of rows, in one pass:
+ *   h = x + res,  y = d_w * h / sqrt(mean(h^2) + eps)
+ * and with out_dtype SC_E4M3 the row's scale s = max |y| / 448 and out = y / s
+ * in 8 bits, rounded to nearest, so that y is about out * s.
+ *
+ * res       NULL: h = x.
+ * sum       where h goes, in dtype (the next residual), or NULL.
+ * d_w       fp32 [channels]; NULL: y = h, for SC_E4M3 only (rows, or weights
+ *           laid out as rows, quantised as they are).
+ * d_scale   fp32 [rows], 4-byte aligned; SC_E4M3 only.
+ * channels  a multiple of 8 in [8, 16384].
+ * dtype     of x, res and sum: SC_F32, SC_F16 or SC_BF16.
+ * out_dtype dtype or SC_E4M3 (whose out may be aligned, and its rows strided, by
+ *           multiples of 8 bytes).
+ *
+ * Squares are summed in fp32 from the unrounded h, and each output is rounded
+ * once.  A row whose max |y| / 448 is below 2^-126 is written as zeros with
+ * scale 0.  An infinity leaves its row of 8-bit values without any: scale inf,
+ * values 0 or NaN.  sum may be x or res themselves (the same pointer and
+ * stride), and so may out where it has their dtype; any other overlap is
+ * refused.
+ */
+sc_status sc_add_norm_fwd(const sc_rows* x, const sc_rows* res, const sc_rows_out* sum, const sc_rows_out* out,
+                          float* d_scale, const float* d_w, int64_t rows, int channels, float eps, sc_dtype dtype,
+                          sc_dtype out_dtype, sc_stream stream);
+
+/*
+ * Its gradients.  h: the forward's sum (or x, without a residual); gout: the
+ * gradient of y; gsum: the gradient that reaches h past the norm, or NULL.
+ *   n = h / sqrt(mean(h^2) + eps),  z = d_w * gout,
+ *   gin = (z - n mean(z n)) / sqrt(mean(h^2) + eps) + gsum,  d_gw = sum over rows of gout * n
+ * gin is the gradient of x and of res alike.  d_gw fp32 [channels], or NULL;
+ * summed in fp32 in an order that depends on the sizes alone, so that the same
+ * inputs give the same bits.  gin may be gout, gsum or h themselves; any other
+ * overlap is refused.  The other arguments as for the forward.
+ */
+sc_status sc_add_norm_bwd(const sc_rows* gout, const sc_rows* h, const sc_rows* gsum, const sc_rows_out* gin,
+                          float* d_gw, const float* d_w, int64_t rows, int channels, float eps, sc_dtype dtype,
+                          sc_stream stream);
+
+/* activations of sc_linear_fwd / sc_linear_bwd */
+typedef enum {
+  SC_ACT_NONE = 0,
+  SC_ACT_RELU = 1, /* max(z, 0) */
+  SC_ACT_GELU = 2, /* z (1 + erf(z / sqrt 2)) / 2 */
+  SC_ACT_SILU = 3  /* z / (1 + exp(-z)) */
+} sc_act;
+
+/*
+ * Matrix product with its epilogue:
+ *   z = x W + d_bias,  out = act(z) + res
+ * on the tensor cores, with fp32 sums; out and pre are rounded once.
+ *
+ * x         [rows, c_in]; in_dtype SC_F16, SC_BF16 or SC_E4M3.
+ * d_W       in_dtype, 16-byte aligned, contiguous: [c_in, c_out]; of SC_E4M3
+ *           laid out once as [c_out, c_in].
+ * d_scale_x, d_scale_w  fp32 [rows] and [c_out], SC_E4M3 only (as
+ *           sc_add_norm_fwd writes them): z = d_scale_x[r] d_scale_w[c] sum_i
+ *           x[r, i] W[c, i] + d_bias[c].
+ * d_bias    fp32 [c_out], or NULL.
+ * res       [rows, c_out] in dtype, or NULL.
+ * out       [rows, c_out] in dtype; may be res itself (the same pointer and
+ *           stride); any other overlap is refused.
+ * pre       where z goes, in dtype, for the backward pass, or NULL.
+ * rows      in [0, 2^31 - 256].
+ * c_in, c_out  multiples of 8 (c_in of 16 for SC_E4M3) up to 65536.
+ * dtype     SC_F16 or SC_BF16; in_dtype's unless that is SC_E4M3.
+ *
+ * Few rows take a form that reads the weights once, spread over the card.
+ * Temporary device memory, where sums are cut along c_in, is allocated and
+ * freed stream-ordered on `stream`.  No sum depends on an order of arrival.
+ */
+sc_status sc_linear_fwd(const sc_rows* x, const void* d_W, const float* d_scale_x, const float* d_scale_w,
+                        const float* d_bias, const sc_rows* res, const sc_rows_out* out, const sc_rows_out* pre,
+                        int64_t rows, int c_in, int c_out, sc_act act, sc_dtype in_dtype, sc_dtype dtype,
+                        sc_stream stream);
+
+/*
+ * Its gradients, of the 16-bit forms, from gout, the gradient of out (which is
+ * also that of res), and the forward's x, W and pre:
+ *   gz = gout * act'(pre),  gin = gz W^T,  d_gW = x^T gz,  d_gbias = sum over rows of gz
+ * gin, d_gW [c_in, c_out] (dtype) and d_gbias (fp32) may each be NULL: not
+ * computed; what only they read may then be NULL too.  pre is read only with
+ * an activation.  gz is rounded to dtype for the products; d_gbias sums it
+ * unrounded.  relu'(0) = 0.  All sums are fp32 and in an order that depends on
+ * the sizes alone.  The outputs must not overlap
+ * the inputs that are read, or each other.
+ */
+sc_status sc_linear_bwd(const sc_rows* gout, const sc_rows* x, const sc_rows* pre, const void* d_W,
+                        const sc_rows_out* gin, void* d_gW, float* d_gbias, int64_t rows, int c_in, int c_out,
+                        sc_act act, sc_dtype dtype, sc_stream stream);
+
+/* Synchronises the stream, returns the status latched by sc_linear_fwd and
+ * sc_linear_bwd on the current device since the last check (SC_ERR_TIMEOUT: a
+ * bounded device-side wait gave up and outputs are not whole) and clears it. */
+sc_status sc_linear_check(sc_stream stream);
+
+/* One gradient: n values at data (device memory, aligned to the type), which
+ * go to out (data itself: in place). */
+typedef struct {
+  const void* data;
+  void* out;
+  int64_t n;
+  sc_dtype dtype; /* SC_F32, SC_F16 or SC_BF16 */
+} sc_grad;
+
+/*
+ * The norm of all gradients together, and their scaling to a largest norm:
+ *   norm = sqrt(sum of squares over all values),  out = data * min(1, max_norm / norm)
+ * A norm that is not finite leaves the values as they are (copied where out is
+ * not data); so does max_norm = infinity.
+ *
+ * grads     host array of `count` entries, read during the call only.  The
+ *           entries' dtypes may differ.  Outputs must not overlap each other
+ *           or another entry's data, which is the caller's to see to.
+ * max_norm  not negative, or infinity.
+ * d_norm    fp32 [1], 4-byte aligned: the norm before the scaling.
+ *
+ * No host synchronisation.  Values whose squares leave fp32's range are squared
+ * in 64 bits, and the sums of 64 squares or fewer are added in 64 bits, in an
+ * order that depends on the sizes alone: the same inputs give the same bits.
+ * Each output is rounded once.
+ */
+sc_status sc_grad_clip(const sc_grad* grads, int64_t count, float max_norm, float* d_norm, sc_stream stream);
 
 /* ------------------------------------------------------- device memory -- */
 

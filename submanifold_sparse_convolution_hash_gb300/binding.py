@@ -32,9 +32,12 @@ SC_KMAP_SPLIT = 0x8000
 SC_KMAP_TILE_TABLE = 0x10000
 SC_ROPE_INTERLEAVED = 0x1
 SC_ATTN_CAUSAL = 0x1
+SC_ACT = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 VARIANTS = {"fused": SC_VARIANT_FUSED, "ws": SC_VARIANT_WS, "simt": SC_VARIANT_SIMT, "split": SC_VARIANT_SPLIT}
 VARIANT_NAMES = {v: k for k, v in VARIANTS.items()}
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_E4M3 = torch.float8_e4m3fn
+_E4M3_CODE = 3
 STATUS = {0: "SC_OK", 1: "SC_ERR_INVALID_ARG", 2: "SC_ERR_OUT_OF_RANGE", 3: "SC_ERR_DUPLICATE_COORD",
           4: "SC_ERR_TABLE_FULL", 5: "SC_ERR_UNSUPPORTED", 6: "SC_ERR_CUDA", 7: "SC_ERR_OOM",
           8: "SC_ERR_TIMEOUT"}
@@ -85,6 +88,12 @@ def lib():
             "sc_attn_fwd": ([P] * 8 + [I64, I64, I64, I32, I32, I32, F, I32, U, P], I32),
             "sc_attn_bwd": ([P] * 11 + [I64, I64, I64, I32, I32, I32, F, I32, U, P], I32),
             "sc_attn_check": ([P], I32),
+            "sc_add_norm_fwd": ([P] * 6 + [I64, I32, F, I32, I32, P], I32),
+            "sc_add_norm_bwd": ([P] * 6 + [I64, I32, F, I32, P], I32),
+            "sc_linear_fwd": ([P] * 8 + [I64, I32, I32, I32, I32, I32, P], I32),
+            "sc_linear_bwd": ([P] * 7 + [I64, I32, I32, I32, I32, P], I32),
+            "sc_linear_check": ([P], I32),
+            "sc_grad_clip": ([P, I64, F, P, P], I32),
             "sc_set_allocator": ([P, P, P], I32),
             "sc_status_str": ([I32], ctypes.c_char_p),
             "sc_last_error": ([], ctypes.c_char_p),
@@ -110,8 +119,9 @@ def exported_symbols() -> list:
                         "sc_kmap_destroy",
                         "sc_subm_conv_fwd", "sc_subm_conv_tune", "sc_subm_conv_fwd_noalloc",
                         "sc_subm_conv_bwd_data", "sc_subm_conv_bwd_weight", "sc_qk_norm_rope_fwd",
-                        "sc_qk_norm_rope_bwd", "sc_attn_fwd", "sc_attn_bwd", "sc_attn_check", "sc_set_allocator",
-                        "sc_status_str", "sc_last_error",
+                        "sc_qk_norm_rope_bwd", "sc_attn_fwd", "sc_attn_bwd", "sc_attn_check", "sc_add_norm_fwd",
+                        "sc_add_norm_bwd", "sc_linear_fwd", "sc_linear_bwd", "sc_linear_check", "sc_grad_clip",
+                        "sc_set_allocator", "sc_status_str", "sc_last_error",
                         "sc_launch_count", "sc_profile_enable", "sc_profile_only", "sc_profile_collect",
                         "sc_profile_reset",
                         "sc_profile_get")]
@@ -719,6 +729,270 @@ def sc_attn_check(stream=None):
     """Synchronises and raises what the attention calls on the current device
     latched since the last check (offsets that leave the rows)."""
     _check(lib().sc_attn_check(_stream(stream)), "sc_attn_check")
+
+
+class _Rows(ctypes.Structure):
+    """sc_rows / sc_rows_out: a strided view of rows [rows, channels]."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
+
+
+def _rows(t, name: str, dtype=None, device=None, shape=None):
+    """The view struct of a CUDA tensor [rows, channels] whose channels are
+    contiguous (the rows' stride is free), by reference."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    stride = t.stride()
+    if len(stride) != 2:
+        raise ValueError(f"{name} must be [rows, channels]")
+    if dtype is not None and (t.dtype is not dtype or t.get_device() != device):
+        raise ValueError(f"{name} must be {dtype} on the other rows' device")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if stride[1] != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name}: the channels must be contiguous")
+    return ctypes.byref(_Rows(t.data_ptr(), stride[0]))
+
+
+def _new_rows(t, name: str, shape, dtype, like):
+    """(t, its view): where to write rows of `shape`, made here if t is None."""
+    if t is not None:
+        return t, _rows(t, name, dtype, like.get_device(), shape)
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    return t, ctypes.byref(_Rows(t.data_ptr(), shape[1]))
+
+
+def _same_device(t, name: str) -> int:
+    """The tensor's device, which has to be the current one: its stream is the call's."""
+    device = t.get_device()
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} lies on device {device}, which is not the current one")
+    return device
+
+
+def sc_add_norm_fwd(x, w=None, res=None, eps: float = 1e-6, e4m3: bool = False, out=None, sum=None, stream=None):
+    """The norm of rows after the residual's addition: h = x + res,
+    y = w * h / sqrt(mean(h^2) + eps), for x and res [rows, channels] (any row
+    stride) and w float32 [channels].
+
+    Returns y, or (y, h) with res.  e4m3: y in 8 bits with a scale for each row
+    (float32 [rows]; y is about out * scale), as (out, scale) or (out, scale,
+    h); w may then be None: h as it is.  out, sum: where to write y and h; sum
+    may be x or res themselves, and so may out unless it has 8 bits."""
+    hx = _rows(x, "x")
+    shape, dtype, device = x.shape, x.dtype, _same_device(x, "x")
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("rows must be float32, float16 or bfloat16")
+    hr = hs = scale = None
+    if res is not None:
+        hr = _rows(res, "res", dtype, device, shape)
+        sum, hs = _new_rows(sum, "sum", shape, dtype, x)
+    elif sum is not None:
+        raise ValueError("sum is the sum with res: pass res too")
+    wp = _f32(w, "w", shape[1], device)
+    out, ho = _new_rows(out, "out", shape, _E4M3 if e4m3 else dtype, x)
+    if e4m3:
+        scale = torch.empty(shape[0], dtype=torch.float32, device=x.device)
+    st = (_lib or lib()).sc_add_norm_fwd(hx, hr, hs, ho, scale.data_ptr() if e4m3 else None, wp, shape[0], shape[1],
+                                         eps, code, _E4M3_CODE if e4m3 else code, _raw_stream(stream))
+    if st:
+        _check(st, "sc_add_norm_fwd")
+    if e4m3:
+        return (out, scale) if res is None else (out, scale, sum)
+    return out if res is None else (out, sum)
+
+
+def sc_add_norm_bwd(gout, h, w, gsum=None, eps: float = 1e-6, need_gw: bool = True, gin=None, stream=None):
+    """(gin, gw): the gradients of sc_add_norm_fwd's rows (x and res alike) and
+    weights (float32; None without need_gw), from gout, the gradient of y, and
+    gsum, the gradient that reaches h past the norm.  h: the forward's sum, or
+    its x without a residual.  gin: where to write, which may be gout, gsum or h."""
+    hh = _rows(h, "h")
+    shape, dtype, device = h.shape, h.dtype, _same_device(h, "h")
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("rows must be float32, float16 or bfloat16")
+    hg = _rows(gout, "gout", dtype, device, shape)
+    hs = None if gsum is None else _rows(gsum, "gsum", dtype, device, shape)
+    if w is None:
+        raise ValueError("w must be the forward's weights")
+    wp = _f32(w, "w", shape[1], device)
+    gin, hi = _new_rows(gin, "gin", shape, dtype, h)
+    gw = torch.empty_like(w) if need_gw else None
+    st = (_lib or lib()).sc_add_norm_bwd(hg, hh, hs, hi, gw.data_ptr() if need_gw else None, wp, shape[0], shape[1],
+                                         eps, code, _raw_stream(stream))
+    if st:
+        _check(st, "sc_add_norm_bwd")
+    return gin, gw
+
+
+def _act_code(act) -> int:
+    code = SC_ACT.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(SC_ACT)}")
+    return code
+
+
+def _weights(W, dtype, device, shape):
+    if (not isinstance(W, torch.Tensor) or W.get_device() != device or W.dtype is not dtype or W.dim() != 2
+            or not W.is_contiguous() or (shape is not None and W.shape != shape)):
+        raise ValueError("W must be a contiguous matrix of the rows' dtype, width and device")
+    return W.data_ptr()
+
+
+def sc_linear_fwd(x, W, bias=None, act: str = "none", res=None, scale_x=None, scale_w=None, dtype=None,
+                  return_pre: bool = False, out=None, stream=None):
+    """out = act(x W + bias) + res for x [rows, c_in] (any row stride), W
+    [c_in, c_out] and bias float32 [c_out]; act: "none", "relu", "gelu" or
+    "silu".  return_pre: (out, pre), pre being x W + bias for the backward pass.
+
+    8 bits: x float8_e4m3fn with scale_x float32 [rows], as sc_add_norm_fwd(...,
+    e4m3=True) gives them, and W float8_e4m3fn [c_out, c_in] with scale_w
+    [c_out], which the same call without weights makes once of W's transpose.
+    The outputs are then of `dtype` (default: res's, else bfloat16)."""
+    hx = _rows(x, "x")
+    (rows, c_in), kind, device = x.shape, x.dtype, _same_device(x, "x")
+    code, e4m3 = _act_code(act), kind is _E4M3
+    if e4m3:
+        wp = _weights(W, kind, device, None)
+        c_out = W.shape[0]
+        if W.shape[1] != c_in:
+            raise ValueError("W of 8 bits must be [c_out, c_in]")
+        if scale_x is None or scale_w is None:
+            raise ValueError("8 bits need scale_x and scale_w")
+        xp, sp = _f32(scale_x, "scale_x", rows, device), _f32(scale_w, "scale_w", c_out, device)
+        if dtype is None:
+            dtype = torch.bfloat16 if res is None else res.dtype
+        in_code = _E4M3_CODE
+    else:
+        if scale_x is not None or scale_w is not None:
+            raise ValueError("scales are for 8 bits only")
+        wp = _weights(W, kind, device, None)
+        c_out = W.shape[1]
+        if W.shape[0] != c_in:
+            raise ValueError("W must be [c_in, c_out]")
+        xp = sp = None
+        if dtype is None:
+            dtype = kind
+        in_code = _DTYPES.get(kind)
+    out_code = _DTYPES.get(dtype)
+    if in_code is None or out_code is None:
+        raise ValueError("rows must be float16, bfloat16 or float8_e4m3fn")
+    shape = torch.Size((rows, c_out))
+    bp = _f32(bias, "bias", c_out, device)
+    hr = None if res is None else _rows(res, "res", dtype, device, shape)
+    out, ho = _new_rows(out, "out", shape, dtype, x)
+    pre, hp = _new_rows(None, "pre", shape, dtype, x) if return_pre else (None, None)
+    st = (_lib or lib()).sc_linear_fwd(hx, wp, xp, sp, bp, hr, ho, hp, rows, c_in, c_out, code, in_code, out_code,
+                                       _raw_stream(stream))
+    if st:
+        _check(st, "sc_linear_fwd")
+    return (out, pre) if return_pre else out
+
+
+def sc_linear_bwd(gout, x, W, pre=None, act: str = "none", bias: bool = False, need_gin: bool = True,
+                  need_gW: bool = True, gin=None, stream=None):
+    """(gin, gW, gbias): the gradients of sc_linear_fwd's x, W and bias (float32)
+    from gout, that of its output (and of res), with the forward's x, W and, with
+    an activation, pre.  None where not needed (bias: whether there is one).
+    gin: where to write the rows'."""
+    hg = _rows(gout, "gout")
+    (rows, c_out), dtype, device = gout.shape, gout.dtype, _same_device(gout, "gout")
+    code, kind = _act_code(act), _DTYPES.get(dtype)
+    if kind is None:
+        raise ValueError("rows must be float16 or bfloat16")
+    hx = _rows(x, "x", dtype, device)
+    c_in = x.shape[1]
+    if x.shape[0] != rows:
+        raise ValueError("x and gout must have the same rows")
+    wp = _weights(W, dtype, device, torch.Size((c_in, c_out)))
+    hp = None
+    if code:
+        hp = _rows(pre, "pre", dtype, device, gout.shape)
+    hi = gw = gb = None
+    if need_gin:
+        gin, hi = _new_rows(gin, "gin", x.shape, dtype, gout)
+    elif gin is not None:
+        raise ValueError("gin is given but not needed")
+    if need_gW:
+        gw = torch.empty_like(W)
+    if bias:
+        gb = torch.empty(c_out, dtype=torch.float32, device=gout.device)
+    st = (_lib or lib()).sc_linear_bwd(hg, hx, hp, wp, hi, gw.data_ptr() if need_gW else None,
+                                       gb.data_ptr() if bias else None, rows, c_in, c_out, code, kind,
+                                       _raw_stream(stream))
+    if st:
+        _check(st, "sc_linear_bwd")
+    return gin, gw, gb
+
+
+def sc_linear_check(stream=None):
+    """Synchronises and raises what the linear layers on the current device
+    latched since the last check (a device-side wait that gave up)."""
+    _check(lib().sc_linear_check(_stream(stream)), "sc_linear_check")
+
+
+class _Grad(ctypes.Structure):
+    """sc_grad: one gradient and where it goes."""
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class GradList:
+    """A training program's gradients, looked over once: contiguous CUDA tensors
+    (float32, float16 or bfloat16, mixed as they come) on one device, of any
+    alignment, and where they go when scaled (`out`, tensors like them; default:
+    in place).  Holds the tensors; whoever replaces one makes a new list."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise ValueError("out must hold a tensor for each gradient")
+        entries, spans = [], []
+        self.device = None
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            for t in (g, o):
+                if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous() or t.dtype not in _DTYPES:
+                    raise ValueError(f"gradient {i} must be a contiguous float32, float16 or bfloat16 CUDA tensor")
+            if o.dtype is not g.dtype or o.numel() != g.numel():
+                raise ValueError(f"out[{i}] must have its gradient's dtype and size")
+            if self.device is None:
+                self.device = g.get_device()
+            if g.get_device() != self.device or o.get_device() != self.device:
+                raise ValueError("the gradients must lie on one device")
+            n, size = g.numel(), g.element_size()
+            entries.append((g.data_ptr(), o.data_ptr(), n, _DTYPES[g.dtype]))
+            if n:
+                spans.append((o.data_ptr(), o.data_ptr() + n * size, i))
+                if o is not g and o.data_ptr() != g.data_ptr():
+                    spans.append((g.data_ptr(), g.data_ptr() + n * size, -1))
+        # what is written lies apart from all else, or two blocks would meet there
+        spans.sort()
+        high = high_w = -1  # the furthest end so far, of any run and of a written one
+        for lo, hi, i in spans:
+            if lo < (high if i >= 0 else high_w):
+                raise ValueError("gradients that are written share memory with one another or with others that are read")
+            high = max(high, hi)
+            if i >= 0:
+                high_w = max(high_w, hi)
+        self.entries = (_Grad * len(entries))(*entries)
+
+
+def sc_grad_clip(grads, max_norm: float, stream=None):
+    """The norm of all gradients together (float32 [1], before the scaling) and
+    their scaling by min(1, max_norm / norm), in place or to a GradList's out;
+    a norm that is not finite scales nothing.  grads: a GradList, or tensors to
+    make one of.  No host synchronisation."""
+    if not isinstance(grads, GradList):
+        grads = GradList(grads)
+    current = torch._C._cuda_getDevice()
+    if grads.device is not None and grads.device != current:
+        raise ValueError(f"the gradients lie on device {grads.device}, which is not the current one")
+    norm = torch.empty(1, dtype=torch.float32, device="cuda")
+    st = (_lib or lib()).sc_grad_clip(grads.entries, len(grads.entries), max_norm, norm.data_ptr(), _raw_stream(stream))
+    if st:
+        _check(st, "sc_grad_clip")
+    return norm
 
 
 _ALLOC_FN = ctypes.CFUNCTYPE(ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p)

@@ -1,0 +1,528 @@
+// The residual's addition and the norm of rows, with 16-bit or 8-bit output, and
+// the gradients.
+//
+// One pass over memory: a row's values stay in the registers of the lanes (up to
+// 1024 channels: at most a warp a row) or of the block that hold it, its sums cross
+// them once, and the next row's loads are issued before this row's sums.  y is a
+// positive factor r = 1 / sqrt(mean h^2 + eps) times w h, so the largest |y| of the
+// 8-bit form is r max |w h| and rides along with the sum of squares.
+#include <type_traits>
+
+#include "sc_internal.cuh"
+
+namespace sc {
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+
+template <typename T>
+struct Vec8 {
+  uint4 raw[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Vec8<T> ld_vec(const T* p) {
+  Vec8<T> v;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v.raw[i] = *(reinterpret_cast<const uint4*>(p) + i);
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ Vec8<T> zero_vec() {
+  Vec8<T> v;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v.raw[i] = make_uint4(0, 0, 0, 0);
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void unpack(const Vec8<T>& v, float (&f)[8]) {
+  if constexpr (std::is_same_v<T, float>) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[4 * i] = __uint_as_float(v.raw[i].x);
+      f[4 * i + 1] = __uint_as_float(v.raw[i].y);
+      f[4 * i + 2] = __uint_as_float(v.raw[i].z);
+      f[4 * i + 3] = __uint_as_float(v.raw[i].w);
+    }
+  } else {
+    const uint32_t w[4] = {v.raw[0].x, v.raw[0].y, v.raw[0].z, v.raw[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 t;
+      if constexpr (std::is_same_v<T, __half>) t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      else t = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void st_vec(T* p, const float (&f)[8]) {
+  if constexpr (std::is_same_v<T, float>) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same_v<T, __half>) {
+        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+// Two values as e4m3, the first in the low byte; beyond 448 they become 448.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The sum of a and, with MAX, the largest of b over a row's lanes: a subgroup of G lanes, or
+// (G = 0) the block.  A block's values cross in shared memory; `turn` alternates two
+// places, so that one barrier a row is enough.
+template <int G, bool MAX>
+__device__ __forceinline__ void row_reduce(float& a, float& b, float2 (*s_red)[32], int turn) {
+  constexpr int W = G == 0 ? 32 : G;
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    const float t = __shfl_xor_sync(0xffffffffu, b, o);
+    b = MAX ? fmaxf(b, t) : b + t;
+  }
+  if constexpr (G == 0) {
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) s_red[turn][threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    float2 v = lane < warps ? s_red[turn][lane] : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+      const float t = __shfl_xor_sync(0xffffffffu, v.y, o);
+      v.y = MAX ? fmaxf(v.y, t) : v.y + t;
+    }
+    a = v.x;
+    b = v.y;
+  }
+}
+
+// Eight weights of the vector `at`: kept in registers over the rows up to two vectors a
+// lane, else read again for each row (they stay in L1).
+__device__ __forceinline__ void ld_w(const float* w, int at, float (&f)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(w + at * 8), b = *reinterpret_cast<const float4*>(w + at * 8 + 4);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+template <int NV>
+struct Weights {
+  static constexpr bool kKept = NV <= 2;
+  float f[kKept ? NV : 1][8];
+  const float* w;
+  int lane, lanes, nvec;
+  __device__ __forceinline__ Weights(const float* w_, int lane_, int lanes_, int nvec_)
+      : w(w_), lane(lane_), lanes(lanes_), nvec(nvec_) {
+    if constexpr (kKept) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) read(v, f[v]);
+    }
+  }
+  __device__ __forceinline__ void read(int v, float (&t)[8]) const {
+    const int at = lane + v * lanes;
+    if (w && at < nvec) {
+      ld_w(w, at, t);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = 1.f;
+    }
+  }
+  __device__ __forceinline__ void get(int v, float (&t)[8]) const {
+    if constexpr (kKept) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = f[v][i];
+    } else {
+      read(v, t);
+    }
+  }
+};
+
+// Whether the next row's loads are issued before this row's sums: where a lane has one or
+// two 16-byte loads a tensor of its own row in flight.
+template <typename T, int NV>
+constexpr bool loads_ahead() {
+  return NV * sizeof(T) <= 4;
+}
+
+struct NormParams {
+  const void *x, *res, *gout;
+  void *sum, *out;
+  int64_t ldx, ldres, ldgout, ldsum, ldout;
+  float* scale;
+  const float* w;
+  float* part;  // backward: [blocks, channels], or null
+  int64_t rows;
+  int channels;
+  float eps;
+};
+
+template <int G>
+constexpr int block_size() {
+  return G == 0 ? 512 : 256;
+}
+
+// A row is held by G lanes (or the block, G = 0), vectors of 8 values lane, lane + G, ...
+template <typename T, int NV, int G, bool E4M3>
+__global__ void __launch_bounds__(block_size<G>()) k_add_norm(const NormParams p) {
+  __shared__ float2 s_red[2][32];
+  const int lanes = G == 0 ? blockDim.x : G;
+  const int lane = threadIdx.x % lanes;
+  const int groups = G == 0 ? 1 : block_size<G>() / (G == 0 ? 1 : G);
+  const int nvec = p.channels >> 3;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const T* x = static_cast<const T*>(p.x);
+  const T* res = static_cast<const T*>(p.res);
+  grid_release();
+  grid_wait();
+  const Weights<NV> w(p.w, lane, lanes, nvec);
+  Vec8<T> nx[NV], nr[NV];
+  auto load = [&](int64_t r) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = lane + v * lanes;
+      const bool in = r < p.rows && at < nvec;
+      nx[v] = in ? ld_vec(x + r * p.ldx + at * 8) : zero_vec<T>();
+      nr[v] = in && res ? ld_vec(res + r * p.ldres + at * 8) : zero_vec<T>();
+    }
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / lanes;
+  constexpr bool kAhead = loads_ahead<T, NV>();
+  if (kAhead) load(row);
+  int turn = 0;
+  // the warp's subgroups stay together (their shuffles name the whole warp)
+  for (int64_t base = row - (G == 0 ? 0 : (threadIdx.x & 31) / lanes); base < p.rows; base += step, row += step) {
+    if (!kAhead) load(row);
+    float h[NV][8];
+    float ss = 0.f, top = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float t[8];
+      unpack(nx[v], h[v]);
+      unpack(nr[v], t);
+      if (res) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[v][i] += t[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(h[v][i], h[v][i], ss);
+      if constexpr (E4M3) {
+        w.get(v, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(h[v][i] * t[i]));
+      }
+    }
+    if (kAhead) load(row + step);
+    if (p.sum && row < p.rows) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int at = lane + v * lanes;
+        if (at < nvec) st_vec(static_cast<T*>(p.sum) + row * p.ldsum + at * 8, h[v]);
+      }
+    }
+    row_reduce<G, true>(ss, top, s_red, turn);
+    turn ^= 1;
+    const float r = p.w ? rsqrtf(ss / static_cast<float>(p.channels) + p.eps) : 1.f;
+    if (row >= p.rows) continue;
+    if constexpr (E4M3) {
+      float s = top * r / kE4m3Max;
+      if (s < 0x1p-126f) s = 0.f;
+      const float f = s > 0.f ? 1.f / s : 0.f;
+      if (lane == 0) p.scale[row] = s;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int at = lane + v * lanes;
+        if (at >= nvec) continue;
+        float y[8];
+        w.get(v, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= h[v][i] * r * f;
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * p.ldout + at * 8) =
+            make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16), e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int at = lane + v * lanes;
+        if (at >= nvec) continue;
+        float y[8];
+        w.get(v, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= h[v][i] * r;
+        st_vec(static_cast<T*>(p.out) + row * p.ldout + at * 8, y);
+      }
+    }
+  }
+}
+
+// The gradients.  With z = w gout and r as in the forward, one crossing of the lanes
+// gives sum h^2 and sum z h, and gin = r z - h r^3 (sum z h) / channels + gsum.  The
+// weights' gradient gathers in registers over the rows that a lane's block walks and
+// goes out once a block.
+template <typename T, int NV, int G>
+__global__ void __launch_bounds__(block_size<G>(), G == 0 ? 1 : (NV * sizeof(T) <= 2 ? 3 : 2))
+    k_add_norm_bwd(const NormParams p) {
+  __shared__ float2 s_red[2][32];
+  __shared__ float s_gw[G == 0 ? 1 : G * NV * 8];
+  const int lanes = G == 0 ? blockDim.x : G;
+  const int lane = threadIdx.x % lanes;
+  const int groups = G == 0 ? 1 : block_size<G>() / (G == 0 ? 1 : G);
+  const int nvec = p.channels >> 3;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const T* x = static_cast<const T*>(p.x);
+  const T* gs = static_cast<const T*>(p.res);
+  const T* go = static_cast<const T*>(p.gout);
+  grid_release();
+  grid_wait();
+  const Weights<NV> w(p.w, lane, lanes, nvec);
+  float gw[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gw[v][i] = 0.f;
+  Vec8<T> nx[NV], ng[NV], ns[NV];
+  auto load = [&](int64_t r) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = lane + v * lanes;
+      const bool in = r < p.rows && at < nvec;
+      nx[v] = in ? ld_vec(x + r * p.ldx + at * 8) : zero_vec<T>();
+      ng[v] = in ? ld_vec(go + r * p.ldgout + at * 8) : zero_vec<T>();
+      ns[v] = in && gs ? ld_vec(gs + r * p.ldres + at * 8) : zero_vec<T>();
+    }
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / lanes;
+  constexpr bool kAhead = loads_ahead<T, NV>();
+  if (kAhead) load(row);
+  int turn = 0;
+  for (int64_t base = row - (G == 0 ? 0 : (threadIdx.x & 31) / lanes); base < p.rows; base += step, row += step) {
+    if (!kAhead) load(row);
+    Vec8<T> cx[NV], cg[NV], cs[NV];
+    float ss = 0.f, zh = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      cx[v] = nx[v];
+      cg[v] = ng[v];
+      cs[v] = ns[v];
+      float h[8], g[8], wv[8];
+      unpack(cx[v], h);
+      unpack(cg[v], g);
+      w.get(v, wv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        ss = fmaf(h[i], h[i], ss);
+        zh = fmaf(g[i] * wv[i], h[i], zh);
+      }
+    }
+    if (kAhead) load(row + step);
+    row_reduce<G, false>(ss, zh, s_red, turn);
+    turn ^= 1;
+    const float n = static_cast<float>(p.channels);
+    const float r = rsqrtf(ss / n + p.eps);
+    const float c = zh / n * r * r;
+    if (row >= p.rows) continue;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = lane + v * lanes;
+      if (at >= nvec) continue;
+      float h[8], g[8], s[8], wv[8];
+      unpack(cx[v], h);
+      unpack(cg[v], g);
+      unpack(cs[v], s);
+      w.get(v, wv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        gw[v][i] = fmaf(g[i], h[i] * r, gw[v][i]);
+        s[i] = fmaf(r, g[i] * wv[i] - c * h[i], s[i]);
+      }
+      st_vec(static_cast<T*>(p.out) + row * p.ldout + at * 8, s);
+    }
+  }
+  if (!p.part) return;
+  float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.channels;
+  if constexpr (G == 0) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = lane + v * lanes;
+      if (at >= nvec) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part[at * 8 + i] = gw[v][i];
+    }
+  } else {
+    // one group after the other, so that the order is fixed
+    const int group = threadIdx.x / lanes;
+    for (int g = 0; g < groups; ++g) {
+      if (g == group) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float* s = s_gw + (v * G + lane) * 8 + i;
+            *s = g == 0 ? gw[v][i] : *s + gw[v][i];
+          }
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < p.channels; c += block_size<G>()) part[c] = s_gw[c];
+  }
+}
+
+// The blocks' partial sums, 32 columns and 32 runs of blocks a thread block.
+__global__ void __launch_bounds__(1024) k_column_join(const float* __restrict__ part, int blocks, int channels,
+                                                      float* __restrict__ out) {
+  __shared__ float s[32][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  grid_release();
+  grid_wait();
+  float a = 0.f;
+  if (c < channels)
+    for (int b = threadIdx.y; b < blocks; b += 32) a += part[static_cast<int64_t>(b) * channels + c];
+  s[threadIdx.y][threadIdx.x] = a;
+  __syncthreads();
+  a = s[threadIdx.x][threadIdx.y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  const int cc = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && cc < channels) out[cc] = a;
+}
+
+cudaError_t launch(const char* name, const void* kern, unsigned grid, unsigned block, NormParams& p, cudaStream_t s) {
+  void* args[] = {&p};
+  cudaError_t e;
+  SC_LAUNCH(name, s, e = launch_after(kern, grid, block, 0, s, args));
+  return e;
+}
+
+// Which form holds a row of nvec vectors, and its threads.
+struct Form {
+  int nv, g, threads;
+};
+Form form_of(int nvec, int64_t rows) {
+  if (nvec <= 4) return {1, 4, 256};
+  if (nvec <= 8) return {1, 8, 256};
+  if (nvec <= 16) return {1, 16, 256};
+  if (nvec <= 32) return {1, 32, 256};
+  if (rows > 2048 && nvec <= 64) return {2, 32, 256};
+  if (rows > 2048 && nvec <= 128) return {4, 32, 256};
+  // few rows: a thread holds as little as it can, and the row's latency is short
+  int nv = nvec <= 512 && rows <= 2048 ? 1 : nvec <= 1024 ? 2 : 4;
+  const int t = (nvec + nv - 1) / nv;
+  return {nv, 0, (t + 31) / 32 * 32};
+}
+
+template <typename T, bool E4M3>
+const void* fwd_kernel(const Form& f) {
+  switch (f.g * 8 + f.nv) {
+    case 4 * 8 + 1: return reinterpret_cast<const void*>(k_add_norm<T, 1, 4, E4M3>);
+    case 8 * 8 + 1: return reinterpret_cast<const void*>(k_add_norm<T, 1, 8, E4M3>);
+    case 16 * 8 + 1: return reinterpret_cast<const void*>(k_add_norm<T, 1, 16, E4M3>);
+    case 32 * 8 + 1: return reinterpret_cast<const void*>(k_add_norm<T, 1, 32, E4M3>);
+    case 32 * 8 + 2: return reinterpret_cast<const void*>(k_add_norm<T, 2, 32, E4M3>);
+    case 32 * 8 + 4: return reinterpret_cast<const void*>(k_add_norm<T, 4, 32, E4M3>);
+    case 1: return reinterpret_cast<const void*>(k_add_norm<T, 1, 0, E4M3>);
+    case 2: return reinterpret_cast<const void*>(k_add_norm<T, 2, 0, E4M3>);
+    default: return reinterpret_cast<const void*>(k_add_norm<T, 4, 0, E4M3>);
+  }
+}
+template <typename T>
+const void* bwd_kernel(const Form& f) {
+  switch (f.g * 8 + f.nv) {
+    case 4 * 8 + 1: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 1, 4>);
+    case 8 * 8 + 1: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 1, 8>);
+    case 16 * 8 + 1: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 1, 16>);
+    case 32 * 8 + 1: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 1, 32>);
+    case 32 * 8 + 2: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 2, 32>);
+    case 32 * 8 + 4: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 4, 32>);
+    case 1: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 1, 0>);
+    case 2: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 2, 0>);
+    default: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 4, 0>);
+  }
+}
+
+unsigned grid_of(const Form& f, int64_t rows, int per_sm) {
+  const int64_t groups = f.g ? f.threads / f.g : 1;
+  const int64_t need = (rows + groups - 1) / groups, most = static_cast<int64_t>(device_sm_count()) * per_sm;
+  return static_cast<unsigned>(need < most ? need : most);
+}
+
+}  // namespace
+
+sc_status column_join(const float* part, int blocks, int channels, float* out, cudaStream_t s) {
+  void* args[] = {&part, &blocks, &channels, &out};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((channels + 31) / 32);
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  SC_LAUNCH("column_join", s, e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(k_column_join), args));
+  return e == cudaSuccess ? SC_OK : set_cuda_error(e, "column sums launch");
+}
+
+sc_status add_norm_fwd(const NormArgs& a) {
+  if (a.rows == 0) return SC_OK;
+  NormParams p{};
+  p.x = a.x.data, p.ldx = a.x.stride;
+  p.res = a.res.data, p.ldres = a.res.stride;
+  p.sum = a.sum.data, p.ldsum = a.sum.stride;
+  p.out = a.out.data, p.ldout = a.out.stride;
+  p.scale = a.scale;
+  p.w = a.w;
+  p.rows = a.rows;
+  p.channels = a.channels;
+  p.eps = a.eps;
+  const Form f = form_of(a.channels / 8, a.rows);
+  const void* k;
+  if (a.dtype == SC_F32) k = a.e4m3 ? fwd_kernel<float, true>(f) : fwd_kernel<float, false>(f);
+  else if (a.dtype == SC_F16) k = a.e4m3 ? fwd_kernel<__half, true>(f) : fwd_kernel<__half, false>(f);
+  else k = a.e4m3 ? fwd_kernel<__nv_bfloat16, true>(f) : fwd_kernel<__nv_bfloat16, false>(f);
+  const cudaError_t e = launch("add_norm_fwd", k, grid_of(f, a.rows, kernel_residency(k, f.threads)), f.threads, p, a.stream);
+  return e == cudaSuccess ? SC_OK : set_cuda_error(e, "norm launch");
+}
+
+sc_status add_norm_bwd(const NormArgs& a) {
+  if (a.rows == 0) {
+    if (!a.gw) return SC_OK;
+    const cudaError_t e = cudaMemsetAsync(a.gw, 0, sizeof(float) * a.channels, a.stream);
+    return e == cudaSuccess ? SC_OK : set_cuda_error(e, "norm weight gradient clear");
+  }
+  NormParams p{};
+  p.x = a.x.data, p.ldx = a.x.stride;
+  p.res = a.res.data, p.ldres = a.res.stride;
+  p.gout = a.gout.data, p.ldgout = a.gout.stride;
+  p.out = a.out.data, p.ldout = a.out.stride;
+  p.w = a.w;
+  p.rows = a.rows;
+  p.channels = a.channels;
+  p.eps = a.eps;
+  const Form f = form_of(a.channels / 8, a.rows);
+  const void* k = a.dtype == SC_F32 ? bwd_kernel<float>(f)
+                                    : a.dtype == SC_F16 ? bwd_kernel<__half>(f) : bwd_kernel<__nv_bfloat16>(f);
+  const unsigned grid = grid_of(f, a.rows, kernel_residency(k, f.threads));
+  if (a.gw) {
+    const sc_status st = dev_alloc(reinterpret_cast<void**>(&p.part), sizeof(float) * grid * a.channels, a.stream);
+    if (st) return st;
+  }
+  const cudaError_t e = launch("add_norm_bwd", k, grid, f.threads, p, a.stream);
+  sc_status st = e == cudaSuccess ? SC_OK : set_cuda_error(e, "norm gradient launch");
+  if (!st && a.gw) st = column_join(p.part, static_cast<int>(grid), a.channels, a.gw, a.stream);
+  dev_free(p.part, a.stream);
+  return st;
+}
+
+}  // namespace sc

@@ -9,6 +9,7 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <tuple>
 #include <unordered_map>
 #include <string>
 #include <vector>
@@ -194,6 +195,20 @@ sc_status kernel_carveout(const void* kern, int ctas_per_sm, size_t smem) {
   if (e != cudaSuccess) return set_cuda_error(e, "kernel carveout attribute");
   last[{dev, kern}] = pct;
   return SC_OK;
+}
+
+int kernel_residency(const void* kern, int threads) {
+  static std::mutex mu;
+  static std::map<std::tuple<int, const void*, int>, int> cache;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lk(mu);
+  int& n = cache[std::make_tuple(dev, kern, threads)];
+  if (n == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) != cudaSuccess || n < 1)) {
+    cudaGetLastError();
+    n = 1;
+  }
+  return n;
 }
 
 cudaError_t launch_after(const void* kern, unsigned grid, unsigned block, size_t smem, cudaStream_t s, void** args) {

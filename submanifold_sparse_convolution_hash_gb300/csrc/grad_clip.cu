@@ -1,0 +1,323 @@
+// The norm of many gradients together, and their scaling to a largest norm.
+//
+// Two passes over memory are what the mathematics asks for (every output depends on
+// every value); the second walks the chunks backwards, so that it begins with what the
+// first left in L2.  The gradients' addresses travel in the launch's parameters (up to
+// 32 KB), so there is no table to upload and a captured graph holds its own copy.
+#include <cmath>
+#include <type_traits>
+
+#include "sc_internal.cuh"
+
+namespace sc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunkBytes = 32768;  // what a block takes at a time, of one gradient
+constexpr int kVecs = kChunkBytes / 16 / kThreads;  // 16-byte loads a thread of it
+
+struct Entry {
+  const void* data;
+  void* out;
+  int64_t n;
+  uint32_t chunk0;  // chunks of the launch before this gradient's
+  uint32_t dtype;
+};
+struct Head {
+  double* part;      // a sum of squares for each block of each of the first pass's launches
+  float* norm;
+  int count;         // gradients of this launch
+  uint32_t chunks;   // and their chunks
+  int slot;          // first pass: where this launch's sums go; second: how many sums there are
+  float max_norm;
+};
+// Up to MAX gradients a launch; few gradients take the short table, whose launch
+// carries 2 KB of parameters and not 31.
+template <int MAX>
+struct Table {
+  Head h;
+  Entry e[MAX];
+};
+constexpr int kSmall = 62, kLarge = 960;
+static_assert(sizeof(Table<kLarge>) <= 32764, "launch parameters");
+
+// The gradient that chunk c belongs to.
+template <int MAX>
+__device__ __forceinline__ int entry_of(const Table<MAX>& t, uint32_t c) {
+  int lo = 0, hi = t.h.count - 1;
+  while (lo < hi) {
+    const int m = (lo + hi + 1) >> 1;
+    if (t.e[m].chunk0 <= c) lo = m;
+    else hi = m - 1;
+  }
+  return lo;
+}
+
+__host__ __device__ __forceinline__ int chunk_values(uint32_t dtype) {
+  return dtype == SC_F32 ? kChunkBytes / 4 : kChunkBytes / 2;
+}
+// The first value of chunk c of its gradient, and how many it has.
+__device__ __forceinline__ int64_t chunk_at(const Entry& e, uint32_t c, int* n) {
+  const int size = chunk_values(e.dtype);
+  const int64_t at = static_cast<int64_t>(c - e.chunk0) * size;
+  *n = static_cast<int>(e.n - at < size ? e.n - at : size);
+  return at;
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v) {
+  if constexpr (std::is_same_v<T, float>) return v;
+  else if constexpr (std::is_same_v<T, __half>) return __half2float(v);
+  else return __bfloat162float(v);
+}
+template <typename T>
+__device__ __forceinline__ T from_f(float v) {
+  if constexpr (std::is_same_v<T, float>) return v;
+  else if constexpr (std::is_same_v<T, __half>) return __float2half_rn(v);
+  else return __float2bfloat16_rn(v);
+}
+// The 16 bytes of a vector as floats.
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint4& u, float (&f)[16 / sizeof(T)]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same_v<T, float>) {
+      f[i] = __uint_as_float(w[i]);
+    } else {
+      float2 t;
+      if constexpr (std::is_same_v<T, __half>) t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      else t = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    }
+  }
+}
+
+// A chunk is a head of values up to the first 16-byte boundary, whole vectors, and a
+// tail: where each begins.
+template <typename T>
+struct Span16 {
+  int head, vecs, tail;
+  __device__ __forceinline__ Span16(const T* p, int n) {
+    constexpr int V = 16 / sizeof(T);
+    head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / static_cast<int>(sizeof(T));
+    if (head > n) head = n;
+    vecs = (n - head) / V;
+    tail = n - head - vecs * V;
+  }
+};
+
+// This thread's share of a chunk's sum of squares.  In fp32 over its 65 values or fewer;
+// where that leaves fp32's range at either end, again in 64 bits.
+template <typename T>
+__device__ __forceinline__ double squares(const T* p, int n) {
+  constexpr int V = 16 / sizeof(T);
+  constexpr int L = kVecs;
+  const Span16<T> sp(p, n);
+  const uint4* body = reinterpret_cast<const uint4*>(p + sp.head);
+  float s[2] = {0.f, 0.f};
+  uint32_t any = 0;
+  uint4 u[L];
+#pragma unroll
+  for (int l = 0; l < L; ++l) {
+    const int v = threadIdx.x + l * kThreads;
+    u[l] = v < sp.vecs ? __ldg(body + v) : make_uint4(0, 0, 0, 0);
+  }
+  float edge = 0.f;
+  if (static_cast<int>(threadIdx.x) < sp.head) edge = to_f(p[threadIdx.x]);
+  else if (threadIdx.x >= 32 && static_cast<int>(threadIdx.x) - 32 < sp.tail)
+    edge = to_f(p[sp.head + sp.vecs * V + threadIdx.x - 32]);
+#pragma unroll
+  for (int l = 0; l < L; ++l) {
+    any |= u[l].x | u[l].y | u[l].z | u[l].w;
+    float f[V];
+    unpack16<T>(u[l], f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i & 1] = fmaf(f[i], f[i], s[i & 1]);
+  }
+  s[0] = fmaf(edge, edge, s[0]);
+  const float sum = s[0] + s[1];
+  if (sum >= 0x1p-90f && sum <= 0x1p126f) return sum;
+  if (!any && edge == 0.f) return 0.0;
+  double d = static_cast<double>(edge) * edge;
+#pragma unroll 1
+  for (int l = 0; l < L; ++l) {
+    const int v = threadIdx.x + l * kThreads;
+    if (v >= sp.vecs) break;
+    float f[V];
+    unpack16<T>(__ldg(body + v), f);
+#pragma unroll 1
+    for (int i = 0; i < V; ++i) d += static_cast<double>(f[i]) * f[i];
+  }
+  return d;
+}
+
+__device__ __forceinline__ double block_sum(double v, double* s_warp) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) v += s_warp[w];
+  return v;
+}
+
+template <int MAX>
+__global__ void __launch_bounds__(kThreads) k_grad_squares(const __grid_constant__ Table<MAX> t) {
+  __shared__ double s_warp[kThreads / 32];
+  grid_release();
+  grid_wait();
+  double sum = 0.0;
+  for (uint32_t c = blockIdx.x; c < t.h.chunks; c += gridDim.x) {
+    const Entry& e = t.e[entry_of(t, c)];
+    int n;
+    const int64_t at = chunk_at(e, c, &n);
+    if (e.dtype == SC_F32) sum += squares(static_cast<const float*>(e.data) + at, n);
+    else if (e.dtype == SC_F16) sum += squares(static_cast<const __half*>(e.data) + at, n);
+    else sum += squares(static_cast<const __nv_bfloat16*>(e.data) + at, n);
+  }
+  sum = block_sum(sum, s_warp);
+  if (threadIdx.x == 0) t.h.part[t.h.slot + blockIdx.x] = sum;
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_chunk(const T* p, T* o, int n, float by) {
+  constexpr int V = 16 / sizeof(T);
+  constexpr int L = kVecs;
+  if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) {  // no common boundary
+    for (int i0 = threadIdx.x; i0 < n; i0 += 8 * kThreads) {
+      T v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i0 + k * kThreads < n) v[k] = p[i0 + k * kThreads];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i0 + k * kThreads < n) o[i0 + k * kThreads] = from_f<T>(to_f(v[k]) * by);
+    }
+    return;
+  }
+  const Span16<T> sp(p, n);
+  const uint4* body = reinterpret_cast<const uint4*>(p + sp.head);
+  uint4* dst = reinterpret_cast<uint4*>(o + sp.head);
+  uint4 u[L];
+#pragma unroll
+  for (int l = 0; l < L; ++l) {
+    const int v = threadIdx.x + l * kThreads;
+    if (v < sp.vecs) u[l] = body[v];
+  }
+  if (static_cast<int>(threadIdx.x) < sp.head) o[threadIdx.x] = from_f<T>(to_f(p[threadIdx.x]) * by);
+  else if (threadIdx.x >= 32 && static_cast<int>(threadIdx.x) - 32 < sp.tail) {
+    const int i = sp.head + sp.vecs * V + threadIdx.x - 32;
+    o[i] = from_f<T>(to_f(p[i]) * by);
+  }
+#pragma unroll
+  for (int l = 0; l < L; ++l) {
+    const int v = threadIdx.x + l * kThreads;
+    if (v >= sp.vecs) continue;
+    float f[V];
+    unpack16<T>(u[l], f);
+    T r[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) r[i] = from_f<T>(f[i] * by);
+    dst[v] = *reinterpret_cast<const uint4*>(r);
+  }
+}
+
+template <int MAX>
+__global__ void __launch_bounds__(kThreads) k_grad_scale(const __grid_constant__ Table<MAX> t) {
+  __shared__ double s_warp[kThreads / 32];
+  grid_release();
+  grid_wait();
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < t.h.slot; i += kThreads) sum += t.h.part[i];
+  const double norm = sqrt(block_sum(sum, s_warp));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *t.h.norm = static_cast<float>(norm);
+  const bool cut = isfinite(norm) && norm > static_cast<double>(t.h.max_norm);
+  const float by = cut ? static_cast<float>(static_cast<double>(t.h.max_norm) / norm) : 1.f;
+  for (uint32_t i = blockIdx.x; i < t.h.chunks; i += gridDim.x) {
+    const uint32_t c = t.h.chunks - 1 - i;
+    const Entry& e = t.e[entry_of(t, c)];
+    if (!cut && e.out == e.data) continue;
+    int n;
+    const int64_t at = chunk_at(e, c, &n);
+    if (e.dtype == SC_F32) scale_chunk(static_cast<const float*>(e.data) + at, static_cast<float*>(e.out) + at, n, by);
+    else if (e.dtype == SC_F16)
+      scale_chunk(static_cast<const __half*>(e.data) + at, static_cast<__half*>(e.out) + at, n, by);
+    else
+      scale_chunk(static_cast<const __nv_bfloat16*>(e.data) + at, static_cast<__nv_bfloat16*>(e.out) + at, n, by);
+  }
+}
+
+unsigned grid_of(const void* kern, uint32_t chunks) {
+  const uint32_t most = static_cast<uint32_t>(device_sm_count() * kernel_residency(kern, kThreads));
+  const uint32_t g = chunks < most ? chunks : most;
+  return g ? g : 1;
+}
+
+// Fills a table with gradients from *at on; those without values are left out.
+template <int MAX>
+void fill(Table<MAX>& t, const sc_grad* grads, int64_t count, int64_t* at) {
+  t.h.count = 0;
+  uint64_t chunks = 0;
+  for (; *at < count && t.h.count < MAX; ++*at) {
+    const sc_grad& g = grads[*at];
+    if (g.n == 0) continue;
+    const uint64_t more = static_cast<uint64_t>((g.n - 1) / chunk_values(g.dtype) + 1);
+    if (chunks + more > 0x7fffffffull) break;
+    Entry& e = t.e[t.h.count++];
+    e.data = g.data;
+    e.out = g.out;
+    e.n = g.n;
+    e.chunk0 = static_cast<uint32_t>(chunks);
+    e.dtype = static_cast<uint32_t>(g.dtype);
+    chunks += more;
+  }
+  t.h.chunks = static_cast<uint32_t>(chunks);
+}
+
+template <int MAX>
+sc_status run(const sc_grad* grads, int64_t count, float max_norm, float* d_norm, cudaStream_t s) {
+  const void* sq = reinterpret_cast<const void*>(k_grad_squares<MAX>);
+  const void* sc = reinterpret_cast<const void*>(k_grad_scale<MAX>);
+  Table<MAX> t{};
+  int slots = 0;
+  for (int64_t at = 0; at < count;) {
+    fill(t, grads, count, &at);
+    if (t.h.count) slots += static_cast<int>(grid_of(sq, t.h.chunks));
+  }
+  t.h.norm = d_norm;
+  t.h.max_norm = max_norm;
+  sc_status st = dev_alloc(reinterpret_cast<void**>(&t.h.part), sizeof(double) * static_cast<size_t>(slots), s);
+  if (st) return st;
+  cudaError_t e = cudaSuccess;
+  void* args[] = {&t};
+  int slot = 0;
+  for (int64_t at = 0; at < count && e == cudaSuccess;) {
+    fill(t, grads, count, &at);
+    if (!t.h.count) continue;
+    t.h.slot = slot;
+    const unsigned g = grid_of(sq, t.h.chunks);
+    SC_LAUNCH("grad_squares", s, e = launch_after(sq, g, kThreads, 0, s, args));
+    slot += static_cast<int>(g);
+  }
+  t.h.slot = slots;
+  bool first = true;
+  for (int64_t at = 0; (at < count || first) && e == cudaSuccess; first = false) {
+    fill(t, grads, count, &at);
+    if (!t.h.count && !first) continue;
+    SC_LAUNCH("grad_scale", s, e = launch_after(sc, grid_of(sc, t.h.chunks), kThreads, 0, s, args));
+  }
+  dev_free(t.h.part, s);
+  return e == cudaSuccess ? SC_OK : set_cuda_error(e, "gradient clipping launch");
+}
+
+}  // namespace
+
+sc_status grad_clip(const sc_grad* grads, int64_t count, float max_norm, float* d_norm, cudaStream_t s) {
+  return count <= kSmall ? run<kSmall>(grads, count, max_norm, d_norm, s)
+                         : run<kLarge>(grads, count, max_norm, d_norm, s);
+}
+
+}  // namespace sc

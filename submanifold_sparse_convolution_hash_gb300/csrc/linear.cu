@@ -1,0 +1,159 @@
+// Matrix products on rows: the layer, its gradients, and the pass that makes the
+// gradient before the activation and sums the bias's.
+#include "linear_internal.cuh"
+
+namespace sc {
+namespace {
+
+constexpr int kLanes = 32, kStreams = 8;
+
+// gz = gout * act'(pre), in 16 bits, and the columns' sums of the unrounded values:
+// a warp holds 256 columns of a row (eight a lane), a block's eight warps take rows in
+// turn, and a block writes its sums once.
+template <bool ACT>
+__global__ void __launch_bounds__(kLanes* kStreams)
+    k_act_grad(const uint16_t* __restrict__ gout, int64_t ldg, const uint16_t* __restrict__ pre, int64_t ldp,
+               uint16_t* __restrict__ gz, float* __restrict__ part, int64_t rows, int channels, int act, bool bf16) {
+  __shared__ float s_sum[kStreams][kLanes * 8 + 8];
+  grid_release();
+  grid_wait();
+  const int c = (blockIdx.x * kLanes + threadIdx.x) * 8;
+  const bool in = c < channels;
+  float sum[8] = {};
+  constexpr int kRows = 4;  // rows in flight
+  const int64_t step = static_cast<int64_t>(gridDim.y) * kStreams;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * kStreams + threadIdx.y; r0 < rows && in; r0 += kRows * step) {
+    uint4 g[kRows], z[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t r = r0 + k * step;
+      if (r >= rows) continue;
+      g[k] = *reinterpret_cast<const uint4*>(gout + r * ldg + c);
+      if (ACT) z[k] = *reinterpret_cast<const uint4*>(pre + r * ldp + c);
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t r = r0 + k * step;
+      if (r >= rows) continue;
+      float f[8];
+      unpack8(g[k], bf16, f);
+      if (ACT) {
+        float t[8];
+        unpack8(z[k], bf16, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= slope_of(t[i], act);
+        *reinterpret_cast<uint4*>(gz + r * channels + c) = pack8(f, bf16);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += f[i];
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s_sum[threadIdx.y][threadIdx.x * 8 + i] = sum[i];
+  __syncthreads();
+  const int t = threadIdx.y * kLanes + threadIdx.x, cc = blockIdx.x * kLanes * 8 + t;
+  if (cc >= channels) return;
+  float a = 0.f;
+#pragma unroll
+  for (int y = 0; y < kStreams; ++y) a += s_sum[y][t];
+  part[static_cast<int64_t>(blockIdx.y) * channels + cc] = a;
+}
+
+}  // namespace
+
+sc_status linear_fwd(const LinearArgs& a) {
+  if (a.rows == 0) return SC_OK;
+  Product p{};
+  p.e4m3 = a.in == SC_E4M3;
+  p.k = a.c_in;
+  const Operand x{a.x.data, a.x.stride, false};
+  const Operand w{a.W, p.e4m3 ? a.c_in : a.c_out, !p.e4m3};
+  // Few rows: the weights are A, whose 128-row tiles spread over the card, and the
+  // rows are a narrow B.
+  p.columns = a.rows <= 128;
+  p.a = p.columns ? w : x;
+  p.b = p.columns ? x : w;
+  p.m = p.columns ? a.c_out : a.rows;
+  p.n = p.columns ? a.rows : a.c_out;
+  p.ep = {a.out.data, a.pre.data, a.res.data, a.out.stride, a.pre.stride, a.res.stride, a.bias,
+          a.scale_x,  a.scale_w,  a.act,      a.dtype == SC_BF16};
+  return product_run(p, a.stream);
+}
+
+sc_status linear_bwd(const LinearBwdArgs& a) {
+  const bool bf16 = a.dtype == SC_BF16;
+  cudaStream_t s = a.stream;
+  if (a.rows == 0) {
+    cudaError_t e = cudaSuccess;
+    if (a.gW) e = cudaMemsetAsync(a.gW, 0, static_cast<size_t>(a.c_in) * a.c_out * 2, s);
+    if (e == cudaSuccess && a.gbias) e = cudaMemsetAsync(a.gbias, 0, sizeof(float) * a.c_out, s);
+    return e == cudaSuccess ? SC_OK : set_cuda_error(e, "weight gradient clear");
+  }
+  const bool act = a.act != SC_ACT_NONE;
+  sc_rows gz{a.gout.data, a.gout.stride};
+  void* buf = nullptr;
+  float* part = nullptr;
+  sc_status st = SC_OK;
+  if (act || a.gbias) {
+    const int cols = (a.c_out + kLanes * 8 - 1) / (kLanes * 8);
+    // six blocks an SM, and at least eight rows a warp
+    int64_t runs = (static_cast<int64_t>(device_sm_count()) * 6 + cols - 1) / cols;
+    const int64_t most = (a.rows + kStreams * 8 - 1) / (kStreams * 8);
+    if (runs > most) runs = most;
+    if (act) {
+      st = dev_alloc(&buf, static_cast<size_t>(a.rows) * a.c_out * 2, s);
+      gz = {buf, a.c_out};
+    }
+    if (!st && a.gbias)
+      st = dev_alloc(reinterpret_cast<void**>(&part), sizeof(float) * static_cast<size_t>(runs) * a.c_out, s);
+    if (!st) {
+      const uint16_t* g = static_cast<const uint16_t*>(a.gout.data);
+      const uint16_t* pre = static_cast<const uint16_t*>(a.pre.data);
+      uint16_t* out = static_cast<uint16_t*>(buf);
+      int64_t ldg = a.gout.stride, ldp = a.pre.stride, rows = a.rows;
+      int channels = a.c_out, kind = a.act;
+      bool b = bf16;
+      void* args[] = {&g, &ldg, &pre, &ldp, &out, &part, &rows, &channels, &kind, &b};
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at[0].val.programmaticStreamSerializationAllowed = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(cols, static_cast<unsigned>(runs));
+      cfg.blockDim = dim3(kLanes, kStreams);
+      cfg.stream = s;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      const void* k = act ? reinterpret_cast<const void*>(k_act_grad<true>)
+                          : reinterpret_cast<const void*>(k_act_grad<false>);
+      cudaError_t e;
+      SC_LAUNCH("act_grad", s, e = cudaLaunchKernelExC(&cfg, k, args));
+      if (e != cudaSuccess) st = set_cuda_error(e, "activation gradient launch");
+      if (!st && a.gbias) st = column_join(part, static_cast<int>(runs), a.c_out, a.gbias, s);
+    }
+  }
+  if (!st && a.gW) {  // c_in x c_out, summed over rows
+    Product p{};
+    p.a = {a.x.data, a.x.stride, true};
+    p.b = {gz.data, gz.stride, true};
+    p.m = a.c_in, p.n = a.c_out, p.k = a.rows;
+    p.ep.out = a.gW, p.ep.ldo = a.c_out, p.ep.bf16 = bf16;
+    st = product_run(p, s);
+  }
+  if (!st && a.gin.data) {  // rows x c_in, summed over c_out
+    const bool few = a.rows <= 128;
+    const Operand g{gz.data, gz.stride, false}, w{a.W, a.c_out, false};
+    Product p{};
+    p.columns = few;
+    p.a = few ? w : g;
+    p.b = few ? g : w;
+    p.m = few ? a.c_in : a.rows, p.n = few ? a.rows : a.c_in, p.k = a.c_out;
+    p.ep.out = a.gin.data, p.ep.ldo = a.gin.stride, p.ep.bf16 = bf16;
+    st = product_run(p, s);
+  }
+  dev_free(part, s);
+  dev_free(buf, s);
+  return st;
+}
+
+}  // namespace sc

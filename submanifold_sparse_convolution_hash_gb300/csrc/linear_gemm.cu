@@ -1,0 +1,465 @@
+// The matrix products of the linear layers: persistent tcgen05 kernels.
+//
+// D tiles of 128 rows a block, or 256 a pair of blocks (cta_group::2: each block then
+// stages half of B as well, so a tile costs half of B's reads), and bn columns.  One
+// thread loads both operands by TMA into a ring of shared-memory stages of 128 bytes of
+// k each, one issues the products, eight warps read the sums from TMEM and finish them;
+// two accumulators let that overlap the next tile's products.
+//
+// Whatever its layout, an operand is staged as 128-byte rows with the 128-byte swizzle.
+// K-major: a row holds 64 (8-bit: 128) values of k of one vector.  MN-major: a row holds
+// 64 consecutive vectors' values at one k, 64 rows a panel.  TMA fills what lies past a
+// tensor's end with zeros, so odd sizes need nothing else.
+//
+// Where there are too few tiles for the card, k is cut into runs; each writes fp32
+// sums, which a second kernel adds in order and finishes.
+#include <cmath>
+
+#include "linear_internal.cuh"
+#include "tc_ptx.cuh"
+#include "tma_map.cuh"
+
+namespace sc {
+namespace {
+
+__device__ int g_product_status;
+__global__ void k_product_take_status(int* taken) { *taken = atomicExch(&g_product_status, 0); }
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr int kMaxStages = 12;
+constexpr int kSmemMost = 220 * 1024;
+constexpr int kGroup = 8;  // tile rows whose tiles are neighbours in time: they share B's columns in L2
+
+struct GemmParams {
+  int64_t m, n;
+  int m_tiles, n_tiles, units, splits;
+  int kb, kb_per;  // k blocks in all, and of a unit
+  int bn, stages, tmem_cols;
+  uint32_t b_bytes, idesc;
+  float* part;  // splits > 1: [splits, output rows, output columns]
+  Epilogue ep;
+};
+
+__device__ __forceinline__ void decode(const GemmParams& p, int u, int* mt, int* nt, int* k0, int* k1, int* split) {
+  const int tiles = p.m_tiles * p.n_tiles;
+  *split = u / tiles;
+  const int t = u - *split * tiles;
+  const int per = kGroup * p.n_tiles, g = t / per, r = t - g * per;
+  const int rows = min(kGroup, p.m_tiles - g * kGroup);
+  *nt = r / rows;
+  *mt = g * kGroup + r - *nt * rows;
+  *k0 = *split * p.kb_per;
+  *k1 = min(p.kb, *k0 + p.kb_per);
+}
+
+template <int CTAS, bool E4M3, bool A_MN, bool B_MN, bool COLUMNS>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const GemmParams p) {
+  constexpr bool PAIR = CTAS == 2;
+  constexpr uint32_t kA = 128 * 128;         // bytes of A a stage and block
+  constexpr int kBlock = E4M3 ? 128 : 64;    // values of k a stage
+  constexpr uint32_t kPanel = 64 * 128;      // MN-major: 64 values of k of 64 vectors
+  extern __shared__ uint8_t s_raw[];
+  __shared__ uint64_t s_bar[2 * kMaxStages + 5];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort_word;
+  volatile int* s_abort = &s_abort_word;
+  const uint32_t base = (smem_u32(s_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const uint32_t stage = kA + p.b_bytes;
+  const uint32_t full = smem_u32(s_bar), empty = full + 8 * kMaxStages, accf = empty + 8 * kMaxStages,
+                 acce = accf + 16, done = acce + 16;
+  if (threadIdx.x == 0) {
+    s_abort_word = 0;
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(accf + 8 * i, 1);
+      mbar_init(acce + 8 * i, kEpiWarps * CTAS);
+    }
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  if (warp == kEpiWarps + 1) {
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(&s_tmem), static_cast<uint32_t>(p.tmem_cols));
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&s_tmem), static_cast<uint32_t>(p.tmem_cols));
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  if (PAIR) cluster_sync_all();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  grid_release();
+  grid_wait();
+
+  const int first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
+  if (warp == kEpiWarps) {
+    // ------------------------------------------------------------- loads
+    if (lane == 0) {
+      const uint32_t full_at = PAIR ? map_to_rank(full, 0) : full;
+      int s = 0;
+      uint32_t ph = 1;
+      for (int u = first; u < p.units && !*s_abort; u += stride) {
+        int mt, nt, k0, k1, split;
+        decode(p, u, &mt, &nt, &k0, &k1, &split);
+        const int am = (mt * CTAS + static_cast<int>(rank)) * 128;
+        const int bw = p.bn / CTAS, bn0 = nt * p.bn + static_cast<int>(rank) * bw;
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!mbar_wait(empty + 8 * s, ph, s_abort)) {
+            *s_abort = 1;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, CTAS * stage);
+          const uint32_t bar = full_at + 8 * s, da = base + s * stage, db = da + kA;
+          const int k = kb * kBlock;
+          auto load = [&](uint32_t dst, const CUtensorMap* t, int x, int y) {
+            if (PAIR) tma_load_2d_pair(dst, t, x, y, bar);
+            else tma_load_2d(dst, t, x, y, bar);
+          };
+          if (A_MN) {
+            load(da, &ta, am, k);
+            load(da + kPanel, &ta, am + 64, k);
+          } else {
+            load(da, &ta, k, am);
+          }
+          if (B_MN) {
+            for (int c = 0; c < bw; c += 64) load(db + c * 128, &tb, bn0 + c, k);
+          } else {
+            load(db, &tb, k, bn0);
+          }
+          if (++s == p.stages) s = 0, ph ^= 1;
+        }
+      }
+      // every stage read again before the block may end (after a timeout: its copies landed;
+      // a stage that was never filled passes at once)
+      for (int i = 0; i < p.stages; ++i) {
+        if (*s_abort) {
+          if (rank == 0) mbar_drain(full + 8 * s, ph);
+        } else if (!mbar_wait(empty + 8 * s, ph, s_abort)) {
+          *s_abort = 1;
+        }
+        if (++s == p.stages) s = 0, ph ^= 1;
+      }
+    }
+    __syncwarp();
+  } else if (warp == kEpiWarps + 1) {
+    // ---------------------------------------------------------- products
+    if (lane == 0 && rank == 0) {
+      const uint64_t a0 = A_MN ? smem_desc_mn(base, kPanel, 1024, 2) : smem_desc(base, 1024, 2);
+      const uint64_t b0 = B_MN ? smem_desc_mn(base + kA, kPanel, 1024, 2) : smem_desc(base + kA, 1024, 2);
+      // one step of 32 bytes of k: along the rows, or 16 rows down
+      constexpr uint64_t kStepA = A_MN ? 16 * 128 / 16 : 2, kStepB = B_MN ? 16 * 128 / 16 : 2;
+      int s = 0, j = 0;
+      uint32_t ph = 0;
+      for (int u = first; u < p.units && !*s_abort; u += stride, ++j) {
+        int mt, nt, k0, k1, split;
+        decode(p, u, &mt, &nt, &k0, &k1, &split);
+        const int b = j & 1;
+        if (!mbar_wait(acce + 8 * b, ((j >> 1) & 1) ^ 1, s_abort)) {
+          *s_abort = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(b * p.bn);
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!mbar_wait(full + 8 * s, ph, s_abort)) {
+            *s_abort = 1;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t at = static_cast<uint64_t>(s) * (stage >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_any<PAIR, E4M3>(d, a0 + at + k * kStepA, b0 + at + k * kStepB, p.idesc, kb > k0 || k > 0);
+          if (PAIR) tc_commit_pair(empty + 8 * s);
+          else tc_commit(empty + 8 * s);
+          if (++s == p.stages) s = 0, ph ^= 1;
+        }
+        if (PAIR) tc_commit_pair(accf + 8 * b);
+        else tc_commit(accf + 8 * b);
+      }
+      if (PAIR) tc_commit_pair(done);
+      else tc_commit(done);
+      if (!mbar_drain(done, 0)) *s_abort = 1;
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ results
+    const int q = warp & 3, half = warp >> 2;
+    const uint32_t acce_at = PAIR ? map_to_rank(acce, 0) : acce;
+    int j = 0;
+    for (int u = first; u < p.units; u += stride, ++j) {
+      int mt, nt, k0, k1, split;
+      decode(p, u, &mt, &nt, &k0, &k1, &split);
+      const int b = j & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(accf + 8 * b, (j >> 1) & 1, s_abort))) {
+        *s_abort = 1;
+        break;
+      }
+      tc_fence_after();
+      const int64_t i = static_cast<int64_t>(mt * CTAS + static_cast<int>(rank)) * 128 + q * 32 + lane;
+      const uint32_t trow = tmem + static_cast<uint32_t>(b * p.bn) + (static_cast<uint32_t>(q * 32) << 16);
+      const int64_t n0 = static_cast<int64_t>(nt) * p.bn;
+      if constexpr (COLUMNS) {
+        const bool in = i < p.m;
+        const bool last = p.splits == 1;
+        const float bias = in && last && p.ep.bias ? p.ep.bias[i] : 0.f, sw = in && last && p.ep.sw ? p.ep.sw[i] : 1.f;
+        for (int c = half * 16; c < p.bn; c += 32) {
+          float v[16];
+          __syncwarp();
+          tmem_ld16(trow + static_cast<uint32_t>(c), v);
+          if (in) {
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+              const int64_t r = n0 + c + t;
+              if (r < p.n) {
+                if (last) finish1(p.ep, r, i, v[t], sw, bias);
+                else p.part[(split * p.n + r) * p.m + i] = v[t];
+              }
+            }
+          }
+        }
+      } else {
+        for (int c = half * 32; c < p.bn; c += 64) {
+          float v[32];
+          __syncwarp();
+          tmem_ld32(trow + static_cast<uint32_t>(c), v);
+          if (i < p.m) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const int64_t col = n0 + c + g * 8;
+              if (col < p.n) {
+                float z[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) z[t] = v[g * 8 + t];
+                if (p.splits == 1) {
+                  finish8(p.ep, i, col, z);
+                } else {
+                  float4* dst = reinterpret_cast<float4*>(p.part + (split * p.m + i) * p.n + col);
+                  dst[0] = make_float4(z[0], z[1], z[2], z[3]);
+                  dst[1] = make_float4(z[4], z[5], z[6], z[7]);
+                }
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_cluster(acce_at + 8 * b);
+        else mbar_arrive(acce + 8 * b);
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if (PAIR) cluster_sync_all();
+  else __syncthreads();
+  if (warp == kEpiWarps + 1) {
+    tc_fence_after();
+    if (PAIR) tmem_dealloc_pair(tmem, static_cast<uint32_t>(p.tmem_cols));
+    else tmem_dealloc(tmem, static_cast<uint32_t>(p.tmem_cols));
+  }
+  if (threadIdx.x == 0 && *s_abort) atomicOr(&g_product_status, kDevErrTimeout);
+}
+
+// Adds the runs' sums in order and finishes them, eight columns a thread.
+__global__ void __launch_bounds__(256) k_gemm_join(const float* __restrict__ part, int splits, int64_t rows, int64_t cols,
+                                                   const Epilogue ep) {
+  grid_release();
+  grid_wait();
+  const int64_t per_row = cols >> 3, total = rows * per_row;
+  for (int64_t t = blockIdx.x * 256ll + threadIdx.x; t < total; t += gridDim.x * 256ll) {
+    const int64_t r = t / per_row, c = (t - r * per_row) * 8;
+    float z[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(part + (s * rows + r) * cols + c);
+      const float4 a = src[0], b = src[1];
+      z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w;
+      z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
+    }
+    finish8(ep, r, c, z);
+  }
+}
+
+// Tiles and cuts of a product.
+struct Plan {
+  int ctas, bn, splits, kb_per;
+};
+
+// The cheapest by an estimate in SM clocks.  A k block of a tile costs its products
+// (4096 16-bit multiply-adds a clock) or its operands' way into shared memory (about 48
+// bytes a clock and SM), whichever is longer; a unit about 1500 clocks before its first
+// product and after its last, half of which overlap its neighbours'; cut sums are
+// written and read once more (about 16 bytes a clock and SM in each direction).
+Plan plan_of(const Product& p, int kb) {
+  const int sms = device_sm_count();
+  Plan best{1, 64, 1, kb};
+  double least = 1e300;
+  for (int form = 0; form < 5; ++form) {
+    const int ctas = form < 2 ? 2 : 1, bn = form == 0 || form == 2 ? 256 : form == 1 || form == 3 ? 128 : 64;
+    const int64_t tiles = ((p.m + 128 * ctas - 1) / (128 * ctas)) * ((p.n + bn - 1) / bn);
+    const int slots = sms / ctas;
+    const double step = fmax(2.0 * bn, (128.0 * 128 + bn * 128.0 / ctas) / 48.0);
+    for (int splits = 1; splits <= kb && splits <= 2 * slots; ++splits) {
+      const int per = (kb + splits - 1) / splits;
+      if ((kb + per - 1) / per != splits) continue;  // the same cut as a smaller number's
+      if (splits > 1 && (tiles * splits > 4 * slots || per < 4)) break;
+      const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
+      double cost = waves * (per * step + 700.0) + 800.0;
+      if (splits > 1) cost += 4000.0 + static_cast<double>(p.m) * p.n * 4.0 * splits * 2.0 / (16.0 * sms);
+      if (cost < least) {
+        least = cost;
+        best = {ctas, bn, splits, per};
+      }
+    }
+  }
+  return best;
+}
+// Few rows: the weights stream through once, so k is cut until the card is busy.
+Plan plan_columns(const Product& p, int kb) {
+  const int sms = device_sm_count();
+  Plan best{1, static_cast<int>((p.n + 15) / 16 * 16), 1, kb};
+  const int64_t tiles = (p.m + 127) / 128;
+  double least = 1e300;
+  for (int splits = 1; splits <= kb && splits <= 64; ++splits) {
+    const int per = (kb + splits - 1) / splits;
+    if ((kb + per - 1) / per != splits) continue;
+    const double waves = static_cast<double>((tiles * splits + sms - 1) / sms);
+    double cost = waves * (per * (128.0 * 128 + best.bn * 128) / 24.0 + 700.0);
+    if (splits > 1) cost += 4000.0 + static_cast<double>(p.m) * p.n * 4.0 * splits * 2.0 / (16.0 * sms);
+    if (cost < least) {
+      least = cost;
+      best.splits = splits;
+      best.kb_per = per;
+    }
+  }
+  return best;
+}
+
+sc_status make_map(CUtensorMap* map, const Operand& o, int64_t vectors, int64_t k, bool e4m3, int box_vectors) {
+  const EncodeTiledFn encode = tensor_map_encoder();
+  if (!encode) return set_error(SC_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const int eb = e4m3 ? 1 : 2;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(o.mn ? vectors : k), static_cast<cuuint64_t>(o.mn ? k : vectors)};
+  // a single run's stride is never used; it has to be a legal one
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>((dims[1] > 1 ? o.ld : (dims[0] + 15) / 16 * 16) * eb)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / eb), static_cast<cuuint32_t>(o.mn ? 64 : box_vectors)};
+  const cuuint32_t one[2] = {1, 1};
+  const CUresult r =
+      encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(o.data),
+             dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SC_OK : set_error(SC_ERR_CUDA, "tensor map of an operand");
+}
+
+const void* kernel_of(const Product& p, int ctas) {
+#define SC_K(...) reinterpret_cast<const void*>(k_gemm<__VA_ARGS__>)
+  if (p.columns) {
+    if (p.e4m3) return SC_K(1, true, false, false, true);
+    return p.a.mn ? SC_K(1, false, true, false, true) : SC_K(1, false, false, false, true);
+  }
+  if (p.e4m3) return ctas == 2 ? SC_K(2, true, false, false, false) : SC_K(1, true, false, false, false);
+  if (p.a.mn) return ctas == 2 ? SC_K(2, false, true, true, false) : SC_K(1, false, true, true, false);
+  if (p.b.mn) return ctas == 2 ? SC_K(2, false, false, true, false) : SC_K(1, false, false, true, false);
+  return ctas == 2 ? SC_K(2, false, false, false, false) : SC_K(1, false, false, false, false);
+#undef SC_K
+}
+
+}  // namespace
+
+sc_status product_run(const Product& p, cudaStream_t s) {
+  const int block = p.e4m3 ? 128 : 64;
+  const int kb = static_cast<int>((p.k + block - 1) / block);
+  const Plan pl = p.columns ? plan_columns(p, kb) : plan_of(p, kb);
+  GemmParams g{};
+  g.m = p.m;
+  g.n = p.n;
+  const int64_t mt = (p.m + 128 * pl.ctas - 1) / (128 * pl.ctas), nt = (p.n + pl.bn - 1) / pl.bn;
+  if (mt * nt * pl.splits > 0x7fffffff) return set_error(SC_ERR_UNSUPPORTED, "a product of over 2^31 tiles");
+  g.m_tiles = static_cast<int>(mt);
+  g.n_tiles = static_cast<int>(nt);
+  g.splits = pl.splits;
+  g.units = static_cast<int>(mt * nt * pl.splits);
+  g.kb = kb;
+  g.kb_per = pl.kb_per;
+  g.bn = pl.bn;
+  g.b_bytes = static_cast<uint32_t>(pl.bn / pl.ctas) * 128;
+  g.tmem_cols = 32;
+  while (g.tmem_cols < 2 * pl.bn) g.tmem_cols *= 2;
+  const uint32_t stage = 128 * 128 + g.b_bytes;
+  g.stages = static_cast<int>(kSmemMost / stage);
+  if (g.stages > kMaxStages) g.stages = kMaxStages;
+  const int M = 128 * pl.ctas;
+  g.idesc = p.e4m3 ? make_idesc_e4m3(M, pl.bn)
+                   : make_idesc(p.ep.bf16, M, pl.bn) | (p.a.mn ? 1u << 15 : 0u) | (p.b.mn ? 1u << 16 : 0u);
+  g.ep = p.ep;
+  CUtensorMap ta, tb;
+  sc_status st = make_map(&ta, p.a, p.m, p.k, p.e4m3, 128);
+  if (!st) st = make_map(&tb, p.b, p.n, p.k, p.e4m3, pl.bn / pl.ctas);
+  if (st) return st;
+  const void* kern = kernel_of(p, pl.ctas);
+  const size_t smem = 1024 + static_cast<size_t>(g.stages) * stage;
+  if ((st = kernel_setup(kern, smem, nullptr))) return st;
+  if (pl.splits > 1) {
+    st = dev_alloc(reinterpret_cast<void**>(&g.part), sizeof(float) * static_cast<size_t>(pl.splits) * p.m * p.n, s);
+    if (st) return st;
+  }
+  const int slots = device_sm_count() / pl.ctas;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(pl.ctas);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((g.units < slots ? g.units : slots) * pl.ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  void* args[] = {&ta, &tb, &g};
+  cudaError_t e;
+  SC_LAUNCH("linear_gemm", s, e = cudaLaunchKernelExC(&cfg, kern, args));
+  if (e == cudaSuccess && pl.splits > 1) {
+    int64_t rows = p.columns ? p.n : p.m, cols = p.columns ? p.m : p.n;
+    int64_t blocks = (rows * (cols / 8) + 255) / 256;
+    if (blocks > device_sm_count() * 8) blocks = device_sm_count() * 8;
+    int splits = pl.splits;
+    Epilogue ep = p.ep;
+    void* jargs[] = {&g.part, &splits, &rows, &cols, &ep};
+    SC_LAUNCH("linear_join", s, e = launch_after(reinterpret_cast<const void*>(k_gemm_join),
+                                                 static_cast<unsigned>(blocks), 256, 0, s, jargs));
+  }
+  dev_free(g.part, s);
+  return e == cudaSuccess ? SC_OK : set_cuda_error(e, "matrix product launch");
+}
+
+sc_status product_take_status(cudaStream_t s, int* bits) {
+  void* d = nullptr;
+  sc_status st = dev_alloc(&d, sizeof(int), s);
+  if (st) return st;
+  SC_LAUNCH("linear_take_status", s, (k_product_take_status<<<1, 1, 0, s>>>(static_cast<int*>(d))));
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyAsync(bits, d, sizeof(int), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  dev_free(d, s);
+  return e == cudaSuccess ? SC_OK : set_cuda_error(e, "product status");
+}
+
+}  // namespace sc

@@ -1,0 +1,134 @@
+// What the matrix products on rows share: the operands' and the epilogue's
+// parameters, activations and their slopes.
+#pragma once
+
+#include "sc_internal.cuh"
+
+namespace sc {
+
+// z = acc * sx[r] * sw[c] + bias[c]; pre = z; out = act(z) + res.
+struct Epilogue {
+  void *out, *pre;
+  const void* res;
+  int64_t ldo, ldp, ldr;
+  const float *bias, *sx, *sw;
+  int act;
+  bool bf16;
+};
+
+namespace {
+
+__device__ __forceinline__ float act_of(float z, int act) {
+  switch (act) {
+    case SC_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
+    case SC_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    case SC_ACT_SILU: return __fdividef(z, 1.f + __expf(-z));
+    default: return z;
+  }
+}
+__device__ __forceinline__ float slope_of(float z, int act) {
+  switch (act) {
+    case SC_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+    case SC_ACT_GELU:
+      return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+    case SC_ACT_SILU: {
+      const float p = __fdividef(1.f, 1.f + __expf(-z));
+      return p * (1.f + z * (1.f - p));
+    }
+    default: return 1.f;
+  }
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack16(uint32_t w, bool bf16) {
+  if (bf16) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ void unpack8(const uint4& u, bool bf16, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = unpack16(w[i], bf16);
+    f[2 * i] = t.x;
+    f[2 * i + 1] = t.y;
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8], bool bf16) {
+  return make_uint4(pack16(f[0], f[1], bf16), pack16(f[2], f[3], bf16), pack16(f[4], f[5], bf16),
+                    pack16(f[6], f[7], bf16));
+}
+__device__ __forceinline__ float load16(const void* p, int64_t at, bool bf16) {
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at])
+              : __half2float(static_cast<const __half*>(p)[at]);
+}
+__device__ __forceinline__ void store16(void* p, int64_t at, float v, bool bf16) {
+  if (bf16) static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p)[at] = __float2half_rn(v);
+}
+
+// Eight columns of row r from c on: z from the sums, then the outputs.
+__device__ __forceinline__ void finish8(const Epilogue& e, int64_t r, int64_t c, float (&z)[8]) {
+  if (e.sw) {
+    const float a = e.sx[r];
+    const float4 s0 = *reinterpret_cast<const float4*>(e.sw + c), s1 = *reinterpret_cast<const float4*>(e.sw + c + 4);
+    z[0] *= a * s0.x, z[1] *= a * s0.y, z[2] *= a * s0.z, z[3] *= a * s0.w;
+    z[4] *= a * s1.x, z[5] *= a * s1.y, z[6] *= a * s1.z, z[7] *= a * s1.w;
+  }
+  if (e.bias) {
+    const float4 s0 = *reinterpret_cast<const float4*>(e.bias + c),
+                 s1 = *reinterpret_cast<const float4*>(e.bias + c + 4);
+    z[0] += s0.x, z[1] += s0.y, z[2] += s0.z, z[3] += s0.w;
+    z[4] += s1.x, z[5] += s1.y, z[6] += s1.z, z[7] += s1.w;
+  }
+  if (e.pre) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.pre) + r * e.ldp + c) = pack8(z, e.bf16);
+  if (e.act) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_of(z[i], e.act);
+  }
+  if (e.res) {
+    float t[8];
+    unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.res) + r * e.ldr + c), e.bf16, t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += t[i];
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + r * e.ldo + c) = pack8(z, e.bf16);
+}
+// One value, for the form whose lanes hold columns.
+__device__ __forceinline__ void finish1(const Epilogue& e, int64_t r, int64_t c, float z, float sw, float bias) {
+  if (e.sw) z *= e.sx[r] * sw;
+  z += bias;
+  if (e.pre) store16(e.pre, r * e.ldp + c, z, e.bf16);
+  z = act_of(z, e.act);
+  if (e.res) z += load16(e.res, r * e.ldr + c, e.bf16);
+  store16(e.out, r * e.ldo + c, z, e.bf16);
+}
+
+}  // namespace
+
+// D [m, n] = A B on the tensor cores, A's row i and B's column j vectors of k
+// values.  An operand is K-major (its vectors lie along k, `ld` apart) or MN-major
+// (memory holds for each k a run over i or j, runs `ld` apart).
+struct Operand {
+  const void* data;
+  int64_t ld;  // elements
+  bool mn;
+};
+struct Product {
+  Operand a, b;
+  int64_t m, n, k;
+  bool e4m3;    // both operands, K-major (else 16 bits: bf16 as in the epilogue)
+  bool columns; // D's rows are the output's columns (few rows: A holds the weights)
+  Epilogue ep;
+};
+sc_status product_run(const Product& p, cudaStream_t s);
+// Reads and clears the status bits the products' kernels latched; synchronises.
+sc_status product_take_status(cudaStream_t s, int* bits);
+
+}  // namespace sc

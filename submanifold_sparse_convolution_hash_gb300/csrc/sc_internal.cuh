@@ -155,6 +155,10 @@ sc_status kernel_setup(const void* kern, size_t smem, int* num_regs);
 // holds the neighbour-index loads); cached, so set only when it changes.
 sc_status kernel_carveout(const void* kern, int ctas_per_sm, size_t smem);
 
+// Blocks of `threads` threads (and no dynamic shared memory) of a kernel that an
+// SM holds, at least 1; cached per device and kernel.
+int kernel_residency(const void* kern, int threads);
+
 // Launches a kernel that may begin while the one before it on the stream still
 // runs (programmatic dependent launch): it calls grid_wait() before it touches
 // what that one writes, and again grid_wait() before it ends if it did not.
@@ -250,6 +254,55 @@ sc_status attn_fwd(const AttnArgs& a);
 sc_status attn_bwd(const AttnArgs& a);
 // Reads and clears the status bits the attention kernels latched; synchronises.
 sc_status attn_take_status(cudaStream_t s, int* bits);
+
+// kernels: rows [rows, channels] (add_norm.cu, linear*.cu, grad_clip.cu)
+struct NormArgs {
+  sc_rows x, res;        // forward: res.data null: no addition; backward: res = the gradient past the norm
+  sc_rows gout;          // backward
+  sc_rows_out sum, out;  // forward (sum.data null: not stored); backward: out = gin
+  float* scale;          // e4m3 output
+  const float* w;        // null: no norm (e4m3 output only)
+  float* gw;             // backward, or null
+  int64_t rows;
+  int channels;
+  float eps;
+  sc_dtype dtype;
+  bool e4m3;
+  cudaStream_t stream;
+};
+sc_status add_norm_fwd(const NormArgs& a);
+sc_status add_norm_bwd(const NormArgs& a);
+// out[c] = the sum over b of part[b * channels + c], b < blocks, in that order's fixed tree
+sc_status column_join(const float* part, int blocks, int channels, float* out, cudaStream_t s);
+
+struct LinearArgs {
+  sc_rows x, res;
+  const void* W;
+  const float *scale_x, *scale_w, *bias;
+  sc_rows_out out, pre;  // pre.data null: not stored
+  int64_t rows;
+  int c_in, c_out;
+  sc_dtype in, dtype;  // of x and W; of out, pre and res
+  int act;
+  cudaStream_t stream;
+};
+sc_status linear_fwd(const LinearArgs& a);
+
+struct LinearBwdArgs {
+  sc_rows gout, x, pre;
+  const void* W;
+  sc_rows_out gin;  // data null: not computed
+  void* gW;         // null: not computed
+  float* gbias;
+  int64_t rows;
+  int c_in, c_out;
+  sc_dtype dtype;
+  int act;
+  cudaStream_t stream;
+};
+sc_status linear_bwd(const LinearBwdArgs& a);
+
+sc_status grad_clip(const sc_grad* grads, int64_t count, float max_norm, float* d_norm, cudaStream_t s);
 
 // A device (or managed) pointer with the given alignment.
 sc_status check_dev_ptr(const void* p, size_t align, const char* what);
