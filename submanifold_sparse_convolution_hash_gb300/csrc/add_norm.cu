@@ -408,7 +408,7 @@ cudaError_t launch(const char* name, const void* kern, unsigned grid, unsigned b
 struct Form {
   int nv, g, threads;
 };
-Form form_of(int nvec, int64_t rows) {
+Form form_of(int nvec, int64_t rows, bool bwd) {
   if (nvec <= 4) return {1, 4, 256};
   if (nvec <= 8) return {1, 8, 256};
   if (nvec <= 16) return {1, 16, 256};
@@ -416,7 +416,7 @@ Form form_of(int nvec, int64_t rows) {
   if (rows > 2048 && nvec <= 64) return {2, 32, 256};
   if (rows > 2048 && nvec <= 128) return {4, 32, 256};
   // few rows: a thread holds as little as it can, and the row's latency is short
-  int nv = nvec <= 512 && rows <= 2048 ? 1 : nvec <= 1024 ? 2 : 4;
+  int nv = nvec <= 512 && (rows <= 2048 || bwd) ? 1 : nvec <= 1024 ? 2 : 4;
   const int t = (nvec + nv - 1) / nv;
   return {nv, 0, (t + 31) / 32 * 32};
 }
@@ -486,7 +486,7 @@ sc_status add_norm_fwd(const NormArgs& a) {
   p.rows = a.rows;
   p.channels = a.channels;
   p.eps = a.eps;
-  const Form f = form_of(a.channels / 8, a.rows);
+  const Form f = form_of(a.channels / 8, a.rows, false);
   const void* k;
   if (a.dtype == SC_F32) k = a.e4m3 ? fwd_kernel<float, true>(f) : fwd_kernel<float, false>(f);
   else if (a.dtype == SC_F16) k = a.e4m3 ? fwd_kernel<__half, true>(f) : fwd_kernel<__half, false>(f);
@@ -510,7 +510,7 @@ sc_status add_norm_bwd(const NormArgs& a) {
   p.rows = a.rows;
   p.channels = a.channels;
   p.eps = a.eps;
-  const Form f = form_of(a.channels / 8, a.rows);
+  const Form f = form_of(a.channels / 8, a.rows, true);
   const void* k = a.dtype == SC_F32 ? bwd_kernel<float>(f)
                                     : a.dtype == SC_F16 ? bwd_kernel<__half>(f) : bwd_kernel<__nv_bfloat16>(f);
   const unsigned grid = grid_of(f, a.rows, kernel_residency(k, f.threads));

@@ -70,6 +70,24 @@ __device__ __forceinline__ float to_f(T v) {
   else if constexpr (std::is_same_v<T, __half>) return __half2float(v);
   else return __bfloat162float(v);
 }
+// And back, rounded.
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float (&f)[16 / sizeof(T)]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same_v<T, float>) {
+      w[i] = __float_as_uint(f[i]);
+    } else if constexpr (std::is_same_v<T, __half>) {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 template <typename T>
 __device__ __forceinline__ T from_f(float v) {
   if constexpr (std::is_same_v<T, float>) return v;
@@ -165,7 +183,7 @@ __device__ __forceinline__ double block_sum(double v, double* s_warp) {
 }
 
 template <int MAX>
-__global__ void __launch_bounds__(kThreads) k_grad_squares(const __grid_constant__ Table<MAX> t) {
+__global__ void __launch_bounds__(kThreads, 4) k_grad_squares(const __grid_constant__ Table<MAX> t) {
   __shared__ double s_warp[kThreads / 32];
   grid_release();
   grid_wait();
@@ -185,48 +203,46 @@ __global__ void __launch_bounds__(kThreads) k_grad_squares(const __grid_constant
 template <typename T>
 __device__ __forceinline__ void scale_chunk(const T* p, T* o, int n, float by) {
   constexpr int V = 16 / sizeof(T);
-  constexpr int L = kVecs;
   if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) {  // no common boundary
     for (int i0 = threadIdx.x; i0 < n; i0 += 8 * kThreads) {
-      T v[8];
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = i0 + k * kThreads < n ? to_f(p[i0 + k * kThreads]) : 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (i0 + k * kThreads < n) v[k] = p[i0 + k * kThreads];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (i0 + k * kThreads < n) o[i0 + k * kThreads] = from_f<T>(to_f(v[k]) * by);
+        if (i0 + k * kThreads < n) o[i0 + k * kThreads] = from_f<T>(f[k] * by);
     }
     return;
   }
   const Span16<T> sp(p, n);
   const uint4* body = reinterpret_cast<const uint4*>(p + sp.head);
   uint4* dst = reinterpret_cast<uint4*>(o + sp.head);
-  uint4 u[L];
-#pragma unroll
-  for (int l = 0; l < L; ++l) {
-    const int v = threadIdx.x + l * kThreads;
-    if (v < sp.vecs) u[l] = body[v];
-  }
-  if (static_cast<int>(threadIdx.x) < sp.head) o[threadIdx.x] = from_f<T>(to_f(p[threadIdx.x]) * by);
-  else if (threadIdx.x >= 32 && static_cast<int>(threadIdx.x) - 32 < sp.tail) {
+  if (static_cast<int>(threadIdx.x) < sp.head) {
+    o[threadIdx.x] = from_f<T>(to_f(p[threadIdx.x]) * by);
+  } else if (threadIdx.x >= 32 && static_cast<int>(threadIdx.x) - 32 < sp.tail) {
     const int i = sp.head + sp.vecs * V + threadIdx.x - 32;
     o[i] = from_f<T>(to_f(p[i]) * by);
   }
+  // four loads in flight a thread; more would leave fewer blocks an SM
+#pragma unroll 1
+  for (int l0 = threadIdx.x; l0 < sp.vecs; l0 += 4 * kThreads) {
+    uint4 u[4];
 #pragma unroll
-  for (int l = 0; l < L; ++l) {
-    const int v = threadIdx.x + l * kThreads;
-    if (v >= sp.vecs) continue;
-    float f[V];
-    unpack16<T>(u[l], f);
-    T r[V];
+    for (int l = 0; l < 4; ++l) u[l] = body[min(l0 + l * kThreads, sp.vecs - 1)];
 #pragma unroll
-    for (int i = 0; i < V; ++i) r[i] = from_f<T>(f[i] * by);
-    dst[v] = *reinterpret_cast<const uint4*>(r);
+    for (int l = 0; l < 4; ++l) {
+      if (l0 + l * kThreads >= sp.vecs) continue;
+      float f[V];
+      unpack16<T>(u[l], f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] *= by;
+      dst[l0 + l * kThreads] = pack16<T>(f);
+    }
   }
 }
 
 template <int MAX>
-__global__ void __launch_bounds__(kThreads) k_grad_scale(const __grid_constant__ Table<MAX> t) {
+__global__ void __launch_bounds__(kThreads, 4) k_grad_scale(const __grid_constant__ Table<MAX> t) {
   __shared__ double s_warp[kThreads / 32];
   grid_release();
   grid_wait();

@@ -11,7 +11,7 @@ constexpr int kLanes = 32, kStreams = 8;
 // a warp holds 256 columns of a row (eight a lane), a block's eight warps take rows in
 // turn, and a block writes its sums once.
 template <bool ACT>
-__global__ void __launch_bounds__(kLanes* kStreams)
+__global__ void __launch_bounds__(kLanes* kStreams, 3)
     k_act_grad(const uint16_t* __restrict__ gout, int64_t ldg, const uint16_t* __restrict__ pre, int64_t ldp,
                uint16_t* __restrict__ gz, float* __restrict__ part, int64_t rows, int channels, int act, bool bf16) {
   __shared__ float s_sum[kStreams][kLanes * 8 + 8];

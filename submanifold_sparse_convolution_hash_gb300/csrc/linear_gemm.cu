@@ -25,10 +25,12 @@ namespace {
 __device__ int g_product_status;
 __global__ void k_product_take_status(int* taken) { *taken = atomicExch(&g_product_status, 0); }
 
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kThreads = (kEpiWarps + 2) * 32;
 constexpr int kMaxStages = 12;
-constexpr int kSmemMost = 220 * 1024;
+constexpr int kSmemMost = 230400;                  // of 232,448, with the barriers and the alignment
+constexpr uint32_t kTile = 32 * 128;              // 32 rows of 128 bytes on their way out
+constexpr uint32_t kStaging = kEpiWarps * kTile;
 constexpr int kGroup = 8;  // tile rows whose tiles are neighbours in time: they share B's columns in L2
 
 struct GemmParams {
@@ -40,6 +42,50 @@ struct GemmParams {
   float* part;  // splits > 1: [splits, output rows, output columns]
   Epilogue ep;
 };
+
+// Maps of what the rows' form writes and reads past the products: tiles of 64 16-bit
+// columns (the sums: 32) and 32 rows.
+struct OutMaps {
+  CUtensorMap out, pre, res, part;
+};
+
+// 32 columns of a row from c on (of which `cols` exist): z from the sums.
+__device__ __forceinline__ void scale32(const Epilogue& e, float sx, int64_t c, int cols, float (&z)[32]) {
+  if (e.sw) {
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      if (4 * g >= cols) break;
+      const float4 s = __ldg(reinterpret_cast<const float4*>(e.sw + c) + g);
+      z[4 * g] *= sx * s.x, z[4 * g + 1] *= sx * s.y, z[4 * g + 2] *= sx * s.z, z[4 * g + 3] *= sx * s.w;
+    }
+  }
+  if (e.bias) {
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      if (4 * g >= cols) break;
+      const float4 s = __ldg(reinterpret_cast<const float4*>(e.bias + c) + g);
+      z[4 * g] += s.x, z[4 * g + 1] += s.y, z[4 * g + 2] += s.z, z[4 * g + 3] += s.w;
+    }
+  }
+}
+template <int ACT>
+__device__ __forceinline__ void each32(float (&z)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) z[i] = act_of(z[i], ACT);
+}
+__device__ __forceinline__ void act32(int act, float (&z)[32]) {
+  if (act == SC_ACT_SILU) each32<SC_ACT_SILU>(z);
+  else if (act == SC_ACT_GELU) each32<SC_ACT_GELU>(z);
+  else if (act == SC_ACT_RELU) each32<SC_ACT_RELU>(z);
+}
+__device__ __forceinline__ void st_shared(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ void decode(const GemmParams& p, int u, int* mt, int* nt, int* k0, int* k1, int* split) {
   const int tiles = p.m_tiles * p.n_tiles;
@@ -53,15 +99,17 @@ __device__ __forceinline__ void decode(const GemmParams& p, int u, int* mt, int*
   *k1 = min(p.kb, *k0 + p.kb_per);
 }
 
-template <int CTAS, bool E4M3, bool A_MN, bool B_MN, bool COLUMNS>
+template <int CTAS, bool E4M3, bool A_MN, bool B_MN, bool COLUMNS, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const GemmParams p) {
+    k_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+           const __grid_constant__ OutMaps om, const __grid_constant__ GemmParams p) {
   constexpr bool PAIR = CTAS == 2;
   constexpr uint32_t kA = 128 * 128;         // bytes of A a stage and block
   constexpr int kBlock = E4M3 ? 128 : 64;    // values of k a stage
   constexpr uint32_t kPanel = 64 * 128;      // MN-major: 64 values of k of 64 vectors
   extern __shared__ uint8_t s_raw[];
   __shared__ uint64_t s_bar[2 * kMaxStages + 5];
+  __shared__ uint64_t s_res[kEpiWarps];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort_word;
   volatile int* s_abort = &s_abort_word;
@@ -82,6 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(acce + 8 * i, kEpiWarps * CTAS);
     }
     mbar_init(done, 1);
+    for (int i = 0; i < kEpiWarps; ++i) mbar_init(smem_u32(s_res + i), 1);
     fence_mbar_init();
   }
   if (warp == kEpiWarps + 1) {
@@ -194,9 +243,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ results
-    const int q = warp & 3, half = warp >> 2;
+    // Sixteen warps, four to each quarter of TMEM's lanes: the activation's instructions
+    // are what few warps would be slow at.
+    const int q = warp & 3, part = warp >> 2;
     const uint32_t acce_at = PAIR ? map_to_rank(acce, 0) : acce;
     int j = 0;
+    // The rows' form: a warp's 32 rows leave through a tile of shared memory by TMA, as
+    // lines of 128 bytes; the residual comes in the same way, into the tile that its sum
+    // leaves from, and ahead of its turn unless `pre` needs the tile first.
+    const uint32_t tile = base + p.stages * stage + warp * kTile;
+    const uint32_t res_bar = smem_u32(s_res + warp);
+    uint32_t res_ph = 0;
+    bool ahead = false;
+    const bool has_res = p.ep.res != nullptr, has_pre = p.ep.pre != nullptr;
+    auto load_res = [&](int mt, int nt, int c) {
+      mbar_arrive_expect_tx(res_bar, kTile);
+      tma_load_2d(tile, &om.res, nt * p.bn + c, (mt * CTAS + static_cast<int>(rank)) * 128 + q * 32, res_bar);
+    };
     for (int u = first; u < p.units; u += stride, ++j) {
       int mt, nt, k0, k1, split;
       decode(p, u, &mt, &nt, &k0, &k1, &split);
@@ -206,14 +269,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const int64_t i = static_cast<int64_t>(mt * CTAS + static_cast<int>(rank)) * 128 + q * 32 + lane;
+      const int64_t i0 = static_cast<int64_t>(mt * CTAS + static_cast<int>(rank)) * 128 + q * 32, i = i0 + lane;
       const uint32_t trow = tmem + static_cast<uint32_t>(b * p.bn) + (static_cast<uint32_t>(q * 32) << 16);
       const int64_t n0 = static_cast<int64_t>(nt) * p.bn;
       if constexpr (COLUMNS) {
         const bool in = i < p.m;
         const bool last = p.splits == 1;
         const float bias = in && last && p.ep.bias ? p.ep.bias[i] : 0.f, sw = in && last && p.ep.sw ? p.ep.sw[i] : 1.f;
-        for (int c = half * 16; c < p.bn; c += 32) {
+        for (int c = part * 16; c < p.bn; c += 64) {
           float v[16];
           __syncwarp();
           tmem_ld16(trow + static_cast<uint32_t>(c), v);
@@ -222,36 +285,109 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < 16; ++t) {
               const int64_t r = n0 + c + t;
               if (r < p.n) {
-                if (last) finish1(p.ep, r, i, v[t], sw, bias);
+                if (last) finish1<BF16>(p.ep, r, i, v[t], sw, bias);
                 else p.part[(split * p.n + r) * p.m + i] = v[t];
               }
             }
           }
         }
-      } else {
-        for (int c = half * 32; c < p.bn; c += 64) {
-          float v[32];
-          __syncwarp();
-          tmem_ld32(trow + static_cast<uint32_t>(c), v);
-          if (i < p.m) {
+      } else if (p.splits > 1) {
+        if (i0 < p.m) {
+          for (int c = part * 32; c < p.bn && n0 + c < p.n; c += 128) {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+            float v[32];
+            tmem_ld32(trow + static_cast<uint32_t>(c), v);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const int64_t col = n0 + c + g * 8;
-              if (col < p.n) {
-                float z[8];
-#pragma unroll
-                for (int t = 0; t < 8; ++t) z[t] = v[g * 8 + t];
-                if (p.splits == 1) {
-                  finish8(p.ep, i, col, z);
-                } else {
-                  float4* dst = reinterpret_cast<float4*>(p.part + (split * p.m + i) * p.n + col);
-                  dst[0] = make_float4(z[0], z[1], z[2], z[3]);
-                  dst[1] = make_float4(z[4], z[5], z[6], z[7]);
-                }
-              }
+            for (int g = 0; g < 8; ++g)
+              st_shared(tile + lane * 128 + ((g ^ (lane & 7)) << 4),
+                        make_uint4(__float_as_uint(v[4 * g]), __float_as_uint(v[4 * g + 1]),
+                                   __float_as_uint(v[4 * g + 2]), __float_as_uint(v[4 * g + 3])));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&om.part, static_cast<int>(n0) + c, static_cast<int>(i0), split, tile);
+              bulk_commit();
             }
           }
         }
+      } else if (i0 < p.m) {
+        const float sx = p.ep.sw && i < p.m ? p.ep.sx[i] : 1.f;
+        bool gone = false;
+        for (int c = part * 64; c < p.bn && n0 + c < p.n; c += 256) {
+          if (has_pre) {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int64_t col = n0 + c + h * 32;
+              float z[32];
+              tmem_ld32(trow + static_cast<uint32_t>(c + h * 32), z);
+              scale32(p.ep, sx, col, static_cast<int>(p.n - col), z);
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                st_shared(tile + lane * 128 + (((h * 4 + g) ^ (lane & 7)) << 4), pack8(z + 8 * g, BF16));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&om.pre, static_cast<int>(n0) + c, static_cast<int>(i0), tile);
+              bulk_commit();
+            }
+          }
+          if (lane == 0 && !ahead) {
+            bulk_wait_read<0>();
+            if (has_res) load_res(mt, nt, c);
+          }
+          __syncwarp();
+          if (has_res) {
+            if (!__all_sync(0xffffffffu, mbar_wait(res_bar, res_ph, s_abort))) {
+              *s_abort = 1;
+              gone = true;
+              break;
+            }
+            res_ph ^= 1u;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t col = n0 + c + h * 32;
+            float z[32];
+            tmem_ld32(trow + static_cast<uint32_t>(c + h * 32), z);
+            scale32(p.ep, sx, col, static_cast<int>(p.n - col), z);
+            act32(p.ep.act, z);
+            if (has_res) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                float r[8];
+                unpack8(ld_shared(tile + lane * 128 + (((h * 4 + g) ^ (lane & 7)) << 4)), BF16, r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[8 * g + e] += r[e];
+              }
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              st_shared(tile + lane * 128 + (((h * 4 + g) ^ (lane & 7)) << 4), pack8(z + 8 * g, BF16));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          // this warp's next tile is its next unit's (a unit has at most one)
+          ahead = has_res && !has_pre && u + stride < p.units;
+          if (lane == 0) {
+            tma_store_2d(&om.out, static_cast<int>(n0) + c, static_cast<int>(i0), tile);
+            bulk_commit();
+          }
+          if (ahead) {
+            int mt2, nt2, x, y, z;
+            decode(p, u + stride, &mt2, &nt2, &x, &y, &z);
+            ahead = static_cast<int64_t>(nt2) * p.bn + part * 64 < p.n &&
+                    static_cast<int64_t>(mt2 * CTAS + static_cast<int>(rank)) * 128 + q * 32 < p.m;
+            if (ahead && lane == 0) {
+              bulk_wait_read<0>();
+              load_res(mt2, nt2, part * 64);
+            }
+          }
+        }
+        if (gone) break;
       }
       __syncwarp();
       tc_fence_before();
@@ -263,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if (warp < kEpiWarps && lane == 0) bulk_wait_all();
   __syncwarp();
   tc_fence_before();
   if (PAIR) cluster_sync_all();
@@ -275,23 +412,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && *s_abort) atomicOr(&g_product_status, kDevErrTimeout);
 }
 
-// Adds the runs' sums in order and finishes them, eight columns a thread.
-__global__ void __launch_bounds__(256) k_gemm_join(const float* __restrict__ part, int splits, int64_t rows, int64_t cols,
-                                                   const Epilogue ep) {
+// Adds the runs' sums and finishes them, eight columns a thread and eight threads for them: each
+// adds every eighth run in order, and the first adds the eight.
+constexpr int kJoinWays = 8;
+__global__ void __launch_bounds__(32 * kJoinWays) k_gemm_join(const float* __restrict__ part, int splits, int64_t rows,
+                                                              int64_t cols, const Epilogue ep) {
+  __shared__ float s_z[kJoinWays - 1][8][33];
   grid_release();
   grid_wait();
   const int64_t per_row = cols >> 3, total = rows * per_row;
-  for (int64_t t = blockIdx.x * 256ll + threadIdx.x; t < total; t += gridDim.x * 256ll) {
-    const int64_t r = t / per_row, c = (t - r * per_row) * 8;
+  for (int64_t t0 = blockIdx.x * 32ll; t0 < total; t0 += gridDim.x * 32ll) {
+    const int64_t t = t0 + threadIdx.x, r = t / per_row, c = (t - r * per_row) * 8;
     float z[8] = {};
+    if (t < total) {
 #pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const float4* src = reinterpret_cast<const float4*>(part + (s * rows + r) * cols + c);
-      const float4 a = src[0], b = src[1];
-      z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w;
-      z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
+      for (int s = threadIdx.y; s < splits; s += kJoinWays) {
+        const float4* src = reinterpret_cast<const float4*>(part + (s * rows + r) * cols + c);
+        const float4 a = src[0], b = src[1];
+        z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w;
+        z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
+      }
     }
-    finish8(ep, r, c, z);
+    if (threadIdx.y > 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s_z[threadIdx.y - 1][i][threadIdx.x] = z[i];
+    }
+    __syncthreads();
+    if (threadIdx.y == 0 && t < total) {
+#pragma unroll
+      for (int w = 0; w < kJoinWays - 1; ++w)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] += s_z[w][i][threadIdx.x];
+      finish8(ep, r, c, z);
+    }
+    __syncthreads();
   }
 }
 
@@ -350,6 +504,23 @@ Plan plan_columns(const Product& p, int kb) {
   return best;
 }
 
+// A map of output rows in tiles of 32 rows of 128 bytes; `parts` of them one after the other.
+sc_status make_out_map(CUtensorMap* map, const void* data, int64_t ld, int64_t rows, int64_t cols, int eb, int parts) {
+  const EncodeTiledFn encode = tensor_map_encoder();
+  if (!encode) return set_error(SC_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(parts)};
+  const cuuint64_t row = static_cast<cuuint64_t>((rows > 1 ? ld : (cols + 7) / 8 * 8) * eb);
+  const cuuint64_t strides[2] = {row, row * static_cast<cuuint64_t>(rows)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / eb), 32, 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = encode(map, eb == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                            parts ? 3 : 2, const_cast<void*>(data), dims, strides, box, one,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SC_OK : set_error(SC_ERR_CUDA, "tensor map of an output");
+}
+
 sc_status make_map(CUtensorMap* map, const Operand& o, int64_t vectors, int64_t k, bool e4m3, int box_vectors) {
   const EncodeTiledFn encode = tensor_map_encoder();
   if (!encode) return set_error(SC_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
@@ -366,8 +537,9 @@ sc_status make_map(CUtensorMap* map, const Operand& o, int64_t vectors, int64_t 
   return r == CUDA_SUCCESS ? SC_OK : set_error(SC_ERR_CUDA, "tensor map of an operand");
 }
 
+template <bool BF16>
 const void* kernel_of(const Product& p, int ctas) {
-#define SC_K(...) reinterpret_cast<const void*>(k_gemm<__VA_ARGS__>)
+#define SC_K(...) reinterpret_cast<const void*>(k_gemm<__VA_ARGS__, BF16>)
   if (p.columns) {
     if (p.e4m3) return SC_K(1, true, false, false, true);
     return p.a.mn ? SC_K(1, false, true, false, true) : SC_K(1, false, false, false, true);
@@ -401,7 +573,8 @@ sc_status product_run(const Product& p, cudaStream_t s) {
   g.tmem_cols = 32;
   while (g.tmem_cols < 2 * pl.bn) g.tmem_cols *= 2;
   const uint32_t stage = 128 * 128 + g.b_bytes;
-  g.stages = static_cast<int>(kSmemMost / stage);
+  const uint32_t staging = p.columns ? 0 : kStaging;
+  g.stages = static_cast<int>((kSmemMost - 1024 - staging) / stage);
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   const int M = 128 * pl.ctas;
   g.idesc = p.e4m3 ? make_idesc_e4m3(M, pl.bn)
@@ -411,12 +584,26 @@ sc_status product_run(const Product& p, cudaStream_t s) {
   sc_status st = make_map(&ta, p.a, p.m, p.k, p.e4m3, 128);
   if (!st) st = make_map(&tb, p.b, p.n, p.k, p.e4m3, pl.bn / pl.ctas);
   if (st) return st;
-  const void* kern = kernel_of(p, pl.ctas);
-  const size_t smem = 1024 + static_cast<size_t>(g.stages) * stage;
+  const void* kern = p.ep.bf16 ? kernel_of<true>(p, pl.ctas) : kernel_of<false>(p, pl.ctas);
+  const size_t smem = 1024 + static_cast<size_t>(g.stages) * stage + staging;
   if ((st = kernel_setup(kern, smem, nullptr))) return st;
   if (pl.splits > 1) {
     st = dev_alloc(reinterpret_cast<void**>(&g.part), sizeof(float) * static_cast<size_t>(pl.splits) * p.m * p.n, s);
     if (st) return st;
+  }
+  OutMaps om{};
+  if (!p.columns) {
+    if (pl.splits > 1) {
+      st = make_out_map(&om.part, g.part, p.n, p.m, p.n, 4, pl.splits);
+    } else {
+      st = make_out_map(&om.out, p.ep.out, p.ep.ldo, p.m, p.n, 2, 0);
+      if (!st && p.ep.pre) st = make_out_map(&om.pre, p.ep.pre, p.ep.ldp, p.m, p.n, 2, 0);
+      if (!st && p.ep.res) st = make_out_map(&om.res, p.ep.res, p.ep.ldr, p.m, p.n, 2, 0);
+    }
+    if (st) {
+      dev_free(g.part, s);
+      return st;
+    }
   }
   const int slots = device_sm_count() / pl.ctas;
   cudaLaunchAttribute at[2];
@@ -433,18 +620,21 @@ sc_status product_run(const Product& p, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  void* args[] = {&ta, &tb, &g};
+  void* args[] = {&ta, &tb, &om, &g};
   cudaError_t e;
   SC_LAUNCH("linear_gemm", s, e = cudaLaunchKernelExC(&cfg, kern, args));
   if (e == cudaSuccess && pl.splits > 1) {
     int64_t rows = p.columns ? p.n : p.m, cols = p.columns ? p.m : p.n;
-    int64_t blocks = (rows * (cols / 8) + 255) / 256;
+    int64_t blocks = (rows * (cols / 8) + 31) / 32;
     if (blocks > device_sm_count() * 8) blocks = device_sm_count() * 8;
     int splits = pl.splits;
     Epilogue ep = p.ep;
     void* jargs[] = {&g.part, &splits, &rows, &cols, &ep};
-    SC_LAUNCH("linear_join", s, e = launch_after(reinterpret_cast<const void*>(k_gemm_join),
-                                                 static_cast<unsigned>(blocks), 256, 0, s, jargs));
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(32, kJoinWays);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    SC_LAUNCH("linear_join", s, e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(k_gemm_join), jargs));
   }
   dev_free(g.part, s);
   return e == cudaSuccess ? SC_OK : set_cuda_error(e, "matrix product launch");

@@ -60,7 +60,7 @@ __device__ __forceinline__ void unpack8(const uint4& u, bool bf16, float (&f)[8]
     f[2 * i + 1] = t.y;
   }
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8], bool bf16) {
+__device__ __forceinline__ uint4 pack8(const float* f, bool bf16) {
   return make_uint4(pack16(f[0], f[1], bf16), pack16(f[2], f[3], bf16), pack16(f[4], f[5], bf16),
                     pack16(f[6], f[7], bf16));
 }
@@ -101,13 +101,14 @@ __device__ __forceinline__ void finish8(const Epilogue& e, int64_t r, int64_t c,
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + r * e.ldo + c) = pack8(z, e.bf16);
 }
 // One value, for the form whose lanes hold columns.
+template <bool BF16>
 __device__ __forceinline__ void finish1(const Epilogue& e, int64_t r, int64_t c, float z, float sw, float bias) {
   if (e.sw) z *= e.sx[r] * sw;
   z += bias;
-  if (e.pre) store16(e.pre, r * e.ldp + c, z, e.bf16);
-  z = act_of(z, e.act);
-  if (e.res) z += load16(e.res, r * e.ldr + c, e.bf16);
-  store16(e.out, r * e.ldo + c, z, e.bf16);
+  if (e.pre) store16(e.pre, r * e.ldp + c, z, BF16);
+  if (e.act) z = act_of(z, e.act);
+  if (e.res) z += load16(e.res, r * e.ldr + c, BF16);
+  store16(e.out, r * e.ldo + c, z, BF16);
 }
 
 }  // namespace

@@ -171,7 +171,7 @@ sc_status sc_linear_fwd(const sc_rows* x, const void* d_W, const float* d_scale_
   const int ei = e4m3 ? 1 : 2;
   Span sx, sr, so, sp;
   if ((st = take_in("x", x, rows, c_in, ei, true, &a.x, &sx))) return st;
-  if (res && (st = take_in("res", res, rows, c_out, 2, false, &a.res, &sr))) return st;
+  if (res && (st = take_in("res", res, rows, c_out, 2, true, &a.res, &sr))) return st;
   if ((st = take_out("out", out, rows, c_out, 2, &a.out, &so))) return st;
   if (pre && (st = take_out("pre", pre, rows, c_out, 2, &a.pre, &sp))) return st;
   if ((st = check_dev_ptr(d_W, 16, "W"))) return st;
