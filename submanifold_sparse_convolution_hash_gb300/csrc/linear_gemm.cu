@@ -29,8 +29,8 @@ constexpr int kEpiWarps = 16;
 constexpr int kThreads = (kEpiWarps + 2) * 32;
 constexpr int kMaxStages = 12;
 constexpr int kSmemMost = 230400;                  // of 232,448, with the barriers and the alignment
-constexpr uint32_t kTile = 32 * 128;              // 32 rows of 128 bytes on their way out
-constexpr uint32_t kStaging = kEpiWarps * kTile;
+constexpr uint32_t kTile = 32 * 64;               // 32 rows of 32 16-bit columns on their way out
+constexpr uint32_t kStaging = kEpiWarps * 2 * kTile;
 constexpr int kGroup = 8;  // tile rows whose tiles are neighbours in time: they share B's columns in L2
 
 struct GemmParams {
@@ -43,8 +43,8 @@ struct GemmParams {
   Epilogue ep;
 };
 
-// Maps of what the rows' form writes and reads past the products: tiles of 64 16-bit
-// columns (the sums: 32) and 32 rows.
+// Maps of what the rows' form writes and reads past the products: tiles of 32 rows and 32
+// columns.
 struct OutMaps {
   CUtensorMap out, pre, res, part;
 };
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kPanel = 64 * 128;      // MN-major: 64 values of k of 64 vectors
   extern __shared__ uint8_t s_raw[];
   __shared__ uint64_t s_bar[2 * kMaxStages + 5];
-  __shared__ uint64_t s_res[kEpiWarps];
+  __shared__ uint64_t s_res[kEpiWarps * 2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort_word;
   volatile int* s_abort = &s_abort_word;
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(acce + 8 * i, kEpiWarps * CTAS);
     }
     mbar_init(done, 1);
-    for (int i = 0; i < kEpiWarps; ++i) mbar_init(smem_u32(s_res + i), 1);
+    for (int i = 0; i < kEpiWarps * 2; ++i) mbar_init(smem_u32(s_res + i), 1);
     fence_mbar_init();
   }
   if (warp == kEpiWarps + 1) {
@@ -248,17 +248,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, part = warp >> 2;
     const uint32_t acce_at = PAIR ? map_to_rank(acce, 0) : acce;
     int j = 0;
-    // The rows' form: a warp's 32 rows leave through a tile of shared memory by TMA, as
-    // lines of 128 bytes; the residual comes in the same way, into the tile that its sum
-    // leaves from, and ahead of its turn unless `pre` needs the tile first.
-    const uint32_t tile = base + p.stages * stage + warp * kTile;
-    const uint32_t res_bar = smem_u32(s_res + warp);
-    uint32_t res_ph = 0;
+    // The rows' form: a warp's 32 rows leave 32 columns at a time through two tiles of
+    // shared memory by TMA, one for `out` and one for `pre`, or by turns.  The residual
+    // comes in the same way, into the tile that its sum leaves from, and where tiles take
+    // turns ahead of its own.
+    const uint32_t tiles = base + p.stages * stage + warp * 2 * kTile;
+    const uint32_t res_bar = smem_u32(s_res + warp * 2);
+    uint32_t res_ph = 0;  // a bit for each tile
+    int turn = 0;
     bool ahead = false;
     const bool has_res = p.ep.res != nullptr, has_pre = p.ep.pre != nullptr;
-    auto load_res = [&](int mt, int nt, int c) {
-      mbar_arrive_expect_tx(res_bar, kTile);
-      tma_load_2d(tile, &om.res, nt * p.bn + c, (mt * CTAS + static_cast<int>(rank)) * 128 + q * 32, res_bar);
+    const uint32_t my_row = lane * 64, my_swz = (lane >> 1) & 3;
+    auto load_res = [&](int mt, int nt, int c, int t) {
+      mbar_arrive_expect_tx(res_bar + 8 * t, kTile);
+      tma_load_2d(tiles + t * kTile, &om.res, nt * p.bn + c, (mt * CTAS + static_cast<int>(rank)) * 128 + q * 32,
+                  res_bar + 8 * t);
     };
     for (int u = first; u < p.units; u += stride, ++j) {
       int mt, nt, k0, k1, split;
@@ -300,13 +304,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(trow + static_cast<uint32_t>(c), v);
 #pragma unroll
             for (int g = 0; g < 8; ++g)
-              st_shared(tile + lane * 128 + ((g ^ (lane & 7)) << 4),
+              st_shared(tiles + lane * 128 + ((g ^ (lane & 7)) << 4),
                         make_uint4(__float_as_uint(v[4 * g]), __float_as_uint(v[4 * g + 1]),
                                    __float_as_uint(v[4 * g + 2]), __float_as_uint(v[4 * g + 3])));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_3d(&om.part, static_cast<int>(n0) + c, static_cast<int>(i0), split, tile);
+              tma_store_3d(&om.part, static_cast<int>(n0) + c, static_cast<int>(i0), split, tiles);
               bulk_commit();
             }
           }
@@ -314,76 +318,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (i0 < p.m) {
         const float sx = p.ep.sw && i < p.m ? p.ep.sx[i] : 1.f;
         bool gone = false;
-        for (int c = part * 64; c < p.bn && n0 + c < p.n; c += 256) {
+        for (int c = part * 32; c < p.bn && n0 + c < p.n; c += 128) {
+          const int t = has_pre ? 0 : turn;
+          const uint32_t tile = tiles + t * kTile;
+          if (has_res && !ahead && lane == 0) {
+            bulk_wait_read<0>();
+            load_res(mt, nt, c, t);
+          }
+          float z[32];
+          __syncwarp();
+          tmem_ld32(trow + static_cast<uint32_t>(c), z);
+          scale32(p.ep, sx, n0 + c, static_cast<int>(p.n - n0 - c), z);
           if (has_pre) {
+            uint4 w[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) w[g] = pack8(z + 8 * g, BF16);
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int64_t col = n0 + c + h * 32;
-              float z[32];
-              tmem_ld32(trow + static_cast<uint32_t>(c + h * 32), z);
-              scale32(p.ep, sx, col, static_cast<int>(p.n - col), z);
-#pragma unroll
-              for (int g = 0; g < 4; ++g)
-                st_shared(tile + lane * 128 + (((h * 4 + g) ^ (lane & 7)) << 4), pack8(z + 8 * g, BF16));
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&om.pre, static_cast<int>(n0) + c, static_cast<int>(i0), tile);
-              bulk_commit();
-            }
+            for (int g = 0; g < 4; ++g) st_shared(tiles + kTile + my_row + ((g ^ my_swz) << 4), w[g]);
           }
-          if (lane == 0 && !ahead) {
-            bulk_wait_read<0>();
-            if (has_res) load_res(mt, nt, c);
-          }
-          __syncwarp();
+          act32(p.ep.act, z);
           if (has_res) {
-            if (!__all_sync(0xffffffffu, mbar_wait(res_bar, res_ph, s_abort))) {
+            if (!__all_sync(0xffffffffu, mbar_wait(res_bar + 8 * t, (res_ph >> t) & 1, s_abort))) {
               *s_abort = 1;
               gone = true;
               break;
             }
-            res_ph ^= 1u;
-          }
+            res_ph ^= 1u << t;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int64_t col = n0 + c + h * 32;
-            float z[32];
-            tmem_ld32(trow + static_cast<uint32_t>(c + h * 32), z);
-            scale32(p.ep, sx, col, static_cast<int>(p.n - col), z);
-            act32(p.ep.act, z);
-            if (has_res) {
+            for (int g = 0; g < 4; ++g) {
+              float r[8];
+              unpack8(ld_shared(tile + my_row + ((g ^ my_swz) << 4)), BF16, r);
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                float r[8];
-                unpack8(ld_shared(tile + lane * 128 + (((h * 4 + g) ^ (lane & 7)) << 4)), BF16, r);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) z[8 * g + e] += r[e];
-              }
+              for (int e = 0; e < 8; ++e) z[8 * g + e] += r[e];
             }
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-              st_shared(tile + lane * 128 + (((h * 4 + g) ^ (lane & 7)) << 4), pack8(z + 8 * g, BF16));
+          } else if (!has_pre) {
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
           }
+#pragma unroll
+          for (int g = 0; g < 4; ++g) st_shared(tile + my_row + ((g ^ my_swz) << 4), pack8(z + 8 * g, BF16));
           fence_proxy_async_smem();
           __syncwarp();
-          // this warp's next tile is its next unit's (a unit has at most one)
-          ahead = has_res && !has_pre && u + stride < p.units;
+          turn ^= 1;
           if (lane == 0) {
             tma_store_2d(&om.out, static_cast<int>(n0) + c, static_cast<int>(i0), tile);
+            if (has_pre) tma_store_2d(&om.pre, static_cast<int>(n0) + c, static_cast<int>(i0), tiles + kTile);
             bulk_commit();
           }
+          // the residual of this warp's next tile: of this unit, else of its next one
+          int u2 = u, c2 = c + 128;
+          if (c2 >= p.bn || n0 + c2 >= p.n) u2 = u + stride, c2 = part * 32;
+          ahead = has_res && !has_pre && u2 < p.units;
           if (ahead) {
-            int mt2, nt2, x, y, z;
-            decode(p, u + stride, &mt2, &nt2, &x, &y, &z);
-            ahead = static_cast<int64_t>(nt2) * p.bn + part * 64 < p.n &&
+            int mt2, nt2, x, y, z2;
+            decode(p, u2, &mt2, &nt2, &x, &y, &z2);
+            ahead = static_cast<int64_t>(nt2) * p.bn + c2 < p.n &&
                     static_cast<int64_t>(mt2 * CTAS + static_cast<int>(rank)) * 128 + q * 32 < p.m;
             if (ahead && lane == 0) {
-              bulk_wait_read<0>();
-              load_res(mt2, nt2, part * 64);
+              bulk_wait_read<1>();
+              load_res(mt2, nt2, c2, turn);
             }
           }
         }
@@ -412,40 +407,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && *s_abort) atomicOr(&g_product_status, kDevErrTimeout);
 }
 
-// Adds the runs' sums and finishes them, eight columns a thread and eight threads for them: each
-// adds every eighth run in order, and the first adds the eight.
-constexpr int kJoinWays = 8;
-__global__ void __launch_bounds__(32 * kJoinWays) k_gemm_join(const float* __restrict__ part, int splits, int64_t rows,
-                                                              int64_t cols, const Epilogue ep) {
-  __shared__ float s_z[kJoinWays - 1][8][33];
+// Adds the runs' sums and finishes them, eight columns a thread.  Many runs: WAYS threads for
+// them, each adding every WAYS-th run in order, and the first adds theirs.
+template <int WAYS>
+__global__ void __launch_bounds__(256) k_gemm_join(const float* __restrict__ part, int splits, int64_t rows,
+                                                   int64_t cols, const Epilogue ep) {
+  constexpr int kCols = 256 / WAYS;
+  __shared__ float s_z[WAYS > 1 ? WAYS - 1 : 1][8][kCols + 1];
   grid_release();
   grid_wait();
+  const int tx = threadIdx.x % kCols, ty = threadIdx.x / kCols;
   const int64_t per_row = cols >> 3, total = rows * per_row;
-  for (int64_t t0 = blockIdx.x * 32ll; t0 < total; t0 += gridDim.x * 32ll) {
-    const int64_t t = t0 + threadIdx.x, r = t / per_row, c = (t - r * per_row) * 8;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kCols; t0 < total; t0 += static_cast<int64_t>(gridDim.x) * kCols) {
+    const int64_t t = t0 + tx, r = t / per_row, c = (t - r * per_row) * 8;
     float z[8] = {};
     if (t < total) {
 #pragma unroll 4
-      for (int s = threadIdx.y; s < splits; s += kJoinWays) {
+      for (int s = ty; s < splits; s += WAYS) {
         const float4* src = reinterpret_cast<const float4*>(part + (s * rows + r) * cols + c);
         const float4 a = src[0], b = src[1];
         z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w;
         z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
       }
     }
-    if (threadIdx.y > 0) {
+    if constexpr (WAYS > 1) {
+      if (ty > 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s_z[threadIdx.y - 1][i][threadIdx.x] = z[i];
+        for (int i = 0; i < 8; ++i) s_z[ty - 1][i][tx] = z[i];
+      }
+      __syncthreads();
+      if (ty == 0) {
+#pragma unroll
+        for (int w = 0; w < WAYS - 1; ++w)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] += s_z[w][i][tx];
+      }
     }
-    __syncthreads();
-    if (threadIdx.y == 0 && t < total) {
-#pragma unroll
-      for (int w = 0; w < kJoinWays - 1; ++w)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] += s_z[w][i][threadIdx.x];
-      finish8(ep, r, c, z);
-    }
-    __syncthreads();
+    if (ty == 0 && t < total) finish8(ep, r, c, z);
+    if constexpr (WAYS > 1) __syncthreads();
   }
 }
 
@@ -504,7 +503,7 @@ Plan plan_columns(const Product& p, int kb) {
   return best;
 }
 
-// A map of output rows in tiles of 32 rows of 128 bytes; `parts` of them one after the other.
+// A map of output rows in tiles of 32 rows and columns; `parts` of them one after the other.
 sc_status make_out_map(CUtensorMap* map, const void* data, int64_t ld, int64_t rows, int64_t cols, int eb, int parts) {
   const EncodeTiledFn encode = tensor_map_encoder();
   if (!encode) return set_error(SC_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
@@ -512,12 +511,12 @@ sc_status make_out_map(CUtensorMap* map, const void* data, int64_t ld, int64_t r
                               static_cast<cuuint64_t>(parts)};
   const cuuint64_t row = static_cast<cuuint64_t>((rows > 1 ? ld : (cols + 7) / 8 * 8) * eb);
   const cuuint64_t strides[2] = {row, row * static_cast<cuuint64_t>(rows)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / eb), 32, 1};
+  const cuuint32_t box[3] = {32, 32, 1};
   const cuuint32_t one[3] = {1, 1, 1};
   const CUresult r = encode(map, eb == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
                             parts ? 3 : 2, const_cast<void*>(data), dims, strides, box, one,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, eb == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SC_OK : set_error(SC_ERR_CUDA, "tensor map of an output");
 }
 
@@ -544,10 +543,12 @@ const void* kernel_of(const Product& p, int ctas) {
     if (p.e4m3) return SC_K(1, true, false, false, true);
     return p.a.mn ? SC_K(1, false, true, false, true) : SC_K(1, false, false, false, true);
   }
-  if (p.e4m3) return ctas == 2 ? SC_K(2, true, false, false, false) : SC_K(1, true, false, false, false);
-  if (p.a.mn) return ctas == 2 ? SC_K(2, false, true, true, false) : SC_K(1, false, true, true, false);
-  if (p.b.mn) return ctas == 2 ? SC_K(2, false, false, true, false) : SC_K(1, false, false, true, false);
-  return ctas == 2 ? SC_K(2, false, false, false, false) : SC_K(1, false, false, false, false);
+#define SC_CTAS(...) (ctas == 2 ? SC_K(2, __VA_ARGS__) : SC_K(1, __VA_ARGS__))
+  if (p.e4m3) return SC_CTAS(true, false, false, false);
+  if (p.a.mn) return SC_CTAS(false, true, true, false);
+  if (p.b.mn) return SC_CTAS(false, false, true, false);
+  return SC_CTAS(false, false, false, false);
+#undef SC_CTAS
 #undef SC_K
 }
 
@@ -625,16 +626,19 @@ sc_status product_run(const Product& p, cudaStream_t s) {
   SC_LAUNCH("linear_gemm", s, e = cudaLaunchKernelExC(&cfg, kern, args));
   if (e == cudaSuccess && pl.splits > 1) {
     int64_t rows = p.columns ? p.n : p.m, cols = p.columns ? p.m : p.n;
-    int64_t blocks = (rows * (cols / 8) + 31) / 32;
+    const bool many = pl.splits > 8;
+    const int per = many ? 32 : 256;
+    int64_t blocks = (rows * (cols / 8) + per - 1) / per;
     if (blocks > device_sm_count() * 8) blocks = device_sm_count() * 8;
     int splits = pl.splits;
     Epilogue ep = p.ep;
     void* jargs[] = {&g.part, &splits, &rows, &cols, &ep};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(32, kJoinWays);
+    cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    SC_LAUNCH("linear_join", s, e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(k_gemm_join), jargs));
+    const void* join = many ? reinterpret_cast<const void*>(k_gemm_join<8>) : reinterpret_cast<const void*>(k_gemm_join<1>);
+    SC_LAUNCH("linear_join", s, e = cudaLaunchKernelExC(&cfg, join, jargs));
   }
   dev_free(g.part, s);
   return e == cudaSuccess ? SC_OK : set_cuda_error(e, "matrix product launch");
