@@ -712,10 +712,10 @@ sc_status sc_linear_bwd(const sc_rows* gout, const sc_rows* x, const sc_rows* pr
                         const sc_rows_out* gin, void* d_gW, float* d_gbias, int64_t rows, int c_in, int c_out,
                         sc_act act, sc_dtype dtype, sc_stream stream);
 
-/* Synchronises the stream, returns the status latched by sc_linear_fwd and
- * sc_linear_bwd on the current device since the last check (SC_ERR_TIMEOUT: a
- * bounded device-side wait gave up and outputs are not whole) and clears it. */
-sc_status sc_linear_check(sc_stream stream);
+/* Synchronises the stream, returns the status latched by the calls on rows on
+ * the current device since the last check (SC_ERR_TIMEOUT: a bounded
+ * device-side wait gave up and outputs are not whole) and clears it. */
+sc_status sc_rows_check(sc_stream stream);
 
 /* One gradient: n values at data (device memory, aligned to the type), which
  * go to out (data itself: in place). */

@@ -26,10 +26,10 @@ from .binding import (  # noqa: F401
     sc_kmap_build,
     sc_kmap_build_conv,
     sc_linear_bwd,
-    sc_linear_check,
     sc_linear_fwd,
     sc_qk_norm_rope_bwd,
     sc_qk_norm_rope_fwd,
+    sc_rows_check,
     sc_subm_conv_bwd_data,
     sc_subm_conv_bwd_weight,
     sc_subm_conv_fwd,

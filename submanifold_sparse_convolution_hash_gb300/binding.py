@@ -92,7 +92,7 @@ def lib():
             "sc_add_norm_bwd": ([P] * 6 + [I64, I32, F, I32, P], I32),
             "sc_linear_fwd": ([P] * 8 + [I64, I32, I32, I32, I32, I32, P], I32),
             "sc_linear_bwd": ([P] * 7 + [I64, I32, I32, I32, I32, P], I32),
-            "sc_linear_check": ([P], I32),
+            "sc_rows_check": ([P], I32),
             "sc_grad_clip": ([P, I64, F, P, P], I32),
             "sc_set_allocator": ([P, P, P], I32),
             "sc_status_str": ([I32], ctypes.c_char_p),
@@ -120,7 +120,7 @@ def exported_symbols() -> list:
                         "sc_subm_conv_fwd", "sc_subm_conv_tune", "sc_subm_conv_fwd_noalloc",
                         "sc_subm_conv_bwd_data", "sc_subm_conv_bwd_weight", "sc_qk_norm_rope_fwd",
                         "sc_qk_norm_rope_bwd", "sc_attn_fwd", "sc_attn_bwd", "sc_attn_check", "sc_add_norm_fwd",
-                        "sc_add_norm_bwd", "sc_linear_fwd", "sc_linear_bwd", "sc_linear_check", "sc_grad_clip",
+                        "sc_add_norm_bwd", "sc_linear_fwd", "sc_linear_bwd", "sc_rows_check", "sc_grad_clip",
                         "sc_set_allocator", "sc_status_str", "sc_last_error",
                         "sc_launch_count", "sc_profile_enable", "sc_profile_only", "sc_profile_collect",
                         "sc_profile_reset",
@@ -926,10 +926,10 @@ def sc_linear_bwd(gout, x, W, pre=None, act: str = "none", bias: bool = False, n
     return gin, gw, gb
 
 
-def sc_linear_check(stream=None):
-    """Synchronises and raises what the linear layers on the current device
+def sc_rows_check(stream=None):
+    """Synchronises and raises what the calls on rows on the current device
     latched since the last check (a device-side wait that gave up)."""
-    _check(lib().sc_linear_check(_stream(stream)), "sc_linear_check")
+    _check(lib().sc_rows_check(_stream(stream)), "sc_rows_check")
 
 
 class _Grad(ctypes.Structure):

@@ -9,6 +9,7 @@
 #include <type_traits>
 
 #include "sc_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace sc {
 namespace {
@@ -166,6 +167,8 @@ struct NormParams {
   int64_t rows;
   int channels;
   float eps;
+  int ring;     // wide gradients: rows ahead
+  int* status;
 };
 
 template <int G>
@@ -271,13 +274,12 @@ __global__ void __launch_bounds__(block_size<G>()) k_add_norm(const NormParams p
 // weights' gradient gathers in registers over the rows that a lane's block walks and
 // goes out once a block.
 template <typename T, int NV, int G>
-__global__ void __launch_bounds__(block_size<G>(), G == 0 ? 1 : (NV * sizeof(T) <= 2 ? 3 : 2))
+__global__ void __launch_bounds__(block_size<G>(), NV * sizeof(T) <= 2 ? 3 : 2)
     k_add_norm_bwd(const NormParams p) {
-  __shared__ float2 s_red[2][32];
-  __shared__ float s_gw[G == 0 ? 1 : G * NV * 8];
-  const int lanes = G == 0 ? blockDim.x : G;
+  __shared__ float s_gw[G * NV * 8];
+  constexpr int lanes = G;
   const int lane = threadIdx.x % lanes;
-  const int groups = G == 0 ? 1 : block_size<G>() / (G == 0 ? 1 : G);
+  constexpr int groups = block_size<G>() / G;
   const int nvec = p.channels >> 3;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const T* x = static_cast<const T*>(p.x);
@@ -305,8 +307,7 @@ __global__ void __launch_bounds__(block_size<G>(), G == 0 ? 1 : (NV * sizeof(T) 
   int64_t row = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / lanes;
   constexpr bool kAhead = loads_ahead<T, NV>();
   if (kAhead) load(row);
-  int turn = 0;
-  for (int64_t base = row - (G == 0 ? 0 : (threadIdx.x & 31) / lanes); base < p.rows; base += step, row += step) {
+  for (int64_t base = row - (threadIdx.x & 31) / lanes; base < p.rows; base += step, row += step) {
     if (!kAhead) load(row);
     Vec8<T> cx[NV], cg[NV], cs[NV];
     float ss = 0.f, zh = 0.f;
@@ -326,8 +327,7 @@ __global__ void __launch_bounds__(block_size<G>(), G == 0 ? 1 : (NV * sizeof(T) 
       }
     }
     if (kAhead) load(row + step);
-    row_reduce<G, false>(ss, zh, s_red, turn);
-    turn ^= 1;
+    row_reduce<G, false>(ss, zh, nullptr, 0);
     const float n = static_cast<float>(p.channels);
     const float r = rsqrtf(ss / n + p.eps);
     const float c = zh / n * r * r;
@@ -351,30 +351,130 @@ __global__ void __launch_bounds__(block_size<G>(), G == 0 ? 1 : (NV * sizeof(T) 
   }
   if (!p.part) return;
   float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.channels;
-  if constexpr (G == 0) {
+  // one group after the other, so that the order is fixed
+  const int group = threadIdx.x / lanes;
+  for (int g = 0; g < groups; ++g) {
+    if (g == group) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float* s = s_gw + (v * G + lane) * 8 + i;
+          *s = g == 0 ? gw[v][i] : *s + gw[v][i];
+        }
+    }
+    __syncthreads();
+  }
+  for (int c = threadIdx.x; c < p.channels; c += block_size<G>()) part[c] = s_gw[c];
+}
+
+// The gradients of wide rows, a block a row.  Rows come ahead of their turn into a ring of
+// shared memory by bulk copies, so that what is in flight does not wait for the block's
+// barriers: with loads into registers, one row ahead, 9,973 rows of 2,056 took 51 us (floor 24).
+constexpr int kRing = 3;
+constexpr size_t kRingMost = 200 * 1024;  // a row of 16,384 f32 channels takes 192 KB: one slot
+template <typename T, int NV>
+__global__ void __launch_bounds__(512, NV == 1 && sizeof(T) == 2 ? 2 : 1) k_add_norm_bwd_wide(const NormParams p) {
+  extern __shared__ __align__(16) uint8_t s_rows[];
+  __shared__ float2 s_red[2][32];
+  __shared__ __align__(8) uint64_t s_full[kRing];
+  __shared__ int s_late[2];
+  const int lanes = blockDim.x, lane = threadIdx.x;
+  const int nvec = p.channels >> 3;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.channels) * sizeof(T), slot_bytes = 3 * row_bytes;
+  const uint32_t base = smem_u32(s_rows), full = smem_u32(s_full);
+  const int64_t step = gridDim.x;
+  if (lane == 0) {
+    for (int i = 0; i < kRing; ++i) mbar_init(full + 8 * i, 1);
+    fence_mbar_init();
+    s_late[0] = s_late[1] = 0;
+  }
+  __syncthreads();
+  grid_release();
+  grid_wait();
+  auto load = [&](int64_t r, int slot) {
+    const uint32_t dst = base + slot * slot_bytes, bar = full + 8 * slot;
+    mbar_arrive_expect_tx(bar, p.res ? slot_bytes : 2 * row_bytes);
+    bulk_g2s(dst, static_cast<const T*>(p.x) + r * p.ldx, row_bytes, bar);
+    bulk_g2s(dst + row_bytes, static_cast<const T*>(p.gout) + r * p.ldgout, row_bytes, bar);
+    if (p.res) bulk_g2s(dst + 2 * row_bytes, static_cast<const T*>(p.res) + r * p.ldres, row_bytes, bar);
+  };
+  if (lane == 0) {
+    for (int i = 0; i < p.ring; ++i)
+      if (blockIdx.x + i * step < p.rows) load(blockIdx.x + i * step, i);
+  }
+  const Weights<NV> w(p.w, lane, lanes, nvec);
+  float gw[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gw[v][i] = 0.f;
+  int slot = 0, turn = 0;
+  uint32_t ph = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += step) {
+    if (!mbar_wait_inl(full + 8 * slot, ph)) s_late[turn] = 1;
+    const uint8_t* src = s_rows + slot * slot_bytes;
+    Vec8<T> cx[NV], cg[NV], cs[NV];
+    float ss = 0.f, zh = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = lane + v * lanes;
+      const bool in = at < nvec;
+      cx[v] = in ? ld_vec(reinterpret_cast<const T*>(src) + at * 8) : zero_vec<T>();
+      cg[v] = in ? ld_vec(reinterpret_cast<const T*>(src + row_bytes) + at * 8) : zero_vec<T>();
+      cs[v] = in && p.res ? ld_vec(reinterpret_cast<const T*>(src + 2 * row_bytes) + at * 8) : zero_vec<T>();
+      float h[8], g[8], wv[8];
+      unpack(cx[v], h);
+      unpack(cg[v], g);
+      w.get(v, wv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        ss = fmaf(h[i], h[i], ss);
+        zh = fmaf(g[i] * wv[i], h[i], zh);
+      }
+    }
+    row_reduce<0, false>(ss, zh, s_red, turn);  // with a barrier: the slot has been read
+    if (s_late[turn]) {  // a copy did not land within seconds: the block gives up as one
+      if (lane == 0) {
+        atomicOr(p.status, kDevErrTimeout);
+        for (int i = 0; i < p.ring; ++i) mbar_drain(full + 8 * i, i < slot ? ph ^ 1 : ph);
+      }
+      break;
+    }
+    turn ^= 1;
+    if (lane == 0 && row + p.ring * step < p.rows) {
+      fence_proxy_async_smem();
+      load(row + p.ring * step, slot);
+    }
+    if (++slot == p.ring) slot = 0, ph ^= 1;
+    const float n = static_cast<float>(p.channels);
+    const float r = rsqrtf(ss / n + p.eps);
+    const float c = zh / n * r * r;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int at = lane + v * lanes;
       if (at >= nvec) continue;
+      float h[8], g[8], s[8], wv[8];
+      unpack(cx[v], h);
+      unpack(cg[v], g);
+      unpack(cs[v], s);
+      w.get(v, wv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) part[at * 8 + i] = gw[v][i];
-    }
-  } else {
-    // one group after the other, so that the order is fixed
-    const int group = threadIdx.x / lanes;
-    for (int g = 0; g < groups; ++g) {
-      if (g == group) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float* s = s_gw + (v * G + lane) * 8 + i;
-            *s = g == 0 ? gw[v][i] : *s + gw[v][i];
-          }
+      for (int i = 0; i < 8; ++i) {
+        gw[v][i] = fmaf(g[i], h[i] * r, gw[v][i]);
+        s[i] = fmaf(r, g[i] * wv[i] - c * h[i], s[i]);
       }
-      __syncthreads();
+      st_vec(static_cast<T*>(p.out) + row * p.ldout + at * 8, s);
     }
-    for (int c = threadIdx.x; c < p.channels; c += block_size<G>()) part[c] = s_gw[c];
+  }
+  if (!p.part) return;
+  float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.channels;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int at = lane + v * lanes;
+    if (at >= nvec) continue;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[at * 8 + i] = gw[v][i];
   }
 }
 
@@ -397,10 +497,11 @@ __global__ void __launch_bounds__(1024) k_column_join(const float* __restrict__ 
   if (threadIdx.x == 0 && cc < channels) out[cc] = a;
 }
 
-cudaError_t launch(const char* name, const void* kern, unsigned grid, unsigned block, NormParams& p, cudaStream_t s) {
+cudaError_t launch(const char* name, const void* kern, unsigned grid, unsigned block, size_t smem, NormParams& p,
+                   cudaStream_t s) {
   void* args[] = {&p};
   cudaError_t e;
-  SC_LAUNCH(name, s, e = launch_after(kern, grid, block, 0, s, args));
+  SC_LAUNCH(name, s, e = launch_after(kern, grid, block, smem, s, args));
   return e;
 }
 
@@ -444,9 +545,9 @@ const void* bwd_kernel(const Form& f) {
     case 32 * 8 + 1: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 1, 32>);
     case 32 * 8 + 2: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 2, 32>);
     case 32 * 8 + 4: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 4, 32>);
-    case 1: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 1, 0>);
-    case 2: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 2, 0>);
-    default: return reinterpret_cast<const void*>(k_add_norm_bwd<T, 4, 0>);
+    case 1: return reinterpret_cast<const void*>(k_add_norm_bwd_wide<T, 1>);
+    case 2: return reinterpret_cast<const void*>(k_add_norm_bwd_wide<T, 2>);
+    default: return reinterpret_cast<const void*>(k_add_norm_bwd_wide<T, 4>);
   }
 }
 
@@ -491,7 +592,8 @@ sc_status add_norm_fwd(const NormArgs& a) {
   if (a.dtype == SC_F32) k = a.e4m3 ? fwd_kernel<float, true>(f) : fwd_kernel<float, false>(f);
   else if (a.dtype == SC_F16) k = a.e4m3 ? fwd_kernel<__half, true>(f) : fwd_kernel<__half, false>(f);
   else k = a.e4m3 ? fwd_kernel<__nv_bfloat16, true>(f) : fwd_kernel<__nv_bfloat16, false>(f);
-  const cudaError_t e = launch("add_norm_fwd", k, grid_of(f, a.rows, kernel_residency(k, f.threads)), f.threads, p, a.stream);
+  const cudaError_t e = launch("add_norm_fwd", k, grid_of(f, a.rows, kernel_residency(k, f.threads)), f.threads, 0, p,
+                               a.stream);
   return e == cudaSuccess ? SC_OK : set_cuda_error(e, "norm launch");
 }
 
@@ -513,13 +615,21 @@ sc_status add_norm_bwd(const NormArgs& a) {
   const Form f = form_of(a.channels / 8, a.rows, true);
   const void* k = a.dtype == SC_F32 ? bwd_kernel<float>(f)
                                     : a.dtype == SC_F16 ? bwd_kernel<__half>(f) : bwd_kernel<__nv_bfloat16>(f);
-  const unsigned grid = grid_of(f, a.rows, kernel_residency(k, f.threads));
+  size_t smem = 0;
+  sc_status st;
+  if (!f.g) {
+    const size_t slot = 3 * static_cast<size_t>(a.channels) * (a.dtype == SC_F32 ? 4 : 2);
+    p.ring = slot * kRing <= kRingMost ? kRing : static_cast<int>(kRingMost / slot);
+    smem = p.ring * slot;
+    if ((st = rows_status_word(&p.status)) || (st = kernel_setup(k, smem, nullptr))) return st;
+  }
+  const unsigned grid = grid_of(f, a.rows, kernel_residency(k, f.threads, smem));
   if (a.gw) {
-    const sc_status st = dev_alloc(reinterpret_cast<void**>(&p.part), sizeof(float) * grid * a.channels, a.stream);
+    st = dev_alloc(reinterpret_cast<void**>(&p.part), sizeof(float) * grid * a.channels, a.stream);
     if (st) return st;
   }
-  const cudaError_t e = launch("add_norm_bwd", k, grid, f.threads, p, a.stream);
-  sc_status st = e == cudaSuccess ? SC_OK : set_cuda_error(e, "norm gradient launch");
+  const cudaError_t e = launch("add_norm_bwd", k, grid, f.threads, smem, p, a.stream);
+  st = e == cudaSuccess ? SC_OK : set_cuda_error(e, "norm gradient launch");
   if (!st && a.gw) st = column_join(p.part, static_cast<int>(grid), a.channels, a.gw, a.stream);
   dev_free(p.part, a.stream);
   return st;

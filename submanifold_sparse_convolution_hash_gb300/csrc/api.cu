@@ -197,14 +197,14 @@ sc_status kernel_carveout(const void* kern, int ctas_per_sm, size_t smem) {
   return SC_OK;
 }
 
-int kernel_residency(const void* kern, int threads) {
+int kernel_residency(const void* kern, int threads, size_t smem) {
   static std::mutex mu;
-  static std::map<std::tuple<int, const void*, int>, int> cache;
+  static std::map<std::tuple<int, const void*, int, size_t>, int> cache;
   int dev = 0;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lk(mu);
-  int& n = cache[std::make_tuple(dev, kern, threads)];
-  if (n == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) != cudaSuccess || n < 1)) {
+  int& n = cache[std::make_tuple(dev, kern, threads, smem)];
+  if (n == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess || n < 1)) {
     cudaGetLastError();
     n = 1;
   }

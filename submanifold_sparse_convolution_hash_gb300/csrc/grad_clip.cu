@@ -1,8 +1,8 @@
 // The norm of many gradients together, and their scaling to a largest norm.
 //
 // Two passes over memory are what the mathematics asks for (every output depends on
-// every value); the second walks the chunks backwards, so that it begins with what the
-// first left in L2.  The gradients' addresses travel in the launch's parameters (up to
+// every value); in the second each block walks its run of chunks backwards, so that it begins
+// with what the first left in L2.  The gradients' addresses travel in the launch's parameters (up to
 // 32 KB), so there is no table to upload and a captured graph holds its own copy.
 #include <cmath>
 #include <type_traits>
@@ -62,6 +62,12 @@ __device__ __forceinline__ int64_t chunk_at(const Entry& e, uint32_t c, int* n) 
   const int64_t at = static_cast<int64_t>(c - e.chunk0) * size;
   *n = static_cast<int>(e.n - at < size ? e.n - at : size);
   return at;
+}
+
+// Where block b's run of chunks begins.  Runs, not every so many-th chunk: the search in the table costs
+// a block about as much as a third of a chunk's way from memory.
+__device__ __forceinline__ uint32_t chunk_of(uint32_t chunks, uint32_t b) {
+  return static_cast<uint32_t>(static_cast<uint64_t>(chunks) * b / gridDim.x);
 }
 
 template <typename T>
@@ -188,8 +194,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_squares(const __grid_const
   grid_release();
   grid_wait();
   double sum = 0.0;
-  for (uint32_t c = blockIdx.x; c < t.h.chunks; c += gridDim.x) {
-    const Entry& e = t.e[entry_of(t, c)];
+  const uint32_t c0 = chunk_of(t.h.chunks, blockIdx.x), c1 = chunk_of(t.h.chunks, blockIdx.x + 1);
+  int i = entry_of(t, c0);
+  for (uint32_t c = c0; c < c1; ++c) {
+    while (i + 1 < t.h.count && t.e[i + 1].chunk0 <= c) ++i;
+    const Entry& e = t.e[i];
     int n;
     const int64_t at = chunk_at(e, c, &n);
     if (e.dtype == SC_F32) sum += squares(static_cast<const float*>(e.data) + at, n);
@@ -252,9 +261,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_scale(const __grid_constan
   if (blockIdx.x == 0 && threadIdx.x == 0) *t.h.norm = static_cast<float>(norm);
   const bool cut = isfinite(norm) && norm > static_cast<double>(t.h.max_norm);
   const float by = cut ? static_cast<float>(static_cast<double>(t.h.max_norm) / norm) : 1.f;
-  for (uint32_t i = blockIdx.x; i < t.h.chunks; i += gridDim.x) {
-    const uint32_t c = t.h.chunks - 1 - i;
-    const Entry& e = t.e[entry_of(t, c)];
+  const uint32_t c0 = chunk_of(t.h.chunks, blockIdx.x), c1 = chunk_of(t.h.chunks, blockIdx.x + 1);
+  if (c0 == c1) return;
+  int i = entry_of(t, c1 - 1);
+  for (uint32_t c = c1; c-- > c0;) {
+    while (t.e[i].chunk0 > c) --i;
+    const Entry& e = t.e[i];
     if (!cut && e.out == e.data) continue;
     int n;
     const int64_t at = chunk_at(e, c, &n);

@@ -6,6 +6,7 @@ namespace sc {
 namespace {
 
 constexpr int kLanes = 32, kStreams = 8;
+constexpr int64_t kFewRows = 128;
 
 // gz = gout * act'(pre), in 16 bits, and the columns' sums of the unrounded values:
 // a warp holds 256 columns of a row (eight a lane), a block's eight warps take rows in
@@ -60,6 +61,16 @@ __global__ void __launch_bounds__(kLanes* kStreams, 3)
   part[static_cast<int64_t>(blockIdx.y) * channels + cc] = a;
 }
 
+// rows x columns, by the form that fits the number of rows.
+sc_status run(Product& p, const Operand& rows_op, const Operand& cols_op, int64_t rows, int64_t cols, cudaStream_t s) {
+  const bool few = rows <= kFewRows;
+  p.a = few ? cols_op : rows_op;
+  p.b = few ? rows_op : cols_op;
+  p.m = few ? cols : rows;
+  p.n = few ? rows : cols;
+  return few ? product_few(p, s) : product_rows(p, s);
+}
+
 }  // namespace
 
 sc_status linear_fwd(const LinearArgs& a) {
@@ -69,16 +80,9 @@ sc_status linear_fwd(const LinearArgs& a) {
   p.k = a.c_in;
   const Operand x{a.x.data, a.x.stride, false};
   const Operand w{a.W, p.e4m3 ? a.c_in : a.c_out, !p.e4m3};
-  // Few rows: the weights are A, whose 128-row tiles spread over the card, and the
-  // rows are a narrow B.
-  p.columns = a.rows <= 128;
-  p.a = p.columns ? w : x;
-  p.b = p.columns ? x : w;
-  p.m = p.columns ? a.c_out : a.rows;
-  p.n = p.columns ? a.rows : a.c_out;
   p.ep = {a.out.data, a.pre.data, a.res.data, a.out.stride, a.pre.stride, a.res.stride, a.bias,
           a.scale_x,  a.scale_w,  a.act,      a.dtype == SC_BF16};
-  return product_run(p, a.stream);
+  return run(p, x, w, a.rows, a.c_out, a.stream);
 }
 
 sc_status linear_bwd(const LinearBwdArgs& a) {
@@ -138,18 +142,13 @@ sc_status linear_bwd(const LinearBwdArgs& a) {
     p.b = {gz.data, gz.stride, true};
     p.m = a.c_in, p.n = a.c_out, p.k = a.rows;
     p.ep.out = a.gW, p.ep.ldo = a.c_out, p.ep.bf16 = bf16;
-    st = product_run(p, s);
+    st = product_rows(p, s);
   }
   if (!st && a.gin.data) {  // rows x c_in, summed over c_out
-    const bool few = a.rows <= 128;
-    const Operand g{gz.data, gz.stride, false}, w{a.W, a.c_out, false};
     Product p{};
-    p.columns = few;
-    p.a = few ? w : g;
-    p.b = few ? g : w;
-    p.m = few ? a.c_in : a.rows, p.n = few ? a.rows : a.c_in, p.k = a.c_out;
+    p.k = a.c_out;
     p.ep.out = a.gin.data, p.ep.ldo = a.gin.stride, p.ep.bf16 = bf16;
-    st = product_run(p, s);
+    st = run(p, {gz.data, gz.stride, false}, {a.W, a.c_out, false}, a.rows, a.c_in, s);
   }
   dev_free(part, s);
   dev_free(buf, s);

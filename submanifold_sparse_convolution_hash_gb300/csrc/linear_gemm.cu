@@ -14,6 +14,8 @@
 // Where there are too few tiles for the card, k is cut into runs; each writes fp32
 // sums, which a second kernel adds in order and finishes.
 #include <cmath>
+#include <map>
+#include <mutex>
 
 #include "linear_internal.cuh"
 #include "tc_ptx.cuh"
@@ -22,8 +24,8 @@
 namespace sc {
 namespace {
 
-__device__ int g_product_status;
-__global__ void k_product_take_status(int* taken) { *taken = atomicExch(&g_product_status, 0); }
+__device__ int g_rows_status;
+__global__ void k_rows_take_status(int* taken) { *taken = atomicExch(&g_rows_status, 0); }
 
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = (kEpiWarps + 2) * 32;
@@ -99,7 +101,7 @@ __device__ __forceinline__ void decode(const GemmParams& p, int u, int* mt, int*
   *k1 = min(p.kb, *k0 + p.kb_per);
 }
 
-template <int CTAS, bool E4M3, bool A_MN, bool B_MN, bool COLUMNS, bool BF16>
+template <int CTAS, bool E4M3, bool A_MN, bool B_MN, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     k_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
            const __grid_constant__ OutMaps om, const __grid_constant__ GemmParams p) {
@@ -276,26 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t i0 = static_cast<int64_t>(mt * CTAS + static_cast<int>(rank)) * 128 + q * 32, i = i0 + lane;
       const uint32_t trow = tmem + static_cast<uint32_t>(b * p.bn) + (static_cast<uint32_t>(q * 32) << 16);
       const int64_t n0 = static_cast<int64_t>(nt) * p.bn;
-      if constexpr (COLUMNS) {
-        const bool in = i < p.m;
-        const bool last = p.splits == 1;
-        const float bias = in && last && p.ep.bias ? p.ep.bias[i] : 0.f, sw = in && last && p.ep.sw ? p.ep.sw[i] : 1.f;
-        for (int c = part * 16; c < p.bn; c += 64) {
-          float v[16];
-          __syncwarp();
-          tmem_ld16(trow + static_cast<uint32_t>(c), v);
-          if (in) {
-#pragma unroll
-            for (int t = 0; t < 16; ++t) {
-              const int64_t r = n0 + c + t;
-              if (r < p.n) {
-                if (last) finish1<BF16>(p.ep, r, i, v[t], sw, bias);
-                else p.part[(split * p.n + r) * p.m + i] = v[t];
-              }
-            }
-          }
-        }
-      } else if (p.splits > 1) {
+      if (p.splits > 1) {
         if (i0 < p.m) {
           for (int c = part * 32; c < p.bn && n0 + c < p.n; c += 128) {
             if (lane == 0) bulk_wait_read<0>();
@@ -404,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (PAIR) tmem_dealloc_pair(tmem, static_cast<uint32_t>(p.tmem_cols));
     else tmem_dealloc(tmem, static_cast<uint32_t>(p.tmem_cols));
   }
-  if (threadIdx.x == 0 && *s_abort) atomicOr(&g_product_status, kDevErrTimeout);
+  if (threadIdx.x == 0 && *s_abort) atomicOr(&g_rows_status, kDevErrTimeout);
 }
 
 // Adds the runs' sums and finishes them, eight columns a thread.  Many runs: WAYS threads for
@@ -453,11 +436,14 @@ struct Plan {
   int ctas, bn, splits, kb_per;
 };
 
-// The cheapest by an estimate in SM clocks.  A k block of a tile costs its products
-// (4096 16-bit multiply-adds a clock) or its operands' way into shared memory (about 48
-// bytes a clock and SM), whichever is longer; a unit about 1500 clocks before its first
-// product and after its last, half of which overlap its neighbours'; cut sums are
-// written and read once more (about 16 bytes a clock and SM in each direction).
+// The cheapest by an estimate in SM clocks.  A k block of a tile costs what shared memory takes to
+// be written by TMA and read by the tensor cores, 128 bytes a clock (a pair's blocks read half
+// of B from each other), and not below 560 (measured: 570 to 590 for tiles of 64 and 128
+// columns, 665 for a pair's 256, 813 for one block's 256).  A unit costs that or what its
+// sixteen warps take to finish it, whichever is longer (about 27 clocks a column for one
+// block, 36 for a pair, whose halves wait for each other: 480,000 x 256 -> 512 with silu took
+// 194 us with one block a tile, 250 with a pair).  Cut sums are written and read once more
+// (about 16 bytes a clock and SM in each direction), by one more launch.
 Plan plan_of(const Product& p, int kb) {
   const int sms = device_sm_count();
   Plan best{1, 64, 1, kb};
@@ -466,38 +452,19 @@ Plan plan_of(const Product& p, int kb) {
     const int ctas = form < 2 ? 2 : 1, bn = form == 0 || form == 2 ? 256 : form == 1 || form == 3 ? 128 : 64;
     const int64_t tiles = ((p.m + 128 * ctas - 1) / (128 * ctas)) * ((p.n + bn - 1) / bn);
     const int slots = sms / ctas;
-    const double step = fmax(2.0 * bn, (128.0 * 128 + bn * 128.0 / ctas) / 48.0);
+    const double step = 1.04 * fmax(560.0, 256.0 + bn / ctas + bn);
+    const double finish = 700.0 + bn * (ctas == 2 ? 36.0 : 27.0);
     for (int splits = 1; splits <= kb && splits <= 2 * slots; ++splits) {
       const int per = (kb + splits - 1) / splits;
       if ((kb + per - 1) / per != splits) continue;  // the same cut as a smaller number's
       if (splits > 1 && (tiles * splits > 4 * slots || per < 4)) break;
       const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
-      double cost = waves * (per * step + 700.0) + 800.0;
-      if (splits > 1) cost += 4000.0 + static_cast<double>(p.m) * p.n * 4.0 * splits * 2.0 / (16.0 * sms);
+      double cost = waves * (fmax(per * step, finish) + 300.0) + 0.5 * finish;
+      if (splits > 1) cost += 5000.0 + static_cast<double>(p.m) * p.n * 4.0 * splits * 2.0 / (16.0 * sms);
       if (cost < least) {
         least = cost;
         best = {ctas, bn, splits, per};
       }
-    }
-  }
-  return best;
-}
-// Few rows: the weights stream through once, so k is cut until the card is busy.
-Plan plan_columns(const Product& p, int kb) {
-  const int sms = device_sm_count();
-  Plan best{1, static_cast<int>((p.n + 15) / 16 * 16), 1, kb};
-  const int64_t tiles = (p.m + 127) / 128;
-  double least = 1e300;
-  for (int splits = 1; splits <= kb && splits <= 64; ++splits) {
-    const int per = (kb + splits - 1) / splits;
-    if ((kb + per - 1) / per != splits) continue;
-    const double waves = static_cast<double>((tiles * splits + sms - 1) / sms);
-    double cost = waves * (per * (128.0 * 128 + best.bn * 128) / 24.0 + 700.0);
-    if (splits > 1) cost += 4000.0 + static_cast<double>(p.m) * p.n * 4.0 * splits * 2.0 / (16.0 * sms);
-    if (cost < least) {
-      least = cost;
-      best.splits = splits;
-      best.kb_per = per;
     }
   }
   return best;
@@ -520,7 +487,21 @@ sc_status make_out_map(CUtensorMap* map, const void* data, int64_t ld, int64_t r
   return r == CUDA_SUCCESS ? SC_OK : set_error(SC_ERR_CUDA, "tensor map of an output");
 }
 
-sc_status make_map(CUtensorMap* map, const Operand& o, int64_t vectors, int64_t k, bool e4m3, int box_vectors) {
+template <bool BF16>
+const void* kernel_of(const Product& p, int ctas) {
+#define SC_K(...) reinterpret_cast<const void*>(k_gemm<__VA_ARGS__, BF16>)
+#define SC_CTAS(...) (ctas == 2 ? SC_K(2, __VA_ARGS__) : SC_K(1, __VA_ARGS__))
+  if (p.e4m3) return SC_CTAS(true, false, false);
+  if (p.a.mn) return SC_CTAS(false, true, true);
+  if (p.b.mn) return SC_CTAS(false, false, true);
+  return SC_CTAS(false, false, false);
+#undef SC_CTAS
+#undef SC_K
+}
+
+}  // namespace
+
+sc_status product_map(CUtensorMap* map, const Operand& o, int64_t vectors, int64_t k, bool e4m3, int box_vectors) {
   const EncodeTiledFn encode = tensor_map_encoder();
   if (!encode) return set_error(SC_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   const int eb = e4m3 ? 1 : 2;
@@ -536,28 +517,28 @@ sc_status make_map(CUtensorMap* map, const Operand& o, int64_t vectors, int64_t 
   return r == CUDA_SUCCESS ? SC_OK : set_error(SC_ERR_CUDA, "tensor map of an operand");
 }
 
-template <bool BF16>
-const void* kernel_of(const Product& p, int ctas) {
-#define SC_K(...) reinterpret_cast<const void*>(k_gemm<__VA_ARGS__, BF16>)
-  if (p.columns) {
-    if (p.e4m3) return SC_K(1, true, false, false, true);
-    return p.a.mn ? SC_K(1, false, true, false, true) : SC_K(1, false, false, false, true);
+sc_status rows_status_word(int** word) {
+  static std::mutex mu;
+  static std::map<int, int*> cache;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return set_cuda_error(e, "cudaGetDevice");
+  std::lock_guard<std::mutex> lk(mu);
+  int*& at = cache[dev];
+  if (!at) {
+    void* q = nullptr;
+    e = cudaGetSymbolAddress(&q, g_rows_status);
+    if (e != cudaSuccess) return set_cuda_error(e, "status word");
+    at = static_cast<int*>(q);
   }
-#define SC_CTAS(...) (ctas == 2 ? SC_K(2, __VA_ARGS__) : SC_K(1, __VA_ARGS__))
-  if (p.e4m3) return SC_CTAS(true, false, false, false);
-  if (p.a.mn) return SC_CTAS(false, true, true, false);
-  if (p.b.mn) return SC_CTAS(false, false, true, false);
-  return SC_CTAS(false, false, false, false);
-#undef SC_CTAS
-#undef SC_K
+  *word = at;
+  return SC_OK;
 }
 
-}  // namespace
-
-sc_status product_run(const Product& p, cudaStream_t s) {
+sc_status product_rows(const Product& p, cudaStream_t s) {
   const int block = p.e4m3 ? 128 : 64;
   const int kb = static_cast<int>((p.k + block - 1) / block);
-  const Plan pl = p.columns ? plan_columns(p, kb) : plan_of(p, kb);
+  const Plan pl = plan_of(p, kb);
   GemmParams g{};
   g.m = p.m;
   g.n = p.n;
@@ -574,37 +555,34 @@ sc_status product_run(const Product& p, cudaStream_t s) {
   g.tmem_cols = 32;
   while (g.tmem_cols < 2 * pl.bn) g.tmem_cols *= 2;
   const uint32_t stage = 128 * 128 + g.b_bytes;
-  const uint32_t staging = p.columns ? 0 : kStaging;
-  g.stages = static_cast<int>((kSmemMost - 1024 - staging) / stage);
+  g.stages = static_cast<int>((kSmemMost - 1024 - kStaging) / stage);
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   const int M = 128 * pl.ctas;
   g.idesc = p.e4m3 ? make_idesc_e4m3(M, pl.bn)
                    : make_idesc(p.ep.bf16, M, pl.bn) | (p.a.mn ? 1u << 15 : 0u) | (p.b.mn ? 1u << 16 : 0u);
   g.ep = p.ep;
   CUtensorMap ta, tb;
-  sc_status st = make_map(&ta, p.a, p.m, p.k, p.e4m3, 128);
-  if (!st) st = make_map(&tb, p.b, p.n, p.k, p.e4m3, pl.bn / pl.ctas);
+  sc_status st = product_map(&ta, p.a, p.m, p.k, p.e4m3, 128);
+  if (!st) st = product_map(&tb, p.b, p.n, p.k, p.e4m3, pl.bn / pl.ctas);
   if (st) return st;
   const void* kern = p.ep.bf16 ? kernel_of<true>(p, pl.ctas) : kernel_of<false>(p, pl.ctas);
-  const size_t smem = 1024 + static_cast<size_t>(g.stages) * stage + staging;
+  const size_t smem = 1024 + static_cast<size_t>(g.stages) * stage + kStaging;
   if ((st = kernel_setup(kern, smem, nullptr))) return st;
   if (pl.splits > 1) {
     st = dev_alloc(reinterpret_cast<void**>(&g.part), sizeof(float) * static_cast<size_t>(pl.splits) * p.m * p.n, s);
     if (st) return st;
   }
   OutMaps om{};
-  if (!p.columns) {
-    if (pl.splits > 1) {
-      st = make_out_map(&om.part, g.part, p.n, p.m, p.n, 4, pl.splits);
-    } else {
-      st = make_out_map(&om.out, p.ep.out, p.ep.ldo, p.m, p.n, 2, 0);
-      if (!st && p.ep.pre) st = make_out_map(&om.pre, p.ep.pre, p.ep.ldp, p.m, p.n, 2, 0);
-      if (!st && p.ep.res) st = make_out_map(&om.res, p.ep.res, p.ep.ldr, p.m, p.n, 2, 0);
-    }
-    if (st) {
-      dev_free(g.part, s);
-      return st;
-    }
+  if (pl.splits > 1) {
+    st = make_out_map(&om.part, g.part, p.n, p.m, p.n, 4, pl.splits);
+  } else {
+    st = make_out_map(&om.out, p.ep.out, p.ep.ldo, p.m, p.n, 2, 0);
+    if (!st && p.ep.pre) st = make_out_map(&om.pre, p.ep.pre, p.ep.ldp, p.m, p.n, 2, 0);
+    if (!st && p.ep.res) st = make_out_map(&om.res, p.ep.res, p.ep.ldr, p.m, p.n, 2, 0);
+  }
+  if (st) {
+    dev_free(g.part, s);
+    return st;
   }
   const int slots = device_sm_count() / pl.ctas;
   cudaLaunchAttribute at[2];
@@ -625,7 +603,7 @@ sc_status product_run(const Product& p, cudaStream_t s) {
   cudaError_t e;
   SC_LAUNCH("linear_gemm", s, e = cudaLaunchKernelExC(&cfg, kern, args));
   if (e == cudaSuccess && pl.splits > 1) {
-    int64_t rows = p.columns ? p.n : p.m, cols = p.columns ? p.m : p.n;
+    int64_t rows = p.m, cols = p.n;
     const bool many = pl.splits > 8;
     const int per = many ? 32 : 256;
     int64_t blocks = (rows * (cols / 8) + per - 1) / per;
@@ -644,16 +622,16 @@ sc_status product_run(const Product& p, cudaStream_t s) {
   return e == cudaSuccess ? SC_OK : set_cuda_error(e, "matrix product launch");
 }
 
-sc_status product_take_status(cudaStream_t s, int* bits) {
+sc_status rows_take_status(cudaStream_t s, int* bits) {
   void* d = nullptr;
   sc_status st = dev_alloc(&d, sizeof(int), s);
   if (st) return st;
-  SC_LAUNCH("linear_take_status", s, (k_product_take_status<<<1, 1, 0, s>>>(static_cast<int*>(d))));
+  SC_LAUNCH("rows_take_status", s, (k_rows_take_status<<<1, 1, 0, s>>>(static_cast<int*>(d))));
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) e = cudaMemcpyAsync(bits, d, sizeof(int), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   dev_free(d, s);
-  return e == cudaSuccess ? SC_OK : set_cuda_error(e, "product status");
+  return e == cudaSuccess ? SC_OK : set_cuda_error(e, "rows status");
 }
 
 }  // namespace sc

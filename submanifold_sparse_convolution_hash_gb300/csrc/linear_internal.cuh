@@ -2,6 +2,8 @@
 // parameters, activations and their slopes.
 #pragma once
 
+#include <cuda.h>
+
 #include "sc_internal.cuh"
 
 namespace sc {
@@ -141,15 +143,35 @@ __device__ __forceinline__ void finish8(const Epilogue& e, int64_t r, int64_t c,
   }
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + r * e.ldo + c) = pack8(z, e.bf16);
 }
-// One value, for the form whose lanes hold columns.
-template <bool BF16>
-__device__ __forceinline__ void finish1(const Epilogue& e, int64_t r, int64_t c, float z, float sw, float bias) {
-  if (e.sw) z *= e.sx[r] * sw;
-  z += bias;
-  if (e.pre) store16(e.pre, r * e.ldp + c, z, BF16);
-  if (e.act) z = act_of(z, e.act);
-  if (e.res) z += load16(e.res, r * e.ldr + c, BF16);
-  store16(e.out, r * e.ldo + c, z, BF16);
+// N rows r, r + step, ... of one column, of which `count` exist: for the form whose lanes hold columns.
+template <bool BF16, int N>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, int64_t r, int step, int count, int64_t c,
+                                            float (&z)[N], float sw, float bias) {
+  if (e.sw) {
+#pragma unroll
+    for (int t = 0; t < N; ++t) z[t] *= e.sx[r + min(t, count - 1) * step] * sw;
+  }
+#pragma unroll
+  for (int t = 0; t < N; ++t) z[t] += bias;
+  if (e.pre) {
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+      if (t < count) store16(e.pre, (r + t * step) * e.ldp + c, z[t], BF16);
+  }
+  if (e.act) {
+#pragma unroll
+    for (int t = 0; t < N; ++t) z[t] = act_of(z[t], e.act);
+  }
+  if (e.res) {
+    float v[N];
+#pragma unroll
+    for (int t = 0; t < N; ++t) v[t] = load16(e.res, (r + min(t, count - 1) * step) * e.ldr + c, BF16);
+#pragma unroll
+    for (int t = 0; t < N; ++t) z[t] += v[t];
+  }
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+    if (t < count) store16(e.out, (r + t * step) * e.ldo + c, z[t], BF16);
 }
 
 }  // namespace
@@ -165,12 +187,13 @@ struct Operand {
 struct Product {
   Operand a, b;
   int64_t m, n, k;
-  bool e4m3;    // both operands, K-major (else 16 bits: bf16 as in the epilogue)
-  bool columns; // D's rows are the output's columns (few rows: A holds the weights)
+  bool e4m3;  // both operands, K-major (else 16 bits: bf16 as in the epilogue)
   Epilogue ep;
 };
-sc_status product_run(const Product& p, cudaStream_t s);
-// Reads and clears the status bits the products' kernels latched; synchronises.
-sc_status product_take_status(cudaStream_t s, int* bits);
-
+// D's rows are the output's (linear_gemm.cu).
+sc_status product_rows(const Product& p, cudaStream_t s);
+// D's rows are the output's columns: A holds the weights, B, K-major, few rows (linear_few.cu).
+sc_status product_few(const Product& p, cudaStream_t s);
+// A tensor map of an operand in boxes of 128 bytes by `box_vectors` (K-major) or 64 values of k.
+sc_status product_map(CUtensorMap* map, const Operand& o, int64_t vectors, int64_t k, bool e4m3, int box_vectors);
 }  // namespace sc

@@ -230,9 +230,9 @@ sc_status sc_linear_bwd(const sc_rows* gout, const sc_rows* x, const sc_rows* pr
   return linear_bwd(a);
 }
 
-sc_status sc_linear_check(sc_stream stream) {
+sc_status sc_rows_check(sc_stream stream) {
   int bits = 0;
-  const sc_status st = product_take_status(reinterpret_cast<cudaStream_t>(stream), &bits);
+  const sc_status st = rows_take_status(reinterpret_cast<cudaStream_t>(stream), &bits);
   return st ? st : status_from_bits(bits);
 }
 

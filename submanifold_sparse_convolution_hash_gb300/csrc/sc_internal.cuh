@@ -155,9 +155,9 @@ sc_status kernel_setup(const void* kern, size_t smem, int* num_regs);
 // holds the neighbour-index loads); cached, so set only when it changes.
 sc_status kernel_carveout(const void* kern, int ctas_per_sm, size_t smem);
 
-// Blocks of `threads` threads (and no dynamic shared memory) of a kernel that an
-// SM holds, at least 1; cached per device and kernel.
-int kernel_residency(const void* kern, int threads);
+// Blocks of `threads` threads and `smem` bytes of dynamic shared memory (beyond
+// 48 KB: after kernel_setup) of a kernel that an SM holds, at least 1; cached.
+int kernel_residency(const void* kern, int threads, size_t smem = 0);
 
 // Launches a kernel that may begin while the one before it on the stream still
 // runs (programmatic dependent launch): it calls grid_wait() before it touches
@@ -301,6 +301,11 @@ struct LinearBwdArgs {
   cudaStream_t stream;
 };
 sc_status linear_bwd(const LinearBwdArgs& a);
+
+// Where on the current device the kernels on rows latch their status.
+sc_status rows_status_word(int** word);
+// Reads and clears it; synchronises.
+sc_status rows_take_status(cudaStream_t s, int* bits);
 
 sc_status grad_clip(const sc_grad* grads, int64_t count, float max_norm, float* d_norm, cudaStream_t s);
 

@@ -250,6 +250,9 @@ LINEAR = [
     (100, 512, 136, "bf16", "gelu", True, True, False, 0),
     (128, 64, 2048, "f16", "silu", True, False, False, 0),
     (129, 64, 64, "f16", "silu", True, False, True, 0),
+    (255, 576, 264, "bf16", "gelu", True, True, True, 0),
+    (256, 4096, 1024, "f16", "none", False, True, False, 0),
+    (257, 1024, 1024, "bf16", "silu", True, True, True, 0),
     (200, 8, 16, "bf16", "none", True, True, True, 0),
     (300, 1000, 8, "f16", "relu", True, True, False, 8),
     (1000, 256, 256, "bf16", "gelu", True, True, True, 0),
@@ -296,7 +299,7 @@ def test_linear_forward(rows, c_in, c_out, dtype, act, bias, residual, pre, room
     linear_check(out, z, x.double(), W.double(), b, res, act, dtype, c_in)
     again = sc.sc_linear_fwd(x, W, bias=b, act=act, res=res)
     assert torch.equal(out, again)
-    sc.sc_linear_check()
+    sc.sc_rows_check()
 
 
 @pytest.mark.parametrize("rows,c_in,c_out,dtype,act,bias,residual,pre,room",
@@ -316,7 +319,7 @@ def test_linear_in_8_bits(rows, c_in, c_out, dtype, act, bias, residual, pre, ro
     wd = (wq.double() * sw.double()[:, None]).t()
     # the scales' product adds two roundings
     linear_check(out, z, xd, wd, b, res, act, dtype, c_in + 64)
-    sc.sc_linear_check()
+    sc.sc_rows_check()
 
 
 LINEAR_GRAD = [c[:6] + (c[8],) for c in LINEAR] + [
@@ -358,7 +361,7 @@ def test_linear_gradients(rows, c_in, c_out, dtype, act, bias, room):
     assert part[0] is None and part[2] is None and torch.equal(part[1], gw)
     part = sc.sc_linear_bwd(gout, x, W, pre=pre, act=act, bias=True, need_gin=True, need_gW=False)
     assert part[1] is None and torch.equal(part[0], gin)
-    sc.sc_linear_check()
+    sc.sc_rows_check()
 
 
 def test_linear_without_rows():
@@ -577,7 +580,7 @@ def test_another_stream_and_a_captured_graph():
     for _, held in graphs:
         for a, r in zip(held, ref):
             assert torch.equal(a, r)
-    sc.sc_linear_check()
+    sc.sc_rows_check()
 
 
 def test_caller_allocator():
