@@ -3,7 +3,7 @@
 //
 // One pass over memory: a row's values stay in the registers of the lanes (up to
 // 1024 channels: at most a warp a row) or of the block that hold it, its sums cross
-// them once, and the next row's loads are issued before this row's sums.  y is a
+// them once, and the next rows' loads are issued before this row's sums.  y is a
 // positive factor r = 1 / sqrt(mean h^2 + eps) times w h, so the largest |y| of the
 // 8-bit form is r max |w h| and rides along with the sum of squares.
 #include <type_traits>
@@ -15,6 +15,9 @@ namespace sc {
 namespace {
 
 constexpr float kE4m3Max = 448.f;
+// Rows ahead of a wide form's, each with its two or three tensors.
+constexpr int kRing = 3;
+constexpr size_t kRingMost = 200 * 1024;  // a gradient's row of 16,384 f32 channels takes 192 KB: one slot
 
 template <typename T>
 struct Vec8 {
@@ -171,18 +174,56 @@ struct NormParams {
   int* status;
 };
 
-template <int G>
-constexpr int block_size() {
-  return G == 0 ? 512 : 256;
+// The rest of a row once its sums are there: the sum, and y in the output's type.
+template <typename T, int NV, bool E4M3>
+__device__ __forceinline__ void store_row(const NormParams& p, const Weights<NV>& w, const float (&h)[NV][8], float ss,
+                                          float top, int64_t row, int lane, int lanes, int nvec) {
+  if (p.sum) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = lane + v * lanes;
+      if (at < nvec) st_vec(static_cast<T*>(p.sum) + row * p.ldsum + at * 8, h[v]);
+    }
+  }
+      const float r = p.w ? rsqrtf(ss / static_cast<float>(p.channels) + p.eps) : 1.f;
+      if constexpr (E4M3) {
+        float s = top * r / kE4m3Max;
+        if (s < 0x1p-126f) s = 0.f;
+        const float f = s > 0.f ? 1.f / s : 0.f;
+        if (lane == 0) p.scale[row] = s;
+  #pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int at = lane + v * lanes;
+          if (at >= nvec) continue;
+          float y[8];
+          w.get(v, y);
+  #pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] *= h[v][i] * r * f;
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * p.ldout + at * 8) =
+              make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16), e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
+        }
+      } else {
+  #pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int at = lane + v * lanes;
+          if (at >= nvec) continue;
+          float y[8];
+          w.get(v, y);
+  #pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] *= h[v][i] * r;
+          st_vec(static_cast<T*>(p.out) + row * p.ldout + at * 8, y);
+        }
+      }
 }
 
-// A row is held by G lanes (or the block, G = 0), vectors of 8 values lane, lane + G, ...
+constexpr int kBlock = 256;  // of the forms in which lanes hold a row
+
+// A row is held by G lanes, vectors of 8 values lane, lane + G, ...
 template <typename T, int NV, int G, bool E4M3>
-__global__ void __launch_bounds__(block_size<G>()) k_add_norm(const NormParams p) {
-  __shared__ float2 s_red[2][32];
-  const int lanes = G == 0 ? blockDim.x : G;
+__global__ void __launch_bounds__(kBlock) k_add_norm(const NormParams p) {
+  constexpr int lanes = G;
   const int lane = threadIdx.x % lanes;
-  const int groups = G == 0 ? 1 : block_size<G>() / (G == 0 ? 1 : G);
+  constexpr int groups = kBlock / G;
   const int nvec = p.channels >> 3;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const T* x = static_cast<const T*>(p.x);
@@ -203,9 +244,8 @@ __global__ void __launch_bounds__(block_size<G>()) k_add_norm(const NormParams p
   int64_t row = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / lanes;
   constexpr bool kAhead = loads_ahead<T, NV>();
   if (kAhead) load(row);
-  int turn = 0;
   // the warp's subgroups stay together (their shuffles name the whole warp)
-  for (int64_t base = row - (G == 0 ? 0 : (threadIdx.x & 31) / lanes); base < p.rows; base += step, row += step) {
+  for (int64_t base = row - (threadIdx.x & 31) / lanes; base < p.rows; base += step, row += step) {
     if (!kAhead) load(row);
     float h[NV][8];
     float ss = 0.f, top = 0.f;
@@ -227,45 +267,8 @@ __global__ void __launch_bounds__(block_size<G>()) k_add_norm(const NormParams p
       }
     }
     if (kAhead) load(row + step);
-    if (p.sum && row < p.rows) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int at = lane + v * lanes;
-        if (at < nvec) st_vec(static_cast<T*>(p.sum) + row * p.ldsum + at * 8, h[v]);
-      }
-    }
-    row_reduce<G, true>(ss, top, s_red, turn);
-    turn ^= 1;
-    const float r = p.w ? rsqrtf(ss / static_cast<float>(p.channels) + p.eps) : 1.f;
-    if (row >= p.rows) continue;
-    if constexpr (E4M3) {
-      float s = top * r / kE4m3Max;
-      if (s < 0x1p-126f) s = 0.f;
-      const float f = s > 0.f ? 1.f / s : 0.f;
-      if (lane == 0) p.scale[row] = s;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int at = lane + v * lanes;
-        if (at >= nvec) continue;
-        float y[8];
-        w.get(v, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] *= h[v][i] * r * f;
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * p.ldout + at * 8) =
-            make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16), e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int at = lane + v * lanes;
-        if (at >= nvec) continue;
-        float y[8];
-        w.get(v, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] *= h[v][i] * r;
-        st_vec(static_cast<T*>(p.out) + row * p.ldout + at * 8, y);
-      }
-    }
+    row_reduce<G, true>(ss, top, nullptr, 0);
+    if (row < p.rows) store_row<T, NV, E4M3>(p, w, h, ss, top, row, lane, lanes, nvec);
   }
 }
 
@@ -274,12 +277,12 @@ __global__ void __launch_bounds__(block_size<G>()) k_add_norm(const NormParams p
 // weights' gradient gathers in registers over the rows that a lane's block walks and
 // goes out once a block.
 template <typename T, int NV, int G>
-__global__ void __launch_bounds__(block_size<G>(), NV * sizeof(T) <= 2 ? 3 : 2)
+__global__ void __launch_bounds__(kBlock, NV * sizeof(T) <= 2 ? 3 : 2)
     k_add_norm_bwd(const NormParams p) {
   __shared__ float s_gw[G * NV * 8];
   constexpr int lanes = G;
   const int lane = threadIdx.x % lanes;
-  constexpr int groups = block_size<G>() / G;
+  constexpr int groups = kBlock / G;
   const int nvec = p.channels >> 3;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const T* x = static_cast<const T*>(p.x);
@@ -365,14 +368,12 @@ __global__ void __launch_bounds__(block_size<G>(), NV * sizeof(T) <= 2 ? 3 : 2)
     }
     __syncthreads();
   }
-  for (int c = threadIdx.x; c < p.channels; c += block_size<G>()) part[c] = s_gw[c];
+  for (int c = threadIdx.x; c < p.channels; c += kBlock) part[c] = s_gw[c];
 }
 
 // The gradients of wide rows, a block a row.  Rows come ahead of their turn into a ring of
 // shared memory by bulk copies, so that what is in flight does not wait for the block's
 // barriers: with loads into registers, one row ahead, 9,973 rows of 2,056 took 51 us (floor 24).
-constexpr int kRing = 3;
-constexpr size_t kRingMost = 200 * 1024;  // a row of 16,384 f32 channels takes 192 KB: one slot
 template <typename T, int NV>
 __global__ void __launch_bounds__(512, NV == 1 && sizeof(T) == 2 ? 2 : 1) k_add_norm_bwd_wide(const NormParams p) {
   extern __shared__ __align__(16) uint8_t s_rows[];
@@ -478,6 +479,82 @@ __global__ void __launch_bounds__(512, NV == 1 && sizeof(T) == 2 ? 2 : 1) k_add_
   }
 }
 
+// The forward of wide rows, a block a row, with the same ring.  (With loads into registers it
+// hung on how many the compiler took: 32,768 rows of 4,096 to 8 bits 140 us at three blocks
+// an SM, 157 at two.)
+template <typename T, int NV, bool E4M3>
+__global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) k_add_norm_wide(const NormParams p) {
+  extern __shared__ __align__(16) uint8_t s_rows[];
+  __shared__ float2 s_red[2][32];
+  __shared__ __align__(8) uint64_t s_full[kRing];
+  __shared__ int s_late[2];
+  const int lanes = blockDim.x, lane = threadIdx.x;
+  const int nvec = p.channels >> 3;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.channels) * sizeof(T), slot_bytes = 2 * row_bytes;
+  const uint32_t base = smem_u32(s_rows), full = smem_u32(s_full);
+  const int64_t step = gridDim.x;
+  if (lane == 0) {
+    for (int i = 0; i < kRing; ++i) mbar_init(full + 8 * i, 1);
+    fence_mbar_init();
+    s_late[0] = s_late[1] = 0;
+  }
+  __syncthreads();
+  grid_release();
+  grid_wait();
+  auto load = [&](int64_t r, int slot) {
+    const uint32_t dst = base + slot * slot_bytes, bar = full + 8 * slot;
+    mbar_arrive_expect_tx(bar, p.res ? slot_bytes : row_bytes);
+    bulk_g2s(dst, static_cast<const T*>(p.x) + r * p.ldx, row_bytes, bar);
+    if (p.res) bulk_g2s(dst + row_bytes, static_cast<const T*>(p.res) + r * p.ldres, row_bytes, bar);
+  };
+  if (lane == 0) {
+    for (int i = 0; i < p.ring; ++i)
+      if (blockIdx.x + i * step < p.rows) load(blockIdx.x + i * step, i);
+  }
+  const Weights<NV> w(p.w, lane, lanes, nvec);
+  int slot = 0, turn = 0;
+  uint32_t ph = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += step) {
+    if (!mbar_wait_inl(full + 8 * slot, ph)) s_late[turn] = 1;
+    const uint8_t* src = s_rows + slot * slot_bytes;
+    float h[NV][8];
+    float ss = 0.f, top = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = lane + v * lanes;
+      unpack(at < nvec ? ld_vec(reinterpret_cast<const T*>(src) + at * 8) : zero_vec<T>(), h[v]);
+      float t[8];
+      if (p.res) {
+        unpack(at < nvec ? ld_vec(reinterpret_cast<const T*>(src + row_bytes) + at * 8) : zero_vec<T>(), t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[v][i] += t[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(h[v][i], h[v][i], ss);
+      if constexpr (E4M3) {
+        w.get(v, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(h[v][i] * t[i]));
+      }
+    }
+    row_reduce<0, true>(ss, top, s_red, turn);  // with a barrier: the slot has been read
+    if (s_late[turn]) {  // a copy did not land within seconds: the block gives up as one
+      if (lane == 0) {
+        atomicOr(p.status, kDevErrTimeout);
+        for (int i = 0; i < p.ring; ++i) mbar_drain(full + 8 * i, i < slot ? ph ^ 1 : ph);
+      }
+      break;
+    }
+    turn ^= 1;
+    if (lane == 0 && row + p.ring * step < p.rows) {
+      fence_proxy_async_smem();
+      load(row + p.ring * step, slot);
+    }
+    if (++slot == p.ring) slot = 0, ph ^= 1;
+    store_row<T, NV, E4M3>(p, w, h, ss, top, row, lane, lanes, nvec);
+  }
+}
+
 // The blocks' partial sums, 32 columns and 32 runs of blocks a thread block.
 __global__ void __launch_bounds__(1024) k_column_join(const float* __restrict__ part, int blocks, int channels,
                                                       float* __restrict__ out) {
@@ -509,15 +586,14 @@ cudaError_t launch(const char* name, const void* kern, unsigned grid, unsigned b
 struct Form {
   int nv, g, threads;
 };
-Form form_of(int nvec, int64_t rows, bool bwd) {
+Form form_of(int nvec, int64_t rows) {
   if (nvec <= 4) return {1, 4, 256};
   if (nvec <= 8) return {1, 8, 256};
   if (nvec <= 16) return {1, 16, 256};
   if (nvec <= 32) return {1, 32, 256};
   if (rows > 2048 && nvec <= 64) return {2, 32, 256};
   if (rows > 2048 && nvec <= 128) return {4, 32, 256};
-  // few rows: a thread holds as little as it can, and the row's latency is short
-  int nv = nvec <= 512 && (rows <= 2048 || bwd) ? 1 : nvec <= 1024 ? 2 : 4;
+  const int nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
   const int t = (nvec + nv - 1) / nv;
   return {nv, 0, (t + 31) / 32 * 32};
 }
@@ -531,9 +607,9 @@ const void* fwd_kernel(const Form& f) {
     case 32 * 8 + 1: return reinterpret_cast<const void*>(k_add_norm<T, 1, 32, E4M3>);
     case 32 * 8 + 2: return reinterpret_cast<const void*>(k_add_norm<T, 2, 32, E4M3>);
     case 32 * 8 + 4: return reinterpret_cast<const void*>(k_add_norm<T, 4, 32, E4M3>);
-    case 1: return reinterpret_cast<const void*>(k_add_norm<T, 1, 0, E4M3>);
-    case 2: return reinterpret_cast<const void*>(k_add_norm<T, 2, 0, E4M3>);
-    default: return reinterpret_cast<const void*>(k_add_norm<T, 4, 0, E4M3>);
+    case 1: return reinterpret_cast<const void*>(k_add_norm_wide<T, 1, E4M3>);
+    case 2: return reinterpret_cast<const void*>(k_add_norm_wide<T, 2, E4M3>);
+    default: return reinterpret_cast<const void*>(k_add_norm_wide<T, 4, E4M3>);
   }
 }
 template <typename T>
@@ -549,6 +625,16 @@ const void* bwd_kernel(const Form& f) {
     case 2: return reinterpret_cast<const void*>(k_add_norm_bwd_wide<T, 2>);
     default: return reinterpret_cast<const void*>(k_add_norm_bwd_wide<T, 4>);
   }
+}
+
+// The ring of a wide form whose rows have so many tensors: its depth and shared memory.
+sc_status ring_setup(const Form& f, const void* kern, int tensors, const NormArgs& a, NormParams* p, size_t* smem) {
+  if (f.g) return SC_OK;
+  const size_t slot = static_cast<size_t>(tensors) * a.channels * (a.dtype == SC_F32 ? 4 : 2);
+  p->ring = slot * kRing <= kRingMost ? kRing : static_cast<int>(kRingMost / slot);
+  *smem = p->ring * slot;
+  const sc_status st = rows_status_word(&p->status);
+  return st ? st : kernel_setup(kern, *smem, nullptr);
 }
 
 unsigned grid_of(const Form& f, int64_t rows, int per_sm) {
@@ -587,13 +673,16 @@ sc_status add_norm_fwd(const NormArgs& a) {
   p.rows = a.rows;
   p.channels = a.channels;
   p.eps = a.eps;
-  const Form f = form_of(a.channels / 8, a.rows, false);
+  const Form f = form_of(a.channels / 8, a.rows);
   const void* k;
   if (a.dtype == SC_F32) k = a.e4m3 ? fwd_kernel<float, true>(f) : fwd_kernel<float, false>(f);
   else if (a.dtype == SC_F16) k = a.e4m3 ? fwd_kernel<__half, true>(f) : fwd_kernel<__half, false>(f);
   else k = a.e4m3 ? fwd_kernel<__nv_bfloat16, true>(f) : fwd_kernel<__nv_bfloat16, false>(f);
-  const cudaError_t e = launch("add_norm_fwd", k, grid_of(f, a.rows, kernel_residency(k, f.threads)), f.threads, 0, p,
-                               a.stream);
+  size_t smem = 0;
+  const sc_status st = ring_setup(f, k, 2, a, &p, &smem);
+  if (st) return st;
+  const cudaError_t e = launch("add_norm_fwd", k, grid_of(f, a.rows, kernel_residency(k, f.threads, smem)), f.threads,
+                               smem, p, a.stream);
   return e == cudaSuccess ? SC_OK : set_cuda_error(e, "norm launch");
 }
 
@@ -612,17 +701,12 @@ sc_status add_norm_bwd(const NormArgs& a) {
   p.rows = a.rows;
   p.channels = a.channels;
   p.eps = a.eps;
-  const Form f = form_of(a.channels / 8, a.rows, true);
+  const Form f = form_of(a.channels / 8, a.rows);
   const void* k = a.dtype == SC_F32 ? bwd_kernel<float>(f)
                                     : a.dtype == SC_F16 ? bwd_kernel<__half>(f) : bwd_kernel<__nv_bfloat16>(f);
   size_t smem = 0;
-  sc_status st;
-  if (!f.g) {
-    const size_t slot = 3 * static_cast<size_t>(a.channels) * (a.dtype == SC_F32 ? 4 : 2);
-    p.ring = slot * kRing <= kRingMost ? kRing : static_cast<int>(kRingMost / slot);
-    smem = p.ring * slot;
-    if ((st = rows_status_word(&p.status)) || (st = kernel_setup(k, smem, nullptr))) return st;
-  }
+  sc_status st = ring_setup(f, k, 3, a, &p, &smem);
+  if (st) return st;
   const unsigned grid = grid_of(f, a.rows, kernel_residency(k, f.threads, smem));
   if (a.gw) {
     st = dev_alloc(reinterpret_cast<void**>(&p.part), sizeof(float) * grid * a.channels, a.stream);

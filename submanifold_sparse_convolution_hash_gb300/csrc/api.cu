@@ -160,7 +160,7 @@ sc_status kernel_setup(const void* kern, size_t smem, int* num_regs) {
     it = cache.emplace(std::make_pair(dev, kern), en).first;
   }
   if (smem > it->second.smem) {
-    if (smem > 48 * 1024) {
+    if (smem > 40 * 1024) {  // a kernel's static share counts towards the 48 KB that need no asking
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       if (e != cudaSuccess) return set_cuda_error(e, "kernel shared-memory attribute");
     }

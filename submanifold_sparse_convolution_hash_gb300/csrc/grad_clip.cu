@@ -56,14 +56,21 @@ __device__ __forceinline__ int entry_of(const Table<MAX>& t, uint32_t c) {
 __host__ __device__ __forceinline__ int chunk_values(uint32_t dtype) {
   return dtype == SC_F32 ? kChunkBytes / 4 : kChunkBytes / 2;
 }
-// The first value of chunk c of its gradient, and how many it has.
-__device__ __forceinline__ int64_t chunk_at(const Entry& e, uint32_t c, int* n) {
-  const int size = chunk_values(e.dtype);
-  const int64_t at = static_cast<int64_t>(c - e.chunk0) * size;
-  *n = static_cast<int>(e.n - at < size ? e.n - at : size);
+// How far a gradient's first value lies behind the 128-byte line that it is on, in values.
+// Chunks are cut from that line on, so that all but the first and the last are whole lines:
+// cut from the values themselves, 500M 16-bit ones a value off a line took 15 % longer.
+__host__ __device__ __forceinline__ int line_shift(const void* p, uint32_t dtype) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 127) / (dtype == SC_F32 ? 4 : 2));
+}
+// Chunk c of its gradient: the value its line begins at (of the first chunk it may lie before
+// the gradient), and the values [*lo, *hi) from there that it has.
+__device__ __forceinline__ int64_t chunk_at(const Entry& e, uint32_t c, int* lo, int* hi) {
+  const int size = chunk_values(e.dtype), shift = line_shift(e.data, e.dtype);
+  const int64_t at = static_cast<int64_t>(c - e.chunk0) * size - shift;
+  *lo = at < 0 ? shift : 0;
+  *hi = static_cast<int>(e.n - at < size ? e.n - at : size);
   return at;
 }
-
 // Where block b's run of chunks begins.  Runs, not every so many-th chunk: the search in the table costs
 // a block about as much as a third of a chunk's way from memory.
 __device__ __forceinline__ uint32_t chunk_of(uint32_t chunks, uint32_t b) {
@@ -118,40 +125,44 @@ __device__ __forceinline__ void unpack16(const uint4& u, float (&f)[16 / sizeof(
   }
 }
 
-// A chunk is a head of values up to the first 16-byte boundary, whole vectors, and a
-// tail: where each begins.
+// A chunk's whole 16-byte vectors [v0, v1), and the values before and after them.
 template <typename T>
 struct Span16 {
-  int head, vecs, tail;
-  __device__ __forceinline__ Span16(const T* p, int n) {
+  int v0, v1, head, tail;  // head values from lo on, tail values from v1's place on
+  __device__ __forceinline__ Span16(int lo, int hi) {
     constexpr int V = 16 / sizeof(T);
-    head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / static_cast<int>(sizeof(T));
-    if (head > n) head = n;
-    vecs = (n - head) / V;
-    tail = n - head - vecs * V;
+    v0 = (lo + V - 1) / V;
+    v1 = hi / V;
+    if (v0 > v1) {  // within one vector
+      v0 = v1;
+      head = hi - lo;
+      tail = 0;
+    } else {
+      head = v0 * V - lo;
+      tail = hi - v1 * V;
+    }
   }
 };
 
 // This thread's share of a chunk's sum of squares.  In fp32 over its 65 values or fewer;
 // where that leaves fp32's range at either end, again in 64 bits.
 template <typename T>
-__device__ __forceinline__ double squares(const T* p, int n) {
+__device__ __forceinline__ double squares(const T* p, int lo, int hi) {
   constexpr int V = 16 / sizeof(T);
   constexpr int L = kVecs;
-  const Span16<T> sp(p, n);
-  const uint4* body = reinterpret_cast<const uint4*>(p + sp.head);
+  const Span16<T> sp(lo, hi);
+  const uint4* body = reinterpret_cast<const uint4*>(p);
   float s[2] = {0.f, 0.f};
   uint32_t any = 0;
   uint4 u[L];
 #pragma unroll
   for (int l = 0; l < L; ++l) {
     const int v = threadIdx.x + l * kThreads;
-    u[l] = v < sp.vecs ? __ldg(body + v) : make_uint4(0, 0, 0, 0);
+    u[l] = v >= sp.v0 && v < sp.v1 ? __ldg(body + v) : make_uint4(0, 0, 0, 0);
   }
   float edge = 0.f;
-  if (static_cast<int>(threadIdx.x) < sp.head) edge = to_f(p[threadIdx.x]);
-  else if (threadIdx.x >= 32 && static_cast<int>(threadIdx.x) - 32 < sp.tail)
-    edge = to_f(p[sp.head + sp.vecs * V + threadIdx.x - 32]);
+  if (static_cast<int>(threadIdx.x) < sp.head) edge = to_f(p[lo + threadIdx.x]);
+  else if (threadIdx.x >= 32 && static_cast<int>(threadIdx.x) - 32 < sp.tail) edge = to_f(p[sp.v1 * V + threadIdx.x - 32]);
 #pragma unroll
   for (int l = 0; l < L; ++l) {
     any |= u[l].x | u[l].y | u[l].z | u[l].w;
@@ -168,10 +179,10 @@ __device__ __forceinline__ double squares(const T* p, int n) {
 #pragma unroll 1
   for (int l = 0; l < L; ++l) {
     const int v = threadIdx.x + l * kThreads;
-    if (v >= sp.vecs) break;
+    if (v < sp.v0 || v >= sp.v1) continue;
     float f[V];
     unpack16<T>(__ldg(body + v), f);
-#pragma unroll 1
+#pragma unroll
     for (int i = 0; i < V; ++i) d += static_cast<double>(f[i]) * f[i];
   }
   return d;
@@ -199,48 +210,48 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_squares(const __grid_const
   for (uint32_t c = c0; c < c1; ++c) {
     while (i + 1 < t.h.count && t.e[i + 1].chunk0 <= c) ++i;
     const Entry& e = t.e[i];
-    int n;
-    const int64_t at = chunk_at(e, c, &n);
-    if (e.dtype == SC_F32) sum += squares(static_cast<const float*>(e.data) + at, n);
-    else if (e.dtype == SC_F16) sum += squares(static_cast<const __half*>(e.data) + at, n);
-    else sum += squares(static_cast<const __nv_bfloat16*>(e.data) + at, n);
+    int lo, hi;
+    const int64_t at = chunk_at(e, c, &lo, &hi);
+    if (e.dtype == SC_F32) sum += squares(static_cast<const float*>(e.data) + at, lo, hi);
+    else if (e.dtype == SC_F16) sum += squares(static_cast<const __half*>(e.data) + at, lo, hi);
+    else sum += squares(static_cast<const __nv_bfloat16*>(e.data) + at, lo, hi);
   }
   sum = block_sum(sum, s_warp);
   if (threadIdx.x == 0) t.h.part[t.h.slot + blockIdx.x] = sum;
 }
 
 template <typename T>
-__device__ __forceinline__ void scale_chunk(const T* p, T* o, int n, float by) {
+__device__ __forceinline__ void scale_chunk(const T* p, T* o, int lo, int hi, float by) {
   constexpr int V = 16 / sizeof(T);
   if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) {  // no common boundary
-    for (int i0 = threadIdx.x; i0 < n; i0 += 8 * kThreads) {
+    for (int i0 = lo + threadIdx.x; i0 < hi; i0 += 8 * kThreads) {
       float f[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = i0 + k * kThreads < n ? to_f(p[i0 + k * kThreads]) : 0.f;
+      for (int k = 0; k < 8; ++k) f[k] = i0 + k * kThreads < hi ? to_f(p[i0 + k * kThreads]) : 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (i0 + k * kThreads < n) o[i0 + k * kThreads] = from_f<T>(f[k] * by);
+        if (i0 + k * kThreads < hi) o[i0 + k * kThreads] = from_f<T>(f[k] * by);
     }
     return;
   }
-  const Span16<T> sp(p, n);
-  const uint4* body = reinterpret_cast<const uint4*>(p + sp.head);
-  uint4* dst = reinterpret_cast<uint4*>(o + sp.head);
+  const Span16<T> sp(lo, hi);
+  const uint4* body = reinterpret_cast<const uint4*>(p);
+  uint4* dst = reinterpret_cast<uint4*>(o);
   if (static_cast<int>(threadIdx.x) < sp.head) {
-    o[threadIdx.x] = from_f<T>(to_f(p[threadIdx.x]) * by);
+    o[lo + threadIdx.x] = from_f<T>(to_f(p[lo + threadIdx.x]) * by);
   } else if (threadIdx.x >= 32 && static_cast<int>(threadIdx.x) - 32 < sp.tail) {
-    const int i = sp.head + sp.vecs * V + threadIdx.x - 32;
+    const int i = sp.v1 * V + threadIdx.x - 32;
     o[i] = from_f<T>(to_f(p[i]) * by);
   }
-  // four loads in flight a thread; more would leave fewer blocks an SM
+  // four loads in flight a thread (eight, or more blocks an SM, measured the same)
 #pragma unroll 1
-  for (int l0 = threadIdx.x; l0 < sp.vecs; l0 += 4 * kThreads) {
+  for (int l0 = sp.v0 + threadIdx.x; l0 < sp.v1; l0 += 4 * kThreads) {
     uint4 u[4];
 #pragma unroll
-    for (int l = 0; l < 4; ++l) u[l] = body[min(l0 + l * kThreads, sp.vecs - 1)];
+    for (int l = 0; l < 4; ++l) u[l] = body[min(l0 + l * kThreads, sp.v1 - 1)];
 #pragma unroll
     for (int l = 0; l < 4; ++l) {
-      if (l0 + l * kThreads >= sp.vecs) continue;
+      if (l0 + l * kThreads >= sp.v1) continue;
       float f[V];
       unpack16<T>(u[l], f);
 #pragma unroll
@@ -268,13 +279,13 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_scale(const __grid_constan
     while (t.e[i].chunk0 > c) --i;
     const Entry& e = t.e[i];
     if (!cut && e.out == e.data) continue;
-    int n;
-    const int64_t at = chunk_at(e, c, &n);
-    if (e.dtype == SC_F32) scale_chunk(static_cast<const float*>(e.data) + at, static_cast<float*>(e.out) + at, n, by);
+    int lo, hi;
+    const int64_t at = chunk_at(e, c, &lo, &hi);
+    if (e.dtype == SC_F32) scale_chunk(static_cast<const float*>(e.data) + at, static_cast<float*>(e.out) + at, lo, hi, by);
     else if (e.dtype == SC_F16)
-      scale_chunk(static_cast<const __half*>(e.data) + at, static_cast<__half*>(e.out) + at, n, by);
+      scale_chunk(static_cast<const __half*>(e.data) + at, static_cast<__half*>(e.out) + at, lo, hi, by);
     else
-      scale_chunk(static_cast<const __nv_bfloat16*>(e.data) + at, static_cast<__nv_bfloat16*>(e.out) + at, n, by);
+      scale_chunk(static_cast<const __nv_bfloat16*>(e.data) + at, static_cast<__nv_bfloat16*>(e.out) + at, lo, hi, by);
   }
 }
 
@@ -292,7 +303,7 @@ void fill(Table<MAX>& t, const sc_grad* grads, int64_t count, int64_t* at) {
   for (; *at < count && t.h.count < MAX; ++*at) {
     const sc_grad& g = grads[*at];
     if (g.n == 0) continue;
-    const uint64_t more = static_cast<uint64_t>((g.n - 1) / chunk_values(g.dtype) + 1);
+    const uint64_t more = static_cast<uint64_t>((g.n - 1 + line_shift(g.data, g.dtype)) / chunk_values(g.dtype) + 1);
     if (chunks + more > 0x7fffffffull) break;
     Entry& e = t.e[t.h.count++];
     e.data = g.data;

@@ -29,8 +29,10 @@ __global__ void __launch_bounds__(kLanes* kStreams, 3)
     for (int k = 0; k < kRows; ++k) {
       const int64_t r = r0 + k * step;
       if (r >= rows) continue;
-      g[k] = *reinterpret_cast<const uint4*>(gout + r * ldg + c);
-      if (ACT) z[k] = *reinterpret_cast<const uint4*>(pre + r * ldp + c);
+      // read once: what is to stay in L2 is gz
+      g[k] = ACT ? __ldcs(reinterpret_cast<const uint4*>(gout + r * ldg + c))
+                 : *reinterpret_cast<const uint4*>(gout + r * ldg + c);
+      if (ACT) z[k] = __ldcs(reinterpret_cast<const uint4*>(pre + r * ldp + c));
     }
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
@@ -136,6 +138,13 @@ sc_status linear_bwd(const LinearBwdArgs& a) {
       if (!st && a.gbias) st = column_join(part, static_cast<int>(runs), a.c_out, a.gbias, s);
     }
   }
+  if (!st && a.gin.data) {  // rows x c_in, summed over c_out
+    Product p{};
+    p.k = a.c_out;
+    p.backwards = act;
+    p.ep.out = a.gin.data, p.ep.ldo = a.gin.stride, p.ep.bf16 = bf16;
+    st = run(p, {gz.data, gz.stride, false}, {a.W, a.c_out, false}, a.rows, a.c_in, s);
+  }
   if (!st && a.gW) {  // c_in x c_out, summed over rows
     Product p{};
     p.a = {a.x.data, a.x.stride, true};
@@ -143,12 +152,6 @@ sc_status linear_bwd(const LinearBwdArgs& a) {
     p.m = a.c_in, p.n = a.c_out, p.k = a.rows;
     p.ep.out = a.gW, p.ep.ldo = a.c_out, p.ep.bf16 = bf16;
     st = product_rows(p, s);
-  }
-  if (!st && a.gin.data) {  // rows x c_in, summed over c_out
-    Product p{};
-    p.k = a.c_out;
-    p.ep.out = a.gin.data, p.ep.ldo = a.gin.stride, p.ep.bf16 = bf16;
-    st = run(p, {gz.data, gz.stride, false}, {a.W, a.c_out, false}, a.rows, a.c_in, s);
   }
   dev_free(part, s);
   dev_free(buf, s);

@@ -34,6 +34,23 @@ __device__ __forceinline__ float ld_cluster(uint32_t at) {
   return v;
 }
 
+// This block's share of the rows (rank, rank + ways, ...), N at a time: the runs' sums in order.
+template <bool BF16, int N>
+__device__ __forceinline__ void join_rows(const FewParams& p, uint32_t base, int rank, int rows, int64_t n0, int64_t col,
+                                          float sw, float bias) {
+#pragma unroll 1
+  for (int t0 = rank; t0 < rows; t0 += N * p.ways) {
+    float z[N] = {};
+#pragma unroll 2
+    for (int w = 0; w < p.ways; ++w) {
+      const uint32_t at = map_to_rank(base + threadIdx.x * 4, static_cast<uint32_t>(w));
+#pragma unroll
+      for (int t = 0; t < N; ++t) z[t] += ld_cluster(at + min(t0 + t * p.ways, rows - 1) * 512);
+    }
+    finish_rows<BF16, N>(p.ep, n0 + t0, p.ways, min(N, (rows - t0 + p.ways - 1) / p.ways), col, z, sw, bias);
+  }
+}
+
 template <bool E4M3, bool A_MN, bool BF16>
 __global__ void __launch_bounds__(kThreads)
     k_gemm_few(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -164,17 +181,11 @@ __global__ void __launch_bounds__(kThreads)
   if (p.ways > 1) {
     cluster_sync_all();
     if (mine) {
-      // eight rows at a time: their loads are in flight together
-      for (int t0 = rank; t0 < rows; t0 += 8 * p.ways) {
-        float z[8] = {};
-#pragma unroll 1
-        for (int w = 0; w < p.ways; ++w) {
-          const uint32_t at = map_to_rank(base + threadIdx.x * 4, static_cast<uint32_t>(w));
-#pragma unroll
-          for (int t = 0; t < 8; ++t) z[t] += ld_cluster(at + min(t0 + t * p.ways, rows - 1) * 512);
-        }
-        finish_rows<BF16, 8>(p.ep, n0 + t0, p.ways, min(8, (rows - t0 + p.ways - 1) / p.ways), col, z, sw, bias);
-      }
+      // up to eight rows at a time: their loads are in flight together
+      const int per = (rows + p.ways - 1) / p.ways;
+      if (per <= 1) join_rows<BF16, 1>(p, base, rank, rows, n0, col, sw, bias);
+      else if (per <= 2) join_rows<BF16, 2>(p, base, rank, rows, n0, col, sw, bias);
+      else join_rows<BF16, 8>(p, base, rank, rows, n0, col, sw, bias);
     }
     __syncwarp();
     cluster_sync_all();

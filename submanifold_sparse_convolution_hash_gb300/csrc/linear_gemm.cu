@@ -39,6 +39,7 @@ struct GemmParams {
   int64_t m, n;
   int m_tiles, n_tiles, units, splits;
   int kb, kb_per;  // k blocks in all, and of a unit
+  bool backwards;  // the last rows first: they are what the kernel before left in L2
   int bn, stages, tmem_cols;
   uint32_t b_bytes, idesc;
   float* part;  // splits > 1: [splits, output rows, output columns]
@@ -91,6 +92,7 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t at) {
 
 __device__ __forceinline__ void decode(const GemmParams& p, int u, int* mt, int* nt, int* k0, int* k1, int* split) {
   const int tiles = p.m_tiles * p.n_tiles;
+  if (p.backwards) u = p.units - 1 - u;
   *split = u / tiles;
   const int t = u - *split * tiles;
   const int per = kGroup * p.n_tiles, g = t / per, r = t - g * per;
@@ -550,6 +552,7 @@ sc_status product_rows(const Product& p, cudaStream_t s) {
   g.units = static_cast<int>(mt * nt * pl.splits);
   g.kb = kb;
   g.kb_per = pl.kb_per;
+  g.backwards = p.backwards;
   g.bn = pl.bn;
   g.b_bytes = static_cast<uint32_t>(pl.bn / pl.ctas) * 128;
   g.tmem_cols = 32;
