@@ -115,15 +115,15 @@ __device__ __forceinline__ void row_reduce(float& a, float& b, float2 (*s_red)[3
 }
 
 // Eight weights of the vector `at`: kept in registers over the rows up to two vectors a
-// lane, else read again for each row (they stay in L1).
+// lane, else read again for each row (they stay in L1).  The narrow gradients read them again
+// too: their registers are worth more (524,288 rows of 256, bf16: 172 us, kept 215).
 __device__ __forceinline__ void ld_w(const float* w, int at, float (&f)[8]) {
   const float4 a = *reinterpret_cast<const float4*>(w + at * 8), b = *reinterpret_cast<const float4*>(w + at * 8 + 4);
   f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
   f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
-template <int NV>
+template <int NV, bool kKept = (NV <= 2)>
 struct Weights {
-  static constexpr bool kKept = NV <= 2;
   float f[kKept ? NV : 1][8];
   const float* w;
   int lane, lanes, nvec;
@@ -218,12 +218,15 @@ __device__ __forceinline__ void store_row(const NormParams& p, const Weights<NV>
 
 constexpr int kBlock = 256;  // of the forms in which lanes hold a row
 
-// A row is held by G lanes, vectors of 8 values lane, lane + G, ...
+// A row is held by G lanes, or by the block (G = 0, at most 256 threads), vectors of 8 values lane,
+// lane + G, ...  Three blocks an SM: 32,768 rows of 4,096 to 8 bits took 140 us so, 157 when three
+// more registers made it two, and 146 to 164 with rows ahead in shared memory.
 template <typename T, int NV, int G, bool E4M3>
-__global__ void __launch_bounds__(kBlock) k_add_norm(const NormParams p) {
-  constexpr int lanes = G;
+__global__ void __launch_bounds__(kBlock, NV * sizeof(T) <= 4 ? 3 : 1) k_add_norm(const NormParams p) {
+  __shared__ float2 s_red[2][32];
+  const int lanes = G ? G : blockDim.x;
   const int lane = threadIdx.x % lanes;
-  constexpr int groups = kBlock / G;
+  constexpr int groups = G ? kBlock / (G ? G : 1) : 1;
   const int nvec = p.channels >> 3;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const T* x = static_cast<const T*>(p.x);
@@ -244,8 +247,9 @@ __global__ void __launch_bounds__(kBlock) k_add_norm(const NormParams p) {
   int64_t row = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / lanes;
   constexpr bool kAhead = loads_ahead<T, NV>();
   if (kAhead) load(row);
+  int turn = 0;
   // the warp's subgroups stay together (their shuffles name the whole warp)
-  for (int64_t base = row - (threadIdx.x & 31) / lanes; base < p.rows; base += step, row += step) {
+  for (int64_t base = row - (G ? (threadIdx.x & 31) / lanes : 0); base < p.rows; base += step, row += step) {
     if (!kAhead) load(row);
     float h[NV][8];
     float ss = 0.f, top = 0.f;
@@ -267,7 +271,8 @@ __global__ void __launch_bounds__(kBlock) k_add_norm(const NormParams p) {
       }
     }
     if (kAhead) load(row + step);
-    row_reduce<G, true>(ss, top, nullptr, 0);
+    row_reduce<G, true>(ss, top, s_red, turn);
+    turn ^= 1;
     if (row < p.rows) store_row<T, NV, E4M3>(p, w, h, ss, top, row, lane, lanes, nvec);
   }
 }
@@ -290,7 +295,7 @@ __global__ void __launch_bounds__(kBlock, NV * sizeof(T) <= 2 ? 3 : 2)
   const T* go = static_cast<const T*>(p.gout);
   grid_release();
   grid_wait();
-  const Weights<NV> w(p.w, lane, lanes, nvec);
+  const Weights<NV, false> w(p.w, lane, lanes, nvec);
   float gw[NV][8];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
@@ -479,9 +484,7 @@ __global__ void __launch_bounds__(512, NV == 1 && sizeof(T) == 2 ? 2 : 1) k_add_
   }
 }
 
-// The forward of wide rows, a block a row, with the same ring.  (With loads into registers it
-// hung on how many the compiler took: 32,768 rows of 4,096 to 8 bits 140 us at three blocks
-// an SM, 157 at two.)
+// The forward of rows that no 256 threads can hold, and of few rows, a block a row, with the same ring.
 template <typename T, int NV, bool E4M3>
 __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) k_add_norm_wide(const NormParams p) {
   extern __shared__ __align__(16) uint8_t s_rows[];
@@ -582,20 +585,23 @@ cudaError_t launch(const char* name, const void* kern, unsigned grid, unsigned b
   return e;
 }
 
-// Which form holds a row of nvec vectors, and its threads.
+// Which form holds a row of nvec vectors: how many a lane, the lanes (0: a block), the block's
+// threads, and whether its rows come through the ring.
 struct Form {
   int nv, g, threads;
+  bool wide;
 };
-Form form_of(int nvec, int64_t rows) {
-  if (nvec <= 4) return {1, 4, 256};
-  if (nvec <= 8) return {1, 8, 256};
-  if (nvec <= 16) return {1, 16, 256};
-  if (nvec <= 32) return {1, 32, 256};
-  if (rows > 2048 && nvec <= 64) return {2, 32, 256};
-  if (rows > 2048 && nvec <= 128) return {4, 32, 256};
-  const int nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
-  const int t = (nvec + nv - 1) / nv;
-  return {nv, 0, (t + 31) / 32 * 32};
+Form form_of(int nvec, int64_t rows, bool bwd) {
+  if (nvec <= 4) return {1, 4, kBlock, false};
+  if (nvec <= 8) return {1, 8, kBlock, false};
+  if (nvec <= 16) return {1, 16, kBlock, false};
+  if (nvec <= 32) return {1, 32, kBlock, false};
+  const bool many = rows > 2048;
+  if (many && nvec <= 64) return {2, 32, kBlock, false};
+  if (many && nvec <= 128) return {4, 32, kBlock, false};
+  const bool regs = !bwd && many && nvec <= 512;
+  const int nv = regs ? (nvec <= 256 ? 1 : 2) : nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
+  return {nv, 0, ((nvec + nv - 1) / nv + 31) / 32 * 32, !regs};
 }
 
 template <typename T, bool E4M3>
@@ -607,8 +613,8 @@ const void* fwd_kernel(const Form& f) {
     case 32 * 8 + 1: return reinterpret_cast<const void*>(k_add_norm<T, 1, 32, E4M3>);
     case 32 * 8 + 2: return reinterpret_cast<const void*>(k_add_norm<T, 2, 32, E4M3>);
     case 32 * 8 + 4: return reinterpret_cast<const void*>(k_add_norm<T, 4, 32, E4M3>);
-    case 1: return reinterpret_cast<const void*>(k_add_norm_wide<T, 1, E4M3>);
-    case 2: return reinterpret_cast<const void*>(k_add_norm_wide<T, 2, E4M3>);
+    case 1: return reinterpret_cast<const void*>(f.wide ? k_add_norm_wide<T, 1, E4M3> : k_add_norm<T, 1, 0, E4M3>);
+    case 2: return reinterpret_cast<const void*>(f.wide ? k_add_norm_wide<T, 2, E4M3> : k_add_norm<T, 2, 0, E4M3>);
     default: return reinterpret_cast<const void*>(k_add_norm_wide<T, 4, E4M3>);
   }
 }
@@ -629,7 +635,7 @@ const void* bwd_kernel(const Form& f) {
 
 // The ring of a wide form whose rows have so many tensors: its depth and shared memory.
 sc_status ring_setup(const Form& f, const void* kern, int tensors, const NormArgs& a, NormParams* p, size_t* smem) {
-  if (f.g) return SC_OK;
+  if (!f.wide) return SC_OK;
   const size_t slot = static_cast<size_t>(tensors) * a.channels * (a.dtype == SC_F32 ? 4 : 2);
   p->ring = slot * kRing <= kRingMost ? kRing : static_cast<int>(kRingMost / slot);
   *smem = p->ring * slot;
@@ -673,7 +679,7 @@ sc_status add_norm_fwd(const NormArgs& a) {
   p.rows = a.rows;
   p.channels = a.channels;
   p.eps = a.eps;
-  const Form f = form_of(a.channels / 8, a.rows);
+  const Form f = form_of(a.channels / 8, a.rows, false);
   const void* k;
   if (a.dtype == SC_F32) k = a.e4m3 ? fwd_kernel<float, true>(f) : fwd_kernel<float, false>(f);
   else if (a.dtype == SC_F16) k = a.e4m3 ? fwd_kernel<__half, true>(f) : fwd_kernel<__half, false>(f);
@@ -701,7 +707,7 @@ sc_status add_norm_bwd(const NormArgs& a) {
   p.rows = a.rows;
   p.channels = a.channels;
   p.eps = a.eps;
-  const Form f = form_of(a.channels / 8, a.rows);
+  const Form f = form_of(a.channels / 8, a.rows, true);
   const void* k = a.dtype == SC_F32 ? bwd_kernel<float>(f)
                                     : a.dtype == SC_F16 ? bwd_kernel<__half>(f) : bwd_kernel<__nv_bfloat16>(f);
   size_t smem = 0;

@@ -29,10 +29,8 @@ __global__ void __launch_bounds__(kLanes* kStreams, 3)
     for (int k = 0; k < kRows; ++k) {
       const int64_t r = r0 + k * step;
       if (r >= rows) continue;
-      // read once: what is to stay in L2 is gz
-      g[k] = ACT ? __ldcs(reinterpret_cast<const uint4*>(gout + r * ldg + c))
-                 : *reinterpret_cast<const uint4*>(gout + r * ldg + c);
-      if (ACT) z[k] = __ldcs(reinterpret_cast<const uint4*>(pre + r * ldp + c));
+      g[k] = *reinterpret_cast<const uint4*>(gout + r * ldg + c);
+      if (ACT) z[k] = *reinterpret_cast<const uint4*>(pre + r * ldp + c);
     }
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
@@ -141,7 +139,6 @@ sc_status linear_bwd(const LinearBwdArgs& a) {
   if (!st && a.gin.data) {  // rows x c_in, summed over c_out
     Product p{};
     p.k = a.c_out;
-    p.backwards = act;
     p.ep.out = a.gin.data, p.ep.ldo = a.gin.stride, p.ep.bf16 = bf16;
     st = run(p, {gz.data, gz.stride, false}, {a.W, a.c_out, false}, a.rows, a.c_in, s);
   }

@@ -79,6 +79,10 @@ __global__ void __launch_bounds__(kThreads)
     mbar_init(accf, 1);
     fence_mbar_init();
   }
+  if (warp == kEpiWarps && lane == 0) {
+    prefetch_map(&ta);
+    prefetch_map(&tb);
+  }
   if (warp == kEpiWarps + 1) {
     tmem_alloc(smem_u32(&s_tmem), static_cast<uint32_t>(p.tmem_cols));
     tmem_relinquish();

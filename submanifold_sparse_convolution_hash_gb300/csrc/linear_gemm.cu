@@ -39,7 +39,6 @@ struct GemmParams {
   int64_t m, n;
   int m_tiles, n_tiles, units, splits;
   int kb, kb_per;  // k blocks in all, and of a unit
-  bool backwards;  // the last rows first: they are what the kernel before left in L2
   int bn, stages, tmem_cols;
   uint32_t b_bytes, idesc;
   float* part;  // splits > 1: [splits, output rows, output columns]
@@ -92,7 +91,6 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t at) {
 
 __device__ __forceinline__ void decode(const GemmParams& p, int u, int* mt, int* nt, int* k0, int* k1, int* split) {
   const int tiles = p.m_tiles * p.n_tiles;
-  if (p.backwards) u = p.units - 1 - u;
   *split = u / tiles;
   const int t = u - *split * tiles;
   const int per = kGroup * p.n_tiles, g = t / per, r = t - g * per;
@@ -136,6 +134,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(done, 1);
     for (int i = 0; i < kEpiWarps * 2; ++i) mbar_init(smem_u32(s_res + i), 1);
     fence_mbar_init();
+  }
+  if (warp == kEpiWarps && lane == 0) {
+    prefetch_map(&ta);
+    prefetch_map(&tb);
   }
   if (warp == kEpiWarps + 1) {
     if (PAIR) {
@@ -552,7 +554,6 @@ sc_status product_rows(const Product& p, cudaStream_t s) {
   g.units = static_cast<int>(mt * nt * pl.splits);
   g.kb = kb;
   g.kb_per = pl.kb_per;
-  g.backwards = p.backwards;
   g.bn = pl.bn;
   g.b_bytes = static_cast<uint32_t>(pl.bn / pl.ctas) * 128;
   g.tmem_cols = 32;

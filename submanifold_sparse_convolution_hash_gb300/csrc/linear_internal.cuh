@@ -188,7 +188,6 @@ struct Product {
   Operand a, b;
   int64_t m, n, k;
   bool e4m3;  // both operands, K-major (else 16 bits: bf16 as in the epilogue)
-  bool backwards;  // product_rows: the last rows first
   Epilogue ep;
 };
 // D's rows are the output's (linear_gemm.cu).

@@ -1,7 +1,10 @@
 // C ABI of the operators on rows (declared in include/sc.h): argument checks, then
 // the kernels of add_norm.cu, linear*.cu and grad_clip.cu.
+#include <cuda.h>
+
 #include <cmath>
 #include <string>
+#include <utility>
 
 #include "linear_internal.cuh"
 #include "views.cuh"
@@ -42,6 +45,40 @@ bool clear_of(const Span& out, const sc_rows_out& o, const Span& in, const sc_ro
   if (!overlap(out, in)) return true;
   return may_be && o.data == i.data && o.stride == i.stride;
 }
+
+// Checks many addresses: those in an allocation that the call has met already need no
+// further asking (48 gradients and their outputs took 10 of a call's 17 us).
+class Allocations {
+ public:
+  sc_status check(const void* p, size_t align, const char* what) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    for (const auto& r : last_)
+      if (at >= r.first && at < r.second && at % align == 0) return SC_OK;
+    const sc_status st = check_dev_ptr(p, align, what);
+    if (st) return st;
+    static const AddressRangeFn range = address_range();
+    CUdeviceptr base = 0;
+    size_t bytes = 0;
+    if (range && range(&base, &bytes, static_cast<CUdeviceptr>(at)) == CUDA_SUCCESS)
+      last_[next_++ % 4] = {static_cast<uintptr_t>(base), static_cast<uintptr_t>(base) + bytes};
+    return SC_OK;
+  }
+
+ private:
+  typedef CUresult (*AddressRangeFn)(CUdeviceptr*, size_t*, CUdeviceptr);
+  static AddressRangeFn address_range() {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuMemGetAddressRange", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    return reinterpret_cast<AddressRangeFn>(f);
+  }
+  std::pair<uintptr_t, uintptr_t> last_[4] = {};
+  unsigned next_ = 0;
+};
 
 sc_status norm_sizes(int64_t rows, int channels, float eps, sc_dtype dtype) {
   if (dtype != SC_F32 && dtype != SC_F16 && dtype != SC_BF16) return invalid("rows must be f32, f16 or bf16");
@@ -242,6 +279,7 @@ sc_status sc_grad_clip(const sc_grad* grads, int64_t count, float max_norm, floa
   if (!(max_norm >= 0.f)) return invalid("max_norm must not be negative or NaN");
   sc_status st = check_dev_ptr(d_norm, 4, "norm");
   if (st) return st;
+  Allocations seen;
   for (int64_t i = 0; i < count; ++i) {
     const sc_grad& g = grads[i];
     if (g.dtype != SC_F32 && g.dtype != SC_F16 && g.dtype != SC_BF16)
@@ -256,8 +294,8 @@ sc_status sc_grad_clip(const sc_grad* grads, int64_t count, float max_norm, floa
     const uintptr_t bytes = static_cast<uintptr_t>(g.n) * size;
     if (d != o && d < o + bytes && o < d + bytes)
       return invalid("gradient " + std::to_string(i) + ": out overlaps data without being it");
-    if ((st = check_dev_ptr(g.data, size, "a gradient"))) return st;
-    if (g.out != g.data && (st = check_dev_ptr(g.out, size, "a gradient's output"))) return st;
+    if ((st = seen.check(g.data, size, "a gradient"))) return st;
+    if (g.out != g.data && (st = seen.check(g.out, size, "a gradient's output"))) return st;
   }
   return grad_clip(grads, count, max_norm, d_norm, reinterpret_cast<cudaStream_t>(stream));
 }
