@@ -7,8 +7,8 @@ off by at most u |y| and fp32's own errors:
 
 - Norm: a row's squares are summed in chains of at most 32 values, then across at most 512 lanes
   pairwise (ten additions) and 16 warps: 64 roundings bound them, 128 with the other operations.
-  Below a format's normal range a rounding is off by half its smallest step (f16: 2^-25; e4m3:
-  2^-10 of the row's scale).
+  Below a format's normal range a rounding is off by half its smallest step (f16: 2^-25; bf16, whose
+  smallest value is 2^-133: 2^-134; e4m3: 2^-10 of the row's scale).
 - Its weight gradient: chains over a block's rows, then over the blocks: at most rows + 64 roundings
   of the sum of magnitudes.
 - Products: the tensor cores add 16 (8 bits: 32) products at a time to a sum and cut what lies
@@ -30,7 +30,7 @@ pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 U = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}
-TINY = {"bf16": 0.0, "f16": 2.0 ** -25, "f32": 0.0}
+TINY = {"bf16": 2.0 ** -134, "f16": 2.0 ** -25, "f32": 0.0}
 E = 2.0 ** -24
 
 
