@@ -627,8 +627,8 @@ typedef struct {
  *
  * res       NULL: h = x.
  * sum       where h goes, in dtype (the next residual), or NULL.
- * d_w       fp32 [channels]; NULL: y = h, for SC_E4M3 only (rows, or weights
- *           laid out as rows, quantised as they are).
+ * d_w       fp32 [channels], 16-byte aligned; NULL: y = h, for SC_E4M3 only
+ *           (rows, or weights laid out as rows, quantised as they are).
  * d_scale   fp32 [rows], 4-byte aligned; SC_E4M3 only.
  * channels  a multiple of 8 in [8, 16384].
  * dtype     of x, res and sum: SC_F32, SC_F16 or SC_BF16.
@@ -673,13 +673,14 @@ typedef enum {
  *   z = x W + d_bias,  out = act(z) + res
  * on the tensor cores, with fp32 sums; out and pre are rounded once.
  *
- * x         [rows, c_in]; in_dtype SC_F16, SC_BF16 or SC_E4M3.
+ * x         [rows, c_in]; in_dtype SC_F16, SC_BF16 or SC_E4M3.  Its rows, and
+ *           res's, must not overlap one another (a stride of 0 is refused).
  * d_W       in_dtype, 16-byte aligned, contiguous: [c_in, c_out]; of SC_E4M3
  *           laid out once as [c_out, c_in].
- * d_scale_x, d_scale_w  fp32 [rows] and [c_out], SC_E4M3 only (as
- *           sc_add_norm_fwd writes them): z = d_scale_x[r] d_scale_w[c] sum_i
+ * d_scale_x, d_scale_w  fp32 [rows] and [c_out] (this one 16-byte aligned),
+ *           SC_E4M3 only (as sc_add_norm_fwd writes them): z = d_scale_x[r] d_scale_w[c] sum_i
  *           x[r, i] W[c, i] + d_bias[c].
- * d_bias    fp32 [c_out], or NULL.
+ * d_bias    fp32 [c_out], 16-byte aligned, or NULL.
  * res       [rows, c_out] in dtype, or NULL.
  * out       [rows, c_out] in dtype; may be res itself (the same pointer and
  *           stride); any other overlap is refused.
@@ -704,7 +705,7 @@ sc_status sc_linear_fwd(const sc_rows* x, const void* d_W, const float* d_scale_
  * gin, d_gW [c_in, c_out] (dtype) and d_gbias (fp32) may each be NULL: not
  * computed; what only they read may then be NULL too.  pre is read only with
  * an activation.  gz is rounded to dtype for the products; d_gbias sums it
- * unrounded.  relu'(0) = 0.  All sums are fp32 and in an order that depends on
+ * unrounded.  The rows of gout and x must not overlap one another.  relu'(0) = 0.  All sums are fp32 and in an order that depends on
  * the sizes alone.  The outputs must not overlap
  * the inputs that are read, or each other.
  */

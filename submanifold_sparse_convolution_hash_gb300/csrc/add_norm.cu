@@ -566,8 +566,19 @@ __global__ void __launch_bounds__(1024) k_column_join(const float* __restrict__ 
   grid_release();
   grid_wait();
   float a = 0.f;
-  if (c < channels)
-    for (int b = threadIdx.y; b < blocks; b += 32) a += part[static_cast<int64_t>(b) * channels + c];
+  if (c < channels) {
+    // loads in flight together, added in order
+    int b = threadIdx.y;
+    for (; b + 7 * 32 < blocks; b += 8 * 32) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = part[static_cast<int64_t>(b + k * 32) * channels + c];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) a += v[k];
+    }
+#pragma unroll 7
+    for (; b < blocks; b += 32) a += part[static_cast<int64_t>(b) * channels + c];
+  }
   s[threadIdx.y][threadIdx.x] = a;
   __syncthreads();
   a = s[threadIdx.x][threadIdx.y];

@@ -2,7 +2,7 @@
 // spread over the whole card.
 //
 // The weights are A here: a block's tile is 128 output columns (the lanes of TMEM) by all the
-// rows, padded to 16 (B, at most 256 of them).  The blocks of a cluster take runs of k of one
+// rows, padded to 16 (B, at most 128 of them).  The blocks of a cluster take runs of k of one
 // tile, leave their fp32 sums in their own shared memory, and each adds a share of the rows over
 // all of them, in the order of the runs, through the cluster's shared memory: one launch, no
 // workspace, no order of arrival.  Two blocks an SM where their tiles are narrow, so that one
@@ -22,7 +22,7 @@ constexpr int kMaxStages = 8;
 
 struct FewParams {
   int64_t m, n;  // output columns, rows
-  int n_tiles, kb, kb_per, bn, stages, tmem_cols, ways;
+  int kb, kb_per, bn, stages, tmem_cols, ways;
   uint32_t b_bytes, idesc;
   int* status;
   Epilogue ep;
@@ -36,7 +36,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t at) {
 
 // This block's share of the rows (rank, rank + ways, ...), N at a time: the runs' sums in order.
 template <bool BF16, int N>
-__device__ __forceinline__ void join_rows(const FewParams& p, uint32_t base, int rank, int rows, int64_t n0, int64_t col,
+__device__ __forceinline__ void join_rows(const FewParams& p, uint32_t base, int rank, int rows, int64_t col,
                                           float sw, float bias) {
 #pragma unroll 1
   for (int t0 = rank; t0 < rows; t0 += N * p.ways) {
@@ -47,7 +47,7 @@ __device__ __forceinline__ void join_rows(const FewParams& p, uint32_t base, int
 #pragma unroll
       for (int t = 0; t < N; ++t) z[t] += ld_cluster(at + min(t0 + t * p.ways, rows - 1) * 512);
     }
-    finish_rows<BF16, N>(p.ep, n0 + t0, p.ways, min(N, (rows - t0 + p.ways - 1) / p.ways), col, z, sw, bias);
+    finish_rows<BF16, N>(p.ep, t0, p.ways, min(N, (rows - t0 + p.ways - 1) / p.ways), col, z, sw, bias);
   }
 }
 
@@ -67,8 +67,7 @@ __global__ void __launch_bounds__(kThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t stage = kA + p.b_bytes;
   const uint32_t full = smem_u32(s_bar), empty = full + 8 * kMaxStages, accf = empty + 8 * kMaxStages;
-  const int rank = static_cast<int>(cluster_rank()), tile = blockIdx.x / p.ways;
-  const int mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
+  const int rank = static_cast<int>(cluster_rank()), mt = blockIdx.x / p.ways;
   const int k0 = min(p.kb, rank * p.kb_per), k1 = min(p.kb, k0 + p.kb_per);  // may be none
   if (threadIdx.x == 0) {
     s_abort_word = 0;
@@ -111,7 +110,7 @@ __global__ void __launch_bounds__(kThreads)
         } else {
           tma_load_2d(da, &ta, kb * kBlock, mt * 128, bar);
         }
-        tma_load_2d(da + kA, &tb, kb * kBlock, nt * p.bn, bar);
+        tma_load_2d(da + kA, &tb, kb * kBlock, 0, bar);
         if (++s == p.stages) s = 0, ph ^= 1;
       }
       // after a timeout: the copies landed before the block may end
@@ -148,8 +147,7 @@ __global__ void __launch_bounds__(kThreads)
   // The products are done and shared memory is free for their sums.
   __syncthreads();
   tc_fence_after();
-  const int64_t n0 = static_cast<int64_t>(nt) * p.bn;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(p.bn), p.n - n0));
+  const int rows = static_cast<int>(p.n);
   const int64_t col = static_cast<int64_t>(mt) * 128 + threadIdx.x;  // of the first four warps
   const bool mine = warp < kEpiWarps && col < p.m;
   const float bias = mine && p.ep.bias ? p.ep.bias[col] : 0.f, sw = mine && p.ep.sw ? p.ep.sw[col] : 1.f;
@@ -165,7 +163,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int t = 0; t < 16; ++t) v[t] = 0.f;
       }
       if (p.ways == 1) {
-        if (mine) finish_rows<BF16, 16>(p.ep, n0 + c, 1, min(16, rows - c), col, v, sw, bias);
+        if (mine) finish_rows<BF16, 16>(p.ep, c, 1, min(16, rows - c), col, v, sw, bias);
       } else {
 #pragma unroll
         for (int t = 0; t < 16; ++t)
@@ -187,9 +185,9 @@ __global__ void __launch_bounds__(kThreads)
     if (mine) {
       // up to eight rows at a time: their loads are in flight together
       const int per = (rows + p.ways - 1) / p.ways;
-      if (per <= 1) join_rows<BF16, 1>(p, base, rank, rows, n0, col, sw, bias);
-      else if (per <= 2) join_rows<BF16, 2>(p, base, rank, rows, n0, col, sw, bias);
-      else join_rows<BF16, 8>(p, base, rank, rows, n0, col, sw, bias);
+      if (per <= 1) join_rows<BF16, 1>(p, base, rank, rows, col, sw, bias);
+      else if (per <= 2) join_rows<BF16, 2>(p, base, rank, rows, col, sw, bias);
+      else join_rows<BF16, 8>(p, base, rank, rows, col, sw, bias);
     }
     __syncwarp();
     cluster_sync_all();
@@ -212,13 +210,12 @@ sc_status product_few(const Product& p, cudaStream_t s) {
   g.m = p.m;
   g.n = p.n;
   g.kb = static_cast<int>((p.k + block - 1) / block);
-  g.n_tiles = static_cast<int>((p.n + 255) / 256);
-  g.bn = static_cast<int>(((p.n + g.n_tiles - 1) / g.n_tiles + 15) / 16 * 16);
+  g.bn = static_cast<int>((p.n + 15) / 16 * 16);
   g.b_bytes = static_cast<uint32_t>(g.bn) * 128;
   g.tmem_cols = 32;
   while (g.tmem_cols < g.bn) g.tmem_cols *= 2;
   g.idesc = p.e4m3 ? make_idesc_e4m3(128, g.bn) : make_idesc(p.ep.bf16, 128, g.bn) | (p.a.mn ? 1u << 15 : 0u);
-  const int64_t tiles = (p.m + 127) / 128 * g.n_tiles;
+  const int64_t tiles = (p.m + 127) / 128;
   // Runs of k until two blocks an SM have work, and no run below two k blocks.
   const int sms = device_sm_count();
   g.ways = 1;
@@ -227,7 +224,6 @@ sc_status product_few(const Product& p, cudaStream_t s) {
   // As many stages as its run has, at most what leaves room for two blocks.
   const uint32_t stage = 128 * 128 + g.b_bytes;
   int stages = static_cast<int>((110u * 1024) / stage);
-  if (stages < 3) stages = static_cast<int>((216u * 1024) / stage);
   if (stages > kMaxStages) stages = kMaxStages;
   g.stages = stages < g.kb_per ? stages : g.kb_per;
   size_t smem = static_cast<size_t>(g.stages) * stage;
@@ -241,7 +237,6 @@ sc_status product_few(const Product& p, cudaStream_t s) {
   g.ep = p.ep;
   const void* kern = p.ep.bf16 ? kernel_of<true>(p) : kernel_of<false>(p);
   if ((st = kernel_setup(kern, smem, nullptr))) return st;
-  if (tiles * g.ways > 0x7fffffff) return set_error(SC_ERR_UNSUPPORTED, "a product of over 2^31 tiles");
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;

@@ -3,8 +3,16 @@
 // D tiles of 128 rows a block, or 256 a pair of blocks (cta_group::2: each block then
 // stages half of B as well, so a tile costs half of B's reads), and bn columns.  One
 // thread loads both operands by TMA into a ring of shared-memory stages of 128 bytes of
-// k each, one issues the products, eight warps read the sums from TMEM and finish them;
+// k each, one issues the products, sixteen warps read the sums from TMEM and finish them;
 // two accumulators let that overlap the next tile's products.
+//
+// What bounds it: long k, the tensor cores and the card's power (8,192 x 4,096 -> 16,384,
+// bf16, gelu: 653 to 700 us by the card's clocks, 1.57 to 1.68 PFLOP/s, where the library's
+// plain product reaches 1.72; in 8 bits 8,192 x 4,096 -> 4,096 94 to 105 us, 2.6 to 2.9); short k,
+// memory (480,000 x 256 -> 512, f16, silu, both outputs: 202 us, 6.1 TB/s); between them
+// shared memory's 128 bytes a clock, which a k block is written to and read from once each.
+// Four stages do what five or six do.  Two pairs that share B by TMA multicast were slower
+// (715 against 658 us on the first of these): clusters of four leave 8 of 152 SMs out.
 //
 // Whatever its layout, an operand is staged as 128-byte rows with the 128-byte swizzle.
 // K-major: a row holds 64 (8-bit: 128) values of k of one vector.  MN-major: a row holds
@@ -41,12 +49,11 @@ struct GemmParams {
   int kb, kb_per;  // k blocks in all, and of a unit
   int bn, stages, tmem_cols;
   uint32_t b_bytes, idesc;
-  float* part;  // splits > 1: [splits, output rows, output columns]
+  float* part;  // splits > 1: the runs' sums [splits, m, n]
   Epilogue ep;
 };
 
-// Maps of what the rows' form writes and reads past the products: tiles of 32 rows and 32
-// columns.
+// Maps of what is written, and read beside the products: tiles of 32 rows and 32 columns.
 struct OutMaps {
   CUtensorMap out, pre, res, part;
 };
@@ -204,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (++s == p.stages) s = 0, ph ^= 1;
       }
+      if (rank != 0) mbar_drain(done, 0);  // nor while the pair's last arrival here is under way
     }
     __syncwarp();
   } else if (warp == kEpiWarps + 1) {
@@ -254,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, part = warp >> 2;
     const uint32_t acce_at = PAIR ? map_to_rank(acce, 0) : acce;
     int j = 0;
-    // The rows' form: a warp's 32 rows leave 32 columns at a time through two tiles of
+    // A warp's 32 rows leave 32 columns at a time through two tiles of
     // shared memory by TMA, one for `out` and one for `pre`, or by turns.  The residual
     // comes in the same way, into the tile that its sum leaves from, and where tiles take
     // turns ahead of its own.
@@ -547,7 +555,7 @@ sc_status product_rows(const Product& p, cudaStream_t s) {
   g.m = p.m;
   g.n = p.n;
   const int64_t mt = (p.m + 128 * pl.ctas - 1) / (128 * pl.ctas), nt = (p.n + pl.bn - 1) / pl.bn;
-  if (mt * nt * pl.splits > 0x7fffffff) return set_error(SC_ERR_UNSUPPORTED, "a product of over 2^31 tiles");
+  if (mt * nt * pl.splits > 0x7f000000) return set_error(SC_ERR_UNSUPPORTED, "a product of over 2^31 tiles");
   g.m_tiles = static_cast<int>(mt);
   g.n_tiles = static_cast<int>(nt);
   g.splits = pl.splits;
