@@ -234,10 +234,14 @@ void keep_pool_memory() {
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || done[dev]) return;
   cudaMemPool_t pool;
+  // a process's first call may be one that is captured, which this one setting would end
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaThreadExchangeStreamCaptureMode(&mode);
   if (cudaDeviceGetDefaultMemPool(&pool, dev) == cudaSuccess) {
     uint64_t thr = ~0ull;
     cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &thr);
   }
+  cudaThreadExchangeStreamCaptureMode(&mode);
   done[dev] = true;
 }
 
