@@ -9,25 +9,26 @@
 namespace sc {
 namespace {
 
-constexpr int kLanes = 32, kStreams = 8;
+constexpr int kThreads = 256;
 constexpr int64_t kFewRows = 128;
 
-// gz = gout * act'(pre), in 16 bits, and the columns' sums of the unrounded values:
-// a warp holds 256 columns of a row (eight a lane), a block's eight warps take rows in
-// turn, and a block writes its sums once.
-template <bool ACT>
-__global__ void __launch_bounds__(kLanes* kStreams, 3)
+// gz = gout * act'(pre), in 16 bits, and the columns' sums of the unrounded values.  A block
+// holds blockDim.x vectors of eight columns of blockDim.y rows, which it takes in turn, and writes
+// its sums once.  The widths are cut evenly into runs of at most 64 vectors: cut into 32 lanes
+// wherever that ends, a fifth of the blocks had 3 of 131 vectors (9,973 x 1,048, gelu).
+template <int ACT, bool BF16>
+__global__ void __launch_bounds__(kThreads, 3)
     k_act_grad(const uint16_t* __restrict__ gout, int64_t ldg, const uint16_t* __restrict__ pre, int64_t ldp,
-               uint16_t* __restrict__ gz, float* __restrict__ part, int64_t rows, int channels, int act, bool bf16) {
-  __shared__ float s_sum[kStreams][kLanes * 8 + 8];
+               uint16_t* __restrict__ gz, float* __restrict__ part, int64_t rows, int channels) {
+  __shared__ float s_sum[kThreads * 8];
   grid_release();
   grid_wait();
-  const int c = (blockIdx.x * kLanes + threadIdx.x) * 8;
+  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
   const bool in = c < channels;
   float sum[8] = {};
   constexpr int kRows = 4;  // rows in flight
-  const int64_t step = static_cast<int64_t>(gridDim.y) * kStreams;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * kStreams + threadIdx.y; r0 < rows && in; r0 += kRows * step) {
+  const int64_t step = static_cast<int64_t>(gridDim.y) * blockDim.y;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * blockDim.y + threadIdx.y; r0 < rows && in; r0 += kRows * step) {
     uint4 g[kRows], z[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
@@ -41,28 +42,40 @@ __global__ void __launch_bounds__(kLanes* kStreams, 3)
       const int64_t r = r0 + k * step;
       if (r >= rows) continue;
       float f[8];
-      unpack8(g[k], bf16, f);
+      unpack8(g[k], BF16, f);
       if (ACT) {
         float t[8];
-        unpack8(z[k], bf16, t);
+        unpack8(z[k], BF16, t);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= slope_of(t[i], act);
-        *reinterpret_cast<uint4*>(gz + r * channels + c) = pack8(f, bf16);
+        for (int i = 0; i < 8; ++i) f[i] *= slope_of(t[i], ACT);
+        *reinterpret_cast<uint4*>(gz + r * channels + c) = pack8(f, BF16);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[i] += f[i];
     }
   }
   if (!part) return;
+  const int width = blockDim.x * 8;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s_sum[threadIdx.y][threadIdx.x * 8 + i] = sum[i];
+  for (int i = 0; i < 8; ++i) s_sum[threadIdx.y * width + threadIdx.x * 8 + i] = sum[i];
   __syncthreads();
-  const int t = threadIdx.y * kLanes + threadIdx.x, cc = blockIdx.x * kLanes * 8 + t;
-  if (cc >= channels) return;
-  float a = 0.f;
-#pragma unroll
-  for (int y = 0; y < kStreams; ++y) a += s_sum[y][t];
-  part[static_cast<int64_t>(blockIdx.y) * channels + cc] = a;
+  for (int t = threadIdx.y * blockDim.x + threadIdx.x; t < width; t += blockDim.x * blockDim.y) {
+    const int cc = blockIdx.x * width + t;
+    if (cc >= channels) break;
+    float a = 0.f;
+    for (int y = 0; y < static_cast<int>(blockDim.y); ++y) a += s_sum[y * width + t];
+    part[static_cast<int64_t>(blockIdx.y) * channels + cc] = a;
+  }
+}
+
+template <bool BF16>
+const void* act_grad_kernel(int act) {
+  switch (act) {
+    case SC_ACT_RELU: return reinterpret_cast<const void*>(k_act_grad<SC_ACT_RELU, BF16>);
+    case SC_ACT_GELU: return reinterpret_cast<const void*>(k_act_grad<SC_ACT_GELU, BF16>);
+    case SC_ACT_SILU: return reinterpret_cast<const void*>(k_act_grad<SC_ACT_SILU, BF16>);
+    default: return reinterpret_cast<const void*>(k_act_grad<SC_ACT_NONE, BF16>);
+  }
 }
 
 // rows x columns, by the form that fits the number of rows.
@@ -104,10 +117,10 @@ sc_status linear_bwd(const LinearBwdArgs& a) {
   float* part = nullptr;
   sc_status st = SC_OK;
   if (act || a.gbias) {
-    const int cols = (a.c_out + kLanes * 8 - 1) / (kLanes * 8);
-    // six blocks an SM, and at least eight rows a warp
+    const int nvec = a.c_out / 8, cols = (nvec + 63) / 64, lanes = (nvec + cols - 1) / cols, streams = kThreads / lanes;
+    // six blocks an SM, and at least eight rows a thread
     int64_t runs = (static_cast<int64_t>(device_sm_count()) * 6 + cols - 1) / cols;
-    const int64_t most = (a.rows + kStreams * 8 - 1) / (kStreams * 8);
+    const int64_t most = (a.rows + streams * 8 - 1) / (streams * 8);
     if (runs > most) runs = most;
     if (act) {
       st = dev_alloc(&buf, static_cast<size_t>(a.rows) * a.c_out * 2, s);
@@ -120,20 +133,18 @@ sc_status linear_bwd(const LinearBwdArgs& a) {
       const uint16_t* pre = static_cast<const uint16_t*>(a.pre.data);
       uint16_t* out = static_cast<uint16_t*>(buf);
       int64_t ldg = a.gout.stride, ldp = a.pre.stride, rows = a.rows;
-      int channels = a.c_out, kind = a.act;
-      bool b = bf16;
-      void* args[] = {&g, &ldg, &pre, &ldp, &out, &part, &rows, &channels, &kind, &b};
+      int channels = a.c_out;
+      void* args[] = {&g, &ldg, &pre, &ldp, &out, &part, &rows, &channels};
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
       at[0].val.programmaticStreamSerializationAllowed = 1;
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(cols, static_cast<unsigned>(runs));
-      cfg.blockDim = dim3(kLanes, kStreams);
+      cfg.blockDim = dim3(lanes, streams);
       cfg.stream = s;
       cfg.attrs = at;
       cfg.numAttrs = 1;
-      const void* k = act ? reinterpret_cast<const void*>(k_act_grad<true>)
-                          : reinterpret_cast<const void*>(k_act_grad<false>);
+      const void* k = bf16 ? act_grad_kernel<true>(a.act) : act_grad_kernel<false>(a.act);
       cudaError_t e;
       SC_LAUNCH("act_grad", s, e = cudaLaunchKernelExC(&cfg, k, args));
       if (e != cudaSuccess) st = set_cuda_error(e, "activation gradient launch");
