@@ -448,28 +448,39 @@ struct Plan {
   int ctas, bn, splits, kb_per;
 };
 
+// Whether an operand's rows begin elsewhere than on lines of 128 bytes.
+bool straddles(const Operand& o, bool e4m3) {
+  return (reinterpret_cast<uintptr_t>(o.data) & 127) || (o.ld * (e4m3 ? 1 : 2)) % 128;
+}
+
 // The cheapest by an estimate in SM clocks.  A k block of a tile costs what shared memory takes to
 // be written by TMA and read by the tensor cores, 128 bytes a clock (a pair's blocks read half
 // of B from each other), and not below 560 (measured: 570 to 590 for tiles of 64 and 128
-// columns, 665 for a pair's 256, 813 for one block's 256).  A unit costs that or what its
+// columns, 665 for a pair's 256, 813 for one block's 256); where an operand's rows straddle lines
+// of 128 bytes, about 1.5 % of a clock more for each byte over 20 KB (9,973 x 1,992 x 1,048: 880 for
+// a pair's 256 columns, 1,210 for one block's).  A unit costs that or what its
 // sixteen warps take to finish it, whichever is longer (about 27 clocks a column for one
 // block, 36 for a pair, whose halves wait for each other: 480,000 x 256 -> 512 with silu took
 // 194 us with one block a tile, 250 with a pair).  Cut sums are written and read once more
 // (about 16 bytes a clock and SM in each direction), by one more launch.
 Plan plan_of(const Product& p, int kb) {
   const int sms = device_sm_count();
+  const bool straddle = straddles(p.a, p.e4m3) || straddles(p.b, p.e4m3);
   Plan best{1, 64, 1, kb};
   double least = 1e300;
   for (int form = 0; form < 5; ++form) {
     const int ctas = form < 2 ? 2 : 1, bn = form == 0 || form == 2 ? 256 : form == 1 || form == 3 ? 128 : 64;
     const int64_t tiles = ((p.m + 128 * ctas - 1) / (128 * ctas)) * ((p.n + bn - 1) / bn);
     const int slots = sms / ctas;
-    const double step = 1.04 * fmax(560.0, 256.0 + bn / ctas + bn);
+    const double load = 128.0 * (128 + bn / ctas);  // bytes of a k block and block
+    const double step = 1.04 * fmax(560.0, 256.0 + bn / ctas + bn) + (straddle && load > 20480 ? 0.0145 * (load - 20480) : 0.0);
     const double finish = 700.0 + bn * (ctas == 2 ? 36.0 : 27.0);
-    for (int splits = 1; splits <= kb && splits <= 2 * slots; ++splits) {
-      const int per = (kb + splits - 1) / splits;
-      if ((kb + per - 1) / per != splits) continue;  // the same cut as a smaller number's
-      if (splits > 1 && (tiles * splits > 4 * slots || per < 4)) break;
+    // whole k, and the cuts that fill one to four waves
+    for (int wave = 0; wave <= 4; ++wave) {
+      int64_t cuts = wave ? wave * slots / tiles : 1;
+      if (wave && cuts > kb / 4) cuts = kb / 4;
+      if (wave && cuts < 2) continue;
+      const int per = static_cast<int>((kb + cuts - 1) / cuts), splits = (kb + per - 1) / per;
       const double waves = static_cast<double>((tiles * splits + slots - 1) / slots);
       double cost = waves * (fmax(per * step, finish) + 300.0) + 0.5 * finish;
       if (splits > 1) cost += 5000.0 + static_cast<double>(p.m) * p.n * 4.0 * splits * 2.0 / (16.0 * sms);
