@@ -971,7 +971,7 @@ class GradList:
         high = high_w = -1  # the furthest end so far, of any run and of a written one
         for lo, hi, i in spans:
             if lo < (high if i >= 0 else high_w):
-                raise ValueError("gradients that are written share memory with one another or with others that are read")
+                raise ValueError("gradients that are written share memory with one another or with others")
             high = max(high, hi)
             if i >= 0:
                 high_w = max(high_w, hi)

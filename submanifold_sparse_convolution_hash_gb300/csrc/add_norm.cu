@@ -188,35 +188,35 @@ __device__ __forceinline__ void store_row(const NormParams& p, const Weights<NV>
       if (at < nvec) st_vec(static_cast<T*>(p.sum) + row * p.ldsum + at * 8, h[v]);
     }
   }
-      const float r = p.w ? rsqrtf(ss / static_cast<float>(p.channels) + p.eps) : 1.f;
-      if constexpr (E4M3) {
-        float s = top * r / kE4m3Max;
-        if (s < 0x1p-126f) s = 0.f;
-        const float f = s > 0.f ? 1.f / s : 0.f;
-        if (lane == 0) p.scale[row] = s;
-  #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int at = lane + v * lanes;
-          if (at >= nvec) continue;
-          float y[8];
-          w.get(v, y);
-  #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] *= h[v][i] * r * f;
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * p.ldout + at * 8) =
-              make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16), e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
-        }
-      } else {
-  #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int at = lane + v * lanes;
-          if (at >= nvec) continue;
-          float y[8];
-          w.get(v, y);
-  #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] *= h[v][i] * r;
-          st_vec(static_cast<T*>(p.out) + row * p.ldout + at * 8, y);
-        }
-      }
+  const float r = p.w ? rsqrtf(ss / static_cast<float>(p.channels) + p.eps) : 1.f;
+  if constexpr (E4M3) {
+    float s = top * r / kE4m3Max;
+    if (s < 0x1p-126f) s = 0.f;
+    const float f = s > 0.f ? 1.f / s : 0.f;
+    if (lane == 0) p.scale[row] = s;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = lane + v * lanes;
+      if (at >= nvec) continue;
+      float y[8];
+      w.get(v, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= h[v][i] * r * f;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * p.ldout + at * 8) =
+          make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16), e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = lane + v * lanes;
+      if (at >= nvec) continue;
+      float y[8];
+      w.get(v, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= h[v][i] * r;
+      st_vec(static_cast<T*>(p.out) + row * p.ldout + at * 8, y);
+    }
+  }
 }
 
 constexpr int kBlock = 256;  // of the forms in which lanes hold a row

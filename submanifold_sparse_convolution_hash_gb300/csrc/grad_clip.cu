@@ -165,7 +165,8 @@ __device__ __forceinline__ double squares(const T* p, int lo, int hi) {
   }
   float edge = 0.f;
   if (static_cast<int>(threadIdx.x) < sp.head) edge = to_f(p[lo + threadIdx.x]);
-  else if (threadIdx.x >= 32 && static_cast<int>(threadIdx.x) - 32 < sp.tail) edge = to_f(p[sp.v1 * V + threadIdx.x - 32]);
+  else if (threadIdx.x >= 32 && static_cast<int>(threadIdx.x) - 32 < sp.tail)
+    edge = to_f(p[sp.v1 * V + threadIdx.x - 32]);
 #pragma unroll
   for (int l = 0; l < L; ++l) {
     any |= u[l].x | u[l].y | u[l].z | u[l].w;
@@ -284,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_scale(const __grid_constan
     if (!cut && e.out == e.data) continue;
     int lo, hi;
     const int64_t at = chunk_at(e, c, &lo, &hi);
-    if (e.dtype == SC_F32) scale_chunk(static_cast<const float*>(e.data) + at, static_cast<float*>(e.out) + at, lo, hi, by);
+    if (e.dtype == SC_F32)
+      scale_chunk(static_cast<const float*>(e.data) + at, static_cast<float*>(e.out) + at, lo, hi, by);
     else if (e.dtype == SC_F16)
       scale_chunk(static_cast<const __half*>(e.data) + at, static_cast<__half*>(e.out) + at, lo, hi, by);
     else

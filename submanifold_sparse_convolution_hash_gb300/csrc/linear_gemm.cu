@@ -92,7 +92,10 @@ __device__ __forceinline__ void st_shared(uint32_t at, const uint4& v) {
 }
 __device__ __forceinline__ uint4 ld_shared(uint32_t at) {
   uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
   return v;
 }
 
@@ -413,7 +416,8 @@ __global__ void __launch_bounds__(256) k_gemm_join(const float* __restrict__ par
   grid_wait();
   const int tx = threadIdx.x % kCols, ty = threadIdx.x / kCols;
   const int64_t per_row = cols >> 3, total = rows * per_row;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kCols; t0 < total; t0 += static_cast<int64_t>(gridDim.x) * kCols) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kCols;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kCols; t0 < total; t0 += stride) {
     const int64_t t = t0 + tx, r = t / per_row, c = (t - r * per_row) * 8;
     float z[8] = {};
     if (t < total) {
@@ -473,7 +477,8 @@ Plan plan_of(const Product& p, int kb) {
     const int64_t tiles = ((p.m + 128 * ctas - 1) / (128 * ctas)) * ((p.n + bn - 1) / bn);
     const int slots = sms / ctas;
     const double load = 128.0 * (128 + bn / ctas);  // bytes of a k block and block
-    const double step = 1.04 * fmax(560.0, 256.0 + bn / ctas + bn) + (straddle && load > 20480 ? 0.0145 * (load - 20480) : 0.0);
+    const double step = 1.04 * fmax(560.0, 256.0 + bn / ctas + bn) +
+                        (straddle && load > 20480 ? 0.0145 * (load - 20480) : 0.0);
     const double finish = 700.0 + bn * (ctas == 2 ? 36.0 : 27.0);
     // whole k, and the cuts that fill one to four waves
     for (int wave = 0; wave <= 4; ++wave) {
@@ -505,8 +510,9 @@ sc_status make_out_map(CUtensorMap* map, const void* data, int64_t ld, int64_t r
   const cuuint32_t one[3] = {1, 1, 1};
   const CUresult r = encode(map, eb == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
                             parts ? 3 : 2, const_cast<void*>(data), dims, strides, box, one,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, eb == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                            CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            eb == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SC_OK : set_error(SC_ERR_CUDA, "tensor map of an output");
 }
 
@@ -638,7 +644,8 @@ sc_status product_rows(const Product& p, cudaStream_t s) {
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    const void* join = many ? reinterpret_cast<const void*>(k_gemm_join<8>) : reinterpret_cast<const void*>(k_gemm_join<1>);
+    const void* join = many ? reinterpret_cast<const void*>(k_gemm_join<8>)
+                            : reinterpret_cast<const void*>(k_gemm_join<1>);
     SC_LAUNCH("linear_join", s, e = cudaLaunchKernelExC(&cfg, join, jargs));
   }
   dev_free(g.part, s);

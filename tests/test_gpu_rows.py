@@ -117,7 +117,8 @@ def test_norm_forward(rows, channels, dtype, residual, room):
         assert torch.equal(got[2], total)
 
 
-@pytest.mark.parametrize("rows,channels,dtype", [(5, 8, "f32"), (70, 264, "bf16"), (3, 4096, "f16"), (2500, 96, "bf16")])
+@pytest.mark.parametrize("rows,channels,dtype",
+                         [(5, 8, "f32"), (70, 264, "bf16"), (3, 4096, "f16"), (2500, 96, "bf16")])
 def test_rows_quantised_as_they_are(rows, channels, dtype):
     g = gen(3)
     x = normal(g, rows, channels, std=3.0, dtype=DT[dtype])
@@ -343,7 +344,8 @@ def test_linear_gradients(rows, c_in, c_out, dtype, act, bias, room):
     tiny = TINY[dtype] if act != "none" else 0.0
     xd, wd = x.double(), W.double()
     ref, size = gz @ wd.t(), gz.abs() @ wd.abs().t() + 1e-30
-    bound = U[dtype] * ref.abs() + 1.01 * ((u + sums(c_out)) * size + slope @ wd.abs().t()) + tiny * wd.abs().sum(1) + TINY[dtype]
+    bound = (U[dtype] * ref.abs() + 1.01 * ((u + sums(c_out)) * size + slope @ wd.abs().t())
+             + tiny * wd.abs().sum(1) + TINY[dtype])
     within(gin, ref, bound, "gin")
     ref, size = xd.t() @ gz, xd.abs().t() @ gz.abs() + 1e-30
     bound = (U[dtype] * ref.abs() + 1.01 * ((u + sums(rows)) * size + xd.abs().t() @ slope)

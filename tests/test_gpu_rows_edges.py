@@ -109,7 +109,8 @@ def test_activations_far_from_zero():
                 y = sc.sc_linear_fwd(x[:rows], eye, act=act)
                 ref = act_ref(x[:rows].double(), act)
                 # the integral is off by 2^-22 (and by 2^-18 of itself): values past the last bits are 0
-                bound = (U[dtype] + 2.0 ** -18) * ref.abs() + 2.0 ** -22 * x[:rows].double().abs().clamp(max=16) + TINY[dtype]
+                bound = ((U[dtype] + 2.0 ** -18) * ref.abs() + 2.0 ** -22 * x[:rows].double().abs().clamp(max=16)
+                         + TINY[dtype])
                 within(y, ref, bound, act)
             pre = x
             gout = torch.ones_like(x)
