@@ -7,8 +7,8 @@
 // two accumulators let that overlap the next tile's products.
 //
 // What bounds it: long k, the tensor cores and the card's power (8,192 x 4,096 -> 16,384,
-// bf16, gelu: 653 to 700 us by the card's clocks, 1.57 to 1.68 PFLOP/s, where the library's
-// plain product reaches 1.72; in 8 bits 8,192 x 4,096 -> 4,096 94 to 105 us, 2.6 to 2.9); short k,
+// bf16, gelu: 626 to 665 us by the card's clocks, 1.65 to 1.76 PFLOP/s, where the library's
+// plain product sustains 1.72; in 8 bits 8,192 x 4,096 -> 4,096 94 to 105 us, 2.6 to 2.9); short k,
 // memory (480,000 x 256 -> 512, f16, silu, both outputs: 202 us, 6.1 TB/s); between them
 // shared memory's 128 bytes a clock, which a k block is written to and read from once each.
 // Four stages do what five or six do.  Two pairs that share B by TMA multicast were slower
@@ -41,7 +41,9 @@ constexpr int kMaxStages = 12;
 constexpr int kSmemMost = 230400;                  // of 232,448, with the barriers and the alignment
 constexpr uint32_t kTile = 32 * 64;               // 32 rows of 32 16-bit columns on their way out
 constexpr uint32_t kStaging = kEpiWarps * 2 * kTile;
-constexpr int kGroup = 8;  // tile rows whose tiles are neighbours in time: they share B's columns in L2
+// Tile rows whose tiles are neighbours in time: they share B's columns in L2, and B is read once for each
+// such group.  8,192 x 4,096 -> 16,384, 32 tile rows, us: 4 670, 8 646, 12 626, 16 626, 32 667.
+constexpr int kGroup = 12;
 
 struct GemmParams {
   int64_t m, n;
