@@ -636,9 +636,13 @@ typedef struct {
  *           multiples of 8 bytes).
  *
  * Squares are summed in fp32 from the unrounded h, and each output is rounded
- * once.  A row whose max |y| / 448 is below 2^-126 is written as zeros with
- * scale 0.  An infinity leaves its row of 8-bit values without any: scale inf,
- * values 0 or NaN.  sum may be x or res themselves (the same pointer and
+ * once.  A row whose squares pass fp32's range (an infinity among them) has
+ * r = 0: values 0, and NaN where h is infinite.  A row whose max |y| / 448 is
+ * below 2^-126 is written as zeros with scale 0.  An infinity, or with weights
+ * squares past fp32's range, leaves its row of 8-bit values without any: scale
+ * inf, values 0 or NaN.  With weights a NaN makes its whole row and the scale
+ * NaN; without them it is one value of a row that keeps the others' scale.
+ * sum may be x or res themselves (the same pointer and
  * stride), and so may out where it has their dtype; any other overlap is
  * refused.
  */

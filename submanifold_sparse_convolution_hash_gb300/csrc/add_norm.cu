@@ -9,6 +9,7 @@
 //
 // Bound by memory: 32,768 rows of 4,096, bf16, residual, to 8 bits 141 us (6.66 TB/s of the 6.78 that a
 // copy reaches), gradients of 480,000 rows of 256, f16, 162 (6.07).
+#include <cmath>
 #include <type_traits>
 
 #include "sc_internal.cuh"
@@ -192,6 +193,8 @@ __device__ __forceinline__ void store_row(const NormParams& p, const Weights<NV>
   if constexpr (E4M3) {
     float s = top * r / kE4m3Max;
     if (s < 0x1p-126f) s = 0.f;
+    // squares past fp32 (r = 0, and top r 0 or NaN): no value, and a scale that says so; a NaN stays one
+    if (p.w && !(ss < INFINITY)) s = ss;
     const float f = s > 0.f ? 1.f / s : 0.f;
     if (lane == 0) p.scale[row] = s;
 #pragma unroll

@@ -5,6 +5,8 @@ Sums of whole numbers below 2^24 are exact in fp32 in any order, and a result of
 256 (bf16) is exact after its rounding, so the products' tests with whole numbers compare for equality: a row
 or a run of k that is lost, or added twice, shows.  The other tolerances are test_gpu_rows.py's; where a
 bound there grows with the number of rows, the longest chain of additions takes its place."""
+import math
+
 import pytest
 import torch
 
@@ -149,6 +151,34 @@ def test_one_row_of_any_stride():
         got = sc.sc_linear_bwd(gout, x, W, pre=gout, act="silu", bias=True)
         want = sc.sc_linear_bwd(gnear.view(1, 72), near.view(1, c), W, pre=gnear.view(1, 72), act="silu", bias=True)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ----------------------------------------------------------- 8-bit scales --
+@pytest.mark.parametrize("rows,channels", [(7, 64), (4001, 24), (2600, 512), (2600, 1000), (2600, 4096), (7, 4096),
+                                           (7, 16384)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_8_bit_scales_of_rows_without_a_norm(rows, channels, dtype):
+    """Lane, block and ring forms: a row whose squares leave fp32's range, an infinity among them or not, has
+    the scale infinity and gives no value; a NaN gives the scale NaN; the other rows know nothing of it."""
+    g = gen(83)
+    x = normal(g, rows, channels, dtype=DT[dtype])
+    w = 1 + normal(g, channels, std=0.1)
+    w[5] = 0.0
+    q0, s0 = sc.sc_add_norm_fwd(x, w, e4m3=True)
+    x[1, 3] = math.inf
+    x[2, 3] = math.nan
+    x[3, 5] = -math.inf  # where the weight is 0
+    x[4] = 2e38
+    x[5, 0], x[5, 7] = math.inf, math.nan
+    q, s = sc.sc_add_norm_fwd(x, w, e4m3=True)
+    for r in (1, 3, 4):
+        assert float(s[r]) == math.inf, r
+        assert (q[r].float() * s[r]).isnan().all(), r
+    for r in (2, 5):
+        assert s[r].isnan() and (q[r].float() * s[r]).isnan().all(), r
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[1:6] = False
+    assert torch.equal(s[keep], s0[keep]) and torch.equal(q.view(torch.uint8)[keep], q0.view(torch.uint8)[keep])
 
 
 # ---------------------------------------------------------------- clipping --
