@@ -734,8 +734,9 @@ typedef struct {
 /*
  * The norm of all gradients together, and their scaling to a largest norm:
  *   norm = sqrt(sum of squares over all values),  out = data * min(1, max_norm / norm)
- * A norm that is not finite leaves the values as they are (copied where out is
- * not data); so does max_norm = infinity.
+ * A norm that is not finite, or is past fp32's range and so written as infinity,
+ * leaves the values as they are (copied where out is not data); so does max_norm
+ * = infinity.
  *
  * grads     host array of `count` entries, read during the call only.  The
  *           entries' dtypes may differ.  Outputs must not overlap each other

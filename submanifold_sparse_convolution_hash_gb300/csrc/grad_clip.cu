@@ -273,8 +273,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_scale(const __grid_constan
   double sum = 0.0;
   for (int i = threadIdx.x; i < t.h.slot; i += kThreads) sum += t.h.part[i];
   const double norm = sqrt(block_sum(sum, s_warp));
-  if (blockIdx.x == 0 && threadIdx.x == 0) *t.h.norm = static_cast<float>(norm);
-  const bool cut = isfinite(norm) && norm > static_cast<double>(t.h.max_norm);
+  const float said = static_cast<float>(norm);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *t.h.norm = said;
+  // a norm past fp32's range is said to be infinite, so it scales nothing either
+  const bool cut = isfinite(said) && norm > static_cast<double>(t.h.max_norm);
   const float by = cut ? static_cast<float>(static_cast<double>(t.h.max_norm) / norm) : 1.f;
   const uint32_t c0 = chunk_of(t.h.chunks, blockIdx.x), c1 = chunk_of(t.h.chunks, blockIdx.x + 1);
   if (c0 == c1) return;

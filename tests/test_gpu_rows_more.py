@@ -199,3 +199,15 @@ def test_clip_many_chunks_a_block():
             within(o, r, (U[d] + 4 * E) * r.abs() + TINY[d], "scaled")
         again = sc.sc_grad_clip(grads, 1.0)
         assert torch.equal(again, got) and all(torch.equal(t, o) for t, o in zip(grads, out))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_clip_leaves_gradients_whose_norm_passes_fp32(dtype):
+    """Finite values, a norm of 9.5e38: said as infinity, so nothing is scaled."""
+    grads = [torch.full((7,), 3e38, device="cuda", dtype=DT[dtype]), torch.ones(70000, device="cuda"),
+             torch.full((3,), -3e38, device="cuda", dtype=DT[dtype])]
+    kept = [t.clone() for t in grads]
+    out = [torch.zeros_like(t) for t in grads]
+    assert float(sc.sc_grad_clip(sc.GradList(grads, out=out), 1.0)) == math.inf
+    assert float(sc.sc_grad_clip(grads, 1.0)) == math.inf
+    assert all(torch.equal(t, k) and torch.equal(o, k) for t, o, k in zip(grads, out, kept))
