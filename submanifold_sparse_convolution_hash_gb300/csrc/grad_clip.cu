@@ -224,8 +224,18 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_squares(const __grid_const
   if (threadIdx.x == 0) t.h.part[t.h.slot + blockIdx.x] = sum;
 }
 
+// What the values are multiplied by.  Below fp32's normal range a factor has lost bits that the
+// product needs (values near 2^127 to a norm of 1): there `by` is 2^126 times it, at most 1, and
+// `down` 2^-126, else 1.  Factors are above 2^-277, so `by` is off by 2^-150 at most and a product by 2^-148.
+struct Factor {
+  float by, down;
+  __device__ __forceinline__ explicit Factor(double f)
+      : by(static_cast<float>(f < 0x1p-126 ? f * 0x1p126 : f)), down(f < 0x1p-126 ? 0x1p-126f : 1.f) {}
+  __device__ __forceinline__ float operator()(float v) const { return v * by * down; }
+};
+
 template <typename T>
-__device__ __forceinline__ void scale_chunk(const T* p, T* o, int lo, int hi, float by) {
+__device__ __forceinline__ void scale_chunk(const T* p, T* o, int lo, int hi, const Factor& by) {
   constexpr int V = 16 / sizeof(T);
   if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) {  // no common boundary
     for (int i0 = lo + threadIdx.x; i0 < hi; i0 += 8 * kThreads) {
@@ -234,7 +244,7 @@ __device__ __forceinline__ void scale_chunk(const T* p, T* o, int lo, int hi, fl
       for (int k = 0; k < 8; ++k) f[k] = i0 + k * kThreads < hi ? to_f(p[i0 + k * kThreads]) : 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (i0 + k * kThreads < hi) o[i0 + k * kThreads] = from_f<T>(f[k] * by);
+        if (i0 + k * kThreads < hi) o[i0 + k * kThreads] = from_f<T>(by(f[k]));
     }
     return;
   }
@@ -242,10 +252,10 @@ __device__ __forceinline__ void scale_chunk(const T* p, T* o, int lo, int hi, fl
   const uint4* body = reinterpret_cast<const uint4*>(p);
   uint4* dst = reinterpret_cast<uint4*>(o);
   if (static_cast<int>(threadIdx.x) < sp.head) {
-    o[lo + threadIdx.x] = from_f<T>(to_f(p[lo + threadIdx.x]) * by);
+    o[lo + threadIdx.x] = from_f<T>(by(to_f(p[lo + threadIdx.x])));
   } else if (threadIdx.x >= 32 && static_cast<int>(threadIdx.x) - 32 < sp.tail) {
     const int i = sp.v1 * V + threadIdx.x - 32;
-    o[i] = from_f<T>(to_f(p[i]) * by);
+    o[i] = from_f<T>(by(to_f(p[i])));
   }
   // four loads in flight a thread (eight, or more blocks an SM, measured the same)
 #pragma unroll 1
@@ -259,7 +269,7 @@ __device__ __forceinline__ void scale_chunk(const T* p, T* o, int lo, int hi, fl
       float f[V];
       unpack16<T>(u[l], f);
 #pragma unroll
-      for (int i = 0; i < V; ++i) f[i] *= by;
+      for (int i = 0; i < V; ++i) f[i] = by(f[i]);
       dst[l0 + l * kThreads] = pack16<T>(f);
     }
   }
@@ -277,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_scale(const __grid_constan
   if (blockIdx.x == 0 && threadIdx.x == 0) *t.h.norm = said;
   // a norm past fp32's range is said to be infinite, so it scales nothing either
   const bool cut = isfinite(said) && norm > static_cast<double>(t.h.max_norm);
-  const float by = cut ? static_cast<float>(static_cast<double>(t.h.max_norm) / norm) : 1.f;
+  const Factor by(cut ? static_cast<double>(t.h.max_norm) / norm : 1.0);
   const uint32_t c0 = chunk_of(t.h.chunks, blockIdx.x), c1 = chunk_of(t.h.chunks, blockIdx.x + 1);
   if (c0 == c1) return;
   int i = entry_of(t, c1 - 1);

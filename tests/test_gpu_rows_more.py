@@ -211,3 +211,16 @@ def test_clip_leaves_gradients_whose_norm_passes_fp32(dtype):
     assert float(sc.sc_grad_clip(sc.GradList(grads, out=out), 1.0)) == math.inf
     assert float(sc.sc_grad_clip(grads, 1.0)) == math.inf
     assert all(torch.equal(t, k) and torch.equal(o, k) for t, o, k in zip(grads, out, kept))
+
+
+@pytest.mark.parametrize("largest", [1.0, 1e-3, 1e-30])
+def test_clip_factors_below_the_normal_range(largest):
+    g = gen(85)
+    grads = [normal(g, 1000, std=3e36), normal(g, 33, std=3e36).bfloat16()]
+    norm, ref = clip_ref(grads, largest)
+    assert largest / norm < 2.0 ** -126
+    got = sc.sc_grad_clip(grads, largest)
+    assert abs(float(got) - norm) <= 64 * E * norm
+    for t, r in zip(grads, ref):
+        u = 4 * E if t.dtype is torch.float32 else U["bf16"] + 4 * E
+        within(t, r, u * r.abs() + 2.0 ** -148, "scaled")
