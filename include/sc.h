@@ -742,7 +742,8 @@ typedef struct {
  *           entries' dtypes may differ.  Outputs must not overlap each other
  *           or another entry's data, which is the caller's to see to.
  * max_norm  not negative, or infinity.
- * d_norm    fp32 [1], 4-byte aligned: the norm before the scaling.
+ * d_norm    fp32 [1], 4-byte aligned, apart from every entry's data and output: the
+ *           norm before the scaling.
  *
  * No host synchronisation.  Values whose squares leave fp32's range are squared
  * in 64 bits, and the sums of 64 squares or fewer are added in 64 bits, in an

@@ -294,6 +294,10 @@ sc_status sc_grad_clip(const sc_grad* grads, int64_t count, float max_norm, floa
     const uintptr_t bytes = static_cast<uintptr_t>(g.n) * size;
     if (d != o && d < o + bytes && o < d + bytes)
       return invalid("gradient " + std::to_string(i) + ": out overlaps data without being it");
+    // a block writes the norm while others still scale
+    const uintptr_t at = reinterpret_cast<uintptr_t>(d_norm);
+    if ((at < d + bytes && d < at + 4) || (at < o + bytes && o < at + 4))
+      return invalid("gradient " + std::to_string(i) + ": the norm lies among its values");
     if ((st = seen.check(g.data, size, "a gradient"))) return st;
     if (g.out != g.data && (st = seen.check(g.out, size, "a gradient's output"))) return st;
   }

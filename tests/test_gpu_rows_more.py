@@ -5,6 +5,7 @@ Sums of whole numbers below 2^24 are exact in fp32 in any order, and a result of
 256 (bf16) is exact after its rounding, so the products' tests with whole numbers compare for equality: a row
 or a run of k that is lost, or added twice, shows.  The other tolerances are test_gpu_rows.py's; where a
 bound there grows with the number of rows, the longest chain of additions takes its place."""
+import ctypes
 import math
 
 import pytest
@@ -224,3 +225,14 @@ def test_clip_factors_below_the_normal_range(largest):
     for t, r in zip(grads, ref):
         u = 4 * E if t.dtype is torch.float32 else U["bf16"] + 4 * E
         within(t, r, u * r.abs() + 2.0 ** -148, "scaled")
+
+
+def test_clip_refuses_a_norm_among_the_gradients():
+    t = torch.ones(64, device="cuda")
+    o = torch.ones(64, device="cuda")
+    L = sc.lib()
+    for norm_at, out in ((t, t), (t, o), (o, o)):
+        entry = (sc._Grad * 1)((t.data_ptr(), out.data_ptr(), 64, 0))
+        assert L.sc_grad_clip(entry, 1, ctypes.c_float(1.0), norm_at.data_ptr() + 4 * 63, None) == 1
+    torch.cuda.synchronize()
+    assert (t == 1).all() and (o == 1).all()
