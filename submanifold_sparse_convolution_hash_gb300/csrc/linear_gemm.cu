@@ -209,11 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every stage read again before the block may end (after a timeout: its copies landed;
       // a stage that was never filled passes at once)
       for (int i = 0; i < p.stages; ++i) {
-        if (*s_abort) {
-          if (rank == 0) mbar_drain(full + 8 * s, ph);
-        } else if (!mbar_wait(empty + 8 * s, ph, s_abort)) {
-          *s_abort = 1;
-        }
+        if (!*s_abort && !mbar_wait(empty + 8 * s, ph, s_abort)) *s_abort = 1;
+        if (*s_abort && rank == 0) mbar_drain(full + 8 * s, ph);
         if (++s == p.stages) s = 0, ph ^= 1;
       }
       if (rank != 0) mbar_drain(done, 0);  // nor while the pair's last arrival here is under way
@@ -392,6 +389,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         else mbar_arrive(acce + 8 * b);
       }
     }
+    // after a timeout: a residual's tile on its way in lands before the block may end
+    if (*s_abort && has_res && lane == 0) {
+      mbar_drain(res_bar, res_ph & 1);
+      mbar_drain(res_bar + 8, (res_ph >> 1) & 1);
+    }
+    __syncwarp();
   }
 
   if (warp < kEpiWarps && lane == 0) bulk_wait_all();
