@@ -113,12 +113,12 @@ __global__ void __launch_bounds__(kThreads)
         tma_load_2d(da + kA, &tb, kb * kBlock, 0, bar);
         if (++s == p.stages) s = 0, ph ^= 1;
       }
-      // after a timeout: the copies landed before the block may end
-      if (*s_abort)
-        for (int i = 0; i < p.stages; ++i) {
-          mbar_drain(full + 8 * s, ph);
-          if (++s == p.stages) s = 0, ph ^= 1;
-        }
+      // every copy landed before the block may end, also where the products gave up on one (a stage
+      // that was never filled passes at once)
+      for (int i = 0; i < p.stages; ++i) {
+        if (!mbar_drain(full + 8 * s, ph)) *s_abort = 1;
+        if (++s == p.stages) s = 0, ph ^= 1;
+      }
     }
   } else if (warp == kEpiWarps + 1) {
     if (lane == 0) {
