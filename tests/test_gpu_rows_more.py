@@ -7,12 +7,14 @@ or a run of k that is lost, or added twice, shows.  The other tolerances are tes
 bound there grows with the number of rows, the longest chain of additions takes its place."""
 import ctypes
 import math
+import threading
 
 import pytest
 import torch
 
 from submanifold_sparse_convolution_hash_gb300 import binding as sc
 from test_gpu_rows import DT, E, TINY, U, clip_ref, gen, norm_grad_ref, norm_inputs, normal, within
+from test_gpu_voxel_transformer import small
 
 pytestmark = pytest.mark.gpu
 
@@ -236,3 +238,46 @@ def test_clip_refuses_a_norm_among_the_gradients():
         assert L.sc_grad_clip(entry, 1, ctypes.c_float(1.0), norm_at.data_ptr() + 4 * 63, None) == 1
     torch.cuda.synchronize()
     assert (t == 1).all() and (o == 1).all()
+
+
+# ------------------------------------------------------------ calls at once --
+def test_blocks_at_once_from_threads():
+    """Three of the example's blocks, each on a stream and a host thread of its own: convolution, norms, products
+    in 16 and 8 bits, attention and clipping side by side on the SMs, the same bits as one after the other."""
+    blocks = [small(20 + i, scans=2 + i, voxels=400 * (i + 1))[1:] for i in range(3)]
+
+    def run(block, feats, gy):
+        y = block.forward(feats)
+        grads = block.backward(gy)[1:]  # the convolution's adds with atomics
+        y8 = block.forward_e4m3(feats)
+        norm = sc.sc_grad_clip(grads, 0.5)
+        return [y, y8, norm] + grads
+
+    for block, _, _ in blocks:
+        block.quantise()
+    want = [run(*b) for b in blocks]
+    torch.cuda.synchronize()
+    got, failed = [[] for _ in blocks], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(6):
+                    got[i].append(run(*blocks[i]))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    torch.cuda.synchronize()
+    for w, many in zip(want, got):
+        assert len(many) == 6
+        for one in many:
+            assert all(torch.equal(a, b) for a, b in zip(w, one))
+    sc.sc_rows_check()
+    sc.sc_attn_check()
