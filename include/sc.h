@@ -630,7 +630,8 @@ typedef struct {
  * d_w       fp32 [channels], 16-byte aligned; NULL: y = h, for SC_E4M3 only
  *           (rows, or weights laid out as rows, quantised as they are).
  * d_scale   fp32 [rows], 4-byte aligned; SC_E4M3 only.
- * channels  a multiple of 8 in [8, 16384].
+ * channels  a multiple of 8 in [8, 16384].  (sc_linear_fwd takes 8-bit rows and
+ *           weights of up to 65536: wider ones than 16384 come from elsewhere.)
  * dtype     of x, res and sum: SC_F32, SC_F16 or SC_BF16.
  * out_dtype dtype or SC_E4M3 (whose out may be aligned, and its rows strided, by
  *           multiples of 8 bytes).
@@ -683,7 +684,7 @@ typedef enum {
  *           laid out once as [c_out, c_in].
  * d_scale_x, d_scale_w  fp32 [rows] and [c_out] (this one 16-byte aligned),
  *           SC_E4M3 only (as sc_add_norm_fwd writes them): z = d_scale_x[r] d_scale_w[c] sum_i
- *           x[r, i] W[c, i] + d_bias[c].
+ *           x[r, i] W[c, i] + d_bias[c], the scales multiplied first, in fp32.
  * d_bias    fp32 [c_out], 16-byte aligned, or NULL.
  * res       [rows, c_out] in dtype, or NULL.
  * out       [rows, c_out] in dtype; may be res itself (the same pointer and
@@ -695,7 +696,9 @@ typedef enum {
  *
  * Few rows take a form that reads the weights once, spread over the card.
  * Temporary device memory, where sums are cut along c_in, is allocated and
- * freed stream-ordered on `stream`.  No sum depends on an order of arrival.
+ * freed stream-ordered on `stream`.  No sum depends on an order of arrival; where
+ * sums are cut may depend, beside the sizes, on which operands' rows begin on
+ * 128-byte lines.
  */
 sc_status sc_linear_fwd(const sc_rows* x, const void* d_W, const float* d_scale_x, const float* d_scale_w,
                         const float* d_bias, const sc_rows* res, const sc_rows_out* out, const sc_rows_out* pre,
@@ -709,9 +712,11 @@ sc_status sc_linear_fwd(const sc_rows* x, const void* d_W, const float* d_scale_
  * gin, d_gW [c_in, c_out] (dtype) and d_gbias (fp32) may each be NULL: not
  * computed; what only they read may then be NULL too.  pre is read only with
  * an activation.  gz is rounded to dtype for the products; d_gbias sums it
- * unrounded.  The rows of gout and x must not overlap one another.  relu'(0) = 0.  All sums are fp32 and in an order that depends on
- * the sizes alone.  The outputs must not overlap
- * the inputs that are read, or each other.
+ * unrounded.  The rows of gout and x must not overlap one another.  relu'(0) = 0.
+ * All sums are fp32, in an order that depends on the sizes and, as cuts of k are
+ * chosen, on which operands' rows begin on 128-byte lines: the same inputs in
+ * places alike give the same bits.  The outputs must not overlap the inputs that
+ * are read, or each other.
  */
 sc_status sc_linear_bwd(const sc_rows* gout, const sc_rows* x, const sc_rows* pre, const void* d_W,
                         const sc_rows_out* gin, void* d_gW, float* d_gbias, int64_t rows, int c_in, int c_out,
@@ -746,9 +751,10 @@ typedef struct {
  *           norm before the scaling.
  *
  * No host synchronisation.  Values whose squares leave fp32's range are squared
- * in 64 bits, and the sums of 64 squares or fewer are added in 64 bits, in an
- * order that depends on the sizes alone: the same inputs give the same bits.
- * Each output is rounded once.
+ * in 64 bits, and the sums of 65 squares or fewer are added in 64 bits, in an
+ * order that depends on the sizes and on where each gradient lies within its
+ * 128-byte line: the same inputs in places alike give the same bits.  The factor
+ * is rounded to fp32, and each output once.
  */
 sc_status sc_grad_clip(const sc_grad* grads, int64_t count, float max_norm, float* d_norm, sc_stream stream);
 

@@ -7,8 +7,10 @@
 // positive factor r = 1 / sqrt(mean h^2 + eps) times w h, so the largest |y| of the
 // 8-bit form is r max |w h| and rides along with the sum of squares.
 //
-// Bound by memory: 32,768 rows of 4,096, bf16, residual, to 8 bits 141 us (6.66 TB/s of the 6.78 that a
-// copy reaches), gradients of 480,000 rows of 256, f16, 162 (6.07).
+// Bound by memory: 32,768 rows of 4,096, bf16, residual, to 8 bits 140 us (6.69 TB/s of the 6.78 that a
+// copy reaches), gradients of 480,000 rows of 256, f16, 162 (6.07).  f32, cold, floors beside: 480,000 rows
+// of 256 forward 326 us (290), to 8 bits 247 (236), gradients 300 (290); 32,768 of 4,096 350 (317),
+// 287 (257), 325 (317).
 #include <cmath>
 #include <type_traits>
 
@@ -287,6 +289,10 @@ __global__ void __launch_bounds__(kBlock, NV * sizeof(T) <= 4 ? 3 : 1) k_add_nor
 // gives sum h^2 and sum z h, and gin = r z - h r^3 (sum z h) / channels + gsum.  The
 // weights' gradient gathers in registers over the rows that a lane's block walks and
 // goes out once a block.
+//
+// At four vectors a lane (520 to 1,024 channels) 128 registers do not hold a row's three tensors and
+// the sums: 112 to 216 bytes spill (131,072 rows of 1,024, bf16, cold: 209 us, floor 158; 65,536 of 2,048, which
+// the wide form takes, 184).
 template <typename T, int NV, int G>
 __global__ void __launch_bounds__(kBlock, NV * sizeof(T) <= 2 ? 3 : 2)
     k_add_norm_bwd(const NormParams p) {
@@ -384,7 +390,9 @@ __global__ void __launch_bounds__(kBlock, NV * sizeof(T) <= 2 ? 3 : 2)
 
 // The gradients of wide rows, a block a row.  Rows come ahead of their turn into a ring of
 // shared memory by bulk copies, so that what is in flight does not wait for the block's
-// barriers: with loads into registers, one row ahead, 9,973 rows of 2,056 took 51 us (floor 24).
+// barriers: with loads into registers, one row ahead, 9,973 rows of 2,056 took 51 us (36 so; floor 24).
+// Above 8,192 channels a lane holds four vectors and spills 40 to 172 bytes, and one block an SM works on
+// one row at a time (11,000 rows of 12,000, bf16, cold: 229 us, floor 156).
 template <typename T, int NV>
 __global__ void __launch_bounds__(512, NV == 1 && sizeof(T) == 2 ? 2 : 1) k_add_norm_bwd_wide(const NormParams p) {
   extern __shared__ __align__(16) uint8_t s_rows[];

@@ -1,7 +1,7 @@
 // Matrix products on rows: the layer, its gradients, and the pass that makes the
 // gradient before the activation and sums the bias's.
 //
-// The gradients are that pass and two products.  120,000 rows, 256 -> 512, f16, silu: 154 us, the pass 56
+// The gradients are that pass and two products.  120,000 rows, 256 -> 512, f16, silu: 155 us, the pass 56
 // (bound by memory: 6.5 TB/s), the products 40 and 39.  Rounding gz to the rows' type is what the
 // tensor cores' operands ask for; a product of it is off by that rounding once more.
 #include "linear_internal.cuh"
@@ -10,6 +10,14 @@ namespace sc {
 namespace {
 
 constexpr int kThreads = 256;
+// Up to here the form for few rows, whose tiles have the rows for columns; above it tiles of 128 rows or more.
+// Kernels, cold, us, in this form and in tiles (with their join), at 16, at 64 and at 128 rows:
+//   4,096 -> 4,096   17.3 22.4   20.7 23.0   24.7 23.8
+//   8,192 -> 1,024   14.7 18.8   18.5 19.5   22.9 21.4
+//   1,024 -> 1,024   10.4 16.3   12.5 16.6   16.4 16.6
+//   4,096 -> 256     12.3 16.3   14.4 16.6   18.5 16.8
+//   256 -> 4,096     10.2 10.5   14.1 10.3   18.5 10.5
+// A rule on the rows alone: where k is short, so that tiles need no cuts, they are faster from 20 rows or so on.
 constexpr int64_t kFewRows = 128;
 
 // gz = gout * act'(pre), in 16 bits, and the columns' sums of the unrounded values.  A block

@@ -7,6 +7,10 @@
 // all of them, in the order of the runs, through the cluster's shared memory: one launch, no
 // workspace, no order of arrival.  Two blocks an SM where their tiles are narrow, so that one
 // streams while the other joins.
+//
+// Bound by latency, launch, first loads and the join: cold, 16 x 4,096 -> 4,096 takes 17 us in bf16, where
+// its 34 MB would take 5, and 14.5 in 8 bits.  Outputs of few tiles leave SMs idle: 1 x 8,192 -> 1,024 (64
+// blocks) takes 14.4 us where 2.5 would do.
 #include <cmath>
 
 #include "linear_internal.cuh"

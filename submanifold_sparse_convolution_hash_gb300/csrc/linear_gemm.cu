@@ -7,10 +7,12 @@
 // two accumulators let that overlap the next tile's products.
 //
 // What bounds it: long k, the tensor cores and the card's power (8,192 x 4,096 -> 16,384,
-// bf16, gelu: 626 to 665 us by the card's clocks, 1.65 to 1.76 PFLOP/s, where the library's
-// plain product sustains 1.72; in 8 bits 8,192 x 4,096 -> 4,096 94 to 105 us, 2.6 to 2.9); short k,
-// memory (480,000 x 256 -> 512, f16, silu, both outputs: 202 us, 6.1 TB/s); between them
-// shared memory's 128 bytes a clock, which a k block is written to and read from once each.
+// bf16, gelu: 626 to 690 us by the card, 680 at the 1,597 MHz that its power limit left one; 1.59 to
+// 1.76 PFLOP/s, where the library's plain product sustains 1.72; in 8 bits 8,192 x 4,096 -> 4,096 91 to 105
+// us, 103 at 1,684 MHz, 2.6 to 3.0); short k, memory (480,000 x 256 -> 512, f16, silu, both outputs:
+// 194 to 213 us, 5.8 to 6.3 TB/s); between them a k block's clocks: for the widest tiles what
+// shared memory takes to be written and read once at 128 bytes a clock (640 of a pair's 665, 768 of 813), for
+// smaller ones about 560 whatever the tile, where that explains 384 to 512.
 // Four stages do what five or six do.  Two pairs that share B by TMA multicast were slower
 // (715 against 658 us on the first of these): clusters of four leave 8 of 152 SMs out.
 //
@@ -42,7 +44,8 @@ constexpr int kSmemMost = 230400;                  // of 232,448, with the barri
 constexpr uint32_t kTile = 32 * 64;               // 32 rows of 32 16-bit columns on their way out
 constexpr uint32_t kStaging = kEpiWarps * 2 * kTile;
 // Tile rows whose tiles are neighbours in time: they share B's columns in L2, and B is read once for each
-// such group.  8,192 x 4,096 -> 16,384, 32 tile rows, us: 4 670, 8 646, 12 626, 16 626, 32 667.
+// such group.  8,192 x 4,096 -> 16,384, 32 tile rows, one card under its power limit, us: 4 719, 8 690,
+// 12 681, 16 673, 32 730.
 constexpr int kGroup = 12;
 
 struct GemmParams {
@@ -464,8 +467,8 @@ bool straddles(const Operand& o, bool e4m3) {
 
 // The cheapest by an estimate in SM clocks.  A k block of a tile costs what shared memory takes to
 // be written by TMA and read by the tensor cores, 128 bytes a clock (a pair's blocks read half
-// of B from each other), and not below 560 (measured: 570 to 590 for tiles of 64 and 128
-// columns, 665 for a pair's 256, 813 for one block's 256); where an operand's rows straddle lines
+// of B from each other), and not below 560, a stage's own cost (measured: 570 to 590 for tiles of 64
+// and 128 columns, 665 for a pair's 256, 813 for one block's 256); where an operand's rows straddle lines
 // of 128 bytes, about 1.5 % of a clock more for each byte over 20 KB (9,973 x 1,992 x 1,048: 880 for
 // a pair's 256 columns, 1,210 for one block's).  A unit costs that or what its
 // sixteen warps take to finish it, whichever is longer (about 27 clocks a column for one
@@ -516,8 +519,8 @@ sc_status make_out_map(CUtensorMap* map, const void* data, int64_t ld, int64_t r
   const CUresult r = encode(map, eb == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
                             parts ? 3 : 2, const_cast<void*>(data), dims, strides, box, one,
                             CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            eb == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                            eb == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SC_OK : set_error(SC_ERR_CUDA, "tensor map of an output");
 }
 

@@ -150,7 +150,8 @@ def test_one_row_of_any_stride():
         w, W = 1 + normal(g, c, std=0.1), normal(g, c, 72, std=0.1, dtype=torch.float16)
         near, gnear = x.clone(memory_format=torch.contiguous_format), gout.clone(memory_format=torch.contiguous_format)
         assert torch.equal(sc.sc_add_norm_fwd(x, w), sc.sc_add_norm_fwd(near.view(1, c), w))
-        assert torch.equal(sc.sc_linear_fwd(x, W, res=gout), sc.sc_linear_fwd(near.view(1, c), W, res=gnear.view(1, 72)))
+        want = sc.sc_linear_fwd(near.view(1, c), W, res=gnear.view(1, 72))
+        assert torch.equal(sc.sc_linear_fwd(x, W, res=gout), want)
         got = sc.sc_linear_bwd(gout, x, W, pre=gout, act="silu", bias=True)
         want = sc.sc_linear_bwd(gnear.view(1, 72), near.view(1, c), W, pre=gnear.view(1, 72), act="silu", bias=True)
         assert all(torch.equal(a, b) for a, b in zip(got, want))

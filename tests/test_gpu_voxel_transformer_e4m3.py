@@ -13,7 +13,8 @@ pytestmark = pytest.mark.gpu
 def quantised(q, s, y, what):
     ref = y.abs().amax(-1) / 448
     within(s, ref, 128 * E * ref, what)
-    within(q.double() * s.double()[:, None], y, (2.0 ** -4 + 512 * E) * y.abs() + 2.0 ** -10 * 1.001 * ref[:, None], what)
+    bound = (2.0 ** -4 + 512 * E) * y.abs() + 2.0 ** -10 * 1.001 * ref[:, None]
+    within(q.double() * s.double()[:, None], y, bound, what)
 
 
 def test_every_step_of_the_8_bit_forward(monkeypatch):
